@@ -55,7 +55,8 @@ typedef enum {
   SAGE_ERR_TIMEOUT = 9,      /* (device) a bounded pipeline wait expired */
   SAGE_ERR_CUDA = 10,        /* a CUDA runtime/driver call failed */
   SAGE_ERR_DEVICE = 11,      /* current device is not compute capability 10.3 */
-  SAGE_ERR_SEQLENS = 12      /* (device) cu_seqlens not non-decreasing / out of range */
+  SAGE_ERR_SEQLENS = 12,     /* (device) cu_seqlens not non-decreasing / out of range */
+  SAGE_ERR_PAGE = 13         /* (device) a page table entry outside of the cache */
 } sage_status;
 
 enum { SAGE_HND = 0, SAGE_NHD = 1 };                       /* §4.1 tensor_layout */
@@ -225,6 +226,73 @@ int sage_attn_varlen_qk_int8_pv_fp16(const sage_packed* q, const sage_packed* k,
 int sage_merge_partials(const sage_tensor* outs, const float* const* lses, int n_parts,
                         const sage_tensor* out, float* lse_out, int batch, int heads,
                         int seqlen, int head_dim, int dtype, int tensor_layout, void* stream);
+
+/* ---- A paged key-value cache ----
+ * k, v: device FP16/BF16 [num_pages, Hkv, page_size, d] (HND) or [num_pages, page_size, Hkv, d] (NHD), any
+ * strides of the first three dimensions (k_stride, v_stride, in that order), channel stride 1.
+ * Token slot t of sequence b lies in page page_table[b * table_stride + t / page_size] at
+ * t % page_size; page_table has max_pages entries per row, of which only those of held tokens are
+ * read. seq_lens: device int32 [batch], the tokens each sequence holds.
+ * mass: device float [num_pages, Hkv, page_size] contiguous, the attention weight each token has drawn,
+ * or NULL. positions: device int32 of the same shape, the tokens' positions, or NULL (the slot).
+ * Errors found on the device: SAGE_ERR_SEQLENS (a length outside of [0, max_seqlen] or of the table's
+ * room: the sequence counts as empty), SAGE_ERR_PAGE (an entry outside of [0, num_pages): its tokens
+ * count as zero rows, are not written and not moved). Nothing outside of the cache is touched. */
+typedef struct {
+  void* k;
+  int64_t k_stride[3];
+  void* v;
+  int64_t v_stride[3];
+  int num_pages, page_size;
+  const int32_t* page_table;
+  int64_t table_stride;
+  int max_pages;
+  const int32_t* seq_lens;
+  float* mass;
+  int32_t* positions;
+} sage_paged_cache;
+
+#define SAGE_STATUS_BYTES ((size_t)256) /* workspace of a call that needs only its status word */
+
+/* Attention of one new token per sequence over its held tokens (its own K and V appended before).
+ *   s_j = sm_scale q.k_j;  softcap > 0: s = softcap tanh(s / softcap);
+ *   slopes: s -= slopes[h] |q_position - position of key j|
+ *   q, out: [batch, Hq, d] (stride_token is the sequence's); lse: device float [batch, Hq] or NULL.
+ *   slopes: device float [Hq] or NULL; q_positions: device int32 [batch] or NULL (seq_len - 1).
+ *   max_seqlen: an upper bound of seq_lens. cache->mass, where not NULL: each held token's weight,
+ *   summed over the query heads of its key/value head, is added. A page that several
+ *   sequences share is given the weights of all, in no fixed order.
+ * A sequence that holds nothing gets out = 0 and lse = -inf. */
+size_t sage_paged_attn_workspace_size(int batch, int heads_q, int heads_kv, int max_seqlen,
+                                      int head_dim, int accumulate);
+int sage_paged_attn(const sage_packed* q, const sage_paged_cache* cache, const sage_packed* out,
+                    float* lse, const float* slopes, const int32_t* q_positions, int batch,
+                    int heads_q, int heads_kv, int max_seqlen, int head_dim, int dtype,
+                    int tensor_layout, float sm_scale, float softcap, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Writes new tokens behind the held ones: token t of k, v [tokens, Hkv, d] belongs to the sequence b with
+ * cu_seqlens[b] <= t < cu_seqlens[b + 1] and goes to slot seq_lens[b] + t - cu_seqlens[b]. seq_lens is
+ * read, not raised. cu_seqlens: device int32 [batch + 1], non-decreasing from 0; NULL: one token per
+ * sequence (tokens == batch). Tokens from cu_seqlens[batch] on are left out. cache->mass becomes 0 there
+ * and cache->positions the token's entry of `positions` (device int32 [tokens]) or its slot. Two
+ * tokens must not share a slot. workspace: NULL, or SAGE_STATUS_BYTES for the device status. */
+int sage_paged_append(const sage_packed* k, const sage_packed* v, const sage_paged_cache* cache,
+                      const int32_t* cu_seqlens, const int32_t* positions, int batch, int tokens,
+                      int heads_kv, int head_dim, int dtype, int tensor_layout, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Cuts every sequence that holds more than `budget` tokens down to `budget`, for each key/value head by
+ * itself: tokens with a position below `sink` or within the last `recent` of the head's largest
+ * position stay, then those with the largest mass (ties: the lowest slot; NaN counts as -inf). Kept
+ * tokens from slot `budget` on move, in order, into the freed slots below it, with their mass and
+ * position; slots from `budget` on keep what they held. new_lens: device int32 [batch], written
+ * min(seq_len, budget); not seq_lens itself. cache->mass and cache->positions are needed. Each page
+ * belongs to one sequence. budget >= 1, sink + recent <= budget. */
+size_t sage_paged_evict_workspace_size(int batch, int heads_kv, int max_seqlen, int budget);
+int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch, int heads_kv,
+                     int max_seqlen, int head_dim, int dtype, int tensor_layout, int budget, int sink,
+                     int recent, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a sage_status. Never NULL. */
 const char* sage_status_string(int status);

@@ -397,3 +397,9 @@ __all__ = ["sage_attn", "sage_attn_varlen", "sage_attn_fp4", "SageError", "works
            "varlen_workspace_bytes", "alloc_workspace", "read_device_status", "export_quant",
            "export_fp16", "e4m3", "e2m1",
            "profile_enable", "profile_read"]
+
+from .paged import (paged_append, paged_attn, paged_attn_workspace_bytes, paged_evict,  # noqa: E402
+                    paged_evict_workspace_bytes)
+
+__all__ += ["paged_attn", "paged_append", "paged_evict", "paged_attn_workspace_bytes",
+            "paged_evict_workspace_bytes"]

@@ -21,9 +21,17 @@ class SagePacked(ctypes.Structure):
     _fields_ = [("data", c_void_p), ("stride_token", c_int64), ("stride_head", c_int64)]
 
 
+class SagePagedCache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("k_stride", c_int64 * 3), ("v", c_void_p), ("v_stride", c_int64 * 3),
+                ("num_pages", c_int), ("page_size", c_int), ("page_table", c_void_p),
+                ("table_stride", c_int64), ("max_pages", c_int), ("seq_lens", c_void_p),
+                ("mass", c_void_p), ("positions", c_void_p)]
+
+
 # name -> (restype, argtypes), mirroring include/sageattn.h
 _T = ctypes.POINTER(SageTensor)
 _P = ctypes.POINTER(SagePacked)
+_C = ctypes.POINTER(SagePagedCache)
 SIGNATURES = {
     "sage_attn_workspace_size": (c_size_t, [c_int] * 7),
     "sage_attn": (c_int, [_T, _T, _T, _T, c_void_p] + [c_int] * 9 + [c_float] + [c_int] * 5
@@ -59,6 +67,13 @@ SIGNATURES = {
     # layout, stream
     "sage_merge_partials": (c_int, [c_void_p, c_void_p, c_int, _T, c_void_p] + [c_int] * 6
                             + [c_void_p]),
+    "sage_paged_attn_workspace_size": (c_size_t, [c_int] * 6),
+    "sage_paged_attn": (c_int, [_P, _C, _P, c_void_p, c_void_p, c_void_p] + [c_int] * 7
+                        + [c_float] * 2 + [c_void_p, c_size_t, c_void_p]),
+    "sage_paged_append": (c_int, [_P, _P, _C, c_void_p, c_void_p] + [c_int] * 6
+                          + [c_void_p, c_size_t, c_void_p]),
+    "sage_paged_evict_workspace_size": (c_size_t, [c_int] * 4),
+    "sage_paged_evict": (c_int, [_C, c_void_p] + [c_int] * 9 + [c_void_p, c_size_t, c_void_p]),
 }
 
 _lib = None

@@ -527,6 +527,7 @@ const char* sage_status_string(int status) {
     case SAGE_ERR_CUDA: return "SAGE_ERR_CUDA: a CUDA call failed";
     case SAGE_ERR_DEVICE: return "SAGE_ERR_DEVICE: device is not compute capability 10.3";
     case SAGE_ERR_SEQLENS: return "SAGE_ERR_SEQLENS: invalid cu_seqlens";
+    case SAGE_ERR_PAGE: return "SAGE_ERR_PAGE: a page table entry outside of the cache";
     default: return "unknown sage_status";
   }
 }

@@ -1,0 +1,431 @@
+// Filling and thinning a paged key-value cache: sage_paged_append writes new tokens into their pages,
+// sage_paged_evict keeps each (sequence, head)'s most attended tokens.
+#include <cmath>
+
+#include "launch.h"
+#include "paged.cuh"
+
+namespace sage {
+
+int make_paged_view(const sage_paged_cache* c, int batch, int heads_kv, int head_dim, int dtype, int layout,
+                    PagedView* view, bool* vec) {
+  if (!c) return SAGE_ERR_INVALID_ARG;
+  if (head_dim < 1 || head_dim > 128) return SAGE_ERR_HEAD_DIM;
+  if (dtype != SAGE_F16 && dtype != SAGE_BF16) return SAGE_ERR_DTYPE;
+  if (layout != SAGE_HND && layout != SAGE_NHD) return SAGE_ERR_INVALID_ARG;
+  if (batch < 0 || heads_kv < 1 || heads_kv > 65535 || c->num_pages < 0 || c->page_size < 1 || c->max_pages < 0 ||
+      (int64_t)c->max_pages * c->page_size > 0x7fffffffLL)
+    return SAGE_ERR_INVALID_ARG;
+  PagedView v{};
+  v.batch = batch; v.hkv = heads_kv; v.d = head_dim;
+  v.page_size = c->page_size; v.num_pages = c->num_pages; v.max_pages = c->max_pages;
+  if (batch > 0) {
+    auto off = [](const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; };
+    if (!c->page_table || !c->seq_lens || off(c->page_table, 4) || off(c->seq_lens, 4) || off(c->mass, 4) ||
+        off(c->positions, 4) || c->table_stride < 0)
+      return SAGE_ERR_INVALID_ARG;
+    if (c->num_pages > 0 && (!c->k || !c->v)) return SAGE_ERR_INVALID_ARG;
+    if (off(c->k, 2) || off(c->v, 2)) return SAGE_ERR_STRIDE;
+    for (int i = 0; i < 3; ++i)
+      if (c->k_stride[i] < 0 || c->v_stride[i] < 0) return SAGE_ERR_STRIDE;
+  }
+  const int hi = layout == SAGE_HND ? 1 : 2, ti = layout == SAGE_HND ? 2 : 1;
+  v.k = c->k; v.k_sp = c->k_stride[0]; v.k_sh = c->k_stride[hi]; v.k_st = c->k_stride[ti];
+  v.v = c->v; v.v_sp = c->v_stride[0]; v.v_sh = c->v_stride[hi]; v.v_st = c->v_stride[ti];
+  v.table = c->page_table; v.table_stride = c->table_stride; v.lens = c->seq_lens;
+  v.mass = c->mass; v.pos = c->positions;
+  bool w = head_dim % 8 == 0 && reinterpret_cast<uintptr_t>(c->k) % 16 == 0 && reinterpret_cast<uintptr_t>(c->v) % 16 == 0;
+  for (int i = 0; i < 3; ++i) w = w && c->k_stride[i] % 8 == 0 && c->v_stride[i] % 8 == 0;
+  *view = v;
+  *vec = w;
+  return SAGE_OK;
+}
+
+namespace {
+
+// ------------------------------------------------------------------------------------- append
+struct AppendArgs {
+  PagedView c;
+  const uint16_t* k; int64_t k_st, k_sh;
+  const uint16_t* v; int64_t v_st, v_sh;
+  const int* cu;        // [batch + 1] or null: one token per sequence
+  const int* new_pos;   // [tokens] or null: the slot
+  int tokens, vec;
+  int* err;             // or null
+};
+
+// One warp per token: the token's sequence by bisection of cu_seqlens, its slot and page, then its K
+// and V rows of every head, 16 bytes per lane. Memory-bound for prompts; for one token per sequence the chain of
+// dependent loads (length, page, row) is what it costs. A 16-bit pattern is copied whatever its type.
+__global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
+  pdl_wait();
+  if (t >= a.tokens) return;
+  int b = t, at = 0;
+  if (a.cu) {
+    int lo = 0, hi = a.c.batch;  // the last b with cu[b] <= t
+    while (hi - lo > 0) {
+      const int mid = lo + (hi - lo + 1) / 2;
+      if (__ldg(&a.cu[mid]) <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+    const int first = __ldg(&a.cu[b]);
+    if (a.err && t == 0 && lane == 0 && first != 0) record_error(a.err, kDevSeqlens);
+    if (b == a.c.batch || first > t) return;  // behind the last sequence, or before the first
+    at = t - first;
+  }
+  const int64_t slot = (int64_t)__ldg(&a.c.lens[b]) + at;
+  if (slot < 0 || slot >= (int64_t)a.c.max_pages * a.c.page_size) {
+    if (a.err && lane == 0) record_error(a.err, kDevSeqlens);
+    return;
+  }
+  const int i = (int)(slot / a.c.page_size), sl = (int)(slot - (int64_t)i * a.c.page_size);
+  const int page = __ldg(&a.c.table[b * a.c.table_stride + i]);
+  if (page < 0 || page >= a.c.num_pages) {
+    if (a.err && lane == 0) record_error(a.err, kDevPage);
+    return;
+  }
+  const uint16_t* ks = a.k + t * a.k_st;
+  const uint16_t* vs = a.v + t * a.v_st;
+  uint16_t* kd = static_cast<uint16_t*>(a.c.k) + page * a.c.k_sp + sl * a.c.k_st;
+  uint16_t* vd = static_cast<uint16_t*>(a.c.v) + page * a.c.v_sp + sl * a.c.v_st;
+  if (a.vec) {
+    const int nch = a.c.d / 8, n = a.c.hkv * nch;
+#pragma unroll 4
+    for (int x = lane; x < n; x += 32) {
+      const int h = x / nch, c = (x - h * nch) * 8;
+      const uint4 kx = __ldg(reinterpret_cast<const uint4*>(ks + h * a.k_sh + c));
+      const uint4 vx = __ldg(reinterpret_cast<const uint4*>(vs + h * a.v_sh + c));
+      *reinterpret_cast<uint4*>(kd + h * a.c.k_sh + c) = kx;
+      *reinterpret_cast<uint4*>(vd + h * a.c.v_sh + c) = vx;
+    }
+  } else {
+    for (int x = lane; x < a.c.hkv * a.c.d; x += 32) {
+      const int h = x / a.c.d, c = x - h * a.c.d;
+      kd[h * a.c.k_sh + c] = ks[h * a.k_sh + c];
+      vd[h * a.c.v_sh + c] = vs[h * a.v_sh + c];
+    }
+  }
+  if (a.c.mass || a.c.pos) {
+    const int p = a.new_pos ? __ldg(&a.new_pos[t]) : (int)slot;
+    for (int h = lane; h < a.c.hkv; h += 32) {
+      const int64_t w = plane_at(a.c, page, h, sl);
+      if (a.c.mass) a.c.mass[w] = 0.f;
+      if (a.c.pos) a.c.pos[w] = p;
+    }
+  }
+}
+
+__global__ void status_clear_kernel(int* err) {
+  pdl_wait();
+  *err = 0;
+}
+
+// ---------------------------------------------------------------------------------- eviction
+struct EvictArgs {
+  PagedView c;
+  int budget, sink, recent, max_len, vec;
+  int* new_lens;
+  int* block_err;  // [batch * hkv]
+  int* err;
+  int* count;      // [batch * hkv]: tokens that move
+  int* to;         // [batch * hkv][pitch]: freed slots below the budget, ascending
+  int* from;       // [batch * hkv][pitch]: kept slots from the budget on, ascending
+  int64_t pitch;
+};
+
+constexpr int kSelThreads = 1024;
+constexpr int kBins = 2048;
+
+// A weight's order as an unsigned code: NaN last (with -inf), both zeros alike.
+__device__ __forceinline__ unsigned weight_code(float w) {
+  return ordered_code(isnan(w) ? -INFINITY : w + 0.0f);
+}
+
+// Sum over the block of x and the exclusive prefix of this thread.
+__device__ __forceinline__ int block_scan(int x, int& total) {
+  __shared__ int s[kSelThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();
+  if (lane == 31) s[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    int v = s[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    s[lane] = v;
+  }
+  __syncthreads();
+  total = s[kSelThreads / 32 - 1];
+  return inc - x + (warp ? s[warp - 1] : 0);
+}
+
+// One CTA per (head, sequence). The budget-th largest weight is found by a radix selection over the
+// ordered codes (three digits of 11, 11 and 10 bits, one histogram each: integer counts, so the
+// result does not depend on any order); then the slots are walked once in order, ties taken from
+// the lowest slot on, and the freed slots below the budget and the kept ones behind it are listed.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+  __shared__ int hist[kBins];
+  __shared__ int s_pick, s_rest, s_last;
+  __shared__ int s_bad;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int64_t me = (int64_t)b * a.c.hkv + h;
+  pdl_wait();
+  const int len = checked_len(a.c, b, a.max_len);
+  if (tid == 0) { s_last = INT32_MIN; s_bad = len < 0 ? kDevSeqlens : 0; }
+  __syncthreads();
+  const int keep = a.budget;
+  if (h == 0 && tid == 0) a.new_lens[b] = len < 0 ? a.c.lens[b] : min(len, keep);
+  if (len <= keep) {  // nothing to drop (or a length that is refused)
+    if (tid == 0) { a.count[me] = 0; a.block_err[me] = s_bad; }
+    return;
+  }
+  const int* table = a.c.table + b * a.c.table_stride;
+  auto where = [&](int j) -> int64_t {
+    const int i = j / a.c.page_size;
+    const int page = __ldg(&table[i]);
+    return page >= 0 && page < a.c.num_pages ? plane_at(a.c, page, h, j - i * a.c.page_size) : -1;
+  };
+  {
+    int last = INT32_MIN;
+    bool bad = false;
+    for (int j = tid; j < len; j += kSelThreads) {
+      const int64_t w = where(j);
+      if (w < 0) bad = true;
+      else last = max(last, a.c.pos[w]);
+    }
+    last = __reduce_max_sync(0xffffffffu, last);
+    if ((tid & 31) == 0) atomicMax(&s_last, last);
+    if (bad) s_bad = kDevPage;
+  }
+  __syncthreads();
+  if (s_bad) {
+    if (tid == 0) { a.count[me] = 0; a.block_err[me] = s_bad; }
+    return;
+  }
+  const int64_t recent_from = (int64_t)s_last - a.recent;
+  auto code_of = [&](int j) -> unsigned {
+    const int64_t w = where(j);
+    const int p = a.c.pos[w];
+    return p < a.sink || p > recent_from ? 0xFFFFFFFFu : weight_code(a.c.mass[w]);
+  };
+  unsigned prefix = 0, mask = 0;
+  int rest = keep;  // how many of the codes that match the prefix are kept
+#pragma unroll 1
+  for (int digit = 0; digit < 3; ++digit) {
+    const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bins = digit == 2 ? 1024 : 2048;
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int j = tid; j < len; j += kSelThreads) {
+      const unsigned c = code_of(j);
+      if ((c & mask) == prefix) atomicAdd(&hist[(c >> shift) & (bins - 1)], 1);
+    }
+    __syncthreads();
+    // bins from the top: the one in which the rest-th largest lies
+    const int hi = kBins - 1 - 2 * tid, x1 = hist[hi], x0 = hist[hi - 1];
+    int total;
+    const int before = block_scan(x1 + x0, total);
+    if (before < rest && rest <= before + x1) { s_pick = hi; s_rest = rest - before; }
+    else if (before + x1 < rest && rest <= before + x1 + x0) { s_pick = hi - 1; s_rest = rest - before - x1; }
+    __syncthreads();
+    prefix |= (unsigned)s_pick << shift;
+    mask |= (unsigned)(bins - 1) << shift;
+    rest = s_rest;
+    __syncthreads();
+  }
+  // the threshold is `prefix`; of the slots that equal it the first `rest` are kept
+  int ties = 0, holes = 0, movers = 0;
+  int* to = a.to + me * a.pitch;
+  int* from = a.from + me * a.pitch;
+#pragma unroll 1
+  for (int j0 = 0; j0 < len; j0 += kSelThreads) {
+    const int j = j0 + tid;
+    const bool in = j < len;
+    const unsigned c = in ? code_of(j) : 0u;
+    const bool tie = in && c == prefix;
+    int n_ties, n;
+    const int my_tie = ties + block_scan(tie, n_ties);
+    const bool kept = in && (c > prefix || (tie && my_tie < rest));
+    const bool hole = in && j < keep && !kept, mover = in && j >= keep && kept;
+    // one scan counts both: a hole in the low half, a mover in the high
+    const int at = block_scan((int)hole | ((int)mover << 16), n);
+    if (hole) to[holes + (at & 0xffff)] = j;
+    if (mover) from[movers + (at >> 16)] = j;
+    ties += n_ties;
+    holes += n & 0xffff;
+    movers += n >> 16;
+  }
+  if (tid == 0) { a.count[me] = movers; a.block_err[me] = 0; }
+}
+
+// Moves the listed tokens: a half warp per token and pass, 16 bytes per lane. Sources lie behind the budget and
+// targets below it, so no move reads what another one writes.
+__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int64_t me = (int64_t)b * a.c.hkv + h;
+  pdl_wait();
+  if (blockIdx.x == 0 && h == 0 && b == 0) {
+    int e = 0;
+    for (int i = threadIdx.x; i < a.c.batch * a.c.hkv; i += 256) e = max(e, a.block_err[i]);
+    e = __reduce_max_sync(0xffffffffu, e);
+    __shared__ int s_e[8];
+    if ((threadIdx.x & 31) == 0) s_e[threadIdx.x >> 5] = e;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 8; ++i) e = max(e, s_e[i]);
+      *a.err = e;
+    }
+  }
+  const int n = a.count[me];
+  const int* table = a.c.table + b * a.c.table_stride;
+  const int lane = threadIdx.x & 15;
+  uint16_t* kb = static_cast<uint16_t*>(a.c.k) + h * a.c.k_sh;
+  uint16_t* vb = static_cast<uint16_t*>(a.c.v) + h * a.c.v_sh;
+  for (int i = blockIdx.x * 16 + (threadIdx.x >> 4); i < n; i += gridDim.x * 16) {
+    const int to = a.to[me * a.pitch + i], from = a.from[me * a.pitch + i];
+    const int ti = to / a.c.page_size, fi = from / a.c.page_size;
+    const int ts = to - ti * a.c.page_size, fs = from - fi * a.c.page_size;
+    const int tp = __ldg(&table[ti]), fp = __ldg(&table[fi]);
+    const uint16_t* ks = kb + fp * a.c.k_sp + fs * a.c.k_st;
+    const uint16_t* vs = vb + fp * a.c.v_sp + fs * a.c.v_st;
+    uint16_t* kd = kb + tp * a.c.k_sp + ts * a.c.k_st;
+    uint16_t* vd = vb + tp * a.c.v_sp + ts * a.c.v_st;
+    if (a.vec) {
+      if (lane * 8 < a.c.d) {
+        const uint4 kx = *reinterpret_cast<const uint4*>(ks + lane * 8);
+        const uint4 vx = *reinterpret_cast<const uint4*>(vs + lane * 8);
+        *reinterpret_cast<uint4*>(kd + lane * 8) = kx;
+        *reinterpret_cast<uint4*>(vd + lane * 8) = vx;
+      }
+    } else {
+      for (int c = lane; c < a.c.d; c += 16) {
+        kd[c] = ks[c];
+        vd[c] = vs[c];
+      }
+    }
+    if (lane == 0) {
+      const int64_t wt = plane_at(a.c, tp, h, ts), wf = plane_at(a.c, fp, h, fs);
+      a.c.mass[wt] = a.c.mass[wf];
+      a.c.pos[wt] = a.c.pos[wf];
+    }
+  }
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+struct EvictLayout {
+  size_t block_err, count, to, from, total;
+  int64_t pitch;
+};
+// A (sequence, head) moves at most min(budget, max_seqlen - budget) tokens.
+bool evict_layout(int batch, int hkv, int max_len, int budget, EvictLayout* L) {
+  if (batch < 0 || hkv < 1 || max_len < 0 || budget < 0) return false;
+  const int64_t most = max_len > budget ? (budget < max_len - budget ? budget : max_len - budget) : 0;
+  L->pitch = most;
+  const size_t n = (size_t)batch * hkv;
+  size_t o = 256;
+  auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
+  L->block_err = take(4 * n);
+  L->count = take(4 * n);
+  L->to = take(4 * n * most);
+  L->from = take(4 * n * most);
+  L->total = o;
+  return true;
+}
+
+}  // namespace
+}  // namespace sage
+
+using namespace sage;
+
+extern "C" {
+
+int sage_paged_append(const sage_packed* k, const sage_packed* v, const sage_paged_cache* cache,
+                      const int32_t* cu_seqlens, const int32_t* positions, int batch, int tokens, int heads_kv,
+                      int head_dim, int dtype, int tensor_layout, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  if (!k || !v || !cache) return SAGE_ERR_INVALID_ARG;
+  AppendArgs a{};
+  bool vec = false;
+  const int s = make_paged_view(cache, batch, heads_kv, head_dim, dtype, tensor_layout, &a.c, &vec);
+  if (s != SAGE_OK) return s;
+  if (tokens < 0 || (!cu_seqlens && tokens != batch)) return SAGE_ERR_INVALID_ARG;
+  if (workspace && (reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < SAGE_STATUS_BYTES))
+    return SAGE_ERR_WORKSPACE;
+  if (batch == 0 || tokens == 0) return SAGE_OK;
+  if (!k->data || !v->data || reinterpret_cast<uintptr_t>(cu_seqlens) % 4 || reinterpret_cast<uintptr_t>(positions) % 4)
+    return SAGE_ERR_INVALID_ARG;
+  for (const sage_packed* t : {k, v}) {
+    if (reinterpret_cast<uintptr_t>(t->data) % 2 || t->stride_token < 0 || t->stride_head < 0) return SAGE_ERR_STRIDE;
+    vec = vec && reinterpret_cast<uintptr_t>(t->data) % 16 == 0 && t->stride_token % 8 == 0 && t->stride_head % 8 == 0;
+  }
+  if (!sage_device_supported()) return SAGE_ERR_DEVICE;
+  a.k = static_cast<const uint16_t*>(k->data); a.k_st = k->stride_token; a.k_sh = k->stride_head;
+  a.v = static_cast<const uint16_t*>(v->data); a.v_st = v->stride_token; a.v_sh = v->stride_head;
+  a.cu = cu_seqlens;
+  a.new_pos = positions;
+  a.tokens = tokens;
+  a.vec = vec ? 1 : 0;
+  a.err = static_cast<int*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (a.err) e = launch_pdl(status_clear_kernel, dim3(1), dim3(1), 0, st, a.err);
+  if (e == cudaSuccess) e = launch_pdl(append_kernel, dim3((unsigned)(((int64_t)tokens + 3) / 4)), dim3(128), 0, st, a);
+  return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "paged append");
+}
+
+size_t sage_paged_evict_workspace_size(int batch, int heads_kv, int max_seqlen, int budget) {
+  EvictLayout L;
+  return evict_layout(batch, heads_kv, max_seqlen, budget, &L) ? L.total : 0;
+}
+
+int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch, int heads_kv, int max_seqlen,
+                     int head_dim, int dtype, int tensor_layout, int budget, int sink, int recent, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (!cache) return SAGE_ERR_INVALID_ARG;
+  EvictArgs a{};
+  bool vec = false;
+  const int s = make_paged_view(cache, batch, heads_kv, head_dim, dtype, tensor_layout, &a.c, &vec);
+  if (s != SAGE_OK) return s;
+  if (max_seqlen < 0 || batch > 65535 || budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget)
+    return SAGE_ERR_INVALID_ARG;
+  if (batch == 0) return SAGE_OK;
+  if (!new_lens || new_lens == cache->seq_lens || reinterpret_cast<uintptr_t>(new_lens) % 4 || !cache->mass ||
+      !cache->positions)
+    return SAGE_ERR_INVALID_ARG;
+  EvictLayout L;
+  if (!evict_layout(batch, heads_kv, max_seqlen, budget, &L)) return SAGE_ERR_INVALID_ARG;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < L.total)
+    return SAGE_ERR_WORKSPACE;
+  if (!sage_device_supported()) return SAGE_ERR_DEVICE;
+  char* w = static_cast<char*>(workspace);
+  a.budget = budget; a.sink = sink; a.recent = recent; a.max_len = max_seqlen; a.vec = vec ? 1 : 0;
+  a.new_lens = new_lens;
+  a.err = reinterpret_cast<int*>(w);
+  a.block_err = reinterpret_cast<int*>(w + L.block_err);
+  a.count = reinterpret_cast<int*>(w + L.count);
+  a.to = reinterpret_cast<int*>(w + L.to);
+  a.from = reinterpret_cast<int*>(w + L.from);
+  a.pitch = L.pitch;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_pdl(evict_select_kernel, dim3(heads_kv, batch), dim3(kSelThreads), 0, st, a);
+  // enough CTAs to fill the GPU, sixteen tokens each and pass, none that could not have work
+  int64_t blocks = (L.pitch + 15) / 16, most = 1216 / ((int64_t)batch * heads_kv);
+  blocks = blocks < 1 ? 1 : blocks;
+  most = most < 1 ? 1 : most;
+  if (e == cudaSuccess)
+    e = launch_pdl(evict_move_kernel, dim3((unsigned)(blocks < most ? blocks : most), heads_kv, batch), dim3(256), 0, st, a);
+  return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "paged eviction");
+}
+
+}  // extern "C"

@@ -1,0 +1,365 @@
+"""Decode attention over a paged cache, appending to it and evicting from it, against float64 and
+plain loops."""
+
+import math
+
+import pytest
+import torch
+
+import paged_reference as ref
+from attn_reference import assert_close, attend
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def on_gpu(c):
+    return {n: (t.to(DEV) if torch.is_tensor(t) else t) for n, t in c.items()}
+
+
+def decode_reference(c, q, sm_scale, cap=0.0, slopes=None, kpos=None, qpos=None, hkv=1):
+    B, hq, d = q.shape
+    g = hq // hkv
+    res = dict(out=torch.zeros(B, hq, d, dtype=torch.float64), lse=torch.full((B, hq), -math.inf, dtype=torch.float64),
+               out_tol=torch.zeros(B, hq, d, dtype=torch.float64), lse_tol=torch.ones(B, hq, dtype=torch.float64), p={}, p_tol={})
+    for b, n in enumerate(c["lens"].tolist()):
+        if n == 0:
+            continue
+        for h in range(hkv):
+            bias = None
+            if slopes is not None:
+                p, s = ref.place(c, b, n)
+                where = torch.arange(n) if kpos is None else kpos[p, h, s]
+                at = n - 1 if qpos is None else int(qpos[b])
+                bias = -slopes[h * g:(h + 1) * g, None].double() * (at - where.double()).abs()
+            r = attend(q[b, h * g:(h + 1) * g], ref.rows(c, "k", b, h, n), ref.rows(c, "v", b, h, n), sm_scale, cap, bias,
+                       dtype=q.dtype)
+            for name in ("out", "lse", "out_tol", "lse_tol"):
+                res[name][b, h * g:(h + 1) * g] = r[name]
+            res["p"][b, h], res["p_tol"][b, h] = r["p"].sum(0), r["p_tol"].sum(0)
+    return res
+
+
+CASES = [
+    # lens, hq, hkv, d, page, dtype, layout, cap, slopes
+    ([1], 1, 1, 64, 16, torch.float16, "HND", 0.0, False),
+    ([1, 0, 17, 64, 65], 8, 2, 128, 16, torch.bfloat16, "HND", 0.0, False),
+    ([300, 5, 0, 129], 14, 2, 128, 7, torch.bfloat16, "NHD", 30.0, False),      # group of 7, pages of 7
+    ([63, 2000, 1], 16, 1, 64, 48, torch.float16, "NHD", 0.0, True),
+    ([500, 777], 40, 2, 72, 32, torch.float16, "HND", 20.0, True),              # group of 20: two row blocks
+    ([130, 1, 90], 6, 3, 33, 8, torch.bfloat16, "HND", 0.0, False),             # rows no 16-byte load fits
+    ([4097] * 3, 32, 8, 128, 64, torch.bfloat16, "HND", 0.0, False),
+    ([20001], 8, 8, 96, 128, torch.bfloat16, "NHD", 50.0, True),                # one sequence over many CTAs
+    ([3] * 150, 4, 4, 64, 4, torch.float16, "HND", 0.0, False),                 # more sequences than threads scan at once
+    ([0, 0], 4, 2, 64, 16, torch.float16, "HND", 0.0, False),
+]
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d,page,dtype,layout,cap,biased", CASES)
+def test_decode(lens, hq, hkv, d, page, dtype, layout, cap, biased):
+    import quantized_attention_mean_gb300 as qa
+    c = ref.make_cache(lens, hkv, d, page, dtype, layout, seed=len(lens) + d)
+    g = torch.Generator().manual_seed(5)
+    q = (torch.randn(len(lens), hq, d, generator=g) * 2).to(dtype)
+    slopes = 2.0 ** (-torch.arange(1, hq + 1).float() / 4) if biased else None
+    G = on_gpu(c)
+    ws = qa.alloc_workspace(qa.paged_attn_workspace_bytes(len(lens), hq, hkv, max(lens), d), DEV)
+    ws.fill_(255)
+    out, lse = qa.paged_attn(q.to(DEV), G["k"], G["v"], G["table"], G["lens"], max(lens), tensor_layout=layout,
+                             softcap=cap, slopes=None if slopes is None else slopes.to(DEV), return_lse=True, workspace=ws)
+    assert qa.read_device_status(ws) == 0
+    r = decode_reference(c, q, 1 / math.sqrt(d), cap, slopes, hkv=hkv)
+    assert_close(out, r["out"], r["out_tol"] + 1e-12, "out")
+    assert_close(lse, r["lse"], r["lse_tol"], "lse")
+
+
+def test_decode_positions_strides_and_scale():
+    # explicit positions in an order of their own, a cache that is a slice of a wider one, strided q and out
+    import quantized_attention_mean_gb300 as qa
+    c = ref.make_cache([200, 33], 2, 64, 16, torch.float16, "HND")
+    hkv, d, hq = 2, 64, 8
+    g = torch.Generator().manual_seed(1)
+    kpos = torch.randint(0, 5000, (c["k"].shape[0], hkv, 16), generator=g, dtype=torch.int32)
+    qpos = torch.tensor([5001, 77], dtype=torch.int32)
+    q = torch.randn(2, hq, d, generator=g).half()
+    slopes = torch.linspace(0.001, 0.02, hq)
+    G = on_gpu(c)
+    wide = torch.zeros(c["k"].shape[0], hkv, 16, 2 * d + 8, dtype=torch.float16, device=DEV)
+    wide[..., 8:8 + d], wide[..., 8 + d:] = G["k"], G["v"]
+    qw = torch.zeros(2, 2 * hq, d, dtype=torch.float16, device=DEV)
+    qw[:, ::2] = q.to(DEV)
+    ow = torch.full((2, 2 * hq, d), 9.0, dtype=torch.float16, device=DEV)
+    lse = torch.empty(2, hq, device=DEV)
+    qa.paged_attn(qw[:, ::2], wide[..., 8:8 + d], wide[..., 8 + d:], G["table"], G["lens"], 999, sm_scale=0.3,
+                  slopes=slopes.to(DEV), key_positions=kpos.to(DEV), q_positions=qpos.to(DEV), return_lse=True,
+                  out=ow[:, ::2], lse=lse)
+    r = decode_reference(c, q, 0.3, 0.0, slopes, kpos, qpos, hkv)
+    assert_close(ow[:, ::2], r["out"], r["out_tol"], "out")
+    assert_close(lse, r["lse"], r["lse_tol"], "lse")
+    assert (ow[:, 1::2] == 9).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d,cap", [(8, 2, 128, 0.0), (20, 1, 64, 30.0), (3, 3, 40, 0.0)])
+def test_decode_accumulates_weights(hq, hkv, d, cap):
+    import quantized_attention_mean_gb300 as qa
+    lens = [700, 1, 0, 65]
+    c = ref.make_cache(lens, hkv, d, 16, torch.bfloat16)
+    g = torch.Generator().manual_seed(2)
+    q = torch.randn(4, hq, d, generator=g).bfloat16()
+    mass0 = torch.rand(c["k"].shape[0], hkv, 16, generator=g)
+    G, mass = on_gpu(c), mass0.to(DEV)
+    for _ in range(2):
+        qa.paged_attn(q.to(DEV), G["k"], G["v"], G["table"], G["lens"], 700, softcap=cap, mass=mass)
+    r = decode_reference(c, q, 1 / math.sqrt(d), cap, hkv=hkv)
+    want, tol = mass0.double(), mass0.double() * 2.0 ** -22 + 1e-7
+    for (b, h), p in r["p"].items():
+        at, s = ref.place(c, b, lens[b])
+        want[at, h, s] += 2 * p
+        tol[at, h, s] += 2 * r["p_tol"][b, h] + 2 * p * 2.0 ** -22
+    assert_close(mass, want, tol, "mass")
+
+
+def test_decode_masked_garbage_and_nan():
+    # slots behind a sequence's end and unused pages hold NaN: nothing of them may show
+    import quantized_attention_mean_gb300 as qa
+    lens = [70, 5]
+    c = ref.make_cache(lens, 2, 128, 16, torch.bfloat16)
+    clean = {n: t.clone() if torch.is_tensor(t) else t for n, t in c.items()}
+    used = torch.zeros(c["k"].shape[0], 16, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        p, s = ref.place(c, b, n)
+        used[p, s] = True
+    for w in "kv":
+        c[w][(~used)[:, None, :].expand(-1, 2, -1)] = math.nan
+    q = torch.randn(2, 8, 128).bfloat16()
+    G = on_gpu(c)
+    out = qa.paged_attn(q.to(DEV), G["k"], G["v"], G["table"], G["lens"], 70)
+    r = decode_reference(clean, q, 1 / math.sqrt(128), hkv=2)
+    assert_close(out, r["out"], r["out_tol"], "out")
+
+
+def test_decode_reports_bad_lengths_and_pages():
+    import quantized_attention_mean_gb300 as qa
+    c = ref.make_cache([40, 40, 40], 2, 64, 16, torch.float16)
+    q = torch.randn(3, 4, 64).half().to(DEV)
+    G = on_gpu(c)
+    ws = qa.alloc_workspace(qa.paged_attn_workspace_bytes(3, 4, 2, 40, 64), DEV)
+    good = qa.paged_attn(q, G["k"], G["v"], G["table"], G["lens"], 40, workspace=ws)
+    assert qa.read_device_status(ws) == 0
+    for bad in (-1, 41, 49, 2 ** 31 - 1):
+        lens = G["lens"].clone()
+        lens[1] = bad
+        out, lse = qa.paged_attn(q, G["k"], G["v"], G["table"], lens, 40 if bad != 49 else 10 ** 6, workspace=qa.alloc_workspace(
+            qa.paged_attn_workspace_bytes(3, 4, 2, 10 ** 6, 64), DEV) if bad == 49 else ws, return_lse=True)
+        if bad != 49:
+            assert qa.read_device_status(ws) == 12
+        assert (out[1] == 0).all() and (lse[1] == -math.inf).all()
+        assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+    for bad in (-1, c["k"].shape[0], 2 ** 31 - 1):
+        table = G["table"].clone()
+        table[2, 1] = bad
+        out = qa.paged_attn(q, G["k"], G["v"], table, G["lens"], 40, workspace=ws)
+        assert qa.read_device_status(ws) == 13
+        assert torch.equal(out[:2], good[:2]) and torch.isfinite(out).all()
+    qa.paged_attn(q, G["k"], G["v"], G["table"], G["lens"], 40, workspace=ws)
+    assert qa.read_device_status(ws) == 0
+
+
+APPENDS = [
+    # old lengths, new counts (None: one each), hkv, d, page, dtype, layout
+    ([0, 15, 16, 100], None, 8, 128, 16, torch.bfloat16, "HND"),
+    ([3, 0, 50], [5, 0, 130], 2, 64, 7, torch.float16, "NHD"),
+    ([10, 2], [1, 33], 3, 35, 8, torch.bfloat16, "NHD"),
+    ([0], [1000], 1, 80, 64, torch.float16, "HND"),
+]
+
+
+@pytest.mark.parametrize("old,new,hkv,d,page,dtype,layout", APPENDS)
+@pytest.mark.parametrize("planes", [False, True])
+def test_append(old, new, hkv, d, page, dtype, layout, planes):
+    import quantized_attention_mean_gb300 as qa
+    counts = [1] * len(old) if new is None else new
+    tail = 0 if new is None else 3                      # tokens behind the last sequence
+    c = ref.make_cache(old, hkv, d, page, dtype, layout, room=max(counts))
+    g = torch.Generator().manual_seed(3)
+    T = sum(counts) + tail
+    k, v = (torch.randn(T, hkv, d, generator=g).to(dtype) for _ in "kv")
+    cu = torch.tensor([0] + list(torch.tensor(counts).cumsum(0)), dtype=torch.int32)
+    mass = torch.full((c["k"].shape[0], hkv, page), 5.0) if planes else None
+    kpos = torch.full((c["k"].shape[0], hkv, page), -3, dtype=torch.int32) if planes else None
+    pos = torch.randint(0, 9999, (T,), generator=g, dtype=torch.int32) if planes else None
+    G = on_gpu(c)
+    gm, gp, gpos = (None if t is None else t.to(DEV) for t in (mass, kpos, pos))
+    ws = qa.alloc_workspace(256, DEV)
+    qa.paged_append(k.to(DEV), v.to(DEV), G["k"], G["v"], G["table"], G["lens"],
+                    cu_seqlens=None if new is None else cu.to(DEV), tensor_layout=layout, mass=gm, key_positions=gp,
+                    positions=gpos, workspace=ws)
+    assert qa.read_device_status(ws) == 0
+    t = 0
+    for b, n in enumerate(counts):
+        p, s = ref.place(c, b, old[b] + n)
+        for i in range(old[b], old[b] + n):
+            for h in range(hkv):
+                ref.set_row(c, "k", p[i], h, s[i], k[t, h])
+                ref.set_row(c, "v", p[i], h, s[i], v[t, h])
+                if planes:
+                    mass[p[i], h, s[i]] = 0.0
+                    kpos[p[i], h, s[i]] = pos[t]
+            t += 1
+    assert torch.equal(G["k"].cpu(), c["k"]) and torch.equal(G["v"].cpu(), c["v"])
+    if planes:
+        assert torch.equal(gm.cpu(), mass) and torch.equal(gp.cpu(), kpos)
+
+
+def test_append_leaves_out_what_has_no_place():
+    import quantized_attention_mean_gb300 as qa
+    c = ref.make_cache([40, 40, 40], 2, 64, 16, torch.float16)      # three pages each: room for 48
+    G = on_gpu(c)
+    ws = qa.alloc_workspace(256, DEV)
+    k = torch.ones(3, 2, 64, dtype=torch.float16, device=DEV)
+    before = G["k"].clone()
+    lens = torch.tensor([48, -1, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    qa.paged_append(k, k, G["k"], G["v"], G["table"], lens, workspace=ws)
+    assert qa.read_device_status(ws) == 12 and torch.equal(G["k"], before)
+    table = G["table"].clone()
+    table[:, 2] = torch.tensor([-1, c["k"].shape[0], 2 ** 31 - 1], dtype=torch.int32)
+    qa.paged_append(k, k, G["k"], G["v"], table, G["lens"], workspace=ws)
+    assert qa.read_device_status(ws) == 13 and torch.equal(G["k"], before)
+    qa.paged_append(k, k, G["k"], G["v"], G["table"], G["lens"], workspace=ws)
+    assert qa.read_device_status(ws) == 0 and not torch.equal(G["k"], before)
+
+
+EVICTIONS = [
+    # lens, hkv, d, page, dtype, layout, budget, sink, recent, ties
+    ([100, 64, 65, 3, 0], 2, 64, 16, torch.float16, "HND", 64, 4, 16, False),
+    ([1500, 40], 3, 128, 7, torch.bfloat16, "NHD", 33, 0, 0, True),
+    ([2, 9], 1, 20, 4, torch.bfloat16, "HND", 1, 0, 1, False),
+    ([5000], 2, 72, 64, torch.float16, "NHD", 2500, 10, 1200, True),
+    ([1030], 1, 64, 128, torch.float16, "HND", 1024, 0, 1024, False),
+]
+
+
+@pytest.mark.parametrize("lens,hkv,d,page,dtype,layout,budget,sink,recent,ties", EVICTIONS)
+def test_evict(lens, hkv, d, page, dtype, layout, budget, sink, recent, ties):
+    import quantized_attention_mean_gb300 as qa
+    c = ref.make_cache(lens, hkv, d, page, dtype, layout, seed=9)
+    g = torch.Generator().manual_seed(4)
+    shape = (c["k"].shape[0], hkv, page)
+    mass = torch.exp(3 * torch.randn(shape, generator=g))
+    if ties:
+        mass = torch.randint(0, 3, shape, generator=g).float()
+        mass[torch.rand(shape, generator=g) < 0.1] = -0.0
+        mass[torch.rand(shape, generator=g) < 0.05] = math.nan
+        mass[torch.rand(shape, generator=g) < 0.05] = -math.inf
+        mass[torch.rand(shape, generator=g) < 0.05] = math.inf
+    pos = torch.zeros(shape, dtype=torch.int32)
+    for b, n in enumerate(lens):
+        p, s = ref.place(c, b, n)
+        for h in range(hkv):
+            pos[p, h, s] = torch.randperm(n, generator=g).to(torch.int32) + 100 * b
+    G, gm, gp = on_gpu(c), mass.to(DEV), pos.to(DEV)
+    ws = qa.alloc_workspace(qa.paged_evict_workspace_bytes(len(lens), hkv, max(lens), budget), DEV)
+    ws.fill_(255)
+    new = qa.paged_evict(G["k"], G["v"], gm, gp, G["table"], G["lens"], budget, max(lens), sink=sink, recent=recent,
+                         tensor_layout=layout, workspace=ws)
+    assert qa.read_device_status(ws) == 0
+    want = ref.evict(c, mass, pos, budget, sink, recent)
+    assert torch.equal(new.cpu(), want)
+    assert torch.equal(gp.cpu(), pos)
+    assert torch.equal(gm.cpu().view(torch.int32), mass.view(torch.int32))
+    assert torch.equal(G["k"].cpu(), c["k"]) and torch.equal(G["v"].cpu(), c["v"])
+
+
+def test_evict_reports_bad_lengths_and_pages():
+    import quantized_attention_mean_gb300 as qa
+    c = ref.make_cache([60, 60], 2, 64, 16, torch.float16)
+    G = on_gpu(c)
+    shape = (c["k"].shape[0], 2, 16)
+    ws = qa.alloc_workspace(qa.paged_evict_workspace_bytes(2, 2, 60, 20), DEV)
+    for what in ("length", "page"):
+        mass, pos = torch.rand(shape, device=DEV), torch.zeros(shape, dtype=torch.int32, device=DEV)
+        lens, table, k = G["lens"].clone(), G["table"].clone(), G["k"].clone()
+        if what == "length":
+            lens[0] = 65
+        else:
+            table[0, 3] = c["k"].shape[0]
+        qa.paged_evict(k, G["v"].clone(), mass, pos, table, lens, 20, 60, workspace=ws)
+        assert qa.read_device_status(ws) == (12 if what == "length" else 13)
+        used = G["table"][0, :3].long()
+        assert torch.equal(k[used], G["k"][used])                 # the bad sequence is left as it was
+
+
+def test_serving_loop_with_eviction():
+    """Prompt, decode steps and evictions as a server runs them, against the same on the CPU."""
+    import quantized_attention_mean_gb300 as qa
+    B, hq, hkv, d, page, budget = 2, 4, 2, 64, 8, 24
+    dtype = torch.float16
+    g = torch.Generator().manual_seed(11)
+    c = ref.make_cache([0, 0], hkv, d, page, dtype, room=64)
+    c["k"].zero_(), c["v"].zero_()
+    shape = (c["k"].shape[0], hkv, page)
+    mass, pos = torch.zeros(shape), torch.zeros(shape, dtype=torch.int32)
+    slopes = torch.tensor([0.5, 0.25, 0.125, 0.0625])
+    G, gm, gp, gs = on_gpu(c), mass.to(DEV), pos.to(DEV), slopes.to(DEV)
+    lens, told = G["lens"], torch.zeros(B, dtype=torch.int32)   # told: the next position of each sequence
+    for step, counts in enumerate([[30, 11]] + [[1, 1]] * 12):
+        T = sum(counts)
+        k, v = (torch.randn(T, hkv, d, generator=g).to(dtype) for _ in "kv")
+        q = torch.randn(B, hq, d, generator=g).to(dtype)
+        cu = torch.tensor([0, counts[0], T], dtype=torch.int32)
+        new_pos = torch.cat([told[b] + torch.arange(n) for b, n in enumerate(counts)]).to(torch.int32)
+        qa.paged_append(k.to(DEV), v.to(DEV), G["k"], G["v"], G["table"], lens, cu_seqlens=cu.to(DEV), mass=gm,
+                        key_positions=gp, positions=new_pos.to(DEV))
+        lens = lens + torch.tensor(counts, dtype=torch.int32, device=DEV)
+        told += torch.tensor(counts, dtype=torch.int32)
+        out = qa.paged_attn(q.to(DEV), G["k"], G["v"], G["table"], lens, 64, slopes=gs, key_positions=gp,
+                            q_positions=(told - 1).to(DEV), mass=gm)
+        # the CPU's copy, from the device's state before the eviction
+        c.update(k=G["k"].cpu(), v=G["v"].cpu(), lens=lens.cpu())
+        r = decode_reference(c, q, 1 / math.sqrt(d), 0.0, slopes, gp.cpu(), told - 1, hkv)
+        assert_close(out, r["out"], r["out_tol"], f"out of step {step}")
+        mass, pos = gm.cpu(), gp.cpu()
+        want = ref.evict(c, mass, pos, budget, 2, 6)
+        lens = qa.paged_evict(G["k"], G["v"], gm, gp, G["table"], lens, budget, 64, sink=2, recent=6)
+        assert torch.equal(lens.cpu(), want) and torch.equal(gp.cpu(), pos) and torch.equal(gm.cpu(), mass)
+        assert torch.equal(G["k"].cpu(), c["k"]) and torch.equal(G["v"].cpu(), c["v"])
+
+
+def test_decode_step_in_a_graph_and_on_another_stream():
+    import quantized_attention_mean_gb300 as qa
+    lens = [500, 33, 64]
+    c = ref.make_cache(lens, 2, 128, 16, torch.bfloat16, room=4)
+    G = on_gpu(c)
+    q = torch.randn(3, 8, 128).bfloat16().to(DEV)
+    k = torch.randn(3, 2, 128).bfloat16().to(DEV)
+    ws = qa.alloc_workspace(qa.paged_attn_workspace_bytes(3, 8, 2, 600, 128), DEV)
+    out = torch.empty_like(q)
+    lens_new = G["lens"] + 1
+
+    def step(stream=None):
+        qa.paged_append(k, k, G["k"], G["v"], G["table"], G["lens"], stream=stream)
+        qa.paged_attn(q, G["k"], G["v"], G["table"], lens_new, 600, out=out, workspace=ws, stream=stream)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step(side)
+    torch.cuda.synchronize()
+    eager = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
+    q.mul_(0.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not torch.equal(out, eager)
+    # outputs that the call allocates on another stream belong to that stream
+    with torch.cuda.stream(side):
+        side.wait_stream(torch.cuda.current_stream())
+    mine = qa.paged_attn(q, G["k"], G["v"], G["table"], lens_new, 600, stream=side)
+    side.synchronize()
+    assert torch.equal(mine, out)
