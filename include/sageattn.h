@@ -227,6 +227,37 @@ int sage_merge_partials(const sage_tensor* outs, const float* const* lses, int n
                         const sage_tensor* out, float* lse_out, int batch, int heads,
                         int seqlen, int head_dim, int dtype, int tensor_layout, void* stream);
 
+/* ---- Attention with modified scores, on 16-bit operands ----
+ * For the layers that the quantised calls cannot take: capped or biased scores, document and
+ * prefix masks.
+ *   s_ij = sm_scale q_i.k_j;  softcap > 0: s = softcap tanh(s / softcap);
+ *   slopes: s -= slopes[h] |i + q_offset - j|
+ *   visible(i, j) = (!is_causal || j <= i + q_offset || j < prefix_lens[b])
+ *                   && (no documents || (doc_q[b][i] == doc_k[b][j] && doc_k[b][j] >= 0))
+ *   out_i = sum_j softmax over the visible j of s_ij, times v_j;  lse_i = ln sum_j exp s_ij
+ * Q K^T and P V are products of the inputs' type with fp32 sums; the softmax is fp32, and its weights
+ * are rounded once to the inputs' type for P V. A row that sees no key gets out = 0 and lse = -inf, and
+ * so does a row all of whose visible scores are -inf.
+ *   q, k, v, out, tensor_layout, is_causal, sm_scale, lse, return_lse: as sage_attn. q_offset shifts the
+ *   queries' positions (the next chunk of a prompt: the number of keys before it); it may be negative.
+ *   slopes: device float [Hq] or NULL. prefix_lens: device int32 [B] or NULL; only with is_causal.
+ *   doc_q [B, Nq], doc_k [B, Nk]: device int32, contiguous, both or neither. A negative id is padding,
+ *   which sees nothing and is seen by nothing; its rows of k and v may hold anything. Apart from
+ *   padding, a key that some row of the call sees must have finite v (a weight of 0 times an infinity
+ *   is NaN in the rows that do not see it).
+ *   workspace: sage_scored_attn_workspace_size() bytes; `packed` != 0 where q, k and v all have 16-byte
+ *   aligned rows (address, and strides and head_dim multiples of 8 elements; no zero stride of a
+ *   dimension longer than 1) and need no padded copy there.
+ * Nq == 0 or B == 0 is a no-op; Nk == 0 writes 0 and -inf. */
+size_t sage_scored_attn_workspace_size(int batch, int heads_q, int heads_kv, int seqlen_q, int seqlen_k,
+                                       int head_dim, int packed);
+int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tensor* v,
+                     const sage_tensor* out, float* lse, const float* slopes,
+                     const int32_t* prefix_lens, const int32_t* doc_q, const int32_t* doc_k, int batch,
+                     int heads_q, int heads_kv, int seqlen_q, int seqlen_k, int head_dim, int dtype,
+                     int tensor_layout, int is_causal, float sm_scale, float softcap, int q_offset,
+                     int return_lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- A paged key-value cache ----
  * k, v: device FP16/BF16 [num_pages, Hkv, page_size, d] (HND) or [num_pages, page_size, Hkv, d] (NHD), any
  * strides of the first three dimensions (k_stride, v_stride, in that order), channel stride 1.
@@ -255,8 +286,7 @@ typedef struct {
 #define SAGE_STATUS_BYTES ((size_t)256) /* workspace of a call that needs only its status word */
 
 /* Attention of one new token per sequence over its held tokens (its own K and V appended before).
- *   s_j = sm_scale q.k_j;  softcap > 0: s = softcap tanh(s / softcap);
- *   slopes: s -= slopes[h] |q_position - position of key j|
+ * Scores as sage_scored_attn's: capped, then biased by slopes[h] |q_position - position of the key|.
  *   q, out: [batch, Hq, d] (stride_token is the sequence's); lse: device float [batch, Hq] or NULL.
  *   slopes: device float [Hq] or NULL; q_positions: device int32 [batch] or NULL (seq_len - 1).
  *   max_seqlen: an upper bound of seq_lens. cache->mass, where not NULL: each held token's weight,

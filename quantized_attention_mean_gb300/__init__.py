@@ -400,6 +400,7 @@ __all__ = ["sage_attn", "sage_attn_varlen", "sage_attn_fp4", "SageError", "works
 
 from .paged import (paged_append, paged_attn, paged_attn_workspace_bytes, paged_evict,  # noqa: E402
                     paged_evict_workspace_bytes)
+from .scored import scored_attn, scored_attn_workspace_bytes  # noqa: E402
 
-__all__ += ["paged_attn", "paged_append", "paged_evict", "paged_attn_workspace_bytes",
+__all__ += ["scored_attn", "scored_attn_workspace_bytes", "paged_attn", "paged_append", "paged_evict", "paged_attn_workspace_bytes",
             "paged_evict_workspace_bytes"]

@@ -67,6 +67,9 @@ SIGNATURES = {
     # layout, stream
     "sage_merge_partials": (c_int, [c_void_p, c_void_p, c_int, _T, c_void_p] + [c_int] * 6
                             + [c_void_p]),
+    "sage_scored_attn_workspace_size": (c_size_t, [c_int] * 7),
+    "sage_scored_attn": (c_int, [_T, _T, _T, _T, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]
+                         + [c_int] * 9 + [c_float] * 2 + [c_int] * 2 + [c_void_p, c_size_t, c_void_p]),
     "sage_paged_attn_workspace_size": (c_size_t, [c_int] * 6),
     "sage_paged_attn": (c_int, [_P, _C, _P, c_void_p, c_void_p, c_void_p] + [c_int] * 7
                         + [c_float] * 2 + [c_void_p, c_size_t, c_void_p]),

@@ -48,6 +48,12 @@ cudaError_t raise_smem_limit(K* kernel, int bytes, std::atomic<int> (&limits)[64
 // SAGE_ERR_CUDA.
 int note_cuda_failure(cudaError_t e, const char* where);
 
+// 4-d tiled map (128-byte swizzle) of 16-bit rows: dims (inner, rows, heads, batch), byte strides of
+// the last three, box (box_inner, box_rows, 1, 1); what lies outside reads as zero.
+bool make_map4(CUtensorMap* m, bool bf16, const void* base, uint64_t inner, uint64_t rows, uint64_t heads,
+               uint64_t batch, uint64_t row_bytes, uint64_t head_bytes, uint64_t batch_bytes,
+               uint32_t box_inner, uint32_t box_rows);
+
 cudaError_t launch_varlen_setup(const Problem& p, cudaStream_t st);
 cudaError_t launch_kv_stats(const Problem& p, int max_len_k, cudaStream_t st);
 cudaError_t launch_short_status_clear(int* err, int words, cudaStream_t st);

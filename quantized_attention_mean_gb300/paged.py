@@ -39,7 +39,7 @@ def _ptr(t):
 def _check_small(name, t, shape, dtype, device):
     if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device
                           or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} {list(shape)} tensor on the cache's device")
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} {list(shape)} tensor on the inputs' device")
 
 
 def _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions):

@@ -1,0 +1,71 @@
+"""Attention with modified scores: capped by a tanh, biased by distance, under document and prefix
+masks, on 16-bit operands. For the layers whose scores the quantised calls cannot take."""
+
+import ctypes
+
+import torch
+
+from . import DTYPE, LAYOUT, _check, _check_dense_args, _dims, _lib, _stream_ptr, _tensor, alloc_workspace
+from .paged import _check_small, _on, _ptr
+
+__all__ = ["scored_attn", "scored_attn_workspace_bytes"]
+
+
+def _addressable(t):
+    """Whether the kernel can read t's rows in place (otherwise they are copied to the workspace)."""
+    return (t.shape[3] % 8 == 0 and t.data_ptr() % 16 == 0
+            and all(n <= 1 or (s > 0 and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()[:3])))
+
+
+def scored_attn_workspace_bytes(batch, heads_q, heads_kv, seqlen_q, seqlen_k, head_dim, packed=True):
+    """``packed``: q, k and v have 16-byte aligned rows (address, strides and head_dim)."""
+    return _lib.load().sage_scored_attn_workspace_size(batch, heads_q, heads_kv, seqlen_q, seqlen_k, head_dim,
+                                                       int(bool(packed)))
+
+
+def scored_attn(q, k, v, tensor_layout="HND", is_causal=False, sm_scale=None, softcap=0.0, slopes=None,
+                prefix_lens=None, doc_ids=None, doc_ids_k=None, q_offset=0, return_lse=False, out=None, lse=None,
+                workspace=None, stream=None):
+    """Attention forward with modified scores; q, k, v, tensor_layout, sm_scale, out and lse as ``sage_attn``.
+
+        s = sm_scale q·k;  softcap > 0: s = softcap·tanh(s / softcap);  slopes: s -= slopes[h]·|i + q_offset - j|
+
+    Key j is visible to query i when (not is_causal, or j <= i + q_offset, or j < prefix_lens[b]) and, with
+    documents, doc_ids[b, i] == doc_ids_k[b, j] >= 0. ``slopes`` fp32 [Hq]; ``prefix_lens`` int32 [B], with
+    is_causal; ``doc_ids`` int32 [B, Nq] and ``doc_ids_k`` int32 [B, Nk] (default: doc_ids, Nq == Nk). A negative
+    id is padding, whose rows of k and v may hold anything. ``q_offset``: how many keys lie before the first
+    query (the next chunk of a prompt). A row that sees no key gives 0 and lse -inf.
+    Returns out, plus lse [B, Hq, Nq] fp32 if return_lse."""
+    _check_dense_args(q, k, v, tensor_layout, out, lse, return_lse, workspace)
+    B, hq, hkv, nq, nk, d = _dims(q, k, tensor_layout)
+    dev = q.device
+    if doc_ids is None and doc_ids_k is not None:
+        raise ValueError("doc_ids_k needs doc_ids")
+    if doc_ids is not None and doc_ids_k is None:
+        if nq != nk:
+            raise ValueError("with Nq != Nk the keys' documents need doc_ids_k")
+        doc_ids_k = doc_ids
+    if prefix_lens is not None and not is_causal:
+        raise ValueError("prefix_lens needs is_causal")
+    _check_small("slopes", slopes, (hq,), torch.float32, dev)
+    _check_small("prefix_lens", prefix_lens, (B,), torch.int32, dev)
+    _check_small("doc_ids", doc_ids, (B, nq), torch.int32, dev)
+    _check_small("doc_ids_k", doc_ids_k, (B, nk), torch.int32, dev)
+    lib = _lib.load()
+    with torch.cuda.device(dev), _on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if return_lse and lse is None:
+            lse = torch.empty((B, hq, nq), dtype=torch.float32, device=dev)
+        if workspace is None:
+            packed = _addressable(q) and _addressable(k) and _addressable(v)
+            workspace = alloc_workspace(lib.sage_scored_attn_workspace_size(B, hq, hkv, nq, nk, d, int(packed)), dev)
+        st = lib.sage_scored_attn(ctypes.byref(_tensor(q)), ctypes.byref(_tensor(k)), ctypes.byref(_tensor(v)),
+                                  ctypes.byref(_tensor(out)), _ptr(lse if return_lse else None), _ptr(slopes),
+                                  _ptr(prefix_lens), _ptr(doc_ids), _ptr(doc_ids_k), B, hq, hkv, nq, nk, d,
+                                  DTYPE[q.dtype], LAYOUT[tensor_layout], int(bool(is_causal)),
+                                  float("nan") if sm_scale is None else float(sm_scale), float(softcap),
+                                  int(q_offset), int(bool(return_lse)), _ptr(workspace), workspace.numel(),
+                                  _stream_ptr(stream))
+    _check(st, "scored_attn")
+    return (out, lse) if return_lse else out

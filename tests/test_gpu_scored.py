@@ -1,0 +1,269 @@
+"""Attention with modified scores against float64: caps, distance bias, causal, prefix and document
+masks, at the sizes where tiles, splits and layouts end."""
+
+import math
+
+import pytest
+import torch
+
+from attn_reference import assert_close, attend
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def docs_of(lengths, pad, B=1, shuffle=False, seed=0):
+    ids = torch.cat([torch.full((n,), i) for i, n in enumerate(lengths)] + [torch.full((pad,), -1)]).to(torch.int32)
+    ids = ids[None].repeat(B, 1)
+    if shuffle:
+        g = torch.Generator().manual_seed(seed)
+        ids = torch.stack([r[torch.randperm(r.numel(), generator=g)] for r in ids])
+    return ids.contiguous()
+
+
+def visible(nq, nk, B, causal, offset, prefix, dq, dk):
+    i, j = torch.arange(nq)[:, None] + offset, torch.arange(nk)[None]
+    seen = torch.ones(B, nq, nk, dtype=torch.bool)
+    if causal:
+        seen = (j <= i)[None].expand(B, nq, nk).clone()
+        if prefix is not None:
+            seen |= (j[None] < prefix[:, None, None])
+    if dq is not None:
+        seen &= (dq[:, :, None] == dk[:, None, :]) & (dk[:, None, :] >= 0)
+    return seen
+
+
+def check(B, hq, hkv, nq, nk, d, dtype, layout="HND", causal=False, cap=0.0, bias=False, prefix=None, dq=None, dk=None,
+          offset=0, scale=None, q=None, k=None, v=None, place=None, clean=None, seed=0):
+    import quantized_attention_mean_gb300 as qa
+    g = torch.Generator().manual_seed(seed + nq + d)
+    q = (torch.randn(B, hq, nq, d, generator=g) * 2).to(dtype) if q is None else q
+    k = torch.randn(B, hkv, nk, d, generator=g).to(dtype) if k is None else k
+    v = torch.randn(B, hkv, nk, d, generator=g).to(dtype) if v is None else v
+    slopes = 2.0 ** (-torch.arange(1, hq + 1).float() * 8 / hq) if bias else None
+    prefix = None if prefix is None else torch.tensor(prefix, dtype=torch.int32)
+    dk = dq if dk is None else dk
+    gpu = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    lay = lambda t: gpu(t if layout == "HND" else t.transpose(1, 2).contiguous())  # noqa: E731
+    lay = place or lay
+    ws = qa.alloc_workspace(qa.scored_attn_workspace_bytes(B, hq, hkv, nq, nk, d, packed=False), DEV)
+    ws.fill_(255)
+    out, lse = qa.scored_attn(lay(q), lay(k), lay(v), tensor_layout=layout, is_causal=causal, softcap=cap, sm_scale=scale,
+                              slopes=gpu(slopes), prefix_lens=gpu(prefix), doc_ids=gpu(dq), doc_ids_k=gpu(dk),
+                              q_offset=offset, return_lse=True, workspace=ws)
+    assert qa.read_device_status(ws) == 0
+    seen = visible(nq, nk, B, causal, offset, prefix, dq, dk)[:, None]
+    grp = hq // hkv
+    kk, vv = (t.repeat_interleave(grp, 1).to(DEV) for t in (k, v if clean is None else clean))
+    if clean is not None:
+        kk = torch.where(torch.isfinite(kk.float()), kk, torch.zeros_like(kk))
+    b = None
+    if bias:
+        dist = (torch.arange(nq)[:, None] + offset - torch.arange(nk)).abs().double()
+        b = (-slopes.double()[:, None, None] * dist)[None].to(DEV)
+    r = attend(q.to(DEV), kk, vv, d ** -0.5 if scale is None else scale, cap, b, seen.expand(B, hq, nq, nk).to(DEV), dtype)
+    o = out if layout == "HND" else out.transpose(1, 2)
+    assert_close(o, r["out"], r["out_tol"], "out")
+    assert_close(lse, r["lse"], r["lse_tol"], "lse")
+    return out, lse
+
+
+F, H = torch.float16, torch.bfloat16
+SIZES = [
+    # B, hq, hkv, nq, nk, d, dtype, layout
+    (1, 1, 1, 1, 1, 64, F, "HND"),
+    (2, 4, 2, 1, 130, 128, H, "NHD"),
+    (1, 2, 1, 128, 128, 64, H, "HND"),
+    (1, 2, 2, 129, 127, 128, F, "HND"),
+    (2, 3, 1, 257, 400, 64, F, "NHD"),
+    (1, 2, 2, 300, 513, 72, H, "HND"),
+    (1, 4, 4, 65, 1000, 96, F, "NHD"),
+    (1, 2, 1, 50, 70, 33, F, "HND"),       # rows that TMA cannot address
+    (2, 2, 1, 140, 140, 20, H, "NHD"),
+    (1, 2, 2, 700, 700, 8, H, "HND"),
+]
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (15.0, False), (0.0, True), (15.0, True)])
+def test_full(size, cap, bias):
+    B, hq, hkv, nq, nk, d, dtype, layout = size
+    check(B, hq, hkv, nq, nk, d, dtype, layout, cap=cap, bias=bias)
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, True)])
+def test_causal_with_offset(size, cap, bias):
+    B, hq, hkv, nq, nk, d, dtype, layout = size
+    for offset in {0, nk - nq, -5, nk}:
+        check(B, hq, hkv, nq, nk, d, dtype, layout, causal=True, cap=cap, bias=bias, offset=offset)
+
+
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (10.0, False), (0.0, True), (10.0, True)])
+@pytest.mark.parametrize("d,dtype", [(64, H), (128, F)])
+def test_prefix(cap, bias, d, dtype):
+    for prefix in ([0, 300, 77], [128, 1, 299], [-4, 1000, 129]):
+        check(3, 2, 1, 300, 300, d, dtype, causal=True, prefix=prefix, cap=cap, bias=bias)
+    check(1, 2, 1, 100, 900, d, dtype, causal=True, prefix=[640], offset=3, cap=cap, bias=bias)
+
+
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, False), (0.0, True), (20.0, True)])
+@pytest.mark.parametrize("d,dtype,layout", [(64, F, "NHD"), (128, H, "HND")])
+@pytest.mark.parametrize("causal", [False, True])
+def test_documents(cap, bias, d, dtype, layout, causal):
+    for lengths, pad in (([600], 0), ([1, 127, 128, 129, 200], 15), ([300, 5, 5, 5, 200], 130), ([], 600), ([7] * 80, 40)):
+        dq = docs_of(lengths, pad, 2)
+        check(2, 2, 1, dq.shape[1], dq.shape[1], d, dtype, layout, causal=causal, cap=cap, bias=bias, dq=dq)
+    dq = docs_of([200, 100, 30], 20, 2, shuffle=True)
+    check(2, 2, 1, 350, 350, d, dtype, layout, causal=causal, cap=cap, bias=bias, dq=dq)
+    # other documents on the key side, some of them nobody's
+    dk = docs_of([50, 0, 120, 300], 33, 1)
+    check(1, 2, 1, 300, dk.shape[1], d, dtype, layout, cap=cap, bias=bias, dq=docs_of([100, 100, 90], 10, 1), dk=dk)
+    # with a prefix
+    check(2, 2, 1, 350, 350, d, dtype, layout, causal=True, cap=cap, bias=bias, dq=docs_of([200, 150], 0, 2),
+          prefix=[140, 260])
+
+
+@pytest.mark.parametrize("nq,nk,hq", [(1, 20000, 2), (100, 9001, 4), (128, 4096, 1), (300, 2500, 1), (5, 513, 1)])
+@pytest.mark.parametrize("d,dtype", [(64, F), (128, H)])
+def test_few_rows_are_split_over_the_keys(nq, nk, hq, d, dtype):
+    check(1, hq, 1, nq, nk, d, dtype, causal=True, offset=nk - nq)
+    check(1, hq, 1, nq, nk, d, dtype, causal=True, offset=nk // 3, bias=True, cap=12.0)
+    # one of the keys' documents, from somewhere in their middle, and padding
+    check(1, hq, 1, nq, nk, d, dtype, "NHD", dq=torch.full((1, nq), 1, dtype=torch.int32),
+          dk=docs_of([nk // 3, nk - nk // 3 - 9], 9, 1))
+
+
+def test_padding_may_hold_anything():
+    dq = docs_of([150, 100], 70, 1)
+    g = torch.Generator().manual_seed(3)
+    for d, dtype in ((64, F), (128, H)):
+        k, v = (torch.randn(1, 2, 320, d, generator=g).to(dtype) for _ in "kv")
+        clean = v.clone()
+        k[:, :, 250:], v[:, :, 250::2], v[:, :, 251::2] = math.nan, math.inf, math.nan
+        clean[:, :, 250:] = 0
+        q = torch.randn(1, 2, 320, d, generator=g).to(dtype)
+        q[:, :, 250:] = math.nan
+        import quantized_attention_mean_gb300 as qa
+        for causal in (False, True):
+            out, lse = qa.scored_attn(q.to(DEV), k.to(DEV), v.to(DEV), is_causal=causal, doc_ids=dq.to(DEV), return_lse=True)
+            kz, qz = torch.nan_to_num(k), torch.nan_to_num(q)
+            seen = visible(320, 320, 1, causal, 0, None, dq, dq)[:, None].expand(1, 2, 320, 320).to(DEV)
+            r = attend(qz.to(DEV), kz.to(DEV), clean.to(DEV), d ** -0.5, seen=seen, dtype=dtype)
+            assert_close(out, r["out"], r["out_tol"], "out")
+            assert_close(lse, r["lse"], r["lse_tol"], "lse")
+            assert (out[:, :, 250:] == 0).all()
+
+
+def test_keys_ahead_may_be_infinite_scores():
+    # a masked key whose score is infinite or NaN leaves the rows that do not see it alone
+    g = torch.Generator().manual_seed(4)
+    q, k, v = (torch.randn(1, 1, 256, 64, generator=g).half() for _ in "qkv")
+    k2 = k.clone()
+    k2[:, :, 200] = math.nan
+    k2[:, :, 220] = math.inf
+    import quantized_attention_mean_gb300 as qa
+    a = qa.scored_attn(q.to(DEV), k.to(DEV), v.to(DEV), is_causal=True, softcap=20.0)
+    b = qa.scored_attn(q.to(DEV), k2.to(DEV), v.to(DEV), is_causal=True, softcap=20.0)
+    assert torch.equal(a[:, :, :200], b[:, :, :200]) and torch.isnan(b[:, :, 200:]).any()
+
+
+def test_large_scores_and_growing_maximum():
+    # scores rise along the keys by far more than the frame allows, then fall
+    n, d = 700, 64
+    k = torch.zeros(1, 1, n, d)
+    k[0, 0, :, 0] = torch.cat([torch.linspace(-60, 60, 500), torch.linspace(60, -200, 200)])
+    q = torch.ones(1, 1, 130, d)
+    v = torch.randn(1, 1, n, d, generator=torch.Generator().manual_seed(1))
+    check(1, 1, 1, 130, n, d, F, q=q.half(), k=k.half(), v=v.half(), scale=1.0)
+    check(1, 1, 1, 130, n, d, H, q=q.bfloat16(), k=k.bfloat16(), v=v.bfloat16(), scale=1.0, bias=True)
+    check(1, 1, 1, 130, n, d, F, q=q.half(), k=k.half(), v=v.half(), scale=1.0, cap=50.0, causal=True, offset=n)
+
+
+def test_strided_and_broadcast_inputs():
+    g = torch.Generator().manual_seed(6)
+    # a fused projection's slices: rows of one tensor
+    B, n, h, d = 2, 200, 3, 64
+    qkv = torch.randn(B, n, 3, h, d, generator=g).bfloat16()
+    q, k, v = (qkv[:, :, i] for i in range(3))
+    fused = qkv.to(DEV)
+    order = iter(range(3))
+    check(B, h, h, n, n, d, H, "NHD", causal=True, q=q.transpose(1, 2), k=k.transpose(1, 2), v=v.transpose(1, 2),
+          place=lambda t: fused[:, :, next(order)])
+    # keys and values shared over the batch by a zero stride, rows that start at odd elements
+    k1, v1 = (torch.randn(1, 2, 300, 64, generator=g).half() for _ in "kv")
+    k2, v2 = k1.expand(2, -1, -1, -1), v1.expand(2, -1, -1, -1)
+    q = torch.randn(2, 2, 100, 64, generator=g).half()
+
+    def odd(t):
+        if t.shape[2] == 300:
+            return t[:1].to(DEV).expand(2, -1, -1, -1)
+        w = torch.zeros(2, 2, 100, 67, dtype=torch.float16, device=DEV)
+        w[..., 1:65] = t.to(DEV)
+        return w[..., 1:65]
+    check(2, 2, 2, 100, 300, 64, F, q=q, k=k2, v=v2, place=odd)
+
+
+def test_no_keys_and_out_strides():
+    import quantized_attention_mean_gb300 as qa
+    q = torch.randn(1, 2, 5, 64, dtype=torch.float16, device=DEV)
+    e = torch.empty(1, 2, 0, 64, dtype=torch.float16, device=DEV)
+    out, lse = qa.scored_attn(q, e, e, return_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    assert qa.scored_attn(q[:, :, :0], q, q).shape == (1, 2, 0, 64)
+    k = torch.randn(1, 2, 300, 64, dtype=torch.float16, device=DEV)
+    want = qa.scored_attn(q, k, k)
+    for width, at in ((67, 1), (80, 8)):
+        wide = torch.full((1, 2, 5, width), 7.0, dtype=torch.float16, device=DEV)
+        qa.scored_attn(q, k, k, out=wide[..., at:at + 64])
+        assert torch.equal(wide[..., at:at + 64], want)
+        assert (wide[..., :at] == 7).all() and (wide[..., at + 64:] == 7).all()
+
+
+def test_in_a_graph_and_on_another_stream():
+    import quantized_attention_mean_gb300 as qa
+    g = torch.Generator().manual_seed(8)
+    q, k, v = (torch.randn(1, 4, 300, 128, generator=g).bfloat16().to(DEV) for _ in "qkv")
+    ids = docs_of([100, 180], 20, 1).to(DEV)
+    kw = dict(is_causal=True, softcap=30.0, doc_ids=ids)
+    eager = qa.scored_attn(q, k, v, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = qa.scored_attn(q, k, v, stream=side, **kw)
+    side.synchronize()
+    assert torch.equal(other, eager)
+    ws = qa.alloc_workspace(qa.scored_attn_workspace_bytes(1, 4, 4, 300, 300, 128), DEV)
+    out = torch.empty_like(q)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for gr in graphs:                                  # two graphs over one workspace
+        with torch.cuda.graph(gr):
+            qa.scored_attn(q, k, v, out=out, workspace=ws, **kw)
+    for gr in graphs * 2:
+        out.zero_()
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
+
+
+def test_prompt_in_chunks_then_decode():
+    """A prompt attended in two chunks, its keys appended to a paged cache, then one more token from
+    the cache: the same rows as one call over the whole."""
+    import quantized_attention_mean_gb300 as qa
+    g = torch.Generator().manual_seed(9)
+    n, hq, hkv, d, page = 401, 4, 2, 64, 16
+    q, k, v = (torch.randn(1, n, h, d, generator=g).half().to(DEV) for h in (hq, hkv, hkv))
+    slopes = torch.tensor([0.5, 0.25, 0.1, 0.0], device=DEV)
+    kw = dict(tensor_layout="NHD", is_causal=True, softcap=25.0, slopes=slopes, return_lse=True)
+    whole, lse = qa.scored_attn(q, k, v, **kw)
+    first, l1 = qa.scored_attn(q[:, :250], k[:, :250], v[:, :250], **kw)
+    second, l2 = qa.scored_attn(q[:, 250:400], k[:, :400], v[:, :400], q_offset=250, **kw)
+    cache = [torch.zeros(30, hkv, page, d, dtype=torch.float16, device=DEV) for _ in "kv"]
+    table = torch.randperm(30, generator=g)[None, :26].to(torch.int32).to(DEV).contiguous()
+    lens = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    qa.paged_append(k[0], v[0], *cache, table, lens, cu_seqlens=cu)
+    last, l3 = qa.paged_attn(q[:, 400], *cache, table, lens + n, 416, softcap=25.0, slopes=slopes, return_lse=True)
+    # both sides round once from nearly equal values: at most one step of fp16 apart, relative 2^-10
+    got = torch.cat([first, second, last[:, None]], 1).float()
+    assert ((got - whole.float()).abs() <= 2.0 ** -10 * whole.float().abs() + 2.0 ** -10).all()
+    assert ((torch.cat([l1, l2, l3[..., None]], 2) - lse).abs() <= 1e-4).all()
