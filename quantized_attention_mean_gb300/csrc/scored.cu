@@ -41,7 +41,7 @@ struct DocTile {
 struct ScoredArgs {
   int batch, hq, hkv, nq, nk, d, dtype, causal, splits, k_tiles, q_offset, vec;
   float c2;           // sm_scale log2(e)
-  float cap2, cap_k;  // cap log2(e); 2 sm_scale log2(e) / cap
+  float cap2, cap_k, cap_x;  // cap log2(e); 2 sm_scale log2(e) / cap; sm_scale / cap
   void* o; int64_t o_sb, o_sh, o_sn;
   float* lse;
   const float* slopes;
@@ -60,11 +60,13 @@ struct Cfg {
   static constexpr int kChunks = DP / 64;
   static constexpr int kQBytes = 128 * DP * 2, kKBytes = 128 * DP * 2, kVBytes = 128 * DP * 2;
   static constexpr int kKStages = DP == 128 ? 3 : 4, kVStages = DP == 128 ? 2 : 4;
-  static constexpr int kSBufs = DP == 64 ? 3 : 2;
-  static constexpr uint32_t kTmemO = kSBufs * 128;
+  // tensor memory: S of tile x at 128 x; P over S (head_dim 128) or beside it; then O
+  static constexpr bool kOver = DP == 128;
+  static constexpr uint32_t kTmemP = kOver ? 0 : 256, kPitchP = kOver ? 128 : 64;
+  static constexpr uint32_t kTmemO = kOver ? 256 : 384;
   static constexpr int kOffK = 2 * kQBytes, kOffV = kOffK + kKStages * kKBytes;
   static constexpr int kOffBar = kOffV + kVStages * kVBytes;
-  static constexpr int kNumBars = 1 + 2 * kKStages + 3 * kVStages + kSBufs + 2 + 2 + 2;
+  static constexpr int kNumBars = 1 + 2 * kKStages + 3 * kVStages + 12;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffMisc + 64 + 1024;
   static_assert(kTmemO + 2 * DP <= 512 && kSmem <= 232448, "tensor and shared memory");
@@ -109,6 +111,25 @@ __device__ __forceinline__ void wait_ld_max(float (&m)[4]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(m[0]), "+f"(m[1]), "+f"(m[2]), "+f"(m[3]) : : "memory");
 }
 
+// O of a row times alpha, in tensor memory.
+template <int DP>
+__device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < DP / 32; ++c) {
+    uint32_t o[32];
+    tmem_ld32(tO + c * 32, o);
+    tmem_wait_ld(o);
+#pragma unroll
+    for (int u = 0; u < 32; u += 2) {
+      float f0, f1;
+      mul2(f0, f1, __uint_as_float(o[u]), __uint_as_float(o[u + 1]), alpha, alpha);
+      o[u] = __float_as_uint(f0);
+      o[u + 1] = __float_as_uint(f1);
+    }
+    tmem_st32(tO + c * 32, o);
+  }
+}
+
 // What every role of a CTA has to agree on.
 struct Work {
   int b, h, split;
@@ -124,7 +145,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     scored_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const ScoredArgs a) {
   using C = Cfg<DP>;
-  constexpr int NB = C::kSBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sK = sm + C::kOffK;
@@ -135,9 +155,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_full = k_empty + C::kKStages;
   uint64_t* v_empty = v_full + C::kVStages;
   uint64_t* v_clean = v_empty + C::kVStages;
-  uint64_t* s_full = v_clean + C::kVStages;  // [NB]
-  uint64_t* p_full = s_full + NB;            // [2]
-  uint64_t* o_full = p_full + 2;             // [2]
+  uint64_t* s_full = v_clean + C::kVStages;  // [2] scores of a tile are in tensor memory
+  uint64_t* s_free = s_full + 2;             // [2] and in registers (P beside S)
+  uint64_t* p_half = s_free + 2;             // [2] P of the first 64 keys is written (P over S)
+  uint64_t* p_full = p_half + 2;             // [2] all of P is
+  uint64_t* o_full = p_full + 2;             // [2] P V is done
   uint64_t* drain = o_full + 2;              // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 4);
@@ -164,8 +186,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_empty[i], nx);
       mbar_init(&v_clean[i], 1);
     }
-    for (int i = 0; i < NB; ++i) mbar_init(&s_full[i], 1);
-    for (int i = 0; i < 2; ++i) { mbar_init(&p_full[i], 128); mbar_init(&o_full[i], 1); mbar_init(&drain[i], 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 128);
+      mbar_init(&p_half[i], 128);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&drain[i], 1);
+    }
     *abort_flag = 0;
     s_red[0] = INT32_MAX;  // smallest id of the rows
     s_red[1] = -1;         // largest
@@ -222,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   w.j1 = hi;
   w.j1a = w.has_b ? max(lo, min(hi, max(hi_a, hi - 1))) : hi;
   const int n_tiles = w.j1 - w.j0;
-  const bool a_short = w.j1a < w.j1;  // tile A leaves out the last key tile
+  const int n_a = w.j1a - w.j0;  // tile A may leave out the last key tile
 
   if (warp >= 8) {
     regs_dec<kRegsCtl>();
@@ -289,9 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok && lane == 0) record_error(a.err, kDevTimeout);
       }
-    } else if (n_tiles > 0 && (warp == 9 || w.has_b)) {
-      // ========================================================= MMA issuer of tile `me`
-      const int me = warp - 9, nx = w.has_b ? 2 : 1, lnx = nx - 1;
+    } else if (n_tiles > 0 && (warp == 9 || (!C::kOver && w.has_b))) {
+      // ========================================================= MMA issuers
+      const int me = warp - 9;
       const uint64_t dq = sdesc_sw128(smem_u32(sm)), dk = sdesc_sw128(smem_u32(sK));
       const uint64_t dv = sdesc_sw128_mn(smem_u32(sV), 16384);
       const uint32_t fmt = BF16 ? 1 : 0;
@@ -300,47 +328,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto wait_all = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
       };
-      const int n_items = n_tiles * nx;
-      // scores of item n (key tile n >> lnx, query tile n & lnx) into S buffer n % NB
-      auto qk_item = [&](int n) {
-        const int kj = n >> lnx, x = n & lnx, st = kj % C::kKStages;
-        if (!wait_all(&k_full[st], (kj / C::kKStages) & 1)) return false;
+      // scores of query tile x against key tile j
+      auto issue_qk = [&](int x, int j) {
+        const int st = j % C::kKStages;
+        if (!wait_all(&k_full[st], (j / C::kKStages) & 1)) return false;
         tc_fence_after();
-        const uint32_t d_s = tmem + static_cast<uint32_t>(n % NB) * 128u;
         const uint64_t qx = dq + static_cast<uint64_t>((x * C::kQBytes) >> 4);
         const uint64_t kx = dk + static_cast<uint64_t>((st * C::kKBytes) >> 4);
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-          mma_f16_ss_warp(d_s, qx + off, kx + off, id_qk, k > 0);
+          mma_f16_ss_warp(tmem + x * 128, qx + off, kx + off, id_qk, k > 0);
         }
-        mma_commit_warp(&s_full[n % NB]);
+        mma_commit_warp(&s_full[x]);
         mma_commit_warp(&k_empty[st]);
         return true;
       };
-      // tile A's item of the last key tile may be left out
-      auto skipped = [&](int n) { return a_short && n == n_items - 2; };
-      bool ok = wait_all(q_full, 0);
-      if (me == 0)
-        for (int n = 0; n < NB && n < n_items && ok; ++n)
-          if (!skipped(n)) ok = qk_item(n);
-      for (int n = me; n < n_items && ok; n += nx) {
-        if (skipped(n)) break;
-        const int j = n >> lnx, sv = j % C::kVStages;
-        ok = wait_all(&p_full[me], j & 1);
-        if (!ok) break;
-        ok = wait_all(&v_in[sv], (j / C::kVStages) & 1);
-        if (!ok) break;
+      // O of query tile x += P V of key tile j
+      auto issue_pv = [&](int x, int j) {
+        const int sv = j % C::kVStages;
+        if (!wait_all(&v_in[sv], (j / C::kVStages) & 1)) return false;
+        if (C::kOver && !wait_all(&p_half[x], j & 1)) return false;
+        if (!C::kOver && !wait_all(&p_full[x], j & 1)) return false;
         tc_fence_after();
-        const uint32_t d_o = tmem + C::kTmemO + static_cast<uint32_t>(me * DP);
-        const uint32_t a_p = tmem + static_cast<uint32_t>(n % NB) * 128u;
+        const uint32_t d_o = tmem + C::kTmemO + x * DP, a_p = tmem + C::kTmemP + x * C::kPitchP;
         const uint64_t vx = dv + static_cast<uint64_t>((sv * C::kVBytes) >> 4);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 8; ++k) {
+          if (C::kOver && k == 4) {
+            if (!wait_all(&p_full[x], j & 1)) return false;
+            tc_fence_after();
+          }
           mma_f16_ts_warp(d_o, a_p + k * 8, vx + ((k * 2048) >> 4), id_pv, (j > 0 || k > 0) ? 1u : 0u);
-        mma_commit_warp(&o_full[me]);
+        }
+        mma_commit_warp(&o_full[x]);
         mma_commit_warp(&v_empty[sv]);
-        if (n + NB < n_items && !skipped(n + NB)) ok = qk_item(n + NB);
+        return true;
+      };
+      bool ok = wait_all(q_full, 0);
+      if constexpr (C::kOver) {
+        // One issuer, the tiles in turn, P V and the next scores of one tile together: the tiles then stay half a
+        // period apart, one in its softmax while the other has the tensor core. (An issuer per tile
+        // lets them fall into step, both in the softmax and then both waiting: 1.5 times slower.)
+        const int nx = w.has_b ? 2 : 1;
+        for (int x = 0; x < nx && ok; ++x)
+          if (x == 1 || n_a > 0) ok = issue_qk(x, 0);
+        for (int j = 0; j < n_tiles && ok; ++j)
+          for (int x = 0; x < nx && ok; ++x) {
+            const int n = x == 0 ? n_a : n_tiles;
+            if (j >= n) continue;
+            ok = issue_pv(x, j);
+            if (ok && j + 1 < n) ok = issue_qk(x, j + 1);
+          }
+      } else {
+        // An issuer per tile: the next scores as soon as the softmax holds the last ones, then P V.
+        const int n = me == 0 ? n_a : n_tiles;
+        if (ok && n > 0) ok = issue_qk(me, 0);
+        for (int j = 0; j < n && ok; ++j) {
+          if (j + 1 < n) {
+            ok = wait_all(&s_free[me], j & 1) && issue_qk(me, j + 1);
+            if (!ok) break;
+          }
+          ok = issue_pv(me, j);
+        }
       }
       // every MMA has finished before tensor memory is released
       mma_commit_warp(&drain[me]);
@@ -354,11 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // =========================================================== softmax of tile x
     const int x = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int nx = w.has_b ? 2 : 1;
     const int row = w.q0 + x * 128 + r;
     const bool active = x == 0 || w.has_b, valid = active && row < a.nq;
-    const uint32_t tO = tmem + lane_base + C::kTmemO + static_cast<uint32_t>(x * DP);
-    const int my_tiles = (x == 0 ? w.j1a : w.j1) - w.j0;
+    const uint32_t tS = tmem + lane_base + x * 128, tP = tmem + lane_base + C::kTmemP + x * C::kPitchP;
+    const uint32_t tO = tmem + lane_base + C::kTmemO + x * DP;
+    const int my_tiles = x == 0 ? n_a : n_tiles;
     const int limit = valid ? limit_of(row) : 0;
     const int dq = a.doc_q ? my_doc : 0;
     const int pos = row + a.q_offset;
@@ -374,16 +424,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       t0 = rcpf(t0);
       t1 = rcpf(t1);
     };
+    const float cap_c[7] = {a.cap2 * 0.9999999403953552f,   a.cap2 * -0.33332881331443787f, a.cap2 * 0.13325709104537964f,
+                            a.cap2 * -0.05347844585776329f, a.cap2 * 0.020331112667918205f, a.cap2 * -0.006239818874746561f,
+                            a.cap2 * 0.0010531365405768156f};
+    // the same for |s| <= cap, less the frame: x = s / cap times a polynomial of x^2 (the minimax
+    // one of tanh(x) / x on [0, 1], found by exchange; the largest error of tanh is 1.1e-7 in fp32)
+    auto cap_poly = [&](float& t0, float& t1, float off) {
+      mul2(t0, t1, t0, t1, a.cap_x, a.cap_x);
+      float z0, z1, y0, y1;
+      mul2(z0, z1, t0, t1, t0, t1);
+      fma2(y0, y1, z0, z1, cap_c[6], cap_c[6], cap_c[5], cap_c[5]);
+#pragma unroll
+      for (int i = 4; i >= 0; --i) fma2(y0, y1, y0, y1, z0, z1, cap_c[i], cap_c[i]);
+      fma2(t0, t1, t0, t1, y0, y1, off, off);
+    };
     float m = kNegInf;  // the frame's maximum, base 2
     float l = 0.f;
     bool ok = true;
-    int s_buf = x, s_par = 0;
     if (active) {
       for (int j = 0; j < my_tiles; ++j) {
-        const uint32_t tS = tmem + lane_base + static_cast<uint32_t>(s_buf) * 128u;
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s_buf], s_par, abort_flag));
-        s_buf += nx;
-        if (s_buf >= NB) { s_buf -= NB; s_par ^= 1; }
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], j & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
         const int kv0 = (w.j0 + j) * 128;
@@ -396,21 +456,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         whole = whole || !valid;  // (rows behind the last one are not written)
         const bool masked = !__all_sync(0xffffffffu, whole);
         uint32_t s[4][32];
-        float t_max, alpha, m_use;
+        float t_max = kNegInf, alpha = 1.0f, m_use = 0.f;
         float g0 = 0.f, g1 = 0.f, g2 = 0.f, g3 = 0.f;
-        // the frame: kept unless the maximum grew by more than 8
+        // S is in registers
+        auto release_s = [&]() {
+          if constexpr (!C::kOver) {
+            tc_fence_before();
+            mbar_arrive(&s_free[x]);
+          }
+        };
+        // The frame is kept unless the maximum grew by more than 8. P V of the last tile is waited for here:
+        // O may then be rescaled and P overwritten (it also keeps p_full at most one phase ahead of its issuer).
         auto reframe = [&]() {
           const bool grow = t_max > m + 8.0f || (m == kNegInf && t_max > kNegInf);
           const float m_new = grow ? t_max : m;
           m_use = m_new == kNegInf ? 0.f : m_new;
           alpha = grow ? ex2f(m - m_use) : 1.0f;
           m = m_new;
+          if (j > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[x], (j - 1) & 1, abort_flag));
+            if (!ok) return;
+            tc_fence_after();
+            if (__any_sync(0xffffffffu, alpha != 1.0f)) rescale_o<DP>(tO, alpha);
+          }
         };
-        // P = 2^(t - m), summed in 32 bits, rounded once to the operands' type, over S's columns;
-        // READY: s holds the scores t themselves, otherwise the products
-        auto weights = [&](auto ready) {
-          constexpr bool READY = decltype(ready)::value;
-          const float c_off = READY ? 0.f : CAP ? a.cap2 - m_use : -m_use;
+        // P = 2^(t - m), summed in 32 bits, rounded once to the operands' type. FORM: 0 s holds the
+        // scores t; 1 the products; 2, 3 the products to be capped, by quotient or by polynomial
+        auto weights = [&](auto form) {
+          constexpr int FORM = decltype(form)::value;
+          const float c_off = FORM == 2 ? a.cap2 - m_use : -m_use;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pw[16];
@@ -420,14 +494,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int v = 0; v < 4; v += 2) {
                 float t0 = __uint_as_float(s[c][u + v]), t1 = __uint_as_float(s[c][u + v + 1]);
-                if constexpr (READY) {
-                  add2(t0, t1, t0, t1, -m_use, -m_use);
-                } else if constexpr (CAP) {
+                if constexpr (FORM == 0) add2(t0, t1, t0, t1, c_off, c_off);
+                if constexpr (FORM == 1) fma2(t0, t1, t0, t1, a.c2, a.c2, c_off, c_off);
+                if constexpr (FORM == 2) {
                   cap_rcp(t0, t1);
                   fma2(t0, t1, t0, t1, cap_m2, cap_m2, c_off, c_off);
-                } else {
-                  fma2(t0, t1, t0, t1, a.c2, a.c2, c_off, c_off);
                 }
+                if constexpr (FORM == 3) cap_poly(t0, t1, c_off);
                 e[v] = ex2f(t0);
                 e[v + 1] = ex2f(t1);
               }
@@ -438,7 +511,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int u = 0; u < 16; ++u) s[c >> 1][(c & 1) * 16 + u] = pw[u];
-            if (c & 1) tmem_st32(tS + (c >> 1) * 32, s[c >> 1]);
+            if (c & 1) {
+              tmem_st32(tP + (c >> 1) * 32, s[c >> 1]);
+              if (C::kOver && c == 1) {
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&p_half[x]);
+              }
+            }
           }
         };
         if (!BIAS && !masked) {
@@ -449,54 +529,68 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
           wait_ld_max(cm);
+          release_s();
           const float top = fmaxf(max3(cm[0], cm[1], cm[2]), cm[3]);
-          t_max = CAP ? fmaf(rcpf(1.0f + ex2f(top * a.cap_k)), cap_m2, a.cap2) : top * a.c2;
-          reframe();
-          weights(std::false_type{});
+          if constexpr (CAP) {
+            float big = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int u = 0; u < 32; u += 2)
+                big = max3(big, fabsf(__uint_as_float(s[c][u])), fabsf(__uint_as_float(s[c][u + 1])));
+            t_max = fmaf(rcpf(1.0f + ex2f(top * a.cap_k)), cap_m2, a.cap2);
+            reframe();
+            if (!ok) break;
+            if (__all_sync(0xffffffffu, big * a.cap_x <= 1.0f)) weights(std::integral_constant<int, 3>{});
+            else weights(std::integral_constant<int, 2>{});
+          } else {
+            t_max = top * a.c2;
+            reframe();
+            if (!ok) break;
+            weights(std::integral_constant<int, 1>{});
+          }
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
-          // scores in base 2: capped or scaled, then biased. The bias is linear along a tile that
-          // lies on one side of every row's position (or whose other side the causal mask hides)
-          float step = 0.f, base = 0.f;
-          bool linear = true;
-          const float dist = static_cast<float>(pos - kv0);  // exact below 2^24
+          release_s();
+          // scores in base 2: capped or scaled, then biased
+          auto scores = [&](auto bias_at) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int u = 0; u < 32; u += 2) {
+                float t0 = __uint_as_float(s[c][u]), t1 = __uint_as_float(s[c][u + 1]);
+                if constexpr (CAP) {
+                  cap_rcp(t0, t1);
+                  if constexpr (BIAS) fma2(t0, t1, t0, t1, cap_m2, cap_m2, bias_at(c * 32 + u), bias_at(c * 32 + u + 1));
+                  else fma2(t0, t1, t0, t1, cap_m2, cap_m2, a.cap2, a.cap2);
+                } else if constexpr (BIAS) {
+                  fma2(t0, t1, t0, t1, a.c2, a.c2, bias_at(c * 32 + u), bias_at(c * 32 + u + 1));
+                } else {
+                  mul2(t0, t1, t0, t1, a.c2, a.c2);
+                }
+                s[c][u] = __float_as_uint(t0);
+                s[c][u + 1] = __float_as_uint(t1);
+              }
+          };
           if constexpr (BIAS) {
+            // The bias is linear along a tile that lies on one side of every row's position (or
+            // whose other side the causal mask hides)
+            const float dist = static_cast<float>(pos - kv0);  // exact below 2^24
+            const float add = CAP ? a.cap2 : 0.f;
             const bool all_left = __all_sync(0xffffffffu, kv0 + 127 <= pos || (a.causal && prefix <= 0));
             const bool all_right = __all_sync(0xffffffffu, kv0 >= pos);
-            step = all_left ? slope : -slope;
-            base = all_left ? -slope * dist : slope * dist;
-            linear = all_left || all_right;
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int u = 0; u < 32; u += 2) {
-              float t0 = __uint_as_float(s[c][u]), t1 = __uint_as_float(s[c][u + 1]);
-              float b0 = 0.f, b1 = 0.f;
-              const float u0 = static_cast<float>(c * 32 + u), u1 = u0 + 1.0f;
-              if constexpr (BIAS) {
-                if (linear) {
-                  fma2(b0, b1, u0, u1, step, step, base, base);
-                } else {
-                  b0 = -slope * fabsf(dist - u0);
-                  b1 = -slope * fabsf(dist - u1);
-                }
-              }
-              if constexpr (CAP) {
-                cap_rcp(t0, t1);
-                fma2(t0, t1, t0, t1, cap_m2, cap_m2, a.cap2, a.cap2);
-                if constexpr (BIAS) add2(t0, t1, t0, t1, b0, b1);
-              } else if constexpr (BIAS) {
-                fma2(t0, t1, t0, t1, a.c2, a.c2, b0, b1);
-              } else {
-                mul2(t0, t1, t0, t1, a.c2, a.c2);
-              }
-              s[c][u] = __float_as_uint(t0);
-              s[c][u + 1] = __float_as_uint(t1);
+            if (all_left || all_right) {
+              const float step = all_left ? slope : -slope, base = fmaf(-step, dist, add);
+              scores([&](int u) { return fmaf(step, static_cast<float>(u), base); });
+            } else {
+              scores([&](int u) { return fmaf(-slope, fabsf(dist - static_cast<float>(u)), add); });
             }
+          } else {
+            scores([](int) { return 0.f; });
+          }
           if (masked) {
             uint32_t bits[4];
             const int n = limit - kv0;
@@ -534,39 +628,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int u = 0; u < 32; ++u)
                 if (!(bits[c] >> u & 1u)) s[c][u] = __float_as_uint(kNegInf);
           }
-          t_max = kNegInf;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int u = 0; u < 32; u += 2)
               t_max = max3(t_max, __uint_as_float(s[c][u]), __uint_as_float(s[c][u + 1]));
           reframe();
-          weights(std::true_type{});
+          if (!ok) break;
+          weights(std::integral_constant<int, 0>{});
         }
         l = fmaf(l, alpha, (g0 + g1) + (g2 + g3));
-        // ---- P V of the previous tile is done: O may be rescaled, and P published (this also keeps
-        // p_full at most one phase ahead of its issuer)
-        if (j > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&o_full[x], (j - 1) & 1, abort_flag));
-          if (!ok) break;
-          tc_fence_after();
-          if (__any_sync(0xffffffffu, alpha != 1.0f)) {
-#pragma unroll 1
-            for (int c = 0; c < DP / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tO + c * 32, o);
-              tmem_wait_ld(o);
-#pragma unroll
-              for (int u = 0; u < 32; u += 2) {
-                float f0, f1;
-                mul2(f0, f1, __uint_as_float(o[u]), __uint_as_float(o[u + 1]), alpha, alpha);
-                o[u] = __float_as_uint(f0);
-                o[u + 1] = __float_as_uint(f1);
-              }
-              tmem_st32(tO + c * 32, o);
-            }
-          }
-        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[x]);
@@ -849,6 +920,7 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
       std::isnan(sm_scale) || sm_scale <= 0.f ? (float)(1.0 / std::sqrt((double)head_dim)) : sm_scale;
   a.c2 = (float)(scale * 1.4426950408889634);
   a.cap2 = (float)(softcap * 1.4426950408889634);
+  a.cap_x = softcap > 0.f ? scale / softcap : 0.f;
   a.cap_k = softcap > 0.f ? (float)(2.0 * 1.4426950408889634 * scale / softcap) : 0.f;
   a.o = out->data; a.o_sb = view[3].sb; a.o_sh = view[3].sh; a.o_sn = view[3].sn;
   a.lse = return_lse ? lse : nullptr;
