@@ -68,7 +68,7 @@ struct Cfg {
   static constexpr int kOffBar = kOffV + kVStages * kVBytes;
   static constexpr int kNumBars = 1 + 2 * kKStages + 3 * kVStages + 12;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmem = kOffMisc + 64 + 1024;
+  static constexpr int kSmem = kOffMisc + 128 + 1024;
   static_assert(kTmemO + 2 * DP <= 512 && kSmem <= 232448, "tensor and shared memory");
 };
 
@@ -93,6 +93,43 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
+template <typename F>
+__device__ __forceinline__ void each2(float (&t)[16], F f) {
+#pragma unroll
+  for (int u = 0; u < 16; u += 2) f(t[u], t[u + 1]);
+}
+// Sixteen products s to cap tanh(s / cap) + (off - cap) in base 2, as off - 2 cap / (1 + e^(2 s / cap)): k = 2 log2(e)
+// / cap, m2 = -2 cap.
+__device__ __forceinline__ void cap_quotient(float (&t)[16], float k, float m2, float off) {
+  each2(t, [&](float& p, float& q) { mul2(p, q, p, q, k, k); });
+#pragma unroll
+  for (int u = 0; u < 16; ++u) t[u] = ex2f(t[u]);
+  each2(t, [&](float& p, float& q) { add2(p, q, p, q, 1.0f, 1.0f); });
+#pragma unroll
+  for (int u = 0; u < 16; ++u) t[u] = rcpf(t[u]);
+  each2(t, [&](float& p, float& q) { fma2(p, q, p, q, m2, m2, off, off); });
+}
+// The same, plus off, for |s| <= cap: x = s / cap times a polynomial of x^2, the minimax one of degree 6 of tanh(x) / x
+// on [0, 1] (found by exchange; tanh is off by at most 1.1e-7 in fp32). One exponential per score
+// is left on the special-function unit, which with the quotient's three bounds the kernel.
+__device__ __forceinline__ void cap_polynomial(float (&t)[16], float k, float cap, float off) {
+  constexpr float c[7] = {0.9999999403953552f,   -0.33332881331443787f,  0.13325709104537964f, -0.05347844585776329f,
+                          0.020331112667918205f, -0.006239818874746561f, 0.0010531365405768156f};
+  float z[16], y[16];
+  each2(t, [&](float& p, float& q) { mul2(p, q, p, q, k, k); });
+#pragma unroll
+  for (int u = 0; u < 16; u += 2) mul2(z[u], z[u + 1], t[u], t[u + 1], t[u], t[u + 1]);
+#pragma unroll
+  for (int u = 0; u < 16; u += 2) fma2(y[u], y[u + 1], z[u], z[u + 1], c[6], c[6], c[5], c[5]);
+#pragma unroll
+  for (int i = 4; i >= 0; --i)
+#pragma unroll
+    for (int u = 0; u < 16; u += 2) fma2(y[u], y[u + 1], y[u], y[u + 1], z[u], z[u + 1], c[i], c[i]);
+  each2(t, [&](float& p, float& q) { mul2(p, q, p, q, cap, cap); });
+#pragma unroll
+  for (int u = 0; u < 16; u += 2) fma2(t[u], t[u + 1], t[u], t[u + 1], y[u], y[u + 1], off, off);
+}
+
 // 32 columns of tensor memory and their largest value (both valid after a tcgen05.wait::ld).
 __device__ __forceinline__ void ld32_max(uint32_t taddr, uint32_t (&r)[32], float& m) {
   asm volatile(
@@ -109,6 +146,94 @@ __device__ __forceinline__ void ld32_max(uint32_t taddr, uint32_t (&r)[32], floa
 }
 __device__ __forceinline__ void wait_ld_max(float (&m)[4]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(m[0]), "+f"(m[1]), "+f"(m[2]), "+f"(m[3]) : : "memory");
+}
+
+// ---- barriers and MMAs by shared-window address. Waits end as those of the shared header do: when the phase
+// completes, when another role has given up (abort flag, where given), or after two seconds.
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint32_t timer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t abort_at) {
+  if (bar_try(bar, parity)) return true;
+  const uint32_t t0 = timer_lo();
+  for (uint32_t it = 1; it < (1u << 30); ++it) {
+    if (bar_try(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      uint32_t gone = 0;
+      if (abort_at) asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gone) : "r"(abort_at) : "memory");
+      if (gone) return false;
+      if (timer_lo() - t0 > (uint32_t)kWaitTimeoutNs) break;
+    }
+  }
+  if (abort_at) asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(abort_at) : "memory");
+  return false;
+}
+// The same by a whole warp, which goes on together and with one answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort_at) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_at));
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+// Upper halves of the operand descriptors (128-byte swizzle, version 1, 1024 bytes between groups of eight
+// rows); lower halves: the address / 16, and for V, read as an MN-major operand, the distance between
+// its blocks of 64 channels (16384 bytes) in the leading-offset field.
+constexpr uint32_t kDescHi = (2u << 29) | (1u << 14) | (1024u >> 4);
+constexpr uint32_t kLboK = 1u << 16, kLboV = (16384u >> 4) << 16;
+// One elected lane of a converged warp issues; `acc` 0: D is overwritten.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo | kLboK), "r"(b_lo | kLboK), "r"(idesc), "r"(acc), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo | kLboV), "r"(idesc), "r"(acc), "n"(kDescHi)
+      : "memory");
+}
+// Arrives on the barrier when every MMA issued by the elected thread so far is done.
+__device__ __forceinline__ void commit_to(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
 }
 
 // O of a row times alpha, in tensor memory.
@@ -130,14 +255,17 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
   }
 }
 
-// What every role of a CTA has to agree on.
-struct Work {
-  int b, h, split;
-  int q0;            // first query row of tile A
-  bool has_b;
-  int j0, j1;        // key tiles
-  int j1a;           // tile A's end (one less where the last tile is behind all of its rows)
-};
+// What the roles of a CTA agree on, as words of shared memory: each role loads what it uses (kept in
+// registers across the split they spilled, and with the shared memory taken a spill is an L2 access).
+enum Word : uint32_t { kWTmem = 0, kWAbort = 4, kWJ0 = 16, kWTiles = 20, kWTilesA = 24, kWPrefix = 28, kWRed = 32, kWSeq = 48, kWSplit = 52 };
+__device__ __forceinline__ int lds(uint32_t at) {
+  int v;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts(uint32_t at, int v) {
+  asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
 
 // CAP / BIAS: the score modification that is compiled in; the masks are a matter of each tile.
 template <int DP, bool BF16, bool CAP, bool BIAS>
@@ -147,255 +275,245 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* sK = sm + C::kOffK;
-  uint8_t* sV = sm + C::kOffV;
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
-  uint64_t* k_full = q_full + 1;
-  uint64_t* k_empty = k_full + C::kKStages;
-  uint64_t* v_full = k_empty + C::kKStages;
-  uint64_t* v_empty = v_full + C::kVStages;
-  uint64_t* v_clean = v_empty + C::kVStages;
-  uint64_t* s_full = v_clean + C::kVStages;  // [2] scores of a tile are in tensor memory
-  uint64_t* s_free = s_full + 2;             // [2] and in registers (P beside S)
-  uint64_t* p_half = s_free + 2;             // [2] P of the first 64 keys is written (P over S)
-  uint64_t* p_full = p_half + 2;             // [2] all of P is
-  uint64_t* o_full = p_full + 2;             // [2] P V is done
-  uint64_t* drain = o_full + 2;              // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 4);
-  int* s_red = reinterpret_cast<int*>(sm + C::kOffMisc + 16);  // [4] document and tile ranges
-
+  // shared-window addresses: operands, barriers, abort flag (32 bits each: the control warps have few registers)
+  const uint32_t sbase = smem_u32(sm), sK = sbase + C::kOffK, sV = sbase + C::kOffV;
+  const uint32_t q_full = sbase + C::kOffBar;
+  const uint32_t k_full = q_full + 8, k_empty = k_full + 8 * C::kKStages;
+  const uint32_t v_full = k_empty + 8 * C::kKStages, v_empty = v_full + 8 * C::kVStages;
+  const uint32_t v_clean = v_empty + 8 * C::kVStages;  // V without what padding held
+  const uint32_t s_full = v_clean + 8 * C::kVStages;   // [2] scores of a tile are in tensor memory
+  const uint32_t s_free = s_full + 16;                 // [2] and in registers (P beside S)
+  const uint32_t p_half = s_free + 16;                 // [2] P of the first 64 keys is written (P over S)
+  const uint32_t p_full = p_half + 16;                 // [2] all of P is
+  const uint32_t o_full = p_full + 16;                 // [2] P V is done
+  const uint32_t drain = o_full + 16;                  // [2]
+  const uint32_t misc = sbase + C::kOffMisc, abort_at = misc + kWAbort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Work w;
-  w.h = blockIdx.x;
-  w.b = blockIdx.z / a.splits;
-  w.split = blockIdx.z - w.b * a.splits;
-  // the pairs with the most keys first when causal
-  const int pair = a.causal ? (int)(gridDim.y - 1 - blockIdx.y) : (int)blockIdx.y;
-  w.q0 = pair * 256;
-  w.has_b = a.nq - w.q0 > 128;
-  const int hk = w.h / (a.hq / a.hkv);
-  const int rows = min(256, a.nq - w.q0);
+  // the work item: head, sequence, key split, pair of query tiles (those with the most keys first when causal)
+  const int q0 = (a.causal ? (int)(gridDim.y - 1 - blockIdx.y) : (int)blockIdx.y) * 256;
+  const bool has_b = a.nq - q0 > 128;
 
   if (threadIdx.x == 0) {
-    const int nx = w.has_b ? 2 : 1;
-    mbar_init(q_full, 1);
-    for (int i = 0; i < C::kKStages; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], nx); }
+    // who releases a stage: the softmax of each tile at head_dim 64, of the last tile at 128
+    const int nx = has_b && !C::kOver ? 2 : 1;
+    bar_init(q_full, 1);
+    for (int i = 0; i < C::kKStages; ++i) { bar_init(k_full + 8 * i, 1); bar_init(k_empty + 8 * i, nx); }
     for (int i = 0; i < C::kVStages; ++i) {
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], nx);
-      mbar_init(&v_clean[i], 1);
+      bar_init(v_full + 8 * i, 1);
+      bar_init(v_empty + 8 * i, nx);
+      bar_init(v_clean + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 128);
-      mbar_init(&p_half[i], 128);
-      mbar_init(&p_full[i], 128);
-      mbar_init(&o_full[i], 1);
-      mbar_init(&drain[i], 1);
+      bar_init(s_full + 8 * i, 1);
+      bar_init(s_free + 8 * i, 128);
+      bar_init(p_half + 8 * i, 128);
+      bar_init(p_full + 8 * i, 128);
+      bar_init(o_full + 8 * i, 1);
+      bar_init(drain + 8 * i, 1);
     }
-    *abort_flag = 0;
-    s_red[0] = INT32_MAX;  // smallest id of the rows
-    s_red[1] = -1;         // largest
-    s_red[2] = INT32_MAX;  // first tile with such ids
-    s_red[3] = -1;         // last
+    sts(abort_at, 0);
+    // smallest and largest id of the rows, first and last key tile with such ids
+    sts(misc + kWRed, INT32_MAX);
+    sts(misc + kWRed + 4, -1);
+    sts(misc + kWRed + 8, INT32_MAX);
+    sts(misc + kWRed + 12, -1);
     fence_mbar_init();
   }
   if (warp == 9) {
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(reinterpret_cast<uint32_t*>(sm + C::kOffMisc + kWTmem), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   pdl_wait();
 
   // ---- the key tiles of this CTA
-  const int prefix = a.prefix ? __ldg(&a.prefix[w.b]) : 0;
-  // keys that rows [.., row] may see at most
-  auto limit_of = [&](int row) -> int {
+  // keys that a row sees at most
+  auto limit_of = [&](int row, int prefix) -> int {
     if (!a.causal) return a.nk;
     long long n = (long long)row + a.q_offset + 1;
     n = n > prefix ? n : prefix;
     return (int)(n < 0 ? 0 : n < a.nk ? n : a.nk);
   };
-  int lo = 0, hi = (limit_of(w.q0 + rows - 1) + 127) / 128;
-  int hi_a = (limit_of(w.q0 + min(rows, 128) - 1) + 127) / 128;
-  int my_doc = 0;
-  if (a.doc_q) {
-    my_doc = -1;
-    if (threadIdx.x < rows) {
-      my_doc = __ldg(&a.doc_q[(int64_t)w.b * a.nq + w.q0 + threadIdx.x]);
-      if (my_doc >= 0) { atomicMin(&s_red[0], my_doc); atomicMax(&s_red[1], my_doc); }
+  {
+    const int b = (int)blockIdx.z / a.splits, split = (int)blockIdx.z - b * a.splits;
+    const int rows = min(256, a.nq - q0), prefix = a.prefix ? __ldg(&a.prefix[b]) : 0;
+    int lo = 0, hi = (limit_of(q0 + rows - 1, prefix) + 127) / 128;
+    const int hi_a = (limit_of(q0 + min(rows, 128) - 1, prefix) + 127) / 128;
+    if (a.doc_q) {
+      int* red = reinterpret_cast<int*>(sm + C::kOffMisc + kWRed);
+      if (threadIdx.x < rows) {
+        const int id = __ldg(&a.doc_q[(int64_t)b * a.nq + q0 + threadIdx.x]);
+        if (id >= 0) { atomicMin(&red[0], id); atomicMax(&red[1], id); }
+      }
+      __syncthreads();
+      const int dlo = red[0], dhi = red[1];
+      for (int j = threadIdx.x; j < hi; j += kThreads) {
+        const DocTile t = a.doc_tiles[(int64_t)b * a.k_tiles + j];
+        if (t.lo <= t.hi && t.hi >= dlo && t.lo <= dhi) { atomicMin(&red[2], j); atomicMax(&red[3], j); }
+      }
+      __syncthreads();
+      lo = min(red[2], hi);
+      hi = min(hi, red[3] + 1);
     }
-    __syncthreads();
-    const int dlo = s_red[0], dhi = s_red[1];
-    for (int j = threadIdx.x; j < hi; j += kThreads) {
-      const DocTile t = a.doc_tiles[(int64_t)w.b * a.k_tiles + j];
-      if (t.lo <= t.hi && t.hi >= dlo && t.lo <= dhi) { atomicMin(&s_red[2], j); atomicMax(&s_red[3], j); }
+    if (hi < lo) hi = lo;
+    if (a.splits > 1) {
+      const int n = hi - lo;
+      hi = lo + (int)((long long)n * (split + 1) / a.splits);
+      lo += (int)((long long)n * split / a.splits);
     }
-    __syncthreads();
-    lo = min(s_red[2], hi);
-    hi = min(hi, s_red[3] + 1);
+    if (threadIdx.x == 0) {
+      sts(misc + kWJ0, lo);
+      sts(misc + kWTiles, hi - lo);
+      // tile A leaves out the last key tile where that lies behind all of its rows
+      sts(misc + kWTilesA, has_b ? max(0, min(hi, max(hi_a, hi - 1)) - lo) : hi - lo);
+      sts(misc + kWPrefix, prefix);
+      sts(misc + kWSeq, b);
+      sts(misc + kWSplit, split);
+    }
   }
-  if (hi < lo) hi = lo;
-  if (a.splits > 1) {
-    const int n = hi - lo;
-    const int x0 = lo + (int)((long long)n * w.split / a.splits), x1 = lo + (int)((long long)n * (w.split + 1) / a.splits);
-    lo = x0;
-    hi = x1;
-  }
-  w.j0 = lo;
-  w.j1 = hi;
-  w.j1a = w.has_b ? max(lo, min(hi, max(hi_a, hi - 1))) : hi;
-  const int n_tiles = w.j1 - w.j0;
-  const int n_a = w.j1a - w.j0;  // tile A may leave out the last key tile
+  __syncthreads();
 
   if (warp >= 8) {
     regs_dec<kRegsCtl>();
     if (warp == 8) {
       // ========================================================= TMA producer
+      const int n_tiles = lds(misc + kWTiles), row0 = lds(misc + kWJ0) * 128, b = lds(misc + kWSeq);
+      const int h = blockIdx.x, hk = h / (a.hq / a.hkv);
       if (lane == 0 && n_tiles > 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
-        mbar_arrive_expect_tx(q_full, (w.has_b ? 2 : 1) * C::kQBytes);
-        for (int t = 0; t < (w.has_b ? 2 : 1); ++t)
+        bar_expect(q_full, (has_b ? 2 : 1) * C::kQBytes);
+        for (int t = 0; t < (has_b ? 2 : 1); ++t)
           for (int c = 0; c < C::kChunks; ++c)
-            tma_load_4d(sm + t * C::kQBytes + c * 16384, &tmQ, q_full, c * 64, w.q0 + t * 128, w.h, w.b);
+            tma_4d(sbase + t * C::kQBytes + c * 16384, &tmQ, q_full, c * 64, q0 + t * 128, h, b);
         int nk = 0, nv = 0;
         bool ok = true;
         for (int j = 0; j < n_tiles; ++j) {
-          const int sk = j % C::kKStages, sv = j % C::kVStages, row = (w.j0 + j) * 128;
-          if (j >= C::kKStages) ok = mbar_wait(&k_empty[sk], ((j / C::kKStages) - 1) & 1, abort_flag);
+          const int sk = j % C::kKStages, sv = j % C::kVStages, row = row0 + j * 128;
+          if (j >= C::kKStages) ok = bar_wait(k_empty + 8 * sk, ((j / C::kKStages) - 1) & 1, abort_at);
           if (!ok) break;
-          mbar_arrive_expect_tx(&k_full[sk], C::kKBytes);
+          bar_expect(k_full + 8 * sk, C::kKBytes);
           for (int c = 0; c < C::kChunks; ++c)
-            tma_load_4d(sK + sk * C::kKBytes + c * 16384, &tmK, &k_full[sk], c * 64, row, hk, w.b);
+            tma_4d(sK + sk * C::kKBytes + c * 16384, &tmK, k_full + 8 * sk, c * 64, row, hk, b);
           ++nk;
-          if (j >= C::kVStages) ok = mbar_wait(&v_empty[sv], ((j / C::kVStages) - 1) & 1, abort_flag);
+          if (j >= C::kVStages) ok = bar_wait(v_empty + 8 * sv, ((j / C::kVStages) - 1) & 1, abort_at);
           if (!ok) break;
-          mbar_arrive_expect_tx(&v_full[sv], C::kVBytes);
+          bar_expect(v_full + 8 * sv, C::kVBytes);
           for (int c = 0; c < C::kChunks; ++c)
-            tma_load_4d(sV + sv * C::kVBytes + c * 16384, &tmV, &v_full[sv], c * 64, row, hk, w.b);
+            tma_4d(sV + sv * C::kVBytes + c * 16384, &tmV, v_full + 8 * sv, c * 64, row, hk, b);
           ++nv;
         }
         if (!ok) {
-          // copies in flight land before the shared memory goes away
-          volatile int never = 0;
-          mbar_wait(q_full, 0, &never);
+          // copies in flight land before the shared memory goes away (abort address 0: no one cuts this short)
+          bar_wait(q_full, 0, 0);
           for (int j = max(0, nk - C::kKStages); j < nk; ++j)
-            mbar_wait(&k_full[j % C::kKStages], (j / C::kKStages) & 1, &never);
+            bar_wait(k_full + 8 * (j % C::kKStages), (j / C::kKStages) & 1, 0);
           for (int j = max(0, nv - C::kVStages); j < nv; ++j)
-            mbar_wait(&v_full[j % C::kVStages], (j / C::kVStages) & 1, &never);
+            bar_wait(v_full + 8 * (j % C::kVStages), (j / C::kVStages) & 1, 0);
           record_error(a.err, kDevTimeout);
         }
       }
     } else if (warp == 11) {
       // ================================== padding: its V rows become zero (they may hold anything)
       if (a.doc_k) {
+        const int n_tiles = lds(misc + kWTiles), j0 = lds(misc + kWJ0), b = lds(misc + kWSeq);
         bool ok = true;
         for (int j = 0; j < n_tiles && ok; ++j) {
           const int sv = j % C::kVStages;
-          ok = __all_sync(0xffffffffu, mbar_wait(&v_full[sv], (j / C::kVStages) & 1, abort_flag));
+          ok = warp_wait(v_full + 8 * sv, (j / C::kVStages) & 1, abort_at);
           if (!ok) break;
-          const DocTile t = a.doc_tiles[(int64_t)w.b * a.k_tiles + w.j0 + j];
+          const DocTile t = a.doc_tiles[(int64_t)b * a.k_tiles + j0 + j];
           if (t.pad) {
             for (int i = 0; i < 4; ++i) {
-              const int row = i * 32 + lane, key = (w.j0 + j) * 128 + row;
-              if (key < a.nk && __ldg(&a.doc_k[(int64_t)w.b * a.nk + key]) < 0)
+              const int row = i * 32 + lane, key = (j0 + j) * 128 + row;
+              if (key < a.nk && __ldg(&a.doc_k[(int64_t)b * a.nk + key]) < 0)
                 for (int c = 0; c < C::kChunks; ++c)
                   for (int u = 0; u < 8; ++u)
-                    *reinterpret_cast<uint4*>(sV + sv * C::kVBytes + c * 16384 + row * 128 + u * 16) =
+                    *reinterpret_cast<uint4*>(sm + C::kOffV + sv * C::kVBytes + c * 16384 + row * 128 + u * 16) =
                         make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&v_clean[sv]);
+          if (lane == 0) bar_arrive(v_clean + 8 * sv);
         }
         if (!ok && lane == 0) record_error(a.err, kDevTimeout);
       }
-    } else if (n_tiles > 0 && (warp == 9 || (!C::kOver && w.has_b))) {
+    } else if (warp == 9 || (!C::kOver && has_b)) {
       // ========================================================= MMA issuers
       const int me = warp - 9;
-      const uint64_t dq = sdesc_sw128(smem_u32(sm)), dk = sdesc_sw128(smem_u32(sK));
-      const uint64_t dv = sdesc_sw128_mn(smem_u32(sV), 16384);
+      const int n_tiles = lds(misc + kWTiles), n_a = lds(misc + kWTilesA);
+      const uint32_t tmem = lds(misc + kWTmem);
       const uint32_t fmt = BF16 ? 1 : 0;
       const uint32_t id_qk = make_idesc(1, fmt, fmt, 128, 128), id_pv = make_idesc(1, fmt, fmt, 128, DP) | kIdescTransB;
-      uint64_t* const v_in = a.doc_k ? v_clean : v_full;
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
-      };
-      // scores of query tile x against key tile j
-      auto issue_qk = [&](int x, int j) {
-        const int st = j % C::kKStages;
-        if (!wait_all(&k_full[st], (j / C::kKStages) & 1)) return false;
+      const uint32_t v_in = a.doc_k ? v_clean : v_full;
+      // scores of query tile x against key tile j into S buffer sb
+      auto issue_qk = [&](int x, int j, int sb) {
+        const uint32_t st = (uint32_t)j % C::kKStages;
+        if (!warp_wait(k_full + 8 * st, (j / C::kKStages) & 1, abort_at)) return false;
         tc_fence_after();
-        const uint64_t qx = dq + static_cast<uint64_t>((x * C::kQBytes) >> 4);
-        const uint64_t kx = dk + static_cast<uint64_t>((st * C::kKBytes) >> 4);
+        const uint32_t qx = (sbase + x * C::kQBytes) >> 4, kx = (sK + st * C::kKBytes) >> 4;
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-          mma_f16_ss_warp(tmem + x * 128, qx + off, kx + off, id_qk, k > 0);
+          constexpr uint32_t kStep = 16384 >> 4;
+          const uint32_t off = (k >> 2) * kStep + (k & 3) * 2;
+          mma_ss(tmem + sb * 128, qx + off, kx + off, id_qk, k > 0);
         }
-        mma_commit_warp(&s_full[x]);
-        mma_commit_warp(&k_empty[st]);
+        commit_to(s_full + 8 * sb);
         return true;
       };
       // O of query tile x += P V of key tile j
-      auto issue_pv = [&](int x, int j) {
-        const int sv = j % C::kVStages;
-        if (!wait_all(&v_in[sv], (j / C::kVStages) & 1)) return false;
-        if (C::kOver && !wait_all(&p_half[x], j & 1)) return false;
-        if (!C::kOver && !wait_all(&p_full[x], j & 1)) return false;
+      auto issue_pv = [&](int x, int j, uint32_t p_col, bool done) {
+        const uint32_t sv = (uint32_t)j % C::kVStages;
+        if (!warp_wait(v_in + 8 * sv, (j / C::kVStages) & 1, abort_at)) return false;
+        if (!warp_wait((C::kOver ? p_half : p_full) + 8 * x, j & 1, abort_at)) return false;
         tc_fence_after();
-        const uint32_t d_o = tmem + C::kTmemO + x * DP, a_p = tmem + C::kTmemP + x * C::kPitchP;
-        const uint64_t vx = dv + static_cast<uint64_t>((sv * C::kVBytes) >> 4);
+        const uint32_t d_o = tmem + C::kTmemO + x * DP, a_p = tmem + p_col;
+        const uint32_t vx = (sV + sv * C::kVBytes) >> 4;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (C::kOver && k == 4) {
-            if (!wait_all(&p_full[x], j & 1)) return false;
+            if (!warp_wait(p_full + 8 * x, j & 1, abort_at)) return false;
             tc_fence_after();
           }
-          mma_f16_ts_warp(d_o, a_p + k * 8, vx + ((k * 2048) >> 4), id_pv, (j > 0 || k > 0) ? 1u : 0u);
+          mma_ts(d_o, a_p + k * 8, vx + (k * 2048 >> 4), id_pv, (j > 0 || k > 0) ? 1u : 0u);
         }
-        mma_commit_warp(&o_full[x]);
-        mma_commit_warp(&v_empty[sv]);
+        if (done) commit_to(o_full + 8 * x);
         return true;
       };
-      bool ok = wait_all(q_full, 0);
+      bool ok = n_tiles == 0 || warp_wait(q_full, 0, abort_at);
       if constexpr (C::kOver) {
-        // One issuer, the tiles in turn, P V and the next scores of one tile together: the tiles then stay half a
-        // period apart, one in its softmax while the other has the tensor core. (An issuer per tile
-        // lets them fall into step, both in the softmax and then both waiting: 1.5 times slower.)
-        const int nx = w.has_b ? 2 : 1;
-        for (int x = 0; x < nx && ok; ++x)
-          if (x == 1 || n_a > 0) ok = issue_qk(x, 0);
-        for (int j = 0; j < n_tiles && ok; ++j)
+        // One issuer, the tiles in turn, P V and the next scores of one tile together: the tiles then stay
+        // half a period apart, one in its softmax while the other has the tensor core. (An issuer per
+        // tile lets them fall into step, both in the softmax and then both waiting: 1.2 times slower.)
+        // Each item has one commit, of its scores, which also tells that P V before them is done: a
+        // second commit in a row holds the issuer up by some 300 cycles, so the softmax releases
+        // the K and V stages. A single query tile has both S buffers and its scores a tile earlier.
+        const int nx = has_b ? 2 : 1, lead = has_b ? 1 : 2;
+#pragma unroll 1
+        for (int j = -lead; j < n_tiles && ok; ++j)
+#pragma unroll 1
           for (int x = 0; x < nx && ok; ++x) {
-            const int n = x == 0 ? n_a : n_tiles;
-            if (j >= n) continue;
-            ok = issue_pv(x, j);
-            if (ok && j + 1 < n) ok = issue_qk(x, j + 1);
+            const int n = x == 0 ? n_a : n_tiles, sb = nx == 2 ? x : j & 1;
+            if (j >= 0 && j < n) ok = issue_pv(x, j, sb * 128, nx == 1 || j + 1 == n);
+            if (ok && j + lead < n) ok = issue_qk(x, j + lead, sb);
           }
       } else {
         // An issuer per tile: the next scores as soon as the softmax holds the last ones, then P V.
         const int n = me == 0 ? n_a : n_tiles;
-        if (ok && n > 0) ok = issue_qk(me, 0);
-        for (int j = 0; j < n && ok; ++j) {
-          if (j + 1 < n) {
-            ok = wait_all(&s_free[me], j & 1) && issue_qk(me, j + 1);
-            if (!ok) break;
-          }
-          ok = issue_pv(me, j);
+#pragma unroll 1
+        for (int j = -1; j < n && ok; ++j) {
+          if (j >= 0 && j + 1 < n) ok = warp_wait(s_free + 8 * me, j & 1, abort_at);
+          if (ok && j + 1 < n) ok = issue_qk(me, j + 1, me);
+          if (ok && j >= 0) ok = issue_pv(me, j, C::kTmemP + me * C::kPitchP, true);
         }
       }
       // every MMA has finished before tensor memory is released
-      mma_commit_warp(&drain[me]);
-      volatile int never = 0;
-      mbar_wait(&drain[me], 0, &never);
+      commit_to(drain + 8 * me);
+      warp_wait(drain + 8 * me, 0, 0);
       __syncwarp();
       if (!ok && lane == 0) record_error(a.err, kDevTimeout);
     }
@@ -404,121 +522,118 @@ __global__ void __launch_bounds__(kThreads, 1)
     // =========================================================== softmax of tile x
     const int x = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int row = w.q0 + x * 128 + r;
-    const bool active = x == 0 || w.has_b, valid = active && row < a.nq;
-    const uint32_t tS = tmem + lane_base + x * 128, tP = tmem + lane_base + C::kTmemP + x * C::kPitchP;
+    const int row = q0 + x * 128 + r;
+    const bool active = x == 0 || has_b, valid = active && row < a.nq;
+    // head_dim 128 and one query tile: the scores alternate between both S buffers, P V of the tile
+    // before is waited for at each tile
+    const bool solo = C::kOver && !has_b;
+    const bool releases = (threadIdx.x & 127) == 0 && (!C::kOver || x == 1 || solo);
+    const uint32_t tmem = lds(misc + kWTmem);
+    const int j0 = lds(misc + kWJ0), prefix = lds(misc + kWPrefix), b = lds(misc + kWSeq), h = blockIdx.x;
     const uint32_t tO = tmem + lane_base + C::kTmemO + x * DP;
-    const int my_tiles = x == 0 ? n_a : n_tiles;
-    const int limit = valid ? limit_of(row) : 0;
-    const int dq = a.doc_q ? my_doc : 0;
+    const int my_tiles = lds(misc + (x == 0 ? kWTilesA : kWTiles));
+    const int limit = valid ? limit_of(row, prefix) : 0;
+    const int dq = !a.doc_q ? 0 : valid ? __ldg(&a.doc_q[(int64_t)b * a.nq + row]) : -1;
     const int pos = row + a.q_offset;
     float slope = 0.f;
-    if constexpr (BIAS) slope = __ldg(&a.slopes[w.h]) * kL2e;
-    // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)): the quotient of two scores
-    const float cap_m2 = -2.0f * a.cap2;
-    auto cap_rcp = [&](float& t0, float& t1) {
-      mul2(t0, t1, t0, t1, a.cap_k, a.cap_k);
-      t0 = ex2f(t0);
-      t1 = ex2f(t1);
-      add2(t0, t1, t0, t1, 1.0f, 1.0f);
-      t0 = rcpf(t0);
-      t1 = rcpf(t1);
-    };
-    const float cap_c[7] = {a.cap2 * 0.9999999403953552f,   a.cap2 * -0.33332881331443787f, a.cap2 * 0.13325709104537964f,
-                            a.cap2 * -0.05347844585776329f, a.cap2 * 0.020331112667918205f, a.cap2 * -0.006239818874746561f,
-                            a.cap2 * 0.0010531365405768156f};
-    // the same for |s| <= cap, less the frame: x = s / cap times a polynomial of x^2 (the minimax
-    // one of tanh(x) / x on [0, 1], found by exchange; the largest error of tanh is 1.1e-7 in fp32)
-    auto cap_poly = [&](float& t0, float& t1, float off) {
-      mul2(t0, t1, t0, t1, a.cap_x, a.cap_x);
-      float z0, z1, y0, y1;
-      mul2(z0, z1, t0, t1, t0, t1);
-      fma2(y0, y1, z0, z1, cap_c[6], cap_c[6], cap_c[5], cap_c[5]);
-#pragma unroll
-      for (int i = 4; i >= 0; --i) fma2(y0, y1, y0, y1, z0, z1, cap_c[i], cap_c[i]);
-      fma2(t0, t1, t0, t1, y0, y1, off, off);
-    };
+    if constexpr (BIAS) slope = __ldg(&a.slopes[h]) * kL2e;
+    const float cap_m2 = -2.0f * a.cap2, cap_in = a.cap_k;
     float m = kNegInf;  // the frame's maximum, base 2
     float l = 0.f;
     bool ok = true;
     if (active) {
-      for (int j = 0; j < my_tiles; ++j) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], j & 1, abort_flag));
+      // head_dim 64: tile B starts when A's first weights are half done, so that one tile's loads and
+      // waits lie beside the other's exponentials (they keep that distance)
+      if (!C::kOver && x == 1 && lds(misc + kWTilesA) > 0) ok = warp_wait(p_half, 0, abort_at);
+      for (int j = 0; j < my_tiles && ok; ++j) {
+        const int sb = solo ? j & 1 : x;
+        const uint32_t tS = tmem + lane_base + sb * 128;
+        const uint32_t tP = C::kOver ? tS : tmem + lane_base + C::kTmemP + x * C::kPitchP;
+        ok = warp_wait(s_full + 8 * sb, (solo ? j >> 1 : j) & 1, abort_at);
         if (!ok) break;
+        if (releases) {  // K of this tile has been read, and V of the last (where this barrier tells it)
+          bar_arrive(k_empty + 8 * ((uint32_t)j % C::kKStages));
+          if (C::kOver && !solo && j > 0) bar_arrive(v_empty + 8 * ((uint32_t)(j - 1) % C::kVStages));
+        }
         tc_fence_after();
-        const int kv0 = (w.j0 + j) * 128;
+        const int kv0 = (j0 + j) * 128;
         // ---- which keys of the tile this row sees, as bits (only where some row of the warp misses one)
         bool whole = limit - kv0 >= 128;
         if (a.doc_k) {
-          const DocTile t = a.doc_tiles[(int64_t)w.b * a.k_tiles + w.j0 + j];
+          const DocTile t = a.doc_tiles[(int64_t)b * a.k_tiles + j0 + j];
           whole = whole && !t.mixed && t.lo == dq;
         }
         whole = whole || !valid;  // (rows behind the last one are not written)
         const bool masked = !__all_sync(0xffffffffu, whole);
         uint32_t s[4][32];
-        float t_max = kNegInf, alpha = 1.0f, m_use = 0.f;
+        float t_max = kNegInf, m_use = 0.f;
         float g0 = 0.f, g1 = 0.f, g2 = 0.f, g3 = 0.f;
         // S is in registers
         auto release_s = [&]() {
           if constexpr (!C::kOver) {
             tc_fence_before();
-            mbar_arrive(&s_free[x]);
+            bar_arrive(s_free + 8 * x);
           }
         };
-        // The frame is kept unless the maximum grew by more than 8. P V of the last tile is waited for here:
-        // O may then be rescaled and P overwritten (it also keeps p_full at most one phase ahead of its issuer).
+        // P V of the tile before is done: O may be rescaled, P overwritten (it also keeps p_full at most one
+        // phase ahead of its issuer). Two tiles at head_dim 128 know it from the scores' barrier.
+        auto wait_pv = [&]() {
+          if (j > 0 && (!C::kOver || solo)) {
+            ok = warp_wait(o_full + 8 * x, (j - 1) & 1, abort_at);
+            if (ok) tc_fence_after();
+          }
+        };
+        // The frame is kept unless the maximum grew by more than 8.
         auto reframe = [&]() {
           const bool grow = t_max > m + 8.0f || (m == kNegInf && t_max > kNegInf);
-          const float m_new = grow ? t_max : m;
-          m_use = m_new == kNegInf ? 0.f : m_new;
-          alpha = grow ? ex2f(m - m_use) : 1.0f;
-          m = m_new;
-          if (j > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[x], (j - 1) & 1, abort_flag));
-            if (!ok) return;
-            tc_fence_after();
-            if (__any_sync(0xffffffffu, alpha != 1.0f)) rescale_o<DP>(tO, alpha);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float alpha = grow ? ex2f(m - t_max) : 1.0f;
+            m = grow ? t_max : m;
+            l *= alpha;
+            if (j > 0) {
+              wait_pv();
+              if (ok) rescale_o<DP>(tO, alpha);
+            }
           }
+          m_use = m == kNegInf ? 0.f : m;
         };
-        // P = 2^(t - m), summed in 32 bits, rounded once to the operands' type. FORM: 0 s holds the
+        // P = 2^(t - m), summed in 32 bits, rounded once to the operands' type, sixteen keys at a time (each
+        // step over all of them before the next, so that latencies overlap). FORM: 0 s holds the
         // scores t; 1 the products; 2, 3 the products to be capped, by quotient or by polynomial
         auto weights = [&](auto form) {
           constexpr int FORM = decltype(form)::value;
-          const float c_off = FORM == 2 ? a.cap2 - m_use : -m_use;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pw[16];
+          for (int g = 0; g < 8; ++g) {
+            float t[16];
 #pragma unroll
-            for (int u = 0; u < 32; u += 4) {
-              float e[4];
+            for (int u = 0; u < 16; ++u) t[u] = __uint_as_float(s[g >> 1][(g & 1) * 16 + u]);
+            if constexpr (FORM == 0) each2(t, [&](float& p, float& q) { add2(p, q, p, q, -m_use, -m_use); });
+            if constexpr (FORM == 1) each2(t, [&](float& p, float& q) { fma2(p, q, p, q, a.c2, a.c2, -m_use, -m_use); });
+            if constexpr (FORM == 2) cap_quotient(t, cap_in, cap_m2, a.cap2 - m_use);
+            if constexpr (FORM == 3) cap_polynomial(t, a.cap_x, a.cap2, -m_use);
 #pragma unroll
-              for (int v = 0; v < 4; v += 2) {
-                float t0 = __uint_as_float(s[c][u + v]), t1 = __uint_as_float(s[c][u + v + 1]);
-                if constexpr (FORM == 0) add2(t0, t1, t0, t1, c_off, c_off);
-                if constexpr (FORM == 1) fma2(t0, t1, t0, t1, a.c2, a.c2, c_off, c_off);
-                if constexpr (FORM == 2) {
-                  cap_rcp(t0, t1);
-                  fma2(t0, t1, t0, t1, cap_m2, cap_m2, c_off, c_off);
-                }
-                if constexpr (FORM == 3) cap_poly(t0, t1, c_off);
-                e[v] = ex2f(t0);
-                e[v + 1] = ex2f(t1);
-              }
-              add2(g0, g1, g0, g1, e[0], e[1]);
-              add2(g2, g3, g2, g3, e[2], e[3]);
-              pw[u / 2] = pack16<BF16>(e[0], e[1]);
-              pw[u / 2 + 1] = pack16<BF16>(e[2], e[3]);
+            for (int u = 0; u < 16; ++u) t[u] = ex2f(t[u]);
+#pragma unroll
+            for (int u = 0; u < 16; u += 4) {
+              add2(g0, g1, g0, g1, t[u], t[u + 1]);
+              add2(g2, g3, g2, g3, t[u + 2], t[u + 3]);
             }
 #pragma unroll
-            for (int u = 0; u < 16; ++u) s[c >> 1][(c & 1) * 16 + u] = pw[u];
-            if (c & 1) {
-              tmem_st32(tP + (c >> 1) * 32, s[c >> 1]);
-              if (C::kOver && c == 1) {
+            for (int u = 0; u < 8; ++u) s[g >> 2][(g & 3) * 8 + u] = pack16<BF16>(t[2 * u], t[2 * u + 1]);
+            if (g == 3) {
+              wait_pv();
+              if (!ok) return;
+              if (releases && j > 0 && (!C::kOver || solo)) bar_arrive(v_empty + 8 * ((uint32_t)(j - 1) % C::kVStages));
+              tmem_st32(tP, s[0]);
+              if (C::kOver) {
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&p_half[x]);
+                bar_arrive(p_half + 8 * x);
+              } else if (x == 0 && j == 0) {
+                bar_arrive(p_half);
               }
             }
+            if (g == 7) tmem_st32(tP + 32, s[1]);
           }
         };
         if (!BIAS && !masked) {
@@ -538,15 +653,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int u = 0; u < 32; u += 2)
                 big = max3(big, fabsf(__uint_as_float(s[c][u])), fabsf(__uint_as_float(s[c][u + 1])));
-            t_max = fmaf(rcpf(1.0f + ex2f(top * a.cap_k)), cap_m2, a.cap2);
+            t_max = fmaf(rcpf(1.0f + ex2f(top * cap_in)), cap_m2, a.cap2);
             reframe();
-            if (!ok) break;
             if (__all_sync(0xffffffffu, big * a.cap_x <= 1.0f)) weights(std::integral_constant<int, 3>{});
             else weights(std::integral_constant<int, 2>{});
           } else {
             t_max = top * a.c2;
             reframe();
-            if (!ok) break;
             weights(std::integral_constant<int, 1>{});
           }
         } else {
@@ -558,35 +671,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           // scores in base 2: capped or scaled, then biased
           auto scores = [&](auto bias_at) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int g = 0; g < 8; ++g) {
+              float t[16];
 #pragma unroll
-              for (int u = 0; u < 32; u += 2) {
-                float t0 = __uint_as_float(s[c][u]), t1 = __uint_as_float(s[c][u + 1]);
-                if constexpr (CAP) {
-                  cap_rcp(t0, t1);
-                  if constexpr (BIAS) fma2(t0, t1, t0, t1, cap_m2, cap_m2, bias_at(c * 32 + u), bias_at(c * 32 + u + 1));
-                  else fma2(t0, t1, t0, t1, cap_m2, cap_m2, a.cap2, a.cap2);
-                } else if constexpr (BIAS) {
-                  fma2(t0, t1, t0, t1, a.c2, a.c2, bias_at(c * 32 + u), bias_at(c * 32 + u + 1));
-                } else {
-                  mul2(t0, t1, t0, t1, a.c2, a.c2);
+              for (int u = 0; u < 16; ++u) t[u] = __uint_as_float(s[g >> 1][(g & 1) * 16 + u]);
+              if constexpr (CAP) cap_quotient(t, cap_in, cap_m2, a.cap2);
+              if constexpr (BIAS) {
+#pragma unroll
+                for (int u = 0; u < 16; u += 2) {
+                  const float b0 = bias_at(g * 16 + u), b1 = bias_at(g * 16 + u + 1);
+                  if constexpr (CAP) add2(t[u], t[u + 1], t[u], t[u + 1], b0, b1);
+                  else fma2(t[u], t[u + 1], t[u], t[u + 1], a.c2, a.c2, b0, b1);
                 }
-                s[c][u] = __float_as_uint(t0);
-                s[c][u + 1] = __float_as_uint(t1);
+              } else if constexpr (!CAP) {
+                each2(t, [&](float& p, float& q) { mul2(p, q, p, q, a.c2, a.c2); });
               }
+#pragma unroll
+              for (int u = 0; u < 16; ++u) s[g >> 1][(g & 1) * 16 + u] = __float_as_uint(t[u]);
+            }
           };
           if constexpr (BIAS) {
             // The bias is linear along a tile that lies on one side of every row's position (or
             // whose other side the causal mask hides)
             const float dist = static_cast<float>(pos - kv0);  // exact below 2^24
-            const float add = CAP ? a.cap2 : 0.f;
             const bool all_left = __all_sync(0xffffffffu, kv0 + 127 <= pos || (a.causal && prefix <= 0));
             const bool all_right = __all_sync(0xffffffffu, kv0 >= pos);
             if (all_left || all_right) {
-              const float step = all_left ? slope : -slope, base = fmaf(-step, dist, add);
+              const float step = all_left ? slope : -slope, base = -step * dist;
               scores([&](int u) { return fmaf(step, static_cast<float>(u), base); });
             } else {
-              scores([&](int u) { return fmaf(-slope, fabsf(dist - static_cast<float>(u)), add); });
+              scores([&](int u) { return -slope * fabsf(dist - static_cast<float>(u)); });
             }
           } else {
             scores([](int) { return 0.f; });
@@ -604,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const int key = kv0 + c * 32 + lane;
-                id[c] = key < a.nk ? __ldg(&a.doc_k[(int64_t)w.b * a.nk + key]) : -1;
+                id[c] = key < a.nk ? __ldg(&a.doc_k[(int64_t)b * a.nk + key]) : -1;
               }
               // each document among the warp's rows in turn: its keys by ballot
               uint32_t todo = __ballot_sync(0xffffffffu, dq >= 0);
@@ -634,25 +748,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = 0; u < 32; u += 2)
               t_max = max3(t_max, __uint_as_float(s[c][u]), __uint_as_float(s[c][u + 1]));
           reframe();
-          if (!ok) break;
           weights(std::integral_constant<int, 0>{});
         }
-        l = fmaf(l, alpha, (g0 + g1) + (g2 + g3));
+        if (!ok) break;
+        l += (g0 + g1) + (g2 + g3);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_full[x]);
+        bar_arrive(p_full + 8 * x);
       }
       // ---- out = O / l and the log-sum-exp; a split writes O and its frame to the workspace
       if (ok && my_tiles > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[x], (my_tiles - 1) & 1, abort_flag));
+        // (two tiles at head_dim 128 commit it once, after their last P V)
+        const int last = C::kOver && !solo ? 0 : my_tiles - 1;
+        ok = warp_wait(o_full + 8 * x, last & 1, abort_at);
         tc_fence_after();
       }
       if (ok) {
-        const int64_t line = ((int64_t)w.b * a.hq + w.h) * a.nq + row;
+        const int b = lds(misc + kWSeq), split = lds(misc + kWSplit);
+        const int64_t line = ((int64_t)b * a.hq + h) * a.nq + row;
         const bool seen = my_tiles > 0 && l != 0.f;
         const float inv = seen ? 1.0f / l : 0.f;
-        uint16_t* const dst = static_cast<uint16_t*>(a.o) + w.b * a.o_sb + w.h * a.o_sh + row * a.o_sn;
-        float* const part = a.part_o + ((int64_t)w.split * a.batch * a.hq * a.nq + line) * DP;
+        uint16_t* const dst = static_cast<uint16_t*>(a.o) + b * a.o_sb + h * a.o_sh + row * a.o_sn;
+        float* const part = a.part_o + ((int64_t)split * a.batch * a.hq * a.nq + line) * DP;
 #pragma unroll 1
         for (int c = 0; c < DP / 32 && c * 32 < a.d; ++c) {
           uint32_t o[32];
@@ -688,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (valid) {
           if (a.splits > 1)
-            *reinterpret_cast<float2*>(a.part_ml + ((int64_t)w.split * a.batch * a.hq * a.nq + line) * 2) =
+            *reinterpret_cast<float2*>(a.part_ml + ((int64_t)split * a.batch * a.hq * a.nq + line) * 2) =
                 make_float2(seen ? m : kNegInf, seen ? l : 0.f);
           else if (a.lse)
             a.lse[line] = seen ? (m + __log2f(l)) * kL2 : kNegInf;
@@ -702,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(lds(misc + kWTmem), 512);
   }
 }
 
