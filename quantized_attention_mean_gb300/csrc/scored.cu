@@ -38,10 +38,16 @@ struct DocTile {
   int pad;     // some padding
 };
 
+// The cap's polynomial (cap_step).
+struct CapPoly {
+  float k, c[5];  // 1 / cap; coefficients times cap, base 2
+};
+
 struct ScoredArgs {
   int batch, hq, hkv, nq, nk, d, dtype, causal, splits, k_tiles, q_offset, vec;
   float c2;           // sm_scale log2(e)
   float cap2, cap_k, cap_x;  // cap log2(e); 2 sm_scale log2(e) / cap; sm_scale / cap
+  CapPoly poly;
   void* o; int64_t o_sb, o_sh, o_sn;
   float* lse;
   const float* slopes;
@@ -109,25 +115,48 @@ __device__ __forceinline__ void cap_quotient(float (&t)[16], float k, float m2, 
   for (int u = 0; u < 16; ++u) t[u] = rcpf(t[u]);
   each2(t, [&](float& p, float& q) { fma2(p, q, p, q, m2, m2, off, off); });
 }
-// The same, plus off, for |s| <= cap: x = s / cap times a polynomial of x^2, the minimax one of degree 6 of tanh(x) / x
-// on [0, 1] (found by exchange; tanh is off by at most 1.1e-7 in fp32). One exponential per score
-// is left on the special-function unit, which with the quotient's three bounds the kernel.
-__device__ __forceinline__ void cap_polynomial(float (&t)[16], float k, float cap, float off) {
-  constexpr float c[7] = {0.9999999403953552f,   -0.33332881331443787f,  0.13325709104537964f, -0.05347844585776329f,
-                          0.020331112667918205f, -0.006239818874746561f, 0.0010531365405768156f};
-  float z[16], y[16];
-  each2(t, [&](float& p, float& q) { mul2(p, q, p, q, k, k); });
+// The same for |s| <= 0.7 cap, plus off + line(u), in four steps: x = s / cap times a polynomial of x^2, the minimax one
+// of degree 4 of tanh(x) / x there (found by exchange; tanh is off by at most 2.5e-7 in fp32). It leaves one
+// exponential per score on the special-function unit, which the quotient's three overload.
+template <typename L>
+__device__ __forceinline__ void cap_step(const CapPoly& p, int part, float (&t)[8], float (&z)[8], float (&y)[8], L line,
+                                         bool lined, float off) {
 #pragma unroll
-  for (int u = 0; u < 16; u += 2) mul2(z[u], z[u + 1], t[u], t[u + 1], t[u], t[u + 1]);
-#pragma unroll
-  for (int u = 0; u < 16; u += 2) fma2(y[u], y[u + 1], z[u], z[u + 1], c[6], c[6], c[5], c[5]);
-#pragma unroll
-  for (int i = 4; i >= 0; --i)
-#pragma unroll
-    for (int u = 0; u < 16; u += 2) fma2(y[u], y[u + 1], y[u], y[u + 1], z[u], z[u + 1], c[i], c[i]);
-  each2(t, [&](float& p, float& q) { mul2(p, q, p, q, cap, cap); });
-#pragma unroll
-  for (int u = 0; u < 16; u += 2) fma2(t[u], t[u + 1], t[u], t[u + 1], y[u], y[u + 1], off, off);
+  for (int u = 0; u < 8; u += 2) {
+    if (part == 0) {
+      mul2(t[u], t[u + 1], t[u], t[u + 1], p.k, p.k);
+      mul2(z[u], z[u + 1], t[u], t[u + 1], t[u], t[u + 1]);
+    } else if (part == 1) {
+      fma2(y[u], y[u + 1], z[u], z[u + 1], p.c[4], p.c[4], p.c[3], p.c[3]);
+      fma2(y[u], y[u + 1], y[u], y[u + 1], z[u], z[u + 1], p.c[2], p.c[2]);
+    } else if (part == 2) {
+      fma2(y[u], y[u + 1], y[u], y[u + 1], z[u], z[u + 1], p.c[1], p.c[1]);
+      fma2(y[u], y[u + 1], y[u], y[u + 1], z[u], z[u + 1], p.c[0], p.c[0]);
+    } else {
+      float f0 = off, f1 = off;
+      if (lined) add2(f0, f1, line(u), line(u + 1), off, off);
+      fma2(t[u], t[u + 1], t[u], t[u + 1], y[u], y[u + 1], f0, f1);
+    }
+  }
+}
+// 16 columns of tensor memory into r[OFF ..] and their largest value.
+template <int OFF>
+__device__ __forceinline__ void ld16_max(uint32_t taddr, uint32_t (&r)[32], float& m) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, [%17];"
+      : "=r"(r[OFF + 0]), "=r"(r[OFF + 1]), "=r"(r[OFF + 2]), "=r"(r[OFF + 3]), "=r"(r[OFF + 4]),
+        "=r"(r[OFF + 5]), "=r"(r[OFF + 6]), "=r"(r[OFF + 7]), "=r"(r[OFF + 8]), "=r"(r[OFF + 9]),
+        "=r"(r[OFF + 10]), "=r"(r[OFF + 11]), "=r"(r[OFF + 12]), "=r"(r[OFF + 13]),
+        "=r"(r[OFF + 14]), "=r"(r[OFF + 15]), "=f"(m)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void wait_ld_max8(float (&m)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(m[0]), "+f"(m[1]), "+f"(m[2]), "+f"(m[3]), "+f"(m[4]), "+f"(m[5]), "+f"(m[6]), "+f"(m[7])
+               :
+               : "memory");
 }
 
 // 32 columns of tensor memory and their largest value (both valid after a tcgen05.wait::ld).
@@ -538,13 +567,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     float slope = 0.f;
     if constexpr (BIAS) slope = __ldg(&a.slopes[h]) * kL2e;
     const float cap_m2 = -2.0f * a.cap2, cap_in = a.cap_k;
-    float m = kNegInf;  // the frame's maximum, base 2
+    // fp16 weights are held at up to 2^(7 + 8): 7 bits more before the smallest lose bits
+    constexpr float kHead = BF16 ? 0.f : 7.0f;
+    constexpr float kSlack = BF16 ? 60.0f : 7.0f;  // by how much a maximum may be overestimated
+    float m = kNegInf;                             // the frame, base 2
     float l = 0.f;
     bool ok = true;
     if (active) {
-      // head_dim 64: tile B starts when A's first weights are half done, so that one tile's loads and
-      // waits lie beside the other's exponentials (they keep that distance)
-      if (!C::kOver && x == 1 && lds(misc + kWTilesA) > 0) ok = warp_wait(p_half, 0, abort_at);
       for (int j = 0; j < my_tiles && ok; ++j) {
         const int sb = solo ? j & 1 : x;
         const uint32_t tS = tmem + lane_base + sb * 128;
@@ -583,8 +612,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) tc_fence_after();
           }
         };
-        // The frame is kept unless the maximum grew by more than 8.
+        // The frame m lies kHead below the maximum that set it, and is kept unless that grew by more than 8.
         auto reframe = [&]() {
+          t_max -= kHead;
           const bool grow = t_max > m + 8.0f || (m == kNegInf && t_max > kNegInf);
           if (__any_sync(0xffffffffu, grow)) {
             const float alpha = grow ? ex2f(m - t_max) : 1.0f;
@@ -597,30 +627,80 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           m_use = m == kNegInf ? 0.f : m;
         };
-        // P = 2^(t - m), summed in 32 bits, rounded once to the operands' type, sixteen keys at a time (each
-        // step over all of them before the next, so that latencies overlap). FORM: 0 s holds the
-        // scores t; 1 the products; 2, 3 the products to be capped, by quotient or by polynomial
-        auto weights = [&](auto form) {
+        // P = 2^(t - m), summed in 32 bits, rounded once to the operands' type. FORM says what s holds: 0 the
+        // scores t; 1 products; 2, 3 products to be capped, by quotient or by polynomial; LINE adds a bias of
+        // base + step u. Eight keys enter per round; a pair's arithmetic, its exponentials and its
+        // sum and rounding lie one round apart and are issued in turn, so that the special-function unit (four
+        // cycles per exponential and warp) never waits for the others.
+        auto weights = [&](auto form, auto line, float step, float base) {
           constexpr int FORM = decltype(form)::value;
+          constexpr bool LINE = decltype(line)::value;
+          constexpr int kLag = FORM == 2 ? 3 : 2;
+          const float off = (FORM == 2 ? a.cap2 : 0.f) - m_use + base;
+          float st[LINE ? 8 : 1];
+          if constexpr (LINE)
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            float t[16];
+            for (int u = 0; u < 8; ++u) st[u] = step * static_cast<float>(u);
+          float r0[8], r1[8], r2[8];  // rounds in flight, the newest first
 #pragma unroll
-            for (int u = 0; u < 16; ++u) t[u] = __uint_as_float(s[g >> 1][(g & 1) * 16 + u]);
-            if constexpr (FORM == 0) each2(t, [&](float& p, float& q) { add2(p, q, p, q, -m_use, -m_use); });
-            if constexpr (FORM == 1) each2(t, [&](float& p, float& q) { fma2(p, q, p, q, a.c2, a.c2, -m_use, -m_use); });
-            if constexpr (FORM == 2) cap_quotient(t, cap_in, cap_m2, a.cap2 - m_use);
-            if constexpr (FORM == 3) cap_polynomial(t, a.cap_x, a.cap2, -m_use);
+          for (int q = 0; q < 16 + kLag; ++q) {
+            float in[8], mid[8], o8 = off;
+            if constexpr (LINE) o8 = fmaf(step, static_cast<float>((FORM == 2 ? q - 2 : q) * 8), off);
+            if (q < 16)
 #pragma unroll
-            for (int u = 0; u < 16; ++u) t[u] = ex2f(t[u]);
+              for (int u = 0; u < 8; ++u) in[u] = __uint_as_float(s[q >> 2][(q & 3) * 8 + u]);
 #pragma unroll
-            for (int u = 0; u < 16; u += 4) {
-              add2(g0, g1, g0, g1, t[u], t[u + 1]);
-              add2(g2, g3, g2, g3, t[u + 2], t[u + 3]);
+            for (int u = 0; u < 8; ++u) mid[u] = FORM == 2 ? r1[u] : r0[u];
+            float z[8], y[8];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              // exponentials of the round before
+              if (FORM == 2) {
+                if (q >= 2 && q < 18) {
+                  float f0 = o8, f1 = o8;
+                  if constexpr (LINE) add2(f0, f1, st[i], st[i + 1], o8, o8);
+                  fma2(mid[i], mid[i + 1], mid[i], mid[i + 1], cap_m2, cap_m2, f0, f1);
+                  mid[i] = ex2f(mid[i]);
+                  mid[i + 1] = ex2f(mid[i + 1]);
+                }
+                if (q >= 1 && q < 17) {
+                  add2(r0[i], r0[i + 1], r0[i], r0[i + 1], 1.0f, 1.0f);
+                  r0[i] = rcpf(r0[i]);
+                  r0[i + 1] = rcpf(r0[i + 1]);
+                }
+              } else if (q >= 1 && q < 17) {
+                mid[i] = ex2f(mid[i]);
+                mid[i + 1] = ex2f(mid[i + 1]);
+              }
+              // arithmetic of the new round
+              if (q < 16) {
+                float f0 = o8, f1 = o8;
+                if constexpr (LINE && FORM != 2 && FORM != 3) add2(f0, f1, st[i], st[i + 1], o8, o8);
+                if constexpr (FORM == 0) add2(in[i], in[i + 1], in[i], in[i + 1], f0, f1);
+                if constexpr (FORM == 1) fma2(in[i], in[i + 1], in[i], in[i + 1], a.c2, a.c2, f0, f1);
+                if constexpr (FORM == 2) {
+                  mul2(in[i], in[i + 1], in[i], in[i + 1], cap_in, cap_in);
+                  in[i] = ex2f(in[i]);
+                  in[i + 1] = ex2f(in[i + 1]);
+                }
+                if constexpr (FORM == 3) cap_step(a.poly, i / 2, in, z, y, [&](int u) { return LINE ? st[u] : 0.f; }, LINE, o8);
+              }
+              // sum and rounding of the oldest round
+              if (q >= kLag) {
+                const float e0 = FORM == 2 ? r2[i] : r1[i], e1 = FORM == 2 ? r2[i + 1] : r1[i + 1];
+                if (i & 2) add2(g2, g3, g2, g3, e0, e1);
+                else add2(g0, g1, g0, g1, e0, e1);
+                const int w = (q - kLag) * 4 + i / 2;
+                s[w >> 5][w & 31] = pack16<BF16>(e0, e1);
+              }
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) s[g >> 2][(g & 3) * 8 + u] = pack16<BF16>(t[2 * u], t[2 * u + 1]);
-            if (g == 3) {
+            for (int u = 0; u < 8; ++u) {
+              if (FORM == 2) { r2[u] = mid[u]; r1[u] = r0[u]; }
+              else r1[u] = mid[u];
+              r0[u] = in[u];
+            }
+            if (q == 7 + kLag) {
               wait_pv();
               if (!ok) return;
               if (releases && j > 0 && (!C::kOver || solo)) bar_arrive(v_empty + 8 * ((uint32_t)(j - 1) % C::kVStages));
@@ -629,23 +709,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 bar_arrive(p_half + 8 * x);
-              } else if (x == 0 && j == 0) {
-                bar_arrive(p_half);
               }
             }
-            if (g == 7) tmem_st32(tP + 32, s[1]);
+            if (q == 15 + kLag) tmem_st32(tP + 32, s[1]);
           }
         };
-        if (!BIAS && !masked) {
+        using No = std::false_type;
+        using Yes = std::true_type;
+        // Weights from products; the polynomial where every product of the warp is within its range.
+        auto weights_of = [&](auto line, bool small, float step, float base) {
+          if constexpr (CAP) {
+            if (small) weights(std::integral_constant<int, 3>{}, line, step, base);
+            else weights(std::integral_constant<int, 2>{}, line, step, base);
+          } else {
+            weights(std::integral_constant<int, 1>{}, line, step, base);
+          }
+        };
+        // The bias along a tile that lies on one side of every row's position (or whose other side the causal
+        // mask hides) is base + step u. Its largest value beside the largest product of each 16 keys bounds the
+        // maximum by at most 15 steps too much, which the frame's headroom takes where they are few.
+        float step = 0.f, base = 0.f;
+        bool line = true;
+        if constexpr (BIAS) {
+          const float dist = static_cast<float>(pos - kv0);  // exact below 2^24
+          const bool all_left = __all_sync(0xffffffffu, kv0 + 127 <= pos || (a.causal && prefix <= 0));
+          line = all_left || __all_sync(0xffffffffu, kv0 >= pos);
+          step = all_left ? slope : -slope;
+          base = -step * dist;
+        }
+        if (!masked && (!BIAS || (line && fabsf(step) * 15.0f <= kSlack))) {
           // products; the cap and the scale keep their order, so their largest gives the maximum
-          float cm[4];
+          bool small = false;
+          auto capped = [&](float v) {
+            return CAP ? fmaf(rcpf(1.0f + ex2f(v * cap_in)), cap_m2, a.cap2) : v * a.c2;
+          };
+          if constexpr (BIAS) {
+            float cm[8];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) ld32_max(tS + c * 32, s[c], cm[c]);
+            for (int c = 0; c < 4; ++c) {
+              ld16_max<0>(tS + c * 32, s[c], cm[2 * c]);
+              ld16_max<16>(tS + c * 32 + 16, s[c], cm[2 * c + 1]);
+            }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
-          wait_ld_max(cm);
-          release_s();
-          const float top = fmaxf(max3(cm[0], cm[1], cm[2]), cm[3]);
+            for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+            wait_ld_max8(cm);
+            const float end = step > 0.f ? 15.0f * step : 0.f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) t_max = fmaxf(t_max, fmaf(step, static_cast<float>(c * 16), capped(cm[c])));
+            t_max += base + end;
+          } else {
+            float cm[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ld32_max(tS + c * 32, s[c], cm[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+            wait_ld_max(cm);
+            t_max = capped(fmaxf(max3(cm[0], cm[1], cm[2]), cm[3]));
+          }
           if constexpr (CAP) {
             float big = 0.f;
 #pragma unroll
@@ -653,15 +773,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int u = 0; u < 32; u += 2)
                 big = max3(big, fabsf(__uint_as_float(s[c][u])), fabsf(__uint_as_float(s[c][u + 1])));
-            t_max = fmaf(rcpf(1.0f + ex2f(top * cap_in)), cap_m2, a.cap2);
-            reframe();
-            if (__all_sync(0xffffffffu, big * a.cap_x <= 1.0f)) weights(std::integral_constant<int, 3>{});
-            else weights(std::integral_constant<int, 2>{});
-          } else {
-            t_max = top * a.c2;
-            reframe();
-            weights(std::integral_constant<int, 1>{});
+            small = __all_sync(0xffffffffu, big * a.cap_x <= 0.7f);
           }
+          release_s();
+          reframe();
+          if constexpr (BIAS) weights_of(Yes{}, small, step, base);
+          else weights_of(No{}, small, 0.f, 0.f);
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
@@ -691,17 +808,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           };
           if constexpr (BIAS) {
-            // The bias is linear along a tile that lies on one side of every row's position (or
-            // whose other side the causal mask hides)
-            const float dist = static_cast<float>(pos - kv0);  // exact below 2^24
-            const bool all_left = __all_sync(0xffffffffu, kv0 + 127 <= pos || (a.causal && prefix <= 0));
-            const bool all_right = __all_sync(0xffffffffu, kv0 >= pos);
-            if (all_left || all_right) {
-              const float step = all_left ? slope : -slope, base = -step * dist;
-              scores([&](int u) { return fmaf(step, static_cast<float>(u), base); });
-            } else {
-              scores([&](int u) { return -slope * fabsf(dist - static_cast<float>(u)); });
-            }
+            const float dist = static_cast<float>(pos - kv0);
+            if (line) scores([&](int u) { return fmaf(step, static_cast<float>(u), base); });
+            else scores([&](int u) { return -slope * fabsf(dist - static_cast<float>(u)); });
           } else {
             scores([](int) { return 0.f; });
           }
@@ -748,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = 0; u < 32; u += 2)
               t_max = max3(t_max, __uint_as_float(s[c][u]), __uint_as_float(s[c][u + 1]));
           reframe();
-          weights(std::integral_constant<int, 0>{});
+          weights(std::integral_constant<int, 0>{}, No{}, 0.f, 0.f);
         }
         if (!ok) break;
         l += (g0 + g1) + (g2 + g3);
@@ -1038,6 +1147,10 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
   a.c2 = (float)(scale * 1.4426950408889634);
   a.cap2 = (float)(softcap * 1.4426950408889634);
   a.cap_x = softcap > 0.f ? scale / softcap : 0.f;
+  const double tanh_c[5] = {0.9999997019767761, -0.3333034813404083, 0.13282497227191925, -0.050881292670965195,
+                            0.013819585554301739};
+  a.poly.k = a.cap_x;
+  for (int i = 0; i < 5; ++i) a.poly.c[i] = (float)(tanh_c[i] * softcap * 1.4426950408889634);
   a.cap_k = softcap > 0.f ? (float)(2.0 * 1.4426950408889634 * scale / softcap) : 0.f;
   a.o = out->data; a.o_sb = view[3].sb; a.o_sh = view[3].sh; a.o_sn = view[3].sn;
   a.lse = return_lse ? lse : nullptr;
