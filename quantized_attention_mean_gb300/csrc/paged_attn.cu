@@ -10,12 +10,18 @@
 //
 // Split: the (sequence, head, 64-key tile) items of the whole batch form one line, cut into equal
 // ranges, one per CTA, so the load is even whatever the lengths (which only the device knows). Each
-// warp takes 16 keys of a tile through its own ring of cp.async stages and keeps its own running
-// maximum, sum and accumulator; no barrier runs inside a range. At a (sequence, head)'s last tile
-// in a range the warps are merged in a fixed order; a result that lies in one range is written
-// out, others go to the workspace and the join kernel sums them in the order of the ranges, so
-// results do not depend on timing.
+// warp takes 16 keys of a tile through its own ring of stages and keeps its own running maximum, sum
+// and accumulator; no barrier runs inside a range. At a (sequence, head)'s last tile in a range the
+// warps are merged in a fixed order; a result that lies in one range is written out, others go to
+// the workspace and the join kernel sums them in the order of the ranges, so results do not depend
+// on timing.
+//
+// Loads: pages of whole 8-row blocks come by TMA, a box of rows per lane, which costs the warp next to no
+// instructions (16-byte cp.async per lane took 835 instructions per warp and tile and stalled at 4.6
+// TB/s); tokens that are not there are boxes outside of the tensor and arrive as zeros. Other
+// page sizes use cp.async, rows that no 16-byte load fits plain loads.
 #include <cmath>
+#include <cstring>
 
 #include "../../include/sageattn.h"
 #include "launch.h"
@@ -31,6 +37,7 @@ constexpr int kTile = kWarps * kKeys;      // keys per tile
 constexpr int kCtas = 304;                 // two resident CTAs per SM
 constexpr int kRows = 16;                  // query heads per row block
 constexpr int kMinTiles = 2;               // tiles a CTA takes at least
+enum { kLoadTma = 0, kLoadVec = 1, kLoadAny = 2 };
 constexpr float kLog2eF = 1.4426950408889634f, kLn2F = 0.6931471805599453f;
 
 struct DecodeArgs {
@@ -41,7 +48,10 @@ struct DecodeArgs {
   const float* slopes;      // [hq] or null
   const int* q_pos;         // [batch] or null (length - 1)
   float sm_scale, cap;
-  int hq, group, row_blocks, max_len, vec;
+  int hq, group, row_blocks, max_len;
+  int load;                 // how rows are read: kLoadTma, kLoadVec or kLoadAny
+  int box_rows;             // rows of a TMA box
+  int page_shift;           // log2 of page_size, or -1
   // workspace
   int* err;                 // status word
   int* cta_err;             // [kCtas]
@@ -55,59 +65,50 @@ struct DecodeArgs {
 template <int DP>
 struct DecodeCfg {
   static constexpr int kStages = DP == 128 ? 3 : 6;
-  static constexpr int kRowBytes = DP * 2;
-  static constexpr int kTileBytes = kKeys * kRowBytes;        // K or V of one warp's tile
+  static constexpr int kChunks = DP / 64;                     // blocks of 64 channels, rows of 128 bytes
+  static constexpr int kChunkBytes = kKeys * 128;
+  static constexpr int kTileBytes = kChunks * kChunkBytes;    // K or V of one warp's tile
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes;
-  static constexpr int kOffMerge = kWarps * kWarpBytes;       // two warps' accumulators
-  static constexpr int kOffMl = kOffMerge + 2 * kRows * DP * 4;
-  static constexpr int kSmem = kOffMl + kWarps * kRows * 2 * 4 + 64;
+  static constexpr int kOffMerge = kWarps * kWarpBytes;       // two warps' accumulators, 64 channels at a time
+  static constexpr int kOffMl = kOffMerge + 2 * kRows * 64 * 4;
+  static constexpr int kOffBar = kOffMl + kWarps * kRows * 2 * 4;
+  static constexpr int kSmem = kOffBar + kWarps * kStages * 8;
 };
 
 // Tiles of a sequence of n tokens.
 __device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
 
-// Total number of (sequence, head, tile) items and, for the item index `at`, its sequence and its place
-// there. All threads call it; lengths that are out of range count as 0 and set `bad`.
-struct Found {
-  long long total, base;
-  int b;
+// The items (sequence, head, tile) of sequences [b0, b0 + blockDim): this thread's count, the sum before it and the
+// sum of all. Lengths that are out of range count as 0 and set `bad`.
+struct Scan {
+  long long n, before, all;
 };
-__device__ Found find_item(const DecodeArgs& a, int heads, long long at, bool& bad) {
+__device__ __forceinline__ Scan scan_items(const DecodeArgs& a, int heads, int b0, bool& bad) {
   __shared__ long long s_sum[32];
-  __shared__ long long s_base;
-  __shared__ int s_b;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  if (threadIdx.x == 0) { s_b = a.c.batch; s_base = 0; }
-  long long run = 0;
-  for (int b0 = 0; b0 < a.c.batch; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
-    long long n = 0;
-    if (b < a.c.batch) {
-      const int len = checked_len(a.c, b, a.max_len);
-      if (len < 0) bad = true;
-      n = (long long)tiles_of(max(len, 0)) * heads;
-    }
-    long long inc = n;
+  const int b = b0 + threadIdx.x;
+  Scan r{0, 0, 0};
+  if (b < a.c.batch) {
+    const int len = checked_len(a.c, b, a.max_len);
+    if (len < 0) bad = true;
+    r.n = (long long)tiles_of(max(len, 0)) * heads;
+  }
+  long long inc = r.n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
-    }
-    __syncthreads();
-    if (lane == 31) s_sum[warp] = inc;
-    __syncthreads();
-    long long before = run, all = 0;
-    for (int w = 0; w < nw; ++w) {
-      if (w < warp) before += s_sum[w];
-      all += s_sum[w];
-    }
-    const long long lo = before + inc - n;
-    if (n > 0 && at >= lo && at < lo + n) { s_b = b; s_base = lo; }
-    run += all;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
   }
   __syncthreads();
-  return {run, s_base, s_b};
+  if (lane == 31) s_sum[warp] = inc;
+  __syncthreads();
+  r.before = inc - r.n;
+  for (int w = 0; w < nw; ++w) {
+    if (w < warp) r.before += s_sum[w];
+    r.all += s_sum[w];
+  }
+  return r;
 }
 
 // CTAs that share `total` items, and the first item of CTA i.
@@ -170,36 +171,67 @@ __device__ __forceinline__ T round_to(float x) {
   else return __float2bfloat16_rn(x);
 }
 
-// The 16 keys of item u that belong to this warp into one stage: K rows, then V rows, 16-byte chunk c of
-// row r at chunk c ^ (r & 7). `page` is the page of row (lane & 15) or -1 where nothing is read;
-// such rows and the channels past d become zero, so they add exactly nothing.
+__device__ __forceinline__ int page_index(const DecodeArgs& a, int key) {
+  return a.page_shift >= 0 ? key >> a.page_shift : key / a.c.page_size;
+}
+// Page and slot of token `key` of sequence b; page -1 where there is none.
+__device__ __forceinline__ void find_page(const DecodeArgs& a, int b, int key, bool live, int& page, int& slot, int& err) {
+  page = -1;
+  slot = 0;
+  if (!live) return;
+  const int i = page_index(a, key);
+  slot = key - i * a.c.page_size;
+  const int pg = __ldg(&a.c.table[b * a.c.table_stride + i]);
+  if (pg >= 0 && pg < a.c.num_pages) page = pg;
+  else err = kDevPage;
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// The 16 keys of an item that belong to this warp into one stage: K, then V, per 64 channels rows of 128
+// bytes whose 16-byte unit c lies at c ^ (row & 7). Tokens that are not there and channels past d
+// become zero. `page`, `slot`: TMA: of this lane's box (K or V by bit 0, channels by bit 1 at head_dim 128, rows by the
+// rest); otherwise of row (lane & 15).
 template <typename T, int DP>
-__device__ __forceinline__ void load_stage(const DecodeArgs& a, const Cursor& u, int page, int slot,
-                                           uint8_t* stage) {
+__device__ __forceinline__ void load_stage(const DecodeArgs& a, const CUtensorMap* tmK, const CUtensorMap* tmV, int h,
+                                           int page, int slot, uint8_t* stage, uint32_t bar) {
   using C = DecodeCfg<DP>;
   const int lane = threadIdx.x & 31;
-  const int h = u.h / a.row_blocks;
+  const uint32_t base = smem_u32(stage);
+  if (a.load == kLoadTma) {
+    if (lane == 0)
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(C::kStageBytes) : "memory");
+    const int kv = lane & 1, chunk = C::kChunks == 2 ? (lane >> 1) & 1 : 0, rows = (lane >> C::kChunks) * a.box_rows;
+    if (rows < kKeys)
+      tma_box(base + kv * C::kTileBytes + chunk * C::kChunkBytes + rows * 128, kv ? tmV : tmK, bar, chunk * 64, slot, h,
+              page >= 0 ? page : a.c.num_pages);
+    return;
+  }
   const T* kb = static_cast<const T*>(a.c.k) + h * a.c.k_sh;
   const T* vb = static_cast<const T*>(a.c.v) + h * a.c.v_sh;
-  constexpr int kChunks = DP / 8, kRowsPer = 32 / kChunks;  // rows that one pass of the warp covers
-  const int c = lane % kChunks;
-  const uint32_t base = smem_u32(stage);
-#pragma unroll
+  constexpr int kUnits = DP / 8, kRowsPer = 32 / kUnits;  // rows that one pass of the warp covers
+  const int c = lane % kUnits;
+#pragma unroll 2
   for (int i = 0; i < kKeys / kRowsPer; ++i) {
-    const int r = i * kRowsPer + lane / kChunks;
+    const int r = i * kRowsPer + lane / kUnits;
     const int pg = __shfl_sync(0xffffffffu, page, r), sl = __shfl_sync(0xffffffffu, slot, r);
     const bool in = pg >= 0 && c * 8 < a.c.d;
-    const int off = r * C::kRowBytes + ((c ^ (r & 7)) << 4);
+    const int off = (c >> 3) * C::kChunkBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
     const T* ks = in ? kb + pg * a.c.k_sp + sl * a.c.k_st + c * 8 : kb;
     const T* vs = in ? vb + pg * a.c.v_sp + sl * a.c.v_st + c * 8 : vb;
-    if (a.vec) {
+    if (a.load == kLoadVec) {
       cp_async16(base + off, ks, in ? 16 : 0);
       cp_async16(base + C::kTileBytes + off, vs, in ? 16 : 0);
     } else {
-      // rows that no 16-byte load fits: element loads
       T* kd = reinterpret_cast<T*>(stage + off);
       T* vd = reinterpret_cast<T*>(stage + C::kTileBytes + off);
-#pragma unroll
+#pragma unroll 1
       for (int e = 0; e < 8; ++e) {
         const bool ok = in && c * 8 + e < a.c.d;
         kd[e] = ok ? ks[e] : T(0.0f);
@@ -209,18 +241,26 @@ __device__ __forceinline__ void load_stage(const DecodeArgs& a, const Cursor& u,
   }
 }
 
-// Page (or -1) and slot of this lane's row (lane & 15) of this warp's part of item u.
-__device__ __forceinline__ void find_page(const DecodeArgs& a, const Cursor& u, bool live, int& page, int& slot,
-                                          int& err) {
-  page = -1;
-  slot = 0;
-  const int key = u.tile * kTile + (threadIdx.x >> 5) * kKeys + (threadIdx.x & 15);
-  if (!live || key >= u.len) return;
-  const int i = key / a.c.page_size;
-  slot = key - i * a.c.page_size;
-  const int pg = __ldg(&a.c.table[u.b * a.c.table_stride + i]);
-  if (pg >= 0 && pg < a.c.num_pages) page = pg;
-  else err = kDevPage;
+// Waits for a stage's TMA boxes, two seconds at most.
+__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity) {
+  unsigned long long t0 = 0;
+  for (uint32_t it = 0; it < (1u << 30); ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000u)
+        : "memory");
+    if (ok) return true;
+    if ((it & 63u) == 63u) {
+      const unsigned long long t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      else if (t - t0 > kWaitTimeoutNs) return false;
+    }
+  }
+  return false;
 }
 
 // Rows r0 and r0 + 8 of a finished (sequence, head) from one warp's accumulators.
@@ -249,33 +289,58 @@ __device__ __forceinline__ void write_rows(const DecodeArgs& a, int b, int row0,
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 2)
+    decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const DecodeArgs a) {
   using C = DecodeCfg<DP>;
   constexpr int S = C::kStages, KS = DP / 16, NT = DP / 8;
-  extern __shared__ __align__(128) uint8_t sm[];
+  // fp16 weights are held at up to 2^(7 + 8): 7 bits more before the smallest lose bits
+  constexpr float kHead = std::is_same<T, __half>::value ? 7.0f : 0.f;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  __shared__ int s_err[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = a.c.hkv * a.row_blocks;
   uint8_t* const ring = sm + warp * C::kWarpBytes;
   float* const merge = reinterpret_cast<float*>(sm + C::kOffMerge);
   float* const ml = reinterpret_cast<float*>(sm + C::kOffMl);
+  const uint32_t bars = smem_u32(sm + C::kOffBar) + warp * S * 8;
+  if (lane < S) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + lane * 8) : "memory");
+  fence_mbar_init();
+  if (a.load == kLoadTma && lane == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
   pdl_wait();
+  // ---- this CTA's range of the line: the total, then the sequence that its first item lies in
+  __shared__ long long s_base;
+  __shared__ int s_b;
   bool bad = false;
-  int err = 0;
-  // total first (any item index finds it), then this CTA's first item
-  const long long total = find_item(a, heads, 0, bad).total;
-  const int ctas = total > 0 ? ctas_of(total) : 0;
-  const int me = blockIdx.x;
-  if (bad) err = kDevSeqlens;
-  long long left = 0;
-  Cursor cu{a.c.batch, 0, 0, 1, 0};
+  if (threadIdx.x == 0) { s_b = a.c.batch; s_base = 0; }
+  Scan sc = scan_items(a, heads, 0, bad);
+  long long total = sc.all;
+  for (int b0 = blockDim.x; b0 < a.c.batch; b0 += blockDim.x) total += scan_items(a, heads, b0, bad).all;
+  const int ctas = total > 0 ? ctas_of(total) : 0, me = blockIdx.x;
+  long long left = 0, i0 = 0;
   if (me < ctas) {
-    const long long i0 = first_item(total, ctas, me);
+    i0 = first_item(total, ctas, me);
     left = first_item(total, ctas, me + 1) - i0;
-    const Found f = find_item(a, heads, i0, bad);
-    cu.b = f.b;
+    long long base = 0;
+    for (int b0 = 0;;) {
+      const long long lo = base + sc.before;
+      if (sc.n > 0 && i0 >= lo && i0 < lo + sc.n) { s_b = b0 + threadIdx.x; s_base = lo; }
+      base += sc.all;
+      b0 += blockDim.x;
+      if (base > i0 || b0 >= a.c.batch) break;
+      sc = scan_items(a, heads, b0, bad);
+    }
+  }
+  __syncthreads();
+  int err = bad ? kDevSeqlens : 0;
+  Cursor cu{a.c.batch, 0, 0, 1, 0};
+  if (left > 0) {
+    cu.b = s_b;
     cu.len = checked_len(a.c, cu.b, a.max_len);
     cu.tiles = tiles_of(cu.len);
-    const long long in = i0 - f.base;
+    const long long in = i0 - s_base;
     cu.h = (int)(in / cu.tiles);
     cu.tile = (int)(in - (long long)cu.h * cu.tiles);
   }
@@ -285,17 +350,25 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(const DecodeArgs
   Cursor ld = cu;
   long long to_load = left;
   int page, slot;
-  find_page(a, ld, to_load > 0, page, slot, err);
-#pragma unroll 1
-  for (int s = 0; s < S - 1; ++s) {
-    if (to_load > 0) {
-      load_stage<T, DP>(a, ld, page, slot, ring + s * C::kStageBytes);
+  const int my_row = a.load == kLoadTma ? (lane >> C::kChunks) * a.box_rows : lane & 15;
+  auto next_page = [&]() {
+    const int key = ld.tile * kTile + warp * kKeys + my_row;
+    find_page(a, ld.b, key, to_load > 0 && my_row < kKeys && key < ld.len, page, slot, err);
+  };
+  bool dead = false;  // a wait has run out: nothing more is loaded
+  auto load_next = [&](int st) {
+    if (to_load > 0 && !dead) {
+      load_stage<T, DP>(a, &tmK, &tmV, ld.h / a.row_blocks, page, slot, ring + st * C::kStageBytes, bars + st * 8);
       next_item(a, heads, ld);
       --to_load;
-      find_page(a, ld, to_load > 0, page, slot, err);
+      next_page();
     }
-    cp_async_commit();
-  }
+    if (a.load != kLoadTma) cp_async_commit();
+  };
+  __syncwarp();
+  next_page();
+#pragma unroll 1
+  for (int st = 0; st < S - 1; ++st) load_next(st);
 
   float o[NT][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
   uint32_t qf[KS][4];
@@ -305,6 +378,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(const DecodeArgs
   const float scale2 = a.sm_scale * kLog2eF;
   const float cap_in = a.cap > 0.f ? a.sm_scale / a.cap : 0.f, cap_out = a.cap * kLog2eF;
   int stage = 0;
+  uint32_t parity = 0;
   const int r0 = lane >> 2, cq = (lane & 3) * 2;
 
 #pragma unroll 1
@@ -343,68 +417,95 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(const DecodeArgs
       l0 = l1 = 0.f;
     }
     // the stage after the ones in flight goes where the previous item was
-    {
-      __syncwarp();
-      const int fill = stage == 0 ? S - 1 : stage - 1;
-      if (to_load > 0) {
-        load_stage<T, DP>(a, ld, page, slot, ring + fill * C::kStageBytes);
-        next_item(a, heads, ld);
-        --to_load;
-        find_page(a, ld, to_load > 0, page, slot, err);
-      }
-      cp_async_commit();
-      cp_async_wait<S - 1>();
-      __syncwarp();
-    }
+    __syncwarp();
+    load_next(stage == 0 ? S - 1 : stage - 1);
     const int key0 = cu.tile * kTile + warp * kKeys;
-    if (key0 < cu.len) {
-      const uint32_t kb = smem_u32(ring + stage * C::kStageBytes), vb = kb + C::kTileBytes;
-      // S = Q K^T: lanes 0-7 / 8-15 address keys 0-7 at channels +0 / +8, 16-23 / 24-31 keys 8-15
-      float s[2][4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-      {
-        const int r = (lane & 7) + ((lane >> 4) << 3);
-        const uint32_t row = kb + r * C::kRowBytes;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t b[4];
-          const int c = 2 * k + ((lane >> 3) & 1);
-          ldsm4(row + ((c ^ (r & 7)) << 4), b);
-          mma16816<T>(s[0], qf[k], b[0], b[1]);
-          mma16816<T>(s[1], qf[k], b[2], b[3]);
+    uint8_t* const here = ring + stage * C::kStageBytes;
+    if (a.load == kLoadTma) {
+      if (!dead && !__all_sync(0xffffffffu, wait_stage(bars + stage * 8, parity))) {
+        dead = true;
+        err = kDevTimeout;
+        // what is in flight lands (or runs out of time) before the shared memory goes away
+        for (int k = 0; k < (int)(left - to_load); ++k) {
+          const int st = stage + k;
+          wait_stage(bars + (st % S) * 8, parity ^ (st >= S ? 1u : 0u));
         }
       }
-      // scores in base 2; lane holds keys 8 n + cq, + 1 of rows r0 (s[n][0..1]) and r0 + 8
+      if (!dead && key0 < cu.len && key0 + kKeys > cu.len) {
+        // slots behind the last token may hold anything: as V rows they become zero (their scores are masked)
+        for (int i = lane; i < (key0 + kKeys - cu.len) * C::kChunks * 8; i += 32) {
+          const int r = cu.len - key0 + i / (C::kChunks * 8), u = i % (C::kChunks * 8);
+          *reinterpret_cast<uint4*>(here + C::kTileBytes + (u >> 3) * C::kChunkBytes + r * 128 + (u & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+    } else {
+      cp_async_wait<S - 1>();
+    }
+    __syncwarp();
+    if (key0 < cu.len) {
+      const bool upper = rows > 8;  // rows r0 + 8 are in use
+      const uint32_t kb = smem_u32(here), vb = kb + C::kTileBytes;
+      // S = Q K^T: lanes 0-7 / 8-15 address keys 0-7 at channels +0 / +8, 16-23 / 24-31 keys 8-15;
+      // two accumulators per half, so that no chain is longer than half the channels
+      float s[2][4], s2[2][4];
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int key = key0 + n * 8 + cq + e;
-          float x0 = s[n][e], x1 = s[n][2 + e];
-          if (a.cap > 0.f) {
-            x0 = tanhf(x0 * cap_in) * cap_out;
-            x1 = tanhf(x1 * cap_in) * cap_out;
-          } else {
-            x0 *= scale2;
-            x1 *= scale2;
-          }
-          const bool in = key < cu.len;
-          if (a.slopes) {
+        for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
+      {
+        const int r = (lane & 7) + ((lane >> 4) << 3), odd = (lane >> 3) & 1;
+        const uint32_t row = kb + r * 128;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint32_t b[4];
+          ldsm4(row + (k >> 2) * C::kChunkBytes + (((((2 * k) & 7) + odd) ^ (r & 7)) << 4), b);
+          mma16816<T>(k & 1 ? s2[0] : s[0], qf[k], b[0], b[1]);
+          mma16816<T>(k & 1 ? s2[1] : s[1], qf[k], b[2], b[3]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
+      // scores in base 2; lane holds keys 8 n + cq, + 1 of rows r0 (s[n][0..1]) and r0 + 8
+      if (a.cap > 0.f) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e < 2 || upper) s[n][e] = tanhf(s[n][e] * cap_in) * cap_out;
+      } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] *= scale2;
+      }
+      if (a.slopes) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = key0 + n * 8 + cq + e;
             int kp = key;
-            if (a.c.pos && in) {
-              const int i = key / a.c.page_size;
-              const int pg = __ldg(&a.c.table[cu.b * a.c.table_stride + i]);
-              if (pg >= 0 && pg < a.c.num_pages)
-                kp = __ldg(&a.c.pos[plane_at(a.c, pg, cu.h / a.row_blocks, key - i * a.c.page_size)]);
+            if (a.c.pos && key < cu.len) {
+              int pg, sl, none = 0;
+              find_page(a, cu.b, key, true, pg, sl, none);
+              if (pg >= 0) kp = __ldg(&a.c.pos[plane_at(a.c, pg, cu.h / a.row_blocks, sl)]);
             }
             const float dist = fabsf((float)((long long)qpos - kp));
-            x0 = fmaf(-sl0, dist, x0);
-            x1 = fmaf(-sl1, dist, x1);
+            s[n][e] = fmaf(-sl0, dist, s[n][e]);
+            s[n][2 + e] = fmaf(-sl1, dist, s[n][2 + e]);
           }
-          s[n][e] = in ? x0 : -INFINITY;
-          s[n][2 + e] = in ? x1 : -INFINITY;
-        }
+      }
+      if (key0 + kKeys > cu.len) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key0 + n * 8 + cq + (e & 1) >= cu.len) s[n][e] = -INFINITY;
+      }
       if (a.scores) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -418,18 +519,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(const DecodeArgs
             }
           }
       }
-      // running maximum and sum of the rows (the four lanes of a row agree on the maximum)
+      // the frame of a row (its four lanes agree) lies kHead below the maximum that set it, and is
+      // kept unless that grew by more than 8: the sums and O are rescaled rarely
       float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
       float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
 #pragma unroll
       for (int w = 1; w < 4; w <<= 1) {
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, w));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, w));
+        if (upper) x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, w));
       }
-      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-      const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
-      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
-        const float f0 = ex2_approx(m0 - u0), f1 = ex2_approx(m1 - u1);
+      x0 -= kHead;
+      x1 -= kHead;
+      const bool g0 = x0 > m0 + 8.0f || (m0 == -INFINITY && x0 > -INFINITY);
+      const bool g1 = x1 > m1 + 8.0f || (m1 == -INFINITY && x1 > -INFINITY);
+      if (__any_sync(0xffffffffu, g0 || g1)) {
+        const float f0 = g0 ? ex2_approx(m0 - x0) : 1.0f, f1 = g1 ? ex2_approx(m1 - x1) : 1.0f;
         l0 *= f0;
         l1 *= f1;
 #pragma unroll
@@ -437,15 +541,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(const DecodeArgs
           o[n][0] *= f0; o[n][1] *= f0;
           o[n][2] *= f1; o[n][3] *= f1;
         }
-        m0 = n0;
-        m1 = n1;
+        m0 = g0 ? x0 : m0;
+        m1 = g1 ? x1 : m1;
       }
+      const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         s[n][0] = ex2_approx(s[n][0] - u0);
         s[n][1] = ex2_approx(s[n][1] - u0);
-        s[n][2] = ex2_approx(s[n][2] - u1);
-        s[n][3] = ex2_approx(s[n][3] - u1);
+        s[n][2] = upper ? ex2_approx(s[n][2] - u1) : 0.f;
+        s[n][3] = upper ? ex2_approx(s[n][3] - u1) : 0.f;
       }
       l0 += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
       l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
@@ -454,19 +559,23 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(const DecodeArgs
       const uint32_t p[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]),
                              pack2<T>(s[1][0], s[1][1]), pack2<T>(s[1][2], s[1][3])};
       {
-        const int r = (lane & 7) + (((lane >> 3) & 1) << 3);  // keys 0-7 / 8-15
-        const uint32_t row = vb + r * C::kRowBytes;
+        const int r = (lane & 7) + (((lane >> 3) & 1) << 3), hi = lane >> 4;  // keys 0-7 / 8-15
+        const uint32_t row = vb + r * 128;
 #pragma unroll
         for (int n = 0; n < NT; n += 2) {
           uint32_t b[4];
-          const int c = n + (lane >> 4);
-          ldsm4t(row + ((c ^ (r & 7)) << 4), b);
+          ldsm4t(row + (n >> 3) * C::kChunkBytes + ((((n & 7) + hi) ^ (r & 7)) << 4), b);
           mma16816<T>(o[n], p, b[0], b[1]);
           mma16816<T>(o[n + 1], p, b[2], b[3]);
         }
       }
     }
-    stage = stage + 1 == S ? 0 : stage + 1;
+    if (stage + 1 == S) {
+      stage = 0;
+      parity ^= 1;
+    } else {
+      ++stage;
+    }
     const bool seg_end = cu.tile + 1 == cu.tiles || left == 1;
     if (seg_end) {
       // ---- merge the warps: sums of a row over its four lanes, then over the warps
@@ -503,28 +612,32 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(const DecodeArgs
       }
       // pairs (0, 2) and (1, 3), then (0, 1)
 #pragma unroll
-      for (int step = 2; step >= 1; step >>= 1) {
-        if (warp >= step && warp < 2 * step) {
-          float* dst = merge + (warp - step) * kRows * DP;
+      for (int c = 0; c < NT; c += 8)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            *reinterpret_cast<float2*>(dst + r0 * DP + n * 8 + cq) = make_float2(o[n][0], o[n][1]);
-            *reinterpret_cast<float2*>(dst + (r0 + 8) * DP + n * 8 + cq) = make_float2(o[n][2], o[n][3]);
-          }
-        }
-        __syncthreads();
-        if (warp < step) {
-          const float* src = merge + warp * kRows * DP;
+        for (int step = 2; step >= 1; step >>= 1) {
+          if (warp >= step && warp < 2 * step) {
+            float* dst = merge + (warp - step) * kRows * 64 + r0 * 64 + cq;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float2 x = *reinterpret_cast<const float2*>(src + r0 * DP + n * 8 + cq);
-            const float2 y = *reinterpret_cast<const float2*>(src + (r0 + 8) * DP + n * 8 + cq);
-            o[n][0] += x.x; o[n][1] += x.y;
-            o[n][2] += y.x; o[n][3] += y.y;
+            for (int n = 0; n < 8; ++n) {
+              *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[c + n][0], o[c + n][1]);
+              if (rows > 8) *reinterpret_cast<float2*>(dst + 8 * 64 + n * 8) = make_float2(o[c + n][2], o[c + n][3]);
+            }
           }
+          __syncthreads();
+          if (warp < step) {
+            const float* src = merge + warp * kRows * 64 + r0 * 64 + cq;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const float2 x = *reinterpret_cast<const float2*>(src + n * 8);
+              o[c + n][0] += x.x; o[c + n][1] += x.y;
+              if (rows > 8) {
+                const float2 y = *reinterpret_cast<const float2*>(src + 8 * 64 + n * 8);
+                o[c + n][2] += y.x; o[c + n][3] += y.y;
+              }
+            }
+          }
+          __syncthreads();
         }
-        __syncthreads();
-      }
       if (warp == 0) {
         // the whole (sequence, head) in this range: the result; a part of it: to the workspace
         const bool whole = tile0 == 0 && cu.tile + 1 == cu.tiles;
@@ -553,9 +666,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(const DecodeArgs
     }
     next_item(a, heads, cu);
   }
-  cp_async_wait<0>();
   // this CTA's error, collected by the join kernel (no word to clear before the call)
-  __shared__ int s_err[kWarps];
   const int we = __reduce_max_sync(0xffffffffu, err);
   if (lane == 0) s_err[warp] = we;
   __syncthreads();
@@ -737,11 +848,12 @@ bool decode_layout(int batch, int hq, int hkv, int64_t max_len, int d, bool mass
 }
 
 template <typename T, int DP>
-cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
+cudaError_t launch_decode_t(const DecodeArgs& a, const CUtensorMap* maps, cudaStream_t st) {
   static std::atomic<int> limits[64];
   cudaError_t e = raise_smem_limit(decode_kernel<T, DP>, DecodeCfg<DP>::kSmem, limits);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_kernel<T, DP>, dim3(kCtas), dim3(kWarps * 32), DecodeCfg<DP>::kSmem, st, a);
+  e = launch_pdl(decode_kernel<T, DP>, dim3(kCtas), dim3(kWarps * 32), DecodeCfg<DP>::kSmem, st, maps[0],
+                 maps[1], a);
   if (e != cudaSuccess) return e;
   e = launch_pdl(join_kernel<T, DP>, dim3(a.c.hkv * a.row_blocks, a.c.batch), dim3(kJoinThreads), 0, st, a);
   if (e != cudaSuccess || !a.scores || a.max_len == 0) return e;
@@ -796,7 +908,30 @@ int sage_paged_attn(const sage_packed* q, const sage_paged_cache* cache, const s
   a.group = heads_q / heads_kv;
   a.row_blocks = (a.group + kRows - 1) / kRows;
   a.max_len = max_seqlen;
-  a.vec = vec ? 1 : 0;
+  // TMA: whole 16-byte rows, pages of whole 8-row blocks, no zero stride of a dimension that is walked
+  const sage_paged_cache& pc = *cache;
+  const int64_t len[3] = {pc.num_pages, tensor_layout == SAGE_HND ? heads_kv : pc.page_size,
+                          tensor_layout == SAGE_HND ? pc.page_size : heads_kv};
+  bool tma = vec && pc.page_size % 8 == 0;
+  for (int i = 0; i < 3; ++i)
+    tma = tma && (len[i] == 1 || (pc.k_stride[i] > 0 && pc.v_stride[i] > 0 && pc.k_stride[i] < (1LL << 38) &&
+                                  pc.v_stride[i] < (1LL << 38))) && len[i] > 0;
+  a.load = tma ? kLoadTma : vec ? kLoadVec : kLoadAny;
+  a.box_rows = pc.page_size % 16 == 0 ? 16 : 8;
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (pc.page_size == 1 << i) a.page_shift = i;
+  CUtensorMap maps[2];
+  std::memset(maps, 0, sizeof(maps));
+  if (tma) {
+    auto map = [&](CUtensorMap* m, const void* base, int64_t sp, int64_t sh, int64_t st) {
+      // (a stride that is never walked is given a legal value)
+      return make_map4(m, dtype == SAGE_BF16, base, head_dim, pc.page_size, heads_kv, pc.num_pages, st * 2,
+                       (heads_kv > 1 ? sh : 128) * 2, (pc.num_pages > 1 ? sp : 128) * 2, 64, a.box_rows);
+    };
+    if (!map(&maps[0], pc.k, a.c.k_sp, a.c.k_sh, a.c.k_st) || !map(&maps[1], pc.v, a.c.v_sp, a.c.v_sh, a.c.v_st))
+      return note_cuda_failure(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
+  }
   char* w = static_cast<char*>(workspace);
   a.err = reinterpret_cast<int*>(w);
   a.cta_err = reinterpret_cast<int*>(w + L.err);
@@ -810,9 +945,9 @@ int sage_paged_attn(const sage_packed* q, const sage_paged_cache* cache, const s
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dtype == SAGE_F16)
-    e = head_dim <= 64 ? launch_decode_t<__half, 64>(a, st) : launch_decode_t<__half, 128>(a, st);
+    e = head_dim <= 64 ? launch_decode_t<__half, 64>(a, maps, st) : launch_decode_t<__half, 128>(a, maps, st);
   else
-    e = head_dim <= 64 ? launch_decode_t<__nv_bfloat16, 64>(a, st) : launch_decode_t<__nv_bfloat16, 128>(a, st);
+    e = head_dim <= 64 ? launch_decode_t<__nv_bfloat16, 64>(a, maps, st) : launch_decode_t<__nv_bfloat16, 128>(a, maps, st);
   return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "paged attention");
 }
 
