@@ -8,9 +8,9 @@
 // a decode step fills the same few, and the tensor work here is a small part of what the memory
 // time allows.
 //
-// Split: the (sequence, head, 64-key tile) items of the whole batch form one line, cut into equal
+// Split: the (sequence, head, key tile) items of the whole batch form one line, cut into equal
 // ranges, one per CTA, so the load is even whatever the lengths (which only the device knows). Each
-// warp takes 16 keys of a tile through its own ring of stages and keeps its own running maximum, sum
+// warp takes 16 or 32 keys of a tile through its own ring of stages and keeps its own running maximum, sum
 // and accumulator; no barrier runs inside a range. At a (sequence, head)'s last tile in a range the
 // warps are merged in a fixed order; a result that lies in one range is written out, others go to
 // the workspace and the join kernel sums them in the order of the ranges, so results do not depend
@@ -32,8 +32,6 @@ namespace sage {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kKeys = 16;                  // keys per warp and tile
-constexpr int kTile = kWarps * kKeys;      // keys per tile
 constexpr int kCtas = 304;                 // two resident CTAs per SM
 constexpr int kRows = 16;                  // query heads per row block
 constexpr int kMinTiles = 2;               // tiles a CTA takes at least
@@ -64,7 +62,9 @@ struct DecodeArgs {
 
 template <int DP>
 struct DecodeCfg {
-  static constexpr int kStages = DP == 128 ? 3 : 6;
+  static constexpr int kStages = 3;
+  static constexpr int kKeys = DP == 128 ? 16 : 32;           // keys per warp and tile (8 KB of K and V)
+  static constexpr int kTile = kWarps * kKeys;                // keys per tile
   static constexpr int kChunks = DP / 64;                     // blocks of 64 channels, rows of 128 bytes
   static constexpr int kChunkBytes = kKeys * 128;
   static constexpr int kTileBytes = kChunks * kChunkBytes;    // K or V of one warp's tile
@@ -77,13 +77,17 @@ struct DecodeCfg {
 };
 
 // Tiles of a sequence of n tokens.
-__device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
+template <int DP>
+__device__ __forceinline__ int tiles_of(int n) {
+  return (n + DecodeCfg<DP>::kTile - 1) / DecodeCfg<DP>::kTile;
+}
 
 // The items (sequence, head, tile) of sequences [b0, b0 + blockDim): this thread's count, the sum before it and the
 // sum of all. Lengths that are out of range count as 0 and set `bad`.
 struct Scan {
   long long n, before, all;
 };
+template <int DP>
 __device__ __forceinline__ Scan scan_items(const DecodeArgs& a, int heads, int b0, bool& bad) {
   __shared__ long long s_sum[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -92,7 +96,7 @@ __device__ __forceinline__ Scan scan_items(const DecodeArgs& a, int heads, int b
   if (b < a.c.batch) {
     const int len = checked_len(a.c, b, a.max_len);
     if (len < 0) bad = true;
-    r.n = (long long)tiles_of(max(len, 0)) * heads;
+    r.n = (long long)tiles_of<DP>(max(len, 0)) * heads;
   }
   long long inc = r.n;
 #pragma unroll
@@ -124,6 +128,7 @@ __device__ __forceinline__ long long first_item(long long total, int ctas, int i
 struct Cursor {
   int b, h, tile, tiles, len;  // h: head * row_blocks + row block
 };
+template <int DP>
 __device__ __forceinline__ void next_item(const DecodeArgs& a, int heads, Cursor& u) {
   if (++u.tile < u.tiles) return;
   u.tile = 0;
@@ -133,7 +138,7 @@ __device__ __forceinline__ void next_item(const DecodeArgs& a, int heads, Cursor
     ++u.b;
     u.len = u.b < a.c.batch ? max(checked_len(a.c, u.b, a.max_len), 0) : 0;
   } while (u.b < a.c.batch && u.len == 0);
-  u.tiles = tiles_of(u.len);
+  u.tiles = tiles_of<DP>(u.len);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -194,10 +199,10 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, ui
       : "memory");
 }
 
-// The 16 keys of an item that belong to this warp into one stage: K, then V, per 64 channels rows of 128
+// The keys of an item that belong to this warp into one stage: K, then V, per 64 channels rows of 128
 // bytes whose 16-byte unit c lies at c ^ (row & 7). Tokens that are not there and channels past d
 // become zero. `page`, `slot`: TMA: of this lane's box (K or V by bit 0, channels by bit 1 at head_dim 128, rows by the
-// rest); otherwise of row (lane & 15).
+// rest); otherwise of row (lane mod the keys).
 template <typename T, int DP>
 __device__ __forceinline__ void load_stage(const DecodeArgs& a, const CUtensorMap* tmK, const CUtensorMap* tmV, int h,
                                            int page, int slot, uint8_t* stage, uint32_t bar) {
@@ -208,7 +213,7 @@ __device__ __forceinline__ void load_stage(const DecodeArgs& a, const CUtensorMa
     if (lane == 0)
       asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(C::kStageBytes) : "memory");
     const int kv = lane & 1, chunk = C::kChunks == 2 ? (lane >> 1) & 1 : 0, rows = (lane >> C::kChunks) * a.box_rows;
-    if (rows < kKeys)
+    if (rows < C::kKeys)
       tma_box(base + kv * C::kTileBytes + chunk * C::kChunkBytes + rows * 128, kv ? tmV : tmK, bar, chunk * 64, slot, h,
               page >= 0 ? page : a.c.num_pages);
     return;
@@ -218,7 +223,7 @@ __device__ __forceinline__ void load_stage(const DecodeArgs& a, const CUtensorMa
   constexpr int kUnits = DP / 8, kRowsPer = 32 / kUnits;  // rows that one pass of the warp covers
   const int c = lane % kUnits;
 #pragma unroll 2
-  for (int i = 0; i < kKeys / kRowsPer; ++i) {
+  for (int i = 0; i < C::kKeys / kRowsPer; ++i) {
     const int r = i * kRowsPer + lane / kUnits;
     const int pg = __shfl_sync(0xffffffffu, page, r), sl = __shfl_sync(0xffffffffu, slot, r);
     const bool in = pg >= 0 && c * 8 < a.c.d;
@@ -292,7 +297,7 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const DecodeArgs a) {
   using C = DecodeCfg<DP>;
-  constexpr int S = C::kStages, KS = DP / 16, NT = DP / 8;
+  constexpr int S = C::kStages, KS = DP / 16, NT = DP / 8, NK = C::kKeys / 8;
   // fp16 weights are held at up to 2^(7 + 8): 7 bits more before the smallest lose bits
   constexpr float kHead = std::is_same<T, __half>::value ? 7.0f : 0.f;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -315,9 +320,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   __shared__ int s_b;
   bool bad = false;
   if (threadIdx.x == 0) { s_b = a.c.batch; s_base = 0; }
-  Scan sc = scan_items(a, heads, 0, bad);
+  Scan sc = scan_items<DP>(a, heads, 0, bad);
   long long total = sc.all;
-  for (int b0 = blockDim.x; b0 < a.c.batch; b0 += blockDim.x) total += scan_items(a, heads, b0, bad).all;
+  for (int b0 = blockDim.x; b0 < a.c.batch; b0 += blockDim.x) total += scan_items<DP>(a, heads, b0, bad).all;
   const int ctas = total > 0 ? ctas_of(total) : 0, me = blockIdx.x;
   long long left = 0, i0 = 0;
   if (me < ctas) {
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       base += sc.all;
       b0 += blockDim.x;
       if (base > i0 || b0 >= a.c.batch) break;
-      sc = scan_items(a, heads, b0, bad);
+      sc = scan_items<DP>(a, heads, b0, bad);
     }
   }
   __syncthreads();
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   if (left > 0) {
     cu.b = s_b;
     cu.len = checked_len(a.c, cu.b, a.max_len);
-    cu.tiles = tiles_of(cu.len);
+    cu.tiles = tiles_of<DP>(cu.len);
     const long long in = i0 - s_base;
     cu.h = (int)(in / cu.tiles);
     cu.tile = (int)(in - (long long)cu.h * cu.tiles);
@@ -350,16 +355,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   Cursor ld = cu;
   long long to_load = left;
   int page, slot;
-  const int my_row = a.load == kLoadTma ? (lane >> C::kChunks) * a.box_rows : lane & 15;
+  const int my_row = a.load == kLoadTma ? (lane >> C::kChunks) * a.box_rows : lane & (C::kKeys - 1);
   auto next_page = [&]() {
-    const int key = ld.tile * kTile + warp * kKeys + my_row;
-    find_page(a, ld.b, key, to_load > 0 && my_row < kKeys && key < ld.len, page, slot, err);
+    const int key = ld.tile * C::kTile + warp * C::kKeys + my_row;
+    find_page(a, ld.b, key, to_load > 0 && my_row < C::kKeys && key < ld.len, page, slot, err);
   };
   bool dead = false;  // a wait has run out: nothing more is loaded
   auto load_next = [&](int st) {
     if (to_load > 0 && !dead) {
       load_stage<T, DP>(a, &tmK, &tmV, ld.h / a.row_blocks, page, slot, ring + st * C::kStageBytes, bars + st * 8);
-      next_item(a, heads, ld);
+      next_item<DP>(a, heads, ld);
       --to_load;
       next_page();
     }
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     // the stage after the ones in flight goes where the previous item was
     __syncwarp();
     load_next(stage == 0 ? S - 1 : stage - 1);
-    const int key0 = cu.tile * kTile + warp * kKeys;
+    const int key0 = cu.tile * C::kTile + warp * C::kKeys;
     uint8_t* const here = ring + stage * C::kStageBytes;
     if (a.load == kLoadTma) {
       if (!dead && !__all_sync(0xffffffffu, wait_stage(bars + stage * 8, parity))) {
@@ -431,9 +436,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           wait_stage(bars + (st % S) * 8, parity ^ (st >= S ? 1u : 0u));
         }
       }
-      if (!dead && key0 < cu.len && key0 + kKeys > cu.len) {
+      if (!dead && key0 < cu.len && key0 + C::kKeys > cu.len) {
         // slots behind the last token may hold anything: as V rows they become zero (their scores are masked)
-        for (int i = lane; i < (key0 + kKeys - cu.len) * C::kChunks * 8; i += 32) {
+        for (int i = lane; i < (key0 + C::kKeys - cu.len) * C::kChunks * 8; i += 32) {
           const int r = cu.len - key0 + i / (C::kChunks * 8), u = i % (C::kChunks * 8);
           *reinterpret_cast<uint4*>(here + C::kTileBytes + (u >> 3) * C::kChunkBytes + r * 128 + (u & 7) * 16) =
               make_uint4(0, 0, 0, 0);
@@ -447,82 +452,97 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     if (key0 < cu.len) {
       const bool upper = rows > 8;  // rows r0 + 8 are in use
       const uint32_t kb = smem_u32(here), vb = kb + C::kTileBytes;
-      // S = Q K^T: lanes 0-7 / 8-15 address keys 0-7 at channels +0 / +8, 16-23 / 24-31 keys 8-15;
-      // two accumulators per half, so that no chain is longer than half the channels
-      float s[2][4], s2[2][4];
+      // S = Q K^T, 16 keys at a time: lanes 0-7 / 8-15 address keys 0-7 at channels +0 / +8, 16-23 / 24-31 keys
+      // 8-15; two accumulators per 8 keys, so that no chain is longer than half the channels
+      float s[NK][4], s2[NK][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NK; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
       {
         const int r = (lane & 7) + ((lane >> 4) << 3), odd = (lane >> 3) & 1;
         const uint32_t row = kb + r * 128;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t b[4];
-          ldsm4(row + (k >> 2) * C::kChunkBytes + (((((2 * k) & 7) + odd) ^ (r & 7)) << 4), b);
-          mma16816<T>(k & 1 ? s2[0] : s[0], qf[k], b[0], b[1]);
-          mma16816<T>(k & 1 ? s2[1] : s[1], qf[k], b[2], b[3]);
-        }
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int n = 0; n < NK; n += 2) {
+            uint32_t b[4];
+            ldsm4(row + n * 1024 + (k >> 2) * C::kChunkBytes + (((((2 * k) & 7) + odd) ^ (r & 7)) << 4), b);
+            mma16816<T>(k & 1 ? s2[n] : s[n], qf[k], b[0], b[1]);
+            mma16816<T>(k & 1 ? s2[n + 1] : s[n + 1], qf[k], b[2], b[3]);
+          }
       }
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NK; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
       // scores in base 2; lane holds keys 8 n + cq, + 1 of rows r0 (s[n][0..1]) and r0 + 8
       if (a.cap > 0.f) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NK; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (e < 2 || upper) s[n][e] = tanhf(s[n][e] * cap_in) * cap_out;
       } else {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NK; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][e] *= scale2;
       }
-      if (a.slopes) {
+      if (a.slopes && !a.c.pos) {
+        const float d0 = (float)(qpos - (key0 + cq));  // exact below 2^24
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NK; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int key = key0 + n * 8 + cq + e;
-            int kp = key;
-            if (a.c.pos && key < cu.len) {
-              int pg, sl, none = 0;
-              find_page(a, cu.b, key, true, pg, sl, none);
-              if (pg >= 0) kp = __ldg(&a.c.pos[plane_at(a.c, pg, cu.h / a.row_blocks, sl)]);
-            }
-            const float dist = fabsf((float)((long long)qpos - kp));
+            const float dist = fabsf(d0 - (float)(n * 8 + e));
             s[n][e] = fmaf(-sl0, dist, s[n][e]);
             s[n][2 + e] = fmaf(-sl1, dist, s[n][2 + e]);
           }
-      }
-      if (key0 + kKeys > cu.len) {
+      } else if (a.slopes) {
+#pragma unroll 1
+        for (int n = 0; n < NK; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+          for (int e = 0; e < 2; ++e) {
+            const int key = key0 + n * 8 + cq + e;
+            int pg, sl, none = 0;
+            find_page(a, cu.b, key, key < cu.len, pg, sl, none);
+            const int kp = pg >= 0 ? __ldg(&a.c.pos[plane_at(a.c, pg, cu.h / a.row_blocks, sl)]) : 0;
+            const float dist = fabsf((float)((long long)qpos - kp));
+#pragma unroll
+            for (int u = 0; u < NK; ++u)
+              if (u == n) {
+                s[u][e] = fmaf(-sl0, dist, s[u][e]);
+                s[u][2 + e] = fmaf(-sl1, dist, s[u][2 + e]);
+              }
+          }
+      }
+      if (key0 + C::kKeys > cu.len) {
+#pragma unroll
+        for (int n = 0; n < NK; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (key0 + n * 8 + cq + (e & 1) >= cu.len) s[n][e] = -INFINITY;
       }
       if (a.scores) {
+        // (the pitch is a multiple of the tile, so pairs are aligned and whole tiles fit)
+        float* dst = a.scores + ((int64_t)cu.b * a.hq + row0 + r0) * a.score_pitch + key0 + cq;
+        if (r0 < rows)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < NK; ++n) *reinterpret_cast<float2*>(dst + n * 8) = make_float2(s[n][0], s[n][1]);
+        if (r0 + 8 < rows)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int key = key0 + n * 8 + cq + e;
-            if (key < cu.len) {
-              float* dst = a.scores + ((int64_t)cu.b * a.hq + row0 + r0) * a.score_pitch + key;
-              if (r0 < rows) dst[0] = s[n][e];
-              if (r0 + 8 < rows) dst[8 * a.score_pitch] = s[n][2 + e];
-            }
-          }
+          for (int n = 0; n < NK; ++n)
+            *reinterpret_cast<float2*>(dst + 8 * a.score_pitch + n * 8) = make_float2(s[n][2], s[n][3]);
       }
       // the frame of a row (its four lanes agree) lies kHead below the maximum that set it, and is
       // kept unless that grew by more than 8: the sums and O are rescaled rarely
-      float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-      float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+      float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < NK; ++n) {
+        x0 = max3(x0, s[n][0], s[n][1]);
+        x1 = max3(x1, s[n][2], s[n][3]);
+      }
 #pragma unroll
       for (int w = 1; w < 4; w <<= 1) {
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, w));
@@ -546,21 +566,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       }
       const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+      for (int n = 0; n < NK; ++n) {
         s[n][0] = ex2_approx(s[n][0] - u0);
         s[n][1] = ex2_approx(s[n][1] - u0);
         s[n][2] = upper ? ex2_approx(s[n][2] - u1) : 0.f;
         s[n][3] = upper ? ex2_approx(s[n][3] - u1) : 0.f;
+        l0 += s[n][0] + s[n][1];
+        l1 += s[n][2] + s[n][3];
       }
-      l0 += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
-      l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
       // P in the operands' 16-bit type (the one rounding of the weights; their sum stays in
-      // 32 bits), which is already the A operand's layout; O += P V
-      const uint32_t p[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]),
-                             pack2<T>(s[1][0], s[1][1]), pack2<T>(s[1][2], s[1][3])};
-      {
+      // 32 bits), which is already the A operand's layout; O += P V, 16 keys at a time
+#pragma unroll
+      for (int g = 0; g < NK; g += 2) {
+        const uint32_t p[4] = {pack2<T>(s[g][0], s[g][1]), pack2<T>(s[g][2], s[g][3]),
+                               pack2<T>(s[g + 1][0], s[g + 1][1]), pack2<T>(s[g + 1][2], s[g + 1][3])};
         const int r = (lane & 7) + (((lane >> 3) & 1) << 3), hi = lane >> 4;  // keys 0-7 / 8-15
-        const uint32_t row = vb + r * 128;
+        const uint32_t row = vb + g * 1024 + r * 128;
 #pragma unroll
         for (int n = 0; n < NT; n += 2) {
           uint32_t b[4];
@@ -664,7 +685,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       ++pieces;
       fresh = true;
     }
-    next_item(a, heads, cu);
+    next_item<DP>(a, heads, cu);
   }
   // this CTA's error, collected by the join kernel (no word to clear before the call)
   const int we = __reduce_max_sync(0xffffffffu, err);
@@ -707,7 +728,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
   // items before this sequence, and in all
   long long before = 0, all = 0;
   for (int i = tid; i < a.c.batch; i += kJoinThreads) {
-    const long long n = (long long)tiles_of(max(checked_len(a.c, i, a.max_len), 0)) * heads;
+    const long long n = (long long)tiles_of<DP>(max(checked_len(a.c, i, a.max_len), 0)) * heads;
     all += n;
     if (i < b) before += n;
   }
@@ -732,7 +753,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
     if (a.lse && tid < rows) a.lse[(int64_t)b * a.hq + row0 + tid] = -INFINITY;
     return;
   }
-  const long long t0 = before + (long long)hb * tiles_of(len), t1 = t0 + tiles_of(len);
+  const long long t0 = before + (long long)hb * tiles_of<DP>(len), t1 = t0 + tiles_of<DP>(len);
   const int ctas = ctas_of(all);
   // the ranges that hold t0 and t1 - 1: range i is [all i / ctas, all (i + 1) / ctas)
   auto range_of = [&](long long t) { return (int)(((t + 1) * ctas - 1) / all); };
@@ -840,7 +861,7 @@ bool decode_layout(int batch, int hq, int hkv, int64_t max_len, int d, bool mass
   L->err = 256;
   L->part_o = take((size_t)kCtas * 2 * kRows * dp * 4);
   L->part_ml = take((size_t)kCtas * 2 * kRows * 2 * 4);
-  L->pitch = (max_len + 3) / 4 * 4;
+  L->pitch = (max_len + 127) / 128 * 128;  // whole tiles of either head_dim
   L->lse2 = take(mass ? (size_t)batch * hq * 4 : 0);
   L->scores = take(mass ? (size_t)batch * hq * L->pitch * 4 : 0);
   L->total = o;
@@ -917,7 +938,8 @@ int sage_paged_attn(const sage_packed* q, const sage_paged_cache* cache, const s
     tma = tma && (len[i] == 1 || (pc.k_stride[i] > 0 && pc.v_stride[i] > 0 && pc.k_stride[i] < (1LL << 38) &&
                                   pc.v_stride[i] < (1LL << 38))) && len[i] > 0;
   a.load = tma ? kLoadTma : vec ? kLoadVec : kLoadAny;
-  a.box_rows = pc.page_size % 16 == 0 ? 16 : 8;
+  const int keys = head_dim <= 64 ? DecodeCfg<64>::kKeys : DecodeCfg<128>::kKeys;
+  a.box_rows = pc.page_size % keys == 0 ? keys : pc.page_size % 16 == 0 ? 16 : 8;
   a.page_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (pc.page_size == 1 << i) a.page_shift = i;

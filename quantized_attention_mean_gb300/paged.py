@@ -14,75 +14,109 @@ captured into a CUDA graph; ``read_device_status(workspace)`` tells of bad ones.
 """
 
 import contextlib
-import ctypes
+from ctypes import byref
 
 import torch
 
-from . import DTYPE, LAYOUT, _check, _check_workspace, _lib, _packed, _stream_ptr, alloc_workspace
-from ._lib import SagePagedCache
+from . import DTYPE, LAYOUT, SageError, _check_workspace, _lib, alloc_workspace
+from ._lib import SagePacked, SagePagedCache
 
 __all__ = ["paged_attn", "paged_append", "paged_evict", "paged_attn_workspace_bytes",
            "paged_evict_workspace_bytes"]
 
 STATUS_BYTES = 256
+INT32_MAX = 2 ** 31 - 1
+_NAN = float("nan")  # sm_scale: the default
 
 
-def _on(stream):
-    """Allocations made for a call on another stream belong to that stream."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+class _Launch:
+    """The device and stream a call runs on; what it allocates belongs to that stream. (A decode step is a few
+    microseconds of GPU time, so the ordinary case, the current device and stream, enters no context.)"""
+
+    __slots__ = ("contexts", "stream")
+
+    def __init__(self, index, stream):
+        self.contexts = None
+        if stream is not None or torch._C._cuda_getDevice() != index:
+            self.contexts = contextlib.ExitStack()
+            self.contexts.enter_context(torch.cuda.device(index))
+            if stream is not None:
+                self.contexts.enter_context(torch.cuda.stream(stream))
+        self.stream = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+    def __enter__(self):
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.contexts is not None:
+            self.contexts.close()
 
 
 def _ptr(t):
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _check_small(name, t, shape, dtype, device):
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device
-                          or not t.is_contiguous()):
+def _check_small(name, t, shape, dtype, index):
+    if t is not None and (t.dtype != dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} {list(shape)} tensor on the inputs' device")
 
 
-def _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions):
-    """Shapes, types and devices of a cache; returns (num_pages, heads_kv, page_size, head_dim)."""
+def _check_range(name, value):
+    """Sizes go to the library as 32-bit integers, which would wrap silently."""
+    if not 0 <= value <= INT32_MAX:
+        raise ValueError(f"{name} must be in [0, 2^31)")
+    return int(value)
+
+
+def _packed(t):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and t.shape[2] != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return SagePacked(t.data_ptr(), s0, s1)
+
+
+def _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions, workspace):
+    """Shapes, types and devices of a cache; returns its description and (heads_kv, head_dim, device index)."""
     if tensor_layout not in LAYOUT:
         raise ValueError("tensor_layout must be 'HND' or 'NHD'")
-    if k_cache.dim() != 4 or tuple(v_cache.shape) != tuple(k_cache.shape):
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be 4-D and of one shape")
     if k_cache.dtype not in DTYPE or v_cache.dtype != k_cache.dtype:
         raise TypeError("k_cache and v_cache must share one dtype, float16 or bfloat16")
     if page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise TypeError("page_table and seq_lens must be int32")
-    if page_table.dim() != 2 or (page_table.numel() and page_table.stride(1) != 1):
+    if page_table.dim() != 2 or (page_table.stride(1) != 1 and page_table.shape[1] > 1):
         raise ValueError("page_table must be [batch, max_pages] with contiguous rows")
-    if seq_lens.dim() != 1 or seq_lens.shape[0] != page_table.shape[0] or not seq_lens.is_contiguous():
+    batch, width = page_table.shape
+    if seq_lens.dim() != 1 or seq_lens.shape[0] != batch or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be a contiguous [batch] tensor")
     if tensor_layout == "HND":
-        pages, heads, size, d = k_cache.shape
+        pages, heads, size, d = shape
     else:
-        pages, size, heads, d = k_cache.shape
-    dev = k_cache.device
-    _check_small("mass", mass, (pages, heads, size), torch.float32, dev)
-    _check_small("key_positions", key_positions, (pages, heads, size), torch.int32, dev)
-    if not all(t.device == dev for t in (v_cache, page_table, seq_lens)):
+        pages, size, heads, d = shape
+    index = k_cache.get_device()
+    if mass is not None:
+        _check_small("mass", mass, (pages, heads, size), torch.float32, index)
+    if key_positions is not None:
+        _check_small("key_positions", key_positions, (pages, heads, size), torch.int32, index)
+    if v_cache.get_device() != index or page_table.get_device() != index or seq_lens.get_device() != index:
         raise ValueError("the cache, its page table and seq_lens must be on one device")
-    return pages, heads, size, d
+    k0, k1, k2, k3 = k_cache.stride()
+    v0, v1, v2, v3 = v_cache.stride()
+    if d != 1 and (k3 != 1 or v3 != 1):
+        raise ValueError("the last dimension must be contiguous")
+    if workspace is not None:
+        _check_workspace(workspace, k_cache.device)
+    cache = SagePagedCache(k_cache.data_ptr(), k0, k1, k2, v_cache.data_ptr(), v0, v1, v2, pages, size,
+                           page_table.data_ptr(), page_table.stride(0), width, seq_lens.data_ptr(), _ptr(mass),
+                           _ptr(key_positions))
+    return cache, heads, d, index
 
 
-def _check_cuda(dev, workspace):
-    if dev.type != "cuda":
+def _check_cuda(index):
+    if index < 0:
         raise ValueError("the cache must be on a CUDA device")
-    _check_workspace(workspace, dev)
-
-
-def _cache(k_cache, v_cache, page_table, seq_lens, size, mass, key_positions):
-    for t in (k_cache, v_cache):
-        if t.stride(3) != 1:
-            raise ValueError("the last dimension must be contiguous")
-    return SagePagedCache(k_cache.data_ptr(), (ctypes.c_int64 * 3)(*k_cache.stride()[:3]), v_cache.data_ptr(),
-                          (ctypes.c_int64 * 3)(*v_cache.stride()[:3]), k_cache.shape[0], size,
-                          page_table.data_ptr(), page_table.stride(0), page_table.shape[1], seq_lens.data_ptr(),
-                          0 if mass is None else mass.data_ptr(),
-                          0 if key_positions is None else key_positions.data_ptr())
 
 
 def paged_attn_workspace_bytes(batch, heads_q, heads_kv, max_seq_len, head_dim, accumulate=False):
@@ -106,38 +140,42 @@ def paged_attn(q, k_cache, v_cache, page_table, seq_lens, max_seq_len, tensor_la
     the key's position is its slot unless ``key_positions`` gives it (a cache that was evicted from), the
     query's is seq_len - 1 unless ``q_positions`` int32 [B] does. ``mass``: the weight each held token
     draws, summed over the query heads of its key/value head, is added to it in place."""
-    pages, hkv, size, d = _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions)
-    if q.dim() != 3 or q.shape[0] != page_table.shape[0] or q.shape[2] != d:
+    cache, hkv, d, index = _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions,
+                                        workspace)
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != page_table.shape[0] or shape[2] != d:
         raise ValueError("q must be [batch, heads, head_dim] with the cache's batch and head_dim")
     if q.dtype != k_cache.dtype:
         raise TypeError("q must have the cache's dtype")
-    if q.device != k_cache.device:
+    if q.get_device() != index:
         raise ValueError("q must be on the cache's device")
-    B, hq, _ = q.shape
-    dev = q.device
-    if out is not None and (tuple(out.shape) != tuple(q.shape) or out.dtype != q.dtype or out.device != dev):
+    B, hq, _ = shape
+    if out is not None and (out.shape != shape or out.dtype != q.dtype or out.get_device() != index):
         raise ValueError("out must have q's shape, dtype and device")
-    _check_small("slopes", slopes, (hq,), torch.float32, dev)
-    _check_small("q_positions", q_positions, (B,), torch.int32, dev)
-    if return_lse:
-        _check_small("lse", lse, (B, hq), torch.float32, dev)
-    _check_cuda(dev, workspace)
+    if slopes is not None:
+        _check_small("slopes", slopes, (hq,), torch.float32, index)
+    if q_positions is not None:
+        _check_small("q_positions", q_positions, (B,), torch.int32, index)
+    if not return_lse:
+        lse = None
+    elif lse is not None:
+        _check_small("lse", lse, (B, hq), torch.float32, index)
+    _check_cuda(index)
+    n = _check_range("max_seq_len", max_seq_len)
     lib = _lib.load()
-    with torch.cuda.device(dev), _on(stream):
+    with _Launch(index, stream) as on:
         if out is None:
-            out = torch.empty((B, hq, d), dtype=q.dtype, device=dev)
+            out = torch.empty(shape, dtype=q.dtype, device=q.device)
         if return_lse and lse is None:
-            lse = torch.empty((B, hq), dtype=torch.float32, device=dev)
+            lse = torch.empty((B, hq), dtype=torch.float32, device=q.device)
         if workspace is None:
-            workspace = alloc_workspace(lib.sage_paged_attn_workspace_size(
-                B, hq, hkv, int(max_seq_len), d, int(mass is not None)), dev)
-        cache = _cache(k_cache, v_cache, page_table, seq_lens, size, mass, key_positions)
-        st = lib.sage_paged_attn(ctypes.byref(_packed(q)), ctypes.byref(cache), ctypes.byref(_packed(out)),
-                                 _ptr(lse if return_lse else None), _ptr(slopes), _ptr(q_positions), B, hq, hkv,
-                                 int(max_seq_len), d, DTYPE[q.dtype], LAYOUT[tensor_layout],
-                                 float("nan") if sm_scale is None else float(sm_scale), float(softcap),
-                                 _ptr(workspace), workspace.numel(), _stream_ptr(stream))
-    _check(st, "paged_attn")
+            workspace = alloc_workspace(lib.sage_paged_attn_workspace_size(B, hq, hkv, n, d, mass is not None), q.device)
+        st = lib.sage_paged_attn(byref(_packed(q)), byref(cache), byref(_packed(out)), _ptr(lse), _ptr(slopes),
+                                 _ptr(q_positions), B, hq, hkv, n, d, DTYPE[q.dtype], LAYOUT[tensor_layout],
+                                 _NAN if sm_scale is None else sm_scale, softcap, workspace.data_ptr(),
+                                 workspace.numel(), on)
+    if st:
+        raise SageError(st, "paged_attn")
     return (out, lse) if return_lse else out
 
 
@@ -148,29 +186,33 @@ def paged_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, 
     one. Tokens behind the last sequence are left out. ``mass`` becomes 0 in the new slots,
     ``key_positions`` the token's entry of ``positions`` int32 [T], or its slot. A token whose slot or page
     is not in the cache is left out, and recorded in ``workspace`` (256 bytes) where one is given."""
-    pages, hkv, size, d = _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions)
-    if k.dim() != 3 or tuple(v.shape) != tuple(k.shape) or tuple(k.shape[1:]) != (hkv, d):
+    cache, hkv, d, index = _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions,
+                                        workspace)
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape or shape[1] != hkv or shape[2] != d:
         raise ValueError("k and v must be [tokens, heads, head_dim] with the cache's heads and head_dim")
     if k.dtype != k_cache.dtype or v.dtype != k.dtype:
         raise TypeError("k and v must have the cache's dtype")
-    if k.device != k_cache.device or v.device != k.device:
+    if k.get_device() != index or v.get_device() != index:
         raise ValueError("k and v must be on the cache's device")
-    B, T, dev = page_table.shape[0], k.shape[0], k.device
-    if cu_seqlens is None and T != B:
-        raise ValueError("without cu_seqlens every sequence gets one token")
-    _check_small("cu_seqlens", cu_seqlens, (B + 1,), torch.int32, dev)
-    _check_small("positions", positions, (T,), torch.int32, dev)
-    if positions is not None and key_positions is None:
-        raise ValueError("positions need the key_positions plane")
-    _check_cuda(dev, workspace)
-    lib = _lib.load()
-    with torch.cuda.device(dev):
-        cache = _cache(k_cache, v_cache, page_table, seq_lens, size, mass, key_positions)
-        st = lib.sage_paged_append(ctypes.byref(_packed(k)), ctypes.byref(_packed(v)), ctypes.byref(cache),
-                                   _ptr(cu_seqlens), _ptr(positions), B, T, hkv, d, DTYPE[k.dtype],
-                                   LAYOUT[tensor_layout], _ptr(workspace),
-                                   0 if workspace is None else workspace.numel(), _stream_ptr(stream))
-    _check(st, "paged_append")
+    B, T = page_table.shape[0], shape[0]
+    if cu_seqlens is None:
+        if T != B:
+            raise ValueError("without cu_seqlens every sequence gets one token")
+    else:
+        _check_small("cu_seqlens", cu_seqlens, (B + 1,), torch.int32, index)
+    if positions is not None:
+        _check_small("positions", positions, (T,), torch.int32, index)
+        if key_positions is None:
+            raise ValueError("positions need the key_positions plane")
+    _check_cuda(index)
+    _check_range("the number of tokens", T)
+    with _Launch(index, stream) as on:
+        st = _lib.load().sage_paged_append(byref(_packed(k)), byref(_packed(v)), byref(cache), _ptr(cu_seqlens),
+                                           _ptr(positions), B, T, hkv, d, DTYPE[k.dtype], LAYOUT[tensor_layout],
+                                           _ptr(workspace), 0 if workspace is None else workspace.numel(), on)
+    if st:
+        raise SageError(st, "paged_append")
 
 
 def paged_evict(k_cache, v_cache, mass, key_positions, page_table, seq_lens, budget, max_seq_len, sink=0, recent=0,
@@ -180,21 +222,22 @@ def paged_evict(k_cache, v_cache, mass, key_positions, page_table, seq_lens, bud
     ``recent`` positions stay, then those with the largest ``mass`` (ties: the lowest slot). Kept tokens
     behind the budget move into the freed slots, with their mass and position; the slots behind the
     budget keep what they held, and their pages are free."""
-    pages, hkv, size, d = _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions)
     if mass is None or key_positions is None:
         raise ValueError("eviction needs the mass and key_positions planes")
+    cache, hkv, d, index = _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions,
+                                        workspace)
     if budget < 1 or sink < 0 or recent < 0 or sink + recent > budget:
         raise ValueError("budget must be at least 1 and hold sink + recent tokens")
-    B, dev = page_table.shape[0], k_cache.device
-    _check_cuda(dev, workspace)
+    B = page_table.shape[0]
+    _check_cuda(index)
+    n, budget = _check_range("max_seq_len", max_seq_len), _check_range("budget", budget)
     lib = _lib.load()
-    with torch.cuda.device(dev), _on(stream):
-        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    with _Launch(index, stream) as on:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
         if workspace is None:
-            workspace = alloc_workspace(lib.sage_paged_evict_workspace_size(B, hkv, int(max_seq_len), int(budget)), dev)
-        cache = _cache(k_cache, v_cache, page_table, seq_lens, size, mass, key_positions)
-        st = lib.sage_paged_evict(ctypes.byref(cache), _ptr(new_lens), B, hkv, int(max_seq_len), d,
-                                  DTYPE[k_cache.dtype], LAYOUT[tensor_layout], int(budget), int(sink), int(recent),
-                                  _ptr(workspace), workspace.numel(), _stream_ptr(stream))
-    _check(st, "paged_evict")
+            workspace = alloc_workspace(lib.sage_paged_evict_workspace_size(B, hkv, n, budget), k_cache.device)
+        st = lib.sage_paged_evict(byref(cache), new_lens.data_ptr(), B, hkv, n, d, DTYPE[k_cache.dtype],
+                                  LAYOUT[tensor_layout], budget, sink, recent, workspace.data_ptr(), workspace.numel(), on)
+    if st:
+        raise SageError(st, "paged_evict")
     return new_lens

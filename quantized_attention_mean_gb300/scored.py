@@ -1,12 +1,12 @@
 """Attention with modified scores: capped by a tanh, biased by distance, under document and prefix
 masks, on 16-bit operands. For the layers whose scores the quantised calls cannot take."""
 
-import ctypes
+from ctypes import byref
 
 import torch
 
-from . import DTYPE, LAYOUT, _check, _check_dense_args, _dims, _lib, _stream_ptr, _tensor, alloc_workspace
-from .paged import _check_small, _on, _ptr
+from . import DTYPE, LAYOUT, SageError, _check_dense_args, _dims, _lib, _tensor, alloc_workspace
+from .paged import _NAN, _check_small, _Launch, _ptr
 
 __all__ = ["scored_attn", "scored_attn_workspace_bytes"]
 
@@ -38,34 +38,40 @@ def scored_attn(q, k, v, tensor_layout="HND", is_causal=False, sm_scale=None, so
     Returns out, plus lse [B, Hq, Nq] fp32 if return_lse."""
     _check_dense_args(q, k, v, tensor_layout, out, lse, return_lse, workspace)
     B, hq, hkv, nq, nk, d = _dims(q, k, tensor_layout)
-    dev = q.device
+    index = q.get_device()
     if doc_ids is None and doc_ids_k is not None:
         raise ValueError("doc_ids_k needs doc_ids")
-    if doc_ids is not None and doc_ids_k is None:
-        if nq != nk:
-            raise ValueError("with Nq != Nk the keys' documents need doc_ids_k")
-        doc_ids_k = doc_ids
-    if prefix_lens is not None and not is_causal:
-        raise ValueError("prefix_lens needs is_causal")
-    _check_small("slopes", slopes, (hq,), torch.float32, dev)
-    _check_small("prefix_lens", prefix_lens, (B,), torch.int32, dev)
-    _check_small("doc_ids", doc_ids, (B, nq), torch.int32, dev)
-    _check_small("doc_ids_k", doc_ids_k, (B, nk), torch.int32, dev)
+    if doc_ids is not None:
+        if doc_ids_k is None:
+            if nq != nk:
+                raise ValueError("with Nq != Nk the keys' documents need doc_ids_k")
+            doc_ids_k = doc_ids
+        _check_small("doc_ids", doc_ids, (B, nq), torch.int32, index)
+        _check_small("doc_ids_k", doc_ids_k, (B, nk), torch.int32, index)
+    if prefix_lens is not None:
+        if not is_causal:
+            raise ValueError("prefix_lens needs is_causal")
+        _check_small("prefix_lens", prefix_lens, (B,), torch.int32, index)
+    if slopes is not None:
+        _check_small("slopes", slopes, (hq,), torch.float32, index)
+    if not -2 ** 31 < q_offset < 2 ** 31:
+        raise ValueError("q_offset must fit in 32 bits")
+    if not return_lse:
+        lse = None
     lib = _lib.load()
-    with torch.cuda.device(dev), _on(stream):
+    with _Launch(index, stream) as on:
         if out is None:
             out = torch.empty_like(q)
         if return_lse and lse is None:
-            lse = torch.empty((B, hq, nq), dtype=torch.float32, device=dev)
+            lse = torch.empty((B, hq, nq), dtype=torch.float32, device=q.device)
         if workspace is None:
             packed = _addressable(q) and _addressable(k) and _addressable(v)
-            workspace = alloc_workspace(lib.sage_scored_attn_workspace_size(B, hq, hkv, nq, nk, d, int(packed)), dev)
-        st = lib.sage_scored_attn(ctypes.byref(_tensor(q)), ctypes.byref(_tensor(k)), ctypes.byref(_tensor(v)),
-                                  ctypes.byref(_tensor(out)), _ptr(lse if return_lse else None), _ptr(slopes),
-                                  _ptr(prefix_lens), _ptr(doc_ids), _ptr(doc_ids_k), B, hq, hkv, nq, nk, d,
-                                  DTYPE[q.dtype], LAYOUT[tensor_layout], int(bool(is_causal)),
-                                  float("nan") if sm_scale is None else float(sm_scale), float(softcap),
-                                  int(q_offset), int(bool(return_lse)), _ptr(workspace), workspace.numel(),
-                                  _stream_ptr(stream))
-    _check(st, "scored_attn")
+            workspace = alloc_workspace(lib.sage_scored_attn_workspace_size(B, hq, hkv, nq, nk, d, packed), q.device)
+        st = lib.sage_scored_attn(byref(_tensor(q)), byref(_tensor(k)), byref(_tensor(v)), byref(_tensor(out)), _ptr(lse),
+                                  _ptr(slopes), _ptr(prefix_lens), _ptr(doc_ids), _ptr(doc_ids_k), B, hq, hkv, nq, nk, d,
+                                  DTYPE[q.dtype], LAYOUT[tensor_layout], bool(is_causal),
+                                  _NAN if sm_scale is None else sm_scale, softcap, q_offset, bool(return_lse),
+                                  workspace.data_ptr(), workspace.numel(), on)
+    if st:
+        raise SageError(st, "scored_attn")
     return (out, lse) if return_lse else out

@@ -101,8 +101,8 @@ def c_cache(**over):
     a = dict(k=FAKE, ks=(2 * 16 * 64, 16 * 64, 64), v=FAKE, vs=(2 * 16 * 64, 16 * 64, 64), pages=6, size=16, table=FAKE,
              ts=2, width=2, lens=FAKE, mass=FAKE, pos=FAKE)
     a.update(over)
-    return SagePagedCache(a["k"], (ctypes.c_int64 * 3)(*a["ks"]), a["v"], (ctypes.c_int64 * 3)(*a["vs"]), a["pages"],
-                          a["size"], a["table"], a["ts"], a["width"], a["lens"], a["mass"], a["pos"])
+    return SagePagedCache(a["k"], *a["ks"], a["v"], *a["vs"], a["pages"], a["size"], a["table"], a["ts"], a["width"],
+                          a["lens"], a["mass"], a["pos"])
 
 
 @pytest.fixture(scope="module")
