@@ -127,6 +127,8 @@ __global__ void status_clear_kernel(int* err) {
 struct EvictArgs {
   PagedView c;
   int budget, sink, recent, max_len, vec;
+  int page_shift;  // log2 of page_size, or -1
+  int cached;      // codes that the selection's shared memory holds
   int* new_lens;
   int* block_err;  // [batch * hkv]
   int* err;
@@ -173,17 +175,25 @@ __device__ __forceinline__ int block_scan(int x, int& total) {
 
 // One CTA per (head, sequence). The budget-th largest weight is found by a radix selection over the
 // ordered codes (three digits of 11, 11 and 10 bits, one histogram each: integer counts, so the
-// result does not depend on any order); then the slots are walked once in order, ties taken from
-// the lowest slot on, and the freed slots below the budget and the kept ones behind it are listed.
+// result does not depend on any order); then the slots are walked in order, ties taken from the
+// lowest slot on, and the freed slots below the budget and the kept ones behind it are listed.
+// A pass over the planes is a chain of two dependent loads per slot (page, then value), so they are read once
+// each with eight slots per thread in flight, and the codes stay in shared memory for the passes of
+// the selection, which read four at a time. (A sequence with more tokens than fit is read again, in
+// chunks, by each pass.)
+constexpr int kAhead = 8;
+constexpr int kMostCached = 48 * 1024;
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+  extern __shared__ __align__(16) unsigned codes[];  // of `cached` slots; 0: no token
   __shared__ int hist[kBins];
-  __shared__ int s_pick, s_rest, s_last;
-  __shared__ int s_bad;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  __shared__ int s_pick, s_rest, s_last, s_bad;
+  __shared__ int s_cnt[32][4];
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t me = (int64_t)b * a.c.hkv + h;
   pdl_wait();
   const int len = checked_len(a.c, b, a.max_len);
   if (tid == 0) { s_last = INT32_MIN; s_bad = len < 0 ? kDevSeqlens : 0; }
+  for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
   __syncthreads();
   const int keep = a.budget;
   if (h == 0 && tid == 0) a.new_lens[b] = len < 0 ? a.c.lens[b] : min(len, keep);
@@ -192,21 +202,28 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     return;
   }
   const int* table = a.c.table + b * a.c.table_stride;
+  // plane index of slot j, or -1 (behind the last token; or on a bad page, which sets `bad`)
+  bool bad = false;
   auto where = [&](int j) -> int64_t {
-    const int i = j / a.c.page_size;
+    if (j >= len) return -1;
+    const int i = a.page_shift >= 0 ? j >> a.page_shift : j / a.c.page_size;
     const int page = __ldg(&table[i]);
-    return page >= 0 && page < a.c.num_pages ? plane_at(a.c, page, h, j - i * a.c.page_size) : -1;
+    if (page >= 0 && page < a.c.num_pages) return plane_at(a.c, page, h, j - i * a.c.page_size);
+    bad = true;
+    return -1;
   };
   {
     int last = INT32_MIN;
-    bool bad = false;
-    for (int j = tid; j < len; j += kSelThreads) {
-      const int64_t w = where(j);
-      if (w < 0) bad = true;
-      else last = max(last, a.c.pos[w]);
+    for (int j0 = tid; j0 < len; j0 += kSelThreads * kAhead) {
+      int64_t w[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) w[u] = where(j0 + u * kSelThreads);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (w[u] >= 0) last = max(last, a.c.pos[w[u]]);
     }
     last = __reduce_max_sync(0xffffffffu, last);
-    if ((tid & 31) == 0) atomicMax(&s_last, last);
+    if (lane == 0) atomicMax(&s_last, last);
     if (bad) s_bad = kDevPage;
   }
   __syncthreads();
@@ -215,23 +232,60 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     return;
   }
   const int64_t recent_from = (int64_t)s_last - a.recent;
-  auto code_of = [&](int j) -> unsigned {
-    const int64_t w = where(j);
-    const int p = a.c.pos[w];
-    return p < a.sink || p > recent_from ? 0xFFFFFFFFu : weight_code(a.c.mass[w]);
+  const int cap = a.cached;  // a multiple of 4
+  const bool once = len <= cap;
+  // codes of the slots [c0, c0 + cap); their first digit is counted with `count`
+  auto load_codes = [&](int c0, bool count) {
+    const int n = min(cap, (len - c0 + 3) & ~3);
+    for (int j0 = tid; j0 < n; j0 += kSelThreads * kAhead) {
+      int64_t w[kAhead];
+      int p[kAhead];
+      float x[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) w[u] = j0 + u * kSelThreads < n ? where(c0 + j0 + u * kSelThreads) : -1;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        p[u] = w[u] >= 0 ? a.c.pos[w[u]] : 0;
+        x[u] = w[u] >= 0 ? a.c.mass[w[u]] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (j0 + u * kSelThreads < n) {
+          const unsigned c = w[u] < 0 ? 0u : p[u] < a.sink || p[u] > recent_from ? 0xFFFFFFFFu : weight_code(x[u]);
+          codes[j0 + u * kSelThreads] = c;
+          if (count && c) atomicAdd(&hist[c >> 21], 1);
+        }
+    }
+    return n;
   };
+  int loaded = 0;
+  if (once) {
+    loaded = load_codes(0, true);
+    __syncthreads();
+  }
   unsigned prefix = 0, mask = 0;
   int rest = keep;  // how many of the codes that match the prefix are kept
 #pragma unroll 1
   for (int digit = 0; digit < 3; ++digit) {
     const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bins = digit == 2 ? 1024 : 2048;
-    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int j = tid; j < len; j += kSelThreads) {
-      const unsigned c = code_of(j);
-      if ((c & mask) == prefix) atomicAdd(&hist[(c >> shift) & (bins - 1)], 1);
+    if (digit > 0) {
+      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
     }
-    __syncthreads();
+    if (digit > 0 || !once)
+      for (int c0 = 0; c0 < len; c0 += cap) {
+        const int n = once ? loaded : load_codes(c0, digit == 0);
+        if (!once) __syncthreads();
+        if (digit > 0)
+          for (int j = tid * 4; j < n; j += kSelThreads * 4) {
+            const uint4 c = *reinterpret_cast<const uint4*>(&codes[j]);
+            if ((c.x & mask) == prefix) atomicAdd(&hist[(c.x >> shift) & (bins - 1)], 1);
+            if ((c.y & mask) == prefix) atomicAdd(&hist[(c.y >> shift) & (bins - 1)], 1);
+            if ((c.z & mask) == prefix) atomicAdd(&hist[(c.z >> shift) & (bins - 1)], 1);
+            if ((c.w & mask) == prefix) atomicAdd(&hist[(c.w >> shift) & (bins - 1)], 1);
+          }
+        __syncthreads();
+      }
     // bins from the top: the one in which the rest-th largest lies
     const int hi = kBins - 1 - 2 * tid, x1 = hist[hi], x0 = hist[hi - 1];
     int total;
@@ -244,34 +298,103 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     rest = s_rest;
     __syncthreads();
   }
-  // the threshold is `prefix`; of the slots that equal it the first `rest` are kept
-  int ties = 0, holes = 0, movers = 0;
+  // The threshold is `prefix`; of the slots that equal it the first `rest` are kept. In each chunk a warp walks its
+  // own stretch, four slots per lane: first what it holds below and behind the budget is counted, which
+  // gives every warp its place in the lists, then the lists are written.
   int* to = a.to + me * a.pitch;
   int* from = a.from + me * a.pitch;
-#pragma unroll 1
-  for (int j0 = 0; j0 < len; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const bool in = j < len;
-    const unsigned c = in ? code_of(j) : 0u;
-    const bool tie = in && c == prefix;
-    int n_ties, n;
-    const int my_tie = ties + block_scan(tie, n_ties);
-    const bool kept = in && (c > prefix || (tie && my_tie < rest));
-    const bool hole = in && j < keep && !kept, mover = in && j >= keep && kept;
-    // one scan counts both: a hole in the low half, a mover in the high
-    const int at = block_scan((int)hole | ((int)mover << 16), n);
-    if (hole) to[holes + (at & 0xffff)] = j;
-    if (mover) from[movers + (at >> 16)] = j;
-    ties += n_ties;
-    holes += n & 0xffff;
-    movers += n >> 16;
+  int ties = 0, holes = 0, movers = 0;  // before this chunk
+  for (int c0 = 0; c0 < len; c0 += cap) {
+    const int n = once ? loaded : load_codes(c0, false);
+    if (!once) __syncthreads();
+    const int span = (n + 32 * 128 - 1) / (32 * 128) * 128;
+    const int j_lo = min(n, warp * span), j_hi = min(n, j_lo + span);
+    int over_lo = 0, over_hi = 0, tie_lo = 0, tie_hi = 0;
+    for (int j = j_lo + lane * 4; j < j_hi; j += 128) {
+      const uint4 v = *reinterpret_cast<const uint4*>(&codes[j]);
+      const unsigned c[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool low = c0 + j + u < keep;
+        over_lo += c[u] > prefix && low;
+        over_hi += c[u] > prefix && !low;
+        tie_lo += c[u] == prefix && low;
+        tie_hi += c[u] == prefix && !low;
+      }
+    }
+    over_lo = __reduce_add_sync(0xffffffffu, over_lo);
+    over_hi = __reduce_add_sync(0xffffffffu, over_hi);
+    tie_lo = __reduce_add_sync(0xffffffffu, tie_lo);
+    tie_hi = __reduce_add_sync(0xffffffffu, tie_hi);
+    if (lane == 0) {
+      s_cnt[warp][0] = over_lo; s_cnt[warp][1] = over_hi;
+      s_cnt[warp][2] = tie_lo; s_cnt[warp][3] = tie_hi;
+    }
+    __syncthreads();
+    // every warp sums the warps before it, and all of them for the next chunk
+    int my_ties = ties, my_holes = holes, my_movers = movers;
+    for (int w = 0; w < 32; ++w) {
+      if (w == warp) { my_ties = ties; my_holes = holes; my_movers = movers; }
+      const int lo = min(n, w * span), hi = min(n, lo + span);
+      const int low = max(0, min(min(c0 + hi, keep), len) - (c0 + lo));  // its slots below the budget
+      const int kept_lo = min(s_cnt[w][2], max(0, rest - ties));
+      const int kept_hi = min(s_cnt[w][3], max(0, rest - ties - s_cnt[w][2]));
+      ties += s_cnt[w][2] + s_cnt[w][3];
+      holes += low - s_cnt[w][0] - kept_lo;
+      movers += s_cnt[w][1] + kept_hi;
+    }
+    for (int j0 = j_lo; j0 < j_hi; j0 += 128) {
+      const int j = j0 + lane * 4;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (j < j_hi) v = *reinterpret_cast<const uint4*>(&codes[j]);
+      const unsigned c[4] = {v.x, v.y, v.z, v.w};
+      int mine = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) mine += c[u] == prefix;
+      int inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      int tie = my_ties + inc - mine;
+      my_ties += __shfl_sync(0xffffffffu, inc, 31);
+      unsigned hole = 0, mover = 0;  // of the four
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool kept = c[u] > prefix || (c[u] == prefix && tie < rest);
+        tie += c[u] == prefix;
+        const bool low = c0 + j + u < keep;
+        hole |= (unsigned)(c[u] != 0 && low && !kept) << u;
+        mover |= (unsigned)(kept && !low) << u;
+      }
+      const int both = __popc(hole) | __popc(mover) << 16;
+      int run = both;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += x;
+      }
+      int at_h = my_holes + ((run - both) & 0xffff), at_m = my_movers + ((run - both) >> 16);
+      const int all = __shfl_sync(0xffffffffu, run, 31);
+      my_holes += all & 0xffff;
+      my_movers += all >> 16;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (hole >> u & 1u) to[at_h++] = c0 + j + u;
+        if (mover >> u & 1u) from[at_m++] = c0 + j + u;
+      }
+    }
+    __syncthreads();
   }
   if (tid == 0) { a.count[me] = movers; a.block_err[me] = 0; }
 }
 
-// Moves the listed tokens: a half warp per token and pass, 16 bytes per lane. Sources lie behind the budget and
-// targets below it, so no move reads what another one writes.
-__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
+// Moves the listed tokens: a half warp per token, 16 bytes per lane. Sources lie behind the budget and
+// targets below it, so no move reads what another one writes. (More tokens in flight per half warp measured
+// slower: 2 and 4 of them 109 and 113 us against 98 for the whole call, 64 heads of up to 32K tokens,
+// since the registers cost resident warps.)
+__global__ void __launch_bounds__(256, 8) evict_move_kernel(const EvictArgs a) {
   const int h = blockIdx.y, b = blockIdx.z;
   const int64_t me = (int64_t)b * a.c.hkv + h;
   pdl_wait();
@@ -418,8 +541,15 @@ int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch
   a.from = reinterpret_cast<int*>(w + L.from);
   a.pitch = L.pitch;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(evict_select_kernel, dim3(heads_kv, batch), dim3(kSelThreads), 0, st, a);
-  // enough CTAs to fill the GPU, sixteen tokens each and pass, none that could not have work
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (cache->page_size == 1 << i) a.page_shift = i;
+  a.cached = max_seqlen < kMostCached ? (max_seqlen + 3) / 4 * 4 : kMostCached;
+  static std::atomic<int> limits[64];
+  cudaError_t e = raise_smem_limit(evict_select_kernel, kMostCached * 4, limits);
+  if (e == cudaSuccess)
+    e = launch_pdl(evict_select_kernel, dim3(heads_kv, batch), dim3(kSelThreads), (size_t)a.cached * 4, st, a);
+  // enough CTAs to fill the GPU, none that could not have work
   int64_t blocks = (L.pitch + 15) / 16, most = 1216 / ((int64_t)batch * heads_kv);
   blocks = blocks < 1 ? 1 : blocks;
   most = most < 1 ? 1 : most;
