@@ -527,13 +527,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       if (a.scores) {
         // (the pitch is a multiple of the tile, so pairs are aligned and whole tiles fit)
         float* dst = a.scores + ((int64_t)cu.b * a.hq + row0 + r0) * a.score_pitch + key0 + cq;
-        if (r0 < rows)
+        if (r0 < rows) {
 #pragma unroll
           for (int n = 0; n < NK; ++n) *reinterpret_cast<float2*>(dst + n * 8) = make_float2(s[n][0], s[n][1]);
-        if (r0 + 8 < rows)
+        }
+        if (r0 + 8 < rows) {
 #pragma unroll
           for (int n = 0; n < NK; ++n)
             *reinterpret_cast<float2*>(dst + 8 * a.score_pitch + n * 8) = make_float2(s[n][2], s[n][3]);
+        }
       }
       // the frame of a row (its four lanes agree) lies kHead below the maximum that set it, and is
       // kept unless that grew by more than 8: the sums and O are rescaled rarely

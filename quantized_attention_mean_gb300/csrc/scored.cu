@@ -38,15 +38,18 @@ struct DocTile {
   int pad;     // some padding
 };
 
-// The cap's polynomial (cap_step).
+// cap tanh(s / cap) for |s| <= 0.7 cap, base 2, as s times a polynomial of s^2: the minimax one of degree 4 of
+// tanh(x) / x on [0, 0.7] (found by exchange; tanh is off by at most 2.5e-7 in fp32) with the scales folded in.
+// It leaves one exponential per score on the special-function unit, which the quotient's three
+// overload. `most`: the largest product |q.k| it is used for (-1: never).
 struct CapPoly {
-  float k, c[5];  // 1 / cap; coefficients times cap, base 2
+  float c[5], most;
 };
 
 struct ScoredArgs {
   int batch, hq, hkv, nq, nk, d, dtype, causal, splits, k_tiles, q_offset, vec;
   float c2;           // sm_scale log2(e)
-  float cap2, cap_k, cap_x;  // cap log2(e); 2 sm_scale log2(e) / cap; sm_scale / cap
+  float cap2, cap_k;  // cap log2(e); 2 sm_scale log2(e) / cap
   CapPoly poly;
   void* o; int64_t o_sb, o_sh, o_sn;
   float* lse;
@@ -115,19 +118,16 @@ __device__ __forceinline__ void cap_quotient(float (&t)[16], float k, float m2, 
   for (int u = 0; u < 16; ++u) t[u] = rcpf(t[u]);
   each2(t, [&](float& p, float& q) { fma2(p, q, p, q, m2, m2, off, off); });
 }
-// The same for |s| <= 0.7 cap, plus off + line(u), in four steps: x = s / cap times a polynomial of x^2, the minimax one
-// of degree 4 of tanh(x) / x there (found by exchange; tanh is off by at most 2.5e-7 in fp32). It leaves one
-// exponential per score on the special-function unit, which the quotient's three overload.
+// Eight products to cap tanh(s / cap) + off + line(u) by the polynomial, in four steps.
 template <typename L>
 __device__ __forceinline__ void cap_step(const CapPoly& p, int part, float (&t)[8], float (&z)[8], float (&y)[8], L line,
                                          bool lined, float off) {
 #pragma unroll
   for (int u = 0; u < 8; u += 2) {
     if (part == 0) {
-      mul2(t[u], t[u + 1], t[u], t[u + 1], p.k, p.k);
       mul2(z[u], z[u + 1], t[u], t[u + 1], t[u], t[u + 1]);
-    } else if (part == 1) {
       fma2(y[u], y[u + 1], z[u], z[u + 1], p.c[4], p.c[4], p.c[3], p.c[3]);
+    } else if (part == 1) {
       fma2(y[u], y[u + 1], y[u], y[u + 1], z[u], z[u + 1], p.c[2], p.c[2]);
     } else if (part == 2) {
       fma2(y[u], y[u + 1], y[u], y[u + 1], z[u], z[u + 1], p.c[1], p.c[1]);
@@ -638,17 +638,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int kLag = FORM == 2 ? 3 : 2;
           const float off = (FORM == 2 ? a.cap2 : 0.f) - m_use + base;
           float st[LINE ? 8 : 1];
-          if constexpr (LINE)
+          if constexpr (LINE) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) st[u] = step * static_cast<float>(u);
+          }
           float r0[8], r1[8], r2[8];  // rounds in flight, the newest first
 #pragma unroll
           for (int q = 0; q < 16 + kLag; ++q) {
             float in[8], mid[8], o8 = off;
             if constexpr (LINE) o8 = fmaf(step, static_cast<float>((FORM == 2 ? q - 2 : q) * 8), off);
-            if (q < 16)
+            if (q < 16) {
 #pragma unroll
               for (int u = 0; u < 8; ++u) in[u] = __uint_as_float(s[q >> 2][(q & 3) * 8 + u]);
+            }
 #pragma unroll
             for (int u = 0; u < 8; ++u) mid[u] = FORM == 2 ? r1[u] : r0[u];
             float z[8], y[8];
@@ -773,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int u = 0; u < 32; u += 2)
                 big = max3(big, fabsf(__uint_as_float(s[c][u])), fabsf(__uint_as_float(s[c][u + 1])));
-            small = __all_sync(0xffffffffu, big * a.cap_x <= 0.7f);
+            small = __all_sync(0xffffffffu, big <= a.poly.most);
           }
           release_s();
           reframe();
@@ -886,9 +888,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tO + c * 32, o);
             tmem_wait_ld(o);
           }
-          if (!seen)
+          if (!seen) {
 #pragma unroll
             for (int u = 0; u < 32; ++u) o[u] = 0u;
+          }
           if (valid && a.splits > 1) {
 #pragma unroll
             for (int u = 0; u < 32; u += 4)
@@ -1146,11 +1149,18 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
       std::isnan(sm_scale) || sm_scale <= 0.f ? (float)(1.0 / std::sqrt((double)head_dim)) : sm_scale;
   a.c2 = (float)(scale * 1.4426950408889634);
   a.cap2 = (float)(softcap * 1.4426950408889634);
-  a.cap_x = softcap > 0.f ? scale / softcap : 0.f;
   const double tanh_c[5] = {0.9999997019767761, -0.3333034813404083, 0.13282497227191925, -0.050881292670965195,
                             0.013819585554301739};
-  a.poly.k = a.cap_x;
-  for (int i = 0; i < 5; ++i) a.poly.c[i] = (float)(tanh_c[i] * softcap * 1.4426950408889634);
+  const double cap_x = softcap > 0.f ? (double)scale / softcap : 0.0;
+  double scaled = softcap * 1.4426950408889634 * cap_x;
+  a.poly.most = softcap > 0.f ? (float)(0.7 / cap_x) : -1.f;
+  for (int i = 0; i < 5; ++i, scaled *= cap_x * cap_x) {
+    const double c = tanh_c[i] * scaled;
+    a.poly.c[i] = (float)c;
+    // (a coefficient near the ends of fp32's range: the quotient)
+    if (!(std::fabs(c) > 1e-30 && std::fabs(c) < 1e30)) a.poly.most = -1.f;
+  }
+  if (!(a.poly.most < 1e6f)) a.poly.most = -1.f;
   a.cap_k = softcap > 0.f ? (float)(2.0 * 1.4426950408889634 * scale / softcap) : 0.f;
   a.o = out->data; a.o_sb = view[3].sb; a.o_sh = view[3].sh; a.o_sn = view[3].sn;
   a.lse = return_lse ? lse : nullptr;
