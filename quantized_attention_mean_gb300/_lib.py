@@ -21,6 +21,11 @@ class SagePacked(ctypes.Structure):
     _fields_ = [("data", c_void_p), ("stride_token", c_int64), ("stride_head", c_int64)]
 
 
+class SageView(ctypes.Structure):
+    """sage_tensor with its strides as single fields: the same layout, cheaper to fill."""
+    _fields_ = [("data", c_void_p), ("stride0", c_int64), ("stride1", c_int64), ("stride2", c_int64)]
+
+
 class SagePagedCache(ctypes.Structure):
     # (the strides as single fields: the same layout as arrays of three, cheaper to fill)
     _fields_ = ([("k", c_void_p)] + [(f"k_stride{i}", c_int64) for i in range(3)] + [("v", c_void_p)]
@@ -70,7 +75,7 @@ SIGNATURES = {
     "sage_merge_partials": (c_int, [c_void_p, c_void_p, c_int, _T, c_void_p] + [c_int] * 6
                             + [c_void_p]),
     "sage_scored_attn_workspace_size": (c_size_t, [c_int] * 7),
-    "sage_scored_attn": (c_int, [_T, _T, _T, _T, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]
+    "sage_scored_attn": (c_int, [c_void_p] * 9  # (tensors by reference: SageTensor or SageView)
                          + [c_int] * 9 + [c_float] * 2 + [c_int] * 2 + [c_void_p, c_size_t, c_void_p]),
     "sage_paged_attn_workspace_size": (c_size_t, [c_int] * 6),
     "sage_paged_attn": (c_int, [_P, _C, _P, c_void_p, c_void_p, c_void_p] + [c_int] * 7

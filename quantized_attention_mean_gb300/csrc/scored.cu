@@ -379,6 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   pdl_wait();
+  // the status word: nothing but a wait of two seconds can set it after this
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *a.err = 0;
 
   // ---- the key tiles of this CTA
   // keys that a row sees at most
@@ -964,10 +966,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Clears the status word; with documents, the ids that each tile of 128 keys holds.
+// The document ids that each tile of 128 keys holds.
 __global__ void __launch_bounds__(128) scored_setup_kernel(const ScoredArgs a) {
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.err = 0;
-  if (!a.doc_k) return;
   __shared__ int s_lo, s_hi, s_pad;
   if (threadIdx.x == 0) { s_lo = INT32_MAX; s_hi = -1; s_pad = 0; }
   __syncthreads();
@@ -1223,8 +1223,8 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
     if (!make_map4(&maps[i], dtype == SAGE_BF16, t.p, inner, t.n, t.heads, batch, sn * 2, sh * 2, sb * 2, 64, 128))
       return note_cuda_failure(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
   }
-  if (e == cudaSuccess) {
-    scored_setup_kernel<<<doc_k ? dim3(L.k_tiles, batch) : dim3(1), 128, 0, st>>>(a);
+  if (e == cudaSuccess && doc_k) {
+    scored_setup_kernel<<<dim3(L.k_tiles, batch), 128, 0, st>>>(a);
     e = cudaGetLastError();
   }
   const dim3 grid(heads_q, (unsigned)pairs, (unsigned)(batch * L.splits));

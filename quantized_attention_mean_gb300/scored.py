@@ -5,16 +5,24 @@ from ctypes import byref
 
 import torch
 
-from . import DTYPE, LAYOUT, SageError, _check_dense_args, _dims, _lib, _tensor, alloc_workspace
+from . import DTYPE, LAYOUT, SageError, _check_dense_args, _dims, _lib, alloc_workspace
+from ._lib import SageView
 from .paged import _NAN, _check_small, _Launch, _ptr
 
 __all__ = ["scored_attn", "scored_attn_workspace_bytes"]
 
 
-def _addressable(t):
-    """Whether the kernel can read t's rows in place (otherwise they are copied to the workspace)."""
-    return (t.shape[3] % 8 == 0 and t.data_ptr() % 16 == 0
-            and all(n <= 1 or (s > 0 and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()[:3])))
+def _view(t, whole):
+    """t for the library, and whether the kernel can read its rows in place (`whole`: head_dim is a multiple
+    of 8; otherwise, and where an address or stride is not, rows are copied to the workspace)."""
+    n0, n1, n2, n3 = t.shape
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1 and n3 != 1:
+        raise ValueError("the last dimension must be contiguous")
+    at = t.data_ptr()
+    return SageView(at, s0, s1, s2), (whole and at % 16 == 0 and (n0 <= 1 or (s0 > 0 and s0 % 8 == 0))
+                                      and (n1 <= 1 or (s1 > 0 and s1 % 8 == 0))
+                                      and (n2 <= 1 or (s2 > 0 and s2 % 8 == 0)))
 
 
 def scored_attn_workspace_bytes(batch, heads_q, heads_kv, seqlen_q, seqlen_k, head_dim, packed=True):
@@ -64,10 +72,11 @@ def scored_attn(q, k, v, tensor_layout="HND", is_causal=False, sm_scale=None, so
             out = torch.empty_like(q)
         if return_lse and lse is None:
             lse = torch.empty((B, hq, nq), dtype=torch.float32, device=q.device)
+        (qv, q_ok), (kv, k_ok), (vv, v_ok), (ov, _) = (_view(t, d % 8 == 0) for t in (q, k, v, out))
         if workspace is None:
-            packed = _addressable(q) and _addressable(k) and _addressable(v)
-            workspace = alloc_workspace(lib.sage_scored_attn_workspace_size(B, hq, hkv, nq, nk, d, packed), q.device)
-        st = lib.sage_scored_attn(byref(_tensor(q)), byref(_tensor(k)), byref(_tensor(v)), byref(_tensor(out)), _ptr(lse),
+            workspace = alloc_workspace(
+                lib.sage_scored_attn_workspace_size(B, hq, hkv, nq, nk, d, q_ok and k_ok and v_ok), q.device)
+        st = lib.sage_scored_attn(byref(qv), byref(kv), byref(vv), byref(ov), _ptr(lse),
                                   _ptr(slopes), _ptr(prefix_lens), _ptr(doc_ids), _ptr(doc_ids_k), B, hq, hkv, nq, nk, d,
                                   DTYPE[q.dtype], LAYOUT[tensor_layout], bool(is_causal),
                                   _NAN if sm_scale is None else sm_scale, softcap, q_offset, bool(return_lse),
