@@ -35,6 +35,7 @@ constexpr int kWarps = 4;
 constexpr int kCtas = 304;                 // two resident CTAs per SM
 constexpr int kRows = 16;                  // query heads per row block
 constexpr int kMinTiles = 2;               // tiles a CTA takes at least
+constexpr int kRanks = 8;                  // CTAs of a cluster
 enum { kLoadTma = 0, kLoadVec = 1, kLoadAny = 2 };
 constexpr float kLog2eF = 1.4426950408889634f, kLn2F = 0.6931471805599453f;
 
@@ -293,7 +294,30 @@ __device__ __forceinline__ void write_rows(const DecodeArgs& a, int b, int row0,
   }
 }
 
-template <typename T, int DP>
+// ---- few heads: a cluster per (sequence, row block of a head), joined through distributed shared memory
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t of_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 ld_rank2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_rank4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// The kernel of both forms. CLUSTER: grid (kRanks x row blocks of heads, batch), each CTA of a cluster takes its
+// share of one sequence's tiles; otherwise kCtas ranges of the line.
+template <typename T, int DP, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const DecodeArgs a) {
   using C = DecodeCfg<DP>;
@@ -315,42 +339,74 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     tma_prefetch_desc(&tmV);
   }
   pdl_wait();
-  // ---- this CTA's range of the line: the total, then the sequence that its first item lies in
+  const int me = blockIdx.x;
+  int err = 0;
+  long long left = 0;
+  Cursor cu{a.c.batch, 0, 0, 1, 0};
   __shared__ long long s_base;
   __shared__ int s_b;
-  bool bad = false;
-  if (threadIdx.x == 0) { s_b = a.c.batch; s_base = 0; }
-  Scan sc = scan_items<DP>(a, heads, 0, bad);
-  long long total = sc.all;
-  for (int b0 = blockDim.x; b0 < a.c.batch; b0 += blockDim.x) total += scan_items<DP>(a, heads, b0, bad).all;
-  const int ctas = total > 0 ? ctas_of(total) : 0, me = blockIdx.x;
-  long long left = 0, i0 = 0;
-  if (me < ctas) {
-    i0 = first_item(total, ctas, me);
-    left = first_item(total, ctas, me + 1) - i0;
-    long long base = 0;
-    for (int b0 = 0;;) {
-      const long long lo = base + sc.before;
-      if (sc.n > 0 && i0 >= lo && i0 < lo + sc.n) { s_b = b0 + threadIdx.x; s_base = lo; }
-      base += sc.all;
-      b0 += blockDim.x;
-      if (base > i0 || b0 >= a.c.batch) break;
-      sc = scan_items<DP>(a, heads, b0, bad);
-    }
-  }
-  __syncthreads();
-  int err = bad ? kDevSeqlens : 0;
-  Cursor cu{a.c.batch, 0, 0, 1, 0};
-  if (left > 0) {
-    cu.b = s_b;
-    cu.len = checked_len(a.c, cu.b, a.max_len);
+  if constexpr (CLUSTER) {
+    const int rank = me % kRanks;
+    cu.b = blockIdx.y;
+    cu.h = me / kRanks;
+    cu.len = max(checked_len(a.c, cu.b, a.max_len), 0);
     cu.tiles = tiles_of<DP>(cu.len);
-    const long long in = i0 - s_base;
-    cu.h = (int)(in / cu.tiles);
-    cu.tile = (int)(in - (long long)cu.h * cu.tiles);
+    cu.tile = cu.tiles * rank / kRanks;
+    left = cu.tiles * (rank + 1) / kRanks - cu.tile;
+  } else {
+    // this CTA's range of the line: the total, then the sequence that its first item lies in
+    bool bad = false;
+    if (threadIdx.x == 0) { s_b = a.c.batch; s_base = 0; }
+    Scan sc = scan_items<DP>(a, heads, 0, bad);
+    long long total = sc.all;
+    for (int b0 = blockDim.x; b0 < a.c.batch; b0 += blockDim.x) total += scan_items<DP>(a, heads, b0, bad).all;
+    const int ctas = total > 0 ? ctas_of(total) : 0;
+    long long i0 = 0;
+    if (me < ctas) {
+      i0 = first_item(total, ctas, me);
+      left = first_item(total, ctas, me + 1) - i0;
+      long long base = 0;
+      for (int b0 = 0;;) {
+        const long long lo = base + sc.before;
+        if (sc.n > 0 && i0 >= lo && i0 < lo + sc.n) { s_b = b0 + threadIdx.x; s_base = lo; }
+        base += sc.all;
+        b0 += blockDim.x;
+        if (base > i0 || b0 >= a.c.batch) break;
+        sc = scan_items<DP>(a, heads, b0, bad);
+      }
+    }
+    __syncthreads();
+    err = bad ? kDevSeqlens : 0;
+    if (left > 0) {
+      cu.b = s_b;
+      cu.len = checked_len(a.c, cu.b, a.max_len);
+      cu.tiles = tiles_of<DP>(cu.len);
+      const long long in = i0 - s_base;
+      cu.h = (int)(in / cu.tiles);
+      cu.tile = (int)(in - (long long)cu.h * cu.tiles);
+    }
   }
   pdl_trigger();
 
+  if constexpr (CLUSTER) {
+    // the status word has one writer (but for a wait that runs out, two seconds from now): the first
+    // CTA looks at the lengths and pages of all sequences
+    if (me == 0 && blockIdx.y == 0) {
+      int e = 0;
+      for (int b = 0; b < a.c.batch; ++b) {
+        const int len = checked_len(a.c, b, a.max_len);
+        if (len < 0) e = max(e, (int)kDevSeqlens);
+        for (int i = threadIdx.x; i < (len + a.c.page_size - 1) / a.c.page_size; i += kWarps * 32) {
+          const int pg = __ldg(&a.c.table[b * a.c.table_stride + i]);
+          if (pg < 0 || pg >= a.c.num_pages) e = max(e, kDevPage);
+        }
+      }
+      e = __reduce_max_sync(0xffffffffu, e);
+      if (lane == 0) s_err[warp] = e;
+      __syncthreads();
+      if (threadIdx.x == 0) *a.err = max(max(s_err[0], s_err[1]), max(s_err[2], s_err[3]));
+    }
+  }
   // ---- fill the ring: S - 1 stages in flight, the page of the stage after them already read
   Cursor ld = cu;
   long long to_load = left;
@@ -380,6 +436,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   float sl0 = 0.f, sl1 = 0.f;
   int qpos = 0, rows = 0, row0 = 0, tile0 = 0, pieces = 0;
   bool fresh = true;
+  if constexpr (CLUSTER) {
+    const int rb = cu.h % a.row_blocks;
+    row0 = cu.h / a.row_blocks * a.group + rb * kRows;
+    rows = min(kRows, a.group - rb * kRows);
+  }
   const float scale2 = a.sm_scale * kLog2eF;
   const float cap_in = a.cap > 0.f ? a.sm_scale / a.cap : 0.f, cap_out = a.cap * kLog2eF;
   int stage = 0;
@@ -599,7 +660,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     } else {
       ++stage;
     }
-    const bool seg_end = cu.tile + 1 == cu.tiles || left == 1;
+    const bool seg_end = !CLUSTER && (cu.tile + 1 == cu.tiles || left == 1);
     if (seg_end) {
       // ---- merge the warps: sums of a row over its four lanes, then over the warps
 #pragma unroll
@@ -688,6 +749,68 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       fresh = true;
     }
     next_item<DP>(a, heads, cu);
+  }
+  if constexpr (CLUSTER) {
+    // every warp's accumulator into its own ring, its statistics beside; then each thread of the
+    // cluster sums one group of four channels of a row over all warps of all ranks, in their order
+    const int rank = me % kRanks;
+#pragma unroll
+    for (int w = 1; w < 4; w <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, w);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, w);
+    }
+    __syncwarp();
+    float* const mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = r0 + half * 8;
+      if (!fresh && r < rows) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          *reinterpret_cast<float2*>(mine + r * DP + n * 8 + cq) = make_float2(o[n][2 * half], o[n][2 * half + 1]);
+      }
+      if ((lane & 3) == 0)
+        *reinterpret_cast<float2*>(&ml[(warp * kRows + r) * 2]) =
+            fresh ? make_float2(-INFINITY, 0.f) : make_float2(half ? m1 : m0, half ? l1 : l0);
+    }
+    if (dead) record_error(a.err, kDevTimeout);
+    cluster_sync();
+    const int cell = rank * kWarps * 32 + threadIdx.x, r = cell / (DP / 4), c = (cell - r * (DP / 4)) * 4;
+    if (r < rows) {
+      const uint32_t ml_at = smem_u32(ml + r * 2), o_at = smem_u32(sm) + (r * DP + c) * 4;
+      float2 st[kRanks * kWarps];
+#pragma unroll
+      for (int p = 0; p < kRanks * kWarps; ++p) st[p] = ld_rank2(of_rank(ml_at + (p % kWarps) * kRows * 8, p / kWarps));
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int p = 0; p < kRanks * kWarps; ++p) m = fmaxf(m, st[p].x);
+      const float u = m == -INFINITY ? 0.f : m;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int p = 0; p < kRanks * kWarps; ++p) {
+        const float w = ex2_approx(st[p].x - u);
+        l = fmaf(st[p].y, w, l);
+        if (st[p].y != 0.f) {  // (a warp without keys wrote no accumulator)
+          const float4 x = ld_rank4(of_rank(o_at + (p % kWarps) * C::kWarpBytes, p / kWarps));
+          acc.x = fmaf(w, x.x, acc.x); acc.y = fmaf(w, x.y, acc.y);
+          acc.z = fmaf(w, x.z, acc.z); acc.w = fmaf(w, x.w, acc.w);
+        }
+      }
+      const float inv = l != 0.f ? 1.0f / l : 0.f;
+      const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+      T* dst = static_cast<T*>(a.o) + (int64_t)blockIdx.y * a.o_sb + (row0 + r) * a.o_sh + c;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < a.c.d) dst[e] = round_to<T>(y[e]);
+      if (c == 0) {
+        const float l2 = l != 0.f ? m + log2f(l) : -INFINITY;
+        const int64_t at = (int64_t)blockIdx.y * a.hq + row0 + r;
+        if (a.lse) a.lse[at] = l2 * kLn2F;
+        if (a.scores) a.lse2[at] = l2;
+      }
+    }
+    cluster_sync();  // no CTA's shared memory goes away while it is read
+    return;
   }
   // this CTA's error, collected by the join kernel (no word to clear before the call)
   const int we = __reduce_max_sync(0xffffffffu, err);
@@ -872,13 +995,40 @@ bool decode_layout(int batch, int hq, int hkv, int64_t max_len, int d, bool mass
 
 template <typename T, int DP>
 cudaError_t launch_decode_t(const DecodeArgs& a, const CUtensorMap* maps, cudaStream_t st) {
-  static std::atomic<int> limits[64];
-  cudaError_t e = raise_smem_limit(decode_kernel<T, DP>, DecodeCfg<DP>::kSmem, limits);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_kernel<T, DP>, dim3(kCtas), dim3(kWarps * 32), DecodeCfg<DP>::kSmem, st, maps[0],
-                 maps[1], a);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(join_kernel<T, DP>, dim3(a.c.hkv * a.row_blocks, a.c.batch), dim3(kJoinThreads), 0, st, a);
+  using C = DecodeCfg<DP>;
+  // Few heads with short sequences: one launch of clusters whose CTAs all run at once, a tile or a few each, joined
+  // through distributed shared memory. Otherwise the line, which balances any lengths but takes a second launch
+  // to join (one sequence of 1000 tokens, 8 key/value heads, in a graph: 7.8 against 12.4 us; beyond
+  // eight tiles per CTA the line's 304 CTAs are faster than the clusters').
+  const int heads = a.c.hkv * a.row_blocks;
+  const bool cluster = (int64_t)heads * a.c.batch * kRanks <= kCtas && a.max_len <= 8 * kRanks * C::kTile;
+  cudaError_t e;
+  if (cluster) {
+    static std::atomic<int> limits[64];
+    e = raise_smem_limit(decode_kernel<T, DP, true>, C::kSmem, limits);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(heads * kRanks, a.c.batch);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kRanks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, decode_kernel<T, DP, true>, maps[0], maps[1], a);
+  } else {
+    static std::atomic<int> limits[64];
+    e = raise_smem_limit(decode_kernel<T, DP, false>, C::kSmem, limits);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(decode_kernel<T, DP, false>, dim3(kCtas), dim3(kWarps * 32), C::kSmem, st, maps[0], maps[1], a);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(join_kernel<T, DP>, dim3(heads, a.c.batch), dim3(kJoinThreads), 0, st, a);
+  }
   if (e != cudaSuccess || !a.scores || a.max_len == 0) return e;
   return launch_pdl(mass_kernel, dim3((a.max_len + 255) / 256, a.c.hkv, a.c.batch), dim3(256), 0, st, a);
 }

@@ -55,17 +55,20 @@ CASES = [
 ]
 
 
+# (a bound far above the lengths takes the form for long sequences)
+@pytest.mark.parametrize("bound", [0, 10 ** 5])
 @pytest.mark.parametrize("lens,hq,hkv,d,page,dtype,layout,cap,biased", CASES)
-def test_decode(lens, hq, hkv, d, page, dtype, layout, cap, biased):
+def test_decode(lens, hq, hkv, d, page, dtype, layout, cap, biased, bound):
     import quantized_attention_mean_gb300 as qa
+    bound = max(max(lens), bound)
     c = ref.make_cache(lens, hkv, d, page, dtype, layout, seed=len(lens) + d)
     g = torch.Generator().manual_seed(5)
     q = (torch.randn(len(lens), hq, d, generator=g) * 2).to(dtype)
     slopes = 2.0 ** (-torch.arange(1, hq + 1).float() / 4) if biased else None
     G = on_gpu(c)
-    ws = qa.alloc_workspace(qa.paged_attn_workspace_bytes(len(lens), hq, hkv, max(lens), d), DEV)
+    ws = qa.alloc_workspace(qa.paged_attn_workspace_bytes(len(lens), hq, hkv, bound, d), DEV)
     ws.fill_(255)
-    out, lse = qa.paged_attn(q.to(DEV), G["k"], G["v"], G["table"], G["lens"], max(lens), tensor_layout=layout,
+    out, lse = qa.paged_attn(q.to(DEV), G["k"], G["v"], G["table"], G["lens"], bound, tensor_layout=layout,
                              softcap=cap, slopes=None if slopes is None else slopes.to(DEV), return_lse=True, workspace=ws)
     assert qa.read_device_status(ws) == 0
     r = decode_reference(c, q, 1 / math.sqrt(d), cap, slopes, hkv=hkv)
@@ -99,8 +102,9 @@ def test_decode_positions_strides_and_scale():
     assert (ow[:, 1::2] == 9).all()
 
 
+@pytest.mark.parametrize("bound", [700, 9000])
 @pytest.mark.parametrize("hq,hkv,d,cap", [(8, 2, 128, 0.0), (20, 1, 64, 30.0), (3, 3, 40, 0.0)])
-def test_decode_accumulates_weights(hq, hkv, d, cap):
+def test_decode_accumulates_weights(hq, hkv, d, cap, bound):
     import quantized_attention_mean_gb300 as qa
     lens = [700, 1, 0, 65]
     c = ref.make_cache(lens, hkv, d, 16, torch.bfloat16)
@@ -109,7 +113,7 @@ def test_decode_accumulates_weights(hq, hkv, d, cap):
     mass0 = torch.rand(c["k"].shape[0], hkv, 16, generator=g)
     G, mass = on_gpu(c), mass0.to(DEV)
     for _ in range(2):
-        qa.paged_attn(q.to(DEV), G["k"], G["v"], G["table"], G["lens"], 700, softcap=cap, mass=mass)
+        qa.paged_attn(q.to(DEV), G["k"], G["v"], G["table"], G["lens"], bound, softcap=cap, mass=mass)
     r = decode_reference(c, q, 1 / math.sqrt(d), cap, hkv=hkv)
     want, tol = mass0.double(), mass0.double() * 2.0 ** -22 + 1e-7
     for (b, h), p in r["p"].items():
@@ -138,30 +142,29 @@ def test_decode_masked_garbage_and_nan():
     assert_close(out, r["out"], r["out_tol"], "out")
 
 
-def test_decode_reports_bad_lengths_and_pages():
+@pytest.mark.parametrize("bound", [40, 9000])
+def test_decode_reports_bad_lengths_and_pages(bound):
     import quantized_attention_mean_gb300 as qa
     c = ref.make_cache([40, 40, 40], 2, 64, 16, torch.float16)
     q = torch.randn(3, 4, 64).half().to(DEV)
     G = on_gpu(c)
-    ws = qa.alloc_workspace(qa.paged_attn_workspace_bytes(3, 4, 2, 40, 64), DEV)
-    good = qa.paged_attn(q, G["k"], G["v"], G["table"], G["lens"], 40, workspace=ws)
+    ws = qa.alloc_workspace(qa.paged_attn_workspace_bytes(3, 4, 2, bound, 64), DEV)
+    good = qa.paged_attn(q, G["k"], G["v"], G["table"], G["lens"], bound, workspace=ws)
     assert qa.read_device_status(ws) == 0
-    for bad in (-1, 41, 49, 2 ** 31 - 1):
+    for bad in (-1, 49, 2 ** 31 - 1) + ((41,) if bound == 40 else ()):     # (three pages hold 48)
         lens = G["lens"].clone()
         lens[1] = bad
-        out, lse = qa.paged_attn(q, G["k"], G["v"], G["table"], lens, 40 if bad != 49 else 10 ** 6, workspace=qa.alloc_workspace(
-            qa.paged_attn_workspace_bytes(3, 4, 2, 10 ** 6, 64), DEV) if bad == 49 else ws, return_lse=True)
-        if bad != 49:
-            assert qa.read_device_status(ws) == 12
+        out, lse = qa.paged_attn(q, G["k"], G["v"], G["table"], lens, bound, workspace=ws, return_lse=True)
+        assert qa.read_device_status(ws) == 12
         assert (out[1] == 0).all() and (lse[1] == -math.inf).all()
         assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
     for bad in (-1, c["k"].shape[0], 2 ** 31 - 1):
         table = G["table"].clone()
         table[2, 1] = bad
-        out = qa.paged_attn(q, G["k"], G["v"], table, G["lens"], 40, workspace=ws)
+        out = qa.paged_attn(q, G["k"], G["v"], table, G["lens"], bound, workspace=ws)
         assert qa.read_device_status(ws) == 13
         assert torch.equal(out[:2], good[:2]) and torch.isfinite(out).all()
-    qa.paged_attn(q, G["k"], G["v"], G["table"], G["lens"], 40, workspace=ws)
+    qa.paged_attn(q, G["k"], G["v"], G["table"], G["lens"], bound, workspace=ws)
     assert qa.read_device_status(ws) == 0
 
 
