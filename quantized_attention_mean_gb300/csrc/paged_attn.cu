@@ -51,6 +51,7 @@ struct DecodeArgs {
   int load;                 // how rows are read: kLoadTma, kLoadVec or kLoadAny
   int box_rows;             // rows of a TMA box
   int page_shift;           // log2 of page_size, or -1
+  int mass4;                // see mass_kernel
   int slices;               // CTAs of the join per (row block of a head, sequence)
   // workspace
   int* err;                 // status word
@@ -955,27 +956,47 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
 }
 
 // --------------------------------------------------------------------------- accumulated weight
-// mass += sum over the group's heads of 2^(t - lse2): the scores written by the decode kernel, one thread per
-// key. Added atomically, since two sequences may share a page; a page of one sequence gets one
-// addition, whose result does not depend on any order.
+// mass += sum over the group's heads of 2^(t - lse2): the scores written by the decode kernel, four keys per
+// thread. Added atomically, since two sequences may share a page; a page of one sequence gets one
+// addition, whose result does not depend on any order. (`mass4`: four slots lie in one page and in one
+// aligned 16 bytes of the plane.)
+constexpr int kMassKeys = 4;
 __global__ void __launch_bounds__(256) mass_kernel(const DecodeArgs a) {
   pdl_wait();
   const int b = blockIdx.z, h = blockIdx.y;
   const int len = max(checked_len(a.c, b, a.max_len), 0);
-  const int key = blockIdx.x * 256 + threadIdx.x;
+  const int key = (blockIdx.x * 256 + threadIdx.x) * kMassKeys;
   if (key >= len) return;
-  const int i = key / a.c.page_size;
-  const int page = __ldg(&a.c.table[b * a.c.table_stride + i]);
-  if (page < 0 || page >= a.c.num_pages) return;
   const int64_t row = (int64_t)b * a.hq + h * a.group;
-  const float* s = a.scores + row * a.score_pitch + key;
-  float sum = 0.f;
-#pragma unroll 8
+  const float* s = a.scores + row * a.score_pitch + key;  // (the pitch is a multiple of 128)
+  float sum[kMassKeys] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int g = 0; g < a.group; ++g) {
     const float l2 = a.lse2[row + g];
-    sum += l2 == -INFINITY ? 0.f : ex2_approx(s[g * a.score_pitch] - l2);
+    const float4 t = *reinterpret_cast<const float4*>(s + g * a.score_pitch);
+    if (l2 != -INFINITY) {
+      sum[0] += ex2_approx(t.x - l2);
+      sum[1] += ex2_approx(t.y - l2);
+      sum[2] += ex2_approx(t.z - l2);
+      sum[3] += ex2_approx(t.w - l2);
+    }
   }
-  atomicAdd(&a.c.mass[plane_at(a.c, page, h, key - i * a.c.page_size)], sum);
+  const int n = min(kMassKeys, len - key);
+  int err = 0;
+  if (a.mass4 && n == kMassKeys) {
+    int page, slot;
+    find_page(a, b, key, true, page, slot, err);
+    if (page >= 0)
+      asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(&a.c.mass[plane_at(a.c, page, h, slot)]),
+                   "f"(sum[0]), "f"(sum[1]), "f"(sum[2]), "f"(sum[3])
+                   : "memory");
+    return;
+  }
+  for (int i = 0; i < n; ++i) {
+    int page, slot;
+    find_page(a, b, key + i, true, page, slot, err);
+    if (page >= 0) atomicAdd(&a.c.mass[plane_at(a.c, page, h, slot)], sum[i]);
+  }
 }
 
 // ------------------------------------------------------------------------------------- host
@@ -1036,7 +1057,8 @@ cudaError_t launch_decode_t(const DecodeArgs& a, const CUtensorMap* maps, cudaSt
     e = launch_pdl(join_kernel<T, DP>, dim3(heads * a.slices, a.c.batch), dim3(kJoinThreads), 0, st, a);
   }
   if (e != cudaSuccess || !a.scores || a.max_len == 0) return e;
-  return launch_pdl(mass_kernel, dim3((a.max_len + 255) / 256, a.c.hkv, a.c.batch), dim3(256), 0, st, a);
+  return launch_pdl(mass_kernel, dim3((unsigned)(((int64_t)a.max_len + 256 * kMassKeys - 1) / (256 * kMassKeys)), a.c.hkv, a.c.batch), dim3(256), 0,
+                    st, a);
 }
 
 }  // namespace
@@ -1124,6 +1146,7 @@ int sage_paged_attn(const sage_packed* q, const sage_paged_cache* cache, const s
     a.lse2 = reinterpret_cast<float*>(w + L.lse2);
     a.scores = reinterpret_cast<float*>(w + L.scores);
     a.score_pitch = L.pitch;
+    a.mass4 = cache->page_size % 4 == 0 && reinterpret_cast<uintptr_t>(cache->mass) % 16 == 0;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
