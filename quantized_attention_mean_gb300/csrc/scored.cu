@@ -158,7 +158,7 @@ __device__ __forceinline__ void ld16_max(uint32_t taddr, uint32_t (&r)[32], floa
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void wait_ld_max8(float (&m)[8]) {
+__device__ __forceinline__ void wait_ld_max(float (&m)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(m[0]), "+f"(m[1]), "+f"(m[2]), "+f"(m[3]), "+f"(m[4]), "+f"(m[5]), "+f"(m[6]), "+f"(m[7])
                :
@@ -382,6 +382,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the status word: nothing but a wait of two seconds can set it after this
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *a.err = 0;
 
+  // Q is on its way while the key tiles are found
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    const int b = (int)blockIdx.z / a.splits;
+    bar_expect(q_full, (has_b ? 2 : 1) * C::kQBytes);
+    for (int t = 0; t < (has_b ? 2 : 1); ++t)
+      for (int c = 0; c < C::kChunks; ++c)
+        tma_4d(sbase + t * C::kQBytes + c * 16384, &tmQ, q_full, c * 64, q0 + t * 128, (int)blockIdx.x, b);
+  }
+
   // ---- the key tiles of this CTA
   // keys that a row sees at most
   auto limit_of = [&](int row, int prefix) -> int {
@@ -439,14 +449,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_tiles = lds(misc + kWTiles), row0 = lds(misc + kWJ0) * 128, b = lds(misc + kWSeq);
       const int left = lds(misc + kWLeft);
       const int h = blockIdx.x, hk = h / (a.hq / a.hkv);
+      if (lane == 0 && n_tiles == 0) bar_wait(q_full, 0, 0);  // (Q lands before the shared memory goes away)
       if (lane == 0 && n_tiles > 0) {
-        tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
-        bar_expect(q_full, (has_b ? 2 : 1) * C::kQBytes);
-        for (int t = 0; t < (has_b ? 2 : 1); ++t)
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_4d(sbase + t * C::kQBytes + c * 16384, &tmQ, q_full, c * 64, q0 + t * 128, h, b);
         int nk = 0, nv = 0;
         bool ok = true;
         for (int j = 0; j < n_tiles; ++j) {
@@ -604,18 +610,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = kNegInf;                             // the frame, base 2
     float l = 0.f;
     bool ok = true;
-    if (active) {
-      for (int j = 0; j < my_tiles && ok; ++j) {
-        const int sb = solo ? j & 1 : x;
-        const uint32_t tS = tmem + lane_base + sb * 128;
-        const uint32_t tP = C::kOver ? tS : tmem + lane_base + C::kTmemP + x * C::kPitchP;
-        ok = warp_wait(s_full + 8 * sb, (solo ? j >> 1 : j) & 1, abort_at);
-        if (!ok) break;
+    uint32_t s[4][32];
+    float cm[BIAS ? 8 : 4];  // the largest products of 16 or 32 keys
+    // the products of step j into s, with their maxima; valid after have_s()
+    auto load_s = [&](int j) {
+      const int sb = solo ? j & 1 : x;
+      const uint32_t tS = tmem + lane_base + sb * 128;
+      ok = warp_wait(s_full + 8 * sb, (solo ? j >> 1 : j) & 1, abort_at);
+      if (!ok) return;
         if (releases) {  // K of this tile has been read, and V of the last (where this barrier tells it)
           bar_arrive(k_empty + 8 * ((uint32_t)j % C::kKStages));
           if (C::kOver && !solo && j > 0) bar_arrive(v_empty + 8 * ((uint32_t)(j - 1) % C::kVStages));
         }
         tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if constexpr (BIAS) {
+            ld16_max<0>(tS + c * 32, s[c], cm[2 * c]);
+            ld16_max<16>(tS + c * 32 + 16, s[c], cm[2 * c + 1]);
+          } else {
+            ld32_max(tS + c * 32, s[c], cm[c]);
+          }
+        }
+    };
+    auto have_s = [&]() {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+      wait_ld_max(cm);
+    };
+    if (active) {
+      for (int j = 0; j < my_tiles && ok; ++j) {
+        load_s(j);
+        if (!ok) break;
+        const uint32_t tP = tmem + lane_base + (C::kOver ? (solo ? j & 1 : x) * 128 : C::kTmemP + x * C::kPitchP);
         const int tile = j0 + (BIAS ? tile_of(j, left) : j), kv0 = tile * 128;
         // ---- which keys of the tile this row sees, as bits (only where some row of the warp misses one)
         bool whole = limit - kv0 >= 128;
@@ -625,7 +652,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         whole = whole || !valid;  // (rows behind the last one are not written)
         const bool masked = !__all_sync(0xffffffffu, whole);
-        uint32_t s[4][32];
         float t_max = kNegInf, m_use = 0.f;
         float g0 = 0.f, g1 = 0.f, g2 = 0.f, g3 = 0.f;
         // S is in registers
@@ -776,27 +802,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto capped = [&](float v) {
             return CAP ? fmaf(rcpf(1.0f + ex2f(v * cap_in)), cap_m2, a.cap2) : v * a.c2;
           };
+          have_s();
           if constexpr (BIAS) {
-            float cm[8];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              ld16_max<0>(tS + c * 32, s[c], cm[2 * c]);
-              ld16_max<16>(tS + c * 32 + 16, s[c], cm[2 * c + 1]);
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
-            wait_ld_max8(cm);
             const float end = step > 0.f ? 15.0f * step : 0.f;
 #pragma unroll
             for (int c = 0; c < 8; ++c) t_max = fmaxf(t_max, fmaf(step, static_cast<float>(c * 16), capped(cm[c])));
             t_max += base + end;
           } else {
-            float cm[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) ld32_max(tS + c * 32, s[c], cm[c]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
-            wait_ld_max(cm);
             t_max = capped(fmaxf(max3(cm[0], cm[1], cm[2]), cm[3]));
           }
           if constexpr (CAP) {
@@ -813,10 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (BIAS) weights_of(Yes{}, small, step, base);
           else weights_of(No{}, small, 0.f, 0.f);
         } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+          have_s();
           release_s();
           // scores in base 2: capped or scaled, then biased
           auto scores = [&](auto bias_at) {
