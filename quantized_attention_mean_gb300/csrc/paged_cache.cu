@@ -129,6 +129,7 @@ struct EvictArgs {
   int budget, sink, recent, max_len, vec;
   int page_shift;  // log2 of page_size, or -1
   int cached;      // codes that the selection's shared memory holds
+  int vec4;        // four slots lie in one page and in aligned 16 bytes of the planes
   int* new_lens;
   int* block_err;  // [batch * hkv]
   int* err;
@@ -202,27 +203,64 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     return;
   }
   const int* table = a.c.table + b * a.c.table_stride;
-  // plane index of slot j, or -1 (behind the last token; or on a bad page, which sets `bad`)
+  // Plane indexes of eight groups of slots, the first of group u at j0 + u G kSelThreads, or -1 (behind `end`; or
+  // on a bad page, which sets `bad`). A group is the G slots of one thread, in one page. Pages are loaded
+  // for all groups before any is looked at: with a branch between, each waits for the last.
   bool bad = false;
-  auto where = [&](int j) -> int64_t {
-    if (j >= len) return -1;
-    const int i = a.page_shift >= 0 ? j >> a.page_shift : j / a.c.page_size;
-    const int page = __ldg(&table[i]);
-    if (page >= 0 && page < a.c.num_pages) return plane_at(a.c, page, h, j - i * a.c.page_size);
-    bad = true;
-    return -1;
-  };
-  {
-    int last = INT32_MIN;
-    for (int j0 = tid; j0 < len; j0 += kSelThreads * kAhead) {
-      int64_t w[kAhead];
+  auto where = [&](auto g, int j0, int end, int64_t (&w)[kAhead]) {
+    constexpr int G = decltype(g)::value;
+    int pg[kAhead], sl[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) w[u] = where(j0 + u * kSelThreads);
+    for (int u = 0; u < kAhead / G; ++u) {
+      const int j = min(j0 + u * G * kSelThreads, len - 1);
+      const int i = a.page_shift >= 0 ? j >> a.page_shift : j / a.c.page_size;
+      sl[u] = j - i * a.c.page_size;
+      pg[u] = __ldg(&table[i]);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead / G; ++u) {
+      const bool in = pg[u] >= 0 && pg[u] < a.c.num_pages;
+      bad = bad || !in;
+      w[u] = in && j0 + u * G * kSelThreads < end ? plane_at(a.c, pg[u], h, sl[u]) : -1;
+    }
+  };
+  // eight positions or weights of a thread; x where there is none (behind `end` within a group: any)
+  auto take = [&](auto g, const auto* plane, const int64_t (&w)[kAhead], auto x, auto (&v)[kAhead]) {
+    constexpr int G = decltype(g)::value;
+#pragma unroll
+    for (int u = 0; u < kAhead / G; ++u) {
+      if constexpr (G == 4) {
+        int4 q = make_int4(0, 0, 0, 0);
+        if (w[u] >= 0) q = *reinterpret_cast<const int4*>(plane + w[u]);
+        const int t[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (std::is_same<decltype(x), float>::value) v[u * 4 + k] = __int_as_float(t[k]);
+          else v[u * 4 + k] = t[k];
+        }
+      } else {
+        v[u] = w[u] >= 0 ? plane[w[u]] : x;
+      }
+    }
+  };
+  auto newest = [&](auto g) {
+    constexpr int G = decltype(g)::value;
+    int last = INT32_MIN;
+    for (int j0 = tid * G; j0 < len; j0 += kSelThreads * kAhead) {
+      int64_t w[kAhead];
+      int p[kAhead];
+      where(g, j0, len, w);
+      take(g, a.c.pos, w, INT32_MIN, p);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
-        if (w[u] >= 0) last = max(last, a.c.pos[w[u]]);
+        if (w[u / G] >= 0 && j0 + (u / G) * G * kSelThreads + u % G < len) last = max(last, p[u]);
     }
-    last = __reduce_max_sync(0xffffffffu, last);
+    return last;
+  };
+  using One = std::integral_constant<int, 1>;
+  using Four = std::integral_constant<int, 4>;
+  {
+    const int last = __reduce_max_sync(0xffffffffu, a.vec4 ? newest(Four{}) : newest(One{}));
     if (lane == 0) atomicMax(&s_last, last);
     if (bad) s_bad = kDevPage;
   }
@@ -235,27 +273,39 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   const int cap = a.cached;  // a multiple of 4
   const bool once = len <= cap;
   // codes of the slots [c0, c0 + cap); their first digit is counted with `count`
-  auto load_codes = [&](int c0, bool count) {
-    const int n = min(cap, (len - c0 + 3) & ~3);
-    for (int j0 = tid; j0 < n; j0 += kSelThreads * kAhead) {
+  auto load_group = [&](auto g, int c0, int n, bool count) {
+    constexpr int G = decltype(g)::value;
+    const int end = min(c0 + n, len);
+    for (int j0 = tid * G; j0 < n; j0 += kSelThreads * kAhead) {
       int64_t w[kAhead];
       int p[kAhead];
       float x[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) w[u] = j0 + u * kSelThreads < n ? where(c0 + j0 + u * kSelThreads) : -1;
+      where(g, c0 + j0, end, w);
+      take(g, a.c.pos, w, 0, p);
+      take(g, a.c.mass, w, 0.f, x);
+      unsigned c[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        p[u] = w[u] >= 0 ? a.c.pos[w[u]] : 0;
-        x[u] = w[u] >= 0 ? a.c.mass[w[u]] : 0.f;
+        const int j = j0 + (u / G) * G * kSelThreads + u % G;
+        c[u] = w[u / G] < 0 || c0 + j >= end                  ? 0u
+               : p[u] < a.sink || (int64_t)p[u] > recent_from ? 0xFFFFFFFFu
+                                                              : weight_code(x[u]);
+        if (count && c[u]) atomicAdd(&hist[c[u] >> 21], 1);
       }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (j0 + u * kSelThreads < n) {
-          const unsigned c = w[u] < 0 ? 0u : p[u] < a.sink || p[u] > recent_from ? 0xFFFFFFFFu : weight_code(x[u]);
-          codes[j0 + u * kSelThreads] = c;
-          if (count && c) atomicAdd(&hist[c >> 21], 1);
+      for (int u = 0; u < kAhead / G; ++u) {
+        const int j = j0 + u * G * kSelThreads;
+        if (j < n) {
+          if constexpr (G == 4) *reinterpret_cast<uint4*>(&codes[j]) = make_uint4(c[4 * u], c[4 * u + 1], c[4 * u + 2], c[4 * u + 3]);
+          else codes[j] = c[u];
         }
+      }
     }
+  };
+  auto load_codes = [&](int c0, bool count) {
+    const int n = min(cap, (len - c0 + 3) & ~3);
+    if (a.vec4) load_group(Four{}, c0, n, count);
+    else load_group(One{}, c0, n, count);
     return n;
   };
   int loaded = 0;
@@ -331,58 +381,62 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       s_cnt[warp][2] = tie_lo; s_cnt[warp][3] = tie_hi;
     }
     __syncthreads();
-    // every warp sums the warps before it, and all of them for the next chunk
-    int my_ties = ties, my_holes = holes, my_movers = movers;
-    for (int w = 0; w < 32; ++w) {
-      if (w == warp) { my_ties = ties; my_holes = holes; my_movers = movers; }
-      const int lo = min(n, w * span), hi = min(n, lo + span);
-      const int low = max(0, min(min(c0 + hi, keep), len) - (c0 + lo));  // its slots below the budget
-      const int kept_lo = min(s_cnt[w][2], max(0, rest - ties));
-      const int kept_hi = min(s_cnt[w][3], max(0, rest - ties - s_cnt[w][2]));
-      ties += s_cnt[w][2] + s_cnt[w][3];
-      holes += low - s_cnt[w][0] - kept_lo;
-      movers += s_cnt[w][1] + kept_hi;
+    // the sums over the warps before this one, and over all for the next chunk: lane w has warp w's counts
+    const int o_lo = s_cnt[lane][0], o_hi = s_cnt[lane][1], t_lo = s_cnt[lane][2], t_hi = s_cnt[lane][3];
+    const int w_lo = min(n, lane * span), w_hi = min(n, w_lo + span);
+    const int low = max(0, min(min(c0 + w_hi, keep), len) - (c0 + w_lo));  // its slots below the budget
+    int t_sum = t_lo + t_hi;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, t_sum, o);
+      if (lane >= o) t_sum += x;
     }
+    const int t_before = ties + t_sum - t_lo - t_hi;
+    const int kept_lo = min(t_lo, max(0, rest - t_before)), kept_hi = min(t_hi, max(0, rest - t_before - t_lo));
+    const int my_h = low - o_lo - kept_lo, my_m = o_hi + kept_hi;
+    int h_sum = my_h, m_sum = my_m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, h_sum, o), y = __shfl_up_sync(0xffffffffu, m_sum, o);
+      if (lane >= o) { h_sum += x; m_sum += y; }
+    }
+    int my_ties = __shfl_sync(0xffffffffu, t_before, warp);
+    int my_holes = holes + __shfl_sync(0xffffffffu, h_sum - my_h, warp);
+    int my_movers = movers + __shfl_sync(0xffffffffu, m_sum - my_m, warp);
+    ties += __shfl_sync(0xffffffffu, t_sum, 31);
+    holes += __shfl_sync(0xffffffffu, h_sum, 31);
+    movers += __shfl_sync(0xffffffffu, m_sum, 31);
+    const unsigned lower = (1u << lane) - 1u;
     for (int j0 = j_lo; j0 < j_hi; j0 += 128) {
       const int j = j0 + lane * 4;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (j < j_hi) v = *reinterpret_cast<const uint4*>(&codes[j]);
       const unsigned c[4] = {v.x, v.y, v.z, v.w};
-      int mine = 0;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) mine += c[u] == prefix;
-      int inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      int tie = my_ties + inc - mine;
-      my_ties += __shfl_sync(0xffffffffu, inc, 31);
-      unsigned hole = 0, mover = 0;  // of the four
+      int tie = my_ties;  // ties before this lane's slots
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const bool kept = c[u] > prefix || (c[u] == prefix && tie < rest);
+        const unsigned t = __ballot_sync(0xffffffffu, c[u] == prefix);
+        tie += __popc(t & lower);
+        my_ties += __popc(t);
+      }
+      bool hole[4], mover[4];
+      int at_h = my_holes, at_m = my_movers;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool kept = c[u] > prefix || (c[u] == prefix && tie < rest), low = c0 + j + u < keep;
         tie += c[u] == prefix;
-        const bool low = c0 + j + u < keep;
-        hole |= (unsigned)(c[u] != 0 && low && !kept) << u;
-        mover |= (unsigned)(kept && !low) << u;
+        hole[u] = c[u] != 0 && low && !kept;
+        mover[u] = kept && !low;
+        const unsigned bh = __ballot_sync(0xffffffffu, hole[u]), bm = __ballot_sync(0xffffffffu, mover[u]);
+        at_h += __popc(bh & lower);
+        at_m += __popc(bm & lower);
+        my_holes += __popc(bh);
+        my_movers += __popc(bm);
       }
-      const int both = __popc(hole) | __popc(mover) << 16;
-      int run = both;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += x;
-      }
-      int at_h = my_holes + ((run - both) & 0xffff), at_m = my_movers + ((run - both) >> 16);
-      const int all = __shfl_sync(0xffffffffu, run, 31);
-      my_holes += all & 0xffff;
-      my_movers += all >> 16;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        if (hole >> u & 1u) to[at_h++] = c0 + j + u;
-        if (mover >> u & 1u) from[at_m++] = c0 + j + u;
+        if (hole[u]) to[at_h++] = c0 + j + u;
+        if (mover[u]) from[at_m++] = c0 + j + u;
       }
     }
     __syncthreads();
@@ -544,6 +598,8 @@ int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch
   a.page_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (cache->page_size == 1 << i) a.page_shift = i;
+  a.vec4 = cache->page_size % 4 == 0 && reinterpret_cast<uintptr_t>(cache->mass) % 16 == 0 &&
+           reinterpret_cast<uintptr_t>(cache->positions) % 16 == 0;
   a.cached = max_seqlen < kMostCached ? (max_seqlen + 3) / 4 * 4 : kMostCached;
   static std::atomic<int> limits[64];
   cudaError_t e = raise_smem_limit(evict_select_kernel, kMostCached * 4, limits);
