@@ -240,7 +240,7 @@ int sage_merge_partials(const sage_tensor* outs, const float* const* lses, int n
  * so does a row all of whose visible scores are -inf.
  *   q, k, v, out, tensor_layout, is_causal, sm_scale, lse, return_lse: as sage_attn. q_offset shifts the
  *   queries' positions (the next chunk of a prompt: the number of keys before it); it may be negative.
- *   slopes: device float [Hq] or NULL. prefix_lens: device int32 [B] or NULL; only with is_causal.
+ *   softcap: 0 (none) or up to 4096. slopes: device float [Hq] or NULL. prefix_lens: device int32 [B] or NULL; only with is_causal.
  *   doc_q [B, Nq], doc_k [B, Nk]: device int32, contiguous, both or neither. A negative id is padding,
  *   which sees nothing and is seen by nothing; its rows of k and v may hold anything. Apart from
  *   padding, a key that some row of the call sees must have finite v (a weight of 0 times an infinity

@@ -362,6 +362,13 @@ int dense_impl(const sage_tensor* q, const sage_tensor* k, const sage_tensor* v,
 
 int note_cuda_failure(cudaError_t e, const char* where) { return cuda_fail(e, where); }
 
+bool softcap_ok(float softcap, float sm_scale, int head_dim) {
+  if (softcap == 0.f) return true;
+  const float scale = std::isnan(sm_scale) || sm_scale <= 0.f ? (float)(1.0 / std::sqrt((double)head_dim)) : sm_scale;
+  // (up to 4096 the capped scores' error, 2^-23 of the cap, stays below the weights' rounding)
+  return softcap > 0.f && softcap <= 4096.f && std::isfinite(4.f * scale / softcap);
+}
+
 bool make_map4(CUtensorMap* m, bool bf16, const void* base, uint64_t inner, uint64_t rows, uint64_t heads,
                uint64_t batch, uint64_t row_bytes, uint64_t head_bytes, uint64_t batch_bytes,
                uint32_t box_inner, uint32_t box_rows) {

@@ -48,6 +48,9 @@ cudaError_t raise_smem_limit(K* kernel, int bytes, std::atomic<int> (&limits)[64
 // SAGE_ERR_CUDA.
 int note_cuda_failure(cudaError_t e, const char* where);
 
+// Whether scores of this scale can be capped: softcap 0 (none), or up to 4096 with a finite scale / softcap.
+bool softcap_ok(float softcap, float sm_scale, int head_dim);
+
 // 4-d tiled map (128-byte swizzle) of 16-bit rows: dims (inner, rows, heads, batch), byte strides of
 // the last three, box (box_inner, box_rows, 1, 1); what lies outside reads as zero.
 bool make_map4(CUtensorMap* m, bool bf16, const void* base, uint64_t inner, uint64_t rows, uint64_t heads,

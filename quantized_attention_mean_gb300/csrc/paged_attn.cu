@@ -221,6 +221,7 @@ __device__ __forceinline__ void load_stage(const DecodeArgs& a, const CUtensorMa
               page >= 0 ? page : a.c.num_pages);
     return;
   }
+  const T* none = reinterpret_cast<const T*>(a.part_o);  // an address that nothing is read from
   const T* kb = static_cast<const T*>(a.c.k) + h * a.c.k_sh;
   const T* vb = static_cast<const T*>(a.c.v) + h * a.c.v_sh;
   constexpr int kUnits = DP / 8, kRowsPer = 32 / kUnits;  // rows that one pass of the warp covers
@@ -231,8 +232,8 @@ __device__ __forceinline__ void load_stage(const DecodeArgs& a, const CUtensorMa
     const int pg = __shfl_sync(0xffffffffu, page, r), sl = __shfl_sync(0xffffffffu, slot, r);
     const bool in = pg >= 0 && c * 8 < a.c.d;
     const int off = (c >> 3) * C::kChunkBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-    const T* ks = in ? kb + pg * a.c.k_sp + sl * a.c.k_st + c * 8 : kb;
-    const T* vs = in ? vb + pg * a.c.v_sp + sl * a.c.v_st + c * 8 : vb;
+    const T* ks = in ? kb + pg * a.c.k_sp + sl * a.c.k_st + c * 8 : none;
+    const T* vs = in ? vb + pg * a.c.v_sp + sl * a.c.v_st + c * 8 : none;
     if (a.load == kLoadVec) {
       cp_async16(base + off, ks, in ? 16 : 0);
       cp_async16(base + C::kTileBytes + off, vs, in ? 16 : 0);
@@ -1083,7 +1084,7 @@ int sage_paged_attn(const sage_packed* q, const sage_paged_cache* cache, const s
   bool vec = false;
   int s = make_paged_view(cache, batch, heads_kv, head_dim, dtype, tensor_layout, &a.c, &vec);
   if (s != SAGE_OK) return s;
-  if (heads_q < 1 || max_seqlen < 0 || batch > 65535 || !(softcap >= 0.f) || std::isinf(softcap))
+  if (heads_q < 1 || max_seqlen < 0 || batch > 65535 || !softcap_ok(softcap, sm_scale, head_dim))
     return SAGE_ERR_INVALID_ARG;
   if (heads_q % heads_kv) return SAGE_ERR_GQA;
   if (batch == 0) return SAGE_OK;

@@ -118,6 +118,20 @@ __device__ __forceinline__ void cap_quotient(float (&t)[16], float k, float m2, 
   for (int u = 0; u < 16; ++u) t[u] = rcpf(t[u]);
   each2(t, [&](float& p, float& q) { fma2(p, q, p, q, m2, m2, off, off); });
 }
+// Sixteen products to cap tanh(s / cap) by the polynomial.
+__device__ __forceinline__ void cap_polynomial(float (&t)[16], const CapPoly& p) {
+  float z[16], y[16];
+#pragma unroll
+  for (int u = 0; u < 16; u += 2) mul2(z[u], z[u + 1], t[u], t[u + 1], t[u], t[u + 1]);
+#pragma unroll
+  for (int u = 0; u < 16; u += 2) fma2(y[u], y[u + 1], z[u], z[u + 1], p.c[4], p.c[4], p.c[3], p.c[3]);
+#pragma unroll
+  for (int i = 2; i >= 0; --i)
+#pragma unroll
+    for (int u = 0; u < 16; u += 2) fma2(y[u], y[u + 1], y[u], y[u + 1], z[u], z[u + 1], p.c[i], p.c[i]);
+#pragma unroll
+  for (int u = 0; u < 16; u += 2) mul2(t[u], t[u + 1], t[u], t[u + 1], y[u], y[u + 1]);
+}
 // Eight products to cap tanh(s / cap) + off + line(u) by the polynomial, in four steps.
 template <typename L>
 __device__ __forceinline__ void cap_step(const CapPoly& p, int part, float (&t)[8], float (&z)[8], float (&y)[8], L line,
@@ -796,6 +810,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           step = all_left ? slope : -slope;
           base = -step * dist;
         }
+        // whether every product of the warp is within the polynomial's range
+        auto all_small = [&]() {
+          float big = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int u = 0; u < 32; u += 2)
+              big = max3(big, fabsf(__uint_as_float(s[c][u])), fabsf(__uint_as_float(s[c][u + 1])));
+          return __all_sync(0xffffffffu, big <= a.poly.most) != 0;
+        };
         if (!masked && (!BIAS || (line && fabsf(step) * 15.0f <= kSlack))) {
           // products; the cap and the scale keep their order, so their largest gives the maximum
           bool small = false;
@@ -811,15 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             t_max = capped(fmaxf(max3(cm[0], cm[1], cm[2]), cm[3]));
           }
-          if constexpr (CAP) {
-            float big = 0.f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int u = 0; u < 32; u += 2)
-                big = max3(big, fabsf(__uint_as_float(s[c][u])), fabsf(__uint_as_float(s[c][u + 1])));
-            small = __all_sync(0xffffffffu, big <= a.poly.most);
-          }
+          if constexpr (CAP) small = all_small();
           release_s();
           reframe();
           if constexpr (BIAS) weights_of(Yes{}, small, step, base);
@@ -827,6 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           have_s();
           release_s();
+          const bool small = CAP && all_small();
           // scores in base 2: capped or scaled, then biased
           auto scores = [&](auto bias_at) {
 #pragma unroll
@@ -834,7 +851,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               float t[16];
 #pragma unroll
               for (int u = 0; u < 16; ++u) t[u] = __uint_as_float(s[g >> 1][(g & 1) * 16 + u]);
-              if constexpr (CAP) cap_quotient(t, cap_in, cap_m2, a.cap2);
+              if constexpr (CAP) {
+                if (small) cap_polynomial(t, a.poly);
+                else cap_quotient(t, cap_in, cap_m2, a.cap2);
+              }
               if constexpr (BIAS) {
 #pragma unroll
                 for (int u = 0; u < 16; u += 2) {
@@ -1139,8 +1159,8 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
   if (head_dim < 1 || head_dim > 128) return SAGE_ERR_HEAD_DIM;
   if (dtype != SAGE_F16 && dtype != SAGE_BF16) return SAGE_ERR_DTYPE;
   if (tensor_layout != SAGE_HND && tensor_layout != SAGE_NHD) return SAGE_ERR_INVALID_ARG;
-  if (batch < 0 || heads_q < 1 || heads_kv < 1 || seqlen_q < 0 || seqlen_k < 0 || !(softcap >= 0.f) ||
-      std::isinf(softcap) || (prefix_lens && !is_causal) || !doc_q != !doc_k || (return_lse && !lse))
+  if (batch < 0 || heads_q < 1 || heads_kv < 1 || seqlen_q < 0 || seqlen_k < 0 ||
+      !softcap_ok(softcap, sm_scale, head_dim) || (prefix_lens && !is_causal) || !doc_q != !doc_k || (return_lse && !lse))
     return SAGE_ERR_INVALID_ARG;
   if (heads_q % heads_kv) return SAGE_ERR_GQA;
   for (const void* p : {(const void*)lse, (const void*)slopes, (const void*)prefix_lens, (const void*)doc_q, (const void*)doc_k})
@@ -1196,9 +1216,8 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
     const double c = tanh_c[i] * scaled;
     a.poly.c[i] = (float)c;
     // (a coefficient near the ends of fp32's range: the quotient)
-    if (!(std::fabs(c) > 1e-30 && std::fabs(c) < 1e30)) a.poly.most = -1.f;
+    if (!(std::fabs(c) > 1e-37 && std::fabs(c) < 1e30)) a.poly.most = -1.f;
   }
-  if (!(a.poly.most < 1e6f)) a.poly.most = -1.f;
   a.cap_k = softcap > 0.f ? (float)(2.0 * 1.4426950408889634 * scale / softcap) : 0.f;
   a.o = out->data; a.o_sb = view[3].sb; a.o_sh = view[3].sh; a.o_sn = view[3].sn;
   a.lse = return_lse ? lse : nullptr;

@@ -13,7 +13,7 @@ import torch
 HALF_STEP = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
 
 
-def attend(q, k, v, sm_scale, cap=0.0, bias=None, seen=None, dtype=torch.bfloat16):
+def attend(q, k, v, sm_scale, cap=0.0, bias=None, seen=None, dtype=torch.bfloat16, relative_cap=False):
     """q [..., M, d], k / v [..., N, d] (any 16-bit or float type), bias / seen [..., M, N].
     Returns dict(out, lse, p, out_tol, lse_tol, p_tol) in float64."""
     q, k, v = q.double(), k.double(), v.double()
@@ -22,7 +22,9 @@ def attend(q, k, v, sm_scale, cap=0.0, bias=None, seen=None, dtype=torch.bfloat1
     ds = size * (q.shape[-1] + 4) * 2.0 ** -23
     if cap:
         s = cap * torch.tanh(s / cap)
-        ds = ds + cap * 2.0 ** -21      # tanh to two steps of its range, the scaling around it
+        # tanh to two steps of its range, the scaling around it; relative_cap: scores far below the cap, which
+        # are held to eight steps of themselves
+        ds = ds + (s.abs() * 2.0 ** -20 if relative_cap else cap * 2.0 ** -21)
     if bias is not None:
         ds = ds + (bias.abs() + s.abs()) * 2.0 ** -22
         s = s + bias

@@ -34,7 +34,7 @@ def visible(nq, nk, B, causal, offset, prefix, dq, dk):
 
 
 def check(B, hq, hkv, nq, nk, d, dtype, layout="HND", causal=False, cap=0.0, bias=False, prefix=None, dq=None, dk=None,
-          offset=0, scale=None, q=None, k=None, v=None, place=None, clean=None, seed=0):
+          offset=0, scale=None, q=None, k=None, v=None, place=None, clean=None, seed=0, relative_cap=False):
     import quantized_attention_mean_gb300 as qa
     g = torch.Generator().manual_seed(seed + nq + d)
     q = (torch.randn(B, hq, nq, d, generator=g) * 2).to(dtype) if q is None else q
@@ -61,7 +61,7 @@ def check(B, hq, hkv, nq, nk, d, dtype, layout="HND", causal=False, cap=0.0, bia
     if bias:
         dist = (torch.arange(nq)[:, None] + offset - torch.arange(nk)).abs().double()
         b = (-slopes.double()[:, None, None] * dist)[None].to(DEV)
-    r = attend(q.to(DEV), kk, vv, d ** -0.5 if scale is None else scale, cap, b, seen.expand(B, hq, nq, nk).to(DEV), dtype)
+    r = attend(q.to(DEV), kk, vv, d ** -0.5 if scale is None else scale, cap, b, seen.expand(B, hq, nq, nk).to(DEV), dtype, relative_cap)
     o = out if layout == "HND" else out.transpose(1, 2)
     assert_close(o, r["out"], r["out_tol"], "out")
     assert_close(lse, r["lse"], r["lse_tol"], "lse")
@@ -178,6 +178,13 @@ def test_large_scores_and_growing_maximum():
     check(1, 1, 1, 130, n, d, F, q=q.half(), k=k.half(), v=v.half(), scale=1.0)
     check(1, 1, 1, 130, n, d, H, q=q.bfloat16(), k=k.bfloat16(), v=v.bfloat16(), scale=1.0, bias=True)
     check(1, 1, 1, 130, n, d, F, q=q.half(), k=k.half(), v=v.half(), scale=1.0, cap=50.0, causal=True, offset=n)
+
+
+@pytest.mark.parametrize("cap,relative", [(1000.0, True), (4096.0, False), (1.0, False), (1e-3, False)])
+def test_caps_from_tiny_to_large(cap, relative):
+    for d, dtype in ((64, F), (128, H)):
+        check(1, 2, 1, 300, 300, d, dtype, cap=cap, relative_cap=relative)
+        check(1, 2, 1, 300, 300, d, dtype, cap=cap, causal=True, bias=True, relative_cap=relative)
 
 
 def test_strided_and_broadcast_inputs():

@@ -53,6 +53,9 @@ def test_attn_checks():
         qa.paged_attn(q.bfloat16(), max_seq_len=32, **c)
     with pytest.raises(ValueError, match="out must"):
         qa.paged_attn(q, max_seq_len=32, out=torch.zeros(3, 4, 32, dtype=torch.float16), **c)
+    for n in (-1, 2 ** 31):
+        with pytest.raises(ValueError, match="CUDA|max_seq_len"):
+            qa.paged_attn(q, max_seq_len=n, **c)
     with pytest.raises(ValueError, match="slopes must"):
         qa.paged_attn(q, max_seq_len=32, slopes=torch.zeros(5), **c)
     with pytest.raises(ValueError, match="q_positions must"):

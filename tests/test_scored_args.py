@@ -40,6 +40,9 @@ def test_mask_checks(on_cuda):
         qa.scored_attn(q, k, k, prefix_lens=torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError, match="prefix_lens must"):
         qa.scored_attn(q, k, k, is_causal=True, prefix_lens=torch.zeros(2, dtype=torch.int32))
+    for offset in (2 ** 31, -2 ** 31):
+        with pytest.raises(ValueError, match="q_offset"):
+            qa.scored_attn(q, k, k, q_offset=offset)
     with pytest.raises(ValueError, match="slopes must"):
         qa.scored_attn(q, k, k, slopes=torch.zeros(2))
 
@@ -73,7 +76,7 @@ def test_c_statuses(lib):
     assert call(lib, layout=2) == 1
     assert call(lib, hq=3) == 5
     assert call(lib, hq=0) == 1 and call(lib, hkv=0) == 1 and call(lib, nq=-1) == 1 and call(lib, nk=-1) == 1
-    for cap in (-1.0, float("nan"), float("inf")):
+    for cap in (-1.0, float("nan"), float("inf"), 4097.0, 1e-39):
         assert call(lib, cap=cap) == 1
     assert call(lib, ret=1) == 1                          # return_lse without an lse buffer
     assert call(lib, prefix=FAKE) == 1                    # a prefix without a causal mask
