@@ -242,9 +242,10 @@ int sage_merge_partials(const sage_tensor* outs, const float* const* lses, int n
  *   queries' positions (the next chunk of a prompt: the number of keys before it); it may be negative.
  *   softcap: 0 (none) or up to 4096. slopes: device float [Hq] or NULL. prefix_lens: device int32 [B] or NULL; only with is_causal.
  *   doc_q [B, Nq], doc_k [B, Nk]: device int32, contiguous, both or neither. A negative id is padding,
- *   which sees nothing and is seen by nothing; its rows of k and v may hold anything. Apart from
- *   padding, a key that some row of the call sees must have finite v (a weight of 0 times an infinity
- *   is NaN in the rows that do not see it).
+ *   which sees nothing and is seen by nothing. Rows of k and v that are padding, or that lie behind the
+ *   last key any row sees under the causal and prefix masks (a buffer longer than what it
+ *   holds), may hold anything; every other row of v must be finite (a weight of 0 times an infinity is NaN
+ *   in the rows that do not see it).
  *   workspace: sage_scored_attn_workspace_size() bytes; `packed` != 0 where q, k and v all have 16-byte
  *   aligned rows (address, and strides and head_dim multiples of 8 elements; no zero stride of a
  *   dimension longer than 1) and need no padded copy there.

@@ -323,7 +323,7 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
 
 // What the roles of a CTA agree on, as words of shared memory: each role loads what it uses (kept in
 // registers across the split they spilled, and with the shared memory taken a spill is an L2 access).
-enum Word : uint32_t { kWTmem = 0, kWAbort = 4, kWJ0 = 16, kWTiles = 20, kWTilesA = 24, kWPrefix = 28, kWRed = 32, kWSeq = 48, kWSplit = 52, kWLeft = 56 };
+enum Word : uint32_t { kWTmem = 0, kWAbort = 4, kWJ0 = 16, kWTiles = 20, kWTilesA = 24, kWPrefix = 28, kWRed = 32, kWSeq = 48, kWSplit = 52, kWLeft = 56, kWSeen = 60, kWClean = 64 };
 __device__ __forceinline__ int lds(uint32_t at) {
   int v;
   asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     const int b = (int)blockIdx.z / a.splits, split = (int)blockIdx.z - b * a.splits;
     const int rows = min(256, a.nq - q0), prefix = a.prefix ? __ldg(&a.prefix[b]) : 0;
-    int lo = 0, hi = (limit_of(q0 + rows - 1, prefix) + 127) / 128;
+    const int seen = limit_of(q0 + rows - 1, prefix);  // (what the last row sees, the rows before it see in part)
+    int lo = 0, hi = (seen + 127) / 128;
     const int hi_a = (limit_of(q0 + min(rows, 128) - 1, prefix) + 127) / 128;
     if (a.doc_q) {
       int* red = reinterpret_cast<int*>(sm + C::kOffMisc + kWRed);
@@ -451,6 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       sts(misc + kWLeft, BIAS ? (int)max(0LL, min(at + 1 - lo, (long long)(hi - lo))) : 0);
       sts(misc + kWPrefix, prefix);
       sts(misc + kWSeq, b);
+      // V rows that no row of this CTA sees may hold anything: padding, and what lies behind the last key seen
+      sts(misc + kWSeen, seen);
+      sts(misc + kWClean, a.doc_k != nullptr || (seen < a.nk && seen < hi * 128));
       sts(misc + kWSplit, split);
     }
   }
@@ -495,21 +499,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == 11) {
-      // ================================== padding: its V rows become zero (they may hold anything)
-      if (a.doc_k) {
+      // ================================== V rows of padding and behind the last key seen become zero
+      if (lds(misc + kWClean)) {
         const int n_tiles = lds(misc + kWTiles), j0 = lds(misc + kWJ0), b = lds(misc + kWSeq);
-        const int left = lds(misc + kWLeft);
+        const int left = lds(misc + kWLeft), seen = lds(misc + kWSeen);
         bool ok = true;
         for (int j = 0; j < n_tiles && ok; ++j) {
           const int sv = j % C::kVStages;
           ok = warp_wait(v_full + 8 * sv, (j / C::kVStages) & 1, abort_at);
           if (!ok) break;
           const int tile = j0 + tile_of(j, left);
-          const DocTile t = a.doc_tiles[(int64_t)b * a.k_tiles + tile];
-          if (t.pad) {
+          const bool pad = a.doc_k && a.doc_tiles[(int64_t)b * a.k_tiles + tile].pad;
+          if (pad || seen < min(a.nk, tile * 128 + 128)) {
             for (int i = 0; i < 4; ++i) {
               const int row = i * 32 + lane, key = tile * 128 + row;
-              if (key < a.nk && __ldg(&a.doc_k[(int64_t)b * a.nk + key]) < 0)
+              if (key < a.nk && (key >= seen || (pad && __ldg(&a.doc_k[(int64_t)b * a.nk + key]) < 0)))
                 for (int c = 0; c < C::kChunks; ++c)
                   for (int u = 0; u < 8; ++u)
                     *reinterpret_cast<uint4*>(sm + C::kOffV + sv * C::kVBytes + c * 16384 + row * 128 + u * 16) =
@@ -529,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tmem = lds(misc + kWTmem);
       const uint32_t fmt = BF16 ? 1 : 0;
       const uint32_t id_qk = make_idesc(1, fmt, fmt, 128, 128), id_pv = make_idesc(1, fmt, fmt, 128, DP) | kIdescTransB;
-      const uint32_t v_in = a.doc_k ? v_clean : v_full;
+      const uint32_t v_in = lds(misc + kWClean) ? v_clean : v_full;
       // scores of query tile x against key tile j into S buffer sb
       auto issue_qk = [&](int x, int j, int sb) {
         const uint32_t st = (uint32_t)j % C::kKStages;

@@ -41,7 +41,8 @@ def scored_attn(q, k, v, tensor_layout="HND", is_causal=False, sm_scale=None, so
     Key j is visible to query i when (not is_causal, or j <= i + q_offset, or j < prefix_lens[b]) and, with
     documents, doc_ids[b, i] == doc_ids_k[b, j] >= 0. ``slopes`` fp32 [Hq]; ``prefix_lens`` int32 [B], with
     is_causal; ``doc_ids`` int32 [B, Nq] and ``doc_ids_k`` int32 [B, Nk] (default: doc_ids, Nq == Nk). A negative
-    id is padding, whose rows of k and v may hold anything. ``q_offset``: how many keys lie before the first
+    id is padding. Rows of k and v that are padding, or that lie behind the last key any row sees under the causal
+    and prefix masks, may hold anything; all others must be finite in v. ``q_offset``: how many keys lie before the first
     query (the next chunk of a prompt). A row that sees no key gives 0 and lse -inf.
     Returns out, plus lse [B, Hq, Nq] fp32 if return_lse."""
     _check_dense_args(q, k, v, tensor_layout, out, lse, return_lse, workspace)

@@ -168,6 +168,21 @@ def test_keys_ahead_may_be_infinite_scores():
     assert torch.equal(a[:, :, :200], b[:, :, :200]) and torch.isnan(b[:, :, 200:]).any()
 
 
+@pytest.mark.parametrize("nq,nk,offset,prefix", [(100, 300, 50, None), (300, 700, 77, None), (5, 4000, 2100, None),
+                                                 (100, 300, 0, [170]), (260, 300, -20, None)])
+@pytest.mark.parametrize("d,dtype", [(64, H), (128, F)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_keys_behind_the_last_seen_may_hold_anything(nq, nk, offset, prefix, d, dtype, bias):
+    # a buffer longer than the tokens it holds: the rest of the last tile is garbage
+    g = torch.Generator().manual_seed(7)
+    k, v = (torch.randn(1, 1, nk, d, generator=g).to(dtype) for _ in "kv")
+    held = max(nq + offset, *(prefix or [0]))
+    clean = v.clone()
+    clean[:, :, held:] = 0
+    k[:, :, held:], v[:, :, held::2], v[:, :, held + 1::2] = math.nan, math.nan, -math.inf
+    check(1, 2, 1, nq, nk, d, dtype, causal=True, offset=offset, prefix=prefix, bias=bias, k=k, v=v, clean=clean)
+
+
 def test_large_scores_and_growing_maximum():
     # scores rise along the keys by far more than the frame allows, then fall
     n, d = 700, 64
@@ -185,6 +200,23 @@ def test_caps_from_tiny_to_large(cap, relative):
     for d, dtype in ((64, F), (128, H)):
         check(1, 2, 1, 300, 300, d, dtype, cap=cap, relative_cap=relative)
         check(1, 2, 1, 300, 300, d, dtype, cap=cap, causal=True, bias=True, relative_cap=relative)
+
+
+def test_slopes_of_either_sign():
+    # a negative slope favours distant keys: the maximum moves with every tile
+    import quantized_attention_mean_gb300 as qa
+    g = torch.Generator().manual_seed(8)
+    for d, dtype in ((64, F), (128, H)):
+        q, k, v = (torch.randn(1, 4, 600, d, generator=g).to(dtype) for _ in "qkv")
+        slopes = torch.tensor([-0.3, -0.01, 0.0, 2.0])
+        dist = (torch.arange(600)[:, None] - torch.arange(600)).abs().double()
+        b = (-slopes.double()[:, None, None] * dist)[None].to(DEV)
+        for causal in (False, True):
+            out, lse = qa.scored_attn(*(t.to(DEV) for t in (q, k, v)), is_causal=causal, slopes=slopes.to(DEV), return_lse=True)
+            seen = visible(600, 600, 1, causal, 0, None, None, None)[:, None].expand(1, 4, 600, 600).to(DEV)
+            r = attend(*(t.to(DEV) for t in (q, k, v)), d ** -0.5, 0.0, b, seen, dtype)
+            assert_close(out, r["out"], r["out_tol"], "out")
+            assert_close(lse, r["lse"], r["lse_tol"], "lse")
 
 
 def test_strided_and_broadcast_inputs():
