@@ -263,8 +263,8 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
  * k, v: device FP16/BF16 [num_pages, Hkv, page_size, d] (HND) or [num_pages, page_size, Hkv, d] (NHD), any
  * strides of the first three dimensions (k_stride, v_stride, in that order), channel stride 1.
  * Token slot t of sequence b lies in page page_table[b * table_stride + t / page_size] at
- * t % page_size; page_table has max_pages entries per row, of which only those of held tokens are
- * read. seq_lens: device int32 [batch], the tokens each sequence holds.
+ * t % page_size; page_table has max_pages entries per row (at most 2^31 - 65536 slots), of which only those
+ * of held tokens are read. seq_lens: device int32 [batch], the tokens each sequence holds.
  * mass: device float [num_pages, Hkv, page_size] contiguous, the attention weight each token has drawn,
  * or NULL. positions: device int32 of the same shape, the tokens' positions, or NULL (the slot).
  * Errors found on the device: SAGE_ERR_SEQLENS (a length outside of [0, max_seqlen] or of the table's
@@ -318,8 +318,10 @@ int sage_paged_append(const sage_packed* k, const sage_packed* v, const sage_pag
  * position stay, then those with the largest mass (ties: the lowest slot; NaN counts as -inf). Kept
  * tokens from slot `budget` on move, in order, into the freed slots below it, with their mass and
  * position; slots from `budget` on keep what they held. new_lens: device int32 [batch], written
- * min(seq_len, budget); not seq_lens itself. cache->mass and cache->positions are needed. Each page
- * belongs to one sequence. budget >= 1, sink + recent <= budget. */
+ * min(seq_len, budget), or seq_len where an error is found: that sequence is left as it was; it must not
+ * overlap seq_lens. cache->mass and cache->positions are needed. Each page belongs to one sequence.
+ * budget >= 1, sink + recent <= budget (where positions repeat and more than `budget` tokens would
+ * have to stay, those of the lowest slots do). */
 size_t sage_paged_evict_workspace_size(int batch, int heads_kv, int max_seqlen, int budget);
 int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch, int heads_kv,
                      int max_seqlen, int head_dim, int dtype, int tensor_layout, int budget, int sink,

@@ -12,6 +12,7 @@
 namespace sage {
 
 constexpr int kDevPage = 13;  // SAGE_ERR_PAGE
+constexpr int64_t kMostSlots = 0x7fff0000;  // of a sequence: the kernels look some thousand slots past the last in 32 bits
 
 struct PagedView {
   void* k; int64_t k_sp, k_sh, k_st;  // element strides of (page, head, token slot)

@@ -14,14 +14,14 @@ int make_paged_view(const sage_paged_cache* c, int batch, int heads_kv, int head
   if (dtype != SAGE_F16 && dtype != SAGE_BF16) return SAGE_ERR_DTYPE;
   if (layout != SAGE_HND && layout != SAGE_NHD) return SAGE_ERR_INVALID_ARG;
   if (batch < 0 || heads_kv < 1 || heads_kv > 65535 || c->num_pages < 0 || c->page_size < 1 || c->max_pages < 0 ||
-      (int64_t)c->max_pages * c->page_size > 0x7fffffffLL)
+      (int64_t)c->max_pages * c->page_size > kMostSlots)
     return SAGE_ERR_INVALID_ARG;
   PagedView v{};
   v.batch = batch; v.hkv = heads_kv; v.d = head_dim;
   v.page_size = c->page_size; v.num_pages = c->num_pages; v.max_pages = c->max_pages;
   if (batch > 0) {
     auto off = [](const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; };
-    if (!c->page_table || !c->seq_lens || off(c->page_table, 4) || off(c->seq_lens, 4) || off(c->mass, 4) ||
+    if ((!c->page_table && c->max_pages > 0) || !c->seq_lens || off(c->page_table, 4) || off(c->seq_lens, 4) || off(c->mass, 4) ||
         off(c->positions, 4) || c->table_stride < 0)
       return SAGE_ERR_INVALID_ARG;
     if (c->num_pages > 0 && (!c->k || !c->v)) return SAGE_ERR_INVALID_ARG;
@@ -197,9 +197,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
   __syncthreads();
   const int keep = a.budget;
-  if (h == 0 && tid == 0) a.new_lens[b] = len < 0 ? a.c.lens[b] : min(len, keep);
   if (len <= keep) {  // nothing to drop (or a length that is refused)
-    if (tid == 0) { a.count[me] = 0; a.block_err[me] = s_bad; }
+    if (tid == 0) {
+      a.count[me] = 0;
+      a.block_err[me] = s_bad;
+      if (h == 0) a.new_lens[b] = a.c.lens[b];
+    }
     return;
   }
   const int* table = a.c.table + b * a.c.table_stride;
@@ -265,6 +268,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     if (bad) s_bad = kDevPage;
   }
   __syncthreads();
+  if (h == 0 && tid == 0) a.new_lens[b] = s_bad ? len : keep;  // (every head reads the same pages)
   if (s_bad) {
     if (tid == 0) { a.count[me] = 0; a.block_err[me] = s_bad; }
     return;
@@ -577,9 +581,11 @@ int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch
   if (max_seqlen < 0 || batch > 65535 || budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget)
     return SAGE_ERR_INVALID_ARG;
   if (batch == 0) return SAGE_OK;
-  if (!new_lens || new_lens == cache->seq_lens || reinterpret_cast<uintptr_t>(new_lens) % 4 || !cache->mass ||
-      !cache->positions)
+  if (!new_lens || reinterpret_cast<uintptr_t>(new_lens) % 4 || !cache->mass || !cache->positions)
     return SAGE_ERR_INVALID_ARG;
+  // (seq_lens is read by the CTAs of every head, after the first has written new_lens)
+  const uintptr_t n0 = reinterpret_cast<uintptr_t>(new_lens), l0 = reinterpret_cast<uintptr_t>(cache->seq_lens);
+  if (n0 < l0 + 4 * (size_t)batch && l0 < n0 + 4 * (size_t)batch) return SAGE_ERR_INVALID_ARG;
   EvictLayout L;
   if (!evict_layout(batch, heads_kv, max_seqlen, budget, &L)) return SAGE_ERR_INVALID_ARG;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < L.total)

@@ -38,10 +38,11 @@ class _Launch:
     def __init__(self, index, stream):
         self.contexts = None
         if stream is not None or torch._C._cuda_getDevice() != index:
-            self.contexts = contextlib.ExitStack()
-            self.contexts.enter_context(torch.cuda.device(index))
-            if stream is not None:
-                self.contexts.enter_context(torch.cuda.stream(stream))
+            with contextlib.ExitStack() as stack:
+                stack.enter_context(torch.cuda.device(index))
+                if stream is not None:
+                    stack.enter_context(torch.cuda.stream(stream))
+                self.contexts = stack.pop_all()
         self.stream = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
     def __enter__(self):
@@ -221,7 +222,8 @@ def paged_evict(k_cache, v_cache, mass, key_positions, page_table, seq_lens, bud
     new lengths int32 [B]. For each key/value head, tokens at positions below ``sink`` or among the last
     ``recent`` positions stay, then those with the largest ``mass`` (ties: the lowest slot). Kept tokens
     behind the budget move into the freed slots, with their mass and position; the slots behind the
-    budget keep what they held, and their pages are free."""
+    budget keep what they held, and their pages are free. A sequence with a bad length or page is left as it was, its
+    length too (``read_device_status``)."""
     if mass is None or key_positions is None:
         raise ValueError("eviction needs the mass and key_positions planes")
     cache, hkv, d, index = _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions,

@@ -123,6 +123,142 @@ def test_decode_accumulates_weights(hq, hkv, d, cap, bound):
     assert_close(mass, want, tol, "mass")
 
 
+def test_decode_mass_of_shared_and_odd_pages():
+    # a prompt's pages shared by three sequences, pages of six slots, positions of their own for the bias
+    import quantized_attention_mean_gb300 as qa
+    hq, hkv, d, page = 4, 2, 64, 6
+    c = ref.make_cache([100, 100, 100], hkv, d, page, torch.float16, seed=2)
+    c["table"][1, :8] = c["table"][0, :8]
+    c["table"][2, :8] = c["table"][0, :8]
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(3, hq, d, generator=g).half()
+    kpos = torch.randint(0, 200, (c["k"].shape[0], hkv, page), generator=g, dtype=torch.int32)
+    qpos = torch.tensor([200, 210, 300], dtype=torch.int32)
+    slopes = torch.tensor([0.01, 0.02, -0.01, 0.0])
+    G, mass = on_gpu(c), torch.zeros(c["k"].shape[0], hkv, page, device=DEV)
+    out = qa.paged_attn(q.to(DEV), G["k"], G["v"], G["table"], G["lens"], 100, slopes=slopes.to(DEV),
+                        key_positions=kpos.to(DEV), q_positions=qpos.to(DEV), mass=mass)
+    r = decode_reference(c, q, d ** -0.5, 0.0, slopes, kpos, qpos, hkv)
+    assert_close(out, r["out"], r["out_tol"], "out")
+    want = torch.zeros(mass.shape, dtype=torch.float64)
+    tol = want + 1e-7
+    for (b, h), p in r["p"].items():
+        at, s = ref.place(c, b, 100)
+        want[at, h, s] += p
+        tol[at, h, s] += r["p_tol"][b, h] + 3 * 2.0 ** -23       # sums of up to six, each below 8: two additions
+    assert_close(mass, want, tol, "mass")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [8, 24])
+@pytest.mark.parametrize("layout", ["HND", "NHD"])
+def test_decode_pages_of_eight_row_blocks(d, page, layout):
+    import quantized_attention_mean_gb300 as qa
+    lens = [1, 8, 9, 23, 24, 25, 500]
+    c = ref.make_cache(lens, 2, d, page, torch.bfloat16, layout, seed=d + page)
+    q = torch.randn(len(lens), 6, d, generator=torch.Generator().manual_seed(1)).bfloat16()
+    G = on_gpu(c)
+    for bound in (500, 10 ** 5):
+        out = qa.paged_attn(q.to(DEV), G["k"], G["v"], G["table"], G["lens"], bound, tensor_layout=layout)
+        r = decode_reference(c, q, d ** -0.5, hkv=2)
+        assert_close(out, r["out"], r["out_tol"], "out")
+
+
+def test_empty_cache_in_place_and_from_another_page():
+    import quantized_attention_mean_gb300 as qa
+    # a cache without pages
+    k = torch.empty(0, 2, 16, 64, dtype=torch.float16, device=DEV)
+    table, lens = torch.zeros(2, 0, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    q = torch.randn(2, 4, 64, dtype=torch.float16, device=DEV)
+    for bound in (0, 10 ** 5):
+        out, lse = qa.paged_attn(q, k, k, table, lens, bound, return_lse=True)
+        assert (out == 0).all() and (lse == -math.inf).all()
+    # the output over the query
+    c = ref.make_cache([300, 40], 2, 64, 16, torch.float16, room=16)
+    G = on_gpu(c)
+    for bound in (300, 10 ** 5):
+        want = qa.paged_attn(q, G["k"], G["v"], G["table"], G["lens"], bound)
+        both = q.clone()
+        qa.paged_attn(both, G["k"], G["v"], G["table"], G["lens"], bound, out=both)
+        assert torch.equal(both, want)
+    # a sequence's first page appended to both, as a shared prefix is copied
+    page = int(c["table"][0, 0])
+    src = [G[n][page].transpose(0, 1).repeat(2, 1, 1) for n in "kv"]
+    view = [G[n][page].transpose(0, 1) for n in "kv"]
+    cu = torch.tensor([0, 16, 32], dtype=torch.int32, device=DEV)
+    other = [G[n].clone() for n in "kv"]
+    qa.paged_append(*src, *other, G["table"], G["lens"], cu_seqlens=cu)
+    one = torch.tensor([0, 16, 16], dtype=torch.int32, device=DEV)
+    two = torch.tensor([0, 0, 16], dtype=torch.int32, device=DEV)
+    qa.paged_append(*view, G["k"], G["v"], G["table"], G["lens"], cu_seqlens=one)
+    qa.paged_append(*view, G["k"], G["v"], G["table"], G["lens"], cu_seqlens=two)
+    assert torch.equal(G["k"], other[0]) and torch.equal(G["v"], other[1])
+
+
+def test_append_and_evict_in_a_graph():
+    import quantized_attention_mean_gb300 as qa
+    c = ref.make_cache([70, 20], 2, 64, 16, torch.float16, room=2)
+    shape = (c["k"].shape[0], 2, 16)
+    mass0 = torch.rand(shape, device=DEV)
+    pos0 = torch.zeros(shape, dtype=torch.int32, device=DEV)
+    k = torch.randn(2, 2, 64, dtype=torch.float16, device=DEV)
+    ws = qa.alloc_workspace(qa.paged_evict_workspace_bytes(2, 2, 80, 32), DEV)
+
+    def state():
+        G = on_gpu(c)
+        return [G["k"], G["v"], mass0.clone(), pos0.clone(), G["table"], G["lens"]]
+
+    def step(s):
+        qa.paged_append(k, k, s[0], s[1], s[4], s[5], mass=s[2], key_positions=s[3])
+        return qa.paged_evict(s[0], s[1], s[2], s[3], s[4], s[5] + 1, 32, 80, recent=8, workspace=ws)
+
+    eager, s = state(), state()
+    want = step(eager)
+    first = [t.clone() for t in s]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        new = step(s)
+    for _ in range(2):
+        for t, f in zip(s, first):
+            t.copy_(f)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(new, want) and all(torch.equal(x, y) for x, y in zip(s, eager))
+
+
+def test_a_cache_past_32_bits():
+    # pages whose rows lie more than 2^32 elements into the cache
+    import quantized_attention_mean_gb300 as qa
+    pages, hkv, page, d = 300000, 1, 128, 128                    # 9.8 GB each
+    k = torch.empty(pages, hkv, page, d, dtype=torch.float16, device=DEV)
+    v = torch.empty_like(k)
+    mass = torch.zeros(pages, hkv, page, device=DEV)
+    pos = torch.zeros(pages, hkv, page, dtype=torch.int32, device=DEV)
+    at = torch.tensor([299999, 1, 299998, 270000], dtype=torch.int32)
+    small = ref.make_cache([400], hkv, d, page, torch.float16, spare=0)
+    small["table"][0] = torch.arange(4, dtype=torch.int32)
+    g = torch.Generator().manual_seed(1)
+    new = [torch.randn(400, hkv, d, generator=g).half() for _ in "kv"]
+    table, lens = at[None].to(DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 400], dtype=torch.int32, device=DEV)
+    qa.paged_append(*(t.to(DEV) for t in new), k, v, table, lens, cu_seqlens=cu, mass=mass, key_positions=pos)
+    p, s = ref.place(small, 0, 400)
+    for which, t in zip("kv", new):
+        small[which][p, :, s] = t
+    q = torch.randn(1, 4, d, generator=g).half()
+    out = qa.paged_attn(q.to(DEV), k, v, table, lens + 400, 400, mass=mass)
+    r = decode_reference(small, q, d ** -0.5, hkv=hkv)
+    assert_close(out, r["out"], r["out_tol"], "out")
+    held = at.long().to(DEV)
+    few, fp = mass[held].cpu(), pos[held].cpu()
+    qa.paged_evict(k, v, mass, pos, table, lens + 400, 100, 400, recent=10)
+    ref.evict(small, few, fp, 100, 0, 10)
+    assert torch.equal(mass[held].cpu(), few) and torch.equal(pos[held].cpu(), fp)
+    keep, ks = ref.place(small, 0, 100)
+    assert torch.equal(k[held].cpu()[keep, :, ks], small["k"][keep, :, ks])
+    assert torch.equal(v[held].cpu()[keep, :, ks], small["v"][keep, :, ks])
+
+
 def test_decode_masked_garbage_and_nan():
     # slots behind a sequence's end and unused pages hold NaN: nothing of them may show
     import quantized_attention_mean_gb300 as qa
@@ -273,6 +409,36 @@ def test_evict(lens, hkv, d, page, dtype, layout, budget, sink, recent, ties):
     assert torch.equal(G["k"].cpu(), c["k"]) and torch.equal(G["v"].cpu(), c["v"])
 
 
+# (longer than the codes that shared memory holds; planes read four slots at a time and one at a time)
+@pytest.mark.parametrize("page,budget", [(64, 30000), (6, 1000)])
+def test_evict_long_sequences(page, budget):
+    import quantized_attention_mean_gb300 as qa
+    lens, hkv, d = [120001, 50000, 49152], 1, 8
+    c = ref.make_cache(lens, hkv, d, page, torch.float16, seed=3)
+    g = torch.Generator().manual_seed(6)
+    shape = (c["k"].shape[0], hkv, page)
+    mass = torch.randint(0, 5000, shape, generator=g).float()    # ties across the chunks
+    pos = torch.zeros(shape, dtype=torch.int32)
+    for b, n in enumerate(lens):
+        p, s = ref.place(c, b, n)
+        pos[p, 0, s] = torch.arange(n, dtype=torch.int32)
+    G, gm, gp = on_gpu(c), mass.to(DEV), pos.to(DEV)
+    new = qa.paged_evict(G["k"], G["v"], gm, gp, G["table"], G["lens"], budget, max(lens), sink=4, recent=300)
+    want = ref.evict(c, mass, pos, budget, 4, 300)
+    assert torch.equal(new.cpu(), want) and torch.equal(gp.cpu(), pos) and torch.equal(gm.cpu(), mass)
+    assert torch.equal(G["k"].cpu(), c["k"]) and torch.equal(G["v"].cpu(), c["v"])
+
+
+def test_evict_where_more_would_have_to_stay():
+    import quantized_attention_mean_gb300 as qa
+    c = ref.make_cache([50], 1, 16, 8, torch.float16)
+    shape = (c["k"].shape[0], 1, 8)
+    mass, pos = torch.rand(shape, generator=torch.Generator().manual_seed(1)), torch.zeros(shape, dtype=torch.int32)
+    G, gm, gp = on_gpu(c), mass.to(DEV), pos.to(DEV)             # every token at position 0
+    new = qa.paged_evict(G["k"], G["v"], gm, gp, G["table"], G["lens"], 20, 50, sink=1)
+    assert new.tolist() == [20] and torch.equal(G["k"].cpu(), c["k"]) and torch.equal(gm.cpu(), mass)
+
+
 def test_evict_reports_bad_lengths_and_pages():
     import quantized_attention_mean_gb300 as qa
     c = ref.make_cache([60, 60], 2, 64, 16, torch.float16)
@@ -290,6 +456,17 @@ def test_evict_reports_bad_lengths_and_pages():
         assert qa.read_device_status(ws) == (12 if what == "length" else 13)
         used = G["table"][0, :3].long()
         assert torch.equal(k[used], G["k"][used])                 # the bad sequence is left as it was
+
+
+def test_evict_leaves_the_length_of_a_bad_sequence():
+    import quantized_attention_mean_gb300 as qa
+    c = ref.make_cache([60, 60, 60], 2, 64, 16, torch.float16)
+    G = on_gpu(c)
+    shape = (c["k"].shape[0], 2, 16)
+    mass, pos = torch.rand(shape, device=DEV), torch.zeros(shape, dtype=torch.int32, device=DEV)
+    lens, table = G["lens"].clone(), G["table"].clone()
+    lens[0], table[1, 3] = 65, -1
+    assert qa.paged_evict(G["k"], G["v"], mass, pos, table, lens, 20, 60).tolist() == [65, 60, 20]
 
 
 def test_serving_loop_with_eviction():

@@ -172,6 +172,15 @@ def test_c_append_and_evict_statuses(lib):
     assert evict(batch=0) == 0
 
 
+def test_slots_and_lengths_at_the_ends(lib):
+    assert attn(lib, c_cache(size=32768, width=65535)) == 1      # 2^31 - 32768 slots: the kernels look past the last
+    assert attn(lib, c_cache(size=32768, width=65534), wsb=0) == 6
+    t = c_cache()
+    for new in (FAKE - 8, FAKE + 8):                             # three lengths that overlap the three of seq_lens
+        assert lib.sage_paged_evict(ctypes.byref(t), ctypes.c_void_p(new), 3, 2, 32, 64, 0, 0, 8, 0, 0,
+                                    ctypes.c_void_p(FAKE * 16), 1 << 40, None) == 1
+
+
 def test_workspace_sizes(lib):
     assert qa.paged_attn_workspace_bytes(1, 3, 2, 10, 64) == 0
     assert qa.paged_attn_workspace_bytes(1, 4, 2, 10, 129) == 0
