@@ -30,7 +30,7 @@ constexpr int kThreads = 384;
 constexpr uint32_t kRegsSoft = 224, kRegsCtl = 56;  // 2 * 128 * 224 + 128 * 56 = 384 * 168
 constexpr float kL2e = 1.4426950408889634f, kL2 = 0.6931471805599453f;
 constexpr float kNegInf = -INFINITY;
-constexpr int kMaxSplits = 16;
+constexpr int kMaxSplits = 32;
 
 struct DocTile {
   int lo, hi;  // smallest and largest non-negative id; lo > hi: none
@@ -48,6 +48,9 @@ struct CapPoly {
 
 struct ScoredArgs {
   int batch, hq, hkv, nq, nk, d, dtype, causal, splits, k_tiles, q_offset, vec;
+  // at most 128 queries: a CTA may take several heads of one key/value head, `per_tile` in each query tile, 2^row_bits
+  // rows apart; ctas_kv: CTAs per key/value head
+  int heads, per_tile, row_bits, ctas_kv;
   float c2;           // sm_scale log2(e)
   float cap2, cap_k;  // cap log2(e); 2 sm_scale log2(e) / cap
   CapPoly poly;
@@ -357,7 +360,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the work item: head, sequence, key split, pair of query tiles (those with the most keys first when causal)
   const int q0 = (a.causal ? (int)(gridDim.y - 1 - blockIdx.y) : (int)blockIdx.y) * 256;
-  const bool has_b = a.nq - q0 > 128;
+  const int hk = (int)blockIdx.x / a.ctas_kv, h_at = ((int)blockIdx.x - hk * a.ctas_kv) * a.heads;
+  const int h0 = hk * (a.hq / a.hkv) + h_at, nh = min(a.heads, a.hq / a.hkv - h_at);  // its heads
+  const bool has_b = nh > a.per_tile || a.nq - q0 > 128;
 
   if (threadIdx.x == 0) {
     // who releases a stage: the softmax of each tile at head_dim 64, of the last tile at 128
@@ -401,9 +406,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmQ);
     const int b = (int)blockIdx.z / a.splits;
     bar_expect(q_full, (has_b ? 2 : 1) * C::kQBytes);
-    for (int t = 0; t < (has_b ? 2 : 1); ++t)
-      for (int c = 0; c < C::kChunks; ++c)
-        tma_4d(sbase + t * C::kQBytes + c * 16384, &tmQ, q_full, c * 64, q0 + t * 128, (int)blockIdx.x, b);
+    if (a.heads == 1) {
+      for (int t = 0; t < (has_b ? 2 : 1); ++t)
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_4d(sbase + t * C::kQBytes + c * 16384, &tmQ, q_full, c * 64, q0 + t * 128, h0, b);
+    } else {
+      // (the rows of heads that are not there come from behind the last head: zeros)
+      for (int i = 0; i < (has_b ? 2 : 1) * a.per_tile; ++i)
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_4d(sbase + i / a.per_tile * C::kQBytes + c * 16384 + (((i % a.per_tile) * 128) << a.row_bits), &tmQ, q_full,
+                 c * 64, 0, i < nh ? h0 + i : a.hq, b);
+    }
   }
 
   // ---- the key tiles of this CTA
@@ -466,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ========================================================= TMA producer
       const int n_tiles = lds(misc + kWTiles), row0 = lds(misc + kWJ0) * 128, b = lds(misc + kWSeq);
       const int left = lds(misc + kWLeft);
-      const int h = blockIdx.x, hk = h / (a.hq / a.hkv);
       if (lane == 0 && n_tiles == 0) bar_wait(q_full, 0, 0);  // (Q lands before the shared memory goes away)
       if (lane == 0 && n_tiles > 0) {
         tma_prefetch_desc(&tmK);
@@ -606,25 +618,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     // =========================================================== softmax of tile x
     const int x = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int row = q0 + x * 128 + r;
-    const bool active = x == 0 || has_b, valid = active && row < a.nq;
+    const int head = a.heads == 1 ? 0 : x * a.per_tile + (r >> a.row_bits);  // of this CTA's
+    const int row = a.heads == 1 ? q0 + x * 128 + r : r & ((1 << a.row_bits) - 1);
+    const bool active = x == 0 || has_b, valid = active && row < a.nq && head < nh;
     // head_dim 128 and one query tile: the scores alternate between both S buffers, P V of the tile
     // before is waited for at each tile
     const bool solo = C::kOver && !has_b;
     const bool releases = (threadIdx.x & 127) == 0 && (!C::kOver || x == 1 || solo);
     const uint32_t tmem = lds(misc + kWTmem);
-    const int j0 = lds(misc + kWJ0), prefix = lds(misc + kWPrefix), b = lds(misc + kWSeq), h = blockIdx.x;
+    const int j0 = lds(misc + kWJ0), prefix = lds(misc + kWPrefix), b = lds(misc + kWSeq), h = h0 + (valid ? head : 0);
     const uint32_t tO = tmem + lane_base + C::kTmemO + x * DP;
     const int my_tiles = lds(misc + (x == 0 ? kWTilesA : kWTiles)), left = lds(misc + kWLeft);
     const int limit = valid ? limit_of(row, prefix) : 0;
     const int dq = !a.doc_q ? 0 : valid ? __ldg(&a.doc_q[(int64_t)b * a.nq + row]) : -1;
     const int pos = row + a.q_offset;
+    constexpr float kSlack = BF16 ? 60.0f : 7.0f;  // by how much a maximum may be overestimated
     float slope = 0.f;
     if constexpr (BIAS) slope = __ldg(&a.slopes[h]) * kL2e;
+    // (a warp's rows may be of heads with different slopes)
+    const bool gentle = !BIAS || __all_sync(0xffffffffu, fabsf(slope) * 15.0f <= kSlack);
     const float cap_m2 = -2.0f * a.cap2, cap_in = a.cap_k;
     // fp16 weights are held at up to 2^(7 + 8): 7 bits more before the smallest lose bits
     constexpr float kHead = BF16 ? 0.f : 7.0f;
-    constexpr float kSlack = BF16 ? 60.0f : 7.0f;  // by how much a maximum may be overestimated
     float m = kNegInf;                             // the frame, base 2
     float l = 0.f;
     bool ok = true;
@@ -824,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               big = max3(big, fabsf(__uint_as_float(s[c][u])), fabsf(__uint_as_float(s[c][u + 1])));
           return __all_sync(0xffffffffu, big <= a.poly.most) != 0;
         };
-        if (!masked && (!BIAS || (line && fabsf(step) * 15.0f <= kSlack))) {
+        if (!masked && (!BIAS || (line && gentle))) {
           // products; the cap and the scale keep their order, so their largest gives the maximum
           bool small = false;
           auto capped = [&](float v) {
@@ -1032,6 +1047,7 @@ __global__ void __launch_bounds__(128) scored_join_kernel(const ScoredArgs a) {
   float l = 0.f, acc[DP / 32];
 #pragma unroll
   for (int c = 0; c < DP / 32; ++c) acc[c] = 0.f;
+#pragma unroll 4
   for (int s = 0; s < a.splits; ++s) {
     const float2 x = *reinterpret_cast<const float2*>(a.part_ml + (s * lines + line) * 2);
     const float f = ex2f(x.x - u);
@@ -1085,22 +1101,49 @@ __global__ void __launch_bounds__(128) scored_copy_kernel(const CopyArgs a) {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 struct ScoredLayout {
   size_t tiles, part_o, part_ml, copy[3], total;
-  int dp, splits, k_tiles;
+  int dp, k_tiles;
+  // the work items (see ScoredArgs) and the key splits of each
+  int heads, per_tile, row_bits, ctas_kv, splits;
 };
-// Key splits: where the (head, pair of query tiles) items leave SMs idle, as many as fill one wave, of at
-// least four key tiles each.
-int splits_of(int batch, int hq, int nq, int nk) {
-  const int64_t items = (int64_t)batch * hq * ((nq + 255) / 256), tiles = (nk + 127) / 128;
+// Key splits: where the items leave SMs idle, as many as fill one wave, of at least four key tiles each.
+int splits_of(int64_t items, int64_t tiles) {
   int64_t s = items > 0 ? 152 / items : 1;
   if (s > tiles / 4) s = tiles / 4;
   if (s > kMaxSplits) s = kMaxSplits;
   return s < 1 ? 1 : (int)s;
 }
+// With at most 128 queries the heads of a key/value head can share a CTA and the keys it loads: as blocks of rows of
+// one query tile, or of two, whose softmaxes then overlap. A step over one tile alone takes 5/8 of a step over two
+// (1.15 and 1.84 us, biased, head_dim 128); a CTA's start and end are worth four steps, and so is the join of
+// splits. The shape of the least time is taken.
+void plan_items(int batch, int hq, int hkv, int nq, int nk, ScoredLayout* L) {
+  const int group = hq / hkv;
+  const int64_t tiles = L->k_tiles;
+  int bits = 3;
+  while (bits < 7 && 1 << bits < nq) ++bits;
+  int64_t best = -1;
+  for (int form = 0; form < (nq <= 128 && group > 1 ? 3 : 1); ++form) {
+    const int per_tile = form == 0 ? 1 : 128 >> bits, room = form == 2 ? 2 * per_tile : per_tile;
+    const int heads = form == 0 ? 1 : group < room ? group : room;
+    if (form == 1 && heads == 1) continue;
+    const int ctas_kv = (group + heads - 1) / heads;
+    const int64_t items = (int64_t)batch * hkv * ctas_kv * (((int64_t)nq + 255) / 256);
+    const int splits = splits_of(items, tiles);
+    const bool two = form == 0 ? nq > 128 : heads > per_tile;
+    const int64_t waves = (items * splits + 151) / 152;
+    const int64_t time = waves * ((tiles + splits - 1) / splits * (two ? 8 : 5) + 20) + (splits > 1 ? 20 : 0);
+    if (best < 0 || time < best) {
+      best = time;
+      L->heads = heads; L->per_tile = per_tile; L->row_bits = form == 0 ? 7 : bits; L->ctas_kv = ctas_kv;
+      L->splits = splits;
+    }
+  }
+}
 bool scored_layout(int batch, int hq, int hkv, int nq, int nk, int d, int packed, ScoredLayout* L) {
   if (batch < 0 || hq < 1 || hkv < 1 || hq % hkv || nq < 0 || nk < 0 || d < 1 || d > 128) return false;
   L->dp = d <= 64 ? 64 : 128;
-  L->splits = splits_of(batch, hq, nq, nk);
   L->k_tiles = (int)(((int64_t)nk + 127) / 128);
+  plan_items(batch, hq, hkv, nq, nk, L);
   size_t o = 256;
   auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
   L->tiles = take((size_t)batch * L->k_tiles * sizeof(DocTile));
@@ -1207,6 +1250,7 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
   a.batch = batch; a.hq = heads_q; a.hkv = heads_kv; a.nq = seqlen_q; a.nk = seqlen_k; a.d = head_dim;
   a.dtype = dtype; a.causal = is_causal ? 1 : 0; a.splits = L.splits; a.k_tiles = L.k_tiles; a.q_offset = q_offset;
   a.vec = fits[3] ? 1 : 0;
+  a.heads = L.heads; a.per_tile = L.per_tile; a.row_bits = L.row_bits; a.ctas_kv = L.ctas_kv;
   const float scale =
       std::isnan(sm_scale) || sm_scale <= 0.f ? (float)(1.0 / std::sqrt((double)head_dim)) : sm_scale;
   a.c2 = (float)(scale * 1.4426950408889634);
@@ -1252,14 +1296,15 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
     }
     // a stride that is never walked (its dimension is 1 long) is given a legal value
     const int64_t sn = t.n > 1 ? t.sn : 128, sh = t.heads > 1 ? t.sh : 128, sb = batch > 1 ? t.sb : 128;
-    if (!make_map4(&maps[i], dtype == SAGE_BF16, t.p, inner, t.n, t.heads, batch, sn * 2, sh * 2, sb * 2, 64, 128))
+    if (!make_map4(&maps[i], dtype == SAGE_BF16, t.p, inner, t.n, t.heads, batch, sn * 2, sh * 2, sb * 2, 64,
+                   i == 0 ? 1 << L.row_bits : 128))
       return note_cuda_failure(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
   }
   if (e == cudaSuccess && doc_k) {
     scored_setup_kernel<<<dim3(L.k_tiles, batch), 128, 0, st>>>(a);
     e = cudaGetLastError();
   }
-  const dim3 grid(heads_q, (unsigned)pairs, (unsigned)(batch * L.splits));
+  const dim3 grid((unsigned)(heads_kv * L.ctas_kv), (unsigned)pairs, (unsigned)(batch * L.splits));
   if (e == cudaSuccess) {
     if (dtype == SAGE_BF16)
       e = L.dp == 64 ? launch_scored<64, true>(a, maps, grid, st) : launch_scored<128, true>(a, maps, grid, st);

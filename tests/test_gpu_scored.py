@@ -134,6 +134,21 @@ def test_few_rows_are_split_over_the_keys(nq, nk, hq, d, dtype):
           dk=docs_of([nk // 3, nk - nk // 3 - 9], 9, 1))
 
 
+# Few queries of several heads in one query tile or two, groups that do not fill them, splits and none
+@pytest.mark.parametrize("B,hq,hkv,nq,nk", [(2, 8, 2, 20, 6000), (2, 14, 2, 16, 6000), (2, 14, 2, 40, 6000),
+                                            (1, 32, 8, 100, 9000), (20, 12, 4, 100, 300), (30, 16, 4, 5, 700),
+                                            (16, 14, 2, 40, 500), (20, 8, 2, 1, 900), (12, 10, 2, 64, 700)])
+@pytest.mark.parametrize("d,dtype,layout", [(64, F, "NHD"), (128, H, "HND"), (40, H, "HND"), (33, F, "NHD")])
+def test_heads_share_a_tile(B, hq, hkv, nq, nk, d, dtype, layout):
+    g = torch.Generator().manual_seed(nq)
+    check(B, hq, hkv, nq, nk, d, dtype, layout, causal=True, offset=nk - nq, bias=True)
+    check(B, hq, hkv, nq, nk, d, dtype, layout, causal=True, offset=-3, cap=9.0,
+          prefix=torch.randint(0, nk, (B,), generator=g).tolist())
+    dk = docs_of([nk // 3, nk - nk // 3 - 9], 9, B)
+    check(B, hq, hkv, nq, nk, d, dtype, layout, dq=torch.randint(-1, 3, (B, nq), generator=g, dtype=torch.int32), dk=dk,
+          bias=True, cap=20.0)
+
+
 def test_padding_may_hold_anything():
     dq = docs_of([150, 100], 70, 1)
     g = torch.Generator().manual_seed(3)
