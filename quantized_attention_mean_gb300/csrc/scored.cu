@@ -435,9 +435,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int hi_a = (limit_of(q0 + min(rows, 128) - 1, prefix) + 127) / 128;
     if (a.doc_q) {
       int* red = reinterpret_cast<int*>(sm + C::kOffMisc + kWRed);
-      if (threadIdx.x < rows) {
-        const int id = __ldg(&a.doc_q[(int64_t)b * a.nq + q0 + threadIdx.x]);
-        if (id >= 0) { atomicMin(&red[0], id); atomicMax(&red[1], id); }
+      if (warp < 8) {
+        const int id = (int)threadIdx.x < rows ? __ldg(&a.doc_q[(int64_t)b * a.nq + q0 + threadIdx.x]) : -1;
+        const int most = __reduce_max_sync(0xffffffffu, id);
+        const int least = (int)__reduce_min_sync(0xffffffffu, (unsigned)id);  // (negative ids come last)
+        if (lane == 0 && most >= 0) { atomicMin(&red[0], least); atomicMax(&red[1], most); }
       }
       __syncthreads();
       const int dlo = red[0], dhi = red[1];
@@ -671,18 +673,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
       wait_ld_max(cm);
     };
+    // the document that a tile's keys are all of, or -2; read a step ahead
+    auto only_of = [&](int j) {
+      const DocTile t = a.doc_tiles[(int64_t)b * a.k_tiles + j0 + (BIAS ? tile_of(j, left) : j)];
+      return t.mixed ? -2 : t.lo;
+    };
+    int only = a.doc_k && my_tiles > 0 ? only_of(0) : 0, only_next = 0;
     if (active) {
-      for (int j = 0; j < my_tiles && ok; ++j) {
+      for (int j = 0; j < my_tiles && ok; ++j, only = only_next) {
+        if (a.doc_k && j + 1 < my_tiles) only_next = only_of(j + 1);
         load_s(j);
         if (!ok) break;
         const uint32_t tP = tmem + lane_base + (C::kOver ? (solo ? j & 1 : x) * 128 : C::kTmemP + x * C::kPitchP);
         const int tile = j0 + (BIAS ? tile_of(j, left) : j), kv0 = tile * 128;
         // ---- which keys of the tile this row sees, as bits (only where some row of the warp misses one)
         bool whole = limit - kv0 >= 128;
-        if (a.doc_k) {
-          const DocTile t = a.doc_tiles[(int64_t)b * a.k_tiles + tile];
-          whole = whole && !t.mixed && t.lo == dq;
-        }
+        if (a.doc_k) whole = whole && only == dq;
         whole = whole || !valid;  // (rows behind the last one are not written)
         const bool masked = !__all_sync(0xffffffffu, whole);
         float t_max = kNegInf, m_use = 0.f;
