@@ -248,7 +248,8 @@ int sage_merge_partials(const sage_tensor* outs, const float* const* lses, int n
  *   in the rows that do not see it).
  *   workspace: sage_scored_attn_workspace_size() bytes; `packed` != 0 where q, k and v all have 16-byte
  *   aligned rows (address, and strides and head_dim multiples of 8 elements; no zero stride of a
- *   dimension longer than 1) and need no padded copy there.
+ *   dimension longer than 1) and need no padded copy there; `packed` + 2 where there are no documents. Where no more
+ *   than SAGE_STATUS_BYTES are needed, workspace may be NULL: no status is kept then.
  * Nq == 0 or B == 0 is a no-op; Nk == 0 writes 0 and -inf. */
 size_t sage_scored_attn_workspace_size(int batch, int heads_q, int heads_kv, int seqlen_q, int seqlen_k,
                                        int head_dim, int packed);
@@ -292,7 +293,7 @@ typedef struct {
  *   slopes: device float [Hq] or NULL; q_positions: device int32 [batch] or NULL (seq_len - 1).
  *   max_seqlen: an upper bound of seq_lens. cache->mass, where not NULL: each held token's weight,
  *   summed over the query heads of its key/value head, is added. A page that several
- *   sequences share is given the weights of all, in no fixed order.
+ *   sequences share is given the weights of all, in no fixed order. workspace: as sage_scored_attn's.
  * A sequence that holds nothing gets out = 0 and lse = -inf. */
 size_t sage_paged_attn_workspace_size(int batch, int heads_q, int heads_kv, int max_seqlen,
                                       int head_dim, int accumulate);

@@ -56,7 +56,7 @@ struct DecodeArgs {
   int mass4;                // see mass_kernel
   int slices;               // CTAs of the join per (row block of a head, sequence)
   // workspace
-  int* err;                 // status word
+  int* err;                 // status word, or null (no workspace: the clusters' form without mass)
   int* cta_err;             // [kCtas]
   float* part_o;            // [kCtas][2][kRows][dp]
   float* part_ml;           // [kCtas][2][kRows][2]
@@ -223,7 +223,7 @@ __device__ __forceinline__ void load_stage(const DecodeArgs& a, const CUtensorMa
               page >= 0 ? page : a.c.num_pages);
     return;
   }
-  const T* none = reinterpret_cast<const T*>(a.part_o);  // an address that nothing is read from
+  const T* none = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(a.q) & ~static_cast<uintptr_t>(15));  // nothing is read from it
   const T* kb = static_cast<const T*>(a.c.k) + h * a.c.k_sh;
   const T* vb = static_cast<const T*>(a.c.v) + h * a.c.v_sh;
   constexpr int kUnits = DP / 8, kRowsPer = 32 / kUnits;  // rows that one pass of the warp covers
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   if constexpr (CLUSTER) {
     // the status word has one writer (but for a wait that runs out, two seconds from now): the first
     // CTA looks at the lengths and pages of all sequences
-    if (me == 0 && blockIdx.y == 0) {
+    if (a.err && me == 0 && blockIdx.y == 0) {
       int e = 0;
       for (int b = 0; b < a.c.batch; ++b) {
         const int len = checked_len(a.c, b, a.max_len);
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         *reinterpret_cast<float2*>(&ml[(warp * kRows + r) * 2]) =
             fresh ? make_float2(-INFINITY, 0.f) : make_float2(half ? m1 : m0, half ? l1 : l0);
     }
-    if (dead) record_error(a.err, kDevTimeout);
+    if (dead && a.err) record_error(a.err, kDevTimeout);
     cluster_sync();
     const int cell = rank * kWarps * 32 + threadIdx.x, r = cell / (DP / 4), c = (cell - r * (DP / 4)) * 4;
     if (r < rows) {
@@ -1008,14 +1008,24 @@ struct DecodeLayout {
   int64_t pitch;
 };
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+// Few heads with short sequences: one launch of clusters whose CTAs all run at once, a tile or a few each, joined
+// through distributed shared memory. Otherwise the line, which balances any lengths but takes a second launch
+// to join (one sequence of 1000 tokens, 8 key/value heads, in a graph: 7.8 against 12.4 us; beyond
+// eight tiles per CTA the line's 304 CTAs are faster than the clusters').
+bool clustered(int batch, int hkv, int row_blocks, int64_t max_len, int d) {
+  const int tile = d <= 64 ? DecodeCfg<64>::kTile : DecodeCfg<128>::kTile;
+  return (int64_t)hkv * row_blocks * batch * kRanks <= kCtas && max_len <= 8 * kRanks * tile;
+}
 bool decode_layout(int batch, int hq, int hkv, int64_t max_len, int d, bool mass, DecodeLayout* L) {
   if (batch < 0 || hq < 1 || hkv < 1 || hq % hkv || max_len < 0 || d < 1 || d > 128) return false;
   const int dp = d <= 64 ? 64 : 128;
-  size_t o = 256 + up256(4 * kCtas);  // status word, then the CTAs' errors
+  // status word; the line's ranges: their errors and their pieces
+  const bool line = !clustered(batch, hkv, (hq / hkv + kRows - 1) / kRows, max_len, d);
+  size_t o = 256 + (line ? up256(4 * kCtas) : 0);
   auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
   L->err = 256;
-  L->part_o = take((size_t)kCtas * 2 * kRows * dp * 4);
-  L->part_ml = take((size_t)kCtas * 2 * kRows * 2 * 4);
+  L->part_o = take(line ? (size_t)kCtas * 2 * kRows * dp * 4 : 0);
+  L->part_ml = take(line ? (size_t)kCtas * 2 * kRows * 2 * 4 : 0);
   L->pitch = (max_len + 127) / 128 * 128;  // whole tiles of either head_dim
   L->lse2 = take(mass ? (size_t)batch * hq * 4 : 0);
   L->scores = take(mass ? (size_t)batch * hq * L->pitch * 4 : 0);
@@ -1026,14 +1036,9 @@ bool decode_layout(int batch, int hq, int hkv, int64_t max_len, int d, bool mass
 template <typename T, int DP>
 cudaError_t launch_decode_t(const DecodeArgs& a, const CUtensorMap* maps, cudaStream_t st) {
   using C = DecodeCfg<DP>;
-  // Few heads with short sequences: one launch of clusters whose CTAs all run at once, a tile or a few each, joined
-  // through distributed shared memory. Otherwise the line, which balances any lengths but takes a second launch
-  // to join (one sequence of 1000 tokens, 8 key/value heads, in a graph: 7.8 against 12.4 us; beyond
-  // eight tiles per CTA the line's 304 CTAs are faster than the clusters').
   const int heads = a.c.hkv * a.row_blocks;
-  const bool cluster = (int64_t)heads * a.c.batch * kRanks <= kCtas && a.max_len <= 8 * kRanks * C::kTile;
   cudaError_t e;
-  if (cluster) {
+  if (clustered(a.c.batch, a.c.hkv, a.row_blocks, a.max_len, a.c.d)) {
     static std::atomic<int> limits[64];
     e = raise_smem_limit(decode_kernel<T, DP, true>, C::kSmem, limits);
     if (e != cudaSuccess) return e;
@@ -1098,7 +1103,8 @@ int sage_paged_attn(const sage_packed* q, const sage_paged_cache* cache, const s
   DecodeLayout L;
   if (!decode_layout(batch, heads_q, heads_kv, max_seqlen, head_dim, cache->mass != nullptr, &L))
     return SAGE_ERR_INVALID_ARG;
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < L.total)
+  // (the status word alone can do without)
+  if (workspace ? reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < L.total : L.total > SAGE_STATUS_BYTES)
     return SAGE_ERR_WORKSPACE;
   if (!sage_device_supported()) return SAGE_ERR_DEVICE;
   a.q = q->data; a.q_sb = q->stride_token; a.q_sh = q->stride_head;

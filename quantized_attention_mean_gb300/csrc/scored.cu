@@ -71,7 +71,7 @@ struct ScoredArgs {
   const int* doc_q;
   const int* doc_k;
   // workspace
-  int* err;
+  int* err;            // status word, or null (no workspace)
   DocTile* doc_tiles;  // [batch][k_tiles]
   float* part_o;       // [splits][batch * hq * nq][dp]
   float* part_ml;      // [splits][batch * hq * nq][2]
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   pdl_wait();
   // the status word: nothing but a wait of two seconds can set it after this
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *a.err = 0;
+  if (a.err && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *a.err = 0;
 
   // Q is on its way while the key tiles are found
   if (warp == 8 && lane == 0) {
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_wait(k_full + 8 * (j % C::kKStages), (j / C::kKStages) & 1, 0);
           for (int j = max(0, nv - C::kVStages); j < nv; ++j)
             bar_wait(v_full + 8 * (j % C::kVStages), (j / C::kVStages) & 1, 0);
-          record_error(a.err, kDevTimeout);
+          if (a.err) record_error(a.err, kDevTimeout);
         }
       }
     } else if (warp == 11) {
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) bar_arrive(v_clean + 8 * sv);
         }
-        if (!ok && lane == 0) record_error(a.err, kDevTimeout);
+        if (!ok && lane == 0 && a.err) record_error(a.err, kDevTimeout);
       }
     } else if (warp == 9 || (!C::kOver && has_b)) {
       // ========================================================= MMA issuers
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit_to(drain + 8 * me);
       warp_wait(drain + 8 * me, 0, 0);
       __syncwarp();
-      if (!ok && lane == 0) record_error(a.err, kDevTimeout);
+      if (!ok && lane == 0 && a.err) record_error(a.err, kDevTimeout);
     }
   } else {
     regs_inc<kRegsSoft>();
@@ -1018,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.lse[line] = seen ? (m + __log2f(l)) * kL2 : kNegInf;
         }
       }
-      if (!ok) record_error(a.err, kDevTimeout);
+      if (!ok && a.err) record_error(a.err, kDevTimeout);
     }
   }
   tc_fence_before();
@@ -1086,7 +1086,7 @@ __global__ void __launch_bounds__(128) scored_join_kernel(const ScoredArgs a) {
 __global__ void __launch_bounds__(128) scored_empty_kernel(const ScoredArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t lines = (int64_t)a.batch * a.hq * a.nq, line = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (line == 0 && lane == 0) *a.err = 0;
+  if (a.err && line == 0 && lane == 0) *a.err = 0;
   if (line >= lines) return;
   const int64_t bh = line / a.nq;
   const int row = (int)(line - bh * a.nq), b = (int)(bh / a.hq), h = (int)(bh - (int64_t)b * a.hq);
@@ -1155,14 +1155,14 @@ void plan_items(int batch, int hq, int hkv, int nq, int nk, ScoredLayout* L) {
     }
   }
 }
-bool scored_layout(int batch, int hq, int hkv, int nq, int nk, int d, int packed, ScoredLayout* L) {
+bool scored_layout(int batch, int hq, int hkv, int nq, int nk, int d, bool packed, bool docs, ScoredLayout* L) {
   if (batch < 0 || hq < 1 || hkv < 1 || hq % hkv || nq < 0 || nk < 0 || d < 1 || d > 128) return false;
   L->dp = d <= 64 ? 64 : 128;
   L->k_tiles = (int)(((int64_t)nk + 127) / 128);
   plan_items(batch, hq, hkv, nq, nk, L);
   size_t o = 256;
   auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
-  L->tiles = take((size_t)batch * L->k_tiles * sizeof(DocTile));
+  L->tiles = take(docs ? (size_t)batch * L->k_tiles * sizeof(DocTile) : 0);
   const size_t lines = (size_t)batch * hq * nq;
   L->part_o = take(L->splits > 1 ? L->splits * lines * L->dp * 4 : 0);
   L->part_ml = take(L->splits > 1 ? L->splits * lines * 8 : 0);
@@ -1210,7 +1210,7 @@ extern "C" {
 size_t sage_scored_attn_workspace_size(int batch, int heads_q, int heads_kv, int seqlen_q, int seqlen_k, int head_dim,
                                        int packed) {
   ScoredLayout L;
-  return scored_layout(batch, heads_q, heads_kv, seqlen_q, seqlen_k, head_dim, packed, &L) ? L.total : 0;
+  return scored_layout(batch, heads_q, heads_kv, seqlen_q, seqlen_k, head_dim, packed & 1, !(packed & 2), &L) ? L.total : 0;
 }
 
 int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tensor* v, const sage_tensor* out,
@@ -1253,12 +1253,13 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
     fits[i] = ok;
   }
   const bool packed = fits[0] && fits[1] && fits[2];
-  if (!scored_layout(batch, heads_q, heads_kv, seqlen_q, seqlen_k, head_dim, packed, &L)) return SAGE_ERR_INVALID_ARG;
+  if (!scored_layout(batch, heads_q, heads_kv, seqlen_q, seqlen_k, head_dim, packed, doc_k != nullptr, &L)) return SAGE_ERR_INVALID_ARG;
   const int64_t pairs = ((int64_t)seqlen_q + 255) / 256;
   if (seqlen_k > 0x7fffff00 || seqlen_q > 0x7fffff00 || (int64_t)q_offset + seqlen_q > 0x7fffff00 ||
       q_offset < -0x7fffff00 || pairs > 65535 || (int64_t)batch * L.splits > 65535 || (int64_t)batch * heads_q * seqlen_q > (1LL << 32))
     return SAGE_ERR_INVALID_ARG;
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < L.total)
+  // (the status word alone can do without)
+  if (workspace ? reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < L.total : L.total > SAGE_STATUS_BYTES)
     return SAGE_ERR_WORKSPACE;
   if (!sage_device_supported()) return SAGE_ERR_DEVICE;
   char* w = static_cast<char*>(workspace);

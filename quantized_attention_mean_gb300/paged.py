@@ -57,6 +57,11 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _workspace(nbytes, device):
+    """What a call needs beside its status word, which no one could read here."""
+    return None if nbytes <= STATUS_BYTES else alloc_workspace(nbytes, device)
+
+
 def _check_small(name, t, shape, dtype, index):
     if t is not None and (t.dtype != dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} {list(shape)} tensor on the inputs' device")
@@ -170,11 +175,11 @@ def paged_attn(q, k_cache, v_cache, page_table, seq_lens, max_seq_len, tensor_la
         if return_lse and lse is None:
             lse = torch.empty((B, hq), dtype=torch.float32, device=q.device)
         if workspace is None:
-            workspace = alloc_workspace(lib.sage_paged_attn_workspace_size(B, hq, hkv, n, d, mass is not None), q.device)
+            workspace = _workspace(lib.sage_paged_attn_workspace_size(B, hq, hkv, n, d, mass is not None), q.device)
         st = lib.sage_paged_attn(byref(_packed(q)), byref(cache), byref(_packed(out)), _ptr(lse), _ptr(slopes),
                                  _ptr(q_positions), B, hq, hkv, n, d, DTYPE[q.dtype], LAYOUT[tensor_layout],
-                                 _NAN if sm_scale is None else sm_scale, softcap, workspace.data_ptr(),
-                                 workspace.numel(), on)
+                                 _NAN if sm_scale is None else sm_scale, softcap, _ptr(workspace),
+                                 0 if workspace is None else workspace.numel(), on)
     if st:
         raise SageError(st, "paged_attn")
     return (out, lse) if return_lse else out

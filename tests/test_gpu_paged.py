@@ -195,6 +195,30 @@ def test_empty_cache_in_place_and_from_another_page():
     assert torch.equal(G["k"], other[0]) and torch.equal(G["v"], other[1])
 
 
+@pytest.mark.parametrize("page,d", [(16, 64), (4, 128), (16, 33)])
+def test_without_a_workspace(page, d):
+    # (pages by TMA, by 16 bytes and element by element; an output row that starts anywhere)
+    import quantized_attention_mean_gb300 as qa
+    lens = [300, 1, 77]
+    c = ref.make_cache(lens, 2, d, page, torch.float16)
+    G = on_gpu(c)
+    q = torch.randn(3, 6, d + 1, generator=torch.Generator().manual_seed(2)).half()[..., 1:]
+    ws = qa.alloc_workspace(qa.paged_attn_workspace_bytes(3, 6, 2, 300, d), DEV)
+    assert ws.numel() == 256
+    wide = torch.zeros(3, 6, d + 1, dtype=torch.float16, device=DEV)
+    wide[..., 1:] = q.to(DEV)
+    a = qa.paged_attn(wide[..., 1:], G["k"], G["v"], G["table"], G["lens"], 300, workspace=ws)
+    b = qa.paged_attn(wide[..., 1:], G["k"], G["v"], G["table"], G["lens"], 300)
+    assert qa.read_device_status(ws) == 0 and torch.equal(a, b)
+    r = decode_reference(c, q, d ** -0.5, hkv=2)
+    assert_close(b, r["out"], r["out_tol"], "out")
+    table = G["table"].clone()
+    table[0, 1] = c["k"].shape[0]
+    qa.paged_attn(wide[..., 1:], G["k"], G["v"], table, G["lens"], 300)           # a bad page: zeros, and no word of it
+    qa.paged_attn(wide[..., 1:], G["k"], G["v"], table, G["lens"], 300, workspace=ws)
+    assert qa.read_device_status(ws) == 13
+
+
 def test_append_and_evict_in_a_graph():
     import quantized_attention_mean_gb300 as qa
     c = ref.make_cache([70, 20], 2, 64, 16, torch.float16, room=2)

@@ -258,6 +258,21 @@ def test_strided_and_broadcast_inputs():
     check(2, 2, 2, 100, 300, 64, F, q=q, k=k2, v=v2, place=odd)
 
 
+def test_without_a_workspace():
+    import quantized_attention_mean_gb300 as qa
+    g = torch.Generator().manual_seed(4)
+    q, k, v = (torch.randn(2, 4, 300, 64, generator=g).half().to(DEV) for _ in "qkv")
+    n = qa.scored_attn_workspace_bytes(2, 4, 4, 300, 300, 64, documents=False)
+    assert n == 256
+    ws = qa.alloc_workspace(n, DEV)
+    ws.fill_(255)
+    a = qa.scored_attn(q, k, v, is_causal=True, softcap=20.0, workspace=ws)
+    assert qa.read_device_status(ws) == 0
+    assert torch.equal(qa.scored_attn(q, k, v, is_causal=True, softcap=20.0), a)
+    assert torch.equal(qa.scored_attn(q[:, :, :0], k, v), q[:, :, :0])
+    assert (qa.scored_attn(q, k[:, :, :0], v[:, :, :0]) == 0).all()
+
+
 def test_no_keys_and_out_strides():
     import quantized_attention_mean_gb300 as qa
     q = torch.randn(1, 2, 5, 64, dtype=torch.float16, device=DEV)

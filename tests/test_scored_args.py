@@ -85,7 +85,10 @@ def test_c_statuses(lib):
     assert call(lib, q=0) == 1 and call(lib, q=FAKE + 1) == 4 and call(lib, st=(64, -64, 64)) == 4
     assert call(lib, offset=2 ** 31 - 1) == 1 and call(lib, offset=-2 ** 31) == 1
     assert call(lib, nq=0) == 0 and call(lib, batch=0) == 0
-    assert call(lib, wsb=256) == 6 and call(lib, ws=0) == 6 and call(lib, ws=FAKE * 16 + 16) == 6
+    assert call(lib, dq=FAKE, dk=FAKE, wsb=256) == 6 and call(lib, dq=FAKE, dk=FAKE, ws=0) == 6
+    assert call(lib, ws=FAKE * 16 + 16) == 6 and call(lib, wsb=128) == 6
+    assert call(lib, nq=2, nk=4096, ws=0) == 6                  # split over the keys
+    assert lib.sage_scored_attn_workspace_size(1, 2, 2, 256, 256, 64, 3) == 256     # no documents: the status word alone
     # a query tensor that needs a copy needs the larger workspace
     small = lib.sage_scored_attn_workspace_size(1, 2, 2, 256, 256, 64, 1)
     assert call(lib, st=(2 * 256 * 64, 256 * 64, 65), wsb=small) == 6
