@@ -14,11 +14,12 @@ captured into a CUDA graph; ``read_device_status(workspace)`` tells of bad ones.
 """
 
 import contextlib
+import functools
 from ctypes import byref
 
 import torch
 
-from . import DTYPE, LAYOUT, SageError, _check_workspace, _lib, alloc_workspace
+from . import DTYPE, LAYOUT, SageError, _check_workspace, _lib
 from ._lib import SagePacked, SagePagedCache
 
 __all__ = ["paged_attn", "paged_append", "paged_evict", "paged_attn_workspace_bytes",
@@ -57,9 +58,29 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _workspace(nbytes, device):
-    """What a call needs beside its status word, which no one could read here."""
-    return None if nbytes <= STATUS_BYTES else alloc_workspace(nbytes, device)
+class _Scratch:
+    """A call's workspace: the caller's, or memory of PyTorch's allocator that belongs to the launching stream and
+    goes back to it after the launch (straight from the allocator: a tensor costs the host 2 us more). None for
+    a status word alone, which no one could read."""
+
+    __slots__ = ("at", "nbytes", "mine")
+
+    def __init__(self, workspace, nbytes, stream):
+        self.mine = False
+        if workspace is not None:
+            self.at, self.nbytes = workspace.data_ptr(), workspace.numel()
+        elif nbytes <= STATUS_BYTES:
+            self.at, self.nbytes = None, 0
+        else:
+            self.at, self.nbytes = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream), nbytes
+            self.mine = True
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        if self.mine:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(self.at)
 
 
 def _check_small(name, t, shape, dtype, index):
@@ -125,11 +146,13 @@ def _check_cuda(index):
         raise ValueError("the cache must be on a CUDA device")
 
 
+@functools.lru_cache(1024)
 def paged_attn_workspace_bytes(batch, heads_q, heads_kv, max_seq_len, head_dim, accumulate=False):
     return _lib.load().sage_paged_attn_workspace_size(batch, heads_q, heads_kv, max_seq_len, head_dim,
                                                       int(bool(accumulate)))
 
 
+@functools.lru_cache(1024)
 def paged_evict_workspace_bytes(batch, heads_kv, max_seq_len, budget):
     return _lib.load().sage_paged_evict_workspace_size(batch, heads_kv, max_seq_len, budget)
 
@@ -174,12 +197,11 @@ def paged_attn(q, k_cache, v_cache, page_table, seq_lens, max_seq_len, tensor_la
             out = torch.empty(shape, dtype=q.dtype, device=q.device)
         if return_lse and lse is None:
             lse = torch.empty((B, hq), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = _workspace(lib.sage_paged_attn_workspace_size(B, hq, hkv, n, d, mass is not None), q.device)
-        st = lib.sage_paged_attn(byref(_packed(q)), byref(cache), byref(_packed(out)), _ptr(lse), _ptr(slopes),
-                                 _ptr(q_positions), B, hq, hkv, n, d, DTYPE[q.dtype], LAYOUT[tensor_layout],
-                                 _NAN if sm_scale is None else sm_scale, softcap, _ptr(workspace),
-                                 0 if workspace is None else workspace.numel(), on)
+        nbytes = 0 if workspace is not None else paged_attn_workspace_bytes(B, hq, hkv, n, d, mass is not None)
+        with _Scratch(workspace, nbytes, on) as w:
+            st = lib.sage_paged_attn(byref(_packed(q)), byref(cache), byref(_packed(out)), _ptr(lse), _ptr(slopes),
+                                     _ptr(q_positions), B, hq, hkv, n, d, DTYPE[q.dtype], LAYOUT[tensor_layout],
+                                     _NAN if sm_scale is None else sm_scale, softcap, w.at, w.nbytes, on)
     if st:
         raise SageError(st, "paged_attn")
     return (out, lse) if return_lse else out
@@ -241,10 +263,10 @@ def paged_evict(k_cache, v_cache, mass, key_positions, page_table, seq_lens, bud
     lib = _lib.load()
     with _Launch(index, stream) as on:
         new_lens = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
-        if workspace is None:
-            workspace = alloc_workspace(lib.sage_paged_evict_workspace_size(B, hkv, n, budget), k_cache.device)
-        st = lib.sage_paged_evict(byref(cache), new_lens.data_ptr(), B, hkv, n, d, DTYPE[k_cache.dtype],
-                                  LAYOUT[tensor_layout], budget, sink, recent, workspace.data_ptr(), workspace.numel(), on)
+        nbytes = 0 if workspace is not None else paged_evict_workspace_bytes(B, hkv, n, budget)
+        with _Scratch(workspace, nbytes, on) as w:
+            st = lib.sage_paged_evict(byref(cache), new_lens.data_ptr(), B, hkv, n, d, DTYPE[k_cache.dtype],
+                                      LAYOUT[tensor_layout], budget, sink, recent, w.at, w.nbytes, on)
     if st:
         raise SageError(st, "paged_evict")
     return new_lens

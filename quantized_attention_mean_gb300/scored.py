@@ -1,13 +1,14 @@
 """Attention with modified scores: capped by a tanh, biased by distance, under document and prefix
 masks, on 16-bit operands. For the layers whose scores the quantised calls cannot take."""
 
+import functools
 from ctypes import byref
 
 import torch
 
 from . import DTYPE, LAYOUT, SageError, _check_dense_args, _dims, _lib
 from ._lib import SageView
-from .paged import _NAN, _check_small, _Launch, _ptr, _workspace
+from .paged import _NAN, _check_small, _Launch, _ptr, _Scratch
 
 __all__ = ["scored_attn", "scored_attn_workspace_bytes"]
 
@@ -25,6 +26,7 @@ def _view(t, whole):
                                       and (n2 <= 1 or (s2 > 0 and s2 % 8 == 0)))
 
 
+@functools.lru_cache(1024)
 def scored_attn_workspace_bytes(batch, heads_q, heads_kv, seqlen_q, seqlen_k, head_dim, packed=True, documents=True):
     """``packed``: q, k and v have 16-byte aligned rows (address, strides and head_dim). ``documents``: doc_ids are given."""
     return _lib.load().sage_scored_attn_workspace_size(batch, heads_q, heads_kv, seqlen_q, seqlen_k, head_dim,
@@ -74,14 +76,14 @@ def scored_attn(q, k, v, tensor_layout="HND", is_causal=False, sm_scale=None, so
         if return_lse and lse is None:
             lse = torch.empty((B, hq, nq), dtype=torch.float32, device=q.device)
         (qv, q_ok), (kv, k_ok), (vv, v_ok), (ov, _) = (_view(t, d % 8 == 0) for t in (q, k, v, out))
-        if workspace is None:
-            workspace = _workspace(lib.sage_scored_attn_workspace_size(B, hq, hkv, nq, nk, d, (q_ok and k_ok and v_ok)
-                                                                       + 2 * (doc_ids is None)), q.device)
-        st = lib.sage_scored_attn(byref(qv), byref(kv), byref(vv), byref(ov), _ptr(lse),
-                                  _ptr(slopes), _ptr(prefix_lens), _ptr(doc_ids), _ptr(doc_ids_k), B, hq, hkv, nq, nk, d,
-                                  DTYPE[q.dtype], LAYOUT[tensor_layout], bool(is_causal),
-                                  _NAN if sm_scale is None else sm_scale, softcap, q_offset, bool(return_lse),
-                                  _ptr(workspace), 0 if workspace is None else workspace.numel(), on)
+        nbytes = 0 if workspace is not None else scored_attn_workspace_bytes(B, hq, hkv, nq, nk, d, q_ok and k_ok and v_ok,
+                                                                             doc_ids is not None)
+        with _Scratch(workspace, nbytes, on) as w:
+            st = lib.sage_scored_attn(byref(qv), byref(kv), byref(vv), byref(ov), _ptr(lse),
+                                      _ptr(slopes), _ptr(prefix_lens), _ptr(doc_ids), _ptr(doc_ids_k), B, hq, hkv, nq, nk, d,
+                                      DTYPE[q.dtype], LAYOUT[tensor_layout], bool(is_causal),
+                                      _NAN if sm_scale is None else sm_scale, softcap, q_offset, bool(return_lse),
+                                      w.at, w.nbytes, on)
     if st:
         raise SageError(st, "scored_attn")
     return (out, lse) if return_lse else out
