@@ -3,29 +3,30 @@
 //
 //   s = sm_scale q.k; s = cap tanh(s / cap); s -= slope |i + q_offset - j|; softmax over visible j; times v
 //
-// One CTA owns two 128-row query tiles (A, B) of one (sequence, head) and walks the 128-key tiles that any of its
-// rows may see:
-//   warp 8      TMA: Q once, then K and V tiles through rings of stages, straight from the caller's tensors
-//   warps 9, 10 issue the MMAs: S = Q K^T (both operands in shared memory) and O += P V with P in tensor
-//               memory and V in its own row order (an MN-major operand), so nothing is transposed
-//   warp 11     zeroes the V rows that no row of the CTA may see (padding, what lies behind the last key seen) before
-//               their tile is multiplied
-//   warps 0-3, 4-7   softmax of tile A / B, one thread per row: S from tensor memory, score
-//               modification, mask, running maximum and sum, P to tensor memory
-// head_dim 128: 512 columns hold one S buffer per query tile beside O, and P overlays it. One warp issues for both
-// tiles, half a step apart, so that one tile's products run while the other's softmax does; P V may start
-// on the first half of P. (With an issuer per tile the two fell into step: 1072 TFLOP/s at 4 x 38 heads of 4096^2,
-// 1250 with one.) One query tile alone uses both S buffers in turn.
-// head_dim 64: P has columns of its own, each tile its issuer, and the next scores are computed as soon as the softmax
-// holds the last ones in registers.
+// One CTA owns two 128-row query tiles (A, B) of one (sequence, head), at head_dim 64 one, and walks the 128-key tiles
+// that any of its rows may see. Softmax warps first, then four control warps:
+//   softmax   four warps per query tile, one thread per row: S from tensor memory, score modification, mask,
+//             running maximum and sum, P to tensor memory
+//   control 0 TMA: Q once, then K and V tiles through rings of stages, straight from the caller's tensors
+//   control 1 issues the MMAs: S = Q K^T (both operands in shared memory) and O += P V with P in tensor memory and
+//             V in its own row order (an MN-major operand), so nothing is transposed
+//   control 3 zeroes the V rows that no row of the CTA may see (padding, what lies behind the last key seen) before
+//             their tile is multiplied
+// head_dim 128: 512 columns hold one S buffer per query tile beside O, and P overlays it. The tiles run half a step
+// apart, so that one tile's products run while the other's softmax does; P V may start on the first half of
+// P. (With an issuer per tile the two fell into step: 1072 TFLOP/s at 4 x 38 heads of 4096^2, 1250 with one.) One
+// query tile alone uses both S buffers in turn.
+// head_dim 64: P has columns of its own, and the next scores are computed as soon as the softmax holds the last ones in
+// registers. 256 columns, 97 KB and 256 threads let two CTAs share an SM, one's start and end under the other's
+// steps (one CTA of two tiles: 628 against 587 us at 4 x 38 heads of 4096^2, 271 against 255 at 8192 causal).
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the last rescale: P then stays below 2^8
 // (fp16: 2^15, see kHead) and the sum is exact in the same frame, so no precision is lost.
 //
 // Bound by the softmax warps: per score one exponential (4 cycles a warp and sub-partition), half an instruction each to
 // scale, sum and round, and the passes through tensor memory around them; products take 63% of the
 // cycles at head_dim 128. Rates (bf16, of 1884 TFLOP/s measured for a library product): 4 x 38 heads of 4096^2, head_dim 128:
-// 1484 TFLOP/s, capped 1130, biased 1386; head_dim 64: 1030, capped 656, biased 897. 32 heads of 8 at 8192, causal, 128:
-// 375 us, capped 510, biased 423, both 580.
+// 1500 TFLOP/s, capped 1140, biased 1420; head_dim 64: 1110, capped 660, biased 940. 32 heads of 8 at 8192, causal, 128:
+// 375-388 us, capped 503, biased 415, both 563.
 #include <cmath>
 
 #include "../../include/sageattn.h"
@@ -36,8 +37,6 @@
 namespace sage {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr uint32_t kRegsSoft = 224, kRegsCtl = 56;  // 2 * 128 * 224 + 128 * 56 = 384 * 168
 constexpr float kL2e = 1.4426950408889634f, kL2 = 0.6931471805599453f;
 constexpr float kNegInf = -INFINITY;
 constexpr int kMaxSplits = 32;
@@ -79,19 +78,23 @@ struct ScoredArgs {
 
 template <int DP>
 struct Cfg {
+  static constexpr int kTiles = DP == 128 ? 2 : 1;  // query tiles of a CTA
+  static constexpr int kRows = 128 * kTiles, kThreads = kRows + 128, kPerSm = 3 - kTiles;
+  static constexpr int kCtl = 4 * kTiles;  // the first of the four control warps
+  // the launch's registers, 2 x 128 x 224 + 128 x 56 = 384 x 168 or 128 x 200 + 128 x 56 = 256 x 128
+  static constexpr uint32_t kRegsSoft = kTiles == 2 ? 224 : 200, kRegsCtl = 56;
   static constexpr int kChunks = DP / 64;
   static constexpr int kQBytes = 128 * DP * 2, kKBytes = 128 * DP * 2, kVBytes = 128 * DP * 2;
-  static constexpr int kKStages = DP == 128 ? 3 : 4, kVStages = DP == 128 ? 2 : 4;
+  static constexpr int kKStages = 3, kVStages = 2;
   // tensor memory: S of tile x at 128 x; P over S (head_dim 128) or beside it; then O
   static constexpr bool kOver = DP == 128;
-  static constexpr uint32_t kTmemP = kOver ? 0 : 256, kPitchP = kOver ? 128 : 64;
-  static constexpr uint32_t kTmemO = kOver ? 256 : 384;
-  static constexpr int kOffK = 2 * kQBytes, kOffV = kOffK + kKStages * kKBytes;
+  static constexpr uint32_t kTmemP = kOver ? 0 : 128, kTmemO = kOver ? 256 : 192, kTmemCols = kOver ? 512 : 256;
+  static constexpr int kOffK = kTiles * kQBytes, kOffV = kOffK + kKStages * kKBytes;
   static constexpr int kOffBar = kOffV + kVStages * kVBytes;
   static constexpr int kNumBars = 1 + 2 * kKStages + 3 * kVStages + 12;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffMisc + 128 + 1024;
-  static_assert(kTmemO + 2 * DP <= 512 && kSmem <= 232448, "tensor and shared memory");
+  static_assert(kTmemO + kTiles * DP <= kTmemCols && kPerSm * (kSmem + 1024) <= 233472, "tensor and shared memory");
 };
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -348,7 +351,7 @@ __device__ __forceinline__ void sts(uint32_t at, int v) {
 
 // CAP / BIAS: the score modification that is compiled in; the masks are a matter of each tile.
 template <int DP, bool BF16, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kPerSm)
     scored_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const ScoredArgs a) {
   using C = Cfg<DP>;
@@ -369,19 +372,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t misc = sbase + C::kOffMisc, abort_at = misc + kWAbort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the work item: head, sequence, key split, pair of query tiles (those with the most keys first when causal)
-  const int q0 = (a.causal ? (int)(gridDim.y - 1 - blockIdx.y) : (int)blockIdx.y) * 256;
+  const int q0 = (a.causal ? (int)(gridDim.y - 1 - blockIdx.y) : (int)blockIdx.y) * C::kRows;
   const int hk = (int)blockIdx.x / a.ctas_kv, h_at = ((int)blockIdx.x - hk * a.ctas_kv) * a.heads;
   const int h0 = hk * (a.hq / a.hkv) + h_at, nh = min(a.heads, a.hq / a.hkv - h_at);  // its heads
-  const bool has_b = nh > a.per_tile || a.nq - q0 > 128;
+  const bool has_b = C::kTiles == 2 && (nh > a.per_tile || a.nq - q0 > 128);
 
   if (threadIdx.x == 0) {
-    // who releases a stage: the softmax of each tile at head_dim 64, of the last tile at 128
-    const int nx = has_b && !C::kOver ? 2 : 1;
     bar_init(q_full, 1);
-    for (int i = 0; i < C::kKStages; ++i) { bar_init(k_full + 8 * i, 1); bar_init(k_empty + 8 * i, nx); }
+    for (int i = 0; i < C::kKStages; ++i) { bar_init(k_full + 8 * i, 1); bar_init(k_empty + 8 * i, 1); }
     for (int i = 0; i < C::kVStages; ++i) {
       bar_init(v_full + 8 * i, 1);
-      bar_init(v_empty + 8 * i, nx);
+      bar_init(v_empty + 8 * i, 1);
       bar_init(v_clean + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -400,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     sts(misc + kWRed + 12, -1);
     fence_mbar_init();
   }
-  if (warp == 9) {
-    tmem_alloc(reinterpret_cast<uint32_t*>(sm + C::kOffMisc + kWTmem), 512);
+  if (warp == C::kCtl + 1) {
+    tmem_alloc(reinterpret_cast<uint32_t*>(sm + C::kOffMisc + kWTmem), C::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.err && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *a.err = 0;
 
   // Q is on its way while the key tiles are found
-  if (warp == 8 && lane == 0) {
+  if (warp == C::kCtl && lane == 0) {
     tma_prefetch_desc(&tmQ);
     const int b = (int)blockIdx.z / a.splits;
     bar_expect(q_full, (has_b ? 2 : 1) * C::kQBytes);
@@ -439,13 +440,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   {
     const int b = (int)blockIdx.z / a.splits, split = (int)blockIdx.z - b * a.splits;
-    const int rows = min(256, a.nq - q0), prefix = a.prefix ? __ldg(&a.prefix[b]) : 0;
+    const int rows = min(C::kRows, a.nq - q0), prefix = a.prefix ? __ldg(&a.prefix[b]) : 0;
     const int seen = limit_of(q0 + rows - 1, prefix);  // (what the last row sees, the rows before it see in part)
     int lo = 0, hi = (seen + 127) / 128;
     const int hi_a = (limit_of(q0 + min(rows, 128) - 1, prefix) + 127) / 128;
     if (a.doc_q) {
       int* red = reinterpret_cast<int*>(sm + C::kOffMisc + kWRed);
-      if (warp < 8) {
+      if (warp < C::kCtl) {
         const int id = (int)threadIdx.x < rows ? __ldg(&a.doc_q[(int64_t)b * a.nq + q0 + threadIdx.x]) : -1;
         const int most = __reduce_max_sync(0xffffffffu, id);
         const int least = (int)__reduce_min_sync(0xffffffffu, (unsigned)id);  // (negative ids come last)
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncthreads();
       const int dlo = red[0], dhi = red[1];
-      for (int j = threadIdx.x; j < hi; j += kThreads) {
+      for (int j = threadIdx.x; j < hi; j += C::kThreads) {
         const DocTile t = a.doc_tiles[(int64_t)b * a.k_tiles + j];
         if (t.lo <= t.hi && t.hi >= dlo && t.lo <= dhi) { atomicMin(&red[2], j); atomicMax(&red[3], j); }
       }
@@ -485,9 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
-  if (warp >= 8) {
-    regs_dec<kRegsCtl>();
-    if (warp == 8) {
+  if (warp >= C::kCtl) {
+    regs_dec<C::kRegsCtl>();
+    if (warp == C::kCtl) {
       // ========================================================= TMA producer
       const int n_tiles = lds(misc + kWTiles), row0 = lds(misc + kWJ0) * 128, b = lds(misc + kWSeq);
       const int left = lds(misc + kWLeft);
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (a.err) record_error(a.err, kDevTimeout);
         }
       }
-    } else if (warp == 11) {
+    } else if (warp == C::kCtl + 3) {
       // ================================== V rows of padding and behind the last key seen become zero
       if (lds(misc + kWClean)) {
         const int n_tiles = lds(misc + kWTiles), j0 = lds(misc + kWJ0), b = lds(misc + kWSeq);
@@ -550,9 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok && lane == 0 && a.err) record_error(a.err, kDevTimeout);
       }
-    } else if (warp == 9 || (!C::kOver && has_b)) {
+    } else if (warp == C::kCtl + 1) {
       // ========================================================= MMA issuers
-      const int me = warp - 9;
       const int n_tiles = lds(misc + kWTiles), n_a = lds(misc + kWTilesA);
       const uint32_t tmem = lds(misc + kWTmem);
       const uint32_t fmt = BF16 ? 1 : 0;
@@ -610,23 +610,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && j + lead < n) ok = issue_qk(x, j + lead, sb);
           }
       } else {
-        // An issuer per tile: the next scores as soon as the softmax holds the last ones, then P V.
-        const int n = me == 0 ? n_a : n_tiles;
+        // the next scores as soon as the softmax holds the last ones, then P V
 #pragma unroll 1
-        for (int j = -1; j < n && ok; ++j) {
-          if (j >= 0 && j + 1 < n) ok = warp_wait(s_free + 8 * me, j & 1, abort_at);
-          if (ok && j + 1 < n) ok = issue_qk(me, j + 1, me);
-          if (ok && j >= 0) ok = issue_pv(me, j, C::kTmemP + me * C::kPitchP, true);
+        for (int j = -1; j < n_tiles && ok; ++j) {
+          if (j >= 0 && j + 1 < n_tiles) ok = warp_wait(s_free, j & 1, abort_at);
+          if (ok && j + 1 < n_tiles) ok = issue_qk(0, j + 1, 0);
+          if (ok && j >= 0) ok = issue_pv(0, j, C::kTmemP, true);
         }
       }
       // every MMA has finished before tensor memory is released
-      commit_to(drain + 8 * me);
-      warp_wait(drain + 8 * me, 0, 0);
+      commit_to(drain);
+      warp_wait(drain, 0, 0);
       __syncwarp();
       if (!ok && lane == 0 && a.err) record_error(a.err, kDevTimeout);
     }
   } else {
-    regs_inc<kRegsSoft>();
+    regs_inc<C::kRegsSoft>();
     // =========================================================== softmax of tile x
     const int x = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -647,7 +646,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr float kSlack = BF16 ? 60.0f : 7.0f;  // by how much a maximum may be overestimated
     float slope = 0.f;
     if constexpr (BIAS) slope = __ldg(&a.slopes[h]) * kL2e;
-    // (a warp's rows may be of heads with different slopes)
+    // (a warp's rows may be of heads with different slopes; where fp16's few bits of slack make many slopes steep, their
+    // maximum is taken exactly)
+    constexpr bool kExact = !BF16 && !CAP;
     const bool gentle = !BIAS || __all_sync(0xffffffffu, fabsf(slope) * 15.0f <= kSlack);
     const float cap_m2 = -2.0f * a.cap2, cap_in = a.cap_k;
     // fp16 weights are held at up to 2^(7 + 8): 7 bits more before the smallest lose bits
@@ -655,34 +656,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = kNegInf;                             // the frame, base 2
     float l = 0.f;
     bool ok = true;
-    uint32_t s[4][32];
-    float cm[BIAS ? 8 : 4];  // the largest products of 16 or 32 keys
-    // the products of step j into s, with their maxima; valid after have_s()
-    auto load_s = [&](int j) {
-      const int sb = solo ? j & 1 : x;
-      const uint32_t tS = tmem + lane_base + sb * 128;
-      ok = warp_wait(s_full + 8 * sb, (solo ? j >> 1 : j) & 1, abort_at);
-      if (!ok) return;
-        if (releases) {  // K of this tile has been read, and V of the last (where this barrier tells it)
-          bar_arrive(k_empty + 8 * ((uint32_t)j % C::kKStages));
-          if (C::kOver && !solo && j > 0) bar_arrive(v_empty + 8 * ((uint32_t)(j - 1) % C::kVStages));
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if constexpr (BIAS) {
-            ld16_max<0>(tS + c * 32, s[c], cm[2 * c]);
-            ld16_max<16>(tS + c * 32 + 16, s[c], cm[2 * c + 1]);
-          } else {
-            ld32_max(tS + c * 32, s[c], cm[c]);
-          }
-        }
-    };
-    auto have_s = [&]() {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
-      wait_ld_max(cm);
-    };
     // the document that a tile's keys are all of, or -2; read a step ahead
     auto only_of = [&](int j) {
       const DocTile t = a.doc_tiles[(int64_t)b * a.k_tiles + j0 + (BIAS ? tile_of(j, left) : j)];
@@ -692,24 +665,185 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (active) {
       for (int j = 0; j < my_tiles && ok; ++j, only = only_next) {
         if (a.doc_k && j + 1 < my_tiles) only_next = only_of(j + 1);
-        load_s(j);
-        if (!ok) break;
-        const uint32_t tP = tmem + lane_base + (C::kOver ? (solo ? j & 1 : x) * 128 : C::kTmemP + x * C::kPitchP);
+        const int sb = solo ? j & 1 : x;
+        const uint32_t tS = tmem + lane_base + sb * 128, tP = C::kOver ? tS : tmem + lane_base + C::kTmemP;
         const int tile = j0 + (BIAS ? tile_of(j, left) : j), kv0 = tile * 128;
-        // ---- which keys of the tile this row sees, as bits (only where some row of the warp misses one)
+        // ---- does every row of the warp see every key of the tile?
         bool whole = limit - kv0 >= 128;
         if (a.doc_k) whole = whole && only == dq;
         whole = whole || !valid;  // (rows behind the last one are not written)
-        const bool masked = !__all_sync(0xffffffffu, whole);
+        // The bias along a tile that lies on one side of every row's position is base + step u. Its largest value
+        // beside the largest product of each 16 keys bounds the maximum by at most 15 steps too much, which the
+        // frame's headroom takes where they are few.
+        bool fast = __all_sync(0xffffffffu, whole);
+        float mul = a.c2, step = 0.f, base = 0.f;
+        const float dist = static_cast<float>(pos - kv0);  // exact below 2^24
+        if constexpr (BIAS) {
+          const bool all_left = __all_sync(0xffffffffu, kv0 + 127 <= pos);
+          fast = fast && (gentle || kExact) && (all_left || __all_sync(0xffffffffu, kv0 >= pos));
+          step = all_left ? slope : -slope;
+          base = -step * dist;
+        }
+        ok = warp_wait(s_full + 8 * sb, (solo ? j >> 1 : j) & 1, abort_at);
+        if (!ok) break;
+        if (releases) {  // K of this tile has been read, and V of the last (where this barrier tells it)
+          bar_arrive(k_empty + 8 * ((uint32_t)j % C::kKStages));
+          if (C::kOver && !solo && j > 0) bar_arrive(v_empty + 8 * ((uint32_t)(j - 1) % C::kVStages));
+        }
+        tc_fence_after();
         float t_max = kNegInf, m_use = 0.f;
         float g0 = 0.f, g1 = 0.f, g2 = 0.f, g3 = 0.f;
-        // S is in registers
-        auto release_s = [&]() {
-          if constexpr (!C::kOver) {
-            tc_fence_before();
-            bar_arrive(s_free + 8 * x);
+        uint32_t s[4][32];
+        if (fast) {
+          // the products; cap and scale keep their order, so the largest of each 16 or 32 gives the maximum
+          float cm[BIAS ? 8 : 4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if constexpr (BIAS) {
+              ld16_max<0>(tS + c * 32, s[c], cm[2 * c]);
+              ld16_max<16>(tS + c * 32 + 16, s[c], cm[2 * c + 1]);
+            } else {
+              ld32_max(tS + c * 32, s[c], cm[c]);
+            }
           }
-        };
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+          wait_ld_max(cm);
+          auto capped = [&](float v) {
+            return CAP ? fmaf(rcpf(1.0f + ex2f(v * cap_in)), cap_m2, a.cap2) : v * a.c2;
+          };
+          if constexpr (BIAS) {
+            if (gentle || !kExact) {
+              const float end = step > 0.f ? 15.0f * step : 0.f;
+#pragma unroll
+              for (int c = 0; c < 8; ++c) t_max = fmaxf(t_max, fmaf(step, static_cast<float>(c * 16), capped(cm[c])));
+              t_max += end;
+            } else {  // (steep slopes: the maximum itself)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                for (int u = 0; u < 32; u += 2) {
+                  float f0, f1;
+                  fma2(f0, f1, __uint_as_float(s[c][u]), __uint_as_float(s[c][u + 1]), a.c2, a.c2,
+                       step * static_cast<float>(c * 32 + u), step * static_cast<float>(c * 32 + u + 1));
+                  t_max = max3(t_max, f0, f1);
+                }
+              }
+            }
+            t_max += base;
+          } else {
+            t_max = capped(fmaxf(max3(cm[0], cm[1], cm[2]), cm[3]));
+          }
+          if constexpr (CAP) {
+            // every product of the warp within the polynomial's range?
+            float big = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+              for (int u = 0; u < 32; u += 2)
+                big = max3(big, fabsf(__uint_as_float(s[c][u])), fabsf(__uint_as_float(s[c][u + 1])));
+            }
+            fast = __all_sync(0xffffffffu, big <= a.poly.most);
+          }
+        }
+        if (!fast) {
+          // 32 or 64 keys at a time, in place: scores (products, where there is neither cap nor bias), masked. A loop, since
+          // the CTAs and warps of an SM are seldom in the same place and share the instruction cache: as straight
+          // code of 128 keys, plain prompts took 8% longer at head_dim 64. (Capped and biased, 64 keys are longer
+          // than 32: packed documents 148 against 141 us; plain shorter, 81 against 88.)
+          int id[4] = {-1, -1, -1, -1};
+          const bool by_doc = a.doc_k && !__all_sync(0xffffffffu, only == dq || !valid);
+          if (by_doc) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int key = kv0 + c * 32 + lane;
+              if (key < a.nk) id[c] = __ldg(&a.doc_k[(int64_t)b * a.nk + key]);
+            }
+          }
+          t_max = kNegInf;
+          constexpr int kN = CAP || BIAS ? 1 : 2;
+#pragma unroll 1
+          for (int c = 0; c < 4; c += kN) {
+            uint32_t part[kN][32], bits[kN];
+#pragma unroll
+            for (int i = 0; i < kN; ++i) tmem_ld32(tS + (c + i) * 32, part[i]);
+            // which of the keys this row sees, as bits; each document among the warp's rows in turn, its keys by ballot
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+              const int k = limit - kv0 - (c + i) * 32;
+              bits[i] = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+            }
+            if (by_doc) {
+              uint32_t todo = __ballot_sync(0xffffffffu, dq >= 0), mine[kN] = {};
+              while (todo) {
+                const int one = __shfl_sync(0xffffffffu, dq, __ffs(todo) - 1);
+                const bool me = dq == one;
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                  const uint32_t v = __ballot_sync(0xffffffffu, (c + i == 0 ? id[0] : c + i == 1 ? id[1] : c + i == 2 ? id[2] : id[3]) == one);
+                  if (me) mine[i] = v;
+                }
+                todo &= ~__ballot_sync(0xffffffffu, me);
+              }
+#pragma unroll
+              for (int i = 0; i < kN; ++i) bits[i] &= mine[i];
+            }
+#pragma unroll
+            for (int i = 0; i < kN; ++i) tmem_wait_ld(part[i]);
+            bool small = false;
+            if constexpr (CAP) {
+              float big = 0.f;
+#pragma unroll
+              for (int i = 0; i < kN; ++i) {
+#pragma unroll
+                for (int u = 0; u < 32; u += 2)
+                  big = max3(big, fabsf(__uint_as_float(part[i][u])), fabsf(__uint_as_float(part[i][u + 1])));
+              }
+              small = __all_sync(0xffffffffu, big <= a.poly.most);
+            }
+#pragma unroll
+            for (int g = 0; g < 2 * kN; ++g) {
+              const int i = g >> 1, at = (g & 1) * 16;
+              float t[16];
+#pragma unroll
+              for (int u = 0; u < 16; ++u) t[u] = __uint_as_float(part[i][at + u]);
+              if constexpr (CAP) {
+                if (small) cap_polynomial(t, a.poly);
+                else cap_quotient(t, cap_in, cap_m2, a.cap2);
+              }
+              if constexpr (BIAS) {
+                const float d0 = dist - static_cast<float>(c * 32 + g * 16);
+#pragma unroll
+                for (int u = 0; u < 16; u += 2) {
+                  const float b0 = -slope * fabsf(d0 - static_cast<float>(u)), b1 = -slope * fabsf(d0 - static_cast<float>(u + 1));
+                  if constexpr (CAP) add2(t[u], t[u + 1], t[u], t[u + 1], b0, b1);
+                  else fma2(t[u], t[u + 1], t[u], t[u + 1], a.c2, a.c2, b0, b1);
+                }
+              }
+#pragma unroll
+              for (int u = 0; u < 16; ++u) {
+                t[u] = bits[i] >> (at + u) & 1u ? t[u] : kNegInf;
+                part[i][at + u] = __float_as_uint(t[u]);
+              }
+#pragma unroll
+              for (int u = 0; u < 16; u += 2) t_max = max3(t_max, t[u], t[u + 1]);
+            }
+#pragma unroll
+            for (int i = 0; i < kN; ++i) tmem_st32(tS + (c + i) * 32, part[i]);
+          }
+          tmem_wait_st();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+          mul = CAP || BIAS ? 1.0f : a.c2;
+          t_max *= CAP || BIAS ? 1.0f : a.c2;
+          step = base = 0.f;
+        }
+        if constexpr (!C::kOver) {  // S is in registers
+          tc_fence_before();
+          bar_arrive(s_free + 8 * x);
+        }
         // P V of the tile before is done: O may be rescaled, P overwritten (it also keeps p_full at most one
         // phase ahead of its issuer). Two tiles at head_dim 128 know it from the scores' barrier.
         auto wait_pv = [&]() {
@@ -719,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         // The frame m lies kHead below the maximum that set it, and is kept unless that grew by more than 8.
-        auto reframe = [&]() {
+        {
           t_max -= kHead;
           const bool grow = t_max > m + 8.0f || (m == kNegInf && t_max > kNegInf);
           if (__any_sync(0xffffffffu, grow)) {
@@ -732,83 +866,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           m_use = m == kNegInf ? 0.f : m;
-        };
-        // P = 2^(t - m), summed in 32 bits, rounded once to the operands' type. FORM says what s holds: 0 the
-        // scores t; 1 products; 2, 3 products to be capped, by quotient or by polynomial; LINE adds a bias of
-        // base + step u. Eight keys enter per round; a pair's arithmetic, its exponentials and its
-        // sum and rounding lie one round apart and are issued in turn, so that the special-function unit (four
-        // cycles per exponential and warp) never waits for the others.
-        auto weights = [&](auto form, auto line, float step, float base) {
-          constexpr int FORM = decltype(form)::value;
-          constexpr bool LINE = decltype(line)::value;
-          constexpr int kLag = FORM == 2 ? 3 : 2;
-          const float off = (FORM == 2 ? a.cap2 : 0.f) - m_use + base;
+        }
+        if (!ok) break;
+        // P = 2^(t - m), summed in 32 bits, rounded once to the operands' type; t is mul s, or with POLY s capped by
+        // the polynomial, and LINE adds a bias of base + step u. Eight keys enter per round; a pair's arithmetic, its
+        // exponentials and its sum and rounding lie one round apart and are issued in turn, so that the
+        // special-function unit (four cycles per exponential and warp) never waits for the others.
+        auto weights = [&](auto poly, auto line) {
+          constexpr bool POLY = decltype(poly)::value, LINE = decltype(line)::value;
+          const float off = base - m_use;
           float st[LINE ? 8 : 1];
           if constexpr (LINE) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) st[u] = step * static_cast<float>(u);
           }
-          float r0[8], r1[8], r2[8];  // rounds in flight, the newest first
+          float r0[8], r1[8];  // rounds in flight, the newest first
 #pragma unroll
-          for (int q = 0; q < 16 + kLag; ++q) {
-            float in[8], mid[8], o8 = off;
-            if constexpr (LINE) o8 = fmaf(step, static_cast<float>((FORM == 2 ? q - 2 : q) * 8), off);
+          for (int q = 0; q < 18; ++q) {
+            float in[8], mid[8], z[8], y[8], o8 = off;
+            if constexpr (LINE) o8 = fmaf(step, static_cast<float>(q * 8), off);
             if (q < 16) {
 #pragma unroll
               for (int u = 0; u < 8; ++u) in[u] = __uint_as_float(s[q >> 2][(q & 3) * 8 + u]);
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) mid[u] = FORM == 2 ? r1[u] : r0[u];
-            float z[8], y[8];
+            for (int u = 0; u < 8; ++u) mid[u] = r0[u];
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
               // exponentials of the round before
-              if (FORM == 2) {
-                if (q >= 2 && q < 18) {
-                  float f0 = o8, f1 = o8;
-                  if constexpr (LINE) add2(f0, f1, st[i], st[i + 1], o8, o8);
-                  fma2(mid[i], mid[i + 1], mid[i], mid[i + 1], cap_m2, cap_m2, f0, f1);
-                  mid[i] = ex2f(mid[i]);
-                  mid[i + 1] = ex2f(mid[i + 1]);
-                }
-                if (q >= 1 && q < 17) {
-                  add2(r0[i], r0[i + 1], r0[i], r0[i + 1], 1.0f, 1.0f);
-                  r0[i] = rcpf(r0[i]);
-                  r0[i + 1] = rcpf(r0[i + 1]);
-                }
-              } else if (q >= 1 && q < 17) {
+              if (q >= 1 && q < 17) {
                 mid[i] = ex2f(mid[i]);
                 mid[i + 1] = ex2f(mid[i + 1]);
               }
               // arithmetic of the new round
               if (q < 16) {
-                float f0 = o8, f1 = o8;
-                if constexpr (LINE && FORM != 2 && FORM != 3) add2(f0, f1, st[i], st[i + 1], o8, o8);
-                if constexpr (FORM == 0) add2(in[i], in[i + 1], in[i], in[i + 1], f0, f1);
-                if constexpr (FORM == 1) fma2(in[i], in[i + 1], in[i], in[i + 1], a.c2, a.c2, f0, f1);
-                if constexpr (FORM == 2) {
-                  mul2(in[i], in[i + 1], in[i], in[i + 1], cap_in, cap_in);
-                  in[i] = ex2f(in[i]);
-                  in[i + 1] = ex2f(in[i + 1]);
+                if constexpr (POLY) {
+                  cap_step(a.poly, i / 2, in, z, y, [&](int u) { return LINE ? st[u] : 0.f; }, LINE, o8);
+                } else {
+                  float f0 = o8, f1 = o8;
+                  if constexpr (LINE) add2(f0, f1, st[i], st[i + 1], o8, o8);
+                  fma2(in[i], in[i + 1], in[i], in[i + 1], mul, mul, f0, f1);
                 }
-                if constexpr (FORM == 3) cap_step(a.poly, i / 2, in, z, y, [&](int u) { return LINE ? st[u] : 0.f; }, LINE, o8);
               }
               // sum and rounding of the oldest round
-              if (q >= kLag) {
-                const float e0 = FORM == 2 ? r2[i] : r1[i], e1 = FORM == 2 ? r2[i + 1] : r1[i + 1];
-                if (i & 2) add2(g2, g3, g2, g3, e0, e1);
-                else add2(g0, g1, g0, g1, e0, e1);
-                const int w = (q - kLag) * 4 + i / 2;
-                s[w >> 5][w & 31] = pack16<BF16>(e0, e1);
+              if (q >= 2) {
+                if (i & 2) add2(g2, g3, g2, g3, r1[i], r1[i + 1]);
+                else add2(g0, g1, g0, g1, r1[i], r1[i + 1]);
+                const int w = (q - 2) * 4 + i / 2;
+                s[w >> 5][w & 31] = pack16<BF16>(r1[i], r1[i + 1]);
               }
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-              if (FORM == 2) { r2[u] = mid[u]; r1[u] = r0[u]; }
-              else r1[u] = mid[u];
+              r1[u] = mid[u];
               r0[u] = in[u];
             }
-            if (q == 7 + kLag) {
+            if (q == 9) {
               wait_pv();
               if (!ok) return;
               if (releases && j > 0 && (!C::kOver || solo)) bar_arrive(v_empty + 8 * ((uint32_t)(j - 1) % C::kVStages));
@@ -819,142 +932,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bar_arrive(p_half + 8 * x);
               }
             }
-            if (q == 15 + kLag) tmem_st32(tP + 32, s[1]);
+            if (q == 17) tmem_st32(tP + 32, s[1]);
           }
         };
-        using No = std::false_type;
-        using Yes = std::true_type;
-        // Weights from products; the polynomial where every product of the warp is within its range.
-        auto weights_of = [&](auto line, bool small, float step, float base) {
-          if constexpr (CAP) {
-            if (small) weights(std::integral_constant<int, 3>{}, line, step, base);
-            else weights(std::integral_constant<int, 2>{}, line, step, base);
-          } else {
-            weights(std::integral_constant<int, 1>{}, line, step, base);
-          }
-        };
-        // The bias along a tile that lies on one side of every row's position (or whose other side the causal
-        // mask hides) is base + step u. Its largest value beside the largest product of each 16 keys bounds the
-        // maximum by at most 15 steps too much, which the frame's headroom takes where they are few.
-        float step = 0.f, base = 0.f;
-        bool line = true;
-        if constexpr (BIAS) {
-          const float dist = static_cast<float>(pos - kv0);  // exact below 2^24
-          const bool all_left = __all_sync(0xffffffffu, kv0 + 127 <= pos || (a.causal && prefix <= 0));
-          line = all_left || __all_sync(0xffffffffu, kv0 >= pos);
-          step = all_left ? slope : -slope;
-          base = -step * dist;
-        }
-        // whether every product of the warp is within the polynomial's range
-        auto all_small = [&]() {
-          float big = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int u = 0; u < 32; u += 2)
-              big = max3(big, fabsf(__uint_as_float(s[c][u])), fabsf(__uint_as_float(s[c][u + 1])));
-          return __all_sync(0xffffffffu, big <= a.poly.most) != 0;
-        };
-        if (!masked && (!BIAS || (line && gentle))) {
-          // products; the cap and the scale keep their order, so their largest gives the maximum
-          bool small = false;
-          auto capped = [&](float v) {
-            return CAP ? fmaf(rcpf(1.0f + ex2f(v * cap_in)), cap_m2, a.cap2) : v * a.c2;
-          };
-          have_s();
-          if constexpr (BIAS) {
-            const float end = step > 0.f ? 15.0f * step : 0.f;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) t_max = fmaxf(t_max, fmaf(step, static_cast<float>(c * 16), capped(cm[c])));
-            t_max += base + end;
-          } else {
-            t_max = capped(fmaxf(max3(cm[0], cm[1], cm[2]), cm[3]));
-          }
-          if constexpr (CAP) small = all_small();
-          release_s();
-          reframe();
-          if constexpr (BIAS) weights_of(Yes{}, small, step, base);
-          else weights_of(No{}, small, 0.f, 0.f);
+        if constexpr (CAP) {
+          if (fast) weights(std::true_type{}, std::integral_constant<bool, BIAS>{});
+          else weights(std::false_type{}, std::false_type{});
         } else {
-          have_s();
-          release_s();
-          const bool small = CAP && all_small();
-          // scores in base 2: capped or scaled, then biased
-          auto scores = [&](auto bias_at) {
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              float t[16];
-#pragma unroll
-              for (int u = 0; u < 16; ++u) t[u] = __uint_as_float(s[g >> 1][(g & 1) * 16 + u]);
-              if constexpr (CAP) {
-                if (small) cap_polynomial(t, a.poly);
-                else cap_quotient(t, cap_in, cap_m2, a.cap2);
-              }
-              if constexpr (BIAS) {
-#pragma unroll
-                for (int u = 0; u < 16; u += 2) {
-                  const float b0 = bias_at(g * 16 + u), b1 = bias_at(g * 16 + u + 1);
-                  if constexpr (CAP) add2(t[u], t[u + 1], t[u], t[u + 1], b0, b1);
-                  else fma2(t[u], t[u + 1], t[u], t[u + 1], a.c2, a.c2, b0, b1);
-                }
-              } else if constexpr (!CAP) {
-                each2(t, [&](float& p, float& q) { mul2(p, q, p, q, a.c2, a.c2); });
-              }
-#pragma unroll
-              for (int u = 0; u < 16; ++u) s[g >> 1][(g & 1) * 16 + u] = __float_as_uint(t[u]);
-            }
-          };
-          if constexpr (BIAS) {
-            const float dist = static_cast<float>(pos - kv0);
-            if (line) scores([&](int u) { return fmaf(step, static_cast<float>(u), base); });
-            else scores([&](int u) { return -slope * fabsf(dist - static_cast<float>(u)); });
-          } else {
-            scores([](int) { return 0.f; });
-          }
-          if (masked) {
-            uint32_t bits[4];
-            const int n = limit - kv0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int k = n - c * 32;
-              bits[c] = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
-            }
-            if (a.doc_k) {
-              int id[4];
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const int key = kv0 + c * 32 + lane;
-                id[c] = key < a.nk ? __ldg(&a.doc_k[(int64_t)b * a.nk + key]) : -1;
-              }
-              // each document among the warp's rows in turn: its keys by ballot
-              uint32_t todo = __ballot_sync(0xffffffffu, dq >= 0);
-              uint32_t mine[4] = {0, 0, 0, 0};
-              while (todo) {
-                const int one = __shfl_sync(0xffffffffu, dq, __ffs(todo) - 1);
-                const bool me = dq == one;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  const uint32_t v = __ballot_sync(0xffffffffu, id[c] == one);
-                  if (me) mine[c] = v;
-                }
-                todo &= ~__ballot_sync(0xffffffffu, me);
-              }
-#pragma unroll
-              for (int c = 0; c < 4; ++c) bits[c] &= mine[c];
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int u = 0; u < 32; ++u)
-                if (!(bits[c] >> u & 1u)) s[c][u] = __float_as_uint(kNegInf);
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int u = 0; u < 32; u += 2)
-              t_max = max3(t_max, __uint_as_float(s[c][u]), __uint_as_float(s[c][u + 1]));
-          reframe();
-          weights(std::integral_constant<int, 0>{}, No{}, 0.f, 0.f);
+          weights(std::false_type{}, std::integral_constant<bool, BIAS>{});
         }
         if (!ok) break;
         l += (g0 + g1) + (g2 + g3);
@@ -1023,10 +1008,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == C::kCtl + 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(lds(misc + kWTmem), 512);
+    tmem_dealloc(lds(misc + kWTmem), C::kTmemCols);
   }
 }
 
@@ -1122,8 +1107,8 @@ struct ScoredLayout {
   int heads, per_tile, row_bits, ctas_kv, splits;
 };
 // Key splits: where the items leave SMs idle, as many as fill one wave, of at least four key tiles each.
-int splits_of(int64_t items, int64_t tiles) {
-  int64_t s = items > 0 ? 152 / items : 1;
+int splits_of(int64_t items, int64_t tiles, int slots) {
+  int64_t s = items > 0 ? slots / items : 1;
   if (s > tiles / 4) s = tiles / 4;
   if (s > kMaxSplits) s = kMaxSplits;
   return s < 1 ? 1 : (int)s;
@@ -1135,18 +1120,20 @@ int splits_of(int64_t items, int64_t tiles) {
 void plan_items(int batch, int hq, int hkv, int nq, int nk, ScoredLayout* L) {
   const int group = hq / hkv;
   const int64_t tiles = L->k_tiles;
+  const int rows = L->dp == 128 ? Cfg<128>::kRows : Cfg<64>::kRows;  // of a CTA
+  const int slots = 152 * (L->dp == 128 ? Cfg<128>::kPerSm : Cfg<64>::kPerSm);
   int bits = 3;
   while (bits < 7 && 1 << bits < nq) ++bits;
   int64_t best = -1;
-  for (int form = 0; form < (nq <= 128 && group > 1 ? 3 : 1); ++form) {
+  for (int form = 0; form < (nq <= 128 && group > 1 ? 1 + rows / 128 : 1); ++form) {
     const int per_tile = form == 0 ? 1 : 128 >> bits, room = form == 2 ? 2 * per_tile : per_tile;
     const int heads = form == 0 ? 1 : group < room ? group : room;
     if (form == 1 && heads == 1) continue;
     const int ctas_kv = (group + heads - 1) / heads;
-    const int64_t items = (int64_t)batch * hkv * ctas_kv * (((int64_t)nq + 255) / 256);
-    const int splits = splits_of(items, tiles);
-    const bool two = form == 0 ? nq > 128 : heads > per_tile;
-    const int64_t waves = (items * splits + 151) / 152;
+    const int64_t items = (int64_t)batch * hkv * ctas_kv * (((int64_t)nq + rows - 1) / rows);
+    const int splits = splits_of(items, tiles, slots);
+    const bool two = rows > 128 && (form == 0 ? nq > 128 : heads > per_tile);
+    const int64_t waves = (items * splits + slots - 1) / slots;
     const int64_t time = waves * ((tiles + splits - 1) / splits * (two ? 8 : 5) + 20) + (splits > 1 ? 20 : 0);
     if (best < 0 || time < best) {
       best = time;
@@ -1179,7 +1166,7 @@ cudaError_t launch_scored_t(const ScoredArgs& a, const CUtensorMap* maps, dim3 g
   static std::atomic<int> limits[64];
   cudaError_t e = raise_smem_limit(scored_kernel<DP, BF16, CAP, BIAS>, Cfg<DP>::kSmem, limits);
   if (e != cudaSuccess) return e;
-  return launch_pdl(scored_kernel<DP, BF16, CAP, BIAS>, grid, dim3(kThreads), Cfg<DP>::kSmem, st, maps[0], maps[1],
+  return launch_pdl(scored_kernel<DP, BF16, CAP, BIAS>, grid, dim3(Cfg<DP>::kThreads), Cfg<DP>::kSmem, st, maps[0], maps[1],
                     maps[2], a);
 }
 template <int DP, bool BF16>
@@ -1254,9 +1241,10 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
   }
   const bool packed = fits[0] && fits[1] && fits[2];
   if (!scored_layout(batch, heads_q, heads_kv, seqlen_q, seqlen_k, head_dim, packed, doc_k != nullptr, &L)) return SAGE_ERR_INVALID_ARG;
-  const int64_t pairs = ((int64_t)seqlen_q + 255) / 256;
+  const int cta_rows = L.dp == 128 ? Cfg<128>::kRows : Cfg<64>::kRows;
+  const int64_t blocks_q = ((int64_t)seqlen_q + cta_rows - 1) / cta_rows;
   if (seqlen_k > 0x7fffff00 || seqlen_q > 0x7fffff00 || (int64_t)q_offset + seqlen_q > 0x7fffff00 ||
-      q_offset < -0x7fffff00 || pairs > 65535 || (int64_t)batch * L.splits > 65535 || (int64_t)batch * heads_q * seqlen_q > (1LL << 32))
+      q_offset < -0x7fffff00 || blocks_q > 65535 || (int64_t)batch * L.splits > 65535 || (int64_t)batch * heads_q * seqlen_q > (1LL << 32))
     return SAGE_ERR_INVALID_ARG;
   // (the status word alone can do without)
   if (workspace ? reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < L.total : L.total > SAGE_STATUS_BYTES)
@@ -1270,7 +1258,7 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
   a.heads = L.heads; a.per_tile = L.per_tile; a.row_bits = L.row_bits; a.ctas_kv = L.ctas_kv;
   const float scale =
       std::isnan(sm_scale) || sm_scale <= 0.f ? (float)(1.0 / std::sqrt((double)head_dim)) : sm_scale;
-  a.c2 = (float)(scale * 1.4426950408889634);
+  a.c2 = std::fmax((float)(scale * 1.4426950408889634), 1.2e-38f);  // (-inf times it is -inf)
   a.cap2 = (float)(softcap * 1.4426950408889634);
   const double tanh_c[5] = {0.9999997019767761, -0.3333034813404083, 0.13282497227191925, -0.050881292670965195,
                             0.013819585554301739};
@@ -1321,7 +1309,7 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
     scored_setup_kernel<<<dim3(L.k_tiles, batch), 128, 0, st>>>(a);
     e = cudaGetLastError();
   }
-  const dim3 grid((unsigned)(heads_kv * L.ctas_kv), (unsigned)pairs, (unsigned)(batch * L.splits));
+  const dim3 grid((unsigned)(heads_kv * L.ctas_kv), (unsigned)blocks_q, (unsigned)(batch * L.splits));
   if (e == cudaSuccess) {
     if (dtype == SAGE_BF16)
       e = L.dp == 64 ? launch_scored<64, true>(a, maps, grid, st) : launch_scored<128, true>(a, maps, grid, st);
