@@ -4,6 +4,7 @@
 
 #include "launch.h"
 #include "paged.cuh"
+#include "sm103_ptx.cuh"
 
 namespace sage {
 
@@ -175,23 +176,40 @@ __device__ __forceinline__ int block_scan(int x, int& total) {
   return inc - x + (warp ? s[warp - 1] : 0);
 }
 
-// One CTA per (head, sequence). The budget-th largest weight is found by a radix selection over the
+// Words of another CTA of the cluster.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int ld_rank(const int* p, int rank) {
+  int v;
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.u32 %0, [a];\n\t}"
+      : "=r"(v)
+      : "r"(smem_u32(p)), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// One CTA per (head, sequence), or a cluster of R, each with a stretch of the slots. The budget-th largest weight is found by a radix selection over the
 // ordered codes (three digits of 11, 11 and 10 bits, one histogram each: integer counts, so the
 // result does not depend on any order); then the slots are walked in order, ties taken from the
 // lowest slot on, and the freed slots below the budget and the kept ones behind it are listed.
 // A pass over the planes is a chain of two dependent loads per slot (page, then value), so they are read once
 // each with eight slots per thread in flight, and the codes stay in shared memory for the passes of
 // the selection, which read four at a time. (A sequence with more tokens than fit is read again, in
-// chunks, by each pass.) 64 heads of 6000 to 32768 tokens, cut to 4096: 33 us here, then 37 to move the rows, which is 75%
-// of a copy's rate; the selection is bound by the latency of its passes on the 64 SMs that have a CTA.
+// chunks, by each pass.) 64 heads of 6000 to 32768 tokens, cut to 4096: 26 us here by clusters of two (33 by one CTA each), then
+// 37 to move the rows, which is 75% of a copy's rate; the selection is bound by the latency of its passes.
 constexpr int kAhead = 8;
 constexpr int kMostCached = 48 * 1024;
+template <int R>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) unsigned codes[];  // of `cached` slots; 0: no token
   __shared__ int hist[kBins];
   __shared__ int s_pick, s_rest, s_last, s_bad;
   __shared__ int s_cnt[32][4];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int s_give[4];  // what the other CTAs of the cluster read
+  const int rank = R > 1 ? (int)(blockIdx.x % R) : 0;
+  const int h = blockIdx.x / R, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t me = (int64_t)b * a.c.hkv + h;
   pdl_wait();
   const int len = checked_len(a.c, b, a.max_len);
@@ -200,13 +218,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   __syncthreads();
   const int keep = a.budget;
   if (len <= keep) {  // nothing to drop (or a length that is refused)
-    if (tid == 0) {
+    if (tid == 0 && rank == 0) {
       a.count[me] = 0;
       a.block_err[me] = s_bad;
       if (h == 0) a.new_lens[b] = a.c.lens[b];
     }
     return;
   }
+  const int per = ((len + R - 1) / R + 3) & ~3;
+  const int begin = min(len, rank * per), stop = min(len, begin + per);  // this CTA's slots
   const int* table = a.c.table + b * a.c.table_stride;
   // Plane indexes of eight groups of slots, the first of group u at j0 + u G kSelThreads, or -1 (behind `end`; or
   // on a bad page, which sets `bad`). A group is the G slots of one thread, in one page. Pages are loaded
@@ -251,14 +271,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   auto newest = [&](auto g) {
     constexpr int G = decltype(g)::value;
     int last = INT32_MIN;
-    for (int j0 = tid * G; j0 < len; j0 += kSelThreads * kAhead) {
+    for (int j0 = begin + tid * G; j0 < stop; j0 += kSelThreads * kAhead) {
       int64_t w[kAhead];
       int p[kAhead];
-      where(g, j0, len, w);
+      where(g, j0, stop, w);
       take(g, a.c.pos, w, INT32_MIN, p);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
-        if (w[u / G] >= 0 && j0 + (u / G) * G * kSelThreads + u % G < len) last = max(last, p[u]);
+        if (w[u / G] >= 0 && j0 + (u / G) * G * kSelThreads + u % G < stop) last = max(last, p[u]);
     }
     return last;
   };
@@ -270,18 +290,28 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     if (bad) s_bad = kDevPage;
   }
   __syncthreads();
-  if (h == 0 && tid == 0) a.new_lens[b] = s_bad ? len : keep;  // (every head reads the same pages)
-  if (s_bad) {
-    if (tid == 0) { a.count[me] = 0; a.block_err[me] = s_bad; }
+  int newest_pos = s_last, wrong = s_bad;
+  if constexpr (R > 1) {
+    if (tid < 2) s_give[tid] = tid == 0 ? s_last : s_bad;
+    cluster_sync();
+    for (int i = 0; i < R; ++i) {
+      newest_pos = max(newest_pos, ld_rank(&s_give[0], i));
+      wrong = max(wrong, ld_rank(&s_give[1], i));
+    }
+    cluster_sync();
+  }
+  if (h == 0 && rank == 0 && tid == 0) a.new_lens[b] = wrong ? len : keep;  // (every head reads the same pages)
+  if (wrong) {
+    if (tid == 0 && rank == 0) { a.count[me] = 0; a.block_err[me] = wrong; }
     return;
   }
-  const int64_t recent_from = (int64_t)s_last - a.recent;
+  const int64_t recent_from = (int64_t)newest_pos - a.recent;
   const int cap = a.cached;  // a multiple of 4
-  const bool once = len <= cap;
+  const bool once = R > 1 || len <= cap;  // (clusters: the host saw to it)
   // codes of the slots [c0, c0 + cap); their first digit is counted with `count`
   auto load_group = [&](auto g, int c0, int n, bool count) {
     constexpr int G = decltype(g)::value;
-    const int end = min(c0 + n, len);
+    const int end = min(c0 + n, stop);
     for (int j0 = tid * G; j0 < n; j0 += kSelThreads * kAhead) {
       int64_t w[kAhead];
       int p[kAhead];
@@ -309,14 +339,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     }
   };
   auto load_codes = [&](int c0, bool count) {
-    const int n = min(cap, (len - c0 + 3) & ~3);
+    const int n = min(cap, (stop - c0 + 3) & ~3);
     if (a.vec4) load_group(Four{}, c0, n, count);
     else load_group(One{}, c0, n, count);
     return n;
   };
   int loaded = 0;
   if (once) {
-    loaded = load_codes(0, true);
+    loaded = load_codes(begin, true);
     __syncthreads();
   }
   unsigned prefix = 0, mask = 0;
@@ -329,7 +359,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       __syncthreads();
     }
     if (digit > 0 || !once)
-      for (int c0 = 0; c0 < len; c0 += cap) {
+      for (int c0 = begin; c0 < stop; c0 += cap) {
         const int n = once ? loaded : load_codes(c0, digit == 0);
         if (!once) __syncthreads();
         if (digit > 0)
@@ -343,7 +373,18 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         __syncthreads();
       }
     // bins from the top: the one in which the rest-th largest lies
-    const int hi = kBins - 1 - 2 * tid, x1 = hist[hi], x0 = hist[hi - 1];
+    const int hi = kBins - 1 - 2 * tid;
+    int x1 = hist[hi], x0 = hist[hi - 1];
+    if constexpr (R > 1) {
+      cluster_sync();
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (i != rank) {
+          x1 += ld_rank(&hist[hi], i);
+          x0 += ld_rank(&hist[hi - 1], i);
+        }
+      cluster_sync();
+    }
     int total;
     const int before = block_scan(x1 + x0, total);
     if (before < rest && rest <= before + x1) { s_pick = hi; s_rest = rest - before; }
@@ -360,7 +401,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   int* to = a.to + me * a.pitch;
   int* from = a.from + me * a.pitch;
   int ties = 0, holes = 0, movers = 0;  // before this chunk
-  for (int c0 = 0; c0 < len; c0 += cap) {
+  int c0 = begin;
+  do {
     const int n = once ? loaded : load_codes(c0, false);
     if (!once) __syncthreads();
     const int span = (n + 32 * 128 - 1) / (32 * 128) * 128;
@@ -387,10 +429,27 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       s_cnt[warp][2] = tie_lo; s_cnt[warp][3] = tie_hi;
     }
     __syncthreads();
+    if constexpr (R > 1) {
+      // what the CTAs before this one hold
+      if (warp < 4) {
+        const int x = __reduce_add_sync(0xffffffffu, s_cnt[lane][warp]);
+        if (lane == 0) s_give[warp] = x;
+      }
+      cluster_sync();
+      for (int i = 0; i < rank; ++i) {
+        const int o_lo = ld_rank(&s_give[0], i), o_hi = ld_rank(&s_give[1], i);
+        const int t_lo = ld_rank(&s_give[2], i), t_hi = ld_rank(&s_give[3], i);
+        const int kept_lo = min(t_lo, max(0, rest - ties)), kept_hi = min(t_hi, max(0, rest - ties - t_lo));
+        const int low = max(0, min(min(len, (i + 1) * per), keep) - i * per);
+        ties += t_lo + t_hi;
+        holes += low - o_lo - kept_lo;
+        movers += o_hi + kept_hi;
+      }
+    }
     // the sums over the warps before this one, and over all for the next chunk: lane w has warp w's counts
     const int o_lo = s_cnt[lane][0], o_hi = s_cnt[lane][1], t_lo = s_cnt[lane][2], t_hi = s_cnt[lane][3];
     const int w_lo = min(n, lane * span), w_hi = min(n, w_lo + span);
-    const int low = max(0, min(min(c0 + w_hi, keep), len) - (c0 + w_lo));  // its slots below the budget
+    const int low = max(0, min(min(c0 + w_hi, keep), stop) - (c0 + w_lo));  // its slots below the budget
     int t_sum = t_lo + t_hi;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -446,8 +505,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       }
     }
     __syncthreads();
-  }
-  if (tid == 0) { a.count[me] = movers; a.block_err[me] = 0; }
+    c0 += cap;
+  } while (c0 < stop);
+  if (tid == 0 && rank == R - 1) { a.count[me] = movers; a.block_err[me] = 0; }
+  if constexpr (R > 1) cluster_sync();  // no CTA's shared memory goes away while it is read
 }
 
 // Moves the listed tokens: a half warp per token, 16 bytes per lane. Sources lie behind the budget and
@@ -503,6 +564,29 @@ __global__ void __launch_bounds__(256, 8) evict_move_kernel(const EvictArgs a) {
       a.c.pos[wt] = a.c.pos[wf];
     }
   }
+}
+
+// The selection by clusters of R for at most `most` slots per CTA (R == 1: more are read in chunks).
+template <int R>
+cudaError_t launch_select(EvictArgs a, int most, int heads_kv, cudaStream_t st) {
+  a.cached = most < kMostCached ? (most + 3) / 4 * 4 : kMostCached;
+  static std::atomic<int> limits[64];
+  const cudaError_t e = raise_smem_limit(evict_select_kernel<R>, kMostCached * 4, limits);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(heads_kv * R, a.c.batch);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = (size_t)a.cached * 4;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = R;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = R > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<R>, a);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -608,11 +692,13 @@ int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch
     if (cache->page_size == 1 << i) a.page_shift = i;
   a.vec4 = cache->page_size % 4 == 0 && reinterpret_cast<uintptr_t>(cache->mass) % 16 == 0 &&
            reinterpret_cast<uintptr_t>(cache->positions) % 16 == 0;
-  a.cached = max_seqlen < kMostCached ? (max_seqlen + 3) / 4 * 4 : kMostCached;
-  static std::atomic<int> limits[64];
-  cudaError_t e = raise_smem_limit(evict_select_kernel, kMostCached * 4, limits);
-  if (e == cudaSuccess)
-    e = launch_pdl(evict_select_kernel, dim3(heads_kv, batch), dim3(kSelThreads), (size_t)a.cached * 4, st, a);
+  // few heads with long sequences: clusters, so that more SMs read and count (1024 threads fill an SM's registers)
+  const int64_t heads = (int64_t)batch * heads_kv;
+  const int ranks = max_seqlen < 4096 ? 1 : heads * 4 <= 152 ? 4 : heads * 2 <= 152 ? 2 : 1;
+  const int share = (max_seqlen + ranks - 1) / ranks;
+  cudaError_t e = ranks == 4 && share <= kMostCached - 4   ? launch_select<4>(a, share, heads_kv, st)
+                  : ranks == 2 && share <= kMostCached - 4 ? launch_select<2>(a, share, heads_kv, st)
+                                                           : launch_select<1>(a, max_seqlen, heads_kv, st);
   // enough CTAs to fill the GPU, none that could not have work
   int64_t blocks = (L.pitch + 15) / 16, most = 1216 / ((int64_t)batch * heads_kv);
   blocks = blocks < 1 ? 1 : blocks;

@@ -433,11 +433,15 @@ def test_evict(lens, hkv, d, page, dtype, layout, budget, sink, recent, ties):
     assert torch.equal(G["k"].cpu(), c["k"]) and torch.equal(G["v"].cpu(), c["v"])
 
 
-# (longer than the codes that shared memory holds; planes read four slots at a time and one at a time)
-@pytest.mark.parametrize("page,budget", [(64, 30000), (6, 1000)])
-def test_evict_long_sequences(page, budget):
+# (one CTA, two or four to a sequence, some of them without a slot; longer than the codes that shared memory holds;
+# planes read four slots at a time and one at a time)
+@pytest.mark.parametrize("lens,page,budget", [
+    ([120001, 50000, 49152], 64, 30000), ([120001, 4097], 6, 1000), ([250001], 32, 400),
+    ([60001, 50000] + [3] * 50, 64, 5000), ([60001, 49152] + [3] * 151, 16, 2000), ([60001] + [3] * 152, 10, 59000),
+    ([5, 9, 4100, 4, 13], 4, 3)])
+def test_evict_long_sequences(lens, page, budget):
     import quantized_attention_mean_gb300 as qa
-    lens, hkv, d = [120001, 50000, 49152], 1, 8
+    hkv, d = 1, 8
     c = ref.make_cache(lens, hkv, d, page, torch.float16, seed=3)
     g = torch.Generator().manual_seed(6)
     shape = (c["k"].shape[0], hkv, page)
@@ -447,8 +451,8 @@ def test_evict_long_sequences(page, budget):
         p, s = ref.place(c, b, n)
         pos[p, 0, s] = torch.arange(n, dtype=torch.int32)
     G, gm, gp = on_gpu(c), mass.to(DEV), pos.to(DEV)
-    new = qa.paged_evict(G["k"], G["v"], gm, gp, G["table"], G["lens"], budget, max(lens), sink=4, recent=300)
-    want = ref.evict(c, mass, pos, budget, 4, 300)
+    new = qa.paged_evict(G["k"], G["v"], gm, gp, G["table"], G["lens"], budget, max(lens), sink=min(4, budget - 1), recent=budget // 9)
+    want = ref.evict(c, mass, pos, budget, min(4, budget - 1), budget // 9)
     assert torch.equal(new.cpu(), want) and torch.equal(gp.cpu(), pos) and torch.equal(gm.cpu(), mass)
     assert torch.equal(G["k"].cpu(), c["k"]) and torch.equal(G["v"].cpu(), c["v"])
 
