@@ -137,7 +137,8 @@ def test_few_rows_are_split_over_the_keys(nq, nk, hq, d, dtype):
 # Few queries of several heads in one query tile or two, groups that do not fill them, splits and none
 @pytest.mark.parametrize("B,hq,hkv,nq,nk", [(2, 8, 2, 20, 6000), (2, 14, 2, 16, 6000), (2, 14, 2, 40, 6000),
                                             (1, 32, 8, 100, 9000), (20, 12, 4, 100, 300), (30, 16, 4, 5, 700),
-                                            (16, 14, 2, 40, 500), (20, 8, 2, 1, 900), (12, 10, 2, 64, 700)])
+                                            (16, 14, 2, 40, 500), (20, 8, 2, 1, 900), (12, 10, 2, 64, 700),
+                                            (1, 40, 2, 3, 2000), (1, 71, 1, 7, 3300), (2, 33, 1, 9, 130)])
 @pytest.mark.parametrize("d,dtype,layout", [(64, F, "NHD"), (128, H, "HND"), (40, H, "HND"), (33, F, "NHD")])
 def test_heads_share_a_tile(B, hq, hkv, nq, nk, d, dtype, layout):
     g = torch.Generator().manual_seed(nq)
@@ -312,6 +313,36 @@ def test_in_a_graph_and_on_another_stream():
         gr.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager)
+
+
+def test_captured_without_a_workspace():
+    # what a captured call takes from the allocator must not be what a later one of the graph is given while it runs
+    import quantized_attention_mean_gb300 as qa
+    g = torch.Generator().manual_seed(5)
+    q, k, v = (torch.randn(1, h, n, 64, generator=g).half().to(DEV) for h, n in ((4, 200), (2, 9000), (2, 9000)))
+    ids = torch.randint(0, 3, (1, 9000), generator=g, dtype=torch.int32).to(DEV)
+    cache = [t[0].transpose(0, 1).reshape(1, 9000, 2, 64)[:, :8960].reshape(560, 16, 2, 64).contiguous() for t in (k, v)]
+    table, lens = torch.arange(560, dtype=torch.int32, device=DEV)[None], torch.tensor([8960], dtype=torch.int32, device=DEV)
+    mass0 = torch.rand(560, 2, 16, generator=g).to(DEV)
+    pos = torch.arange(16, dtype=torch.int32, device=DEV).expand(560, 2, 16).contiguous()
+
+    def step(c, mass, pos):
+        a = qa.scored_attn(q, k, v, is_causal=True, q_offset=8800, doc_ids=ids[:, :200].contiguous(), doc_ids_k=ids)
+        b = qa.paged_attn(a[:, :, 7], *c, table, lens, 10 ** 5, tensor_layout="NHD", mass=mass)
+        n = qa.paged_evict(*c, mass, pos, table, lens, 500, 9000, tensor_layout="NHD")
+        d = qa.scored_attn(q * 0.5, k, v)
+        return a, b, n, d, mass, pos, *c
+
+    want = step([t.clone() for t in cache], mass0.clone(), pos.clone())
+    graph, side = torch.cuda.CUDAGraph(), [t.clone() for t in (*cache, mass0, pos)]
+    with torch.cuda.graph(graph):
+        got = step([side[0], side[1]], side[2], side[3])
+    for _ in range(3):
+        for t, x in zip(side, (*cache, mass0, pos)):
+            t.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
 def test_prompt_in_chunks_then_decode():
