@@ -339,7 +339,10 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
 
 // What the roles of a CTA agree on, as words of shared memory: each role loads what it uses (kept in
 // registers across the split they spilled, and with the shared memory taken a spill is an L2 access).
-enum Word : uint32_t { kWTmem = 0, kWAbort = 4, kWJ0 = 16, kWTiles = 20, kWTilesA = 24, kWPrefix = 28, kWRed = 32, kWSeq = 48, kWSplit = 52, kWLeft = 56, kWSeen = 60, kWClean = 64 };
+enum Word : uint32_t {
+  kWTmem = 0, kWAbort = 4, kWJ0 = 16, kWTiles = 20, kWTilesA = 24, kWPrefix = 28, kWRed = 32,
+  kWSeq = 48, kWSplit = 52, kWLeft = 56, kWSeen = 60, kWClean = 64
+};
 __device__ __forceinline__ int lds(uint32_t at) {
   int v;
   asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
@@ -780,7 +783,8 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kPerSm)
                 const bool me = dq == one;
 #pragma unroll
                 for (int i = 0; i < kN; ++i) {
-                  const uint32_t v = __ballot_sync(0xffffffffu, (c + i == 0 ? id[0] : c + i == 1 ? id[1] : c + i == 2 ? id[2] : id[3]) == one);
+                  const int key_id = c + i == 0 ? id[0] : c + i == 1 ? id[1] : c + i == 2 ? id[2] : id[3];
+                  const uint32_t v = __ballot_sync(0xffffffffu, key_id == one);
                   if (me) mine[i] = v;
                 }
                 todo &= ~__ballot_sync(0xffffffffu, me);
