@@ -644,7 +644,8 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kPerSm)
     const uint32_t tO = tmem + lane_base + C::kTmemO + x * DP;
     const int my_tiles = lds(misc + (x == 0 ? kWTilesA : kWTiles)), left = lds(misc + kWLeft);
     const int limit = valid ? limit_of(row, prefix) : 0;
-    const int dq = !a.doc_q ? 0 : valid ? __ldg(&a.doc_q[(int64_t)b * a.nq + row]) : -1;
+    // (any negative id is padding: -1, apart from the -2 of a tile of several documents)
+    const int dq = !a.doc_q ? 0 : valid ? max(__ldg(&a.doc_q[(int64_t)b * a.nq + row]), -1) : -1;
     const int pos = row + a.q_offset;
     constexpr float kSlack = BF16 ? 60.0f : 7.0f;  // by how much a maximum may be overestimated
     float slope = 0.f;

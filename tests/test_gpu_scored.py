@@ -171,6 +171,22 @@ def test_padding_may_hold_anything():
             assert (out[:, :, 250:] == 0).all()
 
 
+@pytest.mark.parametrize("d,dtype", [(64, H), (128, F)])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, True)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_any_negative_id_is_padding(d, dtype, cap, bias, causal):
+    # (also in the middle, and as whole warps of rows beside rows of documents)
+    for lengths, pad in (([150, 100], 70), ([60, 3, 200, 90], 7), ([60, 100], 96), ([20, 50, 80], 200)):
+        dq = docs_of(lengths, pad, 2)
+        dq[1, 40:55] = -1
+        one = check(2, 2, 1, dq.shape[1], dq.shape[1], d, dtype, causal=causal, cap=cap, bias=bias, dq=dq)
+        for other in (-2, -7, -2 ** 31):
+            ids = torch.where(dq < 0, torch.full_like(dq, other), dq)
+            same = check(2, 2, 1, dq.shape[1], dq.shape[1], d, dtype, causal=causal, cap=cap, bias=bias, dq=ids)
+            assert all(torch.equal(x, y) for x, y in zip(one, same))
+            assert (same[1][1, :, 40:55] == -math.inf).all()
+
+
 def test_keys_ahead_may_be_infinite_scores():
     # a masked key whose score is infinite or NaN leaves the rows that do not see it alone
     g = torch.Generator().manual_seed(4)
