@@ -306,7 +306,9 @@ int sage_paged_attn(const sage_packed* q, const sage_paged_cache* cache, const s
 /* Writes new tokens behind the held ones: token t of k, v [tokens, Hkv, d] belongs to the sequence b with
  * cu_seqlens[b] <= t < cu_seqlens[b + 1] and goes to slot seq_lens[b] + t - cu_seqlens[b]. seq_lens is
  * read, not raised. cu_seqlens: device int32 [batch + 1], non-decreasing from 0; NULL: one token per
- * sequence (tokens == batch). Tokens from cu_seqlens[batch] on are left out. cache->mass becomes 0 there
+ * sequence (tokens == batch). Tokens from cu_seqlens[batch] on are left out, and so are all tokens of a
+ * sequence of negative length, and those whose slot lies behind the table's room or whose page is not in the
+ * cache (SAGE_ERR_SEQLENS, SAGE_ERR_PAGE). cache->mass becomes 0 in the written slots
  * and cache->positions the token's entry of `positions` (device int32 [tokens]) or its slot. Two
  * tokens must not share a slot. workspace: NULL, or SAGE_STATUS_BYTES for the device status. */
 int sage_paged_append(const sage_packed* k, const sage_packed* v, const sage_paged_cache* cache,

@@ -78,8 +78,10 @@ __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
     if (b == a.c.batch || first > t) return;  // behind the last sequence, or before the first
     at = t - first;
   }
-  const int64_t slot = (int64_t)__ldg(&a.c.lens[b]) + at;
-  if (slot < 0 || slot >= (int64_t)a.c.max_pages * a.c.page_size) {
+  const int held = __ldg(&a.c.lens[b]);
+  const int64_t slot = (int64_t)held + at;
+  // (a negative length refuses all of its tokens: the later ones would land on slots in use)
+  if (held < 0 || slot >= (int64_t)a.c.max_pages * a.c.page_size) {
     if (a.err && lane == 0) record_error(a.err, kDevSeqlens);
     return;
   }

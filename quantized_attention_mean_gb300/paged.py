@@ -213,7 +213,8 @@ def paged_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, 
     not raised). ``cu_seqlens`` int32 [B + 1] says which tokens are whose; without it each sequence gets
     one. Tokens behind the last sequence are left out. ``mass`` becomes 0 in the new slots,
     ``key_positions`` the token's entry of ``positions`` int32 [T], or its slot. A token whose slot or page
-    is not in the cache is left out, and recorded in ``workspace`` (256 bytes) where one is given."""
+    is not in the cache is left out, as are all of a sequence of negative length, and recorded in
+    ``workspace`` (256 bytes) where one is given."""
     cache, hkv, d, index = _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions,
                                         workspace)
     shape = k.shape

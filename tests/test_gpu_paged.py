@@ -392,6 +392,34 @@ def test_append_leaves_out_what_has_no_place():
     assert qa.read_device_status(ws) == 0 and not torch.equal(G["k"], before)
 
 
+@pytest.mark.parametrize("lens", [[-3, 5, 7], [5, -10, 7], [5, 7, -2 ** 31], [-1, -2, -9]])
+@pytest.mark.parametrize("told", [True, False])
+def test_append_leaves_a_sequence_of_negative_length_alone(lens, told):
+    # more new tokens than the length is below zero: the later ones must not land on what the sequence holds
+    import quantized_attention_mean_gb300 as qa
+    c = ref.make_cache([20, 20, 20], 2, 64, 16, torch.float16, room=12)
+    counts = [10, 11, 12]
+    g = torch.Generator().manual_seed(4)
+    k, v = (torch.randn(sum(counts), 2, 64, generator=g).half() for _ in "kv")
+    mass = torch.full((c["k"].shape[0], 2, 16), 5.0)
+    kpos = torch.full((c["k"].shape[0], 2, 16), -3, dtype=torch.int32)
+    cu = torch.tensor([0, 10, 21, 33], dtype=torch.int32)
+    G, gm, gp = on_gpu(c), mass.to(DEV), kpos.to(DEV)
+    ws = qa.alloc_workspace(256, DEV) if told else None
+    qa.paged_append(k.to(DEV), v.to(DEV), G["k"], G["v"], G["table"], torch.tensor(lens, dtype=torch.int32, device=DEV),
+                    cu_seqlens=cu.to(DEV), mass=gm, key_positions=gp, workspace=ws)
+    assert ws is None or qa.read_device_status(ws) == 12
+    t = 0
+    for b, n in enumerate(counts):
+        for i in range(n if lens[b] >= 0 else 0):
+            slot = lens[b] + i
+            p, s = int(c["table"][b, slot // 16]), slot % 16
+            c["k"][p, :, s], c["v"][p, :, s], mass[p, :, s], kpos[p, :, s] = k[t + i], v[t + i], 0.0, slot
+        t += n
+    assert torch.equal(G["k"].cpu(), c["k"]) and torch.equal(G["v"].cpu(), c["v"])
+    assert torch.equal(gm.cpu(), mass) and torch.equal(gp.cpu(), kpos)
+
+
 EVICTIONS = [
     # lens, hkv, d, page, dtype, layout, budget, sink, recent, ties
     ([100, 64, 65, 3, 0], 2, 64, 16, torch.float16, "HND", 64, 4, 16, False),
