@@ -1,9 +1,17 @@
 """Serving over a paged key-value cache: append new tokens, attend with one new token per sequence,
 and evict what has drawn the least attention.
 
-    paged_append(k, v, k_cache, v_cache, page_table, seq_lens, ...)
-    out = paged_attn(q, k_cache, v_cache, page_table, seq_lens + 1, max_seq_len, ...)
-    seq_lens = paged_evict(k_cache, v_cache, mass, key_positions, page_table, seq_lens, budget, ...)
+    paged_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens, mass=mass, key_positions=positions)
+    seq_lens = seq_lens + prompt_lens   # the calls read the lengths, the caller raises them
+    next_pos = seq_lens.clone()         # the next token's position: from the first eviction on not its slot
+    for q_new, k_new, v_new in steps:   # one token of every sequence at a time
+        paged_append(k_new, v_new, k_cache, v_cache, page_table, seq_lens, mass=mass, key_positions=positions,
+                     positions=next_pos)
+        seq_lens = seq_lens + 1
+        out = paged_attn(q_new, k_cache, v_cache, page_table, seq_lens, max_len, softcap=50.0, slopes=slopes,
+                         key_positions=positions, q_positions=next_pos, mass=mass)
+        seq_lens = paged_evict(k_cache, v_cache, mass, positions, page_table, seq_lens, budget, max_len, sink=4, recent=128)
+        next_pos = next_pos + 1
 
 The cache is the caller's: ``k_cache`` / ``v_cache`` [num_pages, Hkv, page_size, d] (HND) or
 [num_pages, page_size, Hkv, d] (NHD) in fp16 or bf16, ``page_table`` int32 [B, max_pages], ``seq_lens``

@@ -2,6 +2,9 @@
 plain loops."""
 
 import math
+import os
+import textwrap
+import types
 
 import pytest
 import torch
@@ -559,6 +562,76 @@ def test_serving_loop_with_eviction():
         lens = qa.paged_evict(G["k"], G["v"], gm, gp, G["table"], lens, budget, 64, sink=2, recent=6)
         assert torch.equal(lens.cpu(), want) and torch.equal(gp.cpu(), pos) and torch.equal(gm.cpu(), mass)
         assert torch.equal(G["k"].cpu(), c["k"]) and torch.equal(G["v"].cpu(), c["v"])
+
+
+def documented_loop(where):
+    """The serving loop of the package's documentation, as code."""
+    import quantized_attention_mean_gb300 as qa
+    if where == "paged":
+        text = qa.paged.__doc__
+        text = text[text.index("    paged_append("):text.index("The cache is the caller's")]
+    else:
+        text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+        text = text[text.index("# prompts with capped"):]
+        text = text[:text.index("```")]
+    return textwrap.dedent(text)
+
+
+@pytest.mark.parametrize("where", ["paged", "README"])
+def test_the_documented_serving_loop_keeps_its_tokens(where):
+    """Prompts, then steps of append, attention and eviction, as the documentation writes them: every step sees the tokens
+    that were kept, at their own positions, with the newest; each head keeps its first, its last and `budget` in all."""
+    import quantized_attention_mean_gb300 as qa
+    B, hq, hkv, d, page, budget, longest, dtype = 2, 4, 2, 64, 16, 140, 150, torch.bfloat16
+    prompt, steps = [150, 101], 60
+    g = torch.Generator().manual_seed(21)
+    rows = {n: torch.randn(B, longest + steps, hkv, d, generator=g).to(dtype) for n in "kv"}     # by position
+    qs = torch.randn(B, longest + steps, hq, d, generator=g).to(dtype)
+    slopes = torch.tensor([0.05, 0.02, 0.01, 0.0])
+    c = ref.make_cache([0] * B, hkv, d, page, dtype, room=longest + 2)
+    cache = on_gpu(c)
+    new = lambda t, n: torch.stack([t[b, prompt[b] + n] for b in range(B)]).to(DEV)  # noqa: E731
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    plane = (c["k"].shape[0], hkv, page)
+    names = dict(q=qs[:, :longest].to(DEV), k=rows["k"][:, :longest].to(DEV), v=rows["v"][:, :longest].to(DEV),
+                 held=(torch.arange(longest) < torch.tensor(prompt)[:, None]).to(DEV), k_cache=cache["k"],
+                 v_cache=cache["v"], page_table=cache["table"], seq_lens=cache["lens"],
+                 cu_seqlens=ints([0, prompt[0], sum(prompt)]), prompt_lens=ints(prompt), slopes=slopes.to(DEV),
+                 mass=torch.full(plane, 3.0, device=DEV), positions=torch.full(plane, -5, dtype=torch.int32, device=DEV),
+                 max_len=longest + 2, budget=budget,
+                 steps=[(new(qs, n), new(rows["k"], n), new(rows["v"], n)) for n in range(steps)])
+    if where == "paged":
+        names.update(k=names["k"][names["held"]], v=names["v"][names["held"]])
+    at = -1                                                                      # of the step
+    kept = {(b, h): list(range(prompt[b])) for b in range(B) for h in range(hkv)}  # positions, by sequence and head
+
+    def attn(*args, **kw):
+        nonlocal at
+        at += 1
+        got = qa.paged_attn(*args, **kw)
+        for (b, h), pos in kept.items():
+            pos.append(prompt[b] + at)
+            group = slice(h * hq // hkv, (h + 1) * hq // hkv)
+            bias = -slopes[group, None].double() * (prompt[b] + at - torch.tensor(pos)).double()
+            r = attend(qs[b, prompt[b] + at, group], rows["k"][b, pos, h], rows["v"][b, pos, h], d ** -0.5, 50.0, bias, dtype=dtype)
+            assert_close(got[b, group], r["out"], r["out_tol"], f"sequence {b}, head {h}, step {at}")
+        return got
+
+    def evict(k_cache, v_cache, mass, positions, table, lens, *args, **kw):
+        new_lens = qa.paged_evict(k_cache, v_cache, mass, positions, table, lens, *args, **kw)
+        for (b, h), pos in kept.items():
+            n = min(len(pos), budget)
+            assert int(new_lens[b]) == n
+            p, s = ref.place(c, b, n)
+            left = positions.cpu()[p, h, s].tolist()
+            assert len(set(left)) == n and set(left) <= set(pos)
+            assert set(range(4)) | set(range(max(0, prompt[b] + at - 127), prompt[b] + at + 1)) <= set(left)
+            kept[b, h] = left
+        return new_lens
+
+    calls = dict(paged_append=qa.paged_append, paged_attn=attn, paged_evict=evict, scored_attn=qa.scored_attn)
+    exec(documented_loop(where), {**names, **calls, "qa": types.SimpleNamespace(**calls)})
+    assert at == steps - 1 and all(len(p) == budget for p in kept.values())
 
 
 def test_decode_step_in_a_graph_and_on_another_stream():
