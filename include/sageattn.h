@@ -293,7 +293,10 @@ typedef struct {
  *   slopes: device float [Hq] or NULL; q_positions: device int32 [batch] or NULL (seq_len - 1).
  *   max_seqlen: an upper bound of seq_lens. cache->mass, where not NULL: each held token's weight,
  *   summed over the query heads of its key/value head, is added. A page that several
- *   sequences share is given the weights of all, in no fixed order. workspace: as sage_scored_attn's.
+ *   sequences share is given the weights of all, in no fixed order. workspace: as sage_scored_attn's;
+ *   with mass it holds 4 batch Hq max_seqlen bytes of scores.
+ *   Once a sequence has been evicted from, its slots and its length are no positions: slopes then need
+ *   cache->positions and q_positions.
  * A sequence that holds nothing gets out = 0 and lse = -inf. */
 size_t sage_paged_attn_workspace_size(int batch, int heads_q, int heads_kv, int max_seqlen,
                                       int head_dim, int accumulate);
@@ -309,7 +312,8 @@ int sage_paged_attn(const sage_packed* q, const sage_paged_cache* cache, const s
  * sequence (tokens == batch). Tokens from cu_seqlens[batch] on are left out, and so are all tokens of a
  * sequence of negative length, and those whose slot lies behind the table's room or whose page is not in the
  * cache (SAGE_ERR_SEQLENS, SAGE_ERR_PAGE). cache->mass becomes 0 in the written slots
- * and cache->positions the token's entry of `positions` (device int32 [tokens]) or its slot. Two
+ * and cache->positions the token's entry of `positions` (device int32 [tokens]) or its slot, which is no
+ * position once the sequence has been evicted from (it lies below the kept ones). Two
  * tokens must not share a slot. workspace: NULL, or SAGE_STATUS_BYTES for the device status. */
 int sage_paged_append(const sage_packed* k, const sage_packed* v, const sage_paged_cache* cache,
                       const int32_t* cu_seqlens, const int32_t* positions, int batch, int tokens,
@@ -323,6 +327,7 @@ int sage_paged_append(const sage_packed* k, const sage_packed* v, const sage_pag
  * position; slots from `budget` on keep what they held. new_lens: device int32 [batch], written
  * min(seq_len, budget), or seq_len where an error is found: that sequence is left as it was; it must not
  * overlap seq_lens. cache->mass and cache->positions are needed. Each page belongs to one sequence.
+ * Only sage_paged_attn adds mass: right after a prompt the lowest of the unprotected slots stay.
  * budget >= 1, sink + recent <= budget (where positions repeat and more than `budget` tokens would
  * have to stay, those of the lowest slots do). */
 size_t sage_paged_evict_workspace_size(int batch, int heads_kv, int max_seqlen, int budget);

@@ -175,8 +175,12 @@ def paged_attn(q, k_cache, v_cache, page_table, seq_lens, max_seq_len, tensor_la
     ``max_seq_len``: an upper bound of seq_lens. ``softcap`` > 0: scores become
     softcap·tanh(s / softcap). ``slopes`` fp32 [Hq]: slopes[h]·|q_position - key position| is taken off;
     the key's position is its slot unless ``key_positions`` gives it (a cache that was evicted from), the
-    query's is seq_len - 1 unless ``q_positions`` int32 [B] does. ``mass``: the weight each held token
-    draws, summed over the query heads of its key/value head, is added to it in place."""
+    query's is seq_len - 1 unless ``q_positions`` int32 [B] does. Once a sequence has been evicted from, its slots and its
+    length are no positions any more: with ``slopes`` give both. ``mass``: the weight each held token
+    draws, summed over the query heads of its key/value head, is added to it in place; it takes a workspace of
+    4·B·Hq·max_seq_len bytes, whatever the lengths. A sequence whose length lies outside of [0, max_seq_len] or of the
+    table counts as empty, a token whose page is not in the cache as a row of zeros; ``read_device_status(workspace)``
+    tells of either, and nothing does where no workspace is given."""
     cache, hkv, d, index = _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions,
                                         workspace)
     shape = q.shape
@@ -222,7 +226,9 @@ def paged_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, 
     one. Tokens behind the last sequence are left out. ``mass`` becomes 0 in the new slots,
     ``key_positions`` the token's entry of ``positions`` int32 [T], or its slot. A token whose slot or page
     is not in the cache is left out, as are all of a sequence of negative length, and recorded in
-    ``workspace`` (256 bytes) where one is given."""
+    ``workspace`` (256 bytes) where one is given. Once a sequence has been evicted from, ``key_positions`` needs
+    ``positions``: a new token's slot then lies below the positions that were kept, and the next eviction would
+    take it for an old one."""
     cache, hkv, d, index = _check_cache(k_cache, v_cache, page_table, seq_lens, tensor_layout, mass, key_positions,
                                         workspace)
     shape = k.shape
@@ -258,7 +264,9 @@ def paged_evict(k_cache, v_cache, mass, key_positions, page_table, seq_lens, bud
     new lengths int32 [B]. For each key/value head, tokens at positions below ``sink`` or among the last
     ``recent`` positions stay, then those with the largest ``mass`` (ties: the lowest slot). Kept tokens
     behind the budget move into the freed slots, with their mass and position; the slots behind the
-    budget keep what they held, and their pages are free. A sequence with a bad length or page is left as it was, its
+    budget keep what they held, and their pages are free. Positions that count on from the kept ones make new tokens
+    the last ones: give ``positions`` to ``paged_append`` from then on. Only ``paged_attn`` adds mass: right after a prompt
+    every mass is 0, and besides the protected tokens the lowest slots stay. A sequence with a bad length or page is left as it was, its
     length too (``read_device_status``)."""
     if mass is None or key_positions is None:
         raise ValueError("eviction needs the mass and key_positions planes")
