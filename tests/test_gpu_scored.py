@@ -200,6 +200,37 @@ def test_keys_ahead_may_be_infinite_scores():
     assert torch.equal(a[:, :, :200], b[:, :, :200]) and torch.isnan(b[:, :, 200:]).any()
 
 
+@pytest.mark.parametrize("d,dtype", [(64, H), (64, F), (128, H), (128, F)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_keys_no_row_of_a_warp_sees_leave_the_capped_scores_alone(d, dtype, bias):
+    # large finite scores of keys that are padding, lie behind the last one seen, or are of documents that only other
+    # warps' rows see: the other rows stay as they are, bit for bit (fp32 statistics with them)
+    import quantized_attention_mean_gb300 as qa
+    g = torch.Generator().manual_seed(12)
+    n = 256
+    q, k, v = (torch.randn(1, 2, n, d, generator=g).to(dtype) for _ in "qkv")
+    slopes = torch.tensor([0.02, 0.01], device=DEV) if bias else None
+    ids_k = (torch.arange(n, dtype=torch.int32) % 2)[None].contiguous()
+    ids_q = (torch.arange(n, dtype=torch.int32) // 128)[None].contiguous()
+    pad = torch.zeros(1, n, dtype=torch.int32)
+    pad[0, 5::9] = -1
+    cases = [(dict(doc_ids=ids_q, doc_ids_k=ids_k), torch.arange(1, n, 2), slice(0, 128)),     # (the first 128 rows: even keys)
+             (dict(doc_ids=pad, is_causal=True), torch.arange(5, n, 9), slice(0, n)),
+             (dict(is_causal=True, q_offset=-41), torch.arange(n - 41, n), slice(0, n))]
+    for kw, unseen, rows in cases:
+        kw = {x: y.to(DEV) if torch.is_tensor(y) else y for x, y in kw.items()}
+        got = []
+        for size in (1.0, 100.0, 30000.0):
+            kk, qq = k.clone(), q.clone()
+            kk[:, :, unseen] = (q[:, :, unseen] * size).clamp(-60000, 60000)
+            if "is_causal" in kw and "doc_ids" in kw:
+                qq[:, :, unseen] = kk[:, :, unseen]                       # (rows that are padding)
+            got.append(qa.scored_attn(qq.to(DEV), kk.to(DEV), v.to(DEV), softcap=25.0, slopes=slopes, return_lse=True, **kw))
+        for out, lse in got[1:]:
+            assert torch.equal(out[:, :, rows], got[0][0][:, :, rows])
+            assert torch.equal(lse[:, :, rows], got[0][1][:, :, rows])
+
+
 @pytest.mark.parametrize("nq,nk,offset,prefix", [(100, 300, 50, None), (300, 700, 77, None), (5, 4000, 2100, None),
                                                  (100, 300, 0, [170]), (260, 300, -20, None)])
 @pytest.mark.parametrize("d,dtype", [(64, H), (128, F)])
