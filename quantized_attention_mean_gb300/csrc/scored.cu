@@ -1239,8 +1239,10 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
   if (dtype != SAGE_F16 && dtype != SAGE_BF16) return SAGE_ERR_DTYPE;
   if (tensor_layout != SAGE_HND && tensor_layout != SAGE_NHD) return SAGE_ERR_INVALID_ARG;
   if (batch < 0 || heads_q < 1 || heads_kv < 1 || seqlen_q < 0 || seqlen_k < 0 ||
-      !softcap_ok(softcap, sm_scale, head_dim) || (prefix_lens && !is_causal) || !doc_q != !doc_k || (return_lse && !lse))
+      !softcap_ok(softcap, sm_scale, head_dim) || (prefix_lens && !is_causal) || (return_lse && !lse && batch > 0 && seqlen_q > 0))
     return SAGE_ERR_INVALID_ARG;
+  // (ids of no rows or of no keys have no address)
+  if (!doc_q != !doc_k && batch > 0 && seqlen_q > 0 && seqlen_k > 0) return SAGE_ERR_INVALID_ARG;
   if (heads_q % heads_kv) return SAGE_ERR_GQA;
   for (const void* p : {(const void*)lse, (const void*)slopes, (const void*)prefix_lens, (const void*)doc_q, (const void*)doc_k})
     if (reinterpret_cast<uintptr_t>(p) % 4) return SAGE_ERR_INVALID_ARG;

@@ -337,6 +337,20 @@ def test_no_keys_and_out_strides():
         assert (wide[..., :at] == 7).all() and (wide[..., at + 64:] == 7).all()
 
 
+def test_no_rows_no_keys_no_sequences():
+    import quantized_attention_mean_gb300 as qa
+    q, k = (torch.randn(2, 2, n, 64, dtype=torch.float16, device=DEV) for n in (5, 130))
+    ids = lambda n: torch.zeros(2, n, dtype=torch.int32, device=DEV)  # noqa: E731
+    out, lse = qa.scored_attn(q, k[:, :, :0], k[:, :, :0], doc_ids=ids(5), doc_ids_k=ids(0), return_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    assert qa.scored_attn(q[:, :, :0], k, k, doc_ids=ids(0), doc_ids_k=ids(130)).shape == (2, 2, 0, 64)
+    assert qa.scored_attn(q[:, :, :0], k[:, :, :0], k[:, :, :0], doc_ids=ids(0)).shape == (2, 2, 0, 64)
+    for rows, keys in ((q[:, :, :0], k), (q[:, :, :0], k[:, :, :0]), (q[:0], k[:0]), (q[:0, :, :0], k[:0, :, :0])):
+        out, lse = qa.scored_attn(rows, keys, keys, is_causal=True, return_lse=True)
+        assert out.shape == rows.shape and lse.shape == rows.shape[:3]
+    assert qa.scored_attn(q[:0], k[:0], k[:0], doc_ids=ids(5)[:0], doc_ids_k=ids(130)[:0]).shape == (0, 2, 5, 64)
+
+
 def test_in_a_graph_and_on_another_stream():
     import quantized_attention_mean_gb300 as qa
     g = torch.Generator().manual_seed(8)
