@@ -326,7 +326,7 @@ int sage_paged_append(const sage_packed* k, const sage_packed* v, const sage_pag
  * tokens from slot `budget` on move, in order, into the freed slots below it, with their mass and
  * position; slots from `budget` on keep what they held. new_lens: device int32 [batch], written
  * min(seq_len, budget), or seq_len where an error is found: that sequence is left as it was; it must not
- * overlap seq_lens. cache->mass and cache->positions are needed. Each page belongs to one sequence.
+ * overlap seq_lens. cache->mass and cache->positions are needed where there are pages. Each page belongs to one sequence.
  * Only sage_paged_attn adds mass: right after a prompt the lowest of the unprotected slots stay.
  * budget >= 1, sink + recent <= budget (where positions repeat and more than `budget` tokens would
  * have to stay, those of the lowest slots do). */

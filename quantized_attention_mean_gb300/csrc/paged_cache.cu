@@ -669,7 +669,8 @@ int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch
   if (max_seqlen < 0 || batch > 65535 || budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget)
     return SAGE_ERR_INVALID_ARG;
   if (batch == 0) return SAGE_OK;
-  if (!new_lens || reinterpret_cast<uintptr_t>(new_lens) % 4 || !cache->mass || !cache->positions)
+  // (planes of no pages have no address, and are not read)
+  if (!new_lens || reinterpret_cast<uintptr_t>(new_lens) % 4 || (cache->num_pages > 0 && (!cache->mass || !cache->positions)))
     return SAGE_ERR_INVALID_ARG;
   // (seq_lens is read by the CTAs of every head, after the first has written new_lens)
   const uintptr_t n0 = reinterpret_cast<uintptr_t>(new_lens), l0 = reinterpret_cast<uintptr_t>(cache->seq_lens);

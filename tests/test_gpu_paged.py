@@ -564,6 +564,21 @@ def test_serving_loop_with_eviction():
         assert torch.equal(G["k"].cpu(), c["k"]) and torch.equal(G["v"].cpu(), c["v"])
 
 
+def test_evict_from_a_cache_without_pages():
+    import quantized_attention_mean_gb300 as qa
+    k = torch.empty(0, 2, 16, 64, dtype=torch.float16, device=DEV)
+    mass, pos = torch.empty(0, 2, 16, device=DEV), torch.empty(0, 2, 16, dtype=torch.int32, device=DEV)
+    ws = qa.alloc_workspace(qa.paged_evict_workspace_bytes(2, 2, 100, 10), DEV)
+    for width in (0, 4):
+        table, lens = torch.zeros(2, width, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+        assert qa.paged_evict(k, k, mass, pos, table, lens, 10, 100, workspace=ws).tolist() == [0, 0]
+        assert qa.read_device_status(ws) == 0
+    # tokens that no page holds: left as they were
+    lens = torch.tensor([0, 40], dtype=torch.int32, device=DEV)
+    assert qa.paged_evict(k, k, mass, pos, table, lens, 10, 100, workspace=ws).tolist() == [0, 40]
+    assert qa.read_device_status(ws) == 13
+
+
 def documented_loop(where):
     """The serving loop of the package's documentation, as code."""
     import quantized_attention_mean_gb300 as qa
