@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           for (int e = 0; e < 4; ++e) s[n][e] *= scale2;
       }
       if (a.slopes && !a.c.pos) {
-        const float d0 = (float)(qpos - (key0 + cq));  // exact below 2^24
+        const float d0 = (float)((long long)qpos - (key0 + cq));  // exact below 2^24
 #pragma unroll
         for (int n = 0; n < NK; ++n)
 #pragma unroll

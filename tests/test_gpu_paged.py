@@ -105,6 +105,30 @@ def test_decode_positions_strides_and_scale():
     assert (ow[:, 1::2] == 9).all()
 
 
+@pytest.mark.parametrize("d,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+@pytest.mark.parametrize("planes", [False, True])
+def test_decode_positions_near_the_ends_of_32_bits(d, dtype, planes):
+    # the distance from the query's position to a slot passes 2^31
+    import quantized_attention_mean_gb300 as qa
+    n = 40000
+    c = ref.make_cache([n], 1, d, 64, dtype)
+    q = torch.randn(1, 4, d, generator=torch.Generator().manual_seed(3)).to(dtype)
+    slopes = torch.tensor([1e-3, -2e-4, 1e-4, 0.0])
+    kpos = None
+    if planes:
+        kpos = torch.zeros(c["k"].shape[0], 1, 64, dtype=torch.int32)
+        p, s = ref.place(c, 0, n)
+        kpos[p, 0, s] = torch.arange(n, dtype=torch.int32)
+    G = on_gpu(c)
+    for at in (-2 ** 31, -2 ** 31 + n // 2, 2 ** 31 - 1):
+        qpos = torch.tensor([at], dtype=torch.int32)
+        out, lse = qa.paged_attn(q.to(DEV), G["k"], G["v"], G["table"], G["lens"], n, slopes=slopes.to(DEV),
+                                 key_positions=None if kpos is None else kpos.to(DEV), q_positions=qpos.to(DEV), return_lse=True)
+        r = decode_reference(c, q, d ** -0.5, 0.0, slopes, kpos, qpos.long(), 1)
+        assert_close(out, r["out"], r["out_tol"], f"out at {at}")
+        assert_close(lse, r["lse"], r["lse_tol"], f"lse at {at}")
+
+
 @pytest.mark.parametrize("bound", [700, 9000])
 @pytest.mark.parametrize("hq,hkv,d,cap", [(8, 2, 128, 0.0), (20, 1, 64, 30.0), (3, 3, 40, 0.0)])
 def test_decode_accumulates_weights(hq, hkv, d, cap, bound):
