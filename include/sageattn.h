@@ -239,7 +239,9 @@ int sage_merge_partials(const sage_tensor* outs, const float* const* lses, int n
  * are rounded once to the inputs' type for P V. A row that sees no key gets out = 0 and lse = -inf, and
  * so does a row all of whose visible scores are -inf.
  *   q, k, v, out, tensor_layout, is_causal, sm_scale, lse, return_lse: as sage_attn. q_offset shifts the
- *   queries' positions (the next chunk of a prompt: the number of keys before it); it may be negative.
+ *   queries' positions (the next chunk of a prompt: the number of keys before it); it may be negative. No position and,
+ *   with slopes, no distance may pass 2^31 - 256: -2^31 + 256 <= q_offset (with slopes: q_offset - Nk) and
+ *   q_offset + Nq <= 2^31 - 256, or SAGE_ERR_INVALID_ARG.
  *   softcap: 0 (none) or up to 4096. slopes: device float [Hq] or NULL. prefix_lens: device int32 [B] or NULL; only with is_causal.
  *   doc_q [B, Nq], doc_k [B, Nk]: device int32, contiguous, both or neither. A negative id is padding,
  *   which sees nothing and is seen by nothing. Rows of k and v that are padding, or that lie behind the

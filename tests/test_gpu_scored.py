@@ -282,6 +282,35 @@ def test_slopes_of_either_sign():
             assert_close(lse, r["lse"], r["lse_tol"], "lse")
 
 
+@pytest.mark.parametrize("d,dtype", [(64, H), (128, F)])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_offsets_near_the_ends_of_32_bits(d, dtype, cap):
+    for offset in (-0x7fffff00 + 40000, 0x7fffff00 - 4, -40000, 2 ** 24 + 1):
+        check_slopes(d, dtype, cap, offset)
+    # a distance that passes 2^31 is refused; without slopes there is none
+    import quantized_attention_mean_gb300 as qa
+    q, k = (torch.randn(1, 1, n, d, device=DEV).to(dtype) for n in (4, 300))
+    for offset in (-0x7fffff00, -0x7fffff00 + 299):
+        with pytest.raises(qa.SageError):
+            qa.scored_attn(q, k, k, slopes=torch.ones(1, device=DEV), q_offset=offset, softcap=cap)
+        assert torch.equal(qa.scored_attn(q, k, k, q_offset=offset, softcap=cap), qa.scored_attn(q, k, k, softcap=cap))
+
+
+def check_slopes(d, dtype, cap, offset):
+    import quantized_attention_mean_gb300 as qa
+    g = torch.Generator().manual_seed(13)
+    nq, nk = 4, 40000
+    q, k, v = (torch.randn(1, h, n, d, generator=g).to(dtype).to(DEV) for h, n in ((2, nq), (1, nk), (1, nk)))
+    slopes = torch.tensor([1e-3, -2e-4])
+    dist = (torch.arange(nq)[:, None] + offset - torch.arange(nk)).abs().double()
+    b = (-slopes.double()[:, None, None] * dist)[None].to(DEV)
+    out, lse = qa.scored_attn(q, k, v, slopes=slopes.to(DEV), q_offset=offset, softcap=cap, return_lse=True)
+    kk, vv = (t.expand(1, 2, nk, d) for t in (k, v))
+    r = attend(q, kk, vv, d ** -0.5, cap, b, dtype=dtype)
+    assert_close(out, r["out"], r["out_tol"], f"out at {offset}")
+    assert_close(lse, r["lse"], r["lse_tol"], f"lse at {offset}")
+
+
 def test_strided_and_broadcast_inputs():
     g = torch.Generator().manual_seed(6)
     # a fused projection's slices: rows of one tensor
