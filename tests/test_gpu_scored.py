@@ -134,6 +134,54 @@ def test_few_rows_are_split_over_the_keys(nq, nk, hq, d, dtype):
           dk=docs_of([nk // 3, nk - nk // 3 - 9], 9, 1))
 
 
+# CTAs that walk many key tiles without a split: rings of stages and barrier phases that turn many times, the near-to-far
+# order, the shorter walk of the first query tile; some rows of each warp against float64
+@pytest.mark.parametrize("n,nk,d,dtype,layout,kw", [
+    (8192, 8192, 128, H, "HND", dict(causal=True)),
+    (8192, 8192, 128, H, "NHD", dict(causal=True, cap=50.0)),
+    (8192, 8192, 128, F, "HND", dict(causal=True, bias=True)),
+    (8190, 8190, 128, H, "HND", dict(causal=True, cap=12.0, bias=True)),      # scores that reach the cap
+    (4000, 9001, 128, F, "NHD", dict(causal=True, offset=5001)),
+    (2561, 20001, 128, H, "HND", dict(cap=30.0)),
+    (16383, 16383, 128, F, "NHD", dict(causal=True, docs=True)),
+    (8192, 8192, 128, H, "HND", dict(causal=True, prefix=4999)),
+    (8192, 8192, 64, F, "HND", dict(causal=True)),
+    (8192, 8192, 64, H, "NHD", dict(causal=True, cap=50.0)),
+    (8191, 8191, 64, H, "HND", dict(causal=True, bias=True)),
+    (8192, 8192, 64, F, "HND", dict(causal=True, cap=12.0, bias=True)),
+    (16383, 16383, 64, H, "NHD", dict(causal=True, docs=True)),
+    (16383, 16383, 64, F, "HND", dict(docs=True, cap=30.0, bias=True)),
+    (8192, 8192, 72, H, "NHD", dict(causal=True, prefix=6001, bias=True)),
+    (5000, 16001, 40, F, "HND", dict()),
+])
+def test_long_prompts(n, nk, d, dtype, layout, kw):
+    import quantized_attention_mean_gb300 as qa
+    hq, hkv = 8, 4
+    g = torch.Generator(DEV).manual_seed(n + d)
+    q, k, v = (torch.randn(1, h, m, d, generator=g, device=DEV).to(dtype) for h, m in ((hq, n), (hkv, nk), (hkv, nk)))
+    q = (q * 2).to(dtype)
+    slopes = 2.0 ** (-torch.arange(1, hq + 1, device=DEV).float() * 8 / hq) if kw.get("bias") else None
+    prefix = torch.tensor([kw["prefix"]], dtype=torch.int32, device=DEV) if "prefix" in kw else None
+    ids = docs_of([1, 5000, 130, 127, 6500, 4000], n - 15758).to(DEV) if kw.get("docs") else None
+    causal, offset, cap = kw.get("causal", False), kw.get("offset", 0), kw.get("cap", 0.0)
+    lay = lambda t: t if layout == "HND" else t.transpose(1, 2).contiguous()  # noqa: E731
+    out, lse = qa.scored_attn(lay(q), lay(k), lay(v), tensor_layout=layout, is_causal=causal, softcap=cap, slopes=slopes,
+                              prefix_lens=prefix, doc_ids=ids, q_offset=offset, return_lse=True)
+    out = lay(out) if layout == "HND" else out.transpose(1, 2)
+    rows = torch.cat([torch.arange(3, n, 61, device=DEV), torch.tensor([0, 127, 128, 255, 256, n - 1], device=DEV)])
+    i, j = rows[:, None] + offset, torch.arange(nk, device=DEV)
+    seen = (j <= i) if causal else torch.ones(len(rows), nk, dtype=torch.bool, device=DEV)
+    if prefix is not None:
+        seen = seen | (j < kw["prefix"])
+    if ids is not None:
+        seen = seen & (ids[0, rows, None] == ids[0]) & (ids[0] >= 0)
+    for h in range(hq):
+        bias = -slopes[h].double() * (i - j).abs().double() if slopes is not None else None
+        r = attend(q[0, h, rows], k[0, h * hkv // hq], v[0, h * hkv // hq], d ** -0.5, cap, bias, seen, dtype)
+        assert_close(out[0, h, rows], r["out"], r["out_tol"], f"out of head {h}")
+        assert_close(lse[0, h, rows], r["lse"], r["lse_tol"], f"lse of head {h}")
+
+
 # Few queries of several heads in one query tile or two, groups that do not fill them, splits and none
 @pytest.mark.parametrize("B,hq,hkv,nq,nk", [(2, 8, 2, 20, 6000), (2, 14, 2, 16, 6000), (2, 14, 2, 40, 6000),
                                             (1, 32, 8, 100, 9000), (20, 12, 4, 100, 300), (30, 16, 4, 5, 700),
