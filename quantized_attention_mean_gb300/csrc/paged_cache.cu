@@ -695,9 +695,12 @@ int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch
     if (cache->page_size == 1 << i) a.page_shift = i;
   a.vec4 = cache->page_size % 4 == 0 && reinterpret_cast<uintptr_t>(cache->mass) % 16 == 0 &&
            reinterpret_cast<uintptr_t>(cache->positions) % 16 == 0;
-  // few heads with long sequences: clusters, so that more SMs read and count (1024 threads fill an SM's registers)
+  // Few heads with long sequences: clusters, so that more SMs read and count (1024 threads fill an SM's registers). Their
+  // barriers and sums cost 5 to 8 us, so one CTA is faster up to some 18K tokens. us per call of 8 heads, nothing moved, by
+  // one CTA, clusters of two and of four: 4096 tokens 10.5, 15.1, 18.0; 16384 18.1, 18.8, 19.9; 32768 28.8, 24.1, 22.2
+  // (64 heads: 29.2, 24.6, 45.1, where clusters of four no longer run at once).
   const int64_t heads = (int64_t)batch * heads_kv;
-  const int ranks = max_seqlen < 4096 ? 1 : heads * 4 <= 152 ? 4 : heads * 2 <= 152 ? 2 : 1;
+  const int ranks = max_seqlen <= 18432 ? 1 : heads * 4 <= 152 ? 4 : heads * 2 <= 152 ? 2 : 1;
   const int share = (max_seqlen + ranks - 1) / ranks;
   cudaError_t e = ranks == 4 && share <= kMostCached - 4   ? launch_select<4>(a, share, heads_kv, st)
                   : ranks == 2 && share <= kMostCached - 4 ? launch_select<2>(a, share, heads_kv, st)

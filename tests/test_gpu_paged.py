@@ -512,6 +512,25 @@ def test_evict_long_sequences(lens, page, budget):
     assert torch.equal(G["k"].cpu(), c["k"]) and torch.equal(G["v"].cpu(), c["v"])
 
 
+@pytest.mark.parametrize("bound", [4100, 18432, 18433, 60000])
+@pytest.mark.parametrize("more", [0, 50, 160])
+def test_evict_bounds_above_the_lengths(bound, more):
+    # (the bound and the number of heads choose one CTA or a cluster to a sequence, most of it without a slot)
+    import quantized_attention_mean_gb300 as qa
+    hkv, d, page, budget = 1, 16, 8, 3
+    lens = [5, 9, 4100, 4, 13, 0, 1] + [7] * more
+    c = ref.make_cache(lens, hkv, d, page, torch.float16, seed=5)
+    c["table"] = torch.cat([c["table"], torch.full((len(lens), bound // page), -9, dtype=torch.int32)], 1)
+    g = torch.Generator().manual_seed(6)
+    mass = torch.randint(0, 50, (c["k"].shape[0], hkv, page), generator=g).float()
+    pos = torch.randint(0, 9999, mass.shape, generator=g, dtype=torch.int32)
+    G, gm, gp = on_gpu(c), mass.to(DEV), pos.to(DEV)
+    new = qa.paged_evict(G["k"], G["v"], gm, gp, G["table"], G["lens"], budget, bound, sink=1, recent=2)
+    want = ref.evict(c, mass, pos, budget, 1, 2)
+    assert torch.equal(new.cpu(), want) and torch.equal(gp.cpu(), pos) and torch.equal(gm.cpu(), mass)
+    assert torch.equal(G["k"].cpu(), c["k"]) and torch.equal(G["v"].cpu(), c["v"])
+
+
 def test_evict_where_more_would_have_to_stay():
     import quantized_attention_mean_gb300 as qa
     c = ref.make_cache([50], 1, 16, 8, torch.float16)
