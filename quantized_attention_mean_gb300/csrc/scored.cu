@@ -816,9 +816,10 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kPerSm)
               float big = fmaxf(max3(b4[0], b4[1], b4[2]), b4[3]);
               small = __all_sync(0xffffffffu, big <= a.poly.most);
               // A key that no row of the warp sees must not choose the form: then the products that are seen are looked
-              // at, from tensor memory. (8 heads x 16383 in 14 documents, d 64: 138 us; by selects for every part 155, in
-              // this branch 142; by all products, seen or not, 134.)
-              if (__builtin_expect(!small, 0)) {
+              // at, from tensor memory. (8 heads x 16383 in 14 documents, d 64: 139 us; by selects for every part 155, in
+              // this branch 142; by all products, seen or not, 133. Scores far beyond the cap, 8192 causal, d 128: 951 us;
+              // looked at in parts that every row sees too, 1109.)
+              if (!small && !__all_sync(0xffffffffu, bits[0] == 0xffffffffu)) {
                 big = 0.f;
 #pragma unroll 1
                 for (int u = 0; u < 32; u += 8) {
