@@ -3,12 +3,13 @@
 //   t_j = sm_scale q.k_j, capped to cap tanh(t_j / cap), less slope |pos_q - pos_j|
 //   out = sum_j softmax(t)_j v_j over the sequence's held tokens, lse = ln sum_j exp t_j
 //
-// Every held K and V row is read once, so DRAM bounds it: a ragged batch of 32 sequences of up to 32K tokens (8 heads, head_dim
-// 128) takes 270 us, 94% of what a copy's rate (6.8 TB/s) allows; two contexts of 50-60K tokens with their weights
-// 173 us, 84%; a single short sequence 7.8 us in a graph, the latency of the chain length, page, row. The query heads of one key/value
-// head are the (at most 16) rows of an m16n8k16 product: a tcgen05 tile would have 128 rows, of which
-// a decode step fills the same few, and the tensor work here is a small part of what the memory
-// time allows.
+// Up to 16 query heads per key/value head every held K and V row is read once, so DRAM bounds it: a ragged batch of 32 sequences
+// of up to 32K tokens (8 heads, head_dim 128) takes 280-284 us, 90% of what a copy's rate (6.8 TB/s) allows; two contexts of
+// 50-60K tokens with their weights 175-178 us, 83%; a single short sequence 7.5 us in a graph, the latency of the chain length, page,
+// row. The query heads of one key/value head are the rows of m16n8k16 products, in blocks of 16: a tcgen05 tile would have
+// 128 rows, of which a decode step fills the same few, and the tensor work here is a small part of what the memory time
+// allows. Each further block is an item of its own and reads the rows again, mostly from L2 where they fit: 8 sequences of 32K
+// tokens, one key/value head, 8 query heads 35 us, 16 39, 32 51, 64 87.
 //
 // Split: the (sequence, head, key tile) items of the whole batch form one line, cut into equal
 // ranges, one per CTA, so the load is even whatever the lengths (which only the device knows). Each
@@ -1010,8 +1011,8 @@ struct DecodeLayout {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // Few heads with short sequences: one launch of clusters whose CTAs all run at once, a tile or a few each, joined
 // through distributed shared memory. Otherwise the line, which balances any lengths but takes a second launch
-// to join (one sequence of 1000 tokens, 8 key/value heads, in a graph: 7.8 against 12.4 us; beyond
-// eight tiles per CTA the line's 304 CTAs are faster than the clusters').
+// to join. us in a graph, clusters and line, head_dim 128: 8 heads of 1000 tokens 7.4 and 11.0, of 4000 14.3 and 14.9,
+// of 8000 23.5 and 17.4; 16 of 2000 11.1 and 13.2; 38 of 300 11.5 and 13.4, of 4000 29.2 and 22.1; 128 of 300 25.8 and 17.6.
 bool clustered(int batch, int hkv, int row_blocks, int64_t max_len, int d) {
   const int tile = d <= 64 ? DecodeCfg<64>::kTile : DecodeCfg<128>::kTile;
   return (int64_t)hkv * row_blocks * batch * kRanks <= kCtas && max_len <= 8 * kRanks * tile;
@@ -1132,8 +1133,9 @@ int sage_paged_attn(const sage_packed* q, const sage_paged_cache* cache, const s
   a.page_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (pc.page_size == 1 << i) a.page_shift = i;
-  // the join by 32 channels where its CTAs would leave SMs idle (one sequence of 20000 tokens: 24.2 us against
-  // 25.8; 64 sequences of 200: 28.5 against 25.2)
+  // the join by 32 channels where its CTAs would leave SMs idle (head_dim 128, us by slices and whole: 8 heads of 20000 tokens
+  // 24.3 and 26.0, 16 of 2000 13.2 and 14.2, 38 of 20000 68.9 and 71.0; 64 of 20000 111.8 and 108.7, 256 of 2000 56.0 and 53.0;
+  // head_dim 64 within 2%)
   a.slices = (int64_t)heads_kv * a.row_blocks * batch <= 38 ? (head_dim <= 64 ? 2 : 4) : 1;
   CUtensorMap maps[2];
   std::memset(maps, 0, sizeof(maps));

@@ -515,8 +515,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 
 // Moves the listed tokens: a half warp per token, 16 bytes per lane. Sources lie behind the budget and
 // targets below it, so no move reads what another one writes. (More tokens in flight per half warp measured
-// slower: 2 and 4 of them 109 and 113 us against 98 for the whole call, 64 heads of up to 32K tokens,
-// since the registers cost resident warps.)
+// slower, since the registers cost resident warps: 2 and 4 of them 11 and 15 us more for 64 heads of up to 32K tokens, whose
+// moves take 37.)
 __global__ void __launch_bounds__(256, 8) evict_move_kernel(const EvictArgs a) {
   const int h = blockIdx.y, b = blockIdx.z;
   const int64_t me = (int64_t)b * a.c.hkv + h;

@@ -25,8 +25,11 @@
 // Bound by the softmax warps: per score one exponential (4 cycles a warp and sub-partition), half an instruction each to
 // scale, sum and round, and the passes through tensor memory around them; products take 63% of the
 // cycles at head_dim 128. Rates (bf16, of 1884 TFLOP/s measured for a library product): 4 x 38 heads of 4096^2, head_dim 128:
-// 1500 TFLOP/s, capped 1140, biased 1420; head_dim 64: 1110, capped 660, biased 940. 32 heads of 8 at 8192, causal, 128:
-// 375-388 us, capped 503, biased 415, both 563.
+// 1490-1500 TFLOP/s, capped 1115-1135, biased 1395; head_dim 64: 1090, capped 645, biased 940. 32 heads of 8 at 8192,
+// causal, 128: 368-378 us, capped 505, biased 405, both 566.
+// Two costs depend on the values. A product above 0.7 of the cap sends its warp's tile through the loop for masked
+// tiles, with the quotient: scores far beyond the cap take 951 us there (head_dim 64: 840 for 450). And fp16 with a cap and a
+// slope above 0.32 takes the loop for every tile (see `gentle`): 866 for 566.
 #include <cmath>
 
 #include "../../include/sageattn.h"
@@ -660,7 +663,8 @@ __global__ void __launch_bounds__(Cfg<DP>::kThreads, Cfg<DP>::kPerSm)
     float slope = 0.f;
     if constexpr (BIAS) slope = __ldg(&a.slopes[h]) * kL2e;
     // (a warp's rows may be of heads with different slopes; where fp16's few bits of slack make many slopes steep, their
-    // maximum is taken exactly)
+    // maximum is taken exactly: 8192 causal with slopes of 0.5 455 us, with gentle ones 407; with a cap it would cost a
+    // capped score more per key, and steep slopes take the loop)
     constexpr bool kExact = !BF16 && !CAP;
     const bool gentle = !BIAS || __all_sync(0xffffffffu, fabsf(slope) * 15.0f <= kSlack);
     const float cap_m2 = -2.0f * a.cap2, cap_in = a.cap_k;
