@@ -1281,7 +1281,8 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
   const int64_t blocks_q = ((int64_t)seqlen_q + cta_rows - 1) / cta_rows;
   // (positions, and with slopes distances, that the kernel holds in 32 bits)
   if (seqlen_k > 0x7fffff00 || seqlen_q > 0x7fffff00 || (int64_t)q_offset + seqlen_q > 0x7fffff00 ||
-      q_offset < -0x7fffff00 || (slopes && (int64_t)q_offset - seqlen_k < -0x7fffff00) || blocks_q > 65535 || (int64_t)batch * L.splits > 65535 || (int64_t)batch * heads_q * seqlen_q > (1LL << 32))
+      q_offset < -0x7fffff00 || (slopes && (int64_t)q_offset - seqlen_k < -0x7fffff00) || blocks_q > 65535 ||
+      (int64_t)batch * L.splits > 65535 || (int64_t)batch * heads_q * seqlen_q > (1LL << 32))
     return SAGE_ERR_INVALID_ARG;
   // (the status word alone can do without)
   if (workspace ? reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < L.total : L.total > SAGE_STATUS_BYTES)

@@ -45,7 +45,8 @@ def scored_attn(q, k, v, tensor_layout="HND", is_causal=False, sm_scale=None, so
     is_causal; ``doc_ids`` int32 [B, Nq] and ``doc_ids_k`` int32 [B, Nk] (default: doc_ids, Nq == Nk). A negative
     id is padding. Rows of k and v that are padding, or that lie behind the last key any row sees under the causal
     and prefix masks, may hold anything; all others must be finite in v. ``q_offset``: how many keys lie before the first
-    query (the next chunk of a prompt); positions and, with slopes, distances beyond 2^31 - 256 are refused. A row that sees no key gives 0 and lse -inf.
+    query (the next chunk of a prompt); positions and, with slopes, distances beyond 2^31 - 256 are refused. A row that
+    sees no key gives 0 and lse -inf.
     Returns out, plus lse [B, Hq, Nq] fp32 if return_lse."""
     _check_dense_args(q, k, v, tensor_layout, out, lse, return_lse, workspace)
     B, hq, hkv, nq, nk, d = _dims(q, k, tensor_layout)
