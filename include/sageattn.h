@@ -61,6 +61,8 @@ typedef enum {
 
 enum { SAGE_HND = 0, SAGE_NHD = 1 };                       /* §4.1 tensor_layout */
 enum { SAGE_F16 = 0, SAGE_BF16 = 1 };                      /* input/output dtype */
+enum { SAGE_F32 = 2 };                                     /* weights of sage_qk_norm_rope besides */
+enum { SAGE_S8 = 0, SAGE_E4M3 = 1 };                       /* codes of an 8-bit cache */
 enum { SAGE_PER_BLOCK = 0, SAGE_PER_WARP = 1, SAGE_PER_THREAD = 2 };   /* qk_quant_gran */
 enum { SAGE_ACC_FP32 = 0, SAGE_ACC_FP16_FP32 = 1, SAGE_ACC_FP32_FP32 = 2, SAGE_ACC_FP16 = 3 };
 
@@ -336,6 +338,107 @@ size_t sage_paged_evict_workspace_size(int batch, int heads_kv, int max_seqlen, 
 int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch, int heads_kv,
                      int max_seqlen, int head_dim, int dtype, int tensor_layout, int budget, int sink,
                      int recent, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- Serving from an 8-bit cache: norms and rotation, page tables, append, read, attention ---- */
+
+/* Norms of queries and keys for each (token, head) row and their rotation by position, in one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * w;  pairs p < rot_dim / 2 of channels (p, p + rot_dim / 2), or
+ *   (2 p, 2 p + 1) with interleaved, turned by position * inv_freq[p]:
+ *   (y_i cos a - y_j sin a, y_j cos a + y_i sin a). Channels from rot_dim on are not turned.
+ *   q, q_out: Hq heads of `seqlen` tokens as sage_attn's q; k, k_out: Hkv heads of the same tokens. An
+ *   output may be its input (the same address and strides), and must not overlap an input otherwise.
+ *   positions: device int32, token i of batch b at b positions_stride + i; NULL: i. inv_freq: device
+ *   float [rot_dim / 2] (NULL with rot_dim 0). q_weight, k_weight: device [head_dim] of `dtype` or SAGE_F32
+ *   (weight_dtype), or NULL for ones. Squares are summed in fp32: magnitudes below 1e18.
+ * Angles are exact to 2^-33 of a turn or better at every position. rot_dim even, 0 to head_dim. */
+int sage_qk_norm_rope(const sage_tensor* q, const sage_tensor* k, const sage_tensor* q_out,
+                      const sage_tensor* k_out, const int32_t* positions, int64_t positions_stride,
+                      const float* inv_freq, const void* q_weight, const void* k_weight,
+                      int weight_dtype, int batch, int heads_q, int heads_kv, int seqlen, int head_dim,
+                      int rot_dim, int dtype, int tensor_layout, int interleaved, float eps,
+                      void* stream);
+
+/* Pages for sequences that grow, from a stack of free ones: the first *free_count entries of
+ * free_pages [num_pages] (device int32). Sequence b holds seq_lens[b] tokens and is to hold add_lens[b]
+ * more (device int32 [batch]). In the order of the sequences, each takes the pages it lacks from the top of the
+ * stack into its row of page_table; once one finds too few, it and all later ones that need pages take
+ * none. Table entries of pages that are held already, or behind the last, are not touched.
+ *   new_lens [batch]: seq_lens + add_lens where served, seq_lens otherwise; held_lens [batch]: seq_lens
+ *   where served, -1 otherwise (the appends leave such tokens out); cu_seqlens [batch + 1]: where the new tokens
+ *   of each sequence lie in packed rows, served or not; positions [max_tokens]: next_positions[b] (NULL:
+ *   seq_lens[b]) + the token's place, -1 behind the last; slots [max_tokens] (int64): page * page_size +
+ *   place in the page of each new token, -1 where it has none; new_free_count [1]. All device, none of
+ *   them an input.
+ * A sequence whose lengths are negative, exceed its row of the table, or whose new tokens end behind
+ * max_tokens is not served (SAGE_ERR_SEQLENS, as for a count outside of [0, num_pages], which is clamped;
+ * a held page outside of the cache leaves its slot -1: SAGE_ERR_PAGE). workspace: NULL or
+ * SAGE_STATUS_BYTES. */
+int sage_paged_assign(int32_t* page_table, int64_t table_stride, int max_pages, const int32_t* seq_lens,
+                      const int32_t* add_lens, const int32_t* next_positions, const int32_t* free_pages,
+                      const int32_t* free_count, int num_pages, int page_size, int batch, int max_tokens,
+                      int32_t* new_lens, int32_t* held_lens, int32_t* cu_seqlens, int32_t* positions,
+                      int64_t* slots, int32_t* new_free_count, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* Pages of sequences that shrink, back onto the stack: of the seq_lens[b] tokens that sequence b holds
+ * keep_lens[b] stay; the pages behind them are written to free_pages from *free_count on, in the order of
+ * the sequences and of their rows. The table is not changed. A sequence with lengths out of range or
+ * keep_lens > seq_lens (SAGE_ERR_SEQLENS), or with a page among those given that is not in
+ * [0, num_pages) (SAGE_ERR_PAGE), gives none; where the stack has no room, that sequence and the later ones
+ * do not either (SAGE_ERR_SEQLENS). */
+size_t sage_paged_release_workspace_size(int batch);
+int sage_paged_release(const int32_t* page_table, int64_t table_stride, int max_pages,
+                       const int32_t* seq_lens, const int32_t* keep_lens, int32_t* free_pages,
+                       const int32_t* free_count, int num_pages, int page_size, int batch,
+                       int32_t* new_free_count, void* workspace, size_t workspace_bytes, void* stream);
+
+/* A paged cache in 8 bits. As sage_paged_cache, with codes of k_type / v_type (SAGE_S8, SAGE_E4M3; strides in
+ * elements) and k_scales / v_scales: device float [num_pages, Hkv, page_size / block], contiguous; `block`
+ * divides page_size. Slot t of a page has the scale t / block; a value is code * scale. */
+typedef struct {
+  void* k;
+  int64_t k_stride[3];
+  void* v;
+  int64_t v_stride[3];
+  float* k_scales;
+  float* v_scales;
+  int k_type, v_type;
+  int num_pages, page_size, block;
+  const int32_t* page_table;
+  int64_t table_stride;
+  int max_pages;
+  const int32_t* seq_lens;
+} sage_q8_cache;
+
+/* Writes new tokens behind the held ones, as sage_paged_append, into an 8-bit cache. With x the block's new
+ * tokens of a head and s the scale of the earlier ones (0 where the block starts with a new token), the
+ * scale becomes max(s, need, 2^-100), need = max|x| / 127 for int8, the smallest power of two with
+ * max|x| <= 448 need for E4M3; codes are x / scale rounded to nearest even (as x times fl32(1 / scale)), and
+ * where the scale grew the earlier codes become code * fl32(s / scale), rounded again. k and v must be finite.
+ * Two sequences must not append to one block. */
+int sage_paged_append_q8(const sage_packed* k, const sage_packed* v, const sage_q8_cache* cache,
+                         const int32_t* cu_seqlens, int batch, int tokens, int heads_kv, int head_dim,
+                         int dtype, int tensor_layout, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Values of held tokens in 16 bits: row t of k_out, v_out [tokens, Hkv, d] with cu_seqlens[b] <= t <
+ * cu_seqlens[b + 1] is slot starts[b] + t - cu_seqlens[b] of sequence b (starts: device int32 [batch] or
+ * NULL for 0). Rows of no held token (behind seq_lens, SAGE_ERR_SEQLENS; of a page outside of the cache,
+ * SAGE_ERR_PAGE; behind the last sequence) become 0. workspace: NULL or SAGE_STATUS_BYTES. */
+int sage_paged_read_q8(const sage_packed* k_out, const sage_packed* v_out, const sage_q8_cache* cache,
+                       const int32_t* cu_seqlens, const int32_t* starts, int batch, int tokens,
+                       int heads_kv, int head_dim, int dtype, int tensor_layout, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* sage_paged_attn over an 8-bit cache; positions of keys are their slots. Scales must be finite and not
+ * negative. Weights are rounded to fp16 once, whatever q's type. */
+size_t sage_paged_attn_q8_workspace_size(int batch, int heads_q, int heads_kv, int max_seqlen,
+                                         int head_dim);
+int sage_paged_attn_q8(const sage_packed* q, const sage_q8_cache* cache, const sage_packed* out, float* lse,
+                       const float* slopes, const int32_t* q_positions, int batch, int heads_q,
+                       int heads_kv, int max_seqlen, int head_dim, int dtype, int tensor_layout,
+                       float sm_scale, float softcap, void* workspace, size_t workspace_bytes,
+                       void* stream);
 
 /* Human-readable name of a sage_status. Never NULL. */
 const char* sage_status_string(int status);

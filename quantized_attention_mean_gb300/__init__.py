@@ -402,5 +402,13 @@ from .paged import (paged_append, paged_attn, paged_attn_workspace_bytes, paged_
                     paged_evict_workspace_bytes)
 from .scored import scored_attn, scored_attn_workspace_bytes  # noqa: E402
 
+from .page_tables import (PageAssignment, paged_assign, paged_release,  # noqa: E402
+                          paged_release_workspace_bytes)
+from .paged_q8 import (paged_append_q8, paged_attn_q8, paged_attn_q8_workspace_bytes,  # noqa: E402
+                       paged_read_q8)
+from .rope import qk_norm_rope  # noqa: E402
+
+__all__ += ["qk_norm_rope", "PageAssignment", "paged_assign", "paged_release", "paged_release_workspace_bytes",
+            "paged_append_q8", "paged_read_q8", "paged_attn_q8", "paged_attn_q8_workspace_bytes"]
 __all__ += ["scored_attn", "scored_attn_workspace_bytes", "paged_attn", "paged_append", "paged_evict", "paged_attn_workspace_bytes",
             "paged_evict_workspace_bytes"]

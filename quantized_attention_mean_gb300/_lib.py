@@ -35,10 +35,20 @@ class SagePagedCache(ctypes.Structure):
                    ("mass", c_void_p), ("positions", c_void_p)])
 
 
+class SageQ8Cache(ctypes.Structure):
+    # (the strides as single fields, as above)
+    _fields_ = ([("k", c_void_p)] + [(f"k_stride{i}", c_int64) for i in range(3)] + [("v", c_void_p)]
+                + [(f"v_stride{i}", c_int64) for i in range(3)]
+                + [("k_scales", c_void_p), ("v_scales", c_void_p), ("k_type", c_int), ("v_type", c_int),
+                   ("num_pages", c_int), ("page_size", c_int), ("block", c_int), ("page_table", c_void_p),
+                   ("table_stride", c_int64), ("max_pages", c_int), ("seq_lens", c_void_p)])
+
+
 # name -> (restype, argtypes), mirroring include/sageattn.h
 _T = ctypes.POINTER(SageTensor)
 _P = ctypes.POINTER(SagePacked)
 _C = ctypes.POINTER(SagePagedCache)
+_Q = ctypes.POINTER(SageQ8Cache)
 SIGNATURES = {
     "sage_attn_workspace_size": (c_size_t, [c_int] * 7),
     "sage_attn": (c_int, [_T, _T, _T, _T, c_void_p] + [c_int] * 9 + [c_float] + [c_int] * 5
@@ -84,6 +94,17 @@ SIGNATURES = {
                           + [c_void_p, c_size_t, c_void_p]),
     "sage_paged_evict_workspace_size": (c_size_t, [c_int] * 4),
     "sage_paged_evict": (c_int, [_C, c_void_p] + [c_int] * 9 + [c_void_p, c_size_t, c_void_p]),
+    "sage_qk_norm_rope": (c_int, [c_void_p] * 5 + [c_int64] + [c_void_p] * 3 + [c_int] * 10 + [c_float, c_void_p]),
+    "sage_paged_assign": (c_int, [c_void_p, c_int64, c_int] + [c_void_p] * 5 + [c_int] * 4 + [c_void_p] * 7
+                          + [c_size_t, c_void_p]),
+    "sage_paged_release_workspace_size": (c_size_t, [c_int]),
+    "sage_paged_release": (c_int, [c_void_p, c_int64, c_int] + [c_void_p] * 4 + [c_int] * 3 + [c_void_p] * 2
+                           + [c_size_t, c_void_p]),
+    "sage_paged_append_q8": (c_int, [_P, _P, _Q, c_void_p] + [c_int] * 6 + [c_void_p, c_size_t, c_void_p]),
+    "sage_paged_read_q8": (c_int, [_P, _P, _Q, c_void_p, c_void_p] + [c_int] * 6 + [c_void_p, c_size_t, c_void_p]),
+    "sage_paged_attn_q8_workspace_size": (c_size_t, [c_int] * 5),
+    "sage_paged_attn_q8": (c_int, [_P, _Q, _P, c_void_p, c_void_p, c_void_p] + [c_int] * 7 + [c_float] * 2
+                           + [c_void_p, c_size_t, c_void_p]),
 }
 
 _lib = None

@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsageattn.so")
 SOURCES = ["api.cu", "quant.cu", "attention.cu", "no_alloc.cu", "merge.cu", "short.cu",
-           "paged_attn.cu", "paged_cache.cu", "scored.cu"]
+           "paged_attn.cu", "paged_cache.cu", "scored.cu", "rope.cu", "page_tables.cu", "paged_q8_cache.cu",
+           "paged_q8_attn.cu", "paged_q8_attn64.cu", "paged_q8_attn128.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          f"-I{ROOT}/include"]

@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const AssignArgs a) {
     s_first[tid] = (int)(count - 1 - (served ? last - g.need : 0));
   }
   const int n = min(a.per, a.batch - b0);
+  if (n == 0 && tid == 0) s_cu[0] = a.cu[0] = 0;  // (no sequence at all)
   if (tid == n - 1) s_cu[n] = (int)(t1 < a.max_tokens ? t1 : a.max_tokens);
   if (split == 0 && mine) {
     a.cu[b] = s_cu[tid];
@@ -174,7 +175,8 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const AssignArgs a) {
         const int held = __ldg(&a.lens[b0 + lo]), where = held + i, page = where / a.page_size;
         const int k = page - s_have[lo];
         const int pg = k < 0 ? a.table[(int64_t)(b0 + lo) * a.table_stride + page] : __ldg(&a.free_pages[s_first[lo] - k]);
-        slot = (long long)pg * a.page_size + (where - page * a.page_size);
+        if (pg >= 0 && pg < a.capacity) slot = (long long)pg * a.page_size + (where - page * a.page_size);
+        else if (a.err) record_error(a.err, kDevPage);
       }
     }
     a.positions[t] = pos;

@@ -1,0 +1,742 @@
+// The decode kernel over an 8-bit paged cache (sage_paged_attn_q8) and its launch.
+//
+//   t_j = sm_scale s_k(j) q.c_k(j), capped to cap tanh(t_j / cap), less slope |pos_q - j|
+//   out = sum_j softmax(t)_j s_v(j) c_v(j),  lse = ln sum_j exp t_j;  c: codes, s: their blocks' scales
+//
+// DRAM bounds it, at half the bytes of 16-bit rows, so per byte twice as many instructions are spent as by the kernel
+// over those. What keeps them few:
+// - The products are transposed: keys (then channels) are the 16 rows of m16n8k16, the query heads of a key/value head its
+//   8 columns, so that the usual groups of 4 to 8 heads fill an instruction that they would half leave empty as rows.
+// - Codes become fp16 in registers, exactly (an E4M3 code by one conversion per pair, an int8 code as 1024 + code + 128
+//   by a byte permutation and one subtraction); scales are applied to scores and weights, one per key, never to codes.
+// - q becomes fp16 scaled by a power of two, which takes the largest channel of its row to [2^14, 2^15): channels down to
+//   2^-38 of it keep the bits they have, so nothing is lost against bf16.
+// - V's scale goes into the weight before it is rounded to fp16, w = 2^(t + log2 s_v - F), with F a running frame of
+//   t + log2 s_v of its own: weights of blocks with small scales keep their bits, whatever the largest scale is.
+// - Rows and columns change places between the products by movmatrix; V is read transposed by ldmatrix, two keys by two
+//   channels in a register, of which a byte permutation makes the pairs of keys that the product wants.
+//
+// Split, loads and join as in the kernel over 16-bit rows (decode_line.cuh): ranges of one line of items, or clusters
+// of eight CTAs where heads are few and sequences short.
+#pragma once
+#include "decode_line.cuh"
+#include "launch.h"
+#include "paged_q8.cuh"
+
+namespace sage {
+
+struct Q8Args {
+  DecodeArgs a;
+  const float* ks; const float* vs;
+  int block, blocks;
+  int unit;      // bytes of one copy where rows do not come by TMA: 16, 8, 4, or 1 (plain loads)
+  int bf16;      // type of q and out
+  int q4;        // q allows accesses of four channels
+  int cluster;   // form: clusters, or the line
+  int k_type, v_type;
+};
+
+cudaError_t launch_q8_decode_64(const Q8Args& p, const CUtensorMap* maps, cudaStream_t st);
+cudaError_t launch_q8_decode_128(const Q8Args& p, const CUtensorMap* maps, cudaStream_t st);
+
+template <int DP>
+struct Q8Cfg {
+  static constexpr int kStages = 3;
+  static constexpr int kKeys = DP == 128 ? 32 : 64;           // keys per warp and tile (8 KB of K and V)
+  static constexpr int kTile = 4 * kKeys;                     // keys per tile
+  static constexpr int kTileBytes = kKeys * DP;               // K or V of one warp's tile
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kOffMerge = 4 * kWarpBytes;            // two warps' accumulators of eight heads
+  static constexpr int kOffScale = kOffMerge + 2 * (DP / 16) * 32 * 16;
+  static constexpr int kOffMl = kOffScale + 4 * kStages * 2 * kKeys * 4;
+  static constexpr int kOffBar = kOffMl + 4 * 16 * 4 * 4;
+  static constexpr int kSmem = kOffBar + 4 * kStages * 8;
+};
+
+namespace {
+
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, int src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Four codes as two pairs of fp16: bytes (A, B) and (C, D) of x.
+template <int TYPE, int A, int B, int C, int D>
+__device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  if constexpr (TYPE == SAGE_S8) {
+    const uint32_t u = x ^ 0x80808080u;  // code + 128
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1024 + 128
+    const uint32_t a = __byte_perm(u, 0x64646464u, A | 4 << 4 | B << 8 | 4 << 12);
+    const uint32_t b = __byte_perm(u, 0x64646464u, C | 4 << 4 | D << 8 | 4 << 12);
+    const __half2 ha = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+    const __half2 hb = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+    lo = *reinterpret_cast<const uint32_t*>(&ha);
+    hi = *reinterpret_cast<const uint32_t*>(&hb);
+  } else {
+    const uint32_t u = A == 0 && B == 1 ? x : __byte_perm(x, 0, A | B << 4 | C << 8 | D << 12);
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(u));
+  }
+}
+// Byte offset of 16-byte unit c of row r of a tile: the swizzle that a TMA box of rows of DP bytes is written with.
+template <int DP>
+__device__ __forceinline__ int unit_at(int r, int c) {
+  return DP == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// A warp's keys of one item into a stage: K, V and the keys' scales. Tokens that are not there and channels past d become
+// zero. page, slot: of keys lane, lane + 32, ...
+template <int DP>
+__device__ __forceinline__ void load_q8_stage(const Q8Args& p, const CUtensorMap* tmK, const CUtensorMap* tmV, int h,
+                                              const int (&page)[Q8Cfg<DP>::kKeys / 32], const int (&slot)[Q8Cfg<DP>::kKeys / 32],
+                                              uint8_t* stage, float* scale, uint32_t bar) {
+  using C = Q8Cfg<DP>;
+  constexpr int N = C::kKeys / 32;
+  const DecodeArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(stage);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool in = page[i] >= 0;
+    const int64_t at = in ? ((int64_t)page[i] * a.c.hkv + h) * p.blocks + slot[i] / p.block : 0;
+    const uint32_t dst = smem_u32(scale + lane + 32 * i);
+    cp_async_small<4>(dst, p.ks + at, in ? 4 : 0);
+    cp_async_small<4>(dst + C::kKeys * 4, p.vs + at, in ? 4 : 0);
+  }
+  if (a.load == kLoadTma) {
+    if (lane == 0)
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(C::kStageBytes) : "memory");
+    __syncwarp();
+    const int kv = lane & 1, row = (lane >> 1) * a.box_rows;
+    int pg = 0, sl = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int x = __shfl_sync(0xffffffffu, page[i], row & 31), y = __shfl_sync(0xffffffffu, slot[i], row & 31);
+      if (i == row >> 5) { pg = x; sl = y; }
+    }
+    if (row < C::kKeys)
+      tma_box(base + kv * C::kTileBytes + row * DP, kv ? tmV : tmK, bar, 0, sl, h, pg >= 0 ? pg : a.c.num_pages);
+    return;
+  }
+  const uint8_t* kb = static_cast<const uint8_t*>(a.c.k) + h * a.c.k_sh;
+  const uint8_t* vb = static_cast<const uint8_t*>(a.c.v) + h * a.c.v_sh;
+  constexpr int kUnits = DP / 16, kRowsPer = 32 / kUnits;
+  const int c = lane % kUnits;
+#pragma unroll 1
+  for (int i = 0; i < C::kKeys / kRowsPer; ++i) {
+    const int r = i * kRowsPer + lane / kUnits;
+    int pg = -1, sl = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int x = __shfl_sync(0xffffffffu, page[n], r & 31), y = __shfl_sync(0xffffffffu, slot[n], r & 31);
+      if (n == r >> 5) { pg = x; sl = y; }
+    }
+    const int left = pg >= 0 ? min(16, a.c.d - c * 16) : 0;  // codes of this unit that are there
+    const int off = unit_at<DP>(r, c);
+    const uint8_t* ks = left > 0 ? kb + pg * a.c.k_sp + sl * a.c.k_st + c * 16 : kb;
+    const uint8_t* vs = left > 0 ? vb + pg * a.c.v_sp + sl * a.c.v_st + c * 16 : vb;
+    const uint32_t kd = base + off, vd = base + C::kTileBytes + off;
+    if (p.unit == 16) {
+      cp_async16(kd, ks, left > 0 ? 16 : 0);
+      cp_async16(vd, vs, left > 0 ? 16 : 0);
+    } else if (p.unit == 8) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 8) {
+        const int n = left > e ? 8 : 0;
+        cp_async_small<8>(kd + e, n ? ks + e : kb, n);
+        cp_async_small<8>(vd + e, n ? vs + e : vb, n);
+      }
+    } else if (p.unit == 4) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const int n = left > e ? 4 : 0;
+        cp_async_small<4>(kd + e, n ? ks + e : kb, n);
+        cp_async_small<4>(vd + e, n ? vs + e : vb, n);
+      }
+    } else {
+#pragma unroll 1
+      for (int e = 0; e < 16; ++e) {
+        stage[off + e] = e < left ? ks[e] : 0;
+        stage[C::kTileBytes + off + e] = e < left ? vs[e] : 0;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void store_out(const Q8Args& p, int64_t at, float x) {
+  if (p.bf16) static_cast<__nv_bfloat16*>(p.a.o)[at] = __float2bfloat16_rn(x);
+  else static_cast<__half*>(p.a.o)[at] = __float2half_rn(x);
+}
+
+// NH: blocks of eight query heads, the columns of the products.
+template <int KT, int VT, int DP, int NH>
+__global__ void __launch_bounds__(kWarps * 32, 2)
+    q8_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Q8Args p) {
+  using C = Q8Cfg<DP>;
+  constexpr int S = C::kStages, KS = DP / 16, M = C::kKeys / 16, NP = C::kKeys / 32;
+  constexpr float kHead = 7.0f;  // weights are held at up to 2^(7 + 8), so that the smallest keep their bits in fp16
+  extern __shared__ __align__(1024) uint8_t sm[];
+  __shared__ int s_err[kWarps];
+  const DecodeArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int heads = a.c.hkv * a.row_blocks;
+  uint8_t* const ring = sm + warp * C::kWarpBytes;
+  float* const scales = reinterpret_cast<float*>(sm + C::kOffScale) + warp * S * 2 * C::kKeys;
+  float4* const merge = reinterpret_cast<float4*>(sm + C::kOffMerge);
+  float4* const ml = reinterpret_cast<float4*>(sm + C::kOffMl);  // [warp][row]: m, l, F
+  const uint32_t bars = smem_u32(sm + C::kOffBar) + warp * S * 8;
+  if (lane < S) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + lane * 8) : "memory");
+  fence_mbar_init();
+  if (a.load == kLoadTma && lane == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  pdl_wait();
+  const int me = blockIdx.x;
+  int err = 0;
+  long long left = 0;
+  Cursor cu{a.c.batch, 0, 0, 1, 0};
+  __shared__ long long s_base;
+  __shared__ int s_b;
+  if (p.cluster) {
+    const int rank = me % kRanks;
+    cu.b = blockIdx.y;
+    cu.h = me / kRanks;
+    cu.len = max(checked_len(a.c, cu.b, a.max_len), 0);
+    cu.tiles = tiles_of<C::kTile>(cu.len);
+    cu.tile = cu.tiles * rank / kRanks;
+    left = cu.tiles * (rank + 1) / kRanks - cu.tile;
+  } else {
+    // this CTA's range of the line: the total, then the sequence that its first item lies in
+    bool bad = false;
+    if (threadIdx.x == 0) { s_b = a.c.batch; s_base = 0; }
+    Scan sc = scan_items<C::kTile>(a, heads, 0, bad);
+    long long total = sc.all;
+    for (int b0 = blockDim.x; b0 < a.c.batch; b0 += blockDim.x) total += scan_items<C::kTile>(a, heads, b0, bad).all;
+    const int ctas = total > 0 ? ctas_of(total) : 0;
+    long long i0 = 0;
+    if (me < ctas) {
+      i0 = first_item(total, ctas, me);
+      left = first_item(total, ctas, me + 1) - i0;
+      long long base = 0;
+      for (int b0 = 0;;) {
+        const long long lo = base + sc.before;
+        if (sc.n > 0 && i0 >= lo && i0 < lo + sc.n) { s_b = b0 + threadIdx.x; s_base = lo; }
+        base += sc.all;
+        b0 += blockDim.x;
+        if (base > i0 || b0 >= a.c.batch) break;
+        sc = scan_items<C::kTile>(a, heads, b0, bad);
+      }
+    }
+    __syncthreads();
+    err = bad ? kDevSeqlens : 0;
+    if (left > 0) {
+      cu.b = s_b;
+      cu.len = checked_len(a.c, cu.b, a.max_len);
+      cu.tiles = tiles_of<C::kTile>(cu.len);
+      const long long in = i0 - s_base;
+      cu.h = (int)(in / cu.tiles);
+      cu.tile = (int)(in - (long long)cu.h * cu.tiles);
+    }
+  }
+  pdl_trigger();
+  if (p.cluster && a.err && me == 0 && blockIdx.y == 0) {
+    // the status word has one writer (but for a wait that runs out, two seconds from now): the first
+    // CTA looks at the lengths and pages of all sequences
+    int e = 0;
+    for (int b = 0; b < a.c.batch; ++b) {
+      const int len = checked_len(a.c, b, a.max_len);
+      if (len < 0) e = max(e, (int)kDevSeqlens);
+      for (int64_t i = threadIdx.x; i < ((int64_t)len + a.c.page_size - 1) / a.c.page_size; i += kWarps * 32) {
+        const int pg = __ldg(&a.c.table[b * a.c.table_stride + i]);
+        if (pg < 0 || pg >= a.c.num_pages) e = max(e, kDevPage);
+      }
+    }
+    e = __reduce_max_sync(0xffffffffu, e);
+    if (lane == 0) s_err[warp] = e;
+    __syncthreads();
+    if (threadIdx.x == 0) *a.err = max(max(s_err[0], s_err[1]), max(s_err[2], s_err[3]));
+  }
+  // ---- fill the ring: S - 1 stages in flight, the pages of the stage after them already read
+  Cursor ld = cu;
+  long long to_load = left;
+  int page[NP], slot[NP];
+  auto next_page = [&]() {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int key = ld.tile * C::kTile + warp * C::kKeys + i * 32 + lane;
+      find_page(a, ld.b, key, to_load > 0 && key < ld.len, page[i], slot[i], err);
+    }
+  };
+  bool dead = false;  // a wait has run out: nothing more is loaded
+  auto load_next = [&](int st) {
+    if (to_load > 0 && !dead) {
+      load_q8_stage<DP>(p, &tmK, &tmV, ld.h / a.row_blocks, page, slot, ring + st * C::kStageBytes,
+                        scales + st * 2 * C::kKeys, bars + st * 8);
+      next_item<C::kTile>(a, heads, ld);
+      --to_load;
+      next_page();
+    }
+    cp_async_commit();
+  };
+  __syncwarp();
+  next_page();
+#pragma unroll 1
+  for (int st = 0; st < S - 1; ++st) load_next(st);
+
+  // columns of this thread: heads 8 x + 2 (lane & 3) + e; rows of a fragment: lane >> 2 and + 8
+  const int r0 = lane >> 2, j = lane & 3;
+  float o[KS][NH][4], m[NH][2], F[NH][2], l[NH][2], qs[NH][2], sl[NH][2];
+  uint32_t qf[KS][NH][2];
+  int qpos = 0, rows = 0, row0 = 0, tile0 = 0, pieces = 0;
+  bool fresh = true;
+  if (p.cluster) {
+    const int rb = cu.h % a.row_blocks;
+    row0 = cu.h / a.row_blocks * a.group + rb * kRows;
+    rows = min(kRows, a.group - rb * kRows);
+  }
+  const float factor = a.cap > 0.f ? a.sm_scale / a.cap : a.sm_scale * kLog2eF, cap_out = a.cap * kLog2eF;
+  int stage = 0;
+  uint32_t parity = 0;
+
+#pragma unroll 1
+  for (; left > 0; --left) {
+    if (fresh) {
+      // a new (sequence, head): its query rows as the B operand, its statistics
+      fresh = false;
+      tile0 = cu.tile;
+      const int h = cu.h / a.row_blocks, rb = cu.h - h * a.row_blocks;
+      row0 = h * a.group + rb * kRows;
+      rows = min(kRows, a.group - rb * kRows);
+#pragma unroll
+      for (int x = 0; x < NH; ++x) {
+        const int r = x * 8 + r0;
+        const int64_t at = cu.b * a.q_sb + (int64_t)(row0 + r) * a.q_sh;
+        float most = 0.f;
+        uint2 raw[KS];
+#pragma unroll
+        for (int u = 0; u < KS; ++u) {
+          // channels 16 u + 4 j .. + 3: the places 2 j, 2 j + 1, 2 j + 8 and 2 j + 9 of the product's sum
+          const int c = u * 16 + j * 4;
+          raw[u] = make_uint2(0, 0);
+          if (r < rows && c < a.c.d) {
+            const uint16_t* src = static_cast<const uint16_t*>(a.q) + at + c;
+            if (p.q4) {
+              raw[u] = *reinterpret_cast<const uint2*>(src);
+            } else {
+              uint16_t t[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) t[e] = c + e < a.c.d ? src[e] : 0;
+              raw[u] = make_uint2(t[0] | (uint32_t)t[1] << 16, t[2] | (uint32_t)t[3] << 16);
+            }
+          }
+        }
+        auto value = [&](uint32_t w, int hi) {
+          const uint16_t b = (uint16_t)(hi ? w >> 16 : w);
+          return p.bf16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
+        };
+#pragma unroll
+        for (int u = 0; u < KS; ++u)
+          most = fmaxf(fmaxf(most, fmaxf(fabsf(value(raw[u].x, 0)), fabsf(value(raw[u].x, 1)))),
+                       fmaxf(fabsf(value(raw[u].y, 0)), fabsf(value(raw[u].y, 1))));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        // the row times 2^(14 - e), e the exponent of its largest channel
+        const int e = max(16, min(254, (int)(__float_as_uint(most) >> 23)));
+        const float up = __uint_as_float((uint32_t)(268 - e) << 23), down = __uint_as_float((uint32_t)(e - 14) << 23);
+#pragma unroll
+        for (int u = 0; u < KS; ++u) {
+          qf[u][x][0] = pack2<__half>(value(raw[u].x, 0) * up, value(raw[u].x, 1) * up);
+          qf[u][x][1] = pack2<__half>(value(raw[u].y, 0) * up, value(raw[u].y, 1) * up);
+        }
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+          qs[x][e2] = __shfl_sync(0xffffffffu, down, (2 * j + e2) * 4) * factor;
+          const int rr = x * 8 + 2 * j + e2;
+          sl[x][e2] = a.slopes && rr < rows ? __ldg(&a.slopes[row0 + rr]) * kLog2eF : 0.f;
+          m[x][e2] = F[x][e2] = -INFINITY;
+          l[x][e2] = 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < KS; ++u) o[u][x][0] = o[u][x][1] = o[u][x][2] = o[u][x][3] = 0.f;
+      }
+      qpos = a.q_pos ? __ldg(&a.q_pos[cu.b]) : cu.len - 1;
+    }
+    // the stage after the ones in flight goes where the previous item was
+    __syncwarp();
+    load_next(stage == 0 ? S - 1 : stage - 1);
+    const int key0 = cu.tile * C::kTile + warp * C::kKeys;
+    uint8_t* const here = ring + stage * C::kStageBytes;
+    const float* const sc = scales + stage * 2 * C::kKeys;
+    if (a.load == kLoadTma) {
+      if (!dead && !__all_sync(0xffffffffu, wait_stage(bars + stage * 8, parity))) {
+        dead = true;
+        err = kDevTimeout;
+        // what is in flight lands (or runs out of time) before the shared memory goes away
+        for (int k = 0; k < (int)(left - to_load); ++k) {
+          const int st = stage + k;
+          wait_stage(bars + (st % S) * 8, parity ^ (st >= S ? 1u : 0u));
+        }
+      }
+      if (VT == SAGE_E4M3 && !dead && key0 < cu.len && key0 + C::kKeys > cu.len) {
+        // slots behind the last token may hold anything, a NaN too: as V rows they become zero (their scores are masked)
+        for (int i = lane; i < (key0 + C::kKeys - cu.len) * (DP / 16); i += 32)
+          *reinterpret_cast<uint4*>(here + C::kTileBytes + (cu.len - key0 + i / (DP / 16)) * DP + i % (DP / 16) * 16) =
+              make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+    }
+    cp_async_wait<S - 1>();
+    __syncwarp();
+    if (key0 < cu.len) {
+      const uint32_t kb = smem_u32(here), vb = kb + C::kTileBytes;
+      // ---- S^T = K Q^T: 16 keys x 8 heads each
+      float s[M][NH][4];
+#pragma unroll
+      for (int g = 0; g < M; ++g)
+#pragma unroll
+        for (int x = 0; x < NH; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[g][x][e] = 0.f;
+      {
+        const int kr = lane & 15, hi = lane >> 4;  // keys 0-15 at unit c, then at unit c + 1
+#pragma unroll
+        for (int u = 0; u < KS; u += 2)
+#pragma unroll
+          for (int g = 0; g < M; ++g) {
+            uint32_t b[4], f[4];
+            ldsm4(kb + g * 16 * DP + unit_at<DP>(kr, u + hi), b);
+            widen<KT, 0, 1, 2, 3>(b[0], f[0], f[2]);
+            widen<KT, 0, 1, 2, 3>(b[1], f[1], f[3]);
+#pragma unroll
+            for (int x = 0; x < NH; ++x) mma16816<__half>(s[g][x], f, qf[u][x][0], qf[u][x][1]);
+            widen<KT, 0, 1, 2, 3>(b[2], f[0], f[2]);
+            widen<KT, 0, 1, 2, 3>(b[3], f[1], f[3]);
+#pragma unroll
+            for (int x = 0; x < NH; ++x) mma16816<__half>(s[g][x], f, qf[u + 1][x][0], qf[u + 1][x][1]);
+          }
+      }
+      // ---- scores in base 2; s[g][x][2 b + e]: key 16 g + 8 b + r0, head 8 x + 2 j + e
+      float lv[M][2];  // log2 of V's scales
+      float tm[NH][2], um[NH][2];
+#pragma unroll
+      for (int x = 0; x < NH; ++x) tm[x][0] = tm[x][1] = um[x][0] = um[x][1] = -INFINITY;
+      const bool ragged = key0 + C::kKeys > cu.len;
+#pragma unroll
+      for (int g = 0; g < M; ++g)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int k = g * 16 + b * 8 + r0;
+          const float ks = sc[k];
+          lv[g][b] = lg2_approx(sc[C::kKeys + k]);
+          const float dist = a.slopes ? fabsf((float)((long long)qpos - (key0 + k))) : 0.f;
+#pragma unroll
+          for (int x = 0; x < NH; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float t = s[g][x][2 * b + e] * (qs[x][e] * ks);
+              if (a.cap > 0.f) t = tanhf(t) * cap_out;
+              if (a.slopes) t = fmaf(-sl[x][e], dist, t);
+              if (ragged && key0 + k >= cu.len) t = -INFINITY;
+              s[g][x][2 * b + e] = t;
+              tm[x][e] = fmaxf(tm[x][e], t);
+              um[x][e] = fmaxf(um[x][e], t + lv[g][b]);
+            }
+        }
+      // ---- frames of the sum (m) and of the weights (F, kHead below the largest): the eight lanes of a head agree. They
+      // are kept unless a maximum grew by more than 8, so sums and O are rescaled rarely
+      bool grows = false;
+#pragma unroll
+      for (int x = 0; x < NH; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          grows |= tm[x][e] > m[x][e] + 8.0f || um[x][e] > F[x][e] + (8.0f + kHead);
+      if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+        for (int x = 0; x < NH; ++x)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = tm[x][e], v = um[x][e];
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) {
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, w));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, w));
+            }
+            v -= kHead;
+            if (t > m[x][e]) {
+              l[x][e] *= ex2_approx(m[x][e] - t);
+              m[x][e] = t;
+            }
+            if (v > F[x][e]) {
+              const float f = ex2_approx(F[x][e] - v);
+              F[x][e] = v;
+#pragma unroll
+              for (int u = 0; u < KS; ++u) {
+                o[u][x][e] *= f;
+                o[u][x][2 + e] *= f;
+              }
+            }
+          }
+      }
+      // ---- weights: their sum in 32 bits; with V's scale, rounded once, keys and heads exchanged, as the B operand
+      uint32_t pf[M][NH][2];
+#pragma unroll
+      for (int x = 0; x < NH; ++x) {
+        const float m0 = m[x][0] == -INFINITY ? 0.f : m[x][0], m1 = m[x][1] == -INFINITY ? 0.f : m[x][1];
+        const float f0 = F[x][0] == -INFINITY ? 0.f : F[x][0], f1 = F[x][1] == -INFINITY ? 0.f : F[x][1];
+#pragma unroll
+        for (int g = 0; g < M; ++g)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float t0 = s[g][x][2 * b], t1 = s[g][x][2 * b + 1];
+            l[x][0] += ex2_approx(t0 - m0);
+            l[x][1] += ex2_approx(t1 - m1);
+            pf[g][x][b] = transpose8x8(pack2<__half>(ex2_approx(t0 + lv[g][b] - f0), ex2_approx(t1 + lv[g][b] - f1)));
+          }
+      }
+      // ---- O^T += V^T P^T: 16 channels x 8 heads each, 16 keys at a time. Row r0 of a fragment is channel 2 r0 of its
+      // unit, row r0 + 8 channel 2 r0 + 1: the two channels of a register that the transposed read gives
+      {
+        const int kr = lane & 15, hi = lane >> 4;
+#pragma unroll
+        for (int g = 0; g < M; ++g)
+#pragma unroll
+          for (int u = 0; u < KS; u += 2) {
+            uint32_t b[4], f[4];
+            ldsm4t(vb + g * 16 * DP + unit_at<DP>(kr, u + hi), b);
+            widen<VT, 0, 2, 1, 3>(b[0], f[0], f[1]);
+            widen<VT, 0, 2, 1, 3>(b[1], f[2], f[3]);
+#pragma unroll
+            for (int x = 0; x < NH; ++x) mma16816<__half>(o[u][x], f, pf[g][x][0], pf[g][x][1]);
+            widen<VT, 0, 2, 1, 3>(b[2], f[0], f[1]);
+            widen<VT, 0, 2, 1, 3>(b[3], f[2], f[3]);
+#pragma unroll
+            for (int x = 0; x < NH; ++x) mma16816<__half>(o[u + 1][x], f, pf[g][x][0], pf[g][x][1]);
+          }
+      }
+    }
+    if (stage + 1 == S) {
+      stage = 0;
+      parity ^= 1;
+    } else {
+      ++stage;
+    }
+    if (!p.cluster && (cu.tile + 1 == cu.tiles || left == 1)) {
+      // ---- merge the warps: sums of a head over its eight lanes, then over the warps
+#pragma unroll
+      for (int x = 0; x < NH; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], w);
+          if (r0 == 0) ml[warp * kRows + x * 8 + 2 * j + e] = make_float4(m[x][e], l[x][e], F[x][e], 0.f);
+        }
+      __syncthreads();
+      float Mx[NH][2], L[NH][2], g[NH][2];  // of all warps; from F's frame to m's
+#pragma unroll
+      for (int x = 0; x < NH; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4* at = ml + x * 8 + 2 * j + e;
+          float mm = -INFINITY, ff = -INFINITY, ll = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            mm = fmaxf(mm, at[w * kRows].x);
+            ff = fmaxf(ff, at[w * kRows].z);
+          }
+          const float mu = mm == -INFINITY ? 0.f : mm, fu = ff == -INFINITY ? 0.f : ff;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) ll += at[w * kRows].y * ex2_approx(at[w * kRows].x - mu);
+          const float f = ex2_approx(F[x][e] - fu);
+#pragma unroll
+          for (int u = 0; u < KS; ++u) {
+            o[u][x][e] *= f;
+            o[u][x][2 + e] *= f;
+          }
+          Mx[x][e] = mm;
+          L[x][e] = ll;
+          g[x][e] = ex2_approx(ff - mu);
+        }
+      // pairs (0, 2) and (1, 3), then (0, 1), eight heads at a time
+#pragma unroll
+      for (int x = 0; x < NH; ++x)
+#pragma unroll
+        for (int step = 2; step >= 1; step >>= 1) {
+          if (warp >= step && warp < 2 * step) {
+#pragma unroll
+            for (int u = 0; u < KS; ++u)
+              merge[((warp - step) * KS + u) * 32 + lane] = make_float4(o[u][x][0], o[u][x][1], o[u][x][2], o[u][x][3]);
+          }
+          __syncthreads();
+          if (warp < step) {
+#pragma unroll
+            for (int u = 0; u < KS; ++u) {
+              const float4 y = merge[(warp * KS + u) * 32 + lane];
+              o[u][x][0] += y.x; o[u][x][1] += y.y; o[u][x][2] += y.z; o[u][x][3] += y.w;
+            }
+          }
+          __syncthreads();
+        }
+      if (warp == 0) {
+        // the whole (sequence, head) in this range: the result; a part of it: to the workspace
+        const bool whole = tile0 == 0 && cu.tile + 1 == cu.tiles;
+        const int64_t at = ((int64_t)me * 2 + (pieces > 0)) * kRows;
+#pragma unroll
+        for (int x = 0; x < NH; ++x)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = x * 8 + 2 * j + e;
+            if (r >= rows) continue;
+            const float f = whole ? (L[x][e] != 0.f ? g[x][e] / L[x][e] : 0.f) : g[x][e];
+#pragma unroll
+            for (int u = 0; u < KS; ++u) {
+              const int c = u * 16 + 2 * r0;
+              const float y0 = o[u][x][e] * f, y1 = o[u][x][2 + e] * f;
+              if (whole) {
+                const int64_t to = cu.b * a.o_sb + (int64_t)(row0 + r) * a.o_sh + c;
+                if (c < a.c.d) store_out(p, to, y0);
+                if (c + 1 < a.c.d) store_out(p, to + 1, y1);
+              } else {
+                *reinterpret_cast<float2*>(a.part_o + (at + r) * DP + c) = make_float2(y0, y1);
+              }
+            }
+            if (r0 == 0) {
+              if (!whole) *reinterpret_cast<float2*>(a.part_ml + (at + r) * 2) = make_float2(Mx[x][e], L[x][e]);
+              else if (a.lse)
+                a.lse[(int64_t)cu.b * a.hq + row0 + r] = L[x][e] != 0.f ? (Mx[x][e] + log2f(L[x][e])) * kLn2F : -INFINITY;
+            }
+          }
+      }
+      ++pieces;
+      fresh = true;
+    }
+    next_item<C::kTile>(a, heads, cu);
+  }
+  if (p.cluster) {
+    // every warp's accumulator into its own ring, its statistics beside; then each thread of the
+    // cluster sums one group of four channels of a row over all warps of all ranks, in their order
+    const int rank = me % kRanks;
+    cp_async_wait<0>();
+    __syncwarp();
+    float* const mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int x = 0; x < NH; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = x * 8 + 2 * j + e;
+        if (!fresh) {
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], w);
+          const float f = ex2_approx(F[x][e] - (m[x][e] == -INFINITY ? 0.f : m[x][e]));
+          if (r < rows) {
+#pragma unroll
+            for (int u = 0; u < KS; ++u)
+              *reinterpret_cast<float2*>(mine + r * DP + u * 16 + 2 * r0) = make_float2(o[u][x][e] * f, o[u][x][2 + e] * f);
+          }
+        }
+        if (r0 == 0) ml[warp * kRows + r] = fresh ? make_float4(-INFINITY, 0.f, 0.f, 0.f) : make_float4(m[x][e], l[x][e], 0.f, 0.f);
+      }
+    if (dead && a.err) record_error(a.err, kDevTimeout);
+    cluster_sync();
+    const int cell = rank * kWarps * 32 + threadIdx.x, r = cell / (DP / 4), c = (cell - r * (DP / 4)) * 4;
+    if (r < rows) {
+      const uint32_t ml_at = smem_u32(ml + r), o_at = smem_u32(sm) + (r * DP + c) * 4;
+      float2 st[kRanks * kWarps];
+#pragma unroll
+      for (int q = 0; q < kRanks * kWarps; ++q) st[q] = ld_rank2(of_rank(ml_at + (q % kWarps) * kRows * 16, q / kWarps));
+      float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+      for (int q = 0; q < kRanks * kWarps; ++q) mm = fmaxf(mm, st[q].x);
+      const float u = mm == -INFINITY ? 0.f : mm;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < kRanks * kWarps; ++q) {
+        const float w = ex2_approx(st[q].x - u);
+        ll = fmaf(st[q].y, w, ll);
+        if (st[q].y != 0.f) {  // (a warp without keys wrote no accumulator)
+          const float4 y = ld_rank4(of_rank(o_at + (q % kWarps) * C::kWarpBytes, q / kWarps));
+          acc.x = fmaf(w, y.x, acc.x); acc.y = fmaf(w, y.y, acc.y);
+          acc.z = fmaf(w, y.z, acc.z); acc.w = fmaf(w, y.w, acc.w);
+        }
+      }
+      const float inv = ll != 0.f ? 1.0f / ll : 0.f;
+      const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+      const int64_t to = (int64_t)blockIdx.y * a.o_sb + (int64_t)(row0 + r) * a.o_sh + c;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < a.c.d) store_out(p, to + e, y[e]);
+      if (c == 0 && a.lse) a.lse[(int64_t)blockIdx.y * a.hq + row0 + r] = ll != 0.f ? (mm + log2f(ll)) * kLn2F : -INFINITY;
+    }
+    cluster_sync();  // no CTA's shared memory goes away while it is read
+    return;
+  }
+  cp_async_wait<0>();
+  // this CTA's error, collected by the join kernel (no word to clear before the call)
+  const int we = __reduce_max_sync(0xffffffffu, err);
+  if (lane == 0) s_err[warp] = we;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int e = 0;
+    for (int w = 0; w < kWarps; ++w) e = max(e, s_err[w]);
+    a.cta_err[me] = e;
+  }
+}
+
+template <int KT, int VT, int DP, int NH>
+cudaError_t launch_q8_t(const Q8Args& p, const CUtensorMap* maps, cudaStream_t st) {
+  using C = Q8Cfg<DP>;
+  const DecodeArgs& a = p.a;
+  static std::atomic<int> limits[64];
+  cudaError_t e = raise_smem_limit(q8_decode_kernel<KT, VT, DP, NH>, C::kSmem, limits);
+  if (e != cudaSuccess) return e;
+  const int heads = a.c.hkv * a.row_blocks;
+  if (!p.cluster) {
+    e = launch_pdl(q8_decode_kernel<KT, VT, DP, NH>, dim3(kCtas), dim3(kWarps * 32), C::kSmem, st, maps[0], maps[1], p);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(heads * a.slices, a.c.batch);
+    return p.bf16 ? launch_pdl(join_kernel<__nv_bfloat16, DP, C::kTile>, grid, dim3(kJoinThreads), 0, st, a)
+                  : launch_pdl(join_kernel<__half, DP, C::kTile>, grid, dim3(kJoinThreads), 0, st, a);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(heads * kRanks, a.c.batch);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kRanks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, q8_decode_kernel<KT, VT, DP, NH>, maps[0], maps[1], p);
+}
+
+template <int DP>
+cudaError_t launch_q8(const Q8Args& p, const CUtensorMap* maps, cudaStream_t st) {
+  const bool wide = p.a.group > 8;
+  auto go = [&](auto kt, auto vt) {
+    constexpr int K = decltype(kt)::value, V = decltype(vt)::value;
+    return wide ? launch_q8_t<K, V, DP, 2>(p, maps, st) : launch_q8_t<K, V, DP, 1>(p, maps, st);
+  };
+  using S8 = std::integral_constant<int, SAGE_S8>;
+  using E4 = std::integral_constant<int, SAGE_E4M3>;
+  if (p.k_type == SAGE_S8) return p.v_type == SAGE_S8 ? go(S8{}, S8{}) : go(S8{}, E4{});
+  return p.v_type == SAGE_S8 ? go(E4{}, S8{}) : go(E4{}, E4{});
+}
+
+}  // namespace
+}  // namespace sage
