@@ -10,7 +10,7 @@ namespace sage {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kCtas = 304;                 // two resident CTAs per SM
+constexpr int kCtas = 304;                 // ranges of the line: two resident CTAs per SM
 constexpr int kRows = 16;                  // query heads per row block
 constexpr int kMinTiles = 2;               // tiles a CTA takes at least
 constexpr int kRanks = 8;                  // CTAs of a cluster
@@ -81,9 +81,10 @@ __device__ __forceinline__ Scan scan_items(const DecodeArgs& a, int heads, int b
 }
 
 // CTAs that share `total` items, and the first item of CTA i.
+template <int CTAS>
 __device__ __forceinline__ int ctas_of(long long total) {
   const long long g = (total + kMinTiles - 1) / kMinTiles;
-  return (int)(g < kCtas ? g : kCtas);
+  return (int)(g < CTAS ? g : CTAS);
 }
 __device__ __forceinline__ long long first_item(long long total, int ctas, int i) {
   return total * i / ctas;
@@ -212,10 +213,10 @@ __device__ __forceinline__ float4 ld_rank4(uint32_t addr) {
 // the order of the ranges; sequences that hold nothing get 0 and -inf. CTA (0, 0) also collects the status.
 constexpr int kJoinThreads = 256;
 
-template <typename T, int DP, int TILE>
+template <typename T, int DP, int TILE, int CTAS>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) {
-  __shared__ float s_w[kCtas][kRows];       // weight of each range's piece
-  __shared__ int s_at[kCtas];               // and where it lies
+  __shared__ float s_w[CTAS][kRows];       // weight of each range's piece
+  __shared__ int s_at[CTAS];               // and where it lies
   __shared__ float s_m[kRows], s_l[kRows];
   __shared__ __align__(16) float s_acc[kJoinThreads * 4];
   __shared__ long long s_before[kJoinThreads / 32], s_all[kJoinThreads / 32];
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
   pdl_trigger();
   if (blockIdx.x == 0 && b == 0) {
     int e = 0;
-    for (int i = tid; i < kCtas; i += kJoinThreads) e = max(e, a.cta_err[i]);
+    for (int i = tid; i < CTAS; i += kJoinThreads) e = max(e, a.cta_err[i]);
     e = __reduce_max_sync(0xffffffffu, e);
     if (lane == 0) s_all[warp] = e;
     __syncthreads();
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
     return;
   }
   const long long t0 = before + (long long)hb * tiles_of<TILE>(len), t1 = t0 + tiles_of<TILE>(len);
-  const int ctas = ctas_of(all);
+  const int ctas = ctas_of<CTAS>(all);
   // the ranges that hold t0 and t1 - 1: range i is [all i / ctas, all (i + 1) / ctas)
   auto range_of = [&](long long t) { return (int)(((t + 1) * ctas - 1) / all); };
   const int c0 = range_of(t0), c1 = range_of(t1 - 1);

@@ -56,7 +56,9 @@ bool softcap_ok(float softcap, float sm_scale, int head_dim);
 bool make_map4(CUtensorMap* m, bool bf16, const void* base, uint64_t inner, uint64_t rows, uint64_t heads,
                uint64_t batch, uint64_t row_bytes, uint64_t head_bytes, uint64_t batch_bytes,
                uint32_t box_inner, uint32_t box_rows);
-// The same of 8-bit rows, boxes of 64 or 128 bytes by rows, swizzled over as many bytes.
+// The same of 8-bit rows, boxes of 64 or 128 bytes by rows, swizzled over as many bytes. Where the rows of a box do not follow
+// one another the L2 fetches no more than they are: 256 bytes at a time read 754 MB instead of 524 for token rows of 8 heads
+// of 128 bytes, of which a box takes one.
 bool make_map4_bytes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t heads, uint64_t batch,
                      uint64_t row_bytes, uint64_t head_bytes, uint64_t batch_bytes, uint32_t box_inner, uint32_t box_rows);
 

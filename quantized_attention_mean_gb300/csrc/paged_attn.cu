@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     Scan sc = scan_items<C::kTile>(a, heads, 0, bad);
     long long total = sc.all;
     for (int b0 = blockDim.x; b0 < a.c.batch; b0 += blockDim.x) total += scan_items<C::kTile>(a, heads, b0, bad).all;
-    const int ctas = total > 0 ? ctas_of(total) : 0;
+    const int ctas = total > 0 ? ctas_of<kCtas>(total) : 0;
     long long i0 = 0;
     if (me < ctas) {
       i0 = first_item(total, ctas, me);
@@ -734,7 +734,7 @@ cudaError_t launch_decode_t(const DecodeArgs& a, const CUtensorMap* maps, cudaSt
     if (e != cudaSuccess) return e;
     e = launch_pdl(decode_kernel<T, DP, false>, dim3(kCtas), dim3(kWarps * 32), C::kSmem, st, maps[0], maps[1], a);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(join_kernel<T, DP, C::kTile>, dim3(heads * a.slices, a.c.batch), dim3(kJoinThreads), 0, st, a);
+    e = launch_pdl(join_kernel<T, DP, C::kTile, kCtas>, dim3(heads * a.slices, a.c.batch), dim3(kJoinThreads), 0, st, a);
   }
   if (e != cudaSuccess || !a.scores || a.max_len == 0) return e;
   return launch_pdl(mass_kernel, dim3((unsigned)(((int64_t)a.max_len + 256 * kMassKeys - 1) / (256 * kMassKeys)), a.c.hkv, a.c.batch), dim3(256), 0,

@@ -12,7 +12,8 @@ struct Q8Layout {
   size_t err, part_o, part_ml, total;
 };
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-int tile_of(int d) { return d <= 64 ? Q8Cfg<64>::kTile : Q8Cfg<128>::kTile; }
+int tile_of(int d) { return d <= 64 ? Q8Cfg<64, 1>::kTile : Q8Cfg<128, 1>::kTile; }
+constexpr int kMostRanges = Q8Cfg<128, 1>::kRanges;
 // Few heads with short sequences: one launch of clusters whose CTAs all run at once.
 bool q8_clustered(int batch, int hkv, int row_blocks, int64_t max_len, int d) {
   return (int64_t)hkv * row_blocks * batch * kRanks <= kCtas && max_len <= 8 * kRanks * tile_of(d);
@@ -23,9 +24,9 @@ bool q8_layout(int batch, int hq, int hkv, int64_t max_len, int d, Q8Layout* L) 
   // status word; the line's ranges: their errors and their pieces
   const bool line = !q8_clustered(batch, hkv, (hq / hkv + kRows - 1) / kRows, max_len, d);
   L->err = SAGE_STATUS_BYTES;
-  L->part_o = L->err + (line ? up256(4 * kCtas) : 0);
-  L->part_ml = L->part_o + (line ? up256((size_t)kCtas * 2 * kRows * dp * 4) : 0);
-  L->total = L->part_ml + (line ? up256((size_t)kCtas * 2 * kRows * 2 * 4) : 0);
+  L->part_o = L->err + (line ? up256(4 * kMostRanges) : 0);
+  L->part_ml = L->part_o + (line ? up256((size_t)kMostRanges * 2 * kRows * dp * 4) : 0);
+  L->total = L->part_ml + (line ? up256((size_t)kMostRanges * 2 * kRows * 2 * 4) : 0);
   return true;
 }
 

@@ -39,16 +39,20 @@ struct Q8Args {
 cudaError_t launch_q8_decode_64(const Q8Args& p, const CUtensorMap* maps, cudaStream_t st);
 cudaError_t launch_q8_decode_128(const Q8Args& p, const CUtensorMap* maps, cudaStream_t st);
 
-template <int DP>
+// NH: blocks of eight query heads, the columns of the products. Up to eight heads leave registers for three CTAs per SM
+// with two stages each, more take two CTAs with three stages.
+template <int DP, int NH>
 struct Q8Cfg {
-  static constexpr int kStages = 3;
+  static constexpr int kPerSm = NH == 1 ? 3 : 2;
+  static constexpr int kRanges = 152 * kPerSm;                // of the line
+  static constexpr int kStages = NH == 1 ? 2 : 3;
   static constexpr int kKeys = DP == 128 ? 32 : 64;           // keys per warp and tile (8 KB of K and V)
   static constexpr int kTile = 4 * kKeys;                     // keys per tile
   static constexpr int kTileBytes = kKeys * DP;               // K or V of one warp's tile
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes;
-  static constexpr int kOffMerge = 4 * kWarpBytes;            // two warps' accumulators of eight heads
-  static constexpr int kOffScale = kOffMerge + 2 * (DP / 16) * 32 * 16;
+  static constexpr int kOffMerge = 4 * kWarpBytes;            // one warp's accumulators of eight heads
+  static constexpr int kOffScale = kOffMerge + (DP / 16) * 32 * 16;
   static constexpr int kOffMl = kOffScale + 4 * kStages * 2 * kKeys * 4;
   static constexpr int kOffBar = kOffMl + 4 * 16 * 4 * 4;
   static constexpr int kSmem = kOffBar + 4 * kStages * 8;
@@ -98,12 +102,10 @@ __device__ __forceinline__ int unit_at(int r, int c) {
 
 // A warp's keys of one item into a stage: K, V and the keys' scales. Tokens that are not there and channels past d become
 // zero. page, slot: of keys lane, lane + 32, ...
-template <int DP>
+template <typename C, int DP, int N>
 __device__ __forceinline__ void load_q8_stage(const Q8Args& p, const CUtensorMap* tmK, const CUtensorMap* tmV, int h,
-                                              const int (&page)[Q8Cfg<DP>::kKeys / 32], const int (&slot)[Q8Cfg<DP>::kKeys / 32],
-                                              uint8_t* stage, float* scale, uint32_t bar) {
-  using C = Q8Cfg<DP>;
-  constexpr int N = C::kKeys / 32;
+                                              const int (&page)[N], const int (&slot)[N], uint8_t* stage, float* scale,
+                                              uint32_t bar) {
   const DecodeArgs& a = p.a;
   const int lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(stage);
@@ -180,13 +182,13 @@ __device__ __forceinline__ void store_out(const Q8Args& p, int64_t at, float x) 
   else static_cast<__half*>(p.a.o)[at] = __float2half_rn(x);
 }
 
-// NH: blocks of eight query heads, the columns of the products.
 template <int KT, int VT, int DP, int NH>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+__global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
     q8_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Q8Args p) {
-  using C = Q8Cfg<DP>;
+  using C = Q8Cfg<DP, NH>;
   constexpr int S = C::kStages, KS = DP / 16, M = C::kKeys / 16, NP = C::kKeys / 32;
   constexpr float kHead = 7.0f;  // weights are held at up to 2^(7 + 8), so that the smallest keep their bits in fp16
+  constexpr float kLeastLog = -110.0f;  // smaller scales do not lower the frame of the weights, which stays finite
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ int s_err[kWarps];
   const DecodeArgs& a = p.a;
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     Scan sc = scan_items<C::kTile>(a, heads, 0, bad);
     long long total = sc.all;
     for (int b0 = blockDim.x; b0 < a.c.batch; b0 += blockDim.x) total += scan_items<C::kTile>(a, heads, b0, bad).all;
-    const int ctas = total > 0 ? ctas_of(total) : 0;
+    const int ctas = total > 0 ? ctas_of<C::kRanges>(total) : 0;
     long long i0 = 0;
     if (me < ctas) {
       i0 = first_item(total, ctas, me);
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   bool dead = false;  // a wait has run out: nothing more is loaded
   auto load_next = [&](int st) {
     if (to_load > 0 && !dead) {
-      load_q8_stage<DP>(p, &tmK, &tmV, ld.h / a.row_blocks, page, slot, ring + st * C::kStageBytes,
+      load_q8_stage<C, DP>(p, &tmK, &tmV, ld.h / a.row_blocks, page, slot, ring + st * C::kStageBytes,
                         scales + st * 2 * C::kKeys, bars + st * 8);
       next_item<C::kTile>(a, heads, ld);
       --to_load;
@@ -429,32 +431,79 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           }
       }
       // ---- scores in base 2; s[g][x][2 b + e]: key 16 g + 8 b + r0, head 8 x + 2 j + e
-      float lv[M][2];  // log2 of V's scales
-      float tm[NH][2], um[NH][2];
-#pragma unroll
-      for (int x = 0; x < NH; ++x) tm[x][0] = tm[x][1] = um[x][0] = um[x][1] = -INFINITY;
-      const bool ragged = key0 + C::kKeys > cu.len;
+      float sv[M][2];  // V's scales
+      float most = 0.f, least = INFINITY;
 #pragma unroll
       for (int g = 0; g < M; ++g)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const int k = g * 16 + b * 8 + r0;
-          const float ks = sc[k];
-          lv[g][b] = lg2_approx(sc[C::kKeys + k]);
-          const float dist = a.slopes ? fabsf((float)((long long)qpos - (key0 + k))) : 0.f;
+          const float ks = sc[g * 16 + b * 8 + r0];
+          sv[g][b] = sc[C::kKeys + g * 16 + b * 8 + r0];
+          most = fmaxf(most, sv[g][b]);
+          least = fminf(least, sv[g][b]);
 #pragma unroll
           for (int x = 0; x < NH; ++x)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float t = s[g][x][2 * b + e] * (qs[x][e] * ks);
-              if (a.cap > 0.f) t = tanhf(t) * cap_out;
-              if (a.slopes) t = fmaf(-sl[x][e], dist, t);
-              if (ragged && key0 + k >= cu.len) t = -INFINITY;
-              s[g][x][2 * b + e] = t;
-              tm[x][e] = fmaxf(tm[x][e], t);
-              um[x][e] = fmaxf(um[x][e], t + lv[g][b]);
-            }
+            for (int e = 0; e < 2; ++e) s[g][x][2 * b + e] *= qs[x][e] * ks;
         }
+      if (a.cap > 0.f) {
+#pragma unroll
+        for (int g = 0; g < M; ++g)
+#pragma unroll
+          for (int x = 0; x < NH; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[g][x][e] = tanhf(s[g][x][e]) * cap_out;
+      }
+      if (a.slopes) {
+        const float d0 = (float)((long long)qpos - (key0 + r0));  // exact below 2^24
+#pragma unroll
+        for (int g = 0; g < M; ++g)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float dist = fabsf(d0 - (float)(g * 16 + b * 8));
+#pragma unroll
+            for (int x = 0; x < NH; ++x)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) s[g][x][2 * b + e] = fmaf(-sl[x][e], dist, s[g][x][2 * b + e]);
+          }
+      }
+      if (key0 + C::kKeys > cu.len) {
+#pragma unroll
+        for (int g = 0; g < M; ++g)
+#pragma unroll
+          for (int x = 0; x < NH; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key0 + g * 16 + (e >> 1) * 8 + r0 >= cu.len) s[g][x][e] = -INFINITY;
+      }
+      // largest score t, and largest t + log2 s_v: an upper bound by the largest scale, which where a lane's scales lie
+      // within 2^8 is at most so much too large, otherwise exactly
+      const float lv = fmaxf(lg2_approx(most), kLeastLog);
+      float tm[NH][2], um[NH][2];
+#pragma unroll
+      for (int x = 0; x < NH; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          tm[x][e] = fmaxf(s[0][x][e], s[0][x][2 + e]);
+#pragma unroll
+          for (int g = 1; g < M; ++g) tm[x][e] = max3(tm[x][e], s[g][x][e], s[g][x][2 + e]);
+          um[x][e] = tm[x][e] + lv;
+        }
+      if (__any_sync(0xffffffffu, least * 256.0f < most)) {
+#pragma unroll
+        for (int x = 0; x < NH; ++x) um[x][0] = um[x][1] = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < M; ++g)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float l2 = fmaxf(lg2_approx(sv[g][b]), kLeastLog);
+#pragma unroll
+            for (int x = 0; x < NH; ++x) {
+              um[x][0] = fmaxf(um[x][0], s[g][x][2 * b] + l2);
+              um[x][1] = fmaxf(um[x][1], s[g][x][2 * b + 1] + l2);
+            }
+          }
+      }
       // ---- frames of the sum (m) and of the weights (F, kHead below the largest): the eight lanes of a head agree. They
       // are kept unless a maximum grew by more than 8, so sums and O are rescaled rarely
       bool grows = false;
@@ -490,20 +539,23 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
             }
           }
       }
-      // ---- weights: their sum in 32 bits; with V's scale, rounded once, keys and heads exchanged, as the B operand
+      // ---- weights p = 2^(t - m): their sum in 32 bits; as p s_v 2^(m - F) rounded once, keys and heads exchanged, the B
+      // operand. (The factor is kept where its product with the largest scale is finite: it passes 2^100 only where all
+      // of the tile's p are below 2^-85)
       uint32_t pf[M][NH][2];
 #pragma unroll
       for (int x = 0; x < NH; ++x) {
         const float m0 = m[x][0] == -INFINITY ? 0.f : m[x][0], m1 = m[x][1] == -INFINITY ? 0.f : m[x][1];
-        const float f0 = F[x][0] == -INFINITY ? 0.f : F[x][0], f1 = F[x][1] == -INFINITY ? 0.f : F[x][1];
+        const float top = fminf(100.0f - lv, 126.0f);
+        const float g0 = ex2_approx(fminf(m0 - F[x][0], top)), g1 = ex2_approx(fminf(m1 - F[x][1], top));
 #pragma unroll
         for (int g = 0; g < M; ++g)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const float t0 = s[g][x][2 * b], t1 = s[g][x][2 * b + 1];
-            l[x][0] += ex2_approx(t0 - m0);
-            l[x][1] += ex2_approx(t1 - m1);
-            pf[g][x][b] = transpose8x8(pack2<__half>(ex2_approx(t0 + lv[g][b] - f0), ex2_approx(t1 + lv[g][b] - f1)));
+            const float p0 = ex2_approx(s[g][x][2 * b] - m0), p1 = ex2_approx(s[g][x][2 * b + 1] - m1);
+            l[x][0] += p0;
+            l[x][1] += p1;
+            pf[g][x][b] = transpose8x8(pack2<__half>(p0 * (sv[g][b] * g0), p1 * (sv[g][b] * g1)));
           }
       }
       // ---- O^T += V^T P^T: 16 channels x 8 heads each, 16 keys at a time. Row r0 of a fragment is channel 2 r0 of its
@@ -569,21 +621,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           L[x][e] = ll;
           g[x][e] = ex2_approx(ff - mu);
         }
-      // pairs (0, 2) and (1, 3), then (0, 1), eight heads at a time
+      // added to warp 0's in their order, eight heads at a time
 #pragma unroll
       for (int x = 0; x < NH; ++x)
+#pragma unroll 1
+        for (int w = 1; w < kWarps; ++w) {
+          if (warp == w) {
 #pragma unroll
-        for (int step = 2; step >= 1; step >>= 1) {
-          if (warp >= step && warp < 2 * step) {
-#pragma unroll
-            for (int u = 0; u < KS; ++u)
-              merge[((warp - step) * KS + u) * 32 + lane] = make_float4(o[u][x][0], o[u][x][1], o[u][x][2], o[u][x][3]);
+            for (int u = 0; u < KS; ++u) merge[u * 32 + lane] = make_float4(o[u][x][0], o[u][x][1], o[u][x][2], o[u][x][3]);
           }
           __syncthreads();
-          if (warp < step) {
+          if (warp == 0) {
 #pragma unroll
             for (int u = 0; u < KS; ++u) {
-              const float4 y = merge[(warp * KS + u) * 32 + lane];
+              const float4 y = merge[u * 32 + lane];
               o[u][x][0] += y.x; o[u][x][1] += y.y; o[u][x][2] += y.z; o[u][x][3] += y.w;
             }
           }
@@ -696,18 +747,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 
 template <int KT, int VT, int DP, int NH>
 cudaError_t launch_q8_t(const Q8Args& p, const CUtensorMap* maps, cudaStream_t st) {
-  using C = Q8Cfg<DP>;
+  using C = Q8Cfg<DP, NH>;
   const DecodeArgs& a = p.a;
   static std::atomic<int> limits[64];
   cudaError_t e = raise_smem_limit(q8_decode_kernel<KT, VT, DP, NH>, C::kSmem, limits);
   if (e != cudaSuccess) return e;
   const int heads = a.c.hkv * a.row_blocks;
   if (!p.cluster) {
-    e = launch_pdl(q8_decode_kernel<KT, VT, DP, NH>, dim3(kCtas), dim3(kWarps * 32), C::kSmem, st, maps[0], maps[1], p);
+    e = launch_pdl(q8_decode_kernel<KT, VT, DP, NH>, dim3(C::kRanges), dim3(kWarps * 32), C::kSmem, st, maps[0], maps[1], p);
     if (e != cudaSuccess) return e;
     const dim3 grid(heads * a.slices, a.c.batch);
-    return p.bf16 ? launch_pdl(join_kernel<__nv_bfloat16, DP, C::kTile>, grid, dim3(kJoinThreads), 0, st, a)
-                  : launch_pdl(join_kernel<__half, DP, C::kTile>, grid, dim3(kJoinThreads), 0, st, a);
+    return p.bf16 ? launch_pdl(join_kernel<__nv_bfloat16, DP, C::kTile, C::kRanges>, grid, dim3(kJoinThreads), 0, st, a)
+                  : launch_pdl(join_kernel<__half, DP, C::kTile, C::kRanges>, grid, dim3(kJoinThreads), 0, st, a);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(heads * kRanks, a.c.batch);
