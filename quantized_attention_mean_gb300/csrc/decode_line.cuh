@@ -31,29 +31,31 @@ struct DecodeArgs {
   int page_shift;           // log2 of page_size, or -1
   int mass4;                // four slots of the mass plane lie in one page and in aligned 16 bytes
   int slices;               // CTAs of the join per (row block of a head, sequence)
+  int tile_shift;           // log2 of a tile's keys
+  int side;                 // key/value heads that share an item of the line
+  int part_rows;            // rows of a piece
   // workspace
   int* err;                 // status word, or null (no workspace: the clusters' form without mass)
   int* cta_err;             // [kCtas]
-  float* part_o;            // [kCtas][2][kRows][dp]
-  float* part_ml;           // [kCtas][2][kRows][2]
+  float* part_o;            // [ranges][2][side][part_rows][dp]
+  float* part_ml;           // [ranges][2][side][part_rows][2]
   float* lse2;              // [batch, hq], base 2 (with mass)
   float* scores;            // [batch, hq, score_pitch], base 2 (with mass) or null
   int64_t score_pitch;
 };
 
-// Tiles of a sequence of n tokens.
-template <int TILE>
-__device__ __forceinline__ int tiles_of(int n) {
-  return (n + TILE - 1) / TILE;
+// Tiles of 2^shift keys of a sequence of n tokens.
+__device__ __forceinline__ int tiles_of(int n, int shift) {
+  return (n + (1 << shift) - 1) >> shift;
 }
+__host__ __device__ constexpr int log2_of(int x) { return x <= 1 ? 0 : 1 + log2_of(x / 2); }
 
 // The items (sequence, head, tile) of sequences [b0, b0 + blockDim): this thread's count, the sum before it and the
 // sum of all. Lengths that are out of range count as 0 and set `bad`.
 struct Scan {
   long long n, before, all;
 };
-template <int TILE>
-__device__ __forceinline__ Scan scan_items(const DecodeArgs& a, int heads, int b0, bool& bad) {
+__device__ __forceinline__ Scan scan_items(const DecodeArgs& a, int shift, int heads, int b0, bool& bad) {
   __shared__ long long s_sum[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int b = b0 + threadIdx.x;
@@ -61,7 +63,7 @@ __device__ __forceinline__ Scan scan_items(const DecodeArgs& a, int heads, int b
   if (b < a.c.batch) {
     const int len = checked_len(a.c, b, a.max_len);
     if (len < 0) bad = true;
-    r.n = (long long)tiles_of<TILE>(max(len, 0)) * heads;
+    r.n = (long long)tiles_of(max(len, 0), shift) * heads;
   }
   long long inc = r.n;
 #pragma unroll
@@ -94,8 +96,7 @@ __device__ __forceinline__ long long first_item(long long total, int ctas, int i
 struct Cursor {
   int b, h, tile, tiles, len;  // h: head * row_blocks + row block
 };
-template <int TILE>
-__device__ __forceinline__ void next_item(const DecodeArgs& a, int heads, Cursor& u) {
+__device__ __forceinline__ void next_item(const DecodeArgs& a, int shift, int heads, Cursor& u) {
   if (++u.tile < u.tiles) return;
   u.tile = 0;
   if (++u.h < heads) return;
@@ -104,7 +105,7 @@ __device__ __forceinline__ void next_item(const DecodeArgs& a, int heads, Cursor
     ++u.b;
     u.len = u.b < a.c.batch ? max(checked_len(a.c, u.b, a.max_len), 0) : 0;
   } while (u.b < a.c.batch && u.len == 0);
-  u.tiles = tiles_of<TILE>(u.len);
+  u.tiles = tiles_of(u.len, shift);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -213,34 +214,35 @@ __device__ __forceinline__ float4 ld_rank4(uint32_t addr) {
 // the order of the ranges; sequences that hold nothing get 0 and -inf. CTA (0, 0) also collects the status.
 constexpr int kJoinThreads = 256;
 
-template <typename T, int DP, int TILE, int CTAS>
+template <typename T, int DP, int CTAS>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) {
   __shared__ float s_w[CTAS][kRows];       // weight of each range's piece
-  __shared__ int s_at[CTAS];               // and where it lies
+  __shared__ int s_at[CTAS];               // and its first row
   __shared__ float s_m[kRows], s_l[kRows];
   __shared__ __align__(16) float s_acc[kJoinThreads * 4];
   __shared__ long long s_before[kJoinThreads / 32], s_all[kJoinThreads / 32];
-  const int heads = a.c.hkv * a.row_blocks;
+  const int heads = a.c.hkv / a.side * a.row_blocks;
   const int hb = blockIdx.x / a.slices, slice = blockIdx.x - hb * a.slices;
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_wait();
-  pdl_trigger();
-  if (blockIdx.x == 0 && b == 0) {
+  // The lengths are older than the decode kernel, which waited for what wrote them before it let this one begin: what
+  // follows from them is found while the decode kernel still runs.
+  auto collect = [&]() {  // the status of the call
+    if (blockIdx.x > 0 || b > 0) return;
     int e = 0;
     for (int i = tid; i < CTAS; i += kJoinThreads) e = max(e, a.cta_err[i]);
     e = __reduce_max_sync(0xffffffffu, e);
+    __syncthreads();
     if (lane == 0) s_all[warp] = e;
     __syncthreads();
     if (tid == 0) {
       for (int w = 0; w < kJoinThreads / 32; ++w) e = max(e, (int)s_all[w]);
       *a.err = e;
     }
-    __syncthreads();
-  }
+  };
   // items before this sequence, and in all
   long long before = 0, all = 0;
   for (int i = tid; i < a.c.batch; i += kJoinThreads) {
-    const long long n = (long long)tiles_of<TILE>(max(checked_len(a.c, i, a.max_len), 0)) * heads;
+    const long long n = (long long)tiles_of(max(checked_len(a.c, i, a.max_len), 0), a.tile_shift) * heads;
     all += n;
     if (i < b) before += n;
   }
@@ -258,6 +260,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
   const int h = hb / a.row_blocks, rb = hb - h * a.row_blocks;
   const int row0 = h * a.group + rb * kRows, rows = min(kRows, a.group - rb * kRows);
   if (len == 0) {
+    pdl_wait();
+    pdl_trigger();
+    collect();
     if (slice > 0) return;
     for (int i = tid; i < rows * a.c.d; i += kJoinThreads) {
       const int r = i / a.c.d, c = i - r * a.c.d;
@@ -266,51 +271,80 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
     if (a.lse && tid < rows) a.lse[(int64_t)b * a.hq + row0 + tid] = -INFINITY;
     return;
   }
-  const long long t0 = before + (long long)hb * tiles_of<TILE>(len), t1 = t0 + tiles_of<TILE>(len);
+  const int item = h / a.side * a.row_blocks + rb, sub = h % a.side;
+  const long long t0 = before + (long long)item * tiles_of(len, a.tile_shift), t1 = t0 + tiles_of(len, a.tile_shift);
   const int ctas = ctas_of<CTAS>(all);
   // the ranges that hold t0 and t1 - 1: range i is [all i / ctas, all (i + 1) / ctas)
   auto range_of = [&](long long t) { return (int)(((t + 1) * ctas - 1) / all); };
   const int c0 = range_of(t0), c1 = range_of(t1 - 1);
-  if (c0 == c1) return;  // written by its own range
+  if (c0 == c1) {  // written by its own range
+    pdl_wait();
+    pdl_trigger();
+    collect();
+    return;
+  }
   const int parts = c1 - c0 + 1;
   // a range's first piece is this one's unless it starts before it
-  for (int p = tid; p < parts; p += kJoinThreads) s_at[p] = (c0 + p) * 2 + (first_item(all, ctas, c0 + p) < t0 ? 1 : 0);
+  for (int p = tid; p < parts; p += kJoinThreads) 
+    s_at[p] = (((c0 + p) * 2 + (first_item(all, ctas, c0 + p) < t0 ? 1 : 0)) * a.side + sub) * a.part_rows;
   __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  // accumulators, four channels per thread; threads left over take every n-th piece. The first pieces are fetched
+  // while the statistics are
+  constexpr int kAhead = 4;
+  const int groups = DP / 4 / a.slices, cells = rows * groups;  // groups of four channels
+  const int sets = cells >= kJoinThreads ? 1 : kJoinThreads / cells;
+  const int set = sets > 1 ? tid / cells : 0;
+  float4 x[kAhead];
+  auto fetch = [&](int base) {
+    const int cell = sets > 1 ? tid - set * cells : base + tid;
+    if (set >= sets || cell >= cells) return;
+    const int r = cell / groups, c = (slice * groups + cell - r * groups) * 4;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (set + i * sets < parts) x[i] = *reinterpret_cast<const float4*>(a.part_o + ((int64_t)s_at[set + i * sets] + r) * DP + c);
+  };
+  fetch(0);
   // row statistics: one warp per row
   for (int r = warp; r < rows; r += kJoinThreads / 32) {
     float m = -INFINITY;
-    for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_ml[(s_at[p] * kRows + r) * 2]);
+    for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_ml[(s_at[p] + r) * 2]);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
     const float u = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     for (int p = lane; p < parts; p += 32) {
-      const float2 x = *reinterpret_cast<const float2*>(a.part_ml + (s_at[p] * kRows + r) * 2);
-      const float w = ex2_approx(x.x - u);
+      const float2 y = *reinterpret_cast<const float2*>(a.part_ml + (s_at[p] + r) * 2);
+      const float w = ex2_approx(y.x - u);
       s_w[p][r] = w;
-      l += x.y * w;
+      l += y.y * w;
     }
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
     if (lane == 0) { s_m[r] = m; s_l[r] = l; }
   }
   __syncthreads();
-  // accumulators, four channels per thread; threads left over take every n-th piece
-  const int groups = DP / 4 / a.slices, cells = rows * groups;  // groups of four channels
-  const int sets = cells >= kJoinThreads ? 1 : kJoinThreads / cells;
   for (int base = 0; base < cells; base += kJoinThreads) {
-    const int set = sets > 1 ? tid / cells : 0;
     const int cell = sets > 1 ? tid - set * cells : base + tid;
     const bool on = set < sets && cell < cells;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const int r = on ? cell / groups : 0, c = (slice * groups + (on ? cell - r * groups : 0)) * 4;
+    if (base > 0) fetch(base);
     if (on) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (set + i * sets < parts) {
+          const float w = s_w[set + i * sets][r];
+          acc.x = fmaf(w, x[i].x, acc.x); acc.y = fmaf(w, x[i].y, acc.y);
+          acc.z = fmaf(w, x[i].z, acc.z); acc.w = fmaf(w, x[i].w, acc.w);
+        }
 #pragma unroll 8
-      for (int p = set; p < parts; p += sets) {
-        const float4 x = *reinterpret_cast<const float4*>(a.part_o + ((int64_t)s_at[p] * kRows + r) * DP + c);
+      for (int p = set + kAhead * sets; p < parts; p += sets) {
+        const float4 y = *reinterpret_cast<const float4*>(a.part_o + ((int64_t)s_at[p] + r) * DP + c);
         const float w = s_w[p][r];
-        acc.x = fmaf(w, x.x, acc.x); acc.y = fmaf(w, x.y, acc.y);
-        acc.z = fmaf(w, x.z, acc.z); acc.w = fmaf(w, x.w, acc.w);
+        acc.x = fmaf(w, y.x, acc.x); acc.y = fmaf(w, y.y, acc.y);
+        acc.z = fmaf(w, y.z, acc.z); acc.w = fmaf(w, y.w, acc.w);
       }
     }
     if (sets > 1) {
@@ -318,8 +352,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
       __syncthreads();
       if (tid < cells)
         for (int s = 1; s < sets; ++s) {
-          const float4 x = *reinterpret_cast<const float4*>(&s_acc[(s * cells + tid) * 4]);
-          acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+          const float4 y = *reinterpret_cast<const float4*>(&s_acc[(s * cells + tid) * 4]);
+          acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
         }
     }
     if (on && set == 0) {
@@ -336,6 +370,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
     if (a.lse) a.lse[(int64_t)b * a.hq + row0 + tid] = l2 * kLn2F;
     if (a.scores) a.lse2[(int64_t)b * a.hq + row0 + tid] = l2;
   }
+  collect();
 }
 
 

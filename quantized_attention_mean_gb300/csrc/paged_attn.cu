@@ -128,7 +128,7 @@ template <typename T, int DP, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const DecodeArgs a) {
   using C = DecodeCfg<DP>;
-  constexpr int S = C::kStages, KS = DP / 16, NT = DP / 8, NK = C::kKeys / 8;
+  constexpr int S = C::kStages, KS = DP / 16, NT = DP / 8, NK = C::kKeys / 8, kShift = log2_of(C::kTile);
   // fp16 weights are held at up to 2^(7 + 8): 7 bits more before the smallest lose bits
   constexpr float kHead = std::is_same<T, __half>::value ? 7.0f : 0.f;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -157,16 +157,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     cu.b = blockIdx.y;
     cu.h = me / kRanks;
     cu.len = max(checked_len(a.c, cu.b, a.max_len), 0);
-    cu.tiles = tiles_of<C::kTile>(cu.len);
+    cu.tiles = tiles_of(cu.len, kShift);
     cu.tile = cu.tiles * rank / kRanks;
     left = cu.tiles * (rank + 1) / kRanks - cu.tile;
   } else {
     // this CTA's range of the line: the total, then the sequence that its first item lies in
     bool bad = false;
     if (threadIdx.x == 0) { s_b = a.c.batch; s_base = 0; }
-    Scan sc = scan_items<C::kTile>(a, heads, 0, bad);
+    Scan sc = scan_items(a, kShift, heads, 0, bad);
     long long total = sc.all;
-    for (int b0 = blockDim.x; b0 < a.c.batch; b0 += blockDim.x) total += scan_items<C::kTile>(a, heads, b0, bad).all;
+    for (int b0 = blockDim.x; b0 < a.c.batch; b0 += blockDim.x) total += scan_items(a, kShift, heads, b0, bad).all;
     const int ctas = total > 0 ? ctas_of<kCtas>(total) : 0;
     long long i0 = 0;
     if (me < ctas) {
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         base += sc.all;
         b0 += blockDim.x;
         if (base > i0 || b0 >= a.c.batch) break;
-        sc = scan_items<C::kTile>(a, heads, b0, bad);
+        sc = scan_items(a, kShift, heads, b0, bad);
       }
     }
     __syncthreads();
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     if (left > 0) {
       cu.b = s_b;
       cu.len = checked_len(a.c, cu.b, a.max_len);
-      cu.tiles = tiles_of<C::kTile>(cu.len);
+      cu.tiles = tiles_of(cu.len, kShift);
       const long long in = i0 - s_base;
       cu.h = (int)(in / cu.tiles);
       cu.tile = (int)(in - (long long)cu.h * cu.tiles);
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   auto load_next = [&](int st) {
     if (to_load > 0 && !dead) {
       load_stage<T, DP>(a, &tmK, &tmV, ld.h / a.row_blocks, page, slot, ring + st * C::kStageBytes, bars + st * 8);
-      next_item<C::kTile>(a, heads, ld);
+      next_item(a, kShift, heads, ld);
       --to_load;
       next_page();
     }
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       ++pieces;
       fresh = true;
     }
-    next_item<C::kTile>(a, heads, cu);
+    next_item(a, kShift, heads, cu);
   }
   if constexpr (CLUSTER) {
     // every warp's accumulator into its own ring, its statistics beside; then each thread of the
@@ -734,7 +734,7 @@ cudaError_t launch_decode_t(const DecodeArgs& a, const CUtensorMap* maps, cudaSt
     if (e != cudaSuccess) return e;
     e = launch_pdl(decode_kernel<T, DP, false>, dim3(kCtas), dim3(kWarps * 32), C::kSmem, st, maps[0], maps[1], a);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(join_kernel<T, DP, C::kTile, kCtas>, dim3(heads * a.slices, a.c.batch), dim3(kJoinThreads), 0, st, a);
+    e = launch_pdl(join_kernel<T, DP, kCtas>, dim3(heads * a.slices, a.c.batch), dim3(kJoinThreads), 0, st, a);
   }
   if (e != cudaSuccess || !a.scores || a.max_len == 0) return e;
   return launch_pdl(mass_kernel, dim3((unsigned)(((int64_t)a.max_len + 256 * kMassKeys - 1) / (256 * kMassKeys)), a.c.hkv, a.c.batch), dim3(256), 0,
@@ -808,6 +808,9 @@ int sage_paged_attn(const sage_packed* q, const sage_paged_cache* cache, const s
   // 24.3 and 26.0, 16 of 2000 13.2 and 14.2, 38 of 20000 68.9 and 71.0; 64 of 20000 111.8 and 108.7, 256 of 2000 56.0 and 53.0;
   // head_dim 64 within 2%)
   a.slices = (int64_t)heads_kv * a.row_blocks * batch <= 38 ? (head_dim <= 64 ? 2 : 4) : 1;
+  a.tile_shift = log2_of(head_dim <= 64 ? DecodeCfg<64>::kTile : DecodeCfg<128>::kTile);
+  a.side = 1;
+  a.part_rows = kRows;
   CUtensorMap maps[2];
   std::memset(maps, 0, sizeof(maps));
   if (tma) {

@@ -18,6 +18,8 @@ constexpr int kMostRanges = Q8Cfg<128, 1>::kRanges;
 bool q8_clustered(int batch, int hkv, int row_blocks, int64_t max_len, int d) {
   return (int64_t)hkv * row_blocks * batch * kRanks <= kCtas && max_len <= 8 * kRanks * tile_of(d);
 }
+// Heads whose token rows lie side by side, which a line's item takes together, so that DRAM is read in 256 bytes or more.
+int heads_beside(int hkv, int d) { return hkv % 2 ? 1 : d <= 64 && hkv % 4 == 0 ? 4 : 2; }
 bool q8_layout(int batch, int hq, int hkv, int64_t max_len, int d, Q8Layout* L) {
   if (batch < 0 || hq < 1 || hkv < 1 || hq % hkv || max_len < 0 || d < 1 || d > 128) return false;
   const int dp = d <= 64 ? 64 : 128;
@@ -25,8 +27,9 @@ bool q8_layout(int batch, int hq, int hkv, int64_t max_len, int d, Q8Layout* L) 
   const bool line = !q8_clustered(batch, hkv, (hq / hkv + kRows - 1) / kRows, max_len, d);
   L->err = SAGE_STATUS_BYTES;
   L->part_o = L->err + (line ? up256(4 * kMostRanges) : 0);
-  L->part_ml = L->part_o + (line ? up256((size_t)kMostRanges * 2 * kRows * dp * 4) : 0);
-  L->total = L->part_ml + (line ? up256((size_t)kMostRanges * 2 * kRows * 2 * 4) : 0);
+  const size_t rows = line ? (size_t)kMostRanges * 2 * heads_beside(hkv, d) * (hq / hkv <= 8 ? 8 : kRows) : 0;
+  L->part_ml = L->part_o + up256(rows * dp * 4);
+  L->total = L->part_ml + up256(rows * 2 * 4);
   return true;
 }
 
@@ -104,8 +107,14 @@ int sage_paged_attn_q8(const sage_packed* q, const sage_q8_cache* cache, const s
   a.box_rows = 8;
   while (a.box_rows < keys && view.c.page_size % (a.box_rows * 2) == 0) a.box_rows *= 2;
   a.page_shift = -1;
-  for (int i = 0; i < 31; ++i)
+  p.block_shift = -1;
+  for (int i = 0; i < 31; ++i) {
     if (view.c.page_size == 1 << i) a.page_shift = i;
+    if (view.block == 1 << i) p.block_shift = i;
+  }
+  a.part_rows = a.group <= 8 ? 8 : kRows;
+  a.side = !p.cluster && tensor_layout == SAGE_NHD ? heads_beside(heads_kv, head_dim) : 1;
+  a.tile_shift = log2_of(tile_of(head_dim) / a.side);
   // the join by channels where its CTAs would leave SMs idle
   a.slices = (int64_t)heads_kv * a.row_blocks * batch <= 38 ? (head_dim <= 64 ? 2 : 4) : 1;
   CUtensorMap maps[2];

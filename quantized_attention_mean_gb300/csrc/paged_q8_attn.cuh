@@ -29,6 +29,7 @@ struct Q8Args {
   DecodeArgs a;
   const float* ks; const float* vs;
   int block, blocks;
+  int block_shift;  // log2 of block, or -1
   int unit;      // bytes of one copy where rows do not come by TMA: 16, 8, 4, or 1 (plain loads)
   int bf16;      // type of q and out
   int q4;        // q allows accesses of four channels
@@ -94,6 +95,18 @@ __device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi) {
         : "r"(u));
   }
 }
+// Whether a stage's boxes have landed.
+__device__ __forceinline__ bool ready(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Byte offset of 16-byte unit c of row r of a tile: the swizzle that a TMA box of rows of DP bytes is written with.
 template <int DP>
 __device__ __forceinline__ int unit_at(int r, int c) {
@@ -112,24 +125,37 @@ __device__ __forceinline__ void load_q8_stage(const Q8Args& p, const CUtensorMap
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const bool in = page[i] >= 0;
-    const int64_t at = in ? ((int64_t)page[i] * a.c.hkv + h) * p.blocks + slot[i] / p.block : 0;
+    const int blk = p.block_shift >= 0 ? slot[i] >> p.block_shift : slot[i] / p.block;
+    const int64_t at = in ? ((int64_t)page[i] * a.c.hkv + h) * p.blocks + blk : 0;
     const uint32_t dst = smem_u32(scale + lane + 32 * i);
     cp_async_small<4>(dst, p.ks + at, in ? 4 : 0);
     cp_async_small<4>(dst + C::kKeys * 4, p.vs + at, in ? 4 : 0);
   }
   if (a.load == kLoadTma) {
-    if (lane == 0)
-      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(C::kStageBytes) : "memory");
-    __syncwarp();
-    const int kv = lane & 1, row = (lane >> 1) * a.box_rows;
-    int pg = 0, sl = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int x = __shfl_sync(0xffffffffu, page[i], row & 31), y = __shfl_sync(0xffffffffu, slot[i], row & 31);
-      if (i == row >> 5) { pg = x; sl = y; }
+    // issued by one elected lane with operands that all lanes agree on: lanes with boxes of their own would take turns
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(C::kStageBytes)
+        : "memory");
+#pragma unroll 1
+    for (int row = 0; row < C::kKeys; row += a.box_rows) {
+      int pg = __shfl_sync(0xffffffffu, page[0], row & 31), sl = __shfl_sync(0xffffffffu, slot[0], row & 31);
+      if (N > 1 && row >= 32) {
+        pg = __shfl_sync(0xffffffffu, page[N - 1], row & 31);
+        sl = __shfl_sync(0xffffffffu, slot[N - 1], row & 31);
+      }
+      pg = pg >= 0 ? pg : a.c.num_pages;  // (outside of the tensor: zeros)
+      asm volatile(
+          "{\n\t.reg .pred e;\n\t"
+          "elect.sync _|e, 0xffffffff;\n\t"
+          "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%2, {%5, %6, %7, %8}], [%4];\n\t"
+          "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%3, {%5, %6, %7, %8}], [%4];\n\t}" ::"r"(
+              base + row * DP),
+          "r"(base + C::kTileBytes + row * DP), "l"(reinterpret_cast<uint64_t>(tmK)), "l"(reinterpret_cast<uint64_t>(tmV)), "r"(bar),
+          "r"(0), "r"(sl), "r"(h), "r"(pg)
+          : "memory");
     }
-    if (row < C::kKeys)
-      tma_box(base + kv * C::kTileBytes + row * DP, kv ? tmV : tmK, bar, 0, sl, h, pg >= 0 ? pg : a.c.num_pages);
     return;
   }
   const uint8_t* kb = static_cast<const uint8_t*>(a.c.k) + h * a.c.k_sh;
@@ -192,8 +218,10 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ int s_err[kWarps];
   const DecodeArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int heads = a.c.hkv * a.row_blocks;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (one value for the warp)
+  // an item is a tile of `side` heads that lie side by side: warps of one head share its keys
+  const int side = a.side, sub = warp & (side - 1), part = warp / side;
+  const int heads = a.c.hkv / side * a.row_blocks;
   uint8_t* const ring = sm + warp * C::kWarpBytes;
   float* const scales = reinterpret_cast<float*>(sm + C::kOffScale) + warp * S * 2 * C::kKeys;
   float4* const merge = reinterpret_cast<float4*>(sm + C::kOffMerge);
@@ -208,7 +236,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
   pdl_wait();
   const int me = blockIdx.x;
   int err = 0;
-  long long left = 0;
+  int left = 0;  // (of the line's items, of which this CTA's range has far fewer than 2^31)
   Cursor cu{a.c.batch, 0, 0, 1, 0};
   __shared__ long long s_base;
   __shared__ int s_b;
@@ -217,21 +245,21 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
     cu.b = blockIdx.y;
     cu.h = me / kRanks;
     cu.len = max(checked_len(a.c, cu.b, a.max_len), 0);
-    cu.tiles = tiles_of<C::kTile>(cu.len);
+    cu.tiles = tiles_of(cu.len, a.tile_shift);
     cu.tile = cu.tiles * rank / kRanks;
     left = cu.tiles * (rank + 1) / kRanks - cu.tile;
   } else {
     // this CTA's range of the line: the total, then the sequence that its first item lies in
     bool bad = false;
     if (threadIdx.x == 0) { s_b = a.c.batch; s_base = 0; }
-    Scan sc = scan_items<C::kTile>(a, heads, 0, bad);
+    Scan sc = scan_items(a, a.tile_shift, heads, 0, bad);
     long long total = sc.all;
-    for (int b0 = blockDim.x; b0 < a.c.batch; b0 += blockDim.x) total += scan_items<C::kTile>(a, heads, b0, bad).all;
+    for (int b0 = blockDim.x; b0 < a.c.batch; b0 += blockDim.x) total += scan_items(a, a.tile_shift, heads, b0, bad).all;
     const int ctas = total > 0 ? ctas_of<C::kRanges>(total) : 0;
     long long i0 = 0;
     if (me < ctas) {
       i0 = first_item(total, ctas, me);
-      left = first_item(total, ctas, me + 1) - i0;
+      left = (int)(first_item(total, ctas, me + 1) - i0);
       long long base = 0;
       for (int b0 = 0;;) {
         const long long lo = base + sc.before;
@@ -239,7 +267,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
         base += sc.all;
         b0 += blockDim.x;
         if (base > i0 || b0 >= a.c.batch) break;
-        sc = scan_items<C::kTile>(a, heads, b0, bad);
+        sc = scan_items(a, a.tile_shift, heads, b0, bad);
       }
     }
     __syncthreads();
@@ -247,7 +275,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
     if (left > 0) {
       cu.b = s_b;
       cu.len = checked_len(a.c, cu.b, a.max_len);
-      cu.tiles = tiles_of<C::kTile>(cu.len);
+      cu.tiles = tiles_of(cu.len, a.tile_shift);
       const long long in = i0 - s_base;
       cu.h = (int)(in / cu.tiles);
       cu.tile = (int)(in - (long long)cu.h * cu.tiles);
@@ -273,21 +301,28 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
   }
   // ---- fill the ring: S - 1 stages in flight, the pages of the stage after them already read
   Cursor ld = cu;
-  long long to_load = left;
+  int to_load = left;
   int page[NP], slot[NP];
   auto next_page = [&]() {
+    const int* const row = a.c.table + ld.b * a.c.table_stride;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int key = ld.tile * C::kTile + warp * C::kKeys + i * 32 + lane;
-      find_page(a, ld.b, key, to_load > 0 && key < ld.len, page[i], slot[i], err);
+      const int key = (ld.tile << a.tile_shift) + part * C::kKeys + i * 32 + lane, at = page_index(a, key);
+      const bool live = to_load > 0 && key < ld.len;
+      slot[i] = key - at * a.c.page_size;
+      page[i] = live ? __ldg(row + at) : -1;
+      const bool bad = live && (unsigned)page[i] >= (unsigned)a.c.num_pages;
+      page[i] = bad ? -1 : page[i];
+      err = bad ? kDevPage : err;
     }
   };
   bool dead = false;  // a wait has run out: nothing more is loaded
   auto load_next = [&](int st) {
     if (to_load > 0 && !dead) {
-      load_q8_stage<C, DP>(p, &tmK, &tmV, ld.h / a.row_blocks, page, slot, ring + st * C::kStageBytes,
+      const int h = a.row_blocks == 1 ? ld.h : ld.h / a.row_blocks;
+      load_q8_stage<C, DP>(p, &tmK, &tmV, h * side + sub, page, slot, ring + st * C::kStageBytes,
                         scales + st * 2 * C::kKeys, bars + st * 8);
-      next_item<C::kTile>(a, heads, ld);
+      next_item(a, a.tile_shift, heads, ld);
       --to_load;
       next_page();
     }
@@ -320,7 +355,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
       fresh = false;
       tile0 = cu.tile;
       const int h = cu.h / a.row_blocks, rb = cu.h - h * a.row_blocks;
-      row0 = h * a.group + rb * kRows;
+      row0 = (h * side + sub) * a.group + rb * kRows;
       rows = min(kRows, a.group - rb * kRows);
 #pragma unroll
       for (int x = 0; x < NH; ++x) {
@@ -379,15 +414,16 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
     // the stage after the ones in flight goes where the previous item was
     __syncwarp();
     load_next(stage == 0 ? S - 1 : stage - 1);
-    const int key0 = cu.tile * C::kTile + warp * C::kKeys;
+    const int key0 = (cu.tile << a.tile_shift) + part * C::kKeys;
     uint8_t* const here = ring + stage * C::kStageBytes;
     const float* const sc = scales + stage * 2 * C::kKeys;
     if (a.load == kLoadTma) {
-      if (!dead && !__all_sync(0xffffffffu, wait_stage(bars + stage * 8, parity))) {
+      if (!dead && !__all_sync(0xffffffffu, ready(bars + stage * 8, parity)) &&
+          !__all_sync(0xffffffffu, wait_stage(bars + stage * 8, parity))) {
         dead = true;
         err = kDevTimeout;
         // what is in flight lands (or runs out of time) before the shared memory goes away
-        for (int k = 0; k < (int)(left - to_load); ++k) {
+        for (int k = 0; k < left - to_load; ++k) {
           const int st = stage + k;
           wait_stage(bars + (st % S) * 8, parity ^ (st >= S ? 1u : 0u));
         }
@@ -403,7 +439,8 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
     cp_async_wait<S - 1>();
     __syncwarp();
     if (key0 < cu.len) {
-      const uint32_t kb = smem_u32(here), vb = kb + C::kTileBytes;
+      // (keys 0-15 at unit u = 0, then at unit 1: other units by exclusive or, which the swizzle is)
+      const uint32_t kb = smem_u32(here) + unit_at<DP>(lane & 15, lane >> 4);
       // ---- S^T = K Q^T: 16 keys x 8 heads each
       float s[M][NH][4];
 #pragma unroll
@@ -413,13 +450,12 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[g][x][e] = 0.f;
       {
-        const int kr = lane & 15, hi = lane >> 4;  // keys 0-15 at unit c, then at unit c + 1
 #pragma unroll
         for (int u = 0; u < KS; u += 2)
 #pragma unroll
           for (int g = 0; g < M; ++g) {
             uint32_t b[4], f[4];
-            ldsm4(kb + g * 16 * DP + unit_at<DP>(kr, u + hi), b);
+            ldsm4((kb ^ (u << 4)) + g * 16 * DP, b);
             widen<KT, 0, 1, 2, 3>(b[0], f[0], f[2]);
             widen<KT, 0, 1, 2, 3>(b[1], f[1], f[3]);
 #pragma unroll
@@ -561,13 +597,12 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
       // ---- O^T += V^T P^T: 16 channels x 8 heads each, 16 keys at a time. Row r0 of a fragment is channel 2 r0 of its
       // unit, row r0 + 8 channel 2 r0 + 1: the two channels of a register that the transposed read gives
       {
-        const int kr = lane & 15, hi = lane >> 4;
 #pragma unroll
         for (int g = 0; g < M; ++g)
 #pragma unroll
           for (int u = 0; u < KS; u += 2) {
             uint32_t b[4], f[4];
-            ldsm4t(vb + g * 16 * DP + unit_at<DP>(kr, u + hi), b);
+            ldsm4t((kb ^ (u << 4)) + C::kTileBytes + g * 16 * DP, b);
             widen<VT, 0, 2, 1, 3>(b[0], f[0], f[1]);
             widen<VT, 0, 2, 1, 3>(b[1], f[2], f[3]);
 #pragma unroll
@@ -596,21 +631,19 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
           if (r0 == 0) ml[warp * kRows + x * 8 + 2 * j + e] = make_float4(m[x][e], l[x][e], F[x][e], 0.f);
         }
       __syncthreads();
-      float Mx[NH][2], L[NH][2], g[NH][2];  // of all warps; from F's frame to m's
+      float Mx[NH][2], L[NH][2], g[NH][2];  // of the head's warps; from F's frame to m's
 #pragma unroll
       for (int x = 0; x < NH; ++x)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float4* at = ml + x * 8 + 2 * j + e;
+          const float4* at = ml + sub * kRows + x * 8 + 2 * j + e;
           float mm = -INFINITY, ff = -INFINITY, ll = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
+          for (int w = 0; w < kWarps; w += side) {
             mm = fmaxf(mm, at[w * kRows].x);
             ff = fmaxf(ff, at[w * kRows].z);
           }
           const float mu = mm == -INFINITY ? 0.f : mm, fu = ff == -INFINITY ? 0.f : ff;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) ll += at[w * kRows].y * ex2_approx(at[w * kRows].x - mu);
+          for (int w = 0; w < kWarps; w += side) ll += at[w * kRows].y * ex2_approx(at[w * kRows].x - mu);
           const float f = ex2_approx(F[x][e] - fu);
 #pragma unroll
           for (int u = 0; u < KS; ++u) {
@@ -621,17 +654,17 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
           L[x][e] = ll;
           g[x][e] = ex2_approx(ff - mu);
         }
-      // added to warp 0's in their order, eight heads at a time
+      // added to the head's first warp's in their order, eight heads at a time
 #pragma unroll
       for (int x = 0; x < NH; ++x)
 #pragma unroll 1
-        for (int w = 1; w < kWarps; ++w) {
+        for (int w = side; w < kWarps; ++w) {
           if (warp == w) {
 #pragma unroll
             for (int u = 0; u < KS; ++u) merge[u * 32 + lane] = make_float4(o[u][x][0], o[u][x][1], o[u][x][2], o[u][x][3]);
           }
           __syncthreads();
-          if (warp == 0) {
+          if (warp == (w & (side - 1))) {
 #pragma unroll
             for (int u = 0; u < KS; ++u) {
               const float4 y = merge[u * 32 + lane];
@@ -640,10 +673,10 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
           }
           __syncthreads();
         }
-      if (warp == 0) {
+      if (warp < side) {
         // the whole (sequence, head) in this range: the result; a part of it: to the workspace
         const bool whole = tile0 == 0 && cu.tile + 1 == cu.tiles;
-        const int64_t at = ((int64_t)me * 2 + (pieces > 0)) * kRows;
+        const int64_t at = (((int64_t)me * 2 + (pieces > 0)) * side + sub) * a.part_rows;
 #pragma unroll
         for (int x = 0; x < NH; ++x)
 #pragma unroll
@@ -670,10 +703,11 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
             }
           }
       }
+      if (side == kWarps) __syncthreads();  // (the statistics are written again)
       ++pieces;
       fresh = true;
     }
-    next_item<C::kTile>(a, heads, cu);
+    next_item(a, a.tile_shift, heads, cu);
   }
   if (p.cluster) {
     // every warp's accumulator into its own ring, its statistics beside; then each thread of the
@@ -757,8 +791,8 @@ cudaError_t launch_q8_t(const Q8Args& p, const CUtensorMap* maps, cudaStream_t s
     e = launch_pdl(q8_decode_kernel<KT, VT, DP, NH>, dim3(C::kRanges), dim3(kWarps * 32), C::kSmem, st, maps[0], maps[1], p);
     if (e != cudaSuccess) return e;
     const dim3 grid(heads * a.slices, a.c.batch);
-    return p.bf16 ? launch_pdl(join_kernel<__nv_bfloat16, DP, C::kTile, C::kRanges>, grid, dim3(kJoinThreads), 0, st, a)
-                  : launch_pdl(join_kernel<__half, DP, C::kTile, C::kRanges>, grid, dim3(kJoinThreads), 0, st, a);
+    return p.bf16 ? launch_pdl(join_kernel<__nv_bfloat16, DP, C::kRanges>, grid, dim3(kJoinThreads), 0, st, a)
+                  : launch_pdl(join_kernel<__half, DP, C::kRanges>, grid, dim3(kJoinThreads), 0, st, a);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(heads * kRanks, a.c.batch);
