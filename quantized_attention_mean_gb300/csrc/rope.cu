@@ -14,11 +14,12 @@
 
 #include "../../include/sageattn.h"
 #include "launch.h"
+#include "sm103_ptx.cuh"
 
 namespace sage {
 namespace {
 
-constexpr int kRopeWarps = 8;
+constexpr int kRopeWarps = 4, kRopeBlocks = 4;  // of an SM
 constexpr int kMaxPairs = 64;
 
 struct RopeArgs {
@@ -28,7 +29,7 @@ struct RopeArgs {
   const void* w[2];          // or null
   const int* pos; int64_t pos_sb;  // null: the token's place in its row
   const float* freq;
-  int heads[2], chunks[2];   // chunks: items that share a token's heads
+  int heads[2], chunks;      // chunks: warps that share a token's heads
   int batch, n, d, rot;
   int interleaved, w32, lanes;  // lanes of a row: a power of two
   int64_t items;
@@ -41,17 +42,70 @@ template <typename T> struct Run<T, 4> { using type = uint2; };
 template <typename T> struct Run<T, 2> { using type = uint32_t; };
 template <typename T> struct Run<T, 1> { using type = uint16_t; };
 
+// A run, where heads are left: one predicated access, no branch. (Volatile: an output may be its input.)
+__device__ __forceinline__ void load_if(uint4& r, const void* p, int left) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %5, 0;\n\t@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+               : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w) : "l"(p), "r"(left) : "memory");
+}
+__device__ __forceinline__ void store_if(void* p, const uint4& r, int left) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %5, 0;\n\t@p st.global.v4.u32 [%4], {%0, %1, %2, %3};\n\t}" ::"r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "l"(p), "r"(left)
+               : "memory");
+}
+__device__ __forceinline__ void load_if(uint2& r, const void* p, int left) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %3, 0;\n\t@p ld.global.v2.u32 {%0, %1}, [%2];\n\t}"
+               : "+r"(r.x), "+r"(r.y) : "l"(p), "r"(left) : "memory");
+}
+__device__ __forceinline__ void store_if(void* p, const uint2& r, int left) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %3, 0;\n\t@p st.global.v2.u32 [%2], {%0, %1};\n\t}" ::"r"(r.x), "r"(r.y), "l"(p), "r"(left)
+               : "memory");
+}
+__device__ __forceinline__ void load_if(uint32_t& r, const void* p, int left) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %2, 0;\n\t@p ld.global.u32 %0, [%1];\n\t}"
+               : "+r"(r) : "l"(p), "r"(left) : "memory");
+}
+__device__ __forceinline__ void store_if(void* p, const uint32_t& r, int left) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %2, 0;\n\t@p st.global.u32 [%1], %0;\n\t}" ::"r"(r), "l"(p), "r"(left)
+               : "memory");
+}
+__device__ __forceinline__ void load_if(uint16_t& r, const void* p, int left) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %2, 0;\n\t@p ld.global.u16 %0, [%1];\n\t}"
+               : "+h"(r) : "l"(p), "r"(left) : "memory");
+}
+__device__ __forceinline__ void store_if(void* p, const uint16_t& r, int left) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %2, 0;\n\t@p st.global.u16 [%1], %0;\n\t}" ::"h"(r), "l"(p), "r"(left)
+               : "memory");
+}
+
+// Two fp32 values in a pair of registers.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair make_pair2(float lo, float hi) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+  return p;
+}
+__device__ __forceinline__ void split_pair2(Pair p, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ Pair mul_pair2(Pair x, Pair y) {
+  Pair z;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
+  return z;
+}
+__device__ __forceinline__ Pair fma_pair2(Pair x, Pair y, Pair z) {
+  Pair w;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(w) : "l"(x), "l"(y), "l"(z));
+  return w;
+}
+
 template <typename T>
 __device__ __forceinline__ T narrow(float x) {
   if constexpr (std::is_same<T, __half>::value) return __float2half_rn(x);
   else return __float2bfloat16_rn(x);
 }
 
-// First channels of the two runs of slot x, and the first pair; `on`: which of the runs lie within the row.
-template <int V>
+// First channels of the two runs of slot x, and which of the runs lie within the row.
+template <int V, bool PAIRS>
 __device__ __forceinline__ void slot_runs(const RopeArgs& a, int x, int (&c)[2], bool (&on)[2]) {
   const int half = a.rot / 2, turned = half / V;
-  if (a.interleaved) {
+  if (PAIRS) {
     c[0] = 2 * x * V;
     c[1] = c[0] + V;
   } else if (x < turned) {
@@ -65,143 +119,227 @@ __device__ __forceinline__ void slot_runs(const RopeArgs& a, int x, int (&c)[2],
   on[1] = c[1] < a.d;
 }
 
-// SLOTS: pairs of runs per lane.
-template <typename T, int V, int SLOTS>
-__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeArgs a) {
+// Two 16-bit values of a register.
+template <typename T>
+__device__ __forceinline__ void widen2(uint32_t x, float& lo, float& hi) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+    lo = f.x;
+    hi = f.y;
+  } else {
+    lo = __uint_as_float(x << 16);
+    hi = __uint_as_float(x & 0xffff0000u);
+  }
+}
+
+// SLOTS: pairs of runs per lane. PAIRS: neighbouring channels are turned. A warp takes a share of one token's heads, first
+// of q, then of k, `rows` heads at a time. The next kAhead such steps are in flight, the first ones before the position is
+// known. With x' = x w a pair becomes f (x'_i cos - x'_j sin, x'_j cos + x'_i sin), f the row's norm: the products of weights
+// with cosines and sines are the same for all heads, which leaves six operations for two values.
+// LANES: of a row, or 0: a.lanes.
+template <typename T, int V, int SLOTS, bool PAIRS, int LANES>
+__global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(const RopeArgs a) {
   using R = typename Run<T, V>::type;
+  constexpr int kAhead = V == 8 ? 4 : 2, N = SLOTS * V / 2;  // N: pairs of a lane, two by two
   __shared__ unsigned long long s_turns[kMaxPairs];
   __shared__ float2 s_cs[kRopeWarps][kMaxPairs];
+  __shared__ __align__(16) float s_w[2][128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pairs = a.rot / 2;
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x < pairs) {
+  for (int k = threadIdx.x; k < pairs; k += kRopeWarps * 32) {
     // turns per position modulo 1, in units of 2^-64
-    double f = (double)__ldg(&a.freq[threadIdx.x]) * 0.15915494309189533577;
+    double f = (double)__ldg(&a.freq[k]) * 0.15915494309189533577;
     f -= floor(f);
-    s_turns[threadIdx.x] = __double2ull_rn(f * 18446744073709551616.0);
+    s_turns[k] = __double2ull_rn(f * 18446744073709551616.0);
+  }
+  for (int k = threadIdx.x; k < 2 * a.d; k += kRopeWarps * 32) {
+    const int i = k >= a.d, c = k - i * a.d;
+    const void* w = a.w[i];
+    s_w[i][c] = !w ? 1.f : a.w32 ? __ldg(static_cast<const float*>(w) + c) : to_f32<T>(static_cast<const T*>(w)[c]);
   }
   __syncthreads();
-  const int sub = lane & (a.lanes - 1), row = lane / a.lanes, rows = 32 / a.lanes;
+  const int lanes = LANES ? LANES : a.lanes;
+  const int sub = lane & (lanes - 1), row = lane / lanes, rows = 32 / lanes;
   int c[SLOTS][2];
   bool on[SLOTS][2];
 #pragma unroll
-  for (int s = 0; s < SLOTS; ++s) slot_runs<V>(a, sub + s * a.lanes, c[s], on[s]);
-  const int per_token = a.chunks[0] + a.chunks[1];
+  for (int s = 0; s < SLOTS; ++s) slot_runs<V, PAIRS>(a, sub + s * lanes, c[s], on[s]);
+  int off[SLOTS][2];  // taken off a count of heads, it leaves none
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) off[s][u] = on[s][u] ? 0 : -(1 << 30);
+  R raw[kAhead][SLOTS][2];  // (runs behind the row stay zero)
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) raw[k][s][0] = raw[k][s][1] = R{};
 
   for (int64_t item = (int64_t)blockIdx.x * kRopeWarps + warp; item < a.items; item += (int64_t)gridDim.x * kRopeWarps) {
-    const int64_t token = item / per_token;
-    int chunk = (int)(item - token * per_token);
-    const int which = chunk < a.chunks[0] ? 0 : 1;
-    if (which) chunk -= a.chunks[0];
-    const int b = (int)(token / a.n), i = (int)(token - (int64_t)b * a.n);
-    // ---- cosines and sines of the token, two pairs per lane
-    __syncwarp();
-    if (pairs > 0) {
-      const long long p = a.pos ? __ldg(&a.pos[b * a.pos_sb + i]) : i;
-      for (int k = lane; k < pairs; k += 32) {
-        const long long turns = (long long)(s_turns[k] * (unsigned long long)p);  // modulo one, in [-1/2, 1/2)
-        float sn, cs;
-        sincospif(__ll2float_rn(turns) * 0x1p-63f, &sn, &cs);
-        s_cs[warp][k] = make_float2(cs, sn);
+    const int64_t token = a.chunks == 1 ? item : item / a.chunks;
+    const int chunk = (int)(item - token * a.chunks);
+    const int b = a.batch == 1 ? 0 : (int)(token / a.n), i = (int)(token - (int64_t)b * a.n);
+    // steps: those of q's heads, filled up to a multiple of kAhead, then k's
+    const int hq0 = (int)((int64_t)a.heads[0] * chunk / a.chunks), nq = (int)((int64_t)a.heads[0] * (chunk + 1) / a.chunks) - hq0;
+    const int hk0 = (int)((int64_t)a.heads[1] * chunk / a.chunks), nk = (int)((int64_t)a.heads[1] * (chunk + 1) / a.chunks) - hk0;
+    const int steps_q = ((nq + rows - 1) / rows + kAhead - 1) / kAhead * kAhead, steps = steps_q + (nk + rows - 1) / rows;
+    auto at = [&](const int64_t (&st)[3], int h0) { return b * st[0] + i * st[1] + (h0 + row) * st[2]; };
+    // what is fetched next: this lane's row, the heads that are left from it on, the steps until k's
+    const T* fx = static_cast<const T*>(a.x[0]) + at(a.xs[0], hq0);
+    int64_t f_stride = rows * a.xs[0][2];
+    int f_left = nq - row, f_steps = steps_q;
+    auto fetch = [&](R (&to)[SLOTS][2]) {
+      if (f_steps-- == 0) {
+        fx = static_cast<const T*>(a.x[1]) + at(a.xs[1], hk0);
+        f_stride = rows * a.xs[1][2];
+        f_left = nk - row;
       }
-    }
-    __syncwarp();
-    float2 cs[SLOTS][V];
-    float w[SLOTS][2][V];
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        // the e-th pair of a slot: channels e of both runs, or two neighbours of one of them
-        int pr;
-        bool turned;
-        if (a.interleaved) {
-          pr = (V == 1 ? c[s][0] : e < V / 2 ? c[s][0] + 2 * e : c[s][1] + 2 * (e - V / 2)) / 2;
-          turned = pr < pairs;
-        } else {
-          pr = c[s][0] + e;
-          turned = pr < pairs;
-        }
-        cs[s][e] = turned ? s_cs[warp][pr] : make_float2(1.f, 0.f);
-      }
-      const void* wp = a.w[which];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          w[s][u][e] = 1.f;
-          if (wp && on[s][u])
-            w[s][u][e] = a.w32 ? __ldg(static_cast<const float*>(wp) + c[s][u] + e)
-                               : to_f32<T>(static_cast<const T*>(wp)[c[s][u] + e]);
-        }
-    }
-    // ---- the heads of this item
-    const int heads = a.heads[which], h0 = (int)((int64_t)heads * chunk / a.chunks[which]),
-              h1 = (int)((int64_t)heads * (chunk + 1) / a.chunks[which]);
-    const T* xb = static_cast<const T*>(a.x[which]) + b * a.xs[which][0] + i * a.xs[which][1];
-    T* yb = static_cast<T*>(a.y[which]) + b * a.ys[which][0] + i * a.ys[which][1];
-#pragma unroll 2
-    for (int h = h0 + row; h - row < h1; h += rows) {
-      const bool live = h < h1;
-      float y[SLOTS][2][V];
-      float sum = 0.f;
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          R r{};
-          if (live && on[s][u]) r = *reinterpret_cast<const R*>(xb + h * a.xs[which][2] + c[s][u]);
-          const T* t = reinterpret_cast<const T*>(&r);
+        for (int u = 0; u < 2; ++u) load_if(to[s][u], fx + c[s][u], f_left + off[s][u]);
+      fx += f_stride;
+      f_left -= rows;
+    };
+    long long p = i;
+    if (pairs > 0 && a.pos) p = __ldg(&a.pos[b * a.pos_sb + i]);
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            y[s][u][e] = to_f32<T>(t[e]);
-            sum = fmaf(y[s][u][e], y[s][u][e], sum);
+    for (int k = 0; k < kAhead; ++k) fetch(raw[k]);
+    // ---- cosines and sines of the token, two pairs per lane
+    __syncwarp();
+    for (int k = lane; k < pairs; k += 32) {
+      const long long turns = (long long)(s_turns[k] * (unsigned long long)p);  // modulo one, in [-1/2, 1/2)
+      float sn, cs;
+      sincospif(__ll2float_rn(turns) * 0x1p-63f, &sn, &cs);
+      s_cs[warp][k] = make_float2(cs, sn);
+    }
+    __syncwarp();
+    T* y = nullptr;  // where this lane's row goes
+    int64_t y_stride = 0;
+    Pair ca[N], cb[N], da[N], db[N];  // (x_i, x_j) -> (x_i ca + x_j cb, x_j da + x_i db)
+#pragma unroll 1
+    for (int base = 0, left = 0, live = 0; base < steps; base += kAhead) {
+      if (base == 0 || base == steps_q) {
+        const int w = base < steps_q ? 0 : 1;
+        y = static_cast<T*>(a.y[w]) + at(a.ys[w], w ? hk0 : hq0);
+        y_stride = rows * a.ys[w][2];
+        left = w ? nk : nq;
+        live = left - row;
+        auto turn = [&](int e, float& i0, float& j0, float& j1, float& i1) {
+          // the e-th pair of a lane: channels e of both runs of a slot, or two neighbours of one of them
+          const int s = e / V, v = e % V;
+          const int u0 = PAIRS && V > 1 ? v / (V > 1 ? V / 2 : 1) : 0, u1 = PAIRS && V > 1 ? u0 : 1;
+          const int e0 = PAIRS && V > 1 ? 2 * v % V : v, e1 = PAIRS && V > 1 ? e0 + 1 : v;
+          const int ci = c[s][u0] + e0, cj = c[s][u1] + e1, pr = PAIRS ? ci / 2 : ci;
+          const float2 t = pr < pairs ? s_cs[warp][pr] : make_float2(1.f, 0.f);
+          const float wi = on[s][u0] ? s_w[w][ci] : 0.f, wj = on[s][u1] ? s_w[w][cj] : 0.f;
+          i0 = wi * t.x;
+          j0 = -wj * t.y;
+          j1 = wj * t.x;
+          i1 = wi * t.y;
+        };
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          float p0, p1, p2, p3, q0, q1, q2, q3;
+          turn(2 * e, p0, p1, p2, p3);
+          turn(2 * e + 1, q0, q1, q2, q3);
+          ca[e] = make_pair2(p0, q0);
+          cb[e] = make_pair2(p1, q1);
+          da[e] = make_pair2(p2, q2);
+          db[e] = make_pair2(p3, q3);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        Pair xi[N], xj[N];
+        if constexpr (V == 1) {
+          auto one = [&](int s, int u) { return to_f32<T>(*reinterpret_cast<const T*>(&raw[k][s][u])); };
+          xi[0] = make_pair2(one(0, 0), one(SLOTS - 1, 0));
+          xj[0] = make_pair2(one(0, 1), one(SLOTS - 1, 1));
+        } else {
+#pragma unroll
+          for (int s = 0; s < SLOTS; ++s) {
+            float f[2][V];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int e = 0; e < V; e += 2)
+                widen2<T>(reinterpret_cast<const uint32_t*>(&raw[k][s][u])[e / 2], f[u][e], f[u][e + 1]);
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              // pairs e and e + 1
+              if (PAIRS && V == 2) {
+                xi[s] = make_pair2(f[0][0], f[1][0]);
+                xj[s] = make_pair2(f[0][1], f[1][1]);
+              } else if (PAIRS) {
+                const int u = e / (V / 2), z = 2 * e % V;
+                xi[s * V / 2 + e / 2] = make_pair2(f[u][z], f[u][(z + 2) % V]);
+                xj[s * V / 2 + e / 2] = make_pair2(f[u][z + 1], f[u][(z + 3) % V]);
+              } else {
+                xi[s * V / 2 + e / 2] = make_pair2(f[0][e], f[0][e + 1]);
+                xj[s * V / 2 + e / 2] = make_pair2(f[1][e], f[1][e + 1]);
+              }
+            }
           }
         }
-      for (int o = a.lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float f = rsqrtf(fmaf(sum, a.inv_d, a.eps));
+        fetch(raw[k]);
+        if (left <= 0) continue;  // (a step that fills up, for the whole warp)
+        Pair s2 = mul_pair2(xi[0], xi[0]), t2 = mul_pair2(xj[0], xj[0]);
 #pragma unroll
-      for (int s = 0; s < SLOTS; ++s) {
+        for (int e = 1; e < N; ++e) {
+          s2 = fma_pair2(xi[e], xi[e], s2);
+          t2 = fma_pair2(xj[e], xj[e], t2);
+        }
+        float s0, s1, t0, t1;
+        split_pair2(s2, s0, s1);
+        split_pair2(t2, t0, t1);
+        float sum = (s0 + s1) + (t0 + t1);
+        if constexpr (LANES > 0) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+          for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        } else {
+          for (int o = lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+        const float f = rsqrtf(fmaf(sum, a.inv_d, a.eps));
+        const Pair f2 = make_pair2(f, f);
+        float zi[2 * N], zj[2 * N];
 #pragma unroll
-          for (int e = 0; e < V; ++e) y[s][u][e] = y[s][u][e] * f * w[s][u][e];
+        for (int e = 0; e < N; ++e) {
+          split_pair2(mul_pair2(f2, fma_pair2(xi[e], ca[e], mul_pair2(xj[e], cb[e]))), zi[2 * e], zi[2 * e + 1]);
+          split_pair2(mul_pair2(f2, fma_pair2(xj[e], da[e], mul_pair2(xi[e], db[e]))), zj[2 * e], zj[2 * e + 1]);
+        }
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float *p, *q;
-          if (V > 1 && a.interleaved) {
-            p = e < V / 2 ? &y[s][0][(2 * e) % V] : &y[s][1][(2 * e) % V];
-            q = e < V / 2 ? &y[s][0][(2 * e + 1) % V] : &y[s][1][(2 * e + 1) % V];
-          } else {
-            p = &y[s][0][e];
-            q = &y[s][1][e];
+        for (int s = 0; s < SLOTS; ++s)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            R r;
+            T* t = reinterpret_cast<T*>(&r);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const int z = PAIRS && V > 1 ? s * V + u * (V / 2) + e / 2 : s * V + e;
+              t[e] = narrow<T>((PAIRS && V > 1 ? e & 1 : u) ? zj[z] : zi[z]);
+            }
+            store_if(y + c[s][u], r, live + off[s][u]);
           }
-          const float x0 = *p, x1 = *q;
-          *p = x0 * cs[s][e].x - x1 * cs[s][e].y;
-          *q = x1 * cs[s][e].x + x0 * cs[s][e].y;
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (!live || !on[s][u]) continue;
-          R r;
-          T* t = reinterpret_cast<T*>(&r);
-#pragma unroll
-          for (int e = 0; e < V; ++e) t[e] = narrow<T>(y[s][u][e]);
-          *reinterpret_cast<R*>(yb + h * a.ys[which][2] + c[s][u]) = r;
-        }
+        y += y_stride;
+        left -= rows;
+        live -= rows;
       }
     }
   }
 }
 
-template <typename T>
+template <typename T, bool PAIRS>
 cudaError_t launch_rope(const RopeArgs& a, int v, int blocks, cudaStream_t st) {
   const dim3 g(blocks), t(kRopeWarps * 32);
-  if (v == 8) return launch_pdl(rope_kernel<T, 8, 1>, g, t, 0, st, a);
-  if (v == 4) return launch_pdl(rope_kernel<T, 4, 1>, g, t, 0, st, a);
-  if (v == 2) return launch_pdl(rope_kernel<T, 2, 1>, g, t, 0, st, a);
-  return launch_pdl(rope_kernel<T, 1, 2>, g, t, 0, st, a);
+  if (v == 8 && a.lanes == 8) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 8>, g, t, 0, st, a);
+  if (v == 8 && a.lanes == 4) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 4>, g, t, 0, st, a);
+  if (v == 8) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 0>, g, t, 0, st, a);
+  if (v == 4) return launch_pdl(rope_kernel<T, 4, 1, PAIRS, 0>, g, t, 0, st, a);
+  if (v == 2) return launch_pdl(rope_kernel<T, 2, 1, PAIRS, 0>, g, t, 0, st, a);
+  return launch_pdl(rope_kernel<T, 1, 2, PAIRS, 0>, g, t, 0, st, a);
 }
 
 }  // namespace
@@ -273,17 +411,16 @@ extern "C" int sage_qk_norm_rope(const sage_tensor* q, const sage_tensor* k, con
   while (a.lanes < slots && a.lanes < 32) a.lanes *= 2;
   const int64_t tokens = (int64_t)batch * seqlen;
   // a token's heads are shared by several warps where there are few tokens
-  const int rows = 32 / a.lanes;
-  for (int i = 0; i < 2; ++i) {
-    const int most = (heads[i] + rows - 1) / rows;
-    const int64_t want = (152 * 24 + tokens - 1) / tokens;
-    a.chunks[i] = (int)(want < most ? want : most);
-    if (a.chunks[i] < 1) a.chunks[i] = 1;
-  }
-  a.items = tokens * (a.chunks[0] + a.chunks[1]);
+  const int rows = 32 / a.lanes, most = ((heads_q > heads_kv ? heads_q : heads_kv) + rows - 1) / rows;
+  const int64_t want = (152 * kRopeBlocks * kRopeWarps + tokens - 1) / tokens;
+  a.chunks = (int)(want < most ? want : most);
+  a.items = tokens * a.chunks;
   const int64_t blocks = (a.items + kRopeWarps - 1) / kRopeWarps;
-  const int grid = (int)(blocks < 152 * 3 ? blocks : 152 * 3);
+  const int grid = (int)(blocks < 152 * kRopeBlocks ? blocks : 152 * kRopeBlocks);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == SAGE_F16 ? launch_rope<__half>(a, v, grid, st) : launch_rope<__nv_bfloat16>(a, v, grid, st);
+  const cudaError_t e =
+      dtype == SAGE_F16 ? (a.interleaved ? launch_rope<__half, true>(a, v, grid, st) : launch_rope<__half, false>(a, v, grid, st))
+                        : (a.interleaved ? launch_rope<__nv_bfloat16, true>(a, v, grid, st)
+                                         : launch_rope<__nv_bfloat16, false>(a, v, grid, st));
   return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "norm and rotation");
 }
