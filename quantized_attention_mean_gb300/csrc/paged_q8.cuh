@@ -6,6 +6,7 @@
 #include <cuda_fp8.h>
 
 #include "paged.cuh"
+#include "sm103_ptx.cuh"
 
 namespace sage {
 
@@ -45,16 +46,55 @@ __device__ __forceinline__ float needed_scale(float most) {
   }
   return fmaxf(s, kLeastScale);
 }
-// Code of a value in units of the scale: round to nearest even.
+// Codes of eight values in units of the scale, rounded to nearest even. (int8: the low byte of 3 * 2^22 + u, whose unit is one:
+// u is rounded as by rint. The product that gave u must be rounded before: by __fmul_rn, since a packed product is fused with
+// this addition, which gives other codes near halves. `clamped`: values may lie beyond the codes' range.)
 template <int TYPE>
-__device__ __forceinline__ uint8_t to_code(float u) {
-  if (TYPE == SAGE_S8) return (uint8_t)(int8_t)max(-127, min(127, __float2int_rn(u)));
-  return (uint8_t)__nv_cvt_float_to_fp8(u, __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint2 to_codes(float (&u)[8], bool clamped = false) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float* v = u + 4 * i;
+    if constexpr (TYPE == SAGE_S8) {
+      if (clamped) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fminf(fmaxf(v[e], -127.f), 127.f);
+      }
+      constexpr float kUnit = 12582912.0f;
+      add2(v[0], v[1], v[0], v[1], kUnit, kUnit);
+      add2(v[2], v[3], v[2], v[3], kUnit, kUnit);
+      w[i] = __byte_perm(__byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x0040),
+                         __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x0040), 0x5410);
+    } else {
+      uint16_t lo, hi;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1]), "f"(v[0]));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3]), "f"(v[2]));
+      w[i] = lo | (uint32_t)hi << 16;
+    }
+  }
+  return make_uint2(w[0], w[1]);
 }
+// Four codes as numbers.
 template <int TYPE>
-__device__ __forceinline__ float from_code(uint8_t c) {
-  if (TYPE == SAGE_S8) return (float)(int8_t)c;
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3)));
+__device__ __forceinline__ void from_codes(uint32_t c, float& f0, float& f1, float& f2, float& f3) {
+  if constexpr (TYPE == SAGE_S8) {
+    const uint32_t u = c ^ 0x80808080u;  // code + 128, in the last byte of 2^23 + code + 128
+    constexpr float kBias = 8388736.0f;
+    f0 = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440));
+    f1 = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441));
+    f2 = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442));
+    f3 = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443));
+    add2(f0, f1, f0, f1, -kBias, -kBias);
+    add2(f2, f3, f2, f3, -kBias, -kBias);
+  } else {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(c));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    f0 = a.x; f1 = a.y; f2 = b.x; f3 = b.y;
+  }
 }
 
 }  // namespace sage

@@ -56,13 +56,18 @@ int make_q8_view(const sage_q8_cache* c, int batch, int heads_kv, int head_dim, 
 
 namespace {
 
-// The sequence of row t, the last b with cu[b] <= t (batch: behind the last one).
+// The sequence of row t, the last b with cu[b] <= t (batch: behind the last one): a warp looks at 32 places at a time, so
+// 1024 sequences take two dependent loads where a bisection takes ten.
 __device__ __forceinline__ int sequence_of(const int* cu, int batch, int t) {
-  int lo = 0, hi = batch;
-  while (lo < hi) {
-    const int mid = lo + (hi - lo + 1) / 2;
-    if (__ldg(&cu[mid]) <= t) lo = mid;
-    else hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = batch + 1;  // among lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const bool le = at < n && __ldg(&cu[lo + at]) <= t;
+    const unsigned set = __ballot_sync(0xffffffffu, le);
+    const int last = set ? 31 - __clz(set) : 0;
+    lo += last * step;
+    n = min(step, n - last * step);
   }
   return lo;
 }
@@ -73,127 +78,207 @@ struct AppendArgs {
   const void* x[2]; int64_t x_st[2], x_sh[2];  // k, v: element strides of token and head
   const int* cu;        // [batch + 1] or null: one token per sequence
   int tokens, chunk;    // rows that a CTA looks after
+  int shares;           // CTAs that share a chunk's heads
+  int window;           // slots that are written together: whole blocks of one page
   int in16, out8;       // rows allow 16-byte loads, codes 8-byte stores
   int lanes;            // lanes of a row, 8 channels each: 8 or 16
+  int block_shift;      // log2 of the block, or -1
   int* err;             // or null
 };
 
-// The rows of one block and head: their largest magnitude, the scale, the codes. WARPS warps share a block.
-template <typename T, int TYPE, int WARPS>
-__device__ __forceinline__ void store_block(const AppendArgs& a, int kv, int h, int64_t row0, int rows, int page, int slot0,
-                                            bool joins) {
-  constexpr int kKept = 8;  // rows per lane that stay in registers between the two walks
-  __shared__ float s_most[4];
-  const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
-  const PagedView& c = a.q.c;
-  const int ch = (lane & (a.lanes - 1)) * 8, per = 32 / a.lanes, step = per * WARPS;
-  const int first = warp * per + lane / a.lanes;
-  const bool on = ch < c.d;
-  const T* x = static_cast<const T*>(a.x[kv]) + row0 * a.x_st[kv] + h * a.x_sh[kv];
-  const int64_t xs = a.x_st[kv];
-  uint8_t* base = static_cast<uint8_t*>(kv ? c.v : c.k) + page * (kv ? c.v_sp : c.k_sp) + h * (kv ? c.v_sh : c.k_sh);
-  const int64_t cs = kv ? c.v_st : c.k_st;
-  float* const scales = kv ? a.q.vs : a.q.ks;
-  const int64_t at = scale_at(a.q, page, h, slot0);
-  const int held = slot0 % a.q.block;  // earlier tokens of the block, where it is joined
-  const float was = joins ? scales[at] : 0.f;
-  uint4 kept[kKept];
-  float most = 0.f;
+// A window takes one of three forms. kOne: one block, by a warp. kMany: several small blocks, by a warp, whose rows' largest
+// magnitudes meet in shared memory. kShared: one block, by a CTA.
+enum { kOne, kMany, kShared };
+constexpr int kKept = 8;  // rows of a lane that stay in registers between the two walks over them
+
+// New rows of a window: the first one's token, how many; the page, slot and block of the first; earlier tokens of its block.
+struct Window {
+  int64_t row0;
+  int rows, page, slot0, block0, held;
+};
+
+// Rows of one unit (a head's K or V) for this lane: the first kKept of them.
+template <typename T, int FORM>
+__device__ __forceinline__ void fetch_rows(const AppendArgs& a, const Window& w, int unit, uint4 (&kept)[kKept]) {
+  const int lane = threadIdx.x & 31, ch = (lane & (a.lanes - 1)) * 8, per = 32 / a.lanes;
+  const int kv = unit & 1, h = unit >> 1, step = FORM == kShared ? per * 4 : per;
+  const int first = (FORM == kShared ? (threadIdx.x >> 5) * per : 0) + lane / a.lanes;
+  const T* x = static_cast<const T*>(a.x[kv]) + (w.row0 + first) * a.x_st[kv] + h * a.x_sh[kv];
+  const int64_t jump = step * a.x_st[kv];
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
     kept[i] = make_uint4(0, 0, 0, 0);
-    const int r = first + i * step;
-    if (on && r < rows) kept[i] = load8_raw<T>(x + r * xs, ch, c.d, a.in16);
+    if (ch < a.q.c.d && first + i * step < w.rows) kept[i] = load8_raw<T>(x, ch, a.q.c.d, a.in16);
+    x += jump;
   }
+}
+
+// Largest magnitude of a run of eight, as bit patterns, whose order is that of the magnitudes: a pair of them.
+__device__ __forceinline__ uint32_t largest2(const uint4& raw, uint32_t m) {
+  constexpr uint32_t kAbs = 0x7fff7fffu;
+  m = __vmaxu2(m, raw.x & kAbs);
+  m = __vmaxu2(m, raw.y & kAbs);
+  m = __vmaxu2(m, raw.z & kAbs);
+  return __vmaxu2(m, raw.w & kAbs);
+}
+template <typename T>
+__device__ __forceinline__ float pattern(uint32_t pair) {
+  const uint16_t m = (uint16_t)max(pair & 0xffffu, pair >> 16);
+  return to_f32<T>(*reinterpret_cast<const T*>(&m));
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const uint4& raw, float (&f)[8]) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-  for (int i = 0; i < kKept; ++i) {
-    const T* t = reinterpret_cast<const T*>(&kept[i]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(to_f32<T>(t[e])));
-  }
-  for (int r = first + kKept * step; r < rows; r += step) {
-    float y[8];
-    if (on) {
-      load8<T>(x + r * xs, ch, c.d, a.in16, y);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(y[e]));
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same<T, __half>::value) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    } else {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (WARPS > 1) {
-    __syncthreads();  // (also: every thread has read the old scale)
-    if (lane == 0) s_most[warp] = most;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) most = fmaxf(most, s_most[w]);
-  }
-  const float scale = fmaxf(was, needed_scale<TYPE>(most)), inv = __frcp_rn(scale);
-  __syncwarp();  // (every lane has read the old scale)
-  if (threadIdx.x % (32 * WARPS) == 0) scales[at] = scale;
-  auto put = [&](int slot, const uint8_t (&code)[8]) {
-    uint8_t* d = base + slot * cs + ch;
-    if (a.out8 && ch + 8 <= c.d) {
-      *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(code);
+}
+
+// The largest magnitude of each block, its scale, the codes.
+template <typename T, int TYPE, int FORM>
+__device__ __forceinline__ void store_window(const AppendArgs& a, const Window& w, int unit, uint4 (&kept)[kKept], float* s_most) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const PagedView& c = a.q.c;
+  const int kv = unit & 1, h = unit >> 1;
+  const int ch = (lane & (a.lanes - 1)) * 8, per = 32 / a.lanes, step = FORM == kShared ? per * 4 : per;
+  const int first = (FORM == kShared ? warp * per : 0) + lane / a.lanes;
+  const bool on = ch < c.d;
+  const T* x = static_cast<const T*>(a.x[kv]) + w.row0 * a.x_st[kv] + h * a.x_sh[kv];
+  const int64_t xs = a.x_st[kv], cs = kv ? c.v_st : c.k_st;
+  uint8_t* base = static_cast<uint8_t*>(kv ? c.v : c.k) + w.page * (kv ? c.v_sp : c.k_sp) + h * (kv ? c.v_sh : c.k_sh) + ch;
+  float* const scales = (kv ? a.q.vs : a.q.ks) + ((int64_t)w.page * c.hkv + h) * a.q.blocks;
+  const int block0 = w.block0;
+  const float was = w.held ? scales[block0] : 0.f;
+  auto put = [&](uint8_t* d, const uint2& code) {
+    if (a.out8) {
+      *reinterpret_cast<uint2*>(d) = code;
     } else {
+      const uint8_t* b = reinterpret_cast<const uint8_t*>(&code);
       for (int e = 0; e < 8; ++e)
-        if (ch + e < c.d) d[e] = code[e];
+        if (ch + e < c.d) d[e] = b[e];
     }
   };
-  if (joins && scale > was) {
+  uint8_t* to = base + (int64_t)(w.slot0 + first) * cs;  // this lane's next row
+  const int64_t hop = step * cs;
+  auto write = [&](const uint4& raw, float inv) {
+    float u[8];
+    widen8<T>(raw, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = __fmul_rn(u[e], inv);
+    put(to, to_codes<TYPE>(u));
+  };
+  // the earlier codes of the first block, where its scale has grown
+  auto again = [&](float scale) {
+    if (!w.held || !(scale > was)) return;
     const float f = __fdiv_rn(was, scale);
-    for (int r = first; r < held; r += step) {
+    for (int r = first; r < w.held; r += step) {
       if (!on) break;
-      const int slot = slot0 - held + r;
-      const uint8_t* s = base + slot * cs + ch;
+      uint8_t* s = base + (int64_t)(w.slot0 - w.held + r) * cs;
       alignas(8) uint8_t code[8];
-      if (a.out8 && ch + 8 <= c.d) {
+      if (a.out8) {
         *reinterpret_cast<uint2*>(code) = *reinterpret_cast<const uint2*>(s);
       } else {
         for (int e = 0; e < 8; ++e) code[e] = ch + e < c.d ? s[e] : 0;
       }
+      float u[8];
+      from_codes<TYPE>(reinterpret_cast<const uint32_t*>(code)[0], u[0], u[1], u[2], u[3]);
+      from_codes<TYPE>(reinterpret_cast<const uint32_t*>(code)[1], u[4], u[5], u[6], u[7]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) code[e] = to_code<TYPE>(from_code<TYPE>(code[e]) * f);
-      put(slot, code);
+      for (int e = 0; e < 8; ++e) u[e] = __fmul_rn(u[e], f);
+      put(s, to_codes<TYPE>(u, true));
     }
-  }
-  auto write = [&](int r, const float (&y)[8]) {
-    alignas(8) uint8_t code[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) code[e] = to_code<TYPE>(y[e] * inv);
-    put(slot0 + r, code);
   };
+  if constexpr (FORM == kMany) {
+    // a row's largest magnitude, then each block's over its rows
 #pragma unroll
-  for (int i = 0; i < kKept; ++i) {
-    const int r = first + i * step;
-    if (!on || r >= rows) continue;
-    const T* t = reinterpret_cast<const T*>(&kept[i]);
-    float y[8];
+    for (int i = 0; i < kKept; ++i) {
+      uint32_t m = largest2(kept[i], 0);
+      for (int o = a.lanes / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if ((lane & (a.lanes - 1)) == 0) s_most[first + i * step] = pattern<T>(m);
+    }
+    __syncwarp();
+    auto scale_of = [&](int block) {  // of the window
+      float m = 0.f;
+      const int end = min(w.rows, (block + 1) * a.q.block - w.held);
+      for (int r = max(0, block * a.q.block - w.held); r < end; ++r) m = fmaxf(m, s_most[r]);
+      return fmaxf(block == 0 ? was : 0.f, needed_scale<TYPE>(m));
+    };
+    if (w.held) again(scale_of(0));
+    int last = -1;
+    float scale = 0.f, inv = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = to_f32<T>(t[e]);
-    write(r, y);
-  }
-  for (int r = first + kKept * step; r < rows; r += step) {
-    if (!on) break;
-    float y[8];
-    load8<T>(x + r * xs, ch, c.d, a.in16, y);
-    write(r, y);
+    for (int i = 0; i < kKept; ++i) {
+      const int r = first + i * step, block = a.block_shift >= 0 ? (w.held + r) >> a.block_shift : (w.held + r) / a.q.block;
+      if (r >= w.rows) continue;
+      if (block != last) {
+        scale = scale_of(block);
+        inv = __frcp_rn(scale);
+        last = block;
+      }
+      if (on) write(kept[i], inv);
+      to += hop;
+    }
+    __syncwarp();  // (every lane has read the old scale and the magnitudes)
+    const int blocks = (w.held + w.rows + a.q.block - 1) / a.q.block;
+    if (lane < blocks) scales[block0 + lane] = scale_of(lane);
+    __syncwarp();
+  } else {
+    uint32_t pair = 0;
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) pair = largest2(kept[i], pair);
+    for (int r = first + kKept * step; r < w.rows; r += step)
+      if (on) pair = largest2(load8_raw<T>(x + r * xs, ch, c.d, a.in16), pair);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) pair = __vmaxu2(pair, __shfl_xor_sync(0xffffffffu, pair, o));
+    float most = pattern<T>(pair);
+    if (FORM == kShared) {
+      __syncthreads();  // (also: every thread has read the old scale)
+      if (lane == 0) s_most[warp] = most;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) most = fmaxf(most, s_most[i]);
+    }
+    const float scale = fmaxf(was, needed_scale<TYPE>(most)), inv = __frcp_rn(scale);
+    __syncwarp();  // (every lane has read the old scale)
+    if (FORM == kShared ? threadIdx.x == 0 : lane == 0) scales[block0] = scale;
+    again(scale);
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+      if (on && first + i * step < w.rows) write(kept[i], inv);
+      to += hop;
+    }
+    for (int r = first + kKept * step; r < w.rows; r += step) {
+      if (on) write(load8_raw<T>(x + r * xs, ch, c.d, a.in16), inv);
+      to += hop;
+    }
   }
 }
 
-// CTA (x, y): the blocks whose first new token lies in rows [x chunk, (x + 1) chunk), for one of the heads' K or V
-// (WARPS 4: the CTA shares a block; 1: each of its four warps takes another head or side).
-template <typename T, int WARPS>
-__global__ void __launch_bounds__(128) append_q8_kernel(const AppendArgs a) {
+// CTA (x, y) of line x * shares + y: the windows whose first new token lies in rows [x chunk, (x + 1) chunk), for the y-th
+// share of the heads' K and V (kShared: by the whole CTA, otherwise by a warp each). DRAM bounds it for prompts, which many
+// resident warps keep busy: fetching the next head's rows while one is scaled took twice the registers and was slower.
+template <typename T, int FORM>
+__global__ void __launch_bounds__(128, 7) append_q8_kernel(const AppendArgs a) {
+  __shared__ float s_most[4][32];
   const PagedView& c = a.q.c;
-  const int unit = WARPS == 4 ? blockIdx.y : blockIdx.y * 4 + (threadIdx.x >> 5);
-  const int h = unit >> 1, kv = unit & 1;
+  const int warp = threadIdx.x >> 5, units = 2 * c.hkv;
+  const int share = blockIdx.x % a.shares;  // (CTAs of one window run side by side: they read the same token rows)
+  const int64_t place = blockIdx.x / a.shares;
+  const int unit0 = FORM == kShared ? share : share * 4 + warp, unit_step = FORM == kShared ? a.shares : a.shares * 4;
   pdl_wait();
   pdl_trigger();
-  if (h >= c.hkv) return;  // (a whole warp, or no thread of the CTA)
-  const bool tells = a.err && unit == 0 && (threadIdx.x & 31) == 0 && (WARPS == 1 || threadIdx.x == 0);
-  const int64_t t_end = min((int64_t)a.tokens, ((int64_t)blockIdx.x + 1) * a.chunk);
-  int64_t t = (int64_t)blockIdx.x * a.chunk;
+  if (unit0 >= units) return;  // (a whole warp, or no thread of the CTA)
+  const bool tells = a.err && unit0 == 0 && (threadIdx.x & 31) == 0 && (FORM != kShared || threadIdx.x == 0);
+  const int64_t t_end = min((int64_t)a.tokens, (place + 1) * a.chunk);
+  int64_t t = place * a.chunk;
   int b = a.cu ? sequence_of(a.cu, c.batch, (int)t) : (int)t;
   while (t < t_end) {
     int64_t first = t, end = t + 1;
@@ -208,26 +293,27 @@ __global__ void __launch_bounds__(128) append_q8_kernel(const AppendArgs a) {
     const int len = __ldg(&c.lens[b]);
     const int64_t room = (int64_t)c.max_pages * c.page_size;
     const int64_t slot = (int64_t)len + t - first;
+    int64_t next = end;                      // (without a place: the rest of this sequence)
     if (len < 0 || slot >= room) {
       if (tells) record_error(a.err, kDevSeqlens);
-      t = end;                               // the rest of this sequence
-      if (a.cu) ++b;
-      else b = (int)t;
-      continue;
-    }
-    const int in = (int)(slot % a.q.block);
-    int64_t next = min(end, t + a.q.block - in);
-    if (t == first || in == 0) {             // the first new token of its block
-      const int i = (int)(slot / c.page_size), s0 = (int)(slot - (int64_t)i * c.page_size);
-      const int page = __ldg(&c.table[b * c.table_stride + i]);
-      if (page < 0 || page >= c.num_pages) {
-        if (tells) record_error(a.err, kDevPage);
-      } else if (kv == 0) {
-        if (a.q.k_type == SAGE_S8) store_block<T, SAGE_S8, WARPS>(a, 0, h, t, (int)(next - t), page, s0, in != 0);
-        else store_block<T, SAGE_E4M3, WARPS>(a, 0, h, t, (int)(next - t), page, s0, in != 0);
-      } else {
-        if (a.q.v_type == SAGE_S8) store_block<T, SAGE_S8, WARPS>(a, 1, h, t, (int)(next - t), page, s0, in != 0);
-        else store_block<T, SAGE_E4M3, WARPS>(a, 1, h, t, (int)(next - t), page, s0, in != 0);
+    } else {
+      const int i = (int)(slot / c.page_size), s0 = (int)(slot - (int64_t)i * c.page_size), in = s0 % a.window;
+      next = min(end, t + min(a.window - in, c.page_size - s0));
+      if (t == first || in == 0) {           // the first new token of its window
+        const int page = __ldg(&c.table[b * c.table_stride + i]);
+        if (page < 0 || page >= c.num_pages) {
+          if (tells) record_error(a.err, kDevPage);
+        } else {
+          const int block0 = s0 / a.q.block;
+          const Window w{t, (int)(next - t), page, s0, block0, s0 - block0 * a.q.block};
+#pragma unroll 1
+          for (int u = unit0; u < units; u += unit_step) {
+            uint4 kept[kKept];
+            fetch_rows<T, FORM>(a, w, u, kept);
+            if ((u & 1 ? a.q.v_type : a.q.k_type) == SAGE_S8) store_window<T, SAGE_S8, FORM>(a, w, u, kept, s_most[FORM == kShared ? 0 : warp]);
+            else store_window<T, SAGE_E4M3, FORM>(a, w, u, kept, s_most[FORM == kShared ? 0 : warp]);
+          }
+        }
       }
     }
     t = next;
@@ -243,77 +329,124 @@ struct ReadArgs {
   Q8View q;
   void* y[2]; int64_t y_st[2], y_sh[2];
   const int* cu; const int* starts;  // starts: first slot of each sequence, or null (0)
-  int tokens;
+  int tokens, rows;  // rows of a warp: up to 32
   int* err;
 };
 
-template <int TYPE, int V>
-__device__ __forceinline__ void decode(const uint8_t* p, float scale, float (&y)[V]) {
-  alignas(16) uint8_t code[V];
-  if constexpr (V == 16) *reinterpret_cast<uint4*>(code) = __ldg(reinterpret_cast<const uint4*>(p));
-  else if constexpr (V == 8) *reinterpret_cast<uint2*>(code) = __ldg(reinterpret_cast<const uint2*>(p));
-  else code[0] = *p;
-#pragma unroll
-  for (int e = 0; e < V; ++e) y[e] = from_code<TYPE>(code[e]) * scale;
-}
 template <typename T>
-__device__ __forceinline__ T narrow(float x) {
-  if constexpr (std::is_same<T, __half>::value) return __float2half_rn(x);
-  else return __float2bfloat16_rn(x);
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+// Four codes times their scale, in 16 bits.
+template <typename T>
+__device__ __forceinline__ uint2 values4(uint32_t codes, int type, float scale) {
+  float f0, f1, f2, f3;
+  if (type == SAGE_S8) from_codes<SAGE_S8>(codes, f0, f1, f2, f3);
+  else from_codes<SAGE_E4M3>(codes, f0, f1, f2, f3);
+  mul2(f0, f1, f0, f1, scale, scale);
+  mul2(f2, f3, f2, f3, scale, scale);
+  return make_uint2(narrow2<T>(f0, f1), narrow2<T>(f2, f3));
 }
 
-// A warp per row of the result: V codes per lane and access, the heads one after the other.
+// A warp per `rows` rows of K or of V (blockIdx.y): its lanes find the rows' places side by side, then take V codes each, the same
+// channels of row after row. Few registers and many warps, which keep DRAM busy: four rows of two runs in flight in each of half as
+// many warps took 68 us where this takes 52 (41K tokens of 8 heads, head_dim 128).
 template <typename T, int V>
-__global__ void __launch_bounds__(128) read_q8_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(128, 10) read_q8_kernel(const ReadArgs a) {
   const PagedView& c = a.q.c;
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, kv = blockIdx.y;
+  const int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * a.rows;
   pdl_wait();
   pdl_trigger();
-  if (t >= a.tokens) return;
-  const int b = sequence_of(a.cu, c.batch, (int)t);
+  if (t0 >= a.tokens) return;
+  const int n_rows = (int)min((int64_t)a.rows, a.tokens - t0);
   int page = -1, slot = 0;
-  const int first = __ldg(&a.cu[b]);
-  if (a.err && t == 0 && lane == 0 && first != 0) record_error(a.err, kDevSeqlens);
-  if (b < c.batch && first <= t) {
-    const int len = __ldg(&c.lens[b]);
-    const int64_t s = (a.starts ? __ldg(&a.starts[b]) : 0) + t - first;
-    const int64_t room = (int64_t)c.max_pages * c.page_size;
-    if (s < 0 || s >= len || s >= room) {
-      if (a.err && lane == 0) record_error(a.err, kDevSeqlens);
-    } else {
-      const int i = (int)(s / c.page_size);
-      slot = (int)(s - (int64_t)i * c.page_size);
-      page = __ldg(&c.table[b * c.table_stride + i]);
-      if (page < 0 || page >= c.num_pages) {
-        page = -1;
-        if (a.err && lane == 0) record_error(a.err, kDevPage);
+  if (lane < n_rows) {
+    const int t = (int)t0 + lane;
+    int lo = 0, hi = c.batch;  // the last b with cu[b] <= t
+    while (lo < hi) {
+      const int mid = lo + (hi - lo + 1) / 2;
+      if (__ldg(&a.cu[mid]) <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    const int b = lo, first = __ldg(&a.cu[b]);
+    if (a.err && t == 0 && kv == 0 && first != 0) record_error(a.err, kDevSeqlens);
+    if (b < c.batch && first <= t) {
+      const int len = __ldg(&c.lens[b]);
+      const int64_t s = (a.starts ? __ldg(&a.starts[b]) : 0) + (int64_t)t - first;
+      if (s < 0 || s >= len || s >= (int64_t)c.max_pages * c.page_size) {
+        if (a.err && kv == 0) record_error(a.err, kDevSeqlens);
+      } else {
+        const int i = (int)(s / c.page_size);
+        slot = (int)(s - (int64_t)i * c.page_size);
+        page = __ldg(&c.table[b * c.table_stride + i]);
+        if (page < 0 || page >= c.num_pages) {
+          page = -1;
+          if (a.err && kv == 0) record_error(a.err, kDevPage);
+        }
       }
     }
   }
+  const int block = slot / a.q.block, type = kv ? a.q.v_type : a.q.k_type;
+  const int64_t sp = kv ? c.v_sp : c.k_sp, sh = kv ? c.v_sh : c.k_sh, st = kv ? c.v_st : c.k_st;
+  const uint8_t* codes = static_cast<const uint8_t*>(kv ? c.v : c.k);
+  const float* scales = kv ? a.q.vs : a.q.ks;
   const int runs = (c.d + V - 1) / V, n = c.hkv * runs;
-  for (int x = lane; x < 2 * n; x += 32) {
-    const int kv = x >= n, y = x - kv * n, h = y / runs, ch = (y - h * runs) * V;
-    alignas(16) T out[V];
-    if (page >= 0) {
-      const uint8_t* p = static_cast<const uint8_t*>(kv ? c.v : c.k) + page * (kv ? c.v_sp : c.k_sp) + h * (kv ? c.v_sh : c.k_sh) +
-                         slot * (kv ? c.v_st : c.k_st) + ch;
-      const float scale = __ldg((kv ? a.q.vs : a.q.ks) + scale_at(a.q, page, h, slot));
-      float f[V];
-      if ((kv ? a.q.v_type : a.q.k_type) == SAGE_S8) decode<SAGE_S8, V>(p, scale, f);
-      else decode<SAGE_E4M3, V>(p, scale, f);
+  constexpr int kWords = V >= 4 ? V / 4 : 1;
+  for (int x0 = 0; x0 < n; x0 += 64) {
+    // two runs of a row for each lane
+    const uint8_t* src[2];
+    const float* sc[2];
+    T* dst[2];
+    bool on[2];
 #pragma unroll
-      for (int e = 0; e < V; ++e) out[e] = narrow<T>(f[e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) out[e] = T(0.0f);
+    for (int u = 0; u < 2; ++u) {
+      const int x = x0 + 32 * u + lane, h = x / runs, ch = (x - h * runs) * V;
+      on[u] = x < n;
+      src[u] = codes + h * sh + ch;
+      sc[u] = scales + (int64_t)h * a.q.blocks;
+      dst[u] = static_cast<T*>(a.y[kv]) + t0 * a.y_st[kv] + h * a.y_sh[kv] + ch;
     }
-    T* dst = static_cast<T*>(a.y[kv]) + t * a.y_st[kv] + h * a.y_sh[kv] + ch;
-    if constexpr (V >= 8) {
+#pragma unroll 1
+    for (int j = 0; j < n_rows; ++j) {
+      const int pg = __shfl_sync(0xffffffffu, page, j), sl = __shfl_sync(0xffffffffu, slot, j), bl = __shfl_sync(0xffffffffu, block, j);
+      const int64_t at = pg * sp + sl * st, sat = (int64_t)pg * c.hkv * a.q.blocks + bl;
+      uint32_t raw[2][kWords];
+      float scale[2];
 #pragma unroll
-      for (int e = 0; e < V; e += 8) *reinterpret_cast<uint4*>(dst + e) = *reinterpret_cast<const uint4*>(out + e);
-    } else {
-      dst[0] = out[0];
+      for (int u = 0; u < 2; ++u) {
+        scale[u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) raw[u][i] = 0;
+        if (on[u] && pg >= 0) {
+          const uint8_t* p = src[u] + at;
+          scale[u] = __ldg(sc[u] + sat);
+          if constexpr (V == 8) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+            raw[u][0] = w.x; raw[u][1] = w.y;
+          } else {
+            raw[u][0] = *p;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (on[u]) {
+          if constexpr (V == 8) {
+            const uint2 lo = values4<T>(raw[u][0], type, scale[u]), hi = values4<T>(raw[u][1], type, scale[u]);
+            *reinterpret_cast<uint4*>(dst[u]) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          } else {
+            *reinterpret_cast<uint16_t*>(dst[u]) = (uint16_t)values4<T>(raw[u][0], type, scale[u]).x;
+          }
+        }
+        dst[u] += a.y_st[kv];
+      }
     }
   }
 }
@@ -369,25 +502,36 @@ int sage_paged_append_q8(const sage_packed* k, const sage_packed* v, const sage_
   a.cu = cu_seqlens;
   a.tokens = tokens;
   a.in16 = vec;
-  a.out8 = align >= 8;
+  a.out8 = align >= 8;  // (and head_dim a multiple of 8)
   a.lanes = head_dim <= 64 ? 8 : 16;
   a.err = static_cast<int*>(workspace);
-  // a CTA looks after about one block, or one sequence where those are shorter
-  const int mean = cu_seqlens ? (tokens + batch - 1) / batch : 1, most = a.q.block > 16 ? a.q.block : 16;
-  a.chunk = mean < most ? mean : most;
+  // a window: a block, or as many small ones as a warp's registers hold rows of
+  const int hold = kKept * (32 / a.lanes), block = a.q.block;
+  a.block_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (block == 1 << i) a.block_shift = i;
+  const int form = block > hold ? kShared : block > hold / 2 ? kOne : kMany;
+  a.window = form == kMany ? hold / block * block : block;
+  // a CTA looks after about one window, or one sequence where those are shorter
+  const int mean = cu_seqlens ? (tokens + batch - 1) / batch : 1;
+  a.chunk = mean < a.window ? mean : a.window;
   const int64_t chunks = ((int64_t)tokens + a.chunk - 1) / a.chunk;
+  // and its warps after several heads, unless that leaves SMs without work
+  const int most = form == kShared ? 2 * heads_kv : (2 * heads_kv + 3) / 4;
+  const int64_t want = (152 * (form == kShared ? 16 : 32) + chunks - 1) / chunks;
+  a.shares = (int)(want < most ? want : most);
+  if (chunks * a.shares > 0x7fffffffLL) a.shares = 1;
+  const dim3 grid((unsigned)(chunks * a.shares));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (a.err) e = launch_pdl(clear_status_kernel, dim3(1), dim3(1), 0, st, a.err);
-  const bool shared = a.chunk > 16;
-  const dim3 grid((unsigned)chunks, shared ? 2 * heads_kv : (2 * heads_kv + 3) / 4);
   if (e == cudaSuccess) {
-    if (dtype == SAGE_F16)
-      e = shared ? launch_pdl(append_q8_kernel<__half, 4>, grid, dim3(128), 0, st, a)
-                 : launch_pdl(append_q8_kernel<__half, 1>, grid, dim3(128), 0, st, a);
-    else
-      e = shared ? launch_pdl(append_q8_kernel<__nv_bfloat16, 4>, grid, dim3(128), 0, st, a)
-                 : launch_pdl(append_q8_kernel<__nv_bfloat16, 1>, grid, dim3(128), 0, st, a);
+    auto go = [&](auto one, auto many, auto shared) {
+      return launch_pdl(form == kOne ? one : form == kMany ? many : shared, grid, dim3(128), 0, st, a);
+    };
+    e = dtype == SAGE_F16 ? go(append_q8_kernel<__half, kOne>, append_q8_kernel<__half, kMany>, append_q8_kernel<__half, kShared>)
+                          : go(append_q8_kernel<__nv_bfloat16, kOne>, append_q8_kernel<__nv_bfloat16, kMany>,
+                               append_q8_kernel<__nv_bfloat16, kShared>);
   }
   return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "8-bit append");
 }
@@ -422,15 +566,15 @@ int sage_paged_read_q8(const sage_packed* k_out, const sage_packed* v_out, const
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (a.err) e = launch_pdl(clear_status_kernel, dim3(1), dim3(1), 0, st, a.err);
-  const dim3 grid((unsigned)(((int64_t)tokens + 3) / 4));
-  const int v = vec && align >= 16 ? 16 : vec && align >= 8 ? 8 : 1;
+  // rows of a warp: as many as leave some warps for each SM
+  a.rows = tokens / (152 * 16);
+  a.rows = a.rows < 1 ? 1 : a.rows > 4 ? 4 : a.rows;
+  const dim3 grid((unsigned)(((int64_t)tokens + 4 * a.rows - 1) / (4 * a.rows)), 2);
   if (e == cudaSuccess) {
-    auto go = [&](auto k16, auto k8, auto k1) {
-      return launch_pdl(v == 16 ? k16 : v == 8 ? k8 : k1, grid, dim3(128), 0, st, a);
-    };
-    e = dtype == SAGE_F16 ? go(read_q8_kernel<__half, 16>, read_q8_kernel<__half, 8>, read_q8_kernel<__half, 1>)
-                          : go(read_q8_kernel<__nv_bfloat16, 16>, read_q8_kernel<__nv_bfloat16, 8>,
-                               read_q8_kernel<__nv_bfloat16, 1>);
+    const bool wide = vec && align >= 8;
+    auto go = [&](auto k8, auto k1) { return launch_pdl(wide ? k8 : k1, grid, dim3(128), 0, st, a); };
+    e = dtype == SAGE_F16 ? go(read_q8_kernel<__half, 8>, read_q8_kernel<__half, 1>)
+                          : go(read_q8_kernel<__nv_bfloat16, 8>, read_q8_kernel<__nv_bfloat16, 1>);
   }
   return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "8-bit read");
 }
