@@ -190,9 +190,9 @@ struct ReleaseArgs {
   const int* lens; const int* keep;
   int* free_pages; const int* free_count; int capacity;
   int batch, page_size;
-  int* given;      // [batch]: pages of each sequence that go back
+  int* given;      // [batch]: pages of each sequence that go back, or -1 - its error
   int* new_count;
-  int* err;        // or null
+  int* err;
 };
 
 __device__ __forceinline__ bool shrink_of(const ReleaseArgs& a, int b, int& keep, int& have) {
@@ -216,10 +216,7 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const ReleaseArgs a) {
     bad |= pg < 0 || pg >= a.capacity;
   }
   bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) {
-    a.given[b] = ok && !bad ? have - keep : 0;
-    if (a.err && (!ok || bad)) record_error(a.err, ok ? kDevPage : kDevSeqlens);
-  }
+  if (threadIdx.x == 0) a.given[b] = !ok ? -1 - kDevSeqlens : bad ? -1 - kDevPage : have - keep;
 }
 
 // A CTA per sequence: its pages to their places on the stack.
@@ -229,15 +226,11 @@ __global__ void __launch_bounds__(kThreads) push_kernel(const ReleaseArgs a) {
   const int b = blockIdx.x;
   const int said = __ldg(a.free_count);
   const int count = said < 0 ? 0 : said > a.capacity ? a.capacity : said;
-  // (x: the sequences before this one, y: all)
+  // (x: the pages of the sequences before this one)
   Two sum{0, 0};
-  for (int i = threadIdx.x; i < a.batch; i += kThreads) {
-    const int g = a.given[i];
-    sum.y += g;
-    if (i < b) sum.x += g;
-  }
+  for (int i = threadIdx.x; i < b; i += kThreads) sum.x += max(a.given[i], 0);
   sum = block_sum(sum);
-  const int mine = a.given[b];
+  const int mine = max(a.given[b], 0);
   const bool fits = count + sum.x + mine <= a.capacity;
   if (fits && mine > 0) {
     int keep = 0, have = 0;
@@ -245,23 +238,31 @@ __global__ void __launch_bounds__(kThreads) push_kernel(const ReleaseArgs a) {
     for (int i = threadIdx.x; i < mine; i += kThreads)
       a.free_pages[count + sum.x + i] = __ldg(&a.table[(int64_t)b * a.table_stride + keep + i]);
   }
-  if (a.err && threadIdx.x == 0 && (!fits || said != count)) record_error(a.err, kDevSeqlens);
-  // the last sequence that fits says how high the stack is: the first CTA finds it
+  // the last sequence that fits says how high the stack is: the first CTA finds it, and the status of the call
   if (b == 0) {
     __shared__ unsigned long long s_high;
-    if (threadIdx.x == 0) s_high = 0;
+    __shared__ int s_err;
+    if (threadIdx.x == 0) {
+      s_high = 0;
+      s_err = said != count ? kDevSeqlens : 0;
+    }
     __syncthreads();
     long long run = 0;
     for (int i0 = 0; i0 < a.batch; i0 += kThreads) {
-      const int i = i0 + threadIdx.x, g = i < a.batch ? a.given[i] : 0;
+      const int i = i0 + threadIdx.x, got = i < a.batch ? a.given[i] : 0, g = max(got, 0);
       Two all;
       const Two at = block_before({g, 0}, all);
       const long long high = run + at.x + g;
-      if (g > 0 && count + high <= a.capacity) atomicMax(&s_high, (unsigned long long)high);
+      if (got < 0) atomicMax(&s_err, -1 - got);
+      else if (g > 0 && count + high <= a.capacity) atomicMax(&s_high, (unsigned long long)high);
+      else if (g > 0) atomicMax(&s_err, (int)kDevSeqlens);
       run += all.x;
     }
     __syncthreads();
-    if (threadIdx.x == 0) *a.new_count = count + (int)s_high;
+    if (threadIdx.x == 0) {
+      *a.new_count = count + (int)s_high;
+      *a.err = s_err;
+    }
   }
 }
 
@@ -348,6 +349,7 @@ int sage_paged_release(const int32_t* page_table, int64_t table_stride, int max_
                              new_free_count, num_pages, page_size, batch, workspace, workspace_bytes,
                              sage_paged_release_workspace_size(batch));
   if (s != SAGE_OK) return s;
+  if (!workspace && batch > 0) return SAGE_ERR_WORKSPACE;
   if (!sage_device_supported()) return SAGE_ERR_DEVICE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (batch == 0) {
@@ -362,8 +364,7 @@ int sage_paged_release(const int32_t* page_table, int64_t table_stride, int max_
   a.given = reinterpret_cast<int*>(static_cast<char*>(workspace) + SAGE_STATUS_BYTES);
   a.new_count = new_free_count;
   a.err = static_cast<int*>(workspace);
-  cudaError_t e = launch_pdl(clear_kernel, dim3(1), dim3(1), 0, st, a.err);
-  if (e == cudaSuccess) e = launch_pdl(count_kernel, dim3(batch), dim3(kThreads), 0, st, a);
+  cudaError_t e = launch_pdl(count_kernel, dim3(batch), dim3(kThreads), 0, st, a);
   if (e == cudaSuccess) e = launch_pdl(push_kernel, dim3(batch), dim3(kThreads), 0, st, a);
   return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "page release");
 }

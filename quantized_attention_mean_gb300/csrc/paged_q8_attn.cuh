@@ -40,13 +40,16 @@ struct Q8Args {
 cudaError_t launch_q8_decode_64(const Q8Args& p, const CUtensorMap* maps, cudaStream_t st);
 cudaError_t launch_q8_decode_128(const Q8Args& p, const CUtensorMap* maps, cudaStream_t st);
 
-// NH: blocks of eight query heads, the columns of the products. Up to eight heads leave registers for three CTAs per SM
-// with two stages each, more take two CTAs with three stages.
+// NH: blocks of eight query heads, the columns of the products. Up to eight heads, and sixteen of head_dim 64, leave registers
+// for three CTAs per SM with two stages each, sixteen of 128 take two CTAs with three stages (three: 146 us against 119).
 template <int DP, int NH>
 struct Q8Cfg {
-  static constexpr int kPerSm = NH == 1 ? 3 : 2;
+  static constexpr int kPerSm = NH == 1 || DP == 64 ? 3 : 2;
   static constexpr int kRanges = 152 * kPerSm;                // of the line
-  static constexpr int kStages = NH == 1 ? 2 : 3;
+  static constexpr int kStages = kPerSm == 3 ? 2 : 3;
+  // keys of a step, whose scores are in registers: 64 of sixteen heads would need more of those and twice the code (16
+  // sequences of 30K tokens, head_dim 64: 145 us against 132), of eight heads they are faster (104 against 109)
+  static constexpr int kStep = DP == 64 && NH == 1 ? 64 : 32;
   static constexpr int kKeys = DP == 128 ? 32 : 64;           // keys per warp and tile (8 KB of K and V)
   static constexpr int kTile = 4 * kKeys;                     // keys per tile
   static constexpr int kTileBytes = kKeys * DP;               // K or V of one warp's tile
@@ -212,7 +215,7 @@ template <int KT, int VT, int DP, int NH>
 __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
     q8_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Q8Args p) {
   using C = Q8Cfg<DP, NH>;
-  constexpr int S = C::kStages, KS = DP / 16, M = C::kKeys / 16, NP = C::kKeys / 32;
+  constexpr int S = C::kStages, KS = DP / 16, M = C::kStep / 16, NP = C::kKeys / 32;
   constexpr float kHead = 7.0f;  // weights are held at up to 2^(7 + 8), so that the smallest keep their bits in fp16
   constexpr float kLeastLog = -110.0f;  // smaller scales do not lower the frame of the weights, which stays finite
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -438,9 +441,10 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
     }
     cp_async_wait<S - 1>();
     __syncwarp();
-    if (key0 < cu.len) {
+#pragma unroll 1
+    for (int k0 = 0; k0 < C::kKeys && key0 + k0 < cu.len; k0 += C::kStep) {
       // (keys 0-15 at unit u = 0, then at unit 1: other units by exclusive or, which the swizzle is)
-      const uint32_t kb = smem_u32(here) + unit_at<DP>(lane & 15, lane >> 4);
+      const uint32_t kb = smem_u32(here) + k0 * DP + unit_at<DP>(lane & 15, lane >> 4);
       // ---- S^T = K Q^T: 16 keys x 8 heads each
       float s[M][NH][4];
 #pragma unroll
@@ -473,8 +477,8 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
       for (int g = 0; g < M; ++g)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const float ks = sc[g * 16 + b * 8 + r0];
-          sv[g][b] = sc[C::kKeys + g * 16 + b * 8 + r0];
+          const float ks = sc[k0 + g * 16 + b * 8 + r0];
+          sv[g][b] = sc[C::kKeys + k0 + g * 16 + b * 8 + r0];
           most = fmaxf(most, sv[g][b]);
           least = fminf(least, sv[g][b]);
 #pragma unroll
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
             for (int e = 0; e < 4; ++e) s[g][x][e] = tanhf(s[g][x][e]) * cap_out;
       }
       if (a.slopes) {
-        const float d0 = (float)((long long)qpos - (key0 + r0));  // exact below 2^24
+        const float d0 = (float)((long long)qpos - (key0 + k0 + r0));  // exact below 2^24
 #pragma unroll
         for (int g = 0; g < M; ++g)
 #pragma unroll
@@ -503,14 +507,14 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
               for (int e = 0; e < 2; ++e) s[g][x][2 * b + e] = fmaf(-sl[x][e], dist, s[g][x][2 * b + e]);
           }
       }
-      if (key0 + C::kKeys > cu.len) {
+      if (key0 + k0 + C::kStep > cu.len) {
 #pragma unroll
         for (int g = 0; g < M; ++g)
 #pragma unroll
           for (int x = 0; x < NH; ++x)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (key0 + g * 16 + (e >> 1) * 8 + r0 >= cu.len) s[g][x][e] = -INFINITY;
+              if (key0 + k0 + g * 16 + (e >> 1) * 8 + r0 >= cu.len) s[g][x][e] = -INFINITY;
       }
       // largest score t, and largest t + log2 s_v: an upper bound by the largest scale, which where a lane's scales lie
       // within 2^8 is at most so much too large, otherwise exactly

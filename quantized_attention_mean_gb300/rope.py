@@ -15,8 +15,7 @@ F32 = 2  # SAGE_F32
 
 
 def _check_weight(name, w, d, dtype, index):
-    if w is not None and ((w.dtype != dtype and w.dtype != torch.float32) or w.shape != (d,) or w.get_device() != index
-                          or not w.is_contiguous()):
+    if (w.dtype != dtype and w.dtype != torch.float32) or w.shape != (d,) or w.get_device() != index or not w.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{d}] tensor of q's dtype or float32 on q's device")
 
 
@@ -25,7 +24,7 @@ def _view(t, packed, hnd):
     if st[-1] != 1 and t.shape[-1] != 1:
         raise ValueError("the last dimension must be contiguous")
     if packed:
-        return SageView(t.data_ptr(), 0, st[1], st[0]) if hnd else SageView(t.data_ptr(), 0, st[0], st[1])
+        return SageView(t.data_ptr(), 0, st[0], st[1])
     return SageView(t.data_ptr(), st[0], st[1], st[2])
 
 
@@ -53,6 +52,19 @@ def _same(x, y):
     return x.data_ptr() == y.data_ptr() and x.shape == y.shape and x.stride() == y.stride()
 
 
+def _check_outputs(q, k, q_out, k_out, dtype, index):
+    for name, out, t in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if out is not None:
+            if out.shape != t.shape or out.dtype != dtype or out.get_device() != index:
+                raise ValueError(f"{name} must have its input's shape, dtype and device")
+            # rows are read once each, at any time: an output is its own input or lies apart from both
+            for x in (q, k):
+                if not (x is t and _same(out, t)) and not _apart(out, x):
+                    raise ValueError(f"{name} must be its input itself or not overlap an input")
+    if q_out is not None and k_out is not None and not _apart(q_out, k_out):
+        raise ValueError("q_out and k_out must not overlap")
+
+
 def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, tensor_layout="NHD",
                  interleaved=False, q_out=None, k_out=None, stream=None):
     """For each (token, head) row of q and k: ``y = x / sqrt(mean(x²) + eps) · weight``, then the first
@@ -67,29 +79,35 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
     below 1e18), rounded once at the end; angles are taken in 64 bits, exact at any position."""
     if tensor_layout not in LAYOUT:
         raise ValueError("tensor_layout must be 'HND' or 'NHD'")
-    if q.dim() not in (3, 4) or k.dim() != q.dim():
+    shape, other = q.shape, k.shape
+    dims, dtype = len(shape), q.dtype
+    if (dims != 3 and dims != 4) or len(other) != dims:
         raise ValueError("q and k must be packed [tokens, heads, head_dim] or 4-D tensors")
-    if q.dtype not in DTYPE or k.dtype != q.dtype:
+    if dtype not in DTYPE or k.dtype != dtype:
         raise TypeError("q and k must share one dtype, float16 or bfloat16")
-    packed, hnd = q.dim() == 3, tensor_layout == "HND"
+    packed, hnd = dims == 3, tensor_layout == "HND"
     if packed:
         if hnd:
             raise ValueError("packed rows are [tokens, heads, head_dim]: tensor_layout 'NHD'")
-        B, (N, hq, d), (Nk, hkv, dk) = 1, q.shape, k.shape
-        Bk = 1
+        B, Bk, (N, hq, d), (Nk, hkv, dk) = 1, 1, shape, other
+    elif hnd:
+        (B, hq, N, d), (Bk, hkv, Nk, dk) = shape, other
     else:
-        (B, hq, N, d), (Bk, hkv, Nk, dk) = (q.shape, k.shape) if hnd else (
-            (q.shape[0], q.shape[2], q.shape[1], q.shape[3]), (k.shape[0], k.shape[2], k.shape[1], k.shape[3]))
-    if (Bk, Nk, dk) != (B, N, d):
+        (B, N, hq, d), (Bk, Nk, hkv, dk) = shape, other
+    if Bk != B or Nk != N or dk != d:
         raise ValueError("k must have q's tokens and head_dim")
     index = q.get_device()
     if k.get_device() != index:
         raise ValueError("q and k must be on one CUDA device")
-    _check_weight("q_weight", q_weight, d, q.dtype, index)
-    _check_weight("k_weight", k_weight, d, q.dtype, index)
-    w32 = [w.dtype == torch.float32 for w in (q_weight, k_weight) if w is not None]
-    if len(set(w32)) > 1:
-        raise TypeError("q_weight and k_weight must share one dtype")
+    wtype = dtype
+    if q_weight is not None:
+        _check_weight("q_weight", q_weight, d, dtype, index)
+        wtype = q_weight.dtype
+    if k_weight is not None:
+        _check_weight("k_weight", k_weight, d, dtype, index)
+        if q_weight is not None and k_weight.dtype != wtype:
+            raise TypeError("q_weight and k_weight must share one dtype")
+        wtype = k_weight.dtype
     rot = 0
     if inv_freq is not None:
         _check_small("inv_freq", inv_freq, (inv_freq.numel(),), torch.float32, index)
@@ -102,27 +120,21 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
         _check_small("positions", positions, (B, N) if positions.dim() == 2 and not packed else (N,), torch.int32, index)
     if not 0.0 <= eps < float("inf"):
         raise ValueError("eps must be finite and not negative")
-    for name, out, t in (("q_out", q_out, q), ("k_out", k_out, k)):
-        if out is not None:
-            if out.shape != t.shape or out.dtype != t.dtype or out.get_device() != index:
-                raise ValueError(f"{name} must have its input's shape, dtype and device")
-            # rows are read once each, at any time: an output is its own input or lies apart from both
-            for x in (q, k):
-                if not (x is t and _same(out, t)) and not _apart(out, x):
-                    raise ValueError(f"{name} must be its input itself or not overlap an input")
-    if q_out is not None and k_out is not None and not _apart(q_out, k_out):
-        raise ValueError("q_out and k_out must not overlap")
+    if q_out is not None or k_out is not None:
+        _check_outputs(q, k, q_out, k_out, dtype, index)
     if index < 0:
         raise ValueError("q and k must be on a CUDA device")
     with _Launch(index, stream) as on:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty(shape, dtype=dtype, device=q.device)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        views = [_view(t, packed, hnd) for t in (q, k, q_out, k_out)]
-        st = _lib.load().sage_qk_norm_rope(*[byref(v) for v in views], _ptr(positions), by_row, _ptr(inv_freq),
-                                           _ptr(q_weight), _ptr(k_weight), F32 if any(w32) else DTYPE[q.dtype], B, hq, hkv,
-                                           N, d, rot, DTYPE[q.dtype], LAYOUT[tensor_layout], bool(interleaved), eps, on)
+            k_out = torch.empty(other, dtype=dtype, device=q.device)
+        code = DTYPE[dtype]
+        st = _lib.load().sage_qk_norm_rope(byref(_view(q, packed, hnd)), byref(_view(k, packed, hnd)),
+                                           byref(_view(q_out, packed, hnd)), byref(_view(k_out, packed, hnd)), _ptr(positions),
+                                           by_row, _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight),
+                                           code if wtype == dtype else F32, B, hq, hkv, N, d, rot, code, LAYOUT[tensor_layout],
+                                           bool(interleaved), eps, on)
     if st:
         raise SageError(st, "qk_norm_rope")
     return q_out, k_out
