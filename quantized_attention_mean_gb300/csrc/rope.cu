@@ -31,7 +31,7 @@ struct RopeArgs {
   const float* freq;
   int heads[2], chunks;      // chunks: warps that share a token's heads
   int batch, n, d, rot;
-  int interleaved, w32, lanes;  // lanes of a row: a power of two
+  int interleaved, w32, lanes;  // lanes of a row: a power of two, or where more rows fit a warp as many as it has slots
   int64_t items;
   float eps, inv_d;
 };
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
   }
   __syncthreads();
   const int lanes = LANES ? LANES : a.lanes;
-  const int sub = lane & (lanes - 1), row = lane / lanes, rows = 32 / lanes;
+  const int sub = lane % lanes, row = lane / lanes, rows = 32 / lanes;  // (lanes of no row: 32 is no multiple of five)
   int c[SLOTS][2];
   bool on[SLOTS][2];
 #pragma unroll
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s)
 #pragma unroll
-    for (int u = 0; u < 2; ++u) off[s][u] = on[s][u] ? 0 : -(1 << 30);
+    for (int u = 0; u < 2; ++u) off[s][u] = on[s][u] && row < rows ? 0 : -(1 << 30);
   R raw[kAhead][SLOTS][2];  // (runs behind the row stay zero)
 #pragma unroll
   for (int k = 0; k < kAhead; ++k)
@@ -178,9 +178,17 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
     for (int s = 0; s < SLOTS; ++s) raw[k][s][0] = raw[k][s][1] = R{};
 
   for (int64_t item = (int64_t)blockIdx.x * kRopeWarps + warp; item < a.items; item += (int64_t)gridDim.x * kRopeWarps) {
-    const int64_t token = a.chunks == 1 ? item : item / a.chunks;
-    const int chunk = (int)(item - token * a.chunks);
-    const int b = a.batch == 1 ? 0 : (int)(token / a.n), i = (int)(token - (int64_t)b * a.n);
+    int64_t token = item;
+    int chunk = 0, b = 0;
+    if (a.items <= 0x7fffffff) {  // (32-bit divisions)
+      if (a.chunks > 1) token = (int)item / a.chunks;
+      if (a.batch > 1) b = (int)token / a.n;
+    } else {
+      token = item / a.chunks;
+      b = (int)(token / a.n);
+    }
+    chunk = (int)(item - token * a.chunks);
+    const int i = (int)(token - (int64_t)b * a.n);
     // steps: those of q's heads, filled up to a multiple of kAhead, then k's
     const int hq0 = (int)((int64_t)a.heads[0] * chunk / a.chunks), nq = (int)((int64_t)a.heads[0] * (chunk + 1) / a.chunks) - hq0;
     const int hk0 = (int)((int64_t)a.heads[1] * chunk / a.chunks), nk = (int)((int64_t)a.heads[1] * (chunk + 1) / a.chunks) - hk0;
@@ -296,11 +304,17 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
         split_pair2(s2, s0, s1);
         split_pair2(t2, t0, t1);
         float sum = (s0 + s1) + (t0 + t1);
-        if constexpr (LANES > 0) {
+        if (LANES > 0 ? (LANES & (LANES - 1)) == 0 : (lanes & (lanes - 1)) == 0) {
 #pragma unroll
-          for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          for (int o = 16; o > 0; o >>= 1)
+            if (o < lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         } else {
-          for (int o = lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          // in the order of the lanes, so that all of a row get the same
+          float all = 0.f;
+#pragma unroll
+          for (int o = 0; o < (LANES > 0 ? LANES : 16); ++o)
+            if (o < lanes) all += __shfl_sync(0xffffffffu, sum, (row * lanes + o) & 31);
+          sum = all;
         }
         const float f = rsqrtf(fmaf(sum, a.inv_d, a.eps));
         const Pair f2 = make_pair2(f, f);
@@ -335,6 +349,8 @@ template <typename T, bool PAIRS>
 cudaError_t launch_rope(const RopeArgs& a, int v, int blocks, cudaStream_t st) {
   const dim3 g(blocks), t(kRopeWarps * 32);
   if (v == 8 && a.lanes == 8) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 8>, g, t, 0, st, a);
+  if (v == 8 && a.lanes == 5) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 5>, g, t, 0, st, a);
+  if (v == 8 && a.lanes == 6) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 6>, g, t, 0, st, a);
   if (v == 8 && a.lanes == 4) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 4>, g, t, 0, st, a);
   if (v == 8) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 0>, g, t, 0, st, a);
   if (v == 4) return launch_pdl(rope_kernel<T, 4, 1, PAIRS, 0>, g, t, 0, st, a);
@@ -409,6 +425,7 @@ extern "C" int sage_qk_norm_rope(const sage_tensor* q, const sage_tensor* k, con
   const int slots = turned + (rest + 2 * v - 1) / (2 * v);
   a.lanes = 1;
   while (a.lanes < slots && a.lanes < 32) a.lanes *= 2;
+  if (slots < 16 && 32 / slots > 32 / a.lanes) a.lanes = slots;
   const int64_t tokens = (int64_t)batch * seqlen;
   // a token's heads are shared by several warps where there are few tokens
   const int rows = 32 / a.lanes, most = ((heads_q > heads_kv ? heads_q : heads_kv) + rows - 1) / rows;
