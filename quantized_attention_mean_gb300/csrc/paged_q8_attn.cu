@@ -85,6 +85,9 @@ int sage_paged_attn_q8(const sage_packed* q, const sage_q8_cache* cache, const s
   a.o = out->data; a.o_sb = out->stride_token; a.o_sh = out->stride_head;
   p.q4 = reinterpret_cast<uintptr_t>(q->data) % 8 == 0 && head_dim % 4 == 0 && (batch == 1 || a.q_sb % 4 == 0) &&
          (heads_q == 1 || a.q_sh % 4 == 0);
+  const int run = (head_dim <= 64 ? 64 : 128) / 16;
+  p.o_run = reinterpret_cast<uintptr_t>(out->data) % (2 * run) == 0 && (batch == 1 || a.o_sb % run == 0) &&
+            (heads_q == 1 || a.o_sh % run == 0);
   a.lse = lse;
   a.slopes = slopes;
   a.q_pos = q_positions;

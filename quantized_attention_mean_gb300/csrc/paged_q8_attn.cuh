@@ -33,6 +33,7 @@ struct Q8Args {
   int unit;      // bytes of one copy where rows do not come by TMA: 16, 8, 4, or 1 (plain loads)
   int bf16;      // type of q and out
   int q4;        // q allows accesses of four channels
+  int o_run;     // out allows accesses of dp / 16 channels
   int cluster;   // form: clusters, or the line
   int k_type, v_type;
 };
@@ -55,8 +56,7 @@ struct Q8Cfg {
   static constexpr int kTileBytes = kKeys * DP;               // K or V of one warp's tile
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes;
-  static constexpr int kOffMerge = 4 * kWarpBytes;            // one warp's accumulators of eight heads
-  static constexpr int kOffScale = kOffMerge + (DP / 16) * 32 * 16;
+  static constexpr int kOffScale = 4 * kWarpBytes;
   static constexpr int kOffMl = kOffScale + 4 * kStages * 2 * kKeys * 4;
   static constexpr int kOffBar = kOffMl + 4 * 16 * 4 * 4;
   static constexpr int kSmem = kOffBar + 4 * kStages * 8;
@@ -161,46 +161,62 @@ __device__ __forceinline__ void load_q8_stage(const Q8Args& p, const CUtensorMap
     }
     return;
   }
+  // rows' places, of keys lane, lane + 32, ..., which the lanes that copy a row ask for
   const uint8_t* kb = static_cast<const uint8_t*>(a.c.k) + h * a.c.k_sh;
   const uint8_t* vb = static_cast<const uint8_t*>(a.c.v) + h * a.c.v_sh;
-  constexpr int kUnits = DP / 16, kRowsPer = 32 / kUnits;
-  const int c = lane % kUnits;
-#pragma unroll 1
-  for (int i = 0; i < C::kKeys / kRowsPer; ++i) {
-    const int r = i * kRowsPer + lane / kUnits;
-    int pg = -1, sl = 0;
+  long long ko[N], vo[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int x = __shfl_sync(0xffffffffu, page[n], r & 31), y = __shfl_sync(0xffffffffu, slot[n], r & 31);
-      if (n == r >> 5) { pg = x; sl = y; }
+  for (int i = 0; i < N; ++i) {
+    ko[i] = page[i] >= 0 ? page[i] * a.c.k_sp + slot[i] * a.c.k_st : -1;
+    vo[i] = page[i] >= 0 ? page[i] * a.c.v_sp + slot[i] * a.c.v_st : -1;
+  }
+  auto copy = [&](auto unit) {
+    // a lane takes 16 bytes of a row, in copies of U
+    constexpr int U = decltype(unit)::value, kUnits = DP / 16, kRowsPer = 32 / kUnits;
+    const int c = lane % kUnits, r0 = lane / kUnits, left = a.c.d - c * 16;
+#pragma unroll 2
+    for (int i = 0; i < C::kKeys / kRowsPer; ++i) {
+      const int r = i * kRowsPer + r0;
+      long long kr = __shfl_sync(0xffffffffu, ko[0], r & 31), vr = __shfl_sync(0xffffffffu, vo[0], r & 31);
+      if (N > 1 && i * kRowsPer >= 32) {
+        kr = __shfl_sync(0xffffffffu, ko[N - 1], r & 31);
+        vr = __shfl_sync(0xffffffffu, vo[N - 1], r & 31);
+      }
+      const int n = kr >= 0 ? left : 0;
+      const uint32_t dst = base + unit_at<DP>(r, c);
+      const uint8_t *ks = n > 0 ? kb + kr + c * 16 : kb, *vs = n > 0 ? vb + vr + c * 16 : vb;
+#pragma unroll
+      for (int e = 0; e < 16; e += U) {
+        const int bytes = n > e ? U : 0;
+        const uint8_t *kf = bytes ? ks + e : kb, *vf = bytes ? vs + e : vb;
+        if constexpr (U == 16) {
+          cp_async16(dst, kf, bytes);
+          cp_async16(dst + C::kTileBytes, vf, bytes);
+        } else {
+          cp_async_small<U>(dst + e, kf, bytes);
+          cp_async_small<U>(dst + C::kTileBytes + e, vf, bytes);
+        }
+      }
     }
-    const int left = pg >= 0 ? min(16, a.c.d - c * 16) : 0;  // codes of this unit that are there
-    const int off = unit_at<DP>(r, c);
-    const uint8_t* ks = left > 0 ? kb + pg * a.c.k_sp + sl * a.c.k_st + c * 16 : kb;
-    const uint8_t* vs = left > 0 ? vb + pg * a.c.v_sp + sl * a.c.v_st + c * 16 : vb;
-    const uint32_t kd = base + off, vd = base + C::kTileBytes + off;
-    if (p.unit == 16) {
-      cp_async16(kd, ks, left > 0 ? 16 : 0);
-      cp_async16(vd, vs, left > 0 ? 16 : 0);
-    } else if (p.unit == 8) {
-#pragma unroll
-      for (int e = 0; e < 16; e += 8) {
-        const int n = left > e ? 8 : 0;
-        cp_async_small<8>(kd + e, n ? ks + e : kb, n);
-        cp_async_small<8>(vd + e, n ? vs + e : vb, n);
-      }
-    } else if (p.unit == 4) {
-#pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        const int n = left > e ? 4 : 0;
-        cp_async_small<4>(kd + e, n ? ks + e : kb, n);
-        cp_async_small<4>(vd + e, n ? vs + e : vb, n);
-      }
-    } else {
+  };
+  if (p.unit == 16) copy(std::integral_constant<int, 16>{});
+  else if (p.unit == 8) copy(std::integral_constant<int, 8>{});
+  else if (p.unit == 4) copy(std::integral_constant<int, 4>{});
+  else {
+    // byte by byte: a row takes several turns of the warp
 #pragma unroll 1
-      for (int e = 0; e < 16; ++e) {
-        stage[off + e] = e < left ? ks[e] : 0;
-        stage[C::kTileBytes + off + e] = e < left ? vs[e] : 0;
+    for (int r = 0; r < C::kKeys; ++r) {
+      long long kr = __shfl_sync(0xffffffffu, ko[0], r & 31), vr = __shfl_sync(0xffffffffu, vo[0], r & 31);
+      if (N > 1 && r >= 32) {
+        kr = __shfl_sync(0xffffffffu, ko[N - 1], r & 31);
+        vr = __shfl_sync(0xffffffffu, vo[N - 1], r & 31);
+      }
+#pragma unroll
+      for (int c = lane; c < DP; c += 32) {
+        const bool in = kr >= 0 && c < a.c.d;
+        const int off = unit_at<DP>(r, c / 16) + c % 16;
+        stage[off] = in ? kb[kr + c] : 0;
+        stage[C::kTileBytes + off] = in ? vb[vr + c] : 0;
       }
     }
   }
@@ -209,6 +225,23 @@ __device__ __forceinline__ void load_q8_stage(const Q8Args& p, const CUtensorMap
 __device__ __forceinline__ void store_out(const Q8Args& p, int64_t at, float x) {
   if (p.bf16) static_cast<__nv_bfloat16*>(p.a.o)[at] = __float2bfloat16_rn(x);
   else static_cast<__half*>(p.a.o)[at] = __float2half_rn(x);
+}
+
+// A run of a row's channels, of which `left` are there, times f.
+template <int N>
+__device__ __forceinline__ void store_run(const Q8Args& p, int64_t at, int left, const float (&y)[N], float f) {
+  if (p.o_run && left >= N) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N; i += 2) w[i / 2] = p.bf16 ? pack2<__nv_bfloat16>(y[i] * f, y[i + 1] * f) : pack2<__half>(y[i] * f, y[i + 1] * f);
+    void* to = static_cast<uint16_t*>(p.a.o) + at;
+    if constexpr (N == 8) *static_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *static_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < left) store_out(p, at + i, y[i] * f);
+  }
 }
 
 template <int KT, int VT, int DP, int NH>
@@ -227,7 +260,6 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
   const int heads = a.c.hkv / side * a.row_blocks;
   uint8_t* const ring = sm + warp * C::kWarpBytes;
   float* const scales = reinterpret_cast<float*>(sm + C::kOffScale) + warp * S * 2 * C::kKeys;
-  float4* const merge = reinterpret_cast<float4*>(sm + C::kOffMerge);
   float4* const ml = reinterpret_cast<float4*>(sm + C::kOffMl);  // [warp][row]: m, l, F
   const uint32_t bars = smem_u32(sm + C::kOffBar) + warp * S * 8;
   if (lane < S) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + lane * 8) : "memory");
@@ -625,7 +657,10 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
       ++stage;
     }
     if (!p.cluster && (cu.tile + 1 == cu.tiles || left == 1)) {
-      // ---- merge the warps: sums of a head over its eight lanes, then over the warps
+      // ---- merge the warps: sums of a head over its eight lanes; each warp's accumulator goes where its last tile was,
+      // then every thread sums a run of channels of one head's row over the warps, in their order
+      constexpr int P = DP + 8, kRun = DP / 16;  // (the pitch takes the rows of a store to other banks)
+      const int past = (stage == 0 ? S - 1 : stage - 1) * C::kStageBytes;
 #pragma unroll
       for (int x = 0; x < NH; ++x)
 #pragma unroll
@@ -634,80 +669,56 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
           for (int w = 4; w < 32; w <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], w);
           if (r0 == 0) ml[warp * kRows + x * 8 + 2 * j + e] = make_float4(m[x][e], l[x][e], F[x][e], 0.f);
         }
-      __syncthreads();
-      float Mx[NH][2], L[NH][2], g[NH][2];  // of the head's warps; from F's frame to m's
+      // the whole (sequence, head) in this range: the result; a part of it: to the workspace
+      const bool whole = tile0 == 0 && cu.tile + 1 == cu.tiles;
+      const int hg = a.row_blocks == 1 ? cu.h : cu.h / a.row_blocks, rb = cu.h - hg * a.row_blocks;
+      float* const mine = reinterpret_cast<float*>(ring + past);
+      const int at_row = threadIdx.x >> 4, c = (threadIdx.x & 15) * kRun;
 #pragma unroll
-      for (int x = 0; x < NH; ++x)
+      for (int x = 0; x < NH; ++x) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float4* at = ml + sub * kRows + x * 8 + 2 * j + e;
-          float mm = -INFINITY, ff = -INFINITY, ll = 0.f;
-          for (int w = 0; w < kWarps; w += side) {
-            mm = fmaxf(mm, at[w * kRows].x);
-            ff = fmaxf(ff, at[w * kRows].z);
-          }
-          const float mu = mm == -INFINITY ? 0.f : mm, fu = ff == -INFINITY ? 0.f : ff;
-          for (int w = 0; w < kWarps; w += side) ll += at[w * kRows].y * ex2_approx(at[w * kRows].x - mu);
-          const float f = ex2_approx(F[x][e] - fu);
+        for (int u = 0; u < KS; ++u)
 #pragma unroll
-          for (int u = 0; u < KS; ++u) {
-            o[u][x][e] *= f;
-            o[u][x][2 + e] *= f;
-          }
-          Mx[x][e] = mm;
-          L[x][e] = ll;
-          g[x][e] = ex2_approx(ff - mu);
-        }
-      // added to the head's first warp's in their order, eight heads at a time
-#pragma unroll
-      for (int x = 0; x < NH; ++x)
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float2*>(mine + (2 * j + e) * P + u * 16 + 2 * r0) = make_float2(o[u][x][e], o[u][x][2 + e]);
+        __syncthreads();
+        const int r = x * 8 + at_row;
+        if (r < rows) {
 #pragma unroll 1
-        for (int w = side; w < kWarps; ++w) {
-          if (warp == w) {
+          for (int t = 0; t < side; ++t) {
+            const float4* st = ml + t * kRows + r;
+            float mm = -INFINITY, ff = -INFINITY, ll = 0.f, y[kRun];
+            for (int w = 0; w < kWarps; w += side) {
+              mm = fmaxf(mm, st[w * kRows].x);
+              ff = fmaxf(ff, st[w * kRows].z);
+            }
+            const float mu = mm == -INFINITY ? 0.f : mm, fu = ff == -INFINITY ? 0.f : ff;
 #pragma unroll
-            for (int u = 0; u < KS; ++u) merge[u * 32 + lane] = make_float4(o[u][x][0], o[u][x][1], o[u][x][2], o[u][x][3]);
-          }
-          __syncthreads();
-          if (warp == (w & (side - 1))) {
+            for (int i = 0; i < kRun; ++i) y[i] = 0.f;
+            for (int w = 0; w < kWarps; w += side) {
+              ll += st[w * kRows].y * ex2_approx(st[w * kRows].x - mu);
+              const float f = ex2_approx(st[w * kRows].z - fu);
+              const float* from = reinterpret_cast<const float*>(sm + (t + w) * C::kWarpBytes + past) + at_row * P + c;
 #pragma unroll
-            for (int u = 0; u < KS; ++u) {
-              const float4 y = merge[u * 32 + lane];
-              o[u][x][0] += y.x; o[u][x][1] += y.y; o[u][x][2] += y.z; o[u][x][3] += y.w;
+              for (int i = 0; i < kRun; ++i) y[i] = fmaf(f, from[i], y[i]);
+            }
+            const float g = ex2_approx(ff - mu), f = whole ? (ll != 0.f ? g / ll : 0.f) : g;
+            const int row = (hg * side + t) * a.group + rb * kRows + r;
+            if (whole) {
+              store_run<kRun>(p, cu.b * a.o_sb + (int64_t)row * a.o_sh + c, a.c.d - c, y, f);
+              if (c == 0 && a.lse) a.lse[(int64_t)cu.b * a.hq + row] = ll != 0.f ? (mm + log2f(ll)) * kLn2F : -INFINITY;
+            } else {
+              const int64_t at = (((int64_t)me * 2 + (pieces > 0)) * side + t) * a.part_rows + r;
+#pragma unroll
+              for (int i = 0; i < kRun; i += 4)
+                *reinterpret_cast<float4*>(a.part_o + at * DP + c + i) = make_float4(y[i] * f, y[i + 1] * f, y[i + 2] * f, y[i + 3] * f);
+              if (c == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(mm, ll);
             }
           }
-          __syncthreads();
         }
-      if (warp < side) {
-        // the whole (sequence, head) in this range: the result; a part of it: to the workspace
-        const bool whole = tile0 == 0 && cu.tile + 1 == cu.tiles;
-        const int64_t at = (((int64_t)me * 2 + (pieces > 0)) * side + sub) * a.part_rows;
-#pragma unroll
-        for (int x = 0; x < NH; ++x)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = x * 8 + 2 * j + e;
-            if (r >= rows) continue;
-            const float f = whole ? (L[x][e] != 0.f ? g[x][e] / L[x][e] : 0.f) : g[x][e];
-#pragma unroll
-            for (int u = 0; u < KS; ++u) {
-              const int c = u * 16 + 2 * r0;
-              const float y0 = o[u][x][e] * f, y1 = o[u][x][2 + e] * f;
-              if (whole) {
-                const int64_t to = cu.b * a.o_sb + (int64_t)(row0 + r) * a.o_sh + c;
-                if (c < a.c.d) store_out(p, to, y0);
-                if (c + 1 < a.c.d) store_out(p, to + 1, y1);
-              } else {
-                *reinterpret_cast<float2*>(a.part_o + (at + r) * DP + c) = make_float2(y0, y1);
-              }
-            }
-            if (r0 == 0) {
-              if (!whole) *reinterpret_cast<float2*>(a.part_ml + (at + r) * 2) = make_float2(Mx[x][e], L[x][e]);
-              else if (a.lse)
-                a.lse[(int64_t)cu.b * a.hq + row0 + r] = L[x][e] != 0.f ? (Mx[x][e] + log2f(L[x][e])) * kLn2F : -INFINITY;
-            }
-          }
+        fence_proxy_async_smem();  // (the next tile lands where the accumulators were)
+        __syncthreads();
       }
-      if (side == kWarps) __syncthreads();  // (the statistics are written again)
       ++pieces;
       fresh = true;
     }
