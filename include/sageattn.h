@@ -350,7 +350,8 @@ int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch
  *   positions: device int32, token i of batch b at b positions_stride + i; NULL: i. inv_freq: device
  *   float [rot_dim / 2] (NULL with rot_dim 0). q_weight, k_weight: device [head_dim] of `dtype` or SAGE_F32
  *   (weight_dtype), or NULL for ones. Squares are summed in fp32: magnitudes below 1e18.
- * Angles are exact to 2^-33 of a turn or better at every position. rot_dim even, 0 to head_dim. */
+ * Angles are taken as 64-bit fractions of a turn, off by 2^-53 of inv_freq / 2 pi for each step of the
+ * position. batch * seqlen below 2^31; rot_dim even, 0 to head_dim. */
 int sage_qk_norm_rope(const sage_tensor* q, const sage_tensor* k, const sage_tensor* q_out,
                       const sage_tensor* k_out, const int32_t* positions, int64_t positions_stride,
                       const float* inv_freq, const void* q_weight, const void* k_weight,
@@ -382,7 +383,8 @@ int sage_paged_assign(int32_t* page_table, int64_t table_stride, int max_pages, 
 
 /* Pages of sequences that shrink, back onto the stack: of the seq_lens[b] tokens that sequence b holds
  * keep_lens[b] stay; the pages behind them are written to free_pages from *free_count on, in the order of
- * the sequences and of their rows. The table is not changed. A sequence with lengths out of range or
+ * the sequences and of their rows. The table is not changed. A page belongs to one sequence: one that two
+ * hold would come back twice. A sequence with lengths out of range or
  * keep_lens > seq_lens (SAGE_ERR_SEQLENS), or with a page among those given that is not in
  * [0, num_pages) (SAGE_ERR_PAGE), gives none; where the stack has no room, that sequence and the later ones
  * do not either (SAGE_ERR_SEQLENS). */

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const AssignArgs a) {
   }
   // ---- and of the tokens; behind the last sequence positions and slots are -1
   const int c0 = s_cu[0], c1 = b0 + n == a.batch ? a.max_tokens : s_cu[n];
-  for (int64_t t = c0 + split * kThreads + tid; t < c1; t += a.splits * kThreads) {
+  for (int64_t t = (int64_t)c0 + split * kThreads + tid; t < c1; t += a.splits * kThreads) {
     long long slot = -1;
     int pos = -1;
     if (t < s_cu[n]) {

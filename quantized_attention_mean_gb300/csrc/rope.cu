@@ -373,7 +373,7 @@ extern "C" int sage_qk_norm_rope(const sage_tensor* q, const sage_tensor* k, con
   if (dtype != SAGE_F16 && dtype != SAGE_BF16) return SAGE_ERR_DTYPE;
   if ((q_weight || k_weight) && weight_dtype != dtype && weight_dtype != SAGE_F32) return SAGE_ERR_DTYPE;
   if (tensor_layout != SAGE_HND && tensor_layout != SAGE_NHD) return SAGE_ERR_INVALID_ARG;
-  if (batch < 0 || seqlen < 0 || heads_q < 1 || heads_kv < 1 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 ||
+  if (batch < 0 || seqlen < 0 || (int64_t)batch * seqlen > 0x7fffffff || heads_q < 1 || heads_kv < 1 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 ||
       !(eps >= 0.f) || std::isinf(eps) || positions_stride < 0 || (rot_dim > 0 && !inv_freq))
     return SAGE_ERR_INVALID_ARG;
   if (batch == 0 || seqlen == 0) return SAGE_OK;

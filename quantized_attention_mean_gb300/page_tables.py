@@ -10,7 +10,8 @@ sequences that shrink or end give theirs back.
     free_count = paged_release(page_table, seq_lens, keep_lens, free_pages, free_count, page_size)
     seq_lens = keep_lens
 
-Nothing is read back by the host, so a step can be captured into a CUDA graph.
+A page belongs to one sequence: one that two sequences hold would come back twice. Nothing is read back by the host, so a
+step can be captured into a CUDA graph.
 """
 
 import functools

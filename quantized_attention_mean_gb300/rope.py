@@ -7,7 +7,7 @@ import torch
 
 from . import DTYPE, LAYOUT, SageError, _lib
 from ._lib import SageView
-from .paged import _check_small, _Launch, _ptr
+from .paged import _check_range, _check_small, _Launch, _ptr
 
 __all__ = ["qk_norm_rope"]
 
@@ -124,6 +124,7 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
         _check_outputs(q, k, q_out, k_out, dtype, index)
     if index < 0:
         raise ValueError("q and k must be on a CUDA device")
+    _check_range("the number of tokens", B * N)
     with _Launch(index, stream) as on:
         if q_out is None:
             q_out = torch.empty(shape, dtype=dtype, device=q.device)
