@@ -101,7 +101,7 @@ struct Window {
 template <typename T, int FORM>
 __device__ __forceinline__ void fetch_rows(const AppendArgs& a, const Window& w, int unit, uint4 (&kept)[kKept]) {
   const int lane = threadIdx.x & 31, ch = (lane & (a.lanes - 1)) * 8, per = 32 / a.lanes;
-  const int kv = unit & 1, h = unit >> 1, step = FORM == kShared ? per * 4 : per;
+  const int kv = unit >= a.q.c.hkv, h = unit - kv * a.q.c.hkv, step = FORM == kShared ? per * 4 : per;
   const int first = (FORM == kShared ? (threadIdx.x >> 5) * per : 0) + lane / a.lanes;
   const T* x = static_cast<const T*>(a.x[kv]) + (w.row0 + first) * a.x_st[kv] + h * a.x_sh[kv];
   const int64_t jump = step * a.x_st[kv];
@@ -147,7 +147,7 @@ template <typename T, int TYPE, int FORM>
 __device__ __forceinline__ void store_window(const AppendArgs& a, const Window& w, int unit, uint4 (&kept)[kKept], float* s_most) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const PagedView& c = a.q.c;
-  const int kv = unit & 1, h = unit >> 1;
+  const int kv = unit >= a.q.c.hkv, h = unit - kv * a.q.c.hkv;
   const int ch = (lane & (a.lanes - 1)) * 8, per = 32 / a.lanes, step = FORM == kShared ? per * 4 : per;
   const int first = (FORM == kShared ? warp * per : 0) + lane / a.lanes;
   const bool on = ch < c.d;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(128, 7) append_q8_kernel(const AppendArgs a) {
           for (int u = unit0; u < units; u += unit_step) {
             uint4 kept[kKept];
             fetch_rows<T, FORM>(a, w, u, kept);
-            if ((u & 1 ? a.q.v_type : a.q.k_type) == SAGE_S8) store_window<T, SAGE_S8, FORM>(a, w, u, kept, s_most[FORM == kShared ? 0 : warp]);
+            if ((u >= c.hkv ? a.q.v_type : a.q.k_type) == SAGE_S8) store_window<T, SAGE_S8, FORM>(a, w, u, kept, s_most[FORM == kShared ? 0 : warp]);
             else store_window<T, SAGE_E4M3, FORM>(a, w, u, kept, s_most[FORM == kShared ? 0 : warp]);
           }
         }
@@ -344,14 +344,74 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
   }
 }
 // Four codes times their scale, in 16 bits.
-template <typename T>
-__device__ __forceinline__ uint2 values4(uint32_t codes, int type, float scale) {
+template <typename T, int TYPE>
+__device__ __forceinline__ uint2 values4(uint32_t codes, float scale) {
   float f0, f1, f2, f3;
-  if (type == SAGE_S8) from_codes<SAGE_S8>(codes, f0, f1, f2, f3);
-  else from_codes<SAGE_E4M3>(codes, f0, f1, f2, f3);
+  from_codes<TYPE>(codes, f0, f1, f2, f3);
   mul2(f0, f1, f0, f1, scale, scale);
   mul2(f2, f3, f2, f3, scale, scale);
   return make_uint2(narrow2<T>(f0, f1), narrow2<T>(f2, f3));
+}
+
+// Rows t0 .. of K or V: lane j knows where row j's codes and first scale lie (no row: -1).
+template <typename T, int V, int TYPE>
+__device__ __forceinline__ void copy_rows(const ReadArgs& a, int kv, int64_t t0, int n_rows, long long code_at, long long scale_at) {
+  const PagedView& c = a.q.c;
+  const int lane = threadIdx.x & 31;
+  const int64_t sh = kv ? c.v_sh : c.k_sh;
+  const uint8_t* codes = static_cast<const uint8_t*>(kv ? c.v : c.k);
+  const float* scales = kv ? a.q.vs : a.q.ks;
+  const int runs = (c.d + V - 1) / V, n = c.hkv * runs;
+  constexpr int kWords = V >= 4 ? V / 4 : 1;
+  for (int x0 = 0; x0 < n; x0 += 64) {
+    // two runs of a row for each lane
+    const uint8_t* src[2];
+    const float* sc[2];
+    T* dst[2];
+    bool on[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int x = x0 + 32 * u + lane, h = x / runs, ch = (x - h * runs) * V;
+      on[u] = x < n;
+      src[u] = codes + h * sh + ch;
+      sc[u] = scales + (int64_t)h * a.q.blocks;
+      dst[u] = static_cast<T*>(a.y[kv]) + t0 * a.y_st[kv] + h * a.y_sh[kv] + ch;
+    }
+#pragma unroll 1
+    for (int j = 0; j < n_rows; ++j) {
+      const long long at = __shfl_sync(0xffffffffu, code_at, j), sat = __shfl_sync(0xffffffffu, scale_at, j);
+      uint32_t raw[2][kWords];
+      float scale[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        scale[u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) raw[u][i] = 0;
+        if (on[u] && at >= 0) {
+          const uint8_t* p = src[u] + at;
+          scale[u] = __ldg(sc[u] + sat);
+          if constexpr (V == 8) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+            raw[u][0] = w.x; raw[u][1] = w.y;
+          } else {
+            raw[u][0] = *p;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (on[u]) {
+          if constexpr (V == 8) {
+            const uint2 lo = values4<T, TYPE>(raw[u][0], scale[u]), hi = values4<T, TYPE>(raw[u][1], scale[u]);
+            *reinterpret_cast<uint4*>(dst[u]) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          } else {
+            *reinterpret_cast<uint16_t*>(dst[u]) = (uint16_t)values4<T, TYPE>(raw[u][0], scale[u]).x;
+          }
+        }
+        dst[u] += a.y_st[kv];
+      }
+    }
+  }
 }
 
 // A warp per `rows` rows of K or of V (blockIdx.y): its lanes find the rows' places side by side, then take V codes each, the same
@@ -393,62 +453,11 @@ __global__ void __launch_bounds__(128, 10) read_q8_kernel(const ReadArgs a) {
       }
     }
   }
-  const int block = slot / a.q.block, type = kv ? a.q.v_type : a.q.k_type;
-  const int64_t sp = kv ? c.v_sp : c.k_sp, sh = kv ? c.v_sh : c.k_sh, st = kv ? c.v_st : c.k_st;
-  const uint8_t* codes = static_cast<const uint8_t*>(kv ? c.v : c.k);
-  const float* scales = kv ? a.q.vs : a.q.ks;
-  const int runs = (c.d + V - 1) / V, n = c.hkv * runs;
-  constexpr int kWords = V >= 4 ? V / 4 : 1;
-  for (int x0 = 0; x0 < n; x0 += 64) {
-    // two runs of a row for each lane
-    const uint8_t* src[2];
-    const float* sc[2];
-    T* dst[2];
-    bool on[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int x = x0 + 32 * u + lane, h = x / runs, ch = (x - h * runs) * V;
-      on[u] = x < n;
-      src[u] = codes + h * sh + ch;
-      sc[u] = scales + (int64_t)h * a.q.blocks;
-      dst[u] = static_cast<T*>(a.y[kv]) + t0 * a.y_st[kv] + h * a.y_sh[kv] + ch;
-    }
-#pragma unroll 1
-    for (int j = 0; j < n_rows; ++j) {
-      const int pg = __shfl_sync(0xffffffffu, page, j), sl = __shfl_sync(0xffffffffu, slot, j), bl = __shfl_sync(0xffffffffu, block, j);
-      const int64_t at = pg * sp + sl * st, sat = (int64_t)pg * c.hkv * a.q.blocks + bl;
-      uint32_t raw[2][kWords];
-      float scale[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        scale[u] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) raw[u][i] = 0;
-        if (on[u] && pg >= 0) {
-          const uint8_t* p = src[u] + at;
-          scale[u] = __ldg(sc[u] + sat);
-          if constexpr (V == 8) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-            raw[u][0] = w.x; raw[u][1] = w.y;
-          } else {
-            raw[u][0] = *p;
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (on[u]) {
-          if constexpr (V == 8) {
-            const uint2 lo = values4<T>(raw[u][0], type, scale[u]), hi = values4<T>(raw[u][1], type, scale[u]);
-            *reinterpret_cast<uint4*>(dst[u]) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-          } else {
-            *reinterpret_cast<uint16_t*>(dst[u]) = (uint16_t)values4<T>(raw[u][0], type, scale[u]).x;
-          }
-        }
-        dst[u] += a.y_st[kv];
-      }
-    }
-  }
+  // where this lane's row and its first scale lie
+  const long long code_at = page >= 0 ? page * (kv ? c.v_sp : c.k_sp) + slot * (kv ? c.v_st : c.k_st) : -1;
+  const long long scale_at = page >= 0 ? (long long)page * c.hkv * a.q.blocks + slot / a.q.block : 0;
+  if ((kv ? a.q.v_type : a.q.k_type) == SAGE_S8) copy_rows<T, V, SAGE_S8>(a, kv, t0, n_rows, code_at, scale_at);
+  else copy_rows<T, V, SAGE_E4M3>(a, kv, t0, n_rows, code_at, scale_at);
 }
 
 __global__ void clear_status_kernel(int* err) {
