@@ -42,6 +42,11 @@ CASES = [
     ([3] * 150, 4, 4, 64, 4, 4, torch.float16, S8, S8, "HND", 0.0, False),
     ([0, 0], 4, 2, 64, 16, 16, torch.float16, S8, E4, "HND", 0.0, False),
     ([100, 257], 12, 1, 16, 64, 16, torch.float16, E4, S8, "HND", 0.0, True),
+    ([300, 0, 1000, 77], 8, 4, 64, 32, 16, torch.bfloat16, S8, E4, "NHD", 0.0, True),       # four heads side by side
+    ([5, 700], 48, 4, 64, 16, 16, torch.float16, E4, S8, "NHD", 0.0, False),                # and twelve queries each
+    ([129, 640, 31], 36, 2, 128, 16, 8, torch.bfloat16, S8, E4, "NHD", 25.0, False),        # two row blocks, two heads side by side
+    ([1000] * 9, 24, 2, 128, 32, 32, torch.float16, E4, E4, "HND", 0.0, False),             # twelve queries, head_dim 128
+    ([2, 64, 65, 128], 6, 6, 48, 24, 8, torch.bfloat16, S8, S8, "NHD", 0.0, True),
 ]
 
 
@@ -186,6 +191,38 @@ def test_bad_lengths_and_pages_are_told(bound):
         assert_close(out, w["out"], w["out_tol"], "out")
     qa.paged_attn_q8(q.to(DEV), *planes(G), G["table"], G["lens"], bound, workspace=ws)
     assert qa.read_device_status(ws) == 0
+
+
+def test_the_same_bits_every_time():
+    # ranges that end anywhere, joined by another kernel: results do not depend on which part is done first
+    import quantized_attention_mean_gb300 as qa
+    for layout, d in (("HND", 128), ("NHD", 64)):
+        c = q8.make_cache([5000, 1, 333, 9001], 4, d, 16, 16, S8, E4, layout, seed=5)
+        G = on_gpu(c)
+        q = torch.randn(4, 20, d, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+        for bound in (9001, 10 ** 6):
+            first = qa.paged_attn_q8(q, *planes(G), G["table"], G["lens"], bound, tensor_layout=layout, return_lse=True)
+            for _ in range(20):
+                again = qa.paged_attn_q8(q, *planes(G), G["table"], G["lens"], bound, tensor_layout=layout, return_lse=True)
+                assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_two_streams_at_once():
+    # calls whose workspaces come from the allocator run side by side
+    import quantized_attention_mean_gb300 as qa
+    c = q8.make_cache([4000, 2500], 8, 128, 32, 32, S8, E4, seed=9)
+    G = on_gpu(c)
+    qs = [torch.randn(2, 32, 128, generator=torch.Generator().manual_seed(i)).bfloat16().to(DEV) for i in range(2)]
+    want = [qa.paged_attn_q8(q, *planes(G), G["table"], G["lens"], 10 ** 5) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    got = [[], []]
+    for _ in range(30):
+        for i, st in enumerate(streams):
+            got[i].append(qa.paged_attn_q8(qs[i], *planes(G), G["table"], G["lens"], 10 ** 5, stream=st))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
 
 
 def test_empty_cache_and_result_over_the_query():
