@@ -18,8 +18,14 @@ constexpr int kMostRanges = Q8Cfg<128, 1>::kRanges;
 bool q8_clustered(int batch, int hkv, int row_blocks, int64_t max_len, int d) {
   return (int64_t)hkv * row_blocks * batch * kRanks <= kCtas && max_len <= 8 * kRanks * tile_of(d);
 }
-// Heads whose token rows lie side by side, which a line's item takes together, so that DRAM is read in 256 bytes or more.
-int heads_beside(int hkv, int d) { return hkv % 2 ? 1 : d <= 64 && hkv % 4 == 0 ? 4 : 2; }
+// Heads that an item of the line takes together, each with a part of the warps. Token rows that lie side by side (NHD): so
+// that DRAM is read in 256 bytes or more (32 sequences of up to 32K tokens 212 us with one head, 190 with two). Short sequences of
+// rows by heads: all four warps, so that tiles are filled and fewer of them end (us with one head and with four: 512 x 150 tokens 80
+// and 71, 256 x 30-600 72 and 64, 256 x 300 59 and 58, but 128 x 600 46 and 47, 64 x 1200 41 and 43).
+int heads_beside(bool nhd, int hkv, int d, int64_t max_len) {
+  const int want = nhd ? (d <= 64 ? 4 : 2) : max_len <= 600 ? 4 : 1;
+  return hkv % want == 0 ? want : hkv % 2 == 0 ? 2 : 1;
+}
 bool q8_layout(int batch, int hq, int hkv, int64_t max_len, int d, Q8Layout* L) {
   if (batch < 0 || hq < 1 || hkv < 1 || hq % hkv || max_len < 0 || d < 1 || d > 128) return false;
   const int dp = d <= 64 ? 64 : 128;
@@ -27,7 +33,7 @@ bool q8_layout(int batch, int hq, int hkv, int64_t max_len, int d, Q8Layout* L) 
   const bool line = !q8_clustered(batch, hkv, (hq / hkv + kRows - 1) / kRows, max_len, d);
   L->err = SAGE_STATUS_BYTES;
   L->part_o = L->err + (line ? up256(4 * kMostRanges) : 0);
-  const size_t rows = line ? (size_t)kMostRanges * 2 * heads_beside(hkv, d) * (hq / hkv <= 8 ? 8 : kRows) : 0;
+  const size_t rows = line ? (size_t)kMostRanges * 2 * 4 * (hq / hkv <= 8 ? 8 : kRows) : 0;
   L->part_ml = L->part_o + up256(rows * dp * 4);
   L->total = L->part_ml + up256(rows * 2 * 4);
   return true;
@@ -116,7 +122,7 @@ int sage_paged_attn_q8(const sage_packed* q, const sage_q8_cache* cache, const s
     if (view.block == 1 << i) p.block_shift = i;
   }
   a.part_rows = a.group <= 8 ? 8 : kRows;
-  a.side = !p.cluster && tensor_layout == SAGE_NHD ? heads_beside(heads_kv, head_dim) : 1;
+  a.side = p.cluster ? 1 : heads_beside(tensor_layout == SAGE_NHD, heads_kv, head_dim, max_seqlen);
   a.tile_shift = log2_of(tile_of(head_dim) / a.side);
   // the join by channels where its CTAs would leave SMs idle
   a.slices = (int64_t)heads_kv * a.row_blocks * batch <= 38 ? (head_dim <= 64 ? 2 : 4) : 1;

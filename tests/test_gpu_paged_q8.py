@@ -47,6 +47,8 @@ CASES = [
     ([129, 640, 31], 36, 2, 128, 16, 8, torch.bfloat16, S8, E4, "NHD", 25.0, False),        # two row blocks, two heads side by side
     ([1000] * 9, 24, 2, 128, 32, 32, torch.float16, E4, E4, "HND", 0.0, False),             # twelve queries, head_dim 128
     ([2, 64, 65, 128], 6, 6, 48, 24, 8, torch.bfloat16, S8, S8, "NHD", 0.0, True),
+    ([1, 31, 32, 33, 100, 600, 0, 95] * 5, 16, 4, 128, 16, 16, torch.bfloat16, S8, E4, "HND", 0.0, False),  # short ones: four heads
+    ([63, 64, 65, 500] * 6, 6, 6, 64, 16, 16, torch.float16, E4, S8, "HND", 0.0, True),                     # and two to an item
 ]
 
 
