@@ -49,6 +49,13 @@ CASES = [
     ([2, 64, 65, 128], 6, 6, 48, 24, 8, torch.bfloat16, S8, S8, "NHD", 0.0, True),
     ([1, 31, 32, 33, 100, 600, 0, 95] * 5, 16, 4, 128, 16, 16, torch.bfloat16, S8, E4, "HND", 0.0, False),  # short ones: four heads
     ([63, 64, 65, 500] * 6, 6, 6, 64, 16, 16, torch.float16, E4, S8, "HND", 0.0, True),                     # and two to an item
+    ([900, 33, 0, 1200, 64], 32, 8, 96, 16, 8, torch.bfloat16, E4, S8, "NHD", 20.0, True),   # four, by six units of channels
+    ([700, 1, 40, 129] * 9, 8, 4, 120, 24, 24, torch.float16, S8, E4, "NHD", 0.0, False),
+    ([2000, 64, 31] * 13, 4, 4, 32, 32, 32, torch.bfloat16, S8, S8, "HND", 0.0, True),       # two units
+    ([2000, 64, 31] * 13, 40, 4, 36, 16, 4, torch.float16, E4, E4, "NHD", 0.0, False),
+    ([2000, 64, 31] * 13, 40, 4, 72, 16, 4, torch.bfloat16, S8, E4, "HND", 0.0, False),
+    ([500, 77], 12, 1, 20, 8, 8, torch.bfloat16, S8, E4, "HND", 0.0, True),
+    ([500, 77], 20, 2, 90, 8, 8, torch.float16, E4, S8, "NHD", 0.0, False),
 ]
 
 
