@@ -80,15 +80,20 @@ struct AppendArgs {
   int tokens, chunk;    // rows that a CTA looks after
   int shares;           // CTAs that share a chunk's heads
   int window;           // slots that are written together: whole blocks of one page
-  int in16, out8;       // rows allow 16-byte loads, codes 8-byte stores
-  int lanes;            // lanes of a row, 8 channels each: 8 or 16
+  int in_run, out_run;  // channels of a row's loads and of the codes' stores: 8, 4 or 1
+  int lanes;            // lanes of a row, 8 channels each: 4, 8 or 16
   int block_shift;      // log2 of the block, or -1
   int* err;             // or null
 };
 
-// A window takes one of three forms. kOne: one block, by a warp. kMany: several small blocks, by a warp, whose rows' largest
-// magnitudes meet in shared memory. kShared: one block, by a CTA.
-enum { kOne, kMany, kShared };
+// A window takes one of these forms. kOne: one block, by a warp. kMany: several small blocks, by a warp, whose rows' largest
+// magnitudes and scales meet in shared memory. kTwo, kFour, kEight: one block, by a CTA of so many warps: as many as hold
+// its rows in registers (us for 41K tokens of 8 heads of head_dim 128, K and V: blocks of 32 by two warps 42, by four 59; of 128 by
+// eight 48, by four, which read half of the rows twice, 73).
+enum { kOne, kMany, kTwo, kFour, kEight };
+__host__ __device__ constexpr int warps_of(int form) { return form == kTwo ? 2 : form == kEight ? 8 : 4; }
+__host__ __device__ constexpr bool by_cta(int form) { return form >= kTwo; }
+constexpr int kManyRows = 32;  // of a window of several blocks
 constexpr int kKept = 8;  // rows of a lane that stay in registers between the two walks over them
 
 // New rows of a window: the first one's token, how many; the page, slot and block of the first; earlier tokens of its block.
@@ -97,18 +102,30 @@ struct Window {
   int rows, page, slot0, block0, held;
 };
 
+// Eight channels of a row from ch on, which is one of it; zeros past the last. FULL: all rows and codes allow runs of eight.
+template <typename T, bool FULL>
+__device__ __forceinline__ uint4 load_run(const AppendArgs& a, const T* row, int ch) {
+  if (FULL || a.in_run == 8) return __ldg(reinterpret_cast<const uint4*>(row + ch));
+  if (a.in_run == 4) {
+    const uint2 lo = __ldg(reinterpret_cast<const uint2*>(row + ch));
+    const uint2 hi = ch + 4 < a.q.c.d ? __ldg(reinterpret_cast<const uint2*>(row + ch + 4)) : make_uint2(0, 0);
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+  return load8_raw<T>(row, ch, a.q.c.d, 0);
+}
+
 // Rows of one unit (a head's K or V) for this lane: the first kKept of them.
-template <typename T, int FORM>
+template <typename T, int FORM, bool FULL>
 __device__ __forceinline__ void fetch_rows(const AppendArgs& a, const Window& w, int unit, uint4 (&kept)[kKept]) {
   const int lane = threadIdx.x & 31, ch = (lane & (a.lanes - 1)) * 8, per = 32 / a.lanes;
-  const int kv = unit >= a.q.c.hkv, h = unit - kv * a.q.c.hkv, step = FORM == kShared ? per * 4 : per;
-  const int first = (FORM == kShared ? (threadIdx.x >> 5) * per : 0) + lane / a.lanes;
+  const int kv = unit >= a.q.c.hkv, h = unit - kv * a.q.c.hkv, step = by_cta(FORM) ? per * warps_of(FORM) : per;
+  const int first = (by_cta(FORM) ? (threadIdx.x >> 5) * per : 0) + lane / a.lanes;
   const T* x = static_cast<const T*>(a.x[kv]) + (w.row0 + first) * a.x_st[kv] + h * a.x_sh[kv];
   const int64_t jump = step * a.x_st[kv];
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
     kept[i] = make_uint4(0, 0, 0, 0);
-    if (ch < a.q.c.d && first + i * step < w.rows) kept[i] = load8_raw<T>(x, ch, a.q.c.d, a.in16);
+    if (ch < a.q.c.d && first + i * step < w.rows) kept[i] = load_run<T, FULL>(a, x, ch);
     x += jump;
   }
 }
@@ -143,13 +160,13 @@ __device__ __forceinline__ void widen8(const uint4& raw, float (&f)[8]) {
 }
 
 // The largest magnitude of each block, its scale, the codes.
-template <typename T, int TYPE, int FORM>
+template <typename T, int TYPE, int FORM, bool FULL>
 __device__ __forceinline__ void store_window(const AppendArgs& a, const Window& w, int unit, uint4 (&kept)[kKept], float* s_most) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const PagedView& c = a.q.c;
   const int kv = unit >= a.q.c.hkv, h = unit - kv * a.q.c.hkv;
-  const int ch = (lane & (a.lanes - 1)) * 8, per = 32 / a.lanes, step = FORM == kShared ? per * 4 : per;
-  const int first = (FORM == kShared ? warp * per : 0) + lane / a.lanes;
+  const int ch = (lane & (a.lanes - 1)) * 8, per = 32 / a.lanes, step = by_cta(FORM) ? per * warps_of(FORM) : per;
+  const int first = (by_cta(FORM) ? warp * per : 0) + lane / a.lanes;
   const bool on = ch < c.d;
   const T* x = static_cast<const T*>(a.x[kv]) + w.row0 * a.x_st[kv] + h * a.x_sh[kv];
   const int64_t xs = a.x_st[kv], cs = kv ? c.v_st : c.k_st;
@@ -158,8 +175,11 @@ __device__ __forceinline__ void store_window(const AppendArgs& a, const Window& 
   const int block0 = w.block0;
   const float was = w.held ? scales[block0] : 0.f;
   auto put = [&](uint8_t* d, const uint2& code) {
-    if (a.out8) {
+    if (FULL || a.out_run == 8) {
       *reinterpret_cast<uint2*>(d) = code;
+    } else if (a.out_run == 4) {
+      *reinterpret_cast<uint32_t*>(d) = code.x;
+      if (ch + 4 < c.d) *reinterpret_cast<uint32_t*>(d + 4) = code.y;
     } else {
       const uint8_t* b = reinterpret_cast<const uint8_t*>(&code);
       for (int e = 0; e < 8; ++e)
@@ -183,7 +203,7 @@ __device__ __forceinline__ void store_window(const AppendArgs& a, const Window& 
       if (!on) break;
       uint8_t* s = base + (int64_t)(w.slot0 - w.held + r) * cs;
       alignas(8) uint8_t code[8];
-      if (a.out8) {
+      if (FULL || a.out_run == 8) {
         *reinterpret_cast<uint2*>(code) = *reinterpret_cast<const uint2*>(s);
       } else {
         for (int e = 0; e < 8; ++e) code[e] = ch + e < c.d ? s[e] : 0;
@@ -197,58 +217,64 @@ __device__ __forceinline__ void store_window(const AppendArgs& a, const Window& 
     }
   };
   if constexpr (FORM == kMany) {
-    // a row's largest magnitude, then each block's over its rows
+    // a row's largest magnitude, then each block's over its rows, by a lane each
+    float* const s_scale = s_most + kManyRows;  // [2][kManyRows]: scales, their reciprocals
+    // (the lanes of a row halve the rows twice while they exchange, two rows in a register)
+    const int far = a.lanes / 2, near = a.lanes / 4;
+    const bool up = lane & far, up2 = lane & near;
+    uint32_t q[4];
 #pragma unroll
-    for (int i = 0; i < kKept; ++i) {
-      uint32_t m = largest2(kept[i], 0);
-      for (int o = a.lanes / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if ((lane & (a.lanes - 1)) == 0) s_most[first + i * step] = pattern<T>(m);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = largest2(kept[2 * i], 0), y = largest2(kept[2 * i + 1], 0);
+      q[i] = __vmaxu2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
+    }
+    const uint32_t x0 = __vmaxu2(up ? q[2] : q[0], __shfl_xor_sync(0xffffffffu, up ? q[0] : q[2], far));
+    const uint32_t x1 = __vmaxu2(up ? q[3] : q[1], __shfl_xor_sync(0xffffffffu, up ? q[1] : q[3], far));
+    uint32_t m2 = __vmaxu2(up2 ? x1 : x0, __shfl_xor_sync(0xffffffffu, up2 ? x0 : x1, near));
+    for (int o = near / 2; o > 0; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+    if ((lane & (near - 1)) == 0) {
+      const int row = first + ((up ? 4 : 0) + (up2 ? 2 : 0)) * step;
+      if (row < w.rows) s_most[row] = pattern<T>(m2 & 0xffffu);
+      if (row + step < w.rows) s_most[row + step] = pattern<T>(m2 >> 16);
+    }
+    __syncwarp();  // (also: every lane has read the old scale)
+    if (lane * a.q.block < w.held + w.rows) {
+      float m = 0.f;
+      const int end = min(w.rows, (lane + 1) * a.q.block - w.held);
+      for (int r = max(0, lane * a.q.block - w.held); r < end; ++r) m = fmaxf(m, s_most[r]);
+      const float scale = fmaxf(lane == 0 ? was : 0.f, needed_scale<TYPE>(m));
+      s_scale[lane] = scale;
+      s_scale[kManyRows + lane] = __frcp_rn(scale);
+      scales[block0 + lane] = scale;
     }
     __syncwarp();
-    auto scale_of = [&](int block) {  // of the window
-      float m = 0.f;
-      const int end = min(w.rows, (block + 1) * a.q.block - w.held);
-      for (int r = max(0, block * a.q.block - w.held); r < end; ++r) m = fmaxf(m, s_most[r]);
-      return fmaxf(block == 0 ? was : 0.f, needed_scale<TYPE>(m));
-    };
-    if (w.held) again(scale_of(0));
-    int last = -1;
-    float scale = 0.f, inv = 0.f;
+    if (w.held) again(s_scale[0]);
 #pragma unroll
     for (int i = 0; i < kKept; ++i) {
       const int r = first + i * step, block = a.block_shift >= 0 ? (w.held + r) >> a.block_shift : (w.held + r) / a.q.block;
-      if (r >= w.rows) continue;
-      if (block != last) {
-        scale = scale_of(block);
-        inv = __frcp_rn(scale);
-        last = block;
-      }
-      if (on) write(kept[i], inv);
+      if (on && r < w.rows) write(kept[i], s_scale[kManyRows + block]);
       to += hop;
     }
-    __syncwarp();  // (every lane has read the old scale and the magnitudes)
-    const int blocks = (w.held + w.rows + a.q.block - 1) / a.q.block;
-    if (lane < blocks) scales[block0 + lane] = scale_of(lane);
-    __syncwarp();
+    __syncwarp();  // (the next unit writes there)
   } else {
     uint32_t pair = 0;
 #pragma unroll
     for (int i = 0; i < kKept; ++i) pair = largest2(kept[i], pair);
     for (int r = first + kKept * step; r < w.rows; r += step)
-      if (on) pair = largest2(load8_raw<T>(x + r * xs, ch, c.d, a.in16), pair);
+      if (on) pair = largest2(load_run<T, FULL>(a, x + r * xs, ch), pair);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) pair = __vmaxu2(pair, __shfl_xor_sync(0xffffffffu, pair, o));
     float most = pattern<T>(pair);
-    if (FORM == kShared) {
+    if (by_cta(FORM)) {
       __syncthreads();  // (also: every thread has read the old scale)
       if (lane == 0) s_most[warp] = most;
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) most = fmaxf(most, s_most[i]);
+      for (int i = 0; i < warps_of(FORM); ++i) most = fmaxf(most, s_most[i]);
     }
     const float scale = fmaxf(was, needed_scale<TYPE>(most)), inv = __frcp_rn(scale);
     __syncwarp();  // (every lane has read the old scale)
-    if (FORM == kShared ? threadIdx.x == 0 : lane == 0) scales[block0] = scale;
+    if (by_cta(FORM) ? threadIdx.x == 0 : lane == 0) scales[block0] = scale;
     again(scale);
 #pragma unroll
     for (int i = 0; i < kKept; ++i) {
@@ -256,27 +282,27 @@ __device__ __forceinline__ void store_window(const AppendArgs& a, const Window& 
       to += hop;
     }
     for (int r = first + kKept * step; r < w.rows; r += step) {
-      if (on) write(load8_raw<T>(x + r * xs, ch, c.d, a.in16), inv);
+      if (on) write(load_run<T, FULL>(a, x + r * xs, ch), inv);
       to += hop;
     }
   }
 }
 
 // CTA (x, y) of line x * shares + y: the windows whose first new token lies in rows [x chunk, (x + 1) chunk), for the y-th
-// share of the heads' K and V (kShared: by the whole CTA, otherwise by a warp each). DRAM bounds it for prompts, which many
+// share of the heads' K and V (kTwo to kEight: by the whole CTA, otherwise by a warp each). DRAM bounds it for prompts, which many
 // resident warps keep busy: fetching the next head's rows while one is scaled took twice the registers and was slower.
-template <typename T, int FORM>
-__global__ void __launch_bounds__(128, 7) append_q8_kernel(const AppendArgs a) {
-  __shared__ float s_most[4][32];
+template <typename T, int FORM, bool FULL>
+__global__ void __launch_bounds__(32 * warps_of(FORM), 28 / warps_of(FORM)) append_q8_kernel(const AppendArgs a) {
+  __shared__ float s_most[4][FORM == kMany ? 3 * kManyRows : 8];
   const PagedView& c = a.q.c;
   const int warp = threadIdx.x >> 5, units = 2 * c.hkv;
   const int share = blockIdx.x % a.shares;  // (CTAs of one window run side by side: they read the same token rows)
   const int64_t place = blockIdx.x / a.shares;
-  const int unit0 = FORM == kShared ? share : share * 4 + warp, unit_step = FORM == kShared ? a.shares : a.shares * 4;
+  const int unit0 = by_cta(FORM) ? share : share * 4 + warp, unit_step = by_cta(FORM) ? a.shares : a.shares * 4;
   pdl_wait();
   pdl_trigger();
   if (unit0 >= units) return;  // (a whole warp, or no thread of the CTA)
-  const bool tells = a.err && unit0 == 0 && (threadIdx.x & 31) == 0 && (FORM != kShared || threadIdx.x == 0);
+  const bool tells = a.err && unit0 == 0 && (threadIdx.x & 31) == 0 && (!by_cta(FORM) || threadIdx.x == 0);
   const int64_t t_end = min((int64_t)a.tokens, (place + 1) * a.chunk);
   int64_t t = place * a.chunk;
   int b = a.cu ? sequence_of(a.cu, c.batch, (int)t) : (int)t;
@@ -309,9 +335,9 @@ __global__ void __launch_bounds__(128, 7) append_q8_kernel(const AppendArgs a) {
 #pragma unroll 1
           for (int u = unit0; u < units; u += unit_step) {
             uint4 kept[kKept];
-            fetch_rows<T, FORM>(a, w, u, kept);
-            if ((u >= c.hkv ? a.q.v_type : a.q.k_type) == SAGE_S8) store_window<T, SAGE_S8, FORM>(a, w, u, kept, s_most[FORM == kShared ? 0 : warp]);
-            else store_window<T, SAGE_E4M3, FORM>(a, w, u, kept, s_most[FORM == kShared ? 0 : warp]);
+            fetch_rows<T, FORM, FULL>(a, w, u, kept);
+            if ((u >= c.hkv ? a.q.v_type : a.q.k_type) == SAGE_S8) store_window<T, SAGE_S8, FORM, FULL>(a, w, u, kept, s_most[by_cta(FORM) ? 0 : warp]);
+            else store_window<T, SAGE_E4M3, FORM, FULL>(a, w, u, kept, s_most[by_cta(FORM) ? 0 : warp]);
           }
         }
       }
@@ -393,6 +419,8 @@ __device__ __forceinline__ void copy_rows(const ReadArgs& a, int kv, int64_t t0,
           if constexpr (V == 8) {
             const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
             raw[u][0] = w.x; raw[u][1] = w.y;
+          } else if constexpr (V == 4) {
+            raw[u][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
           } else {
             raw[u][0] = *p;
           }
@@ -404,6 +432,8 @@ __device__ __forceinline__ void copy_rows(const ReadArgs& a, int kv, int64_t t0,
           if constexpr (V == 8) {
             const uint2 lo = values4<T, TYPE>(raw[u][0], scale[u]), hi = values4<T, TYPE>(raw[u][1], scale[u]);
             *reinterpret_cast<uint4*>(dst[u]) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          } else if constexpr (V == 4) {
+            *reinterpret_cast<uint2*>(dst[u]) = values4<T, TYPE>(raw[u][0], scale[u]);
           } else {
             *reinterpret_cast<uint16_t*>(dst[u]) = (uint16_t)values4<T, TYPE>(raw[u][0], scale[u]).x;
           }
@@ -469,13 +499,16 @@ int check_status_word(const void* workspace, size_t bytes) {
   return workspace && (reinterpret_cast<uintptr_t>(workspace) % 256 || bytes < SAGE_STATUS_BYTES) ? SAGE_ERR_WORKSPACE
                                                                                                  : SAGE_OK;
 }
-// A packed operand of rows; *vec: every row of whole 16-byte accesses.
-int check_rows(const sage_packed* t, int tokens, int heads, int d, bool written, bool* vec) {
+// A packed operand of rows; *run: channels that an access of every row can take, 8, 4 or 1.
+int check_rows(const sage_packed* t, int tokens, int heads, int d, bool written, int* run) {
   if (!t->data) return SAGE_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(t->data) % 2 || t->stride_token < 0 || t->stride_head < 0) return SAGE_ERR_STRIDE;
   if (written && ((tokens > 1 && t->stride_token == 0) || (heads > 1 && t->stride_head == 0))) return SAGE_ERR_STRIDE;
-  *vec = *vec && reinterpret_cast<uintptr_t>(t->data) % 16 == 0 && d % 8 == 0 && (tokens <= 1 || t->stride_token % 8 == 0) &&
-         (heads <= 1 || t->stride_head % 8 == 0);
+  auto fits = [&](int n) {
+    return reinterpret_cast<uintptr_t>(t->data) % (2 * n) == 0 && d % n == 0 && (tokens <= 1 || t->stride_token % n == 0) &&
+           (heads <= 1 || t->stride_head % n == 0);
+  };
+  *run = *run == 8 && fits(8) ? 8 : *run >= 4 && fits(4) ? 4 : 1;
   return SAGE_OK;
 }
 
@@ -498,10 +531,10 @@ int sage_paged_append_q8(const sage_packed* k, const sage_packed* v, const sage_
   if (tokens < 0 || (!cu_seqlens && tokens != batch) || reinterpret_cast<uintptr_t>(cu_seqlens) % 4) return SAGE_ERR_INVALID_ARG;
   if (check_status_word(workspace, workspace_bytes) != SAGE_OK) return SAGE_ERR_WORKSPACE;
   if (batch == 0 || tokens == 0) return SAGE_OK;
-  bool vec = true;
+  int run = 8;
   const sage_packed* t[2] = {k, v};
   for (int i = 0; i < 2; ++i) {
-    s = check_rows(t[i], tokens, heads_kv, head_dim, false, &vec);
+    s = check_rows(t[i], tokens, heads_kv, head_dim, false, &run);
     if (s != SAGE_OK) return s;
     a.x[i] = t[i]->data;
     a.x_st[i] = t[i]->stride_token;
@@ -510,24 +543,29 @@ int sage_paged_append_q8(const sage_packed* k, const sage_packed* v, const sage_
   if (!sage_device_supported()) return SAGE_ERR_DEVICE;
   a.cu = cu_seqlens;
   a.tokens = tokens;
-  a.in16 = vec;
-  a.out8 = align >= 8;  // (and head_dim a multiple of 8)
-  a.lanes = head_dim <= 64 ? 8 : 16;
+  a.in_run = run;
+  a.out_run = align >= 8 ? 8 : align >= 4 ? 4 : 1;  // (and head_dim a multiple of it)
+  a.lanes = head_dim <= 32 ? 4 : head_dim <= 64 ? 8 : 16;
   a.err = static_cast<int*>(workspace);
   // a window: a block, or as many small ones as a warp's registers hold rows of
   const int hold = kKept * (32 / a.lanes), block = a.q.block;
   a.block_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (block == 1 << i) a.block_shift = i;
-  const int form = block > hold ? kShared : block > hold / 2 ? kOne : kMany;
-  a.window = form == kMany ? hold / block * block : block;
+  const int many = hold < kManyRows ? hold : kManyRows;
+  const int form = block > 4 * hold   ? kEight
+                   : block > 2 * hold ? kFour
+                   : block > hold     ? kTwo
+                   : 2 * block > (cache->page_size < many ? cache->page_size : many) ? kOne : kMany;
+  a.window = form == kMany ? many / block * block : block;
   // a CTA looks after about one window, or one sequence where those are shorter
   const int mean = cu_seqlens ? (tokens + batch - 1) / batch : 1;
   a.chunk = mean < a.window ? mean : a.window;
   const int64_t chunks = ((int64_t)tokens + a.chunk - 1) / a.chunk;
   // and its warps after several heads, unless that leaves SMs without work
-  const int most = form == kShared ? 2 * heads_kv : (2 * heads_kv + 3) / 4;
-  const int64_t want = (152 * (form == kShared ? 16 : 32) + chunks - 1) / chunks;
+  const int most = by_cta(form) ? 2 * heads_kv : (2 * heads_kv + 3) / 4;
+  const int per_sm = (form == kTwo || form == kFour ? 64 : 128) / warps_of(form);
+  const int64_t want = (152 * per_sm + chunks - 1) / chunks;
   a.shares = (int)(want < most ? want : most);
   if (chunks * a.shares > 0x7fffffffLL) a.shares = 1;
   const dim3 grid((unsigned)(chunks * a.shares));
@@ -535,12 +573,19 @@ int sage_paged_append_q8(const sage_packed* k, const sage_packed* v, const sage_
   cudaError_t e = cudaSuccess;
   if (a.err) e = launch_pdl(clear_status_kernel, dim3(1), dim3(1), 0, st, a.err);
   if (e == cudaSuccess) {
-    auto go = [&](auto one, auto many, auto shared) {
-      return launch_pdl(form == kOne ? one : form == kMany ? many : shared, grid, dim3(128), 0, st, a);
+    auto go = [&](auto... kernels) {
+      decltype(&append_q8_kernel<__half, kOne, true>) of[] = {kernels...};
+      return launch_pdl(of[form], grid, dim3(32 * warps_of(form)), 0, st, a);
     };
-    e = dtype == SAGE_F16 ? go(append_q8_kernel<__half, kOne>, append_q8_kernel<__half, kMany>, append_q8_kernel<__half, kShared>)
-                          : go(append_q8_kernel<__nv_bfloat16, kOne>, append_q8_kernel<__nv_bfloat16, kMany>,
-                               append_q8_kernel<__nv_bfloat16, kShared>);
+    auto typed = [&](auto t, auto full) {
+      using T = decltype(t);
+      constexpr bool F = decltype(full)::value;
+      return go(append_q8_kernel<T, kOne, F>, append_q8_kernel<T, kMany, F>, append_q8_kernel<T, kTwo, F>,
+                append_q8_kernel<T, kFour, F>, append_q8_kernel<T, kEight, F>);
+    };
+    const bool full = a.in_run == 8 && a.out_run == 8;
+    if (dtype == SAGE_F16) e = full ? typed(__half{}, std::true_type{}) : typed(__half{}, std::false_type{});
+    else e = full ? typed(__nv_bfloat16{}, std::true_type{}) : typed(__nv_bfloat16{}, std::false_type{});
   }
   return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "8-bit append");
 }
@@ -558,10 +603,10 @@ int sage_paged_read_q8(const sage_packed* k_out, const sage_packed* v_out, const
     return SAGE_ERR_INVALID_ARG;
   if (check_status_word(workspace, workspace_bytes) != SAGE_OK) return SAGE_ERR_WORKSPACE;
   if (tokens == 0) return SAGE_OK;
-  bool vec = true;
+  int run = 8;
   const sage_packed* t[2] = {k_out, v_out};
   for (int i = 0; i < 2; ++i) {
-    s = check_rows(t[i], tokens, heads_kv, head_dim, true, &vec);
+    s = check_rows(t[i], tokens, heads_kv, head_dim, true, &run);
     if (s != SAGE_OK) return s;
     a.y[i] = t[i]->data;
     a.y_st[i] = t[i]->stride_token;
@@ -580,10 +625,11 @@ int sage_paged_read_q8(const sage_packed* k_out, const sage_packed* v_out, const
   a.rows = a.rows < 1 ? 1 : a.rows > 4 ? 4 : a.rows;
   const dim3 grid((unsigned)(((int64_t)tokens + 4 * a.rows - 1) / (4 * a.rows)), 2);
   if (e == cudaSuccess) {
-    const bool wide = vec && align >= 8;
-    auto go = [&](auto k8, auto k1) { return launch_pdl(wide ? k8 : k1, grid, dim3(128), 0, st, a); };
-    e = dtype == SAGE_F16 ? go(read_q8_kernel<__half, 8>, read_q8_kernel<__half, 1>)
-                          : go(read_q8_kernel<__nv_bfloat16, 8>, read_q8_kernel<__nv_bfloat16, 1>);
+    const int v = run == 8 && align >= 8 ? 8 : run >= 4 && align >= 4 ? 4 : 1;
+    auto go = [&](auto k8, auto k4, auto k1) { return launch_pdl(v == 8 ? k8 : v == 4 ? k4 : k1, grid, dim3(128), 0, st, a); };
+    using B = __nv_bfloat16;
+    e = dtype == SAGE_F16 ? go(read_q8_kernel<__half, 8>, read_q8_kernel<__half, 4>, read_q8_kernel<__half, 1>)
+                          : go(read_q8_kernel<B, 8>, read_q8_kernel<B, 4>, read_q8_kernel<B, 1>);
   }
   return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "8-bit read");
 }

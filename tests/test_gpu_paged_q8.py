@@ -265,6 +265,16 @@ APPENDS = [
     ([0, 9], [5, 6], 2, 16, 4, 1, torch.bfloat16, S8, E4, "NHD"),      # a scale per token
     ([1] * 40, [2] * 40, 5, 128, 8, 4, torch.bfloat16, S8, E4, "HND"),
     ([0, 0], [0, 0], 2, 64, 16, 16, torch.float16, S8, E4, "HND"),
+    ([3, 0, 20], [64, 31, 100], 2, 120, 64, 32, torch.bfloat16, S8, E4, "NHD"),     # a block by two warps
+    ([5, 100, 0], [400, 27, 128], 3, 128, 128, 128, torch.float16, E4, S8, "HND"),  # by eight
+    ([129], [390], 1, 96, 192, 192, torch.bfloat16, S8, S8, "NHD"),
+    ([6, 0, 63], [60, 2, 70], 3, 36, 64, 64, torch.float16, S8, E4, "NHD"),         # runs of four channels
+    ([6, 0, 63], [60, 2, 70], 2, 20, 64, 8, torch.bfloat16, E4, S8, "HND"),
+    ([1, 0, 15, 40], [70, 33, 1, 1], 4, 32, 32, 1, torch.bfloat16, S8, S8, "HND"),  # rows of four lanes
+    ([1, 0, 15, 40], [70, 33, 1, 1], 2, 24, 48, 16, torch.float16, E4, S8, "NHD"),
+    ([30, 2], [80, 200], 2, 32, 64, 64, torch.bfloat16, S8, E4, "HND"),
+    ([30, 2], [80, 200], 2, 12, 40, 40, torch.float16, S8, S8, "NHD"),
+    ([2, 0, 9], [17, 40, 1], 2, 64, 12, 6, torch.bfloat16, S8, E4, "HND"),          # two blocks of six to a window
 ]
 
 
