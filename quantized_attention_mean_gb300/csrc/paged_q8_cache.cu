@@ -379,16 +379,72 @@ __device__ __forceinline__ uint2 values4(uint32_t codes, float scale) {
   return make_uint2(narrow2<T>(f0, f1), narrow2<T>(f2, f3));
 }
 
+// V codes at p as channels at y, or zeros.
+template <typename T, int V, int TYPE>
+struct CodeRun {
+  uint32_t raw[V == 8 ? 2 : 1];
+  float scale;
+  __device__ __forceinline__ void load(const uint8_t* p, const float* s, bool in) {
+    scale = 0.f;
+#pragma unroll
+    for (uint32_t& w : raw) w = 0;
+    if (!in) return;
+    scale = __ldg(s);
+    if constexpr (V == 8) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+      raw[0] = w.x; raw[1] = w.y;
+    } else if constexpr (V == 4) {
+      raw[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    } else {
+      raw[0] = *p;
+    }
+  }
+  __device__ __forceinline__ void store(T* y) const {
+    const uint2 lo = values4<T, TYPE>(raw[0], scale);
+    if constexpr (V == 8) {
+      const uint2 hi = values4<T, TYPE>(raw[1], scale);
+      *reinterpret_cast<uint4*>(y) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    } else if constexpr (V == 4) {
+      *reinterpret_cast<uint2*>(y) = lo;
+    } else {
+      *reinterpret_cast<uint16_t*>(y) = (uint16_t)lo.x;
+    }
+  }
+};
+
 // Rows t0 .. of K or V: lane j knows where row j's codes and first scale lie (no row: -1).
 template <typename T, int V, int TYPE>
 __device__ __forceinline__ void copy_rows(const ReadArgs& a, int kv, int64_t t0, int n_rows, long long code_at, long long scale_at) {
   const PagedView& c = a.q.c;
   const int lane = threadIdx.x & 31;
-  const int64_t sh = kv ? c.v_sh : c.k_sh;
+  const int64_t sh = kv ? c.v_sh : c.k_sh, ys = a.y_st[kv];
   const uint8_t* codes = static_cast<const uint8_t*>(kv ? c.v : c.k);
   const float* scales = kv ? a.q.vs : a.q.ks;
+  T* const y = static_cast<T*>(a.y[kv]) + t0 * ys;
   const int runs = (c.d + V - 1) / V, n = c.hkv * runs;
-  constexpr int kWords = V >= 4 ? V / 4 : 1;
+  CodeRun<T, V, TYPE> run[2];
+  if (n <= 32) {
+    // short rows: the lanes take the runs of several, two each
+    const int side = 32 / n, g = lane / n, x = lane - g * n, h = x / runs, ch = (x - h * runs) * V;
+    const uint8_t* src = codes + h * sh + ch;
+    const float* sc = scales + (int64_t)h * a.q.blocks;
+    T* const dst = y + h * a.y_sh[kv] + ch;
+#pragma unroll 1
+    for (int j0 = 0; j0 < n_rows; j0 += 2 * side) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int j = j0 + u * side + g;
+        const long long at = __shfl_sync(0xffffffffu, code_at, j & 31), sat = __shfl_sync(0xffffffffu, scale_at, j & 31);
+        run[u].load(src + at, sc + sat, j < n_rows && at >= 0);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int j = j0 + u * side + g;
+        if (g < side && j < n_rows) run[u].store(dst + j * ys);
+      }
+    }
+    return;
+  }
   for (int x0 = 0; x0 < n; x0 += 64) {
     // two runs of a row for each lane
     const uint8_t* src[2];
@@ -401,44 +457,17 @@ __device__ __forceinline__ void copy_rows(const ReadArgs& a, int kv, int64_t t0,
       on[u] = x < n;
       src[u] = codes + h * sh + ch;
       sc[u] = scales + (int64_t)h * a.q.blocks;
-      dst[u] = static_cast<T*>(a.y[kv]) + t0 * a.y_st[kv] + h * a.y_sh[kv] + ch;
+      dst[u] = y + h * a.y_sh[kv] + ch;
     }
 #pragma unroll 1
     for (int j = 0; j < n_rows; ++j) {
       const long long at = __shfl_sync(0xffffffffu, code_at, j), sat = __shfl_sync(0xffffffffu, scale_at, j);
-      uint32_t raw[2][kWords];
-      float scale[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) run[u].load(src[u] + at, sc[u] + sat, on[u] && at >= 0);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        scale[u] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) raw[u][i] = 0;
-        if (on[u] && at >= 0) {
-          const uint8_t* p = src[u] + at;
-          scale[u] = __ldg(sc[u] + sat);
-          if constexpr (V == 8) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-            raw[u][0] = w.x; raw[u][1] = w.y;
-          } else if constexpr (V == 4) {
-            raw[u][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-          } else {
-            raw[u][0] = *p;
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (on[u]) {
-          if constexpr (V == 8) {
-            const uint2 lo = values4<T, TYPE>(raw[u][0], scale[u]), hi = values4<T, TYPE>(raw[u][1], scale[u]);
-            *reinterpret_cast<uint4*>(dst[u]) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-          } else if constexpr (V == 4) {
-            *reinterpret_cast<uint2*>(dst[u]) = values4<T, TYPE>(raw[u][0], scale[u]);
-          } else {
-            *reinterpret_cast<uint16_t*>(dst[u]) = (uint16_t)values4<T, TYPE>(raw[u][0], scale[u]).x;
-          }
-        }
-        dst[u] += a.y_st[kv];
+        if (on[u]) run[u].store(dst[u]);
+        dst[u] += ys;
       }
     }
   }
@@ -621,11 +650,13 @@ int sage_paged_read_q8(const sage_packed* k_out, const sage_packed* v_out, const
   cudaError_t e = cudaSuccess;
   if (a.err) e = launch_pdl(clear_status_kernel, dim3(1), dim3(1), 0, st, a.err);
   // rows of a warp: as many as leave some warps for each SM
+  const int v = run == 8 && align >= 8 ? 8 : run >= 4 && align >= 4 ? 4 : 1;
+  const int runs = heads_kv * ((head_dim + v - 1) / v), most = runs <= 32 ? 8 * (32 / runs) : 4;
   a.rows = tokens / (152 * 16);
-  a.rows = a.rows < 1 ? 1 : a.rows > 4 ? 4 : a.rows;
+  a.rows = a.rows < 1 ? 1 : a.rows > most ? most : a.rows;
+  if (a.rows > 32) a.rows = 32;
   const dim3 grid((unsigned)(((int64_t)tokens + 4 * a.rows - 1) / (4 * a.rows)), 2);
   if (e == cudaSuccess) {
-    const int v = run == 8 && align >= 8 ? 8 : run >= 4 && align >= 4 ? 4 : 1;
     auto go = [&](auto k8, auto k4, auto k1) { return launch_pdl(v == 8 ? k8 : v == 4 ? k4 : k1, grid, dim3(128), 0, st, a); };
     using B = __nv_bfloat16;
     e = dtype == SAGE_F16 ? go(read_q8_kernel<__half, 8>, read_q8_kernel<__half, 4>, read_q8_kernel<__half, 1>)
