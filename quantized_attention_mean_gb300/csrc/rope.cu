@@ -123,6 +123,23 @@ __device__ __forceinline__ void slot_runs(const RopeArgs& a, int x, int (&c)[2],
   on[1] = c[1] < a.d;
 }
 
+// N floats from shared memory, at a multiple of N floats (N >= 4: of four).
+template <int N>
+__device__ __forceinline__ void copy_run(float* to, const float* from) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(from + i);
+      to[i] = f.x; to[i + 1] = f.y; to[i + 2] = f.z; to[i + 3] = f.w;
+    }
+  } else if constexpr (N == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(from);
+    to[0] = f.x; to[1] = f.y;
+  } else {
+    to[0] = *from;
+  }
+}
+
 // Two 16-bit values of a register.
 template <typename T>
 __device__ __forceinline__ void widen2(uint32_t x, float& lo, float& hi) {
@@ -146,7 +163,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
   using R = typename Run<T, V>::type;
   constexpr int kAhead = V == 8 ? 4 : 2, N = SLOTS * V / 2;  // N: pairs of a lane, two by two
   __shared__ unsigned long long s_turns[kMaxPairs];
-  __shared__ float2 s_cs[kRopeWarps][kMaxPairs];
+  __shared__ __align__(16) float2 s_cs[kRopeWarps][128];  // of the channels' pairs, (1, 0) past the turned ones
   __shared__ __align__(16) float s_w[2][128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pairs = a.rot / 2;
@@ -158,11 +175,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
     f -= floor(f);
     s_turns[k] = __double2ull_rn(f * 18446744073709551616.0);
   }
-  for (int k = threadIdx.x; k < 2 * a.d; k += kRopeWarps * 32) {
-    const int i = k >= a.d, c = k - i * a.d;
+  for (int k = threadIdx.x; k < 256; k += kRopeWarps * 32) {
+    const int i = k >> 7, c = k & 127;
     const void* w = a.w[i];
-    s_w[i][c] = !w ? 1.f : a.w32 ? __ldg(static_cast<const float*>(w) + c) : to_f32<T>(static_cast<const T*>(w)[c]);
+    s_w[i][c] = c >= a.d ? 0.f : !w ? 1.f : a.w32 ? __ldg(static_cast<const float*>(w) + c) : to_f32<T>(static_cast<const T*>(w)[c]);
   }
+  for (int k = pairs + lane; k < 128; k += 32) s_cs[warp][k] = make_float2(1.f, 0.f);
   __syncthreads();
   const int lanes = LANES ? LANES : a.lanes;
   const int sub = lane % lanes, row = lane / lanes, rows = 32 / lanes;  // (lanes of no row: 32 is no multiple of five)
@@ -239,28 +257,40 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
         y_stride = rows * a.ys[w][2];
         left = w ? nk : nq;
         live = left - row;
-        auto turn = [&](int e, float& i0, float& j0, float& j1, float& i1) {
-          // the e-th pair of a lane: channels e of both runs of a slot, or two neighbours of one of them
-          const int s = e / V, v = e % V;
-          const int u0 = PAIRS && V > 1 ? v / (V > 1 ? V / 2 : 1) : 0, u1 = PAIRS && V > 1 ? u0 : 1;
-          const int e0 = PAIRS && V > 1 ? 2 * v % V : v, e1 = PAIRS && V > 1 ? e0 + 1 : v;
-          const int ci = c[s][u0] + e0, cj = c[s][u1] + e1, pr = PAIRS ? ci / 2 : ci;
-          const float2 t = pr < pairs ? s_cs[warp][pr] : make_float2(1.f, 0.f);
-          const float wi = on[s][u0] ? s_w[w][ci] : 0.f, wj = on[s][u1] ? s_w[w][cj] : 0.f;
-          i0 = wi * t.x;
-          j0 = -wj * t.y;
-          j1 = wj * t.x;
-          i1 = wi * t.y;
+        // weights of a run and cosines and sines of the pairs that follow one another from k on (neither leaves its array:
+        // slots past the row end below channel 128 too)
+        float p[4][SLOTS * V];
+        auto put = [&](int e, float wi, float wj, const float2& t) {
+          p[0][e] = wi * t.x;
+          p[1][e] = -wj * t.y;
+          p[2][e] = wj * t.x;
+          p[3][e] = wi * t.y;
         };
 #pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+          float wt[2][V];
+          copy_run<V>(wt[0], &s_w[w][c[s][0]]);
+          copy_run<V>(wt[1], &s_w[w][c[s][1]]);
+          float2 t[V];
+          if constexpr (PAIRS && V > 1) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              copy_run<V>(reinterpret_cast<float*>(t), &s_cs[warp][c[s][u] / 2].x);
+#pragma unroll
+              for (int z = 0; z < V / 2; ++z) put(s * V + u * (V / 2) + z, wt[u][2 * z], wt[u][2 * z + 1], t[z]);
+            }
+          } else {
+            copy_run<2 * V>(reinterpret_cast<float*>(t), &s_cs[warp][PAIRS ? c[s][0] / 2 : c[s][0]].x);
+#pragma unroll
+            for (int z = 0; z < V; ++z) put(s * V + z, wt[0][z], wt[1][z], t[z]);
+          }
+        }
+#pragma unroll
         for (int e = 0; e < N; ++e) {
-          float p0, p1, p2, p3, q0, q1, q2, q3;
-          turn(2 * e, p0, p1, p2, p3);
-          turn(2 * e + 1, q0, q1, q2, q3);
-          ca[e] = make_pair2(p0, q0);
-          cb[e] = make_pair2(p1, q1);
-          da[e] = make_pair2(p2, q2);
-          db[e] = make_pair2(p3, q3);
+          ca[e] = make_pair2(p[0][2 * e], p[0][2 * e + 1]);
+          cb[e] = make_pair2(p[1][2 * e], p[1][2 * e + 1]);
+          da[e] = make_pair2(p[2][2 * e], p[2][2 * e + 1]);
+          db[e] = make_pair2(p[3][2 * e], p[3][2 * e + 1]);
         }
       }
 #pragma unroll
