@@ -12,7 +12,7 @@
 // lose an angle at position 2^20 by 0.06. All arithmetic on values is in 32 bits, rounded once.
 //
 // 8192 tokens of 32 + 8 heads, head_dim 128, bf16 (168 MB): 31.4 us, 5.35 TB/s, 79% of a copy; 64 tokens: 4.2 us of GPU time.
-// 8194 tokens of 16 + 16 heads, head_dim 72, 36 channels in neighbouring pairs (76 MB): 23.8 us, since a row of 72 channels leaves
+// 8194 tokens of 16 + 16 heads, head_dim 72, 36 channels in neighbouring pairs (76 MB): 21.9 us, since a row of 72 channels leaves
 // two lanes of 32 and a seventh of the others idle and a token's sines and products serve fewer channels.
 #include <cmath>
 
