@@ -211,10 +211,11 @@ __device__ __forceinline__ float4 ld_rank4(uint32_t addr) {
 
 // ------------------------------------------------------------------------------------- join
 // One CTA per (row block of a head, sequence), or per 32 of its channels: the results that lie in several ranges summed in
-// the order of the ranges; sequences that hold nothing get 0 and -inf. CTA (0, 0) also collects the status.
+// the order of the ranges; sequences that hold nothing get 0 and -inf. CTA (0, 0) also collects the status. AVERAGES: pieces
+// are averages of their values instead of sums in their frames (an 8-bit cache's values go up to fp32's largest, sums beyond).
 constexpr int kJoinThreads = 256;
 
-template <typename T, int DP, int CTAS>
+template <typename T, int DP, int CTAS, bool AVERAGES = false>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) {
   __shared__ float s_w[CTAS][kRows];       // weight of each range's piece
   __shared__ int s_at[CTAS];               // and its first row
@@ -317,11 +318,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
     for (int p = lane; p < parts; p += 32) {
       const float2 y = *reinterpret_cast<const float2*>(a.part_ml + (s_at[p] + r) * 2);
       const float w = ex2_approx(y.x - u);
-      s_w[p][r] = w;
+      s_w[p][r] = AVERAGES ? y.y * w : w;
       l += y.y * w;
     }
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+    if constexpr (AVERAGES) {
+      const float inv = l != 0.f ? 1.0f / l : 0.f;
+      for (int p = lane; p < parts; p += 32) s_w[p][r] *= inv;
+    }
     if (lane == 0) { s_m[r] = m; s_l[r] = l; }
   }
   __syncthreads();
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
         }
     }
     if (on && set == 0) {
-      const float inv = s_l[r] != 0.f ? 1.0f / s_l[r] : 0.f;
+      const float inv = AVERAGES ? 1.0f : s_l[r] != 0.f ? 1.0f / s_l[r] : 0.f;
       T* dst = static_cast<T*>(a.o) + b * a.o_sb + (row0 + r) * a.o_sh + c;
       const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll

@@ -247,6 +247,11 @@ __device__ __forceinline__ void store_run(const Q8Args& p, int64_t at, int left,
   }
 }
 
+// The clusters' sums, of up to 2^14 weights of up to 2^8 each (the running maximum may lag so far), lie in fp32 whatever the
+// values are once they are taken down by
+constexpr float kSumDown = 0x1p-22f;
+static_assert(8 * kRanks * Q8Cfg<64, 1>::kTile <= 1 << 14 && 8 * kRanks * Q8Cfg<128, 1>::kTile <= 1 << 14, "keys of a cluster");
+
 // DP: bytes of a row in shared memory; KS: units of 16 channels that the products take.
 template <int KT, int VT, int DP, int NH, int KS>
 __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
@@ -706,7 +711,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
 #pragma unroll
               for (int i = 0; i < kRun; ++i) y[i] = fmaf(f, from[i], y[i]);
             }
-            const float g = ex2_approx(ff - mu), f = whole ? (ll != 0.f ? g / ll : 0.f) : g;
+            const float f = ll != 0.f ? __fdividef(ex2_approx(ff - mu), ll) : 0.f;  // (a part is an average too: its sum may pass fp32)
             const int row = (hg * side + t) * a.group + rb * kRows + r;
             if (whole) {
               store_run<kRun>(p, cu.b * a.o_sb + (int64_t)row * a.o_sh + c, a.c.d - c, y, f);
@@ -747,7 +752,8 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
           if (r < rows) {
 #pragma unroll
             for (int u = 0; u < KS; ++u)
-              *reinterpret_cast<float2*>(mine + r * DP + u * 16 + 2 * r0) = make_float2(o[u][x][e] * f, o[u][x][2 + e] * f);
+              *reinterpret_cast<float2*>(mine + r * DP + u * 16 + 2 * r0) =
+                  make_float2(o[u][x][e] * kSumDown * f, o[u][x][2 + e] * kSumDown * f);
           }
         }
         if (r0 == 0) ml[warp * kRows + r] = fresh ? make_float4(-INFINITY, 0.f, 0.f, 0.f) : make_float4(m[x][e], l[x][e], 0.f, 0.f);
@@ -775,7 +781,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
           acc.z = fmaf(w, y.z, acc.z); acc.w = fmaf(w, y.w, acc.w);
         }
       }
-      const float inv = ll != 0.f ? 1.0f / ll : 0.f;
+      const float inv = ll != 0.f ? 1.0f / (ll * kSumDown) : 0.f;
       const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
       const int64_t to = (int64_t)blockIdx.y * a.o_sb + (int64_t)(row0 + r) * a.o_sh + c;
 #pragma unroll
@@ -810,8 +816,8 @@ cudaError_t launch_q8_t(const Q8Args& p, const CUtensorMap* maps, cudaStream_t s
     e = launch_pdl(q8_decode_kernel<KT, VT, DP, NH, KS>, dim3(C::kRanges), dim3(kWarps * 32), C::kSmem, st, maps[0], maps[1], p);
     if (e != cudaSuccess) return e;
     const dim3 grid(heads * a.slices, a.c.batch);
-    return p.bf16 ? launch_pdl(join_kernel<__nv_bfloat16, DP, C::kRanges>, grid, dim3(kJoinThreads), 0, st, a)
-                  : launch_pdl(join_kernel<__half, DP, C::kRanges>, grid, dim3(kJoinThreads), 0, st, a);
+    return p.bf16 ? launch_pdl(join_kernel<__nv_bfloat16, DP, C::kRanges, true>, grid, dim3(kJoinThreads), 0, st, a)
+                  : launch_pdl(join_kernel<__half, DP, C::kRanges, true>, grid, dim3(kJoinThreads), 0, st, a);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(heads * kRanks, a.c.batch);

@@ -101,6 +101,22 @@ def test_scales_of_very_different_blocks(d, kt, vt, bound):
     assert_close(lse, r["lse"], r["lse_tol"], "lse")
 
 
+@pytest.mark.parametrize("lens,bound", [([700, 81], 700), ([700, 81], 10 ** 5), ([20001, 3], 20001)])
+@pytest.mark.parametrize("d,hq,vt", [(64, 6, E4), (128, 24, S8)])
+def test_values_near_the_largest(d, hq, vt, lens, bound):
+    # values of 2^127, as 16-bit ones may be: their sums pass fp32, their averages do not
+    import quantized_attention_mean_gb300 as qa
+    c = q8.make_cache(lens, 2, d, 16, 16, S8, vt, seed=d)
+    c["v"] = q8.to_codes(torch.randint(100, 128, c["v"].shape, generator=torch.Generator().manual_seed(d)).float(), vt)
+    c["vs"].fill_(2.0 ** 120)
+    q = torch.randn(2, hq, d, generator=torch.Generator().manual_seed(1)).bfloat16()
+    G = on_gpu(c)
+    out, lse = qa.paged_attn_q8(q.to(DEV), *planes(G), G["table"], G["lens"], bound, return_lse=True)
+    r = q8.attend(c, q, d ** -0.5, hkv=2)
+    assert_close(out, r["out"], r["out_tol"], "out")
+    assert_close(lse, r["lse"], r["lse_tol"], "lse")
+
+
 def test_queries_of_every_size():
     # rows of q far above and below fp16's range, and of channels of very different sizes
     import quantized_attention_mean_gb300 as qa
