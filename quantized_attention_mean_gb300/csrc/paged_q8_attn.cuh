@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
       }
       // ---- scores in base 2; s[g][x][2 b + e]: key 16 g + 8 b + r0, head 8 x + 2 j + e
       float sv[M][2];  // V's scales
-      float most = 0.f, least = INFINITY;
+      float most = 0.f;
 #pragma unroll
       for (int g = 0; g < M; ++g)
 #pragma unroll
@@ -521,7 +521,6 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
           const float ks = sc[k0 + g * 16 + b * 8 + r0];
           sv[g][b] = sc[C::kKeys + k0 + g * 16 + b * 8 + r0];
           most = fmaxf(most, sv[g][b]);
-          least = fminf(least, sv[g][b]);
 #pragma unroll
           for (int x = 0; x < NH; ++x)
 #pragma unroll
@@ -557,8 +556,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
             for (int e = 0; e < 4; ++e)
               if (key0 + k0 + g * 16 + (e >> 1) * 8 + r0 >= cu.len) s[g][x][e] = -INFINITY;
       }
-      // largest score t, and largest t + log2 s_v: an upper bound by the largest scale, which where a lane's scales lie
-      // within 2^8 is at most so much too large, otherwise exactly
+      // a lane's largest score t, and a bound of its t + log2 s_v: the largest score with the largest scale
       const float lv = fmaxf(lg2_approx(most), kLeastLog);
       float tm[NH][2], um[NH][2];
 #pragma unroll
@@ -570,21 +568,6 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
           for (int g = 1; g < M; ++g) tm[x][e] = max3(tm[x][e], s[g][x][e], s[g][x][2 + e]);
           um[x][e] = tm[x][e] + lv;
         }
-      if (__any_sync(0xffffffffu, least * 256.0f < most)) {
-#pragma unroll
-        for (int x = 0; x < NH; ++x) um[x][0] = um[x][1] = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < M; ++g)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const float l2 = fmaxf(lg2_approx(sv[g][b]), kLeastLog);
-#pragma unroll
-            for (int x = 0; x < NH; ++x) {
-              um[x][0] = fmaxf(um[x][0], s[g][x][2 * b] + l2);
-              um[x][1] = fmaxf(um[x][1], s[g][x][2 * b + 1] + l2);
-            }
-          }
-      }
       // ---- frames of the sum (m) and of the weights (F, kHead below the largest): the eight lanes of a head agree. They
       // are kept unless a maximum grew by more than 8, so sums and O are rescaled rarely
       bool grows = false;
@@ -594,6 +577,26 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
         for (int e = 0; e < 2; ++e)
           grows |= tm[x][e] > m[x][e] + 8.0f || um[x][e] > F[x][e] + (8.0f + kHead);
       if (__any_sync(0xffffffffu, grows)) {
+        // (the bound may say so in vain, where a lane's scales lie far apart; a frame follows what there is: with weights below
+        // 2^kHead of the largest, small ones lose their bits)
+        float least = sv[0][0];
+#pragma unroll
+        for (int g = 0; g < M; ++g) least = fminf(least, fminf(sv[g][0], sv[g][1]));
+        if (__any_sync(0xffffffffu, least < most)) {
+#pragma unroll
+          for (int x = 0; x < NH; ++x) um[x][0] = um[x][1] = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < M; ++g)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float l2 = fmaxf(lg2_approx(sv[g][b]), kLeastLog);
+#pragma unroll
+              for (int x = 0; x < NH; ++x) {
+                um[x][0] = fmaxf(um[x][0], s[g][x][2 * b] + l2);
+                um[x][1] = fmaxf(um[x][1], s[g][x][2 * b + 1] + l2);
+              }
+            }
+        }
 #pragma unroll
         for (int x = 0; x < NH; ++x)
 #pragma unroll

@@ -117,6 +117,38 @@ def test_values_near_the_largest(d, hq, vt, lens, bound):
     assert_close(lse, r["lse"], r["lse_tol"], "lse")
 
 
+@pytest.mark.parametrize("bound", [2000, 10 ** 5])
+@pytest.mark.parametrize("d,hq,vt", [(64, 8, E4), (64, 16, S8), (128, 8, S8), (128, 16, E4)])
+def test_a_sink_with_a_small_scale_before_a_long_tail(d, hq, vt, bound):
+    # one key of 32 draws nearly all attention and adds nothing; V scales beside it are 2^8 of its own, at keys of no weight; the
+    # others, 2^-18 to 2^-22 of its weight and all alike, make the result: their weights keep their bits beside the sink's
+    import quantized_attention_mean_gb300 as qa
+    lens = [2000, 320]
+    c = q8.make_cache(lens, 1, d, 16, 1, S8, vt, seed=d + hq)
+    k = torch.zeros(c["k"].shape)
+    v = torch.randint(1, 100, c["v"].shape, generator=torch.Generator().manual_seed(d)).float()
+    c["ks"].fill_(20 * math.log(2) * d ** 0.5 / (100 * 64))             # 100 of channel 0, where q is 64: 20 in base 2
+    c["vs"].fill_(2.0 ** 4)
+    for b, n in enumerate(lens):
+        for t in range(0, n, 8):
+            p, s = int(c["table"][b, t // 16]), t % 16
+            if t % 32 == 0:
+                k[p, :, s, 0] = 100
+                v[p, :, s] = 0
+            else:
+                k[p, :, s, 0] = -127
+                c["vs"][p, :, s] = 2.0 ** 12
+    c["k"], c["v"] = q8.to_codes(k, S8), q8.to_codes(v, vt)
+    q = torch.zeros(2, hq, d)
+    q[..., 0] = 58 + torch.arange(hq) * (14 / hq)
+    q = q.half()
+    G = on_gpu(c)
+    out, lse = qa.paged_attn_q8(q.to(DEV), *planes(G), G["table"], G["lens"], bound, return_lse=True)
+    r = q8.attend(c, q, d ** -0.5)
+    assert_close(out, r["out"], r["out_tol"], "out")
+    assert_close(lse, r["lse"], r["lse_tol"], "lse")
+
+
 def test_queries_of_every_size():
     # rows of q far above and below fp16's range, and of channels of very different sizes
     import quantized_attention_mean_gb300 as qa
