@@ -38,7 +38,7 @@ struct DecodeArgs {
   int* err;                 // status word, or null (no workspace: the clusters' form without mass)
   int* cta_err;             // [kCtas]
   float* part_o;            // [ranges][2][side][part_rows][dp]
-  float* part_ml;           // [ranges][2][side][part_rows][2]
+  float* part_ml;           // [ranges][2][side][part_rows][2], or [4] with FRAMES
   float* lse2;              // [batch, hq], base 2 (with mass)
   float* scores;            // [batch, hq, score_pitch], base 2 (with mass) or null
   int64_t score_pitch;
@@ -211,15 +211,15 @@ __device__ __forceinline__ float4 ld_rank4(uint32_t addr) {
 
 // ------------------------------------------------------------------------------------- join
 // One CTA per (row block of a head, sequence), or per 32 of its channels: the results that lie in several ranges summed in
-// the order of the ranges; sequences that hold nothing get 0 and -inf. CTA (0, 0) also collects the status. AVERAGES: pieces
-// are averages of their values instead of sums in their frames (an 8-bit cache's values go up to fp32's largest, sums beyond).
+// the order of the ranges; sequences that hold nothing get 0 and -inf. CTA (0, 0) also collects the status. FRAMES: a
+// piece's accumulator has a frame of its own besides that of the sum of its weights.
 constexpr int kJoinThreads = 256;
 
-template <typename T, int DP, int CTAS, bool AVERAGES = false>
+template <typename T, int DP, int CTAS, bool FRAMES = false>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) {
   __shared__ float s_w[CTAS][kRows];       // weight of each range's piece
   __shared__ int s_at[CTAS];               // and its first row
-  __shared__ float s_m[kRows], s_l[kRows];
+  __shared__ float s_m[kRows], s_l[kRows], s_f[kRows];
   __shared__ __align__(16) float s_acc[kJoinThreads * 4];
   __shared__ long long s_before[kJoinThreads / 32], s_all[kJoinThreads / 32];
   const int heads = a.c.hkv / a.side * a.row_blocks;
@@ -309,25 +309,32 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
   fetch(0);
   // row statistics: one warp per row
   for (int r = warp; r < rows; r += kJoinThreads / 32) {
-    float m = -INFINITY;
-    for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_ml[(s_at[p] + r) * 2]);
+    constexpr int kStats = FRAMES ? 4 : 2;
+    float m = -INFINITY, f = -INFINITY;
+    for (int p = lane; p < parts; p += 32) {
+      m = fmaxf(m, a.part_ml[(s_at[p] + r) * kStats]);
+      if (FRAMES) f = fmaxf(f, a.part_ml[(s_at[p] + r) * kStats + 2]);
+    }
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-    const float u = m == -INFINITY ? 0.f : m;
+    for (int w = 16; w > 0; w >>= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+      if (FRAMES) f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, w));
+    }
+    const float u = m == -INFINITY ? 0.f : m, fu = f == -INFINITY ? 0.f : f;
     float l = 0.f;
     for (int p = lane; p < parts; p += 32) {
-      const float2 y = *reinterpret_cast<const float2*>(a.part_ml + (s_at[p] + r) * 2);
+      const float2 y = *reinterpret_cast<const float2*>(a.part_ml + (s_at[p] + r) * kStats);
       const float w = ex2_approx(y.x - u);
-      s_w[p][r] = AVERAGES ? y.y * w : w;
+      s_w[p][r] = FRAMES ? ex2_approx(a.part_ml[(s_at[p] + r) * kStats + 2] - fu) : w;
       l += y.y * w;
     }
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-    if constexpr (AVERAGES) {
-      const float inv = l != 0.f ? 1.0f / l : 0.f;
-      for (int p = lane; p < parts; p += 32) s_w[p][r] *= inv;
+    if (lane == 0) {
+      s_m[r] = m;
+      s_l[r] = l;
+      if (FRAMES) s_f[r] = l != 0.f ? ex2_approx(fu - u) / l : 0.f;
     }
-    if (lane == 0) { s_m[r] = m; s_l[r] = l; }
   }
   __syncthreads();
   for (int base = 0; base < cells; base += kJoinThreads) {
@@ -362,7 +369,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
         }
     }
     if (on && set == 0) {
-      const float inv = AVERAGES ? 1.0f : s_l[r] != 0.f ? 1.0f / s_l[r] : 0.f;
+      const float inv = FRAMES ? s_f[r] : s_l[r] != 0.f ? 1.0f / s_l[r] : 0.f;
       T* dst = static_cast<T*>(a.o) + b * a.o_sb + (row0 + r) * a.o_sh + c;
       const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll

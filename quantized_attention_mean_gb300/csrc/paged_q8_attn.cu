@@ -37,7 +37,7 @@ bool q8_layout(int batch, int hq, int hkv, int64_t max_len, int d, Q8Layout* L) 
   L->part_o = L->err + (line ? up256(4 * kMostRanges) : 0);
   const size_t rows = line ? (size_t)kMostRanges * 2 * 4 * (hq / hkv <= 8 ? 8 : kRows) : 0;
   L->part_ml = L->part_o + up256(rows * dp * 4);
-  L->total = L->part_ml + up256(rows * 2 * 4);
+  L->total = L->part_ml + up256(rows * 4 * 4);
   return true;
 }
 

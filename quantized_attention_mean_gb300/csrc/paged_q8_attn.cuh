@@ -247,11 +247,6 @@ __device__ __forceinline__ void store_run(const Q8Args& p, int64_t at, int left,
   }
 }
 
-// The clusters' sums, of up to 2^14 weights of up to 2^8 each (the running maximum may lag so far), lie in fp32 whatever the
-// values are once they are taken down by
-constexpr float kSumDown = 0x1p-22f;
-static_assert(8 * kRanks * Q8Cfg<64, 1>::kTile <= 1 << 14 && 8 * kRanks * Q8Cfg<128, 1>::kTile <= 1 << 14, "keys of a cluster");
-
 // DP: bytes of a row in shared memory; KS: units of 16 channels that the products take.
 template <int KT, int VT, int DP, int NH, int KS>
 __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
@@ -259,6 +254,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
   using C = Q8Cfg<DP, NH>;
   constexpr int S = C::kStages, M = C::kStep / 16, NP = C::kKeys / 32;
   constexpr float kHead = 7.0f;  // weights are held at up to 2^(7 + 8), so that the smallest keep their bits in fp16
+  constexpr float kLeastFrame = -3.4028234e38f;  // of no key: finite, so that differences are numbers
   constexpr float kLeastLog = -110.0f;  // smaller scales do not lower the frame of the weights, which stays finite
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ int s_err[kWarps];
@@ -383,6 +379,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
   uint32_t qf[KS][NH][2];
   int qpos = 0, rows = 0, row0 = 0, tile0 = 0, pieces = 0;
   bool fresh = true;
+  float gap = 0.f;
   if (p.cluster) {
     const int rb = cu.h % a.row_blocks;
     row0 = cu.h / a.row_blocks * a.group + rb * kRows;
@@ -447,7 +444,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
           qs[x][e2] = __shfl_sync(0xffffffffu, down, (2 * j + e2) * 4) * factor;
           const int rr = x * 8 + 2 * j + e2;
           sl[x][e2] = a.slopes && rr < rows ? __ldg(&a.slopes[row0 + rr]) * kLog2eF : 0.f;
-          m[x][e2] = F[x][e2] = -INFINITY;
+          m[x][e2] = F[x][e2] = kLeastFrame;
           l[x][e2] = 0.f;
         }
 #pragma unroll
@@ -568,17 +565,18 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
           for (int g = 1; g < M; ++g) tm[x][e] = max3(tm[x][e], s[g][x][e], s[g][x][2 + e]);
           um[x][e] = tm[x][e] + lv;
         }
-      // ---- frames of the sum (m) and of the weights (F, kHead below the largest): the eight lanes of a head agree. They
-      // are kept unless a maximum grew by more than 8, so sums and O are rescaled rarely
-      bool grows = false;
+      // ---- frames of the sum (m) and of the weights (F, kHead below the largest); `gap`: the largest m - F. The eight lanes of a
+      // head agree. Frames are kept unless a maximum grew by more than 8, so sums and O are rescaled rarely
+      const float top = fminf(100.0f - lv, 126.0f);
+      bool grows = gap > top, far = false;
 #pragma unroll
       for (int x = 0; x < NH; ++x)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           grows |= tm[x][e] > m[x][e] + 8.0f || um[x][e] > F[x][e] + (8.0f + kHead);
       if (__any_sync(0xffffffffu, grows)) {
-        // (the bound may say so in vain, where a lane's scales lie far apart; a frame follows what there is: with weights below
-        // 2^kHead of the largest, small ones lose their bits)
+        // (the bound may say so in vain where a lane's scales differ; a frame above the largest weight would cost the small ones
+        // their bits)
         float least = sv[0][0];
 #pragma unroll
         for (int g = 0; g < M; ++g) least = fminf(least, fminf(sv[g][0], sv[g][1]));
@@ -622,16 +620,40 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
               }
             }
           }
+        gap = m[0][0] - F[0][0];
+#pragma unroll
+        for (int x = 0; x < NH; ++x)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) gap = fmaxf(gap, m[x][e] - F[x][e]);
+        far = __any_sync(0xffffffffu, gap > top);
+        if (far) {
+          // the sums; then t + log2 s_v - F - 100 in the place of t - m, which adds nothing to them, and 2^100 in that of the scale
+#pragma unroll
+          for (int g = 0; g < M; ++g)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float l2 = lg2_approx(sv[g][b]) - 100.0f;
+              sv[g][b] = 0x1p100f;
+#pragma unroll
+              for (int x = 0; x < NH; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float& t = s[g][x][2 * b + e];
+                  l[x][e] += ex2_approx(t - m[x][e]);
+                  t = t + (m[x][e] - F[x][e]) + l2;
+                }
+            }
+        }
       }
       // ---- weights p = 2^(t - m): their sum in 32 bits; as p s_v 2^(m - F) rounded once, keys and heads exchanged, the B
-      // operand. (The factor is kept where its product with the largest scale is finite: it passes 2^100 only where all
-      // of the tile's p are below 2^-85)
+      // operand. That product is good while 2^(m - F) times the largest scale stays below 2^100: p too small for fp32 are then
+      // too small for fp16 as weights. Past that (`far`: scales that outweigh scores 85 and more below the top one) weights are
+      // formed as 2^(t + log2 s_v - F), which the logarithm puts off by 2^-15 at most
       uint32_t pf[M][NH][2];
 #pragma unroll
       for (int x = 0; x < NH; ++x) {
-        const float m0 = m[x][0] == -INFINITY ? 0.f : m[x][0], m1 = m[x][1] == -INFINITY ? 0.f : m[x][1];
-        const float top = fminf(100.0f - lv, 126.0f);
-        const float g0 = ex2_approx(fminf(m0 - F[x][0], top)), g1 = ex2_approx(fminf(m1 - F[x][1], top));
+        const float m0 = m[x][0], m1 = m[x][1];
+        const float g0 = ex2_approx(m0 - (far ? m0 : F[x][0])), g1 = ex2_approx(m1 - (far ? m1 : F[x][1]));
 #pragma unroll
         for (int g = 0; g < M; ++g)
 #pragma unroll
@@ -714,7 +736,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
 #pragma unroll
               for (int i = 0; i < kRun; ++i) y[i] = fmaf(f, from[i], y[i]);
             }
-            const float f = ll != 0.f ? __fdividef(ex2_approx(ff - mu), ll) : 0.f;  // (a part is an average too: its sum may pass fp32)
+            const float f = !whole ? 1.0f : ll != 0.f ? ex2_approx(ff - mu) / ll : 0.f;
             const int row = (hg * side + t) * a.group + rb * kRows + r;
             if (whole) {
               store_run<kRun>(p, cu.b * a.o_sb + (int64_t)row * a.o_sh + c, a.c.d - c, y, f);
@@ -724,7 +746,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
 #pragma unroll
               for (int i = 0; i < kRun; i += 4)
                 *reinterpret_cast<float4*>(a.part_o + at * DP + c + i) = make_float4(y[i] * f, y[i + 1] * f, y[i + 2] * f, y[i + 3] * f);
-              if (c == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(mm, ll);
+              if (c == 0) *reinterpret_cast<float4*>(a.part_ml + at * 4) = make_float4(mm, ll, ff, 0.f);
             }
           }
         }
@@ -737,8 +759,9 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
     next_item(a, a.tile_shift, heads, cu);
   }
   if (p.cluster) {
-    // every warp's accumulator into its own ring, its statistics beside; then each thread of the
-    // cluster sums one group of four channels of a row over all warps of all ranks, in their order
+    // every warp's accumulator into its own ring, its statistics beside; then each thread of the cluster sums one group of
+    // four channels of a row over all warps of all ranks, in their order
+    constexpr int kParts = kRanks * kWarps, kLanes = DP / 4;  // kLanes: of a row
     const int rank = me % kRanks;
     cp_async_wait<0>();
     __syncwarp();
@@ -749,48 +772,66 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<DP, NH>::kPerSm)
       for (int e = 0; e < 2; ++e) {
         const int r = x * 8 + 2 * j + e;
         if (!fresh) {
-#pragma unroll
-          for (int w = 4; w < 32; w <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], w);
-          const float f = ex2_approx(F[x][e] - (m[x][e] == -INFINITY ? 0.f : m[x][e]));
           if (r < rows) {
 #pragma unroll
             for (int u = 0; u < KS; ++u)
-              *reinterpret_cast<float2*>(mine + r * DP + u * 16 + 2 * r0) =
-                  make_float2(o[u][x][e] * kSumDown * f, o[u][x][2 + e] * kSumDown * f);
+              *reinterpret_cast<float2*>(mine + r * DP + u * 16 + 2 * r0) = make_float2(o[u][x][e], o[u][x][2 + e]);
           }
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], w);
         }
-        if (r0 == 0) ml[warp * kRows + r] = fresh ? make_float4(-INFINITY, 0.f, 0.f, 0.f) : make_float4(m[x][e], l[x][e], 0.f, 0.f);
+        if (r0 == 0)
+          ml[warp * kRows + r] = fresh ? make_float4(-INFINITY, 0.f, -INFINITY, 0.f) : make_float4(m[x][e], l[x][e], F[x][e], 0.f);
       }
     if (dead && a.err) record_error(a.err, kDevTimeout);
     cluster_sync();
-    const int cell = rank * kWarps * 32 + threadIdx.x, r = cell / (DP / 4), c = (cell - r * (DP / 4)) * 4;
-    if (r < rows && c < KS * 16) {
-      const uint32_t ml_at = smem_u32(ml + r), o_at = smem_u32(sm) + (r * DP + c) * 4;
-      float2 st[kRanks * kWarps];
+    const int cell = rank * kWarps * 32 + threadIdx.x, r = cell / kLanes, c = (cell - r * kLanes) * 4;
+    if (__any_sync(0xffffffffu, r < rows)) {
+      // the lanes of a row look up the warps' frames side by side
+      const uint32_t ml_at = smem_u32(ml + min(r, kRows - 1)), o_at = smem_u32(sm) + (r * DP + c) * 4;
+      float4 st[kParts / kLanes];
+      float mm = -INFINITY, ff = -INFINITY, ll = 0.f;
 #pragma unroll
-      for (int q = 0; q < kRanks * kWarps; ++q) st[q] = ld_rank2(of_rank(ml_at + (q % kWarps) * kRows * 16, q / kWarps));
-      float mm = -INFINITY, ll = 0.f;
+      for (int i = 0; i < kParts / kLanes; ++i) {
+        const int q = i * kLanes + lane % kLanes;
+        st[i] = ld_rank4(of_rank(ml_at + (q % kWarps) * kRows * 16, q / kWarps));
+        mm = fmaxf(mm, st[i].x);
+        ff = fmaxf(ff, st[i].z);
+      }
 #pragma unroll
-      for (int q = 0; q < kRanks * kWarps; ++q) mm = fmaxf(mm, st[q].x);
-      const float u = mm == -INFINITY ? 0.f : mm;
+      for (int w = kLanes / 2; w > 0; w >>= 1) {
+        mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, w));
+        ff = fmaxf(ff, __shfl_xor_sync(0xffffffffu, ff, w));
+      }
+      const float mu = mm == -INFINITY ? 0.f : mm, fu = ff == -INFINITY ? 0.f : ff;
+      float in[kParts / kLanes];  // weight of a warp's accumulator
+#pragma unroll
+      for (int i = 0; i < kParts / kLanes; ++i) {
+        ll = fmaf(st[i].y, ex2_approx(st[i].x - mu), ll);
+        in[i] = ex2_approx(st[i].z - fu);
+      }
+#pragma unroll
+      for (int w = kLanes / 2; w > 0; w >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, w);
+      const bool on = r < rows && c < KS * 16;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int q = 0; q < kRanks * kWarps; ++q) {
-        const float w = ex2_approx(st[q].x - u);
-        ll = fmaf(st[q].y, w, ll);
-        if (st[q].y != 0.f) {  // (a warp without keys wrote no accumulator)
+      for (int q = 0; q < kParts; ++q) {
+        const float w = __shfl_sync(0xffffffffu, in[q / kLanes], q % kLanes, kLanes);
+        if (on && w != 0.f) {  // (a warp without keys wrote no accumulator)
           const float4 y = ld_rank4(of_rank(o_at + (q % kWarps) * C::kWarpBytes, q / kWarps));
           acc.x = fmaf(w, y.x, acc.x); acc.y = fmaf(w, y.y, acc.y);
           acc.z = fmaf(w, y.z, acc.z); acc.w = fmaf(w, y.w, acc.w);
         }
       }
-      const float inv = ll != 0.f ? 1.0f / (ll * kSumDown) : 0.f;
-      const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-      const int64_t to = (int64_t)blockIdx.y * a.o_sb + (int64_t)(row0 + r) * a.o_sh + c;
+      if (on) {
+        const float f = ll != 0.f ? ex2_approx(ff - mu) / ll : 0.f;
+        const float y[4] = {acc.x * f, acc.y * f, acc.z * f, acc.w * f};
+        const int64_t to = (int64_t)blockIdx.y * a.o_sb + (int64_t)(row0 + r) * a.o_sh + c;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (c + e < a.c.d) store_out(p, to + e, y[e]);
-      if (c == 0 && a.lse) a.lse[(int64_t)blockIdx.y * a.hq + row0 + r] = ll != 0.f ? (mm + log2f(ll)) * kLn2F : -INFINITY;
+        for (int e = 0; e < 4; ++e)
+          if (c + e < a.c.d) store_out(p, to + e, y[e]);
+        if (c == 0 && a.lse) a.lse[(int64_t)blockIdx.y * a.hq + row0 + r] = ll != 0.f ? (mm + log2f(ll)) * kLn2F : -INFINITY;
+      }
     }
     cluster_sync();  // no CTA's shared memory goes away while it is read
     return;

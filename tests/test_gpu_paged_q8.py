@@ -114,6 +114,33 @@ def test_values_near_the_largest(d, hq, vt, lens, bound):
     out, lse = qa.paged_attn_q8(q.to(DEV), *planes(G), G["table"], G["lens"], bound, return_lse=True)
     r = q8.attend(c, q, d ** -0.5, hkv=2)
     assert_close(out, r["out"], r["out_tol"], "out")
+@pytest.mark.parametrize("bound", [700, 10 ** 5])
+@pytest.mark.parametrize("lo,hi,gap", [(-110, 20, 122), (-10, 120, 122), (-60, 60, 124), (-60, 100, 140), (-110, 110, 200)])
+@pytest.mark.parametrize("d,hq,kt,vt", [(64, 6, S8, E4), (128, 24, E4, S8)])
+def test_v_scales_that_outweigh_the_scores(d, hq, kt, vt, lo, hi, gap, bound):
+    # keys with the top score and V scales of 2^lo beside keys 2^gap less likely with V scales of 2^hi, which make the result
+    import quantized_attention_mean_gb300 as qa
+    hkv, lens = 2, [700, 81]
+    c = q8.make_cache(lens, hkv, d, 16, 4, kt, vt, seed=lo + d)
+    g = torch.Generator().manual_seed(gap)
+    k = torch.randint(-3, 4, c["k"].shape, generator=g).float()
+    k[..., 0] = 0
+    c["ks"].fill_(gap * math.log(2) * d ** 0.5 / (96 * 64))             # 96 of channel 0, where q is 64: `gap` in base 2
+    c["vs"].fill_(2.0 ** hi)
+    for b, n in enumerate(lens):
+        for t in range(5, n, 64):
+            p, s = int(c["table"][b, t // 16]), t % 16
+            k[p, :, s, 0] = 96
+            c["vs"][p, :, s // 4] = 2.0 ** lo
+    c["k"] = q8.to_codes(k, kt)
+    q = torch.randn(2, hq, d, generator=g) * 4
+    q[..., 0] = 64
+    q = q.bfloat16()
+    G = on_gpu(c)
+    out, lse = qa.paged_attn_q8(q.to(DEV), *planes(G), G["table"], G["lens"], bound, return_lse=True)
+    lift = max(0, gap - hi)                                             # the bound's absolute part lies below what is compared
+    r = q8.attend(dict(c, vs=(c["vs"].double() * 2.0 ** lift)), q, d ** -0.5, hkv=hkv)
+    assert_close(out.double() * 2.0 ** lift, r["out"], r["out_tol"], "out")
     assert_close(lse, r["lse"], r["lse_tol"], "lse")
 
 
