@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(32 * warps_of(FORM), 28 / warps_of(FORM)) appe
       first = __ldg(&a.cu[b]);
       if (tells && t == 0 && first != 0) record_error(a.err, kDevSeqlens);
       if (b >= c.batch) return;              // behind the last sequence
-      if (first > t) return;                 // before the first
+      if (first > t) { t = first; continue; }  // before the first: rows that are left out
       end = min((int64_t)__ldg(&a.cu[b + 1]), (int64_t)a.tokens);
       if (end <= t) { ++b; continue; }       // a sequence without tokens (b grows: at most batch of them)
     }

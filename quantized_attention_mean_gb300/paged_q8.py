@@ -134,8 +134,9 @@ def paged_append_q8(k, v, k_cache, v_cache, k_scales, v_scales, page_table, seq_
                     tensor_layout="HND", workspace=None, stream=None):
     """``paged_append`` into an 8-bit cache: writes new tokens k, v [T, Hkv, d] (fp16 or bf16, finite) as codes behind the
     ``seq_lens`` tokens their sequences hold (seq_lens is not raised). ``cu_seqlens`` int32 [B + 1] says which tokens are
-    whose; without it each sequence gets one. Tokens behind the last sequence are left out, and so are those whose slot or
-    page is not in the cache and all of a sequence of negative length (recorded in ``workspace``, 256 bytes, where given).
+    whose; without it each sequence gets one. Tokens behind the last sequence are left out, and so are those before the first
+    (``cu_seqlens[0]`` should be 0), those whose slot or page is not in the cache and all of a sequence of negative length (these
+    are recorded in ``workspace``, 256 bytes, where given).
 
     The scale of a block becomes ``max(s, need, 2^-100)``: s that of its earlier tokens, 0 if the first new token begins the
     block; need = max|x| / 127 for int8, the smallest power of two with max|x| ≤ 448 · need for E4M3. Codes are x / scale

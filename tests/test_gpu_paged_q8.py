@@ -474,6 +474,27 @@ def test_what_has_no_place_is_left_out():
         assert torch.equal(y.cpu(), x)
 
 
+@pytest.mark.parametrize("lead", [1, 3, 20, 200])
+@pytest.mark.parametrize("hkv,d,page,block,kt,vt", [(2, 64, 16, 16, S8, E4), (1, 128, 128, 128, E4, S8), (2, 32, 32, 1, S8, S8),
+                                                    (3, 72, 64, 64, S8, E4)])
+def test_rows_before_the_first_sequence_are_left_out(hkv, d, page, block, kt, vt, lead):
+    # cu_seqlens of a slice of a batch: the rows of the sequences before it are not written, all others are; the status says so
+    import quantized_attention_mean_gb300 as qa
+    held, new = [5, 16, 0], [40, 3, 70]
+    c = q8.make_cache(held, hkv, d, page, block, kt, vt, seed=lead, room=max(new) + 1)
+    cu = [lead, lead + 40, lead + 43, lead + 113]
+    k, v = (torch.randn(cu[-1] + 2, hkv, d, generator=torch.Generator().manual_seed(i)).bfloat16() for i in range(2))
+    G = on_gpu(c)
+    ws = qa.alloc_workspace(256, DEV).fill_(255)
+    qa.paged_append_q8(k.to(DEV), v.to(DEV), *planes(G), G["table"], G["lens"],
+                       cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV), workspace=ws)
+    assert qa.read_device_status(ws) == 12
+    q8.append(c, k, v, cu)
+    for w in "kv":
+        assert same(G[w], c[w]), f"codes of {w}"
+        assert torch.equal(G[w + "s"].cpu(), c[w + "s"]), f"scales of {w}"
+
+
 def test_broadcast_keys_and_zero_tokens_and_tiny_values():
     import quantized_attention_mean_gb300 as qa
     hkv, d = 4, 64
