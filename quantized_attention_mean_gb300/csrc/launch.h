@@ -65,6 +65,9 @@ bool make_map4_bytes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
 cudaError_t launch_varlen_setup(const Problem& p, cudaStream_t st);
 cudaError_t launch_kv_stats(const Problem& p, int max_len_k, cudaStream_t st);
 cudaError_t launch_short_status_clear(int* err, int words, cudaStream_t st);
+cudaError_t launch_status_clear(int* err, cudaStream_t st);
+// What a call with nothing to do returns: the status word of its workspace (may be null) says so too.
+int empty_call(void* workspace, size_t workspace_bytes, cudaStream_t st);
 cudaError_t launch_finalize(const Problem& p, int n_stats, cudaStream_t st);
 cudaError_t launch_quant(const Problem& p, int max_len_q, int max_len_k, cudaStream_t st);
 cudaError_t launch_export_codes(const __half* codes, int64_t rows_pp, int dp, int d, int planes,

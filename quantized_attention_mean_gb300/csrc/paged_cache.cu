@@ -127,6 +127,29 @@ __global__ void status_clear_kernel(int* err) {
   *err = 0;
 }
 
+}  // namespace
+
+cudaError_t launch_status_clear(int* err, cudaStream_t st) {
+  return launch_pdl(status_clear_kernel, dim3(1), dim3(1), 0, st, err);
+}
+
+int empty_call(void* workspace, size_t workspace_bytes, cudaStream_t st) {
+  if (!workspace) return SAGE_OK;
+  if (reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < SAGE_STATUS_BYTES) return SAGE_ERR_WORKSPACE;
+  // (a call that has nothing to do may have been given no memory of the device, or there may be none)
+  cudaPointerAttributes at{};
+  if (!sage_device_supported()) return SAGE_OK;
+  if (cudaPointerGetAttributes(&at, workspace) != cudaSuccess) {
+    cudaGetLastError();
+    return SAGE_OK;
+  }
+  if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) return SAGE_OK;
+  const cudaError_t e = launch_status_clear(static_cast<int*>(workspace), st);
+  return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "status reset");
+}
+
+namespace {
+
 // ---------------------------------------------------------------------------------- eviction
 struct EvictArgs {
   PagedView c;
@@ -648,7 +671,7 @@ int sage_paged_append(const sage_packed* k, const sage_packed* v, const sage_pag
   a.err = static_cast<int*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (a.err) e = launch_pdl(status_clear_kernel, dim3(1), dim3(1), 0, st, a.err);
+  if (a.err) e = launch_status_clear(a.err, st);
   if (e == cudaSuccess) e = launch_pdl(append_kernel, dim3((unsigned)(((int64_t)tokens + 3) / 4)), dim3(128), 0, st, a);
   return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "paged append");
 }

@@ -522,11 +522,6 @@ __global__ void __launch_bounds__(128, 10) read_q8_kernel(const ReadArgs a) {
   else copy_rows<T, V, SAGE_E4M3>(a, kv, t0, n_rows, code_at, scale_at);
 }
 
-__global__ void clear_status_kernel(int* err) {
-  pdl_wait();
-  *err = 0;
-}
-
 int check_status_word(const void* workspace, size_t bytes) {
   return workspace && (reinterpret_cast<uintptr_t>(workspace) % 256 || bytes < SAGE_STATUS_BYTES) ? SAGE_ERR_WORKSPACE
                                                                                                  : SAGE_OK;
@@ -562,7 +557,7 @@ int sage_paged_append_q8(const sage_packed* k, const sage_packed* v, const sage_
   if (dtype != SAGE_F16 && dtype != SAGE_BF16) return SAGE_ERR_DTYPE;
   if (tokens < 0 || (!cu_seqlens && tokens != batch) || reinterpret_cast<uintptr_t>(cu_seqlens) % 4) return SAGE_ERR_INVALID_ARG;
   if (check_status_word(workspace, workspace_bytes) != SAGE_OK) return SAGE_ERR_WORKSPACE;
-  if (batch == 0 || tokens == 0) return SAGE_OK;
+  if (batch == 0 || tokens == 0) return empty_call(workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
   int run = 8;
   const sage_packed* t[2] = {k, v};
   for (int i = 0; i < 2; ++i) {
@@ -603,7 +598,7 @@ int sage_paged_append_q8(const sage_packed* k, const sage_packed* v, const sage_
   const dim3 grid((unsigned)(chunks * a.shares));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (a.err) e = launch_pdl(clear_status_kernel, dim3(1), dim3(1), 0, st, a.err);
+  if (a.err) e = launch_status_clear(a.err, st);
   if (e == cudaSuccess) {
     auto go = [&](auto... kernels) {
       decltype(&append_q8_kernel<__half, kOne, true>) of[] = {kernels...};
@@ -634,7 +629,7 @@ int sage_paged_read_q8(const sage_packed* k_out, const sage_packed* v_out, const
   if (tokens < 0 || !cu_seqlens || reinterpret_cast<uintptr_t>(cu_seqlens) % 4 || reinterpret_cast<uintptr_t>(starts) % 4)
     return SAGE_ERR_INVALID_ARG;
   if (check_status_word(workspace, workspace_bytes) != SAGE_OK) return SAGE_ERR_WORKSPACE;
-  if (tokens == 0) return SAGE_OK;
+  if (tokens == 0) return empty_call(workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
   int run = 8;
   const sage_packed* t[2] = {k_out, v_out};
   for (int i = 0; i < 2; ++i) {
@@ -651,7 +646,7 @@ int sage_paged_read_q8(const sage_packed* k_out, const sage_packed* v_out, const
   a.err = static_cast<int*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (a.err) e = launch_pdl(clear_status_kernel, dim3(1), dim3(1), 0, st, a.err);
+  if (a.err) e = launch_status_clear(a.err, st);
   // rows of a warp: as many as leave some warps for each SM
   const int v = run == 8 && align >= 8 ? 8 : run >= 4 && align >= 4 ? 4 : 1;
   const int runs = heads_kv * ((head_dim + v - 1) / v), most = runs <= 32 ? 8 * (32 / runs) : 4;

@@ -545,6 +545,44 @@ def test_a_cache_past_32_bits():
     assert torch.equal(b[:, 0].cpu(), q8.values(c, "v", 0, 0, 400).float().half())
 
 
+def test_calls_with_nothing_to_do_say_so():
+    # a workspace that held another call's error: an empty call leaves no status of it
+    import quantized_attention_mean_gb300 as qa
+    c = q8.make_cache([30, 5], 2, 64, 16, 16, S8, E4)
+    G = on_gpu(c)
+    none = {n: (t[:0] if n in ("table", "lens") else t) for n, t in G.items()}
+    x = torch.randn(2, 2, 64, dtype=torch.float16, device=DEV)
+    cu = torch.zeros(3, dtype=torch.int32, device=DEV)
+    ws = qa.alloc_workspace(qa.paged_attn_q8_workspace_bytes(2, 4, 2, 10 ** 5, 64), DEV)
+    calls = [
+        lambda **kw: qa.paged_append_q8(x[:0], x[:0], *planes(G), G["table"], G["lens"], cu_seqlens=cu, workspace=ws, **kw),
+        lambda **kw: qa.paged_append_q8(x[:0], x[:0], *planes(none), none["table"], none["lens"], workspace=ws, **kw),
+        lambda **kw: qa.paged_append_q8(x, x, *planes(none), none["table"], none["lens"], cu_seqlens=cu[:1], workspace=ws, **kw),
+        lambda **kw: qa.paged_read_q8(*planes(G), G["table"], G["lens"], cu, 0, workspace=ws, **kw),
+        lambda **kw: qa.paged_attn_q8(torch.empty(0, 4, 64, dtype=torch.float16, device=DEV), *planes(none), none["table"],
+                                      none["lens"], 10 ** 5, workspace=ws, **kw),
+    ]
+    side = torch.cuda.Stream()
+    for call in calls:
+        ws.fill_(255)
+        call()
+        assert qa.read_device_status(ws) == 0
+        ws.fill_(255)
+        side.wait_stream(torch.cuda.current_stream())
+        call(stream=side)
+        assert qa.read_device_status(ws, side) == 0
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        ws.fill_(255)
+        graph.replay()
+        assert qa.read_device_status(ws) == 0
+        call_ws = qa.alloc_workspace(512, DEV)[64:]
+        with pytest.raises((qa.SageError, ValueError)):
+            qa.paged_read_q8(*planes(G), G["table"], G["lens"], cu, 0, workspace=call_ws)
+    assert same(G["k"], c["k"]) and torch.equal(G["ks"].cpu(), c["ks"])
+
+
 # ------------------------------------------------------------------------------------- together
 def freqs(n):
     return (10000.0 ** (-torch.arange(n, dtype=torch.float64) / n)).float().to(DEV)
