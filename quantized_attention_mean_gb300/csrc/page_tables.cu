@@ -122,7 +122,11 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const AssignArgs a) {
     s_first[tid] = (int)(count - 1 - (served ? last - g.need : 0));
   }
   const int n = min(a.per, a.batch - b0);
-  if (n == 0 && tid == 0) s_cu[0] = a.cu[0] = 0;  // (no sequence at all)
+  if (n == 0 && tid == 0) {  // (no sequence at all)
+    s_cu[0] = 0;
+    if (split == 0) a.cu[0] = 0;
+    if (split == 0 && a.err && given != count) record_error(a.err, kDevSeqlens);
+  }
   if (tid == n - 1) s_cu[n] = (int)(t1 < a.max_tokens ? t1 : a.max_tokens);
   if (split == 0 && mine) {
     a.cu[b] = s_cu[tid];
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const ReleaseArgs a) {
   if (threadIdx.x == 0) a.given[b] = !ok ? -1 - kDevSeqlens : bad ? -1 - kDevPage : have - keep;
 }
 
-// A CTA per sequence: its pages to their places on the stack.
+// A CTA per sequence: its pages to their places on the stack. (One CTA where there is no sequence: the count alone.)
 __global__ void __launch_bounds__(kThreads) push_kernel(const ReleaseArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(kThreads) push_kernel(const ReleaseArgs a) {
   Two sum{0, 0};
   for (int i = threadIdx.x; i < b; i += kThreads) sum.x += max(a.given[i], 0);
   sum = block_sum(sum);
-  const int mine = max(a.given[b], 0);
+  const int mine = b < a.batch ? max(a.given[b], 0) : 0;
   const bool fits = count + sum.x + mine <= a.capacity;
   if (fits && mine > 0) {
     int keep = 0, have = 0;
@@ -262,14 +266,9 @@ __global__ void __launch_bounds__(kThreads) push_kernel(const ReleaseArgs a) {
     __syncthreads();
     if (threadIdx.x == 0) {
       *a.new_count = count + (int)s_high;
-      *a.err = s_err;
+      if (a.err) *a.err = s_err;
     }
   }
-}
-
-__global__ void clear_kernel(int* err) {
-  pdl_wait();
-  *err = 0;
 }
 
 // What both calls ask of the table, the lengths and the stack.
@@ -327,7 +326,7 @@ int sage_paged_assign(int32_t* page_table, int64_t table_stride, int max_pages, 
   a.new_count = new_free_count;
   a.err = static_cast<int*>(workspace);
   cudaError_t e = cudaSuccess;
-  if (a.err) e = launch_pdl(clear_kernel, dim3(1), dim3(1), 0, st, a.err);
+  if (a.err) e = launch_status_clear(a.err, st);
   // as many sequences per CTA as leave a CTA for each SM; those of long rows share their tokens
   a.per = (batch + 151) / 152;
   a.per = a.per < 1 ? 1 : a.per > kThreads ? kThreads : a.per;
@@ -353,20 +352,17 @@ int sage_paged_release(const int32_t* page_table, int64_t table_stride, int max_
   if (!workspace && batch > 0) return SAGE_ERR_WORKSPACE;
   if (!sage_device_supported()) return SAGE_ERR_DEVICE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (batch == 0) {
-    const cudaError_t e = cudaMemcpyAsync(new_free_count, free_count, 4, cudaMemcpyDeviceToDevice, st);
-    return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "page release");
-  }
   ReleaseArgs a{};
   a.table = page_table; a.table_stride = table_stride; a.max_pages = max_pages;
   a.lens = seq_lens; a.keep = keep_lens;
   a.free_pages = free_pages; a.free_count = free_count; a.capacity = num_pages;
   a.batch = batch; a.page_size = page_size;
-  a.given = reinterpret_cast<int*>(static_cast<char*>(workspace) + SAGE_STATUS_BYTES);
+  a.given = batch > 0 ? reinterpret_cast<int*>(static_cast<char*>(workspace) + SAGE_STATUS_BYTES) : nullptr;
   a.new_count = new_free_count;
   a.err = static_cast<int*>(workspace);
-  cudaError_t e = launch_pdl(count_kernel, dim3(batch), dim3(kThreads), 0, st, a);
-  if (e == cudaSuccess) e = launch_pdl(push_kernel, dim3(batch), dim3(kThreads), 0, st, a);
+  cudaError_t e = cudaSuccess;
+  if (batch > 0) e = launch_pdl(count_kernel, dim3(batch), dim3(kThreads), 0, st, a);
+  if (e == cudaSuccess) e = launch_pdl(push_kernel, dim3(batch > 0 ? batch : 1), dim3(kThreads), 0, st, a);
   return e == cudaSuccess ? SAGE_OK : note_cuda_failure(e, "page release");
 }
 

@@ -174,6 +174,22 @@ def test_release_of_bad_pages_and_without_room():
     assert qa.paged_release(none, ints([]), ints([]), stack, ints([2]), 4).item() == 2
 
 
+@pytest.mark.parametrize("said,count,status", [(2, 2, 0), (9, 4, 12), (-3, 0, 12)])
+def test_no_sequences_and_a_count_out_of_range(said, count, status):
+    # with no sequence the count is clamped and told of as with some
+    import quantized_attention_mean_gb300 as qa
+    none, free = torch.zeros(0, 3, dtype=torch.int32, device=DEV), ints([7, 8, 9, 10])
+    ws = qa.alloc_workspace(qa.paged_release_workspace_bytes(0), DEV).fill_(255)
+    a = qa.paged_assign(none, ints([]), ints([]), free, ints([said]), 4, 2, workspace=ws)
+    assert qa.read_device_status(ws) == status
+    assert a.free_count.item() == count and a.cu_seqlens.tolist() == [0] and a.positions.tolist() == [-1, -1]
+    ws.fill_(255)
+    assert qa.paged_release(none, ints([]), ints([]), free, ints([said]), 4, workspace=ws).item() == count
+    assert qa.read_device_status(ws) == status
+    assert qa.paged_release(none, ints([]), ints([]), free, ints([said]), 4).item() == count
+    assert free.tolist() == [7, 8, 9, 10]
+
+
 def test_pages_go_round():
     # random growth and ends over many steps: no page is ever held twice, and none is lost
     import quantized_attention_mean_gb300 as qa
