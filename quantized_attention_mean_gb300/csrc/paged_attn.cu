@@ -766,7 +766,7 @@ int sage_paged_attn(const sage_packed* q, const sage_paged_cache* cache, const s
   if (heads_q < 1 || max_seqlen < 0 || batch > 65535 || !softcap_ok(softcap, sm_scale, head_dim))
     return SAGE_ERR_INVALID_ARG;
   if (heads_q % heads_kv) return SAGE_ERR_GQA;
-  if (batch == 0) return SAGE_OK;
+  if (batch == 0) return empty_call(workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
   if (!q->data || !out->data) return SAGE_ERR_INVALID_ARG;
   for (const sage_packed* t : {q, out})
     if (reinterpret_cast<uintptr_t>(t->data) % 2 || t->stride_token < 0 || t->stride_head < 0) return SAGE_ERR_STRIDE;

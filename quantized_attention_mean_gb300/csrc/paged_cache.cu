@@ -134,11 +134,10 @@ cudaError_t launch_status_clear(int* err, cudaStream_t st) {
 }
 
 int empty_call(void* workspace, size_t workspace_bytes, cudaStream_t st) {
-  if (!workspace) return SAGE_OK;
-  if (reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < SAGE_STATUS_BYTES) return SAGE_ERR_WORKSPACE;
-  // (a call that has nothing to do may have been given no memory of the device, or there may be none)
-  cudaPointerAttributes at{};
+  // (nothing is asked of the workspace of a call that has nothing to do: it need be no memory of the device, nor must there be one)
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < SAGE_STATUS_BYTES) return SAGE_OK;
   if (!sage_device_supported()) return SAGE_OK;
+  cudaPointerAttributes at{};
   if (cudaPointerGetAttributes(&at, workspace) != cudaSuccess) {
     cudaGetLastError();
     return SAGE_OK;
@@ -654,7 +653,7 @@ int sage_paged_append(const sage_packed* k, const sage_packed* v, const sage_pag
   if (tokens < 0 || (!cu_seqlens && tokens != batch)) return SAGE_ERR_INVALID_ARG;
   if (workspace && (reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < SAGE_STATUS_BYTES))
     return SAGE_ERR_WORKSPACE;
-  if (batch == 0 || tokens == 0) return SAGE_OK;
+  if (batch == 0 || tokens == 0) return empty_call(workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
   if (!k->data || !v->data || reinterpret_cast<uintptr_t>(cu_seqlens) % 4 || reinterpret_cast<uintptr_t>(positions) % 4)
     return SAGE_ERR_INVALID_ARG;
   for (const sage_packed* t : {k, v}) {
@@ -691,7 +690,7 @@ int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch
   if (s != SAGE_OK) return s;
   if (max_seqlen < 0 || batch > 65535 || budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget)
     return SAGE_ERR_INVALID_ARG;
-  if (batch == 0) return SAGE_OK;
+  if (batch == 0) return empty_call(workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
   // (planes of no pages have no address, and are not read)
   if (!new_lens || reinterpret_cast<uintptr_t>(new_lens) % 4 || (cache->num_pages > 0 && (!cache->mass || !cache->positions)))
     return SAGE_ERR_INVALID_ARG;

@@ -1251,7 +1251,7 @@ int sage_scored_attn(const sage_tensor* q, const sage_tensor* k, const sage_tens
   if (heads_q % heads_kv) return SAGE_ERR_GQA;
   for (const void* p : {(const void*)lse, (const void*)slopes, (const void*)prefix_lens, (const void*)doc_q, (const void*)doc_k})
     if (reinterpret_cast<uintptr_t>(p) % 4) return SAGE_ERR_INVALID_ARG;
-  if (batch == 0 || seqlen_q == 0) return SAGE_OK;
+  if (batch == 0 || seqlen_q == 0) return empty_call(workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
   const sage_tensor* ts[4] = {q, k, v, out};
   View view[4];
   for (int i = 0; i < 4; ++i) {

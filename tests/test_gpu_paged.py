@@ -401,6 +401,29 @@ def test_append(old, new, hkv, d, page, dtype, layout, planes):
         assert torch.equal(gm.cpu(), mass) and torch.equal(gp.cpu(), kpos)
 
 
+def test_calls_with_nothing_to_do_clear_the_status():
+    # a workspace that held another call's error
+    import quantized_attention_mean_gb300 as qa
+    c = ref.make_cache([30, 5], 2, 64, 16, torch.float16)
+    G = on_gpu(c)
+    table, lens = G["table"][:0], G["lens"][:0]
+    x = torch.randn(2, 2, 64, dtype=torch.float16, device=DEV)
+    cu = torch.zeros(3, dtype=torch.int32, device=DEV)
+    mass, pos = torch.zeros(c["k"].shape[0], 2, 16, device=DEV), torch.zeros(c["k"].shape[0], 2, 16, dtype=torch.int32, device=DEV)
+    ws = qa.alloc_workspace(max(qa.paged_attn_workspace_bytes(2, 4, 2, 10 ** 5, 64), qa.paged_evict_workspace_bytes(2, 2, 64, 16), 256), DEV)
+    none = torch.empty(0, 4, 64, dtype=torch.float16, device=DEV)
+    dense = torch.randn(1, 4, 8, 64, dtype=torch.float16, device=DEV)
+    for call in (
+            lambda: qa.paged_append(x[:0], x[:0], G["k"], G["v"], G["table"], G["lens"], cu_seqlens=cu, workspace=ws),
+            lambda: qa.paged_append(x[:0], x[:0], G["k"], G["v"], table, lens, workspace=ws),
+            lambda: qa.paged_attn(none, G["k"], G["v"], table, lens, 10 ** 5, workspace=ws),
+            lambda: qa.paged_evict(G["k"], G["v"], mass, pos, table, lens, 16, 64, workspace=ws),
+            lambda: qa.scored_attn(dense[:, :, :0], dense, dense, workspace=ws)):
+        ws.fill_(255)
+        call()
+        assert qa.read_device_status(ws) == 0
+
+
 def test_append_leaves_out_what_has_no_place():
     import quantized_attention_mean_gb300 as qa
     c = ref.make_cache([40, 40, 40], 2, 64, 16, torch.float16)      # three pages each: room for 48
