@@ -25,6 +25,8 @@ namespace {
 
 constexpr int kRopeWarps = 4, kRopeBlocks = 4;  // of an SM
 constexpr int kMaxPairs = 64;
+// Means of squares that fp32 holds with all their bits: below, the squares of a row lose theirs; above, their sum may overflow.
+constexpr float kLeastSquare = 0x1p-90f, kMostSquare = 0x1p120f;
 
 struct RopeArgs {
   const void* x[2];          // q, k
@@ -157,8 +159,9 @@ __device__ __forceinline__ void widen2(uint32_t x, float& lo, float& hi) {
 // of q, then of k, `rows` heads at a time. The next kAhead such steps are in flight, the first ones before the position is
 // known. With x' = x w a pair becomes f (x'_i cos - x'_j sin, x'_j cos + x'_i sin), f the row's norm: the products of weights
 // with cosines and sines are the same for all heads, which leaves six operations for two values.
-// LANES: of a row, or 0: a.lanes.
-template <typename T, int V, int SLOTS, bool PAIRS, int LANES>
+// LANES: of a row, or 0: a.lanes. ANY: rows whose mean of squares fp32 does not hold are taken by a power of two first; what
+// looks for them in the loop costs 2 to 8%, so that only calls that may have some do (bf16 with eps below kLeastSquare).
+template <typename T, int V, int SLOTS, bool PAIRS, int LANES, bool ANY>
 __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(const RopeArgs a) {
   using R = typename Run<T, V>::type;
   constexpr int kAhead = V == 8 ? 4 : 2, N = SLOTS * V / 2;  // N: pairs of a lane, two by two
@@ -328,29 +331,58 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
         }
         fetch(raw[k]);
         if (left <= 0) continue;  // (a step that fills up, for the whole warp)
-        Pair s2 = mul_pair2(xi[0], xi[0]), t2 = mul_pair2(xj[0], xj[0]);
+        auto over_row = [&](float x, auto join) {
+          if (LANES > 0 ? (LANES & (LANES - 1)) == 0 : (lanes & (lanes - 1)) == 0) {
 #pragma unroll
-        for (int e = 1; e < N; ++e) {
-          s2 = fma_pair2(xi[e], xi[e], s2);
-          t2 = fma_pair2(xj[e], xj[e], t2);
-        }
-        float s0, s1, t0, t1;
-        split_pair2(s2, s0, s1);
-        split_pair2(t2, t0, t1);
-        float sum = (s0 + s1) + (t0 + t1);
-        if (LANES > 0 ? (LANES & (LANES - 1)) == 0 : (lanes & (lanes - 1)) == 0) {
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1)
-            if (o < lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        } else {
+            for (int o = 16; o > 0; o >>= 1)
+              if (o < lanes) x = join(x, __shfl_xor_sync(0xffffffffu, x, o));
+            return x;
+          }
           // in the order of the lanes, so that all of a row get the same
           float all = 0.f;
 #pragma unroll
           for (int o = 0; o < (LANES > 0 ? LANES : 16); ++o)
-            if (o < lanes) all += __shfl_sync(0xffffffffu, sum, (row * lanes + o) & 31);
-          sum = all;
+            if (o < lanes) all = join(all, __shfl_sync(0xffffffffu, x, (row * lanes + o) & 31));
+          return all;
+        };
+        auto squares = [&]() {
+          Pair s2 = mul_pair2(xi[0], xi[0]), t2 = mul_pair2(xj[0], xj[0]);
+#pragma unroll
+          for (int e = 1; e < N; ++e) {
+            s2 = fma_pair2(xi[e], xi[e], s2);
+            t2 = fma_pair2(xj[e], xj[e], t2);
+          }
+          float s0, s1, t0, t1;
+          split_pair2(s2, s0, s1);
+          split_pair2(t2, t0, t1);
+          return over_row((s0 + s1) + (t0 + t1), [](float x, float y) { return x + y; });
+        };
+        float v = fmaf(squares(), a.inv_d, a.eps);
+        if constexpr (ANY) {
+          const bool odd = live > 0 && row < rows && !(v > kLeastSquare && v < kMostSquare);
+          if (__any_sync(0xffffffffu, odd)) {
+            // its largest channel, or the root of eps, comes to about one
+            float most = 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              float x0, x1, x2, x3;
+              split_pair2(xi[e], x0, x1);
+              split_pair2(xj[e], x2, x3);
+              most = fmaxf(fmaxf(most, fmaxf(fabsf(x0), fabsf(x1))), fmaxf(fabsf(x2), fabsf(x3)));
+            }
+            most = fmaxf(over_row(most, [](float x, float y) { return fmaxf(x, y); }), sqrtf(a.eps));
+            const int e0 = max(1, min(253, (int)(__float_as_uint(most) >> 23)));
+            const float up = odd ? __uint_as_float((uint32_t)(254 - e0) << 23) : 1.f;
+            const Pair up2 = make_pair2(up, up);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              xi[e] = mul_pair2(xi[e], up2);
+              xj[e] = mul_pair2(xj[e], up2);
+            }
+            v = fmaf(squares(), a.inv_d, a.eps * up * up);
+          }
         }
-        const float f = rsqrtf(fmaf(sum, a.inv_d, a.eps));
+        const float f = rsqrtf(v);
         const Pair f2 = make_pair2(f, f);
         float zi[2 * N], zj[2 * N];
 #pragma unroll
@@ -382,14 +414,22 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
 template <typename T, bool PAIRS>
 cudaError_t launch_rope(const RopeArgs& a, int v, int blocks, cudaStream_t st) {
   const dim3 g(blocks), t(kRopeWarps * 32);
-  if (v == 8 && a.lanes == 8) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 8>, g, t, 0, st, a);
-  if (v == 8 && a.lanes == 5) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 5>, g, t, 0, st, a);
-  if (v == 8 && a.lanes == 6) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 6>, g, t, 0, st, a);
-  if (v == 8 && a.lanes == 4) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 4>, g, t, 0, st, a);
-  if (v == 8) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 0>, g, t, 0, st, a);
-  if (v == 4) return launch_pdl(rope_kernel<T, 4, 1, PAIRS, 0>, g, t, 0, st, a);
-  if (v == 2) return launch_pdl(rope_kernel<T, 2, 1, PAIRS, 0>, g, t, 0, st, a);
-  return launch_pdl(rope_kernel<T, 1, 2, PAIRS, 0>, g, t, 0, st, a);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    if (a.eps < kLeastSquare) {  // (fp16 rows have no such squares)
+      if (v == 8) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 0, true>, g, t, 0, st, a);
+      if (v == 4) return launch_pdl(rope_kernel<T, 4, 1, PAIRS, 0, true>, g, t, 0, st, a);
+      if (v == 2) return launch_pdl(rope_kernel<T, 2, 1, PAIRS, 0, true>, g, t, 0, st, a);
+      return launch_pdl(rope_kernel<T, 1, 2, PAIRS, 0, true>, g, t, 0, st, a);
+    }
+  }
+  if (v == 8 && a.lanes == 8) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 8, false>, g, t, 0, st, a);
+  if (v == 8 && a.lanes == 5) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 5, false>, g, t, 0, st, a);
+  if (v == 8 && a.lanes == 6) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 6, false>, g, t, 0, st, a);
+  if (v == 8 && a.lanes == 4) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 4, false>, g, t, 0, st, a);
+  if (v == 8) return launch_pdl(rope_kernel<T, 8, 1, PAIRS, 0, false>, g, t, 0, st, a);
+  if (v == 4) return launch_pdl(rope_kernel<T, 4, 1, PAIRS, 0, false>, g, t, 0, st, a);
+  if (v == 2) return launch_pdl(rope_kernel<T, 2, 1, PAIRS, 0, false>, g, t, 0, st, a);
+  return launch_pdl(rope_kernel<T, 1, 2, PAIRS, 0, false>, g, t, 0, st, a);
 }
 
 }  // namespace

@@ -159,6 +159,35 @@ def test_zero_rows_and_large_values():
     assert (out[0] == 0).all()
 
 
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -140, 2.0 ** -100, 1e-6])
+@pytest.mark.parametrize("hq,hkv,d,pairs,interleaved", [(5, 3, 64, 32, False), (3, 1, 128, 64, True), (16, 2, 36, 9, False), (2, 2, 33, 16, True)])
+def test_rows_of_every_magnitude(hq, hkv, d, pairs, interleaved, eps):
+    # rows from the smallest bf16 on, beside ordinary ones: where eps does not outweigh them, squares that leave fp32 on either side
+    import quantized_attention_mean_gb300 as qa
+    g = torch.Generator().manual_seed(d)
+    sizes = [1.0, 1e-10, 1e-18, 1e-21, 1e-25, 1e-38, 2e-40, 1e10, 1e17, 1e19, 1e25, 3e37]
+    if eps > 2.0 ** -90:
+        sizes = sizes[:9]                                               # (magnitudes below 1e18)
+    T = 4 * len(sizes)
+    q, k = (torch.randn(T, h, d, generator=g).clamp(-8, 8) for h in (hq, hkv))
+    order = torch.randperm(T * hq, generator=g)[:T * hq].view(T, hq) % len(sizes)
+    q = (q.double() * torch.tensor(sizes, dtype=torch.float64)[order][..., None]).bfloat16()
+    k = (k.double() * torch.tensor(sizes, dtype=torch.float64)[torch.arange(T) % len(sizes)][:, None, None]).bfloat16()
+    q[3, 0, 1:] = 0                                                     # one value of its row, as large as it gets
+    q[3, 0, 0] = torch.finfo(torch.bfloat16).max if eps < 2.0 ** -90 else 1e17
+    for x in (q, k):                                                    # (a row of zeros has no value with eps = 0)
+        x[..., 0] = torch.where((x == 0).all(-1), torch.tensor(2.0 ** -133).bfloat16(), x[..., 0])
+    w = (1 + 0.3 * torch.randn(d, generator=g)).float()
+    pos, freq = torch.arange(T, dtype=torch.int32), freqs(pairs)
+    a, b = q.to(DEV), k.to(DEV)
+    got = qa.qk_norm_rope(a, b, pos.to(DEV), freq.to(DEV), w.to(DEV), w.to(DEV), eps=eps, interleaved=interleaved)
+    for name, x, y in (("q", q, got[0]), ("k", k, got[1])):
+        want, tol = reference(x, w, pos, freq, eps, interleaved)
+        assert_close(y, want, tol + 2.0 ** -126, name)                  # (results below bf16's normal range may become 0)
+    qa.qk_norm_rope(a, b, pos.to(DEV), freq.to(DEV), w.to(DEV), w.to(DEV), eps=eps, interleaved=interleaved, q_out=a, k_out=b)
+    assert torch.equal(a, got[0]) and torch.equal(b, got[1])
+
+
 def test_empty_and_on_another_stream_and_captured():
     import quantized_attention_mean_gb300 as qa
     freq = freqs(32).to(DEV)
