@@ -351,8 +351,9 @@ int sage_paged_evict(const sage_paged_cache* cache, int32_t* new_lens, int batch
  *   float [rot_dim / 2] (NULL with rot_dim 0). q_weight, k_weight: device [head_dim] of `dtype` or SAGE_F32
  *   (weight_dtype), or NULL for ones. Squares are summed in fp32: magnitudes below 1e18; with eps below
  *   2^-90, where small rows matter, any.
- * Angles are taken as 64-bit fractions of a turn, off by 2^-53 of inv_freq / 2 pi for each step of the
- * position. batch * seqlen below 2^31; rot_dim even, 0 to head_dim. */
+ * Angles are taken as 64-bit fractions of a turn, off by at most 2^-52 of themselves and 2^-65 of a turn for
+ * each step of the position.
+ * batch * seqlen below 2^31; rot_dim even, 0 to head_dim. */
 int sage_qk_norm_rope(const sage_tensor* q, const sage_tensor* k, const sage_tensor* q_out,
                       const sage_tensor* k_out, const int32_t* positions, int64_t positions_stride,
                       const float* inv_freq, const void* q_weight, const void* k_weight,

@@ -8,8 +8,9 @@
 // time, whose lanes hold the same channels of every row, so that weights, cosines and sines stay in registers over the
 // heads. A lane owns two runs of V channels that hold whole pairs, so a rotation needs no exchange between lanes and
 // the mean of squares one butterfly. The angle is taken in turns modulo one, as a 64-bit fixed-point product of the
-// position and inv_freq / 2 pi (off by 2^-54 of inv_freq and 2^-65 per position, however far that is); 32-bit floats would
-// lose an angle at position 2^20 by 0.06. All arithmetic on values is in 32 bits, rounded once.
+// position and inv_freq / 2 pi, which is off by 2^-52 of itself (its constant and its product are rounded) and 2^-65: the angle
+// by 2^-52 of itself and 2^-65 of a turn per position, 5e-7 inv_freq + 4e-10 at 2^31. 32-bit floats would lose an angle at position
+// 2^20 by 0.06. All arithmetic on values is in 32 bits, rounded once.
 //
 // 8192 tokens of 32 + 8 heads, head_dim 128, bf16 (168 MB): 31.4 us, 5.35 TB/s, 79% of a copy; 64 tokens: 4.2 us of GPU time.
 // 8194 tokens of 16 + 16 heads, head_dim 72, 36 channels in neighbouring pairs (76 MB): 21.9 us, since a row of 72 channels leaves
@@ -173,10 +174,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
   pdl_wait();
   pdl_trigger();
   for (int k = threadIdx.x; k < pairs; k += kRopeWarps * 32) {
-    // turns per position modulo 1, in units of 2^-64
-    double f = (double)__ldg(&a.freq[k]) * 0.15915494309189533577;
+    // turns per position modulo 1, in units of 2^-64 (one of a negative frequency is not taken from one, which would round it)
+    const float freq = __ldg(&a.freq[k]);
+    double f = (double)fabsf(freq) * 0.15915494309189533577;
     f -= floor(f);
-    s_turns[k] = __double2ull_rn(f * 18446744073709551616.0);
+    const unsigned long long turns = __double2ull_rn(f * 18446744073709551616.0);
+    s_turns[k] = freq < 0.f ? 0ull - turns : turns;
   }
   for (int k = threadIdx.x; k < 256; k += kRopeWarps * 32) {
     const int i = k >> 7, c = k & 127;
