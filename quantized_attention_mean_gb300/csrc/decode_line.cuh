@@ -10,7 +10,7 @@ namespace sage {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kCtas = 304;                 // ranges of the line: two resident CTAs per SM
+constexpr int kCtas = 304;                 // two resident CTAs per SM: the most of the clusters' form, ranges of the 16-bit line
 constexpr int kRows = 16;                  // query heads per row block
 constexpr int kMinTiles = 2;               // tiles a CTA takes at least
 constexpr int kRanks = 8;                  // CTAs of a cluster
@@ -36,7 +36,7 @@ struct DecodeArgs {
   int part_rows;            // rows of a piece
   // workspace
   int* err;                 // status word, or null (no workspace: the clusters' form without mass)
-  int* cta_err;             // [kCtas]
+  int* cta_err;             // [ranges]: one word for each CTA of the line, whose number is the kernel's own
   float* part_o;            // [ranges][2][side][part_rows][dp]
   float* part_ml;           // [ranges][2][side][part_rows][2], or [4] with FRAMES
   float* lse2;              // [batch, hq], base 2 (with mass)
@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeArgs a) 
   const int heads = a.c.hkv / a.side * a.row_blocks;
   const int hb = blockIdx.x / a.slices, slice = blockIdx.x - hb * a.slices;
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // The lengths are older than the decode kernel, which waited for what wrote them before it let this one begin: what
-  // follows from them is found while the decode kernel still runs.
+  // The lengths are older than the decode kernel, which waited for what wrote them before it let this one begin (as it did
+  // before it let a kernel begin that another host thread has put between them): what follows from them is found while the
+  // decode kernel still runs.
   auto collect = [&]() {  // the status of the call
     if (blockIdx.x > 0 || b > 0) return;
     int e = 0;

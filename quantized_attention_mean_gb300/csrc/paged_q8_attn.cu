@@ -13,7 +13,10 @@ struct Q8Layout {
 };
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 int tile_of(int d) { return d <= 64 ? Q8Cfg<64, 1>::kTile : Q8Cfg<128, 1>::kTile; }
+// Ranges that the workspace has room for, whichever kernel runs.
 constexpr int kMostRanges = Q8Cfg<128, 1>::kRanges;
+static_assert(kMostRanges >= Q8Cfg<64, 1>::kRanges && kMostRanges >= Q8Cfg<64, 2>::kRanges && kMostRanges >= Q8Cfg<128, 2>::kRanges,
+              "a line's ranges need room");
 // Few heads with short sequences: one launch of clusters whose CTAs all run at once.
 bool q8_clustered(int batch, int hkv, int row_blocks, int64_t max_len, int d) {
   return (int64_t)hkv * row_blocks * batch * kRanks <= kCtas && max_len <= 8 * kRanks * tile_of(d);
