@@ -293,7 +293,8 @@ __device__ __forceinline__ void store_window(const AppendArgs& a, const Window& 
 
 // CTA (x, y) of line x * shares + y: the windows whose first new token lies in rows [x chunk, (x + 1) chunk), for the y-th
 // share of the heads' K and V (kTwo to kEight: by the whole CTA, otherwise by a warp each). DRAM bounds it for prompts, which many
-// resident warps keep busy: fetching the next head's rows while one is scaled took twice the registers and was slower.
+// resident warps keep busy: fetching the next head's rows while one is scaled took twice the registers and was slower. At 72
+// registers kOne spills 20 to 36 bytes and kMany 4.
 template <typename T, int FORM, bool FULL>
 __global__ void __launch_bounds__(32 * warps_of(FORM), 28 / warps_of(FORM)) append_q8_kernel(const AppendArgs a) {
   __shared__ float s_most[4][FORM == kMany ? 3 * kManyRows : 8];

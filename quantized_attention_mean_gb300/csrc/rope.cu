@@ -162,6 +162,7 @@ __device__ __forceinline__ void widen2(uint32_t x, float& lo, float& hi) {
 // with cosines and sines are the same for all heads, which leaves six operations for two values.
 // LANES: of a row, or 0: a.lanes. ANY: rows whose mean of squares fp32 does not hold are taken by a power of two first; what
 // looks for them in the loop costs 2 to 8%, so that only calls that may have some do (bf16 with eps below kLeastSquare).
+// At 128 registers the forms of neighbouring pairs on five or six lanes spill one (4 bytes).
 template <typename T, int V, int SLOTS, bool PAIRS, int LANES, bool ANY>
 __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(const RopeArgs a) {
   using R = typename Run<T, V>::type;

@@ -10,7 +10,9 @@
 
 Token slot t of sequence b lies in page ``page_table[b, t // page_size]`` at ``t % page_size``; its scale is that of block
 ``t % page_size // block`` of the page and head, its value code · scale. Scales follow the tokens: the largest magnitude in
-a block decides, and a token that needs a larger scale than its block has makes the block's codes be rounded again. A cache
+a block decides, and a token that needs a larger scale than its block has makes the block's codes be rounded again. Keys are
+rounded as they are: what all keys have in common in a channel, which ``sage_attn`` takes off first, widens their scale (int8
+keys of unit variance about channel means of size 4: results off by 6% instead of 2%; E4M3 keys four times as much). A cache
 in 8 bits has no mass or position planes: it is not evicted from (``paged_evict`` takes 16-bit caches).
 """
 

@@ -583,6 +583,39 @@ def test_calls_with_nothing_to_do_say_so():
     assert same(G["k"], c["k"]) and torch.equal(G["ks"].cpu(), c["ks"])
 
 
+@pytest.mark.parametrize("bound", [300, 10 ** 5])
+@pytest.mark.parametrize("kt,vt,block,offset", [(S8, E4, 16, 0.0), (S8, S8, 64, 2.0), (E4, E4, 16, 0.5), (S8, E4, 1, 4.0)])
+def test_against_attention_over_the_unrounded_keys_and_values(kt, vt, block, offset, bound):
+    # what eight bits cost: scores move by half a step of every channel of a key, values by half a step of their own
+    import quantized_attention_mean_gb300 as qa
+    lens, hq, hkv, d, page = [300, 77], 8, 2, 64, 64
+    c = q8.make_cache([0, 0], hkv, d, page, block, kt, vt, seed=1, room=300)
+    g = torch.Generator().manual_seed(block)
+    k = (torch.randn(377, hkv, d, generator=g) + offset * torch.randn(hkv, d, generator=g)).half()
+    v = torch.randn(377, hkv, d, generator=g).half()
+    q = torch.randn(2, hq, d, generator=g).half()
+    G = on_gpu(c)
+    cu = [0, 300, 377]
+    qa.paged_append_q8(k.to(DEV), v.to(DEV), *planes(G), G["table"], G["lens"], cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV))
+    out = qa.paged_attn_q8(q.to(DEV), *planes(G), G["table"], torch.tensor(lens, dtype=torch.int32, device=DEV), bound)
+    c.update(k=G["k"].cpu(), v=G["v"].cpu(), ks=G["ks"].cpu(), vs=G["vs"].cpu(), lens=torch.tensor(lens, dtype=torch.int32))
+    kernel = q8.attend(c, q, d ** -0.5, hkv=hkv)["out_tol"]
+
+    def half_step(x, scale, dt):
+        # an int8 code is off by half a scale (and the reciprocal's rounding), an E4M3 one by 2^-4 of itself or half of 2^-9
+        return (scale * 0.5001).expand_as(x) if dt == S8 else torch.maximum(x.abs() * 2.0 ** -4, scale * 2.0 ** -10)
+
+    for b, n in enumerate(lens):
+        p, s = ref.place(c, b, n)
+        for h in range(hkv):
+            x, kk, vv = (t.double() for t in (q[b, h * 4:h * 4 + 4], k[cu[b]:cu[b + 1], h], v[cu[b]:cu[b + 1], h]))
+            dk, dv = (half_step(t, c[w + "s"][p, h, s // block].double()[:, None], dt) for t, w, dt in ((kk, "k", kt), (vv, "v", vt)))
+            weights = torch.softmax(x @ kk.T * d ** -0.5, -1)
+            moved = (x.abs() @ dk.T * d ** -0.5).amax(-1, keepdim=True)
+            tol = torch.expm1(2 * moved) * (weights @ vv.abs()) + torch.exp(2 * moved) * (weights @ dv)
+            assert_close(out[b, h * 4:h * 4 + 4], weights @ vv, tol + kernel[b, h * 4:h * 4 + 4], "out")
+
+
 # ------------------------------------------------------------------------------------- together
 def freqs(n):
     return (10000.0 ** (-torch.arange(n, dtype=torch.float64) / n)).float().to(DEV)
