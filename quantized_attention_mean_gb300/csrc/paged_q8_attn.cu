@@ -25,8 +25,8 @@ bool q8_clustered(int batch, int hkv, int row_blocks, int64_t max_len, int d) {
 // that DRAM is read in 256 bytes or more, of which rows of other sizes than 128 begin and end inside of its 64-byte pieces
 // (us with one, two and four heads: 32 sequences of up to 32K tokens 212, 188, 199; 32 x 8000 of head_dim 96 -, 100, 76, of 80
 // -, 103, 97). Short sequences of rows by heads: all four warps, so that tiles are filled and fewer of them end (us with one head
-// and with four: 512 x 150 tokens 80 and 71, 256 x 30-600 72 and 64, 256 x 300 59 and 58, but 128 x 600 46 and 47, 64 x 1200
-// 41 and 43).
+// and with four: 512 x 150 tokens 82 and 72, 256 x 30-600 72 and 64, 256 x 300 59 and 57, but 128 x 600 46 and 47, 64 x 1200
+// 41 and 43; at head_dim 64 512 x 150 62 and 59, 256 x 300 48 and 45).
 int heads_beside(bool nhd, int hkv, int d, int64_t max_len) {
   const int want = nhd ? (d == 128 ? 2 : 4) : max_len <= 600 ? 4 : 1;
   return hkv % want == 0 ? want : hkv % 2 == 0 ? 2 : 1;

@@ -12,12 +12,13 @@
 // - q becomes fp16 scaled by a power of two, which takes the largest channel of its row to [2^14, 2^15): channels down to
 //   2^-38 of it keep the bits they have, so nothing is lost against bf16.
 // - V's scale goes into the weight before it is rounded to fp16, w = 2^(t + log2 s_v - F), with F a running frame of
-//   t + log2 s_v of its own: weights of blocks with small scales keep their bits, whatever the largest scale is.
+//   t + log2 s_v of its own: weights of blocks with small scales keep their bits, whatever the largest scale is. Results of warps,
+//   clusters and ranges are joined by their F, sums by their m.
 // - Rows and columns change places between the products by movmatrix; V is read transposed by ldmatrix, two keys by two
 //   channels in a register, of which a byte permutation makes the pairs of keys that the product wants.
 //
 // 32 sequences of 0.1 to 32K tokens, 32 / 8 heads of head_dim 128 (1.11 GB): 184 us, 6.0 TB/s, 89% of a copy; two of 50 to 60K tokens, 32
-// heads of 64, biased: 94 us, 4.9 TB/s, of which 18 us are start, join and the CTAs' uneven ends; one of 1000 tokens: 7.3 us.
+// heads of 64, biased: 97 us, 4.8 TB/s, of which 18 us are start, join and the CTAs' uneven ends; one of 1000 tokens: 7.4 us.
 //
 // Split, loads and join as in the kernel over 16-bit rows (decode_line.cuh): ranges of one line of items, or clusters
 // of eight CTAs where heads are few and sequences short.
